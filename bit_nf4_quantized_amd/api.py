@@ -42,9 +42,14 @@ EXPORTS = (
     "qlora_linear_fwd_noalloc", "qlora_check_conversions", "qlora_probe_mfma", "qlora_probe_read",
     "qlora_quantize_batch", "qlora_quant_batch_workspace",
 )
+# every symbol declared in include/qlora_adapters.h
+ADAPTER_EXPORTS = (
+    "qlora_adam_state_numel", "qlora_clip_grad_norm_batch", "qlora_adamw_batch",
+)
 QLORA_NOALLOC_SCRATCH_BYTES = (2 << 20) + (64 << 10)
 QLORA_QUANT_BATCH_MAX = 16
 QLORA_CLIP_WORKSPACE_BYTES = 8192
+QLORA_ADAM_STATE_BLOCK = 256
 
 
 class AdamParams(ctypes.Structure):
@@ -75,6 +80,13 @@ class QNF4(ctypes.Structure):
         ("no_dq", ctypes.c_int32),
         ("absmax32", ctypes.c_void_p),
     ]
+
+
+class QAdamState(ctypes.Structure):
+    """Mirror of the C struct qlora_adam_state (host struct of device pointers)."""
+
+    _fields_ = [("bits", ctypes.c_int32), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 class QLoRAError(RuntimeError):
@@ -154,6 +166,13 @@ def _load():
     lib.qlora_probe_read.argtypes = [vp, sz, ctypes.c_uint32, vp, vp]
     lib.qlora_probe_read.restype = ctypes.c_int
     lib.qlora_int8_dequantize.restype = ctypes.c_int
+    lib.qlora_adam_state_numel.argtypes = [ctypes.c_int, P(i64), P(i64)]
+    lib.qlora_clip_grad_norm_batch.argtypes = [ctypes.c_int, P(vp), ctypes.c_int, P(i64), ctypes.c_float, vp, vp, vp,
+                                               sz, vp]
+    lib.qlora_adamw_batch.argtypes = [ctypes.c_int, P(vp), P(vp), ctypes.c_int, P(vp), P(i64), P(QAdamState),
+                                      P(AdamParams), vp, vp]
+    for name in ADAPTER_EXPORTS:
+        getattr(lib, name).restype = ctypes.c_int
     _LIB = lib
     return lib
 
@@ -184,11 +203,11 @@ def _on_stream(fn):
     import functools
     import inspect
 
-    sig = inspect.signature(fn)
+    at = list(inspect.signature(fn).parameters).index("stream")
 
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
-        stream = sig.bind_partial(*args, **kwargs).arguments.get("stream")
+        stream = args[at] if len(args) > at else kwargs.get("stream")
         if stream is None:
             return fn(*args, **kwargs)
         import torch
@@ -317,6 +336,128 @@ def qlora_adam_step(theta, g, m, v, step: int, lr: float, beta1: float = 0.9, be
     hp = AdamParams(lr, beta1, beta2, eps, weight_decay, step)
     _check(_load().qlora_adam_step(_ptr(theta), _ptr(g), _ptr(m), _ptr(v), n, ctypes.byref(hp), _ptr(coef),
                                    _ptr(theta_bf16), _stream(stream)), "qlora_adam_step")
+
+
+# ---- the optimiser step over many tensors -------------------------------------------
+
+@dataclass
+class AdamWState:
+    """The AdamW state of a list of tensors (qlora_adam_state): tensor k's
+    values start at the sum of the earlier sizes, each rounded up to 256."""
+
+    bits: int                 # 32 or 8
+    numel: list               # elements of each tensor
+    m: "torch.Tensor"         # [total] float32, or float8_e4m3fn codes
+    v: "torch.Tensor"         # [total] float32, or float8_e4m3fn codes of sqrt(v)
+    m_scale: "torch.Tensor | None" = None   # float32 [total / 256] (8 bits)
+    v_scale: "torch.Tensor | None" = None
+
+    @staticmethod
+    def zeros(tensors, bits: int = 8, device=None, pin_memory: bool = False) -> "AdamWState":
+        """The state before the first step of ``tensors``, on their device or in pinned host memory."""
+        import torch
+
+        if bits not in (8, 32):
+            raise ValueError("bits must be 8 or 32")
+        numel = [t.numel() for t in tensors]
+        total = sum(-(-n // QLORA_ADAM_STATE_BLOCK) * QLORA_ADAM_STATE_BLOCK for n in numel)
+        if device is None:
+            device = "cpu" if pin_memory else (tensors[0].device if len(tensors) else "cuda")
+        z = lambda n, dt: torch.zeros(n, dtype=dt, device=device, pin_memory=pin_memory)  # noqa: E731
+        if bits == 32:
+            return AdamWState(32, numel, z(total, torch.float32), z(total, torch.float32))
+        nb = total // QLORA_ADAM_STATE_BLOCK
+        return AdamWState(8, numel, z(total, torch.uint8).view(torch.float8_e4m3fn),
+                          z(total, torch.uint8).view(torch.float8_e4m3fn), z(nb, torch.float32), z(nb, torch.float32))
+
+
+def _ptr_array(tensors, dtype, numel, device, name):
+    """Device addresses of a list of contiguous tensors as a ctypes array; sizes must match numel."""
+    if len(tensors) != len(numel):
+        raise ValueError(f"{name}: one tensor per parameter ({len(numel)}), got {len(tensors)}")
+    for t, n in zip(tensors, numel):
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must all be {dtype}, got {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} must all be on {device}, got {t.device}")
+        if t.numel() != n:
+            raise ValueError(f"{name} must have the parameters' sizes")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    return (ctypes.c_void_p * len(numel))(*[t.data_ptr() for t in tensors])
+
+
+def _grad_dtype(grads):
+    import torch
+
+    if not grads or grads[0].dtype == torch.float32:
+        return QLORA_F32, torch.float32
+    if grads[0].dtype == torch.bfloat16:
+        return QLORA_BF16, torch.bfloat16
+    raise TypeError("gradients must be float32 or bfloat16")
+
+
+@_on_stream
+def qlora_clip_grad_norm_batch(grads, max_norm: float, coef=None, norm=None, workspace=None, stream=None):
+    """coef = min(1, max_norm / (||g|| + 1e-6)) over all tensors of ``grads``
+    (all float32 or all bfloat16) and the norm (float64), as 1-element device tensors."""
+    import torch
+
+    grads = list(grads)
+    gd, dtype = _grad_dtype(grads)
+    dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+    if dev.type != "cuda":
+        raise ValueError("grads must be device tensors")
+    numel = [t.numel() for t in grads]
+    gp = _ptr_array(grads, dtype, numel, dev, "grads")
+    coef = coef if coef is not None else torch.empty(1, dtype=torch.float32, device=dev)
+    norm = norm if norm is not None else torch.empty(1, dtype=torch.float64, device=dev)
+    _need(coef, torch.float32, (1,), "coef")
+    _need(norm, torch.float64, (1,), "norm")
+    ws = _workspace(QLORA_CLIP_WORKSPACE_BYTES, dev, workspace)
+    _check(_load().qlora_clip_grad_norm_batch(len(grads), gp, gd, (ctypes.c_int64 * len(grads))(*numel),
+                                              float(max_norm), _ptr(coef), _ptr(norm), _ptr(ws),
+                                              ws.numel() * ws.element_size(), _stream(stream)),
+           "qlora_clip_grad_norm_batch")
+    return coef, norm
+
+
+@_on_stream
+def qlora_adamw_batch(thetas, grads, state: AdamWState, step: int, lr: float, beta1: float = 0.9,
+                      beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0, coef=None,
+                      thetas_bf16=None, stream=None):
+    """One AdamW step in place on the float32 tensors ``thetas`` and their
+    ``state``, for gradients ``grads`` (all float32 or all bfloat16) clipped by
+    ``coef`` (1-element tensor); ``thetas_bf16`` receive the rounded copies."""
+    import torch
+
+    thetas, grads = list(thetas), list(grads)
+    n = len(thetas)
+    gd, gtype = _grad_dtype(grads)
+    numel = [t.numel() for t in thetas]
+    if numel != list(state.numel):
+        raise ValueError("the state belongs to tensors of other sizes")
+    dev = thetas[0].device if n else torch.device("cuda", torch.cuda.current_device())
+    if dev.type != "cuda":
+        raise ValueError("thetas must be device tensors")
+    tp = _ptr_array(thetas, torch.float32, numel, dev, "thetas")
+    gp = _ptr_array(grads, gtype, numel, dev, "grads")
+    bp = None if thetas_bf16 is None else _ptr_array(list(thetas_bf16), torch.bfloat16, numel, dev, "thetas_bf16")
+    total = sum([(k + 255) // 256 * 256 for k in numel])
+    held = torch.float32 if state.bits == 32 else torch.float8_e4m3fn
+    _need_mem(state.m, held, (total,), "state.m")
+    _need_mem(state.v, held, (total,), "state.v")
+    if state.bits == 8:
+        _need_mem(state.m_scale, torch.float32, (total // QLORA_ADAM_STATE_BLOCK,), "state.m_scale")
+        _need_mem(state.v_scale, torch.float32, (total // QLORA_ADAM_STATE_BLOCK,), "state.v_scale")
+    if coef is not None:
+        _need(coef, torch.float32, (1,), "coef")
+    st = QAdamState(state.bits, state.m.data_ptr(), state.v.data_ptr(),
+                    state.m_scale.data_ptr() if state.bits == 8 else None,
+                    state.v_scale.data_ptr() if state.bits == 8 else None)
+    hp = AdamParams(lr, beta1, beta2, eps, weight_decay, step)
+    _check(_load().qlora_adamw_batch(n, tp, gp, gd, bp, (ctypes.c_int64 * n)(*numel), ctypes.byref(st),
+                                     ctypes.byref(hp), _ptr(coef), _stream(stream)), "qlora_adamw_batch")
 
 
 @_on_stream

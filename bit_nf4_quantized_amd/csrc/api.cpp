@@ -1,5 +1,7 @@
 // C ABI of the QLoRA NF4 library: host-side validation, sizes, the NF4
-// codebook, and stream-ordered kernel launches. See include/qlora_nf4.h.
+// codebook, and stream-ordered kernel launches. See include/qlora_nf4.h
+// and include/qlora_adapters.h.
+#include "qlora_adapters.h"
 #include "qlora_nf4.h"
 
 #include <math.h>
@@ -398,6 +400,20 @@ int linear_bwd_impl(const qlora_nf4* W, const uint16_t* X, const uint16_t* dY, i
 
 bool valid_dropout(float p) { return isfinite(p) && p >= 0.0f && p < 1.0f; }
 
+constexpr int64_t kMaxNumel = (int64_t)1 << 40;
+
+bool valid_adam(const qlora_adam_params* hp) {
+  return hp && hp->step >= 1 && hp->lr >= 0.0f && isfinite(hp->lr) && hp->eps >= 0.0f && isfinite(hp->eps) &&
+         hp->beta1 >= 0.0f && hp->beta1 < 1.0f && hp->beta2 >= 0.0f && hp->beta2 < 1.0f && isfinite(hp->weight_decay);
+}
+
+qlora::AdamHyper adam_hyper(const qlora_adam_params* hp) {
+  qlora::AdamHyper h;
+  h.lr = hp->lr; h.beta1 = hp->beta1; h.beta2 = hp->beta2; h.eps = hp->eps; h.wd = hp->weight_decay;
+  h.step = hp->step;
+  return h;
+}
+
 // The device-side address of p: device memory as it is, pinned host memory
 // through its device mapping; nullptr for anything else (pageable host
 // memory, managed memory, or an address HIP does not know).
@@ -527,10 +543,7 @@ int qlora_adam_step(float* theta, const float* g, float* m, float* v, int64_t n,
                     const float* coef, uint16_t* theta_bf16, hipStream_t stream) {
   if (!hp) return QLORA_ERR_ARG;
   if (n < 0) return QLORA_ERR_SHAPE;
-  if (hp->step < 1 || !(hp->lr >= 0.0f) || !isfinite(hp->lr) || !(hp->eps >= 0.0f) || !isfinite(hp->eps) ||
-      !(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) || !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f) ||
-      !isfinite(hp->weight_decay))
-    return QLORA_ERR_ARG;
+  if (!valid_adam(hp)) return QLORA_ERR_ARG;
   if (n == 0) return QLORA_OK;
   if (!theta || !g || !m || !v) return QLORA_ERR_ARG;
   if (!aligned16(theta) || !aligned16(g) || !aligned16(m) || !aligned16(v) || !aligned16(theta_bf16) ||
@@ -543,11 +556,83 @@ int qlora_adam_step(float* theta, const float* g, float* m, float* v, int64_t n,
   const float* cd = coef ? static_cast<const float*>(device_view(coef)) : nullptr;
   uint16_t* bd = theta_bf16 ? static_cast<uint16_t*>(device_view(theta_bf16)) : nullptr;
   if (!td || !gd || !md || !vd || (coef && !cd) || (theta_bf16 && !bd)) return QLORA_ERR_ARG;
-  qlora::AdamHyper h;
-  h.lr = hp->lr; h.beta1 = hp->beta1; h.beta2 = hp->beta2; h.eps = hp->eps; h.wd = hp->weight_decay;
-  h.step = hp->step;
+  const qlora::AdamHyper h = adam_hyper(hp);
   (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
   const hipError_t e = qlora::launch_adam(td, gd, md, vd, n, h, cd, bd, stream);
+  return e == hipSuccess ? QLORA_OK : hip_fail(e);
+}
+
+int qlora_adam_state_numel(int n, const int64_t* numel, int64_t* total) {
+  if (n < 0 || (n > 0 && !numel) || !total) return QLORA_ERR_ARG;
+  int64_t sum = 0;
+  for (int k = 0; k < n; ++k) {
+    if (numel[k] < 0 || numel[k] > kMaxNumel) return QLORA_ERR_SHAPE;
+    sum += qlora::adam_state_span(numel[k]);
+    if (sum > kMaxNumel) return QLORA_ERR_SHAPE;
+  }
+  *total = sum;
+  return QLORA_OK;
+}
+
+int qlora_clip_grad_norm_batch(int n, const void* const* g, qlora_dtype grad_dtype, const int64_t* numel,
+                               float max_norm, float* coef, double* norm, void* ws, size_t ws_bytes,
+                               hipStream_t stream) {
+  int64_t total = 0;
+  const int st = qlora_adam_state_numel(n, numel, &total);
+  if (st != QLORA_OK) return st;
+  if (grad_dtype != QLORA_F32 && grad_dtype != QLORA_BF16) return QLORA_ERR_ARG;
+  if (!(max_norm > 0.0f)) return QLORA_ERR_ARG;
+  if ((n > 0 && !g) || (!coef && !norm)) return QLORA_ERR_ARG;
+  if (!ws || ws_bytes < QLORA_CLIP_WORKSPACE_BYTES) return QLORA_ERR_WORKSPACE;
+  for (int k = 0; k < n; ++k) {
+    if (numel[k] > 0 && !g[k]) return QLORA_ERR_ARG;
+    if (numel[k] > 0 && !aligned16(g[k])) return QLORA_ERR_ALIGN;
+  }
+  if (!aligned16(ws) || (reinterpret_cast<uintptr_t>(coef) & 3u) || (reinterpret_cast<uintptr_t>(norm) & 7u))
+    return QLORA_ERR_ALIGN;
+  (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
+  const hipError_t e = qlora::launch_clip_norm_batch(n, g, grad_dtype == QLORA_BF16, numel, (double)max_norm, coef,
+                                                     norm, static_cast<double*>(ws), stream);
+  return e == hipSuccess ? QLORA_OK : hip_fail(e);
+}
+
+int qlora_adamw_batch(int n, float* const* theta, const void* const* g, qlora_dtype grad_dtype,
+                      uint16_t* const* theta_bf16, const int64_t* numel, const qlora_adam_state* state,
+                      const qlora_adam_params* hp, const float* coef, hipStream_t stream) {
+  if (!state || !valid_adam(hp)) return QLORA_ERR_ARG;
+  if ((state->bits != 8 && state->bits != 32) || (grad_dtype != QLORA_F32 && grad_dtype != QLORA_BF16))
+    return QLORA_ERR_ARG;
+  int64_t total = 0;
+  const int st = qlora_adam_state_numel(n, numel, &total);
+  if (st != QLORA_OK) return st;
+  if (total == 0) return QLORA_OK;
+  if (!theta || !g || !state->m || !state->v) return QLORA_ERR_ARG;
+  if (state->bits == 8 && (!state->m_scale || !state->v_scale)) return QLORA_ERR_ARG;
+  for (int k = 0; k < n; ++k) {
+    if (numel[k] == 0) continue;
+    if (!theta[k] || !g[k] || (theta_bf16 && !theta_bf16[k])) return QLORA_ERR_ARG;
+    if (!aligned16(theta[k]) || !aligned16(g[k]) || (theta_bf16 && !aligned16(theta_bf16[k]))) return QLORA_ERR_ALIGN;
+  }
+  if (!aligned16(state->m) || !aligned16(state->v) || (reinterpret_cast<uintptr_t>(state->m_scale) & 3u) ||
+      (reinterpret_cast<uintptr_t>(state->v_scale) & 3u) || (reinterpret_cast<uintptr_t>(coef) & 3u))
+    return QLORA_ERR_ALIGN;
+  // the state may sit in pinned host memory, as for qlora_adam_step
+  qlora::AdamBatch b;
+  b.n = n;
+  b.theta = theta;
+  b.g = g;
+  b.g16 = grad_dtype == QLORA_BF16;
+  b.theta16 = theta_bf16;
+  b.numel = numel;
+  b.bits8 = state->bits == 8;
+  b.m = device_view(state->m);
+  b.v = device_view(state->v);
+  b.m_scale = b.bits8 ? static_cast<float*>(device_view(state->m_scale)) : nullptr;
+  b.v_scale = b.bits8 ? static_cast<float*>(device_view(state->v_scale)) : nullptr;
+  if (!b.m || !b.v || (b.bits8 && (!b.m_scale || !b.v_scale))) return QLORA_ERR_ARG;
+  const qlora::AdamHyper h = adam_hyper(hp);
+  (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
+  const hipError_t e = qlora::launch_adamw_batch(b, h, coef, stream);
   return e == hipSuccess ? QLORA_OK : hip_fail(e);
 }
 

@@ -150,6 +150,26 @@ hipError_t launch_clip_norm(const float* g, int64_t n, double max_norm, float* c
 hipError_t launch_adam(float* theta, const float* g, float* m, float* v, int64_t n, const AdamHyper& h,
                        const float* coef, uint16_t* theta_bf16, hipStream_t stream);
 
+// The step over many tensors (optim_batch.hip). State values of tensor k start
+// at sum_{j < k} adam_state_span(numel[j]).
+constexpr int64_t adam_state_span(int64_t numel) { return (numel + 255) / 256 * 256; }
+struct AdamBatch {
+  int n;
+  float* const* theta;
+  const void* const* g;
+  bool g16;
+  uint16_t* const* theta16;   // or nullptr
+  const int64_t* numel;
+  bool bits8;
+  void* m;
+  void* v;
+  float* m_scale;             // 8-bit state only
+  float* v_scale;
+};
+hipError_t launch_clip_norm_batch(int n, const void* const* g, bool g16, const int64_t* numel, double max_norm,
+                                  float* coef, double* norm, double* part, hipStream_t stream);
+hipError_t launch_adamw_batch(const AdamBatch& b, const AdamHyper& h, const float* coef, hipStream_t stream);
+
 // Adapter merge into the bf16 dequantised base (merge.hip).
 hipError_t launch_merge(const NF4View& W, const NF4Table& tab, const uint16_t* L1, const uint16_t* L2, int r,
                         float s, uint16_t* out, hipStream_t stream);

@@ -23,25 +23,13 @@
 //                          theta -= lr (m/bc1 / (sqrt(v/bc2) + eps) + wd theta),
 //                          and the bf16 copy of theta for the layer
 // Every result is deterministic (fixed reduction order, no atomics).
+#include "adam.h"
 #include "common.h"
 #include "launch.h"
 
 namespace qlora {
 
 namespace {
-
-constexpr int kNormBlocks = 1024;
-
-__device__ __forceinline__ double tree_sum_256(double v, double* s) {
-  const int t = threadIdx.x;
-  s[t] = v;
-  __syncthreads();
-  for (int w = 128; w > 0; w >>= 1) {
-    if (t < w) s[t] += s[t + w];
-    __syncthreads();
-  }
-  return s[0];
-}
 
 __global__ __launch_bounds__(256) void sumsq_partial_kernel(const float* __restrict__ g, int64_t n,
                                                             double* __restrict__ part) {
@@ -60,38 +48,6 @@ __global__ __launch_bounds__(256) void sumsq_partial_kernel(const float* __restr
     for (int64_t i = 4 * n4; i < n; ++i) acc += (double)g[i] * g[i];
   const double tot = tree_sum_256(acc, s);
   if (threadIdx.x == 0) part[blockIdx.x] = tot;
-}
-
-__global__ __launch_bounds__(1024) void clip_finalize_kernel(const double* __restrict__ part, double max_norm,
-                                                             float* __restrict__ coef, double* __restrict__ norm) {
-  __shared__ double s[1024];
-  const int t = threadIdx.x;
-  s[t] = part[t];
-  __syncthreads();
-  for (int w = 512; w > 0; w >>= 1) {
-    if (t < w) s[t] += s[t + w];
-    __syncthreads();
-  }
-  if (t == 0) {
-    const double nrm = sqrt(s[0]);
-    const double c = max_norm / (nrm + 1e-6);
-    if (coef) *coef = (float)(c < 1.0 ? c : 1.0);
-    if (norm) *norm = nrm;
-  }
-}
-
-struct AdamConsts {
-  float lr, b1, b2, omb1, omb2, eps, wd, bc1, bc2;
-};
-
-__device__ __forceinline__ void adam_one(float& th, float g, float& m, float& v, float cf, const AdamConsts& k) {
-  const float gc = cf * g;
-  m = k.b1 * m + k.omb1 * gc;
-  v = k.b2 * v + k.omb2 * (gc * gc);
-  const float mh = m / k.bc1;
-  const float vh = v / k.bc2;
-  const float upd = mh / (__builtin_sqrtf(vh) + k.eps);
-  th = th - k.lr * (upd + k.wd * th);
 }
 
 __global__ __launch_bounds__(256) void adam_kernel(float* __restrict__ theta, const float* __restrict__ g,
@@ -141,12 +97,7 @@ hipError_t launch_clip_norm(const float* g, int64_t n, double max_norm, float* c
 hipError_t launch_adam(float* theta, const float* g, float* m, float* v, int64_t n, const AdamHyper& h,
                        const float* coef, uint16_t* theta_bf16, hipStream_t stream) {
   if (n <= 0) return hipSuccess;
-  AdamConsts k;
-  k.lr = h.lr; k.b1 = h.beta1; k.b2 = h.beta2; k.eps = h.eps; k.wd = h.wd;
-  k.omb1 = (float)(1.0 - (double)h.beta1);
-  k.omb2 = (float)(1.0 - (double)h.beta2);
-  k.bc1 = (float)(1.0 - pow((double)h.beta1, (double)h.step));
-  k.bc2 = (float)(1.0 - pow((double)h.beta2, (double)h.step));
+  const AdamConsts k = adam_consts(h);
   int64_t blocks = (n / 4 + 255) / 256;
   const int64_t cap = (int64_t)device_cu_count() * 16;
   if (blocks > cap) blocks = cap;

@@ -1,0 +1,73 @@
+/*
+ * qlora_adapters.h -- many adapters on one quantised base: the C ABI of the
+ * entry points beside qlora_nf4.h (same library, same conventions, status
+ * codes, types and workspace rules).
+ *
+ *   - qlora_linear_multi_fwd / _bwd: the QLoRA linear with an adapter per row;
+ *   - qlora_preference_loss: a preference loss over pairs of sequences, with
+ *     the gradient of the logits;
+ *   - qlora_clip_grad_norm_batch / qlora_adamw_batch: the optimiser step over
+ *     all adapter tensors at once, with fp32 or 8-bit state.
+ */
+#ifndef QLORA_ADAPTERS_H
+#define QLORA_ADAPTERS_H
+
+#include "qlora_nf4.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * The optimiser step over many tensors at once: the adapters as they were
+ * allocated, one (dL1, dL2) pair per linear, with no copy into a flat vector.
+ * theta[k], g[k], theta_bf16[k] are host arrays of n device pointers, numel[k]
+ * the tensors' sizes (0 .. 2^40; empty tensors are skipped); gradients are all
+ * fp32 or all bf16 (grad_dtype). Every tensor is 16-byte aligned, in device
+ * memory, and no two overlap. n may be 0. Deterministic; nothing is allocated.
+ *
+ * qlora_adam_state: the two state vectors of all tensors, one array each:
+ * tensor k's values start at element off_k = sum_{j < k} 256 ceil(numel_j / 256),
+ * and the arrays hold qlora_adam_state_numel values (the padding behind a
+ * tensor is scratch). The arrays may be device or pinned host memory ("paged
+ * out", section 方法总览 item 4). Zeros are the state before the first step.
+ *   bits 32  m, v: fp32; the scales are not used (may be NULL).
+ *   bits 8   m: E4M3 codes (OCP E4M3FN) of the first moment, v: E4M3 codes of
+ *            sqrt(second moment); m_scale, v_scale: fp32, one per 256 values.
+ *            A value is code * scale. Written per block of 256 as
+ *            scale = RN32(top / 448), code = E4M3(RN32(x RN32(448 / top))),
+ *            nearest, ties to the even code, top the block's largest magnitude
+ *            (below 2^-100: all zeros); a nonzero sqrt(v) gets at least the
+ *            smallest code, so that it never leaves eps alone to divide by.
+ *
+ * qlora_clip_grad_norm_batch: qlora_clip_grad_norm's norm and coef over all
+ * tensors' gradients (float64 sums in a fixed order; bf16 gradients are
+ * squared exactly). coef, norm, ws as there, in device memory.
+ *
+ * qlora_adamw_batch: qlora_adam_step's update of every tensor, element by
+ * element with the same arithmetic (weight decay decoupled from the moments);
+ * with 8 bits, v is the square of the stored root, and theta is stepped with
+ * this step's m and v before they are rounded to codes.
+ *   theta_bf16  bf16 copies, or NULL for none.
+ *   coef        device fp32 [1], or NULL for 1.
+ */
+typedef struct {
+  int32_t bits;
+  void *m;
+  void *v;
+  float *m_scale;
+  float *v_scale;
+} qlora_adam_state;
+int qlora_adam_state_numel(int n, const int64_t *numel, int64_t *total);
+int qlora_clip_grad_norm_batch(int n, const void *const *g, qlora_dtype grad_dtype, const int64_t *numel,
+                               float max_norm, float *coef, double *norm, void *ws, size_t ws_bytes,
+                               hipStream_t stream);
+int qlora_adamw_batch(int n, float *const *theta, const void *const *g, qlora_dtype grad_dtype,
+                      uint16_t *const *theta_bf16, const int64_t *numel, const qlora_adam_state *state,
+                      const qlora_adam_params *hp, const float *coef, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* QLORA_ADAPTERS_H */

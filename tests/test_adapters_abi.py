@@ -1,0 +1,111 @@
+"""Host-side checks of the entry points of include/qlora_adapters.h (CPU only):
+the library exports what the header declares, reports the sizes the layouts
+imply, and rejects bad arguments before anything is enqueued."""
+
+import ctypes
+import os
+import re
+
+import pytest
+
+from bit_nf4_quantized_amd import api
+from oracle import optim_batch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "qlora_adapters.h")
+P = 4096   # a 16-byte aligned address that is never dereferenced
+
+
+def declared_functions():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = re.findall(r"^\s*(?:const\s+)?[A-Za-z_][A-Za-z0-9_ ]*[\s\*]+(qlora_[a-z0-9_]+)\s*\(", text, flags=re.M)
+    return sorted(set(names))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(api.LIB_PATH):
+        from bit_nf4_quantized_amd import build
+        build.build()
+    return api.library()
+
+
+def test_exports_every_declared_symbol(lib):
+    names = declared_functions()
+    assert sorted(api.ADAPTER_EXPORTS) == names
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+def ptrs(*a):
+    return (ctypes.c_void_p * max(len(a), 1))(*a)
+
+
+def sizes(*a):
+    return (ctypes.c_int64 * max(len(a), 1))(*a)
+
+
+def test_adam_state_numel(lib):
+    total = ctypes.c_int64(-1)
+    for numel in ([], [0], [1], [256], [257, 0, 3], [10 ** 9 + 1] * 5):
+        assert lib.qlora_adam_state_numel(len(numel), sizes(*numel), ctypes.byref(total)) == api.QLORA_OK
+        assert total.value == optim_batch.offsets(numel)[-1]
+    assert lib.qlora_adam_state_numel(-1, sizes(1), ctypes.byref(total)) == api.QLORA_ERR_ARG
+    assert lib.qlora_adam_state_numel(1, None, ctypes.byref(total)) == api.QLORA_ERR_ARG
+    assert lib.qlora_adam_state_numel(1, sizes(1), None) == api.QLORA_ERR_ARG
+    assert lib.qlora_adam_state_numel(1, sizes(-1), ctypes.byref(total)) == api.QLORA_ERR_SHAPE
+    assert lib.qlora_adam_state_numel(1, sizes((1 << 40) + 1), ctypes.byref(total)) == api.QLORA_ERR_SHAPE
+    assert lib.qlora_adam_state_numel(2, sizes(1 << 40, 1 << 40), ctypes.byref(total)) == api.QLORA_ERR_SHAPE
+
+
+def test_clip_grad_norm_batch_refusals(lib):
+    def call(n=1, g=ptrs(P), dt=0, numel=sizes(8), mx=0.3, coef=P, norm=P, ws=P, wsb=8192):
+        return lib.qlora_clip_grad_norm_batch(n, g, dt, numel, mx, coef, norm, ws, wsb, None)
+
+    E = api
+    assert call(n=-1) == E.QLORA_ERR_ARG
+    assert call(g=None) == E.QLORA_ERR_ARG
+    assert call(g=ptrs(None)) == E.QLORA_ERR_ARG
+    assert call(dt=2) == E.QLORA_ERR_ARG
+    assert call(numel=sizes(-8)) == E.QLORA_ERR_SHAPE
+    assert call(mx=0.0) == E.QLORA_ERR_ARG
+    assert call(mx=float("nan")) == E.QLORA_ERR_ARG
+    assert call(coef=None, norm=None) == E.QLORA_ERR_ARG
+    assert call(ws=None) == E.QLORA_ERR_WORKSPACE
+    assert call(wsb=8191) == E.QLORA_ERR_WORKSPACE
+    assert call(g=ptrs(P + 8)) == E.QLORA_ERR_ALIGN
+    assert call(norm=P + 4) == E.QLORA_ERR_ALIGN
+    assert call(coef=P + 2) == E.QLORA_ERR_ALIGN
+
+
+def test_adamw_batch_refusals(lib):
+    good_hp = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1)
+
+    def call(n=1, th=ptrs(P), g=ptrs(P), dt=0, tb=None, numel=sizes(8), bits=8, m=P, v=P, ms=P, vs=P, coef=None, **hp):
+        st = api.QAdamState(bits, m, v, ms, vs)
+        h = api.AdamParams(**{**good_hp, **hp})
+        return lib.qlora_adamw_batch(n, th, g, dt, tb, numel, ctypes.byref(st), ctypes.byref(h), coef, None)
+
+    E = api
+    assert call(n=0) == E.QLORA_OK
+    assert call(numel=sizes(0), th=ptrs(None)) == E.QLORA_OK
+    assert call(n=-1) == E.QLORA_ERR_ARG
+    assert call(th=None) == E.QLORA_ERR_ARG
+    assert call(th=ptrs(None)) == E.QLORA_ERR_ARG
+    assert call(g=ptrs(None)) == E.QLORA_ERR_ARG
+    assert call(tb=ptrs(None)) == E.QLORA_ERR_ARG
+    assert call(dt=3) == E.QLORA_ERR_ARG
+    assert call(bits=4) == E.QLORA_ERR_ARG
+    assert call(m=None) == E.QLORA_ERR_ARG
+    assert call(ms=None) == E.QLORA_ERR_ARG
+    assert call(numel=sizes(-1)) == E.QLORA_ERR_SHAPE
+    for bad in (dict(step=0), dict(lr=-1.0), dict(lr=float("inf")), dict(beta1=1.0), dict(beta2=-0.1),
+                dict(eps=-1.0), dict(weight_decay=float("nan"))):
+        assert call(**bad) == E.QLORA_ERR_ARG, bad
+    assert call(th=ptrs(P + 4)) == E.QLORA_ERR_ALIGN
+    assert call(g=ptrs(P + 4)) == E.QLORA_ERR_ALIGN
+    assert call(tb=ptrs(P + 2)) == E.QLORA_ERR_ALIGN
+    assert call(v=P + 8) == E.QLORA_ERR_ALIGN
+    assert call(vs=P + 2) == E.QLORA_ERR_ALIGN
+    assert call(coef=P + 1) == E.QLORA_ERR_ALIGN
+    assert lib.qlora_adamw_batch(1, ptrs(P), ptrs(P), 0, None, sizes(8), None, None, None, None) == E.QLORA_ERR_ARG

@@ -10,7 +10,9 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from dataclasses import dataclass
+from operator import attrgetter
 
 import numpy as np
 
@@ -50,6 +52,7 @@ QLORA_NOALLOC_SCRATCH_BYTES = (2 << 20) + (64 << 10)
 QLORA_QUANT_BATCH_MAX = 16
 QLORA_CLIP_WORKSPACE_BYTES = 8192
 QLORA_ADAM_STATE_BLOCK = 256
+_DTYPE_OF = attrgetter("dtype")
 
 
 class AdamParams(ctypes.Structure):
@@ -167,10 +170,8 @@ def _load():
     lib.qlora_probe_read.restype = ctypes.c_int
     lib.qlora_int8_dequantize.restype = ctypes.c_int
     lib.qlora_adam_state_numel.argtypes = [ctypes.c_int, P(i64), P(i64)]
-    lib.qlora_clip_grad_norm_batch.argtypes = [ctypes.c_int, P(vp), ctypes.c_int, P(i64), ctypes.c_float, vp, vp, vp,
-                                               sz, vp]
-    lib.qlora_adamw_batch.argtypes = [ctypes.c_int, P(vp), P(vp), ctypes.c_int, P(vp), P(i64), P(QAdamState),
-                                      P(AdamParams), vp, vp]
+    lib.qlora_clip_grad_norm_batch.argtypes = [ctypes.c_int, vp, ctypes.c_int, vp, ctypes.c_float, vp, vp, vp, sz, vp]
+    lib.qlora_adamw_batch.argtypes = [ctypes.c_int, vp, vp, ctypes.c_int, vp, vp, P(QAdamState), P(AdamParams), vp, vp]
     for name in ADAPTER_EXPORTS:
         getattr(lib, name).restype = ctypes.c_int
     _LIB = lib
@@ -371,20 +372,26 @@ class AdamWState:
                           z(total, torch.uint8).view(torch.float8_e4m3fn), z(nb, torch.float32), z(nb, torch.float32))
 
 
-def _ptr_array(tensors, dtype, numel, device, name):
-    """Device addresses of a list of contiguous tensors as a ctypes array; sizes must match numel."""
-    if len(tensors) != len(numel):
-        raise ValueError(f"{name}: one tensor per parameter ({len(numel)}), got {len(tensors)}")
-    for t, n in zip(tensors, numel):
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must all be {dtype}, got {t.dtype}")
-        if t.device != device:
-            raise ValueError(f"{name} must all be on {device}, got {t.device}")
-        if t.numel() != n:
-            raise ValueError(f"{name} must have the parameters' sizes")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    return (ctypes.c_void_p * len(numel))(*[t.data_ptr() for t in tensors])
+def _pointers(tensors, dtype, numel, device, name):
+    """Device addresses of a list of contiguous tensors (array of int64); sizes
+    must match numel. Whole-list calls: a model has hundreds of adapter tensors,
+    and the step on the GPU should not wait for this loop."""
+    import torch
+
+    T = torch.Tensor
+    if list(map(T.numel, tensors)) != numel:
+        raise ValueError(f"{name} must be one tensor of each parameter's size")
+    if set(map(_DTYPE_OF, tensors)) - {dtype}:
+        raise TypeError(f"{name} must all be {dtype}")
+    if set(map(T.get_device, tensors)) - {device.index}:
+        raise ValueError(f"{name} must all be on {device}")
+    if not all(map(T.is_contiguous, tensors)):
+        raise ValueError(f"{name} must be contiguous")
+    return array("q", map(T.data_ptr, tensors))
+
+
+def _array_ptr(a):
+    return None if a is None else a.buffer_info()[0]
 
 
 def _grad_dtype(grads):
@@ -408,17 +415,16 @@ def qlora_clip_grad_norm_batch(grads, max_norm: float, coef=None, norm=None, wor
     dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
     if dev.type != "cuda":
         raise ValueError("grads must be device tensors")
-    numel = [t.numel() for t in grads]
-    gp = _ptr_array(grads, dtype, numel, dev, "grads")
+    numel = list(map(torch.Tensor.numel, grads))
+    gp, sizes = _pointers(grads, dtype, numel, dev, "grads"), array("q", numel)
     coef = coef if coef is not None else torch.empty(1, dtype=torch.float32, device=dev)
     norm = norm if norm is not None else torch.empty(1, dtype=torch.float64, device=dev)
     _need(coef, torch.float32, (1,), "coef")
     _need(norm, torch.float64, (1,), "norm")
     ws = _workspace(QLORA_CLIP_WORKSPACE_BYTES, dev, workspace)
-    _check(_load().qlora_clip_grad_norm_batch(len(grads), gp, gd, (ctypes.c_int64 * len(grads))(*numel),
-                                              float(max_norm), _ptr(coef), _ptr(norm), _ptr(ws),
-                                              ws.numel() * ws.element_size(), _stream(stream)),
-           "qlora_clip_grad_norm_batch")
+    _check(_load().qlora_clip_grad_norm_batch(len(grads), _array_ptr(gp), gd, _array_ptr(sizes), float(max_norm),
+                                              _ptr(coef), _ptr(norm), _ptr(ws), ws.numel() * ws.element_size(),
+                                              _stream(stream)), "qlora_clip_grad_norm_batch")
     return coef, norm
 
 
@@ -434,15 +440,15 @@ def qlora_adamw_batch(thetas, grads, state: AdamWState, step: int, lr: float, be
     thetas, grads = list(thetas), list(grads)
     n = len(thetas)
     gd, gtype = _grad_dtype(grads)
-    numel = [t.numel() for t in thetas]
+    numel = list(map(torch.Tensor.numel, thetas))
     if numel != list(state.numel):
         raise ValueError("the state belongs to tensors of other sizes")
     dev = thetas[0].device if n else torch.device("cuda", torch.cuda.current_device())
     if dev.type != "cuda":
         raise ValueError("thetas must be device tensors")
-    tp = _ptr_array(thetas, torch.float32, numel, dev, "thetas")
-    gp = _ptr_array(grads, gtype, numel, dev, "grads")
-    bp = None if thetas_bf16 is None else _ptr_array(list(thetas_bf16), torch.bfloat16, numel, dev, "thetas_bf16")
+    tp, gp = _pointers(thetas, torch.float32, numel, dev, "thetas"), _pointers(grads, gtype, numel, dev, "grads")
+    bp = None if thetas_bf16 is None else _pointers(list(thetas_bf16), torch.bfloat16, numel, dev, "thetas_bf16")
+    sizes = array("q", numel)
     total = sum([(k + 255) // 256 * 256 for k in numel])
     held = torch.float32 if state.bits == 32 else torch.float8_e4m3fn
     _need_mem(state.m, held, (total,), "state.m")
@@ -456,8 +462,9 @@ def qlora_adamw_batch(thetas, grads, state: AdamWState, step: int, lr: float, be
                     state.m_scale.data_ptr() if state.bits == 8 else None,
                     state.v_scale.data_ptr() if state.bits == 8 else None)
     hp = AdamParams(lr, beta1, beta2, eps, weight_decay, step)
-    _check(_load().qlora_adamw_batch(n, tp, gp, gd, bp, (ctypes.c_int64 * n)(*numel), ctypes.byref(st),
-                                     ctypes.byref(hp), _ptr(coef), _stream(stream)), "qlora_adamw_batch")
+    _check(_load().qlora_adamw_batch(n, _array_ptr(tp), _array_ptr(gp), gd, _array_ptr(bp), _array_ptr(sizes),
+                                     ctypes.byref(st), ctypes.byref(hp), _ptr(coef), _stream(stream)),
+           "qlora_adamw_batch")
 
 
 @_on_stream

@@ -13,6 +13,7 @@ import os
 from array import array
 from dataclasses import dataclass
 from operator import attrgetter
+from typing import NamedTuple
 
 import numpy as np
 
@@ -46,6 +47,7 @@ EXPORTS = (
 )
 # every symbol declared in include/qlora_adapters.h
 ADAPTER_EXPORTS = (
+    "qlora_preference_workspace", "qlora_preference_loss",
     "qlora_adam_state_numel", "qlora_clip_grad_norm_batch", "qlora_adamw_batch",
 )
 QLORA_NOALLOC_SCRATCH_BYTES = (2 << 20) + (64 << 10)
@@ -169,6 +171,10 @@ def _load():
     lib.qlora_probe_read.argtypes = [vp, sz, ctypes.c_uint32, vp, vp]
     lib.qlora_probe_read.restype = ctypes.c_int
     lib.qlora_int8_dequantize.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.qlora_preference_workspace.argtypes = [i64, i64, i64, P(sz)]
+    lib.qlora_preference_loss.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, vp, vp, f32, f32, f32, vp, vp, vp, vp,
+                                          i64, vp, sz, vp]
     lib.qlora_adam_state_numel.argtypes = [ctypes.c_int, P(i64), P(i64)]
     lib.qlora_clip_grad_norm_batch.argtypes = [ctypes.c_int, vp, ctypes.c_int, vp, ctypes.c_float, vp, vp, vp, sz, vp]
     lib.qlora_adamw_batch.argtypes = [ctypes.c_int, vp, vp, ctypes.c_int, vp, vp, P(QAdamState), P(AdamParams), vp, vp]
@@ -337,6 +343,74 @@ def qlora_adam_step(theta, g, m, v, step: int, lr: float, beta1: float = 0.9, be
     hp = AdamParams(lr, beta1, beta2, eps, weight_decay, step)
     _check(_load().qlora_adam_step(_ptr(theta), _ptr(g), _ptr(m), _ptr(v), n, ctypes.byref(hp), _ptr(coef),
                                    _ptr(theta_bf16), _stream(stream)), "qlora_adam_step")
+
+
+# ---- preference loss -----------------------------------------------------------------
+
+class PreferenceOut(NamedTuple):
+    loss: "torch.Tensor"              # float32 [1]
+    rewards: "torch.Tensor"           # float32 [S]
+    logps: "torch.Tensor"             # float32 [S, T]; 0 where the position does not count
+    dlogits: "torch.Tensor | None"    # the logits' dtype and shape
+
+
+def qlora_preference_workspace(pairs: int, T: int, V: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_load().qlora_preference_workspace(pairs, T, V, ctypes.byref(out)), "qlora_preference_workspace")
+    return out.value
+
+
+def _row_stride(t, name):
+    """Elements between the rows of a [S, T, V] tensor whose rows are evenly spaced."""
+    S, T, V = t.shape
+    a, b, c = t.stride()
+    ld = b if T > 1 else a if S > 1 else max(V, 1)
+    if (V > 1 and c != 1) or (S > 1 and T > 1 and a != T * b):
+        raise ValueError(f"{name} must have rows of adjacent values at one stride")
+    return max(ld, V) if S * T <= 1 else ld
+
+
+@_on_stream
+def qlora_preference_loss(logits, labels, ref_logps, beta: float, label_smoothing: float = 0.0,
+                          grad_scale: float = 1.0, need_grad: bool = True, dlogits=None, workspace=None,
+                          stream=None) -> PreferenceOut:
+    """Preference loss of ``logits`` [S, T, V] (float32 or bfloat16; the first
+    S / 2 sequences are the preferred ones of the pairs) against the
+    reference's ``ref_logps`` [S, T], and its gradient. ``labels`` [S, T]
+    (int64): positions outside [0, V) do not count. ``dlogits`` may be the
+    logits themselves."""
+    import torch
+
+    if logits.dim() != 3 or logits.shape[0] % 2:
+        raise ValueError("logits must be [2 pairs, T, V]")
+    S, T, V = logits.shape
+    dt = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}.get(logits.dtype)
+    if dt is None:
+        raise TypeError("logits must be float32 or bfloat16")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor")
+    dev = logits.device
+    ld = _row_stride(logits, "logits")
+    _need(labels, torch.int64, (S, T), "labels")
+    _need(ref_logps, torch.float32, (S, T), "ref_logps")
+    if need_grad:
+        if dlogits is None:
+            dlogits = torch.empty((S, T, V), dtype=logits.dtype, device=dev)
+        if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or dlogits.device != dev:
+            raise ValueError("dlogits must have the logits' dtype, shape and device")
+        ldd = _row_stride(dlogits, "dlogits")
+    else:
+        dlogits, ldd = None, 0
+    if labels.device != dev or ref_logps.device != dev:
+        raise ValueError("labels and ref_logps must be on the logits' device")
+    small = torch.empty(1 + S + S * T, dtype=torch.float32, device=dev)   # loss, rewards, logps
+    loss, rewards, logps = small[:1], small[1:1 + S], small[1 + S:].view(S, T)
+    ws = _workspace(qlora_preference_workspace(S // 2, T, V), dev, workspace)
+    _check(_load().qlora_preference_loss(_ptr(logits), dt, S // 2, T, V, ld, _ptr(labels), _ptr(ref_logps),
+                                         float(beta), float(label_smoothing), float(grad_scale), _ptr(loss),
+                                         _ptr(rewards), _ptr(logps), _ptr(dlogits), ldd, _ptr(ws),
+                                         ws.numel() * ws.element_size(), _stream(stream)), "qlora_preference_loss")
+    return PreferenceOut(loss, rewards, logps, dlogits)
 
 
 # ---- the optimiser step over many tensors -------------------------------------------

@@ -636,6 +636,69 @@ int qlora_adamw_batch(int n, float* const* theta, const void* const* g, qlora_dt
   return e == hipSuccess ? QLORA_OK : hip_fail(e);
 }
 
+// Shapes of a preference loss: S T rows of V logits; rows is S T.
+static int check_preference(int64_t pairs, int64_t T, int64_t V, int64_t* rows) {
+  if (pairs < 0 || T < 0 || V < 1 || pairs > ((int64_t)1 << 20) || T > ((int64_t)1 << 30) || V > ((int64_t)1 << 30))
+    return QLORA_ERR_SHAPE;
+  *rows = 2 * pairs * T;
+  return *rows > 0x7FFFFFFF ? QLORA_ERR_SHAPE : QLORA_OK;
+}
+
+int qlora_preference_workspace(int64_t pairs, int64_t T, int64_t V, size_t* bytes) {
+  if (!bytes) return QLORA_ERR_ARG;
+  int64_t rows = 0;
+  const int st = check_preference(pairs, T, V, &rows);
+  if (st != QLORA_OK) return st;
+  *bytes = qlora::pref_workspace_layout(pairs, T).total;
+  return QLORA_OK;
+}
+
+int qlora_preference_loss(const void* logits, qlora_dtype dtype, int64_t pairs, int64_t T, int64_t V, int64_t ld,
+                          const int64_t* labels, const float* ref_logps, float beta, float label_smoothing,
+                          float grad_scale, float* loss, float* rewards, float* logps, void* dlogits, int64_t ldd,
+                          void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (dtype != QLORA_F32 && dtype != QLORA_BF16) return QLORA_ERR_ARG;
+  if (!isfinite(beta) || !isfinite(grad_scale) || !(label_smoothing >= 0.0f && label_smoothing <= 1.0f))
+    return QLORA_ERR_ARG;
+  int64_t rows = 0;
+  size_t need = 0;
+  int st = check_preference(pairs, T, V, &rows);
+  if (st != QLORA_OK) return st;
+  if (ld < V || (dlogits && ldd < V)) return QLORA_ERR_SHAPE;
+  if (dlogits == logits && dlogits && ldd != ld) return QLORA_ERR_SHAPE;   // in place: the same rows
+  if (!loss || (pairs > 0 && !rewards) || (rows > 0 && (!logits || !labels || !ref_logps || !logps)))
+    return QLORA_ERR_ARG;
+  st = qlora_preference_workspace(pairs, T, V, &need);
+  if (st != QLORA_OK) return st;
+  if (!ws || ws_bytes < need) return QLORA_ERR_WORKSPACE;
+  const uintptr_t elem = dtype == QLORA_F32 ? 3u : 1u;
+  const auto off = [](const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; };
+  if (off(logits, elem) || off(dlogits, elem) || off(labels, 7u) || off(ref_logps, 3u) || off(loss, 3u) ||
+      off(rewards, 3u) || off(logps, 3u) || !aligned16(ws))
+    return QLORA_ERR_ALIGN;
+  qlora::PrefCall c;
+  c.logits = logits;
+  c.bf16 = dtype == QLORA_BF16;
+  c.labels = labels;
+  c.ref = ref_logps;
+  c.S = (int)(2 * pairs);
+  c.T = (int)T;
+  c.V = (int)V;
+  c.ld = ld;
+  c.ldd = ldd;
+  c.beta = beta;
+  c.eps = label_smoothing;
+  c.gscale = grad_scale;
+  c.loss = loss;
+  c.rewards = rewards;
+  c.logps = logps;
+  c.dlogits = dlogits;
+  c.ws = ws;
+  (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
+  const hipError_t e = qlora::launch_preference(c, stream);
+  return e == hipSuccess ? QLORA_OK : hip_fail(e);
+}
+
 int qlora_lora_dropout(const uint16_t* X, int64_t numel, float p, uint64_t seed, uint16_t* Xd, hipStream_t stream) {
   if (!valid_dropout(p)) return QLORA_ERR_ARG;
   if (numel < 0 || (numel % 8) != 0 || numel > ((int64_t)1 << 40)) return QLORA_ERR_SHAPE;

@@ -170,6 +170,38 @@ hipError_t launch_clip_norm_batch(int n, const void* const* g, bool g16, const i
                                   float* coef, double* norm, double* part, hipStream_t stream);
 hipError_t launch_adamw_batch(const AdamBatch& b, const AdamHyper& h, const float* coef, hipStream_t stream);
 
+// Preference loss over pairs of sequences (preference.hip). S = 2 pairs; rows
+// of V logits (element strides ld, ldd).
+struct PrefWorkspace {
+  size_t stat_off;     // fp32 pairs [S T]: maximum and inverse sum of each row
+  size_t pair_off;     // fp64 [S / 2]: the pairs' losses
+  size_t weight_off;   // fp32 [S]: the sequences' gradient weights
+  size_t total;
+};
+inline PrefWorkspace pref_workspace_layout(int64_t pairs, int64_t T) {
+  PrefWorkspace L;
+  L.stat_off = 0;
+  L.pair_off = align_up((size_t)(2 * pairs * T) * 8, 256);
+  L.weight_off = L.pair_off + align_up((size_t)pairs * 8, 256);
+  L.total = L.weight_off + align_up((size_t)pairs * 8 + 1, 256);
+  return L;
+}
+struct PrefCall {
+  const void* logits;
+  bool bf16;
+  const int64_t* labels;
+  const float* ref;
+  int S, T, V;
+  int64_t ld, ldd;
+  float beta, eps, gscale;
+  float* loss;
+  float* rewards;
+  float* logps;
+  void* dlogits;              // or nullptr
+  void* ws;
+};
+hipError_t launch_preference(const PrefCall& c, hipStream_t stream);
+
 // Adapter merge into the bf16 dequantised base (merge.hip).
 hipError_t launch_merge(const NF4View& W, const NF4Table& tab, const uint16_t* L1, const uint16_t* L2, int r,
                         float s, uint16_t* out, hipStream_t stream);

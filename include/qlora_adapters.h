@@ -19,6 +19,40 @@ extern "C" {
 #endif
 
 /*
+ * qlora_preference_loss: a loss over pairs of sequences from the paired log
+ * ratios of a policy and a reference, and the gradient of the policy's logits
+ * (Rafailov et al., "Direct Preference Optimization", NeurIPS 2023, eq. 7).
+ * Sequences s = 0 .. pairs - 1 are the preferred ones, s + pairs the other one
+ * of the same pair; S = 2 pairs.
+ *   lp[s][t]  = logits[s][t][y] - log sum_v exp(logits[s][t][v]),  y = labels[s][t]
+ *   reward[s] = beta sum_t (lp[s][t] - ref_logps[s][t]) over the counted t
+ *   h_p       = reward[p] - reward[pairs + p]
+ *   loss      = 1 / pairs sum_p (1 - e) softplus(-h_p) + e softplus(h_p)   (0 without pairs)
+ *   dlogits   = grad_scale d loss / d logits
+ * A position counts when its label lies in [0, V); the others' logits and
+ * references are not used, their lp is 0 and their gradient rows are zero. A
+ * sequence may have no counted position. -inf logits take no probability.
+ *   logits     device, dtype, rows [s T + t] of V values, ld >= V elements
+ *              apart; any element alignment.
+ *   labels     device int64 [S T]: the token that row (s, t) predicts.
+ *   ref_logps  device fp32 [S T]: the reference's lp.
+ *   label_smoothing  e in [0, 1].  grad_scale: the upstream gradient.
+ *   loss [1], rewards [S], logps [S T]: device fp32.
+ *   dlogits    device, dtype, rows ldd >= V elements apart, written once; NULL
+ *              for the loss alone. It may be logits itself (then ldd == ld), and
+ *              otherwise does not overlap them.
+ *   ws         qlora_preference_workspace bytes.
+ * exp and the sum of a row are fp32 around the row's running maximum, rewards
+ * and loss float64 sums in a fixed order, the gradient is rounded once to dtype.
+ * Limits: pairs <= 2^20, T and V <= 2^30, S T <= 2^31 - 1.
+ */
+int qlora_preference_workspace(int64_t pairs, int64_t T, int64_t V, size_t *bytes);
+int qlora_preference_loss(const void *logits, qlora_dtype dtype, int64_t pairs, int64_t T, int64_t V, int64_t ld,
+                          const int64_t *labels, const float *ref_logps, float beta, float label_smoothing,
+                          float grad_scale, float *loss, float *rewards, float *logps, void *dlogits, int64_t ldd,
+                          void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
  * The optimiser step over many tensors at once: the adapters as they were
  * allocated, one (dL1, dL2) pair per linear, with no copy into a flat vector.
  * theta[k], g[k], theta_bf16[k] are host arrays of n device pointers, numel[k]

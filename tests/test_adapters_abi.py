@@ -109,3 +109,31 @@ def test_adamw_batch_refusals(lib):
     assert call(vs=P + 2) == E.QLORA_ERR_ALIGN
     assert call(coef=P + 1) == E.QLORA_ERR_ALIGN
     assert lib.qlora_adamw_batch(1, ptrs(P), ptrs(P), 0, None, sizes(8), None, None, None, None) == E.QLORA_ERR_ARG
+
+
+def test_preference_refusals(lib):
+    n = ctypes.c_size_t()
+    for pairs, T, V in ((0, 0, 1), (1, 1, 1), (3, 100, 32000), (1 << 20, 1, 7)):
+        assert lib.qlora_preference_workspace(pairs, T, V, ctypes.byref(n)) == api.QLORA_OK
+        assert n.value >= 8 * pairs * T + 8 * pairs
+    for pairs, T, V in ((-1, 1, 1), (1, -1, 1), (1, 1, 0), ((1 << 20) + 1, 1, 1), (1 << 15, 1 << 15, 8), (1, 1, (1 << 30) + 1)):
+        assert lib.qlora_preference_workspace(pairs, T, V, ctypes.byref(n)) == api.QLORA_ERR_SHAPE, (pairs, T, V)
+    assert lib.qlora_preference_workspace(1, 1, 1, None) == api.QLORA_ERR_ARG
+
+    def call(x=P, dt=0, pairs=1, T=2, V=8, ld=8, lab=P, ref=P, beta=0.1, eps=0.0, gs=1.0, loss=P, rew=P, lp=P,
+             dx=2 * P, ldd=8, ws=P, wsb=1 << 20):
+        return lib.qlora_preference_loss(x, dt, pairs, T, V, ld, lab, ref, beta, eps, gs, loss, rew, lp, dx, ldd, ws,
+                                         wsb, None)
+
+    E = api
+    for bad in (dict(dt=5), dict(beta=float("inf")), dict(eps=-0.1), dict(eps=1.1), dict(eps=float("nan")),
+                dict(gs=float("nan")), dict(x=None), dict(lab=None), dict(ref=None), dict(loss=None),
+                dict(rew=None), dict(lp=None)):
+        assert call(**bad) == E.QLORA_ERR_ARG, bad
+    for bad in (dict(pairs=-1), dict(V=0), dict(ld=7), dict(ldd=7), dict(dx=P, ldd=9)):
+        assert call(**bad) == E.QLORA_ERR_SHAPE, bad
+    for bad in (dict(ws=None), dict(wsb=16)):
+        assert call(**bad) == E.QLORA_ERR_WORKSPACE, bad
+    for bad in (dict(x=P + 2), dict(dx=P + 1), dict(lab=P + 4), dict(ref=P + 2), dict(lp=P + 1), dict(ws=P + 8),
+                dict(dt=1, x=P + 1)):
+        assert call(**bad) == E.QLORA_ERR_ALIGN, bad

@@ -47,6 +47,7 @@ EXPORTS = (
 )
 # every symbol declared in include/qlora_adapters.h
 ADAPTER_EXPORTS = (
+    "qlora_linear_multi_workspace", "qlora_linear_multi_fwd", "qlora_linear_multi_bwd",
     "qlora_preference_workspace", "qlora_preference_loss",
     "qlora_adam_state_numel", "qlora_clip_grad_norm_batch", "qlora_adamw_batch",
 )
@@ -172,6 +173,11 @@ def _load():
     lib.qlora_probe_read.restype = ctypes.c_int
     lib.qlora_int8_dequantize.restype = ctypes.c_int
     f32 = ctypes.c_float
+    lib.qlora_linear_multi_workspace.argtypes = [i64, i64, i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, P(sz)]
+    lib.qlora_linear_multi_fwd.argtypes = [P(QNF4), vp, i64, vp, ctypes.c_int, vp, vp, ctypes.c_int, vp, vp, vp, vp,
+                                           sz, vp]
+    lib.qlora_linear_multi_bwd.argtypes = [P(QNF4), vp, vp, i64, vp, ctypes.c_int, vp, vp, ctypes.c_int, vp, vp, vp,
+                                           vp, vp, ctypes.c_int, vp, sz, vp]
     lib.qlora_preference_workspace.argtypes = [i64, i64, i64, P(sz)]
     lib.qlora_preference_loss.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, vp, vp, f32, f32, f32, vp, vp, vp, vp,
                                           i64, vp, sz, vp]
@@ -927,6 +933,89 @@ def qlora_linear_bwd(q: NF4Tensor, X, dY, L1, L2, scale: float, T=None, need_dX:
                                                 float(scale), float(p), int(seed), _ptr(T), _ptr(dX), _ptr(dL1),
                                                 _ptr(dL2), gd, _ptr(ws), ws.numel() * ws.element_size(),
                                                 _stream(stream)), "qlora_linear_bwd_dropout")
+    return dX, dL1, dL2
+
+
+# ---- the linear with an adapter per row ---------------------------------------------
+
+def qlora_linear_multi_workspace(M: int, K: int, N: int, r: int, n_adapters: int, backward: bool = False) -> int:
+    out = ctypes.c_size_t()
+    _check(_load().qlora_linear_multi_workspace(M, K, N, r, n_adapters, int(backward), ctypes.byref(out)),
+           "qlora_linear_multi_workspace")
+    return out.value
+
+
+def _need_multi(q, X, row_adapter, L1, L2, scale):
+    """Shared argument checks; returns (M, K, N, r, adapters)."""
+    import torch
+
+    if X.dim() != 2 or L1.dim() != 3:
+        raise ValueError("X must be [M, K] and L1 [adapters, K, r]")
+    M, K = X.shape
+    N, (A, _, r) = q.rows, L1.shape
+    if K != q.cols:
+        raise ValueError("X columns must equal the weight's in_features")
+    _need(X, torch.bfloat16, (M, K), "X")
+    _need(row_adapter, torch.int32, (M,), "row_adapter")
+    _need(L1, torch.bfloat16, (A, K, r), "L1")
+    _need(L2, torch.bfloat16, (A, r, N), "L2")
+    _need(scale, torch.float32, (A,), "scale")
+    return M, K, N, r, A
+
+
+@_on_stream
+def qlora_linear_multi_fwd(q: NF4Tensor, X, row_adapter, L1, L2, scale, want_T: bool = False, Y=None, T_out=None,
+                           workspace=None, stream=None):
+    """Y[m] = X[m] dequant(Wt)^T + scale[a] (X[m] L1[a]) L2[a], a = row_adapter[m] (int32 [M]; an id outside
+    [0, adapters) gives the base alone), L1 [adapters, K, r], L2 [adapters, r, N], scale float32 [adapters];
+    returns (Y, T) with T = bf16(X[m] L1[a]) or None."""
+    import torch
+
+    M, K, N, r, A = _need_multi(q, X, row_adapter, L1, L2, scale)
+    Y = Y if Y is not None else torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
+    _need(Y, torch.bfloat16, (M, N), "Y")
+    if want_T and T_out is None:
+        T_out = torch.empty((M, r), dtype=torch.bfloat16, device=X.device)
+    if T_out is not None:
+        _need(T_out, torch.bfloat16, (M, r), "T_out")
+    st = q.struct()
+    ws = _workspace(qlora_linear_multi_workspace(M, K, N, r, A), X.device, workspace)
+    _check(_load().qlora_linear_multi_fwd(ctypes.byref(st), _ptr(X), M, _ptr(row_adapter), A, _ptr(L1), _ptr(L2), r,
+                                          _ptr(scale), _ptr(Y), _ptr(T_out), _ptr(ws),
+                                          ws.numel() * ws.element_size(), _stream(stream)), "qlora_linear_multi_fwd")
+    return Y, T_out
+
+
+@_on_stream
+def qlora_linear_multi_bwd(q: NF4Tensor, X, dY, row_adapter, L1, L2, scale, T=None, need_dX: bool = True,
+                           grad_dtype=None, dX=None, dL1=None, dL2=None, workspace=None, stream=None):
+    """Returns (dX or None, dL1, dL2) of qlora_linear_multi_fwd for upstream gradient dY; dL1 and dL2 have
+    the shapes of L1 and L2 (zeros for adapters without rows)."""
+    import torch
+
+    grad_dtype = torch.float32 if grad_dtype is None else grad_dtype
+    if grad_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("grad_dtype must be float32 or bfloat16")
+    M, K, N, r, A = _need_multi(q, X, row_adapter, L1, L2, scale)
+    _need(dY, torch.bfloat16, (M, N), "dY")
+    if T is not None:
+        _need(T, torch.bfloat16, (M, r), "T")
+    if need_dX:
+        dX = dX if dX is not None else torch.empty((M, K), dtype=torch.bfloat16, device=X.device)
+        _need(dX, torch.bfloat16, (M, K), "dX")
+    else:
+        dX = None
+    dL1 = dL1 if dL1 is not None else torch.empty((A, K, r), dtype=grad_dtype, device=X.device)
+    dL2 = dL2 if dL2 is not None else torch.empty((A, r, N), dtype=grad_dtype, device=X.device)
+    _need(dL1, grad_dtype, (A, K, r), "dL1")
+    _need(dL2, grad_dtype, (A, r, N), "dL2")
+    st = q.struct()
+    gd = QLORA_F32 if grad_dtype == torch.float32 else QLORA_BF16
+    ws = _workspace(qlora_linear_multi_workspace(M, K, N, r, A, True), X.device, workspace)
+    _check(_load().qlora_linear_multi_bwd(ctypes.byref(st), _ptr(X), _ptr(dY), M, _ptr(row_adapter), A, _ptr(L1),
+                                          _ptr(L2), r, _ptr(scale), _ptr(T), _ptr(dX), _ptr(dL1), _ptr(dL2), gd,
+                                          _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "qlora_linear_multi_bwd")
     return dX, dL1, dL2
 
 

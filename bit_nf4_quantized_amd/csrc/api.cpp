@@ -26,6 +26,9 @@ int hip_fail(hipError_t e) {
   return QLORA_ERR_HIP;
 }
 
+static_assert(qlora::kMultiMaxRows == QLORA_MULTI_MAX_ROWS && qlora::kMultiMaxAdapters == QLORA_MULTI_MAX_ADAPTERS,
+              "limits of the header and of the kernels");
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // N(0,1) quantile by bisection on the CDF 1/2 erfc(-x / sqrt 2), to full
@@ -633,6 +636,70 @@ int qlora_adamw_batch(int n, float* const* theta, const void* const* g, qlora_dt
   const qlora::AdamHyper h = adam_hyper(hp);
   (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
   const hipError_t e = qlora::launch_adamw_batch(b, h, coef, stream);
+  return e == hipSuccess ? QLORA_OK : hip_fail(e);
+}
+
+// Arguments shared by the linears with an adapter per row (every pointer but
+// the workspace that must be there and aligned; counts last).
+static int check_multi(const qlora_nf4* W, const void* X, int64_t M, const int32_t* row_adapter, int n_adapters,
+                       const void* L1, const void* L2, int r, const float* scale) {
+  const int st = check_linear(W, M, r, 1.0f);
+  if (st != QLORA_OK) return st;
+  if (n_adapters < 1 || n_adapters > QLORA_MULTI_MAX_ADAPTERS || !L1 || !L2 || !scale) return QLORA_ERR_ARG;
+  if (M > QLORA_MULTI_MAX_ROWS) return QLORA_ERR_SHAPE;
+  if (M > 0 && (!X || !row_adapter)) return QLORA_ERR_ARG;
+  if (!aligned16(X) || !aligned16(L1) || !aligned16(L2) || (reinterpret_cast<uintptr_t>(row_adapter) & 3u) ||
+      (reinterpret_cast<uintptr_t>(scale) & 3u))
+    return QLORA_ERR_ALIGN;
+  return QLORA_OK;
+}
+
+int qlora_linear_multi_workspace(int64_t M, int64_t K, int64_t N, int r, int n_adapters, int backward,
+                                 size_t* bytes) {
+  if (!bytes || n_adapters < 1 || n_adapters > QLORA_MULTI_MAX_ADAPTERS) return QLORA_ERR_ARG;
+  const int st = qlora_linear_workspace(M < 0 ? -1 : 0, K, N, r, bytes);   // the rules of the single linear
+  if (st != QLORA_OK) return st;
+  if (M > QLORA_MULTI_MAX_ROWS) return QLORA_ERR_SHAPE;
+  *bytes = qlora::multi_workspace_layout(M, K, N, r, n_adapters, backward != 0).total;
+  return QLORA_OK;
+}
+
+int qlora_linear_multi_fwd(const qlora_nf4* W, const uint16_t* X, int64_t M, const int32_t* row_adapter,
+                           int n_adapters, const uint16_t* L1, const uint16_t* L2, int r, const float* scale,
+                           uint16_t* Y, uint16_t* T_out, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const int st = check_multi(W, X, M, row_adapter, n_adapters, L1, L2, r, scale);
+  if (st != QLORA_OK) return st;
+  if (M == 0) return QLORA_OK;
+  if (!Y) return QLORA_ERR_ARG;
+  if (!ws) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(Y) || !aligned16(T_out) || !aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (!qlora::multi_forward_supported(M, W->cols, W->rows, r)) return QLORA_ERR_SHAPE;
+  if (ws_bytes < qlora::multi_workspace_layout(M, W->cols, W->rows, r, n_adapters, false).total)
+    return QLORA_ERR_WORKSPACE;
+  (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
+  const hipError_t e = qlora::multi_forward(view_of(W), tables(W->qtype).tab, X, M, row_adapter, n_adapters, L1, L2,
+                                            r, scale, Y, T_out, ws, stream);
+  return e == hipSuccess ? QLORA_OK : hip_fail(e);
+}
+
+int qlora_linear_multi_bwd(const qlora_nf4* W, const uint16_t* X, const uint16_t* dY, int64_t M,
+                           const int32_t* row_adapter, int n_adapters, const uint16_t* L1, const uint16_t* L2, int r,
+                           const float* scale, const uint16_t* T, uint16_t* dX, void* dL1, void* dL2,
+                           qlora_dtype grad_dtype, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const int st = check_multi(W, X, M, row_adapter, n_adapters, L1, L2, r, scale);
+  if (st != QLORA_OK) return st;
+  if (grad_dtype != QLORA_F32 && grad_dtype != QLORA_BF16) return QLORA_ERR_ARG;
+  if (!dL1 || !dL2 || (M > 0 && !dY)) return QLORA_ERR_ARG;
+  if (!ws) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(dY) || !aligned16(T) || !aligned16(dX) || !aligned16(dL1) || !aligned16(dL2) || !aligned16(ws))
+    return QLORA_ERR_ALIGN;
+  if (!qlora::multi_dense_supported(W->cols, W->rows, r)) return QLORA_ERR_SHAPE;
+  if (ws_bytes < qlora::multi_workspace_layout(M, W->cols, W->rows, r, n_adapters, true).total)
+    return QLORA_ERR_WORKSPACE;
+  (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
+  const hipError_t e =
+      qlora::multi_backward(view_of(W), tables(W->qtype).tab, X, dY, M, row_adapter, n_adapters, L1, L2, r, scale, T,
+                            dX, dL1, dL2, grad_dtype == QLORA_BF16, ws, stream);
   return e == hipSuccess ? QLORA_OK : hip_fail(e);
 }
 

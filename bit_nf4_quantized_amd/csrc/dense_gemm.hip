@@ -122,8 +122,10 @@ struct StageOffsets {
 
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 
+// perm (optional): the rows are taken through this list.
 template <int NI>
-__device__ __forceinline__ StageOffsets<NI> stage_offsets(int64_t ld, int64_t row0, int64_t nrows) {
+__device__ __forceinline__ StageOffsets<NI> stage_offsets(int64_t ld, int64_t row0, int64_t nrows,
+                                                          const int32_t* perm = nullptr) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lr = lane >> 3;
   StageOffsets<NI> o;
@@ -133,6 +135,7 @@ __device__ __forceinline__ StageOffsets<NI> stage_offsets(int64_t ld, int64_t ro
     const int chunk = (lane & 7) ^ swz(rloc);
     int64_t r = row0 + rloc;
     if (r > nrows - 1) r = nrows - 1;
+    if (perm) r = perm[r];
     o.off[j] = (uint32_t)((r * ld + chunk * 8) * 2);
   }
   return o;
@@ -159,18 +162,38 @@ __device__ __forceinline__ void stage_load(const uint16_t* __restrict__ P, const
   for (int j = 0; j < NI; ++j) stage_load_one(P, o, lds, j);
 }
 
+// A wave-uniform address in scalar registers, as the copies take it.
+__device__ __forceinline__ const uint16_t* uniform(const uint16_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<const uint16_t*>(lo | (hi << 32));
+}
+
 __device__ __forceinline__ int lds_off(int row, int chunk) { return row * TK + ((chunk ^ swz(row)) << 3); }
 
 // One TMX x TN output tile at (m0, n0). smem holds the stage tiles: two A
-// buffers, then three B buffers, kStageElems elements each.
-template <bool ADD, int TMX>
-__device__ __forceinline__ void gemm_tile(const DenseArgs& p, int64_t m0, int64_t n0, uint16_t* smem) {
+// buffers, then three B buffers, kStageElems elements each. MULTI: the tile's
+// rows are rows m0 .. of the grouped order, and the slab has the K2 columns of
+// every segment that meets them, with zeros (slab.zero_row) in the place of
+// the other segments' rows.
+template <bool ADD, int TMX, bool MULTI>
+__device__ __forceinline__ void gemm_tile(const DenseArgs& p, const MultiSlab& slab, int64_t m0, int64_t n0,
+                                          uint16_t* smem) {
   using S = TileShape<TMX>;
   constexpr int WTM = S::kWtm, MI = S::kMi;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / WGN, wn = wave % WGN;
-  const int nmain = (int)(p.K / TK), nslab = (int)(p.K2 / TK);
+  const int nmain = (int)(p.K / TK);
+  int nslab = (int)(p.K2 / TK), seg0 = 0;
+  const int per_seg = nslab;                        // slab stages per segment (MULTI)
+  if constexpr (MULTI) {
+    const RouteRange rg = route_range(slab.rv, (int)m0, (int)m0 + TMX);
+    seg0 = rg.lo;
+    nslab = (rg.hi > rg.lo ? rg.hi - rg.lo : 0) * per_seg;
+  }
   const int nk = nmain + nslab;
+  const int32_t* perm = MULTI ? slab.rv.perm : nullptr;
 
   f32x16_t acc[MI][NJ];
 #pragma unroll
@@ -180,43 +203,71 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, int64_t m0, int64_
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-  const StageOffsets<S::kIpwA> offA = stage_offsets<S::kIpwA>(p.lda, m0, p.M);
+  const StageOffsets<S::kIpwA> offA = stage_offsets<S::kIpwA>(p.lda, m0, p.M, perm);
   const StageOffsets<S::kIpwB> offB = stage_offsets<S::kIpwB>(p.ldb, n0, p.N);
-  const StageOffsets<S::kIpwA> offA2 = stage_offsets<S::kIpwA>(p.ld2, m0, p.M);
+  const StageOffsets<S::kIpwA> offA2 = stage_offsets<S::kIpwA>(p.ld2, m0, p.M, perm);
   const StageOffsets<S::kIpwB> offB2 = stage_offsets<S::kIpwB>(p.ld2, n0, p.N);
   // Stage st covers columns [64 st, 64 st + 64) of (A, B) for st < nmain,
   // then the slab (A2, B2). Operand selection is branch-free so that the
   // copy can be scheduled among the MFMAs of the same block.
+  // MULTI: slab stage i's segment and first column, A2's copy instruction j
+  // of it, and its operand B2
+  auto slab_at = [&](int i, int* col) {
+    const int s = __builtin_amdgcn_readfirstlane(i / per_seg);
+    *col = (i - s * per_seg) * TK;
+    return seg0 + s;
+  };
+  auto slab_a = [&](int k, int j) -> uint32_t {
+    const int rloc = (wave * S::kIpwA + j) * RPI + (lane >> 3);
+    const int row = (int)m0 + rloc;
+    const bool in = row >= slab.rv.start[k] && row < slab.rv.start[k + 1];
+    const uint32_t chunk = (uint32_t)((lane & 7) ^ swz(rloc));
+    return in ? offA2.off[j] : (uint32_t)((slab.zero_row * p.ld2 + chunk * 8) * 2);
+  };
+  auto slab_b = [&](int k) -> const uint16_t* {
+    int a = __builtin_amdgcn_readfirstlane(slab.rv.adapter[k]);
+    if (slab.slot) a = __builtin_amdgcn_readfirstlane(slab.slot[a]);
+    return p.B2 + (int64_t)a * slab.b2_stride;
+  };
   auto a_buf = [&](int st) { return smem + (st & 1) * kStageElems; };
   auto b_buf = [&](int st) { return smem + (2 + st % 3) * kStageElems; };
-  auto issue = [&](int st) {
-    const bool slab = st >= nmain;
-    const int64_t k0 = (int64_t)(slab ? st - nmain : st) * TK;
-    StageOffsets<S::kIpwA> oa;
-    StageOffsets<S::kIpwB> ob;
-#pragma unroll
-    for (int j = 0; j < S::kIpwA; ++j) oa.off[j] = slab ? offA2.off[j] : offA.off[j];
-#pragma unroll
-    for (int j = 0; j < S::kIpwB; ++j) ob.off[j] = slab ? offB2.off[j] : offB.off[j];
-    stage_load((slab ? p.A2 : p.A) + k0, oa, a_buf(st));
-    stage_load((slab ? p.B2 : p.B) + k0, ob, b_buf(st));
-  };
   // copy instruction q of stage st: q < kIpwA are the A tile's, the rest
-  // the B tile's
-  auto issue_one = [&](int st, int q) {
-    const bool slab = st >= nmain;
-    const int64_t k0 = (int64_t)(slab ? st - nmain : st) * TK;
-    if (q < S::kIpwA) {
-      StageOffsets<S::kIpwA> oa;
-#pragma unroll
-      for (int j = 0; j < S::kIpwA; ++j) oa.off[j] = slab ? offA2.off[j] : offA.off[j];
-      stage_load_one((slab ? p.A2 : p.A) + k0, oa, a_buf(st), q);
+  // the B tile's. in_slab: whether st may be a slab stage (MULTI, where the
+  // two kinds run in loops of their own).
+  auto issue_one = [&](int st, int q, bool in_slab) {
+    if constexpr (MULTI) {
+      int k = 0, k0 = st * TK;
+      if (in_slab) k = slab_at(st - nmain, &k0);
+      if (q < S::kIpwA) {
+        StageOffsets<S::kIpwA> oa;
+        oa.off[q] = in_slab ? slab_a(k, q) : offA.off[q];
+        stage_load_one(uniform((in_slab ? p.A2 : p.A) + k0), oa, a_buf(st), q);
+      } else {
+        StageOffsets<S::kIpwB> ob;
+        const int j = q - S::kIpwA;
+        ob.off[j] = in_slab ? offB2.off[j] : offB.off[j];
+        stage_load_one(uniform((in_slab ? slab_b(k) : p.B) + k0), ob, b_buf(st), j);
+      }
     } else {
-      StageOffsets<S::kIpwB> ob;
+      const bool slab2 = st >= nmain;
+      const int64_t k0 = (int64_t)(slab2 ? st - nmain : st) * TK;
+      if (q < S::kIpwA) {
+        StageOffsets<S::kIpwA> oa;
 #pragma unroll
-      for (int j = 0; j < S::kIpwB; ++j) ob.off[j] = slab ? offB2.off[j] : offB.off[j];
-      stage_load_one((slab ? p.B2 : p.B) + k0, ob, b_buf(st), q - S::kIpwA);
+        for (int j = 0; j < S::kIpwA; ++j) oa.off[j] = slab2 ? offA2.off[j] : offA.off[j];
+        stage_load_one((slab2 ? p.A2 : p.A) + k0, oa, a_buf(st), q);
+      } else {
+        StageOffsets<S::kIpwB> ob;
+#pragma unroll
+        for (int j = 0; j < S::kIpwB; ++j) ob.off[j] = slab2 ? offB2.off[j] : offB.off[j];
+        stage_load_one((slab2 ? p.B2 : p.B) + k0, ob, b_buf(st), q - S::kIpwA);
+      }
     }
+  };
+  auto issue = [&](int st) {
+    const bool in_slab = st >= nmain;
+#pragma unroll
+    for (int q = 0; q < S::kIpwA + S::kIpwB; ++q) issue_one(st, q, in_slab);
   };
   bf16x8_t fa[2][MI], fb[2][NJ];  // two register sets of k-step fragments
   auto frag = [&](int st, int kk, int set) {
@@ -262,7 +313,7 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, int64_t m0, int64_
   // The MFMAs of one k-step (register set `set`) with copy instructions
   // first .. first+cnt-1 of stage cst spread evenly among them (the order is
   // pinned: the scheduler would otherwise bunch them).
-  auto mma_copies = [&](int set, int cst, int first, int cnt, bool on) {
+  auto mma_copies = [&](int set, int cst, int first, int cnt, bool on, bool in_slab) {
     constexpr int nm = MI * NJ;
 #pragma unroll
     for (int q = 0; q < nm; ++q) {
@@ -270,7 +321,7 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, int64_t m0, int64_
           __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][q / NJ], fb[set][q % NJ], acc[q / NJ][q % NJ], 0, 0, 0);
 #pragma unroll
       for (int c = 0; c < cnt; ++c)
-        if (on && (c * nm) / cnt == q) issue_one(cst, first + c);
+        if (on && (c * nm) / cnt == q) issue_one(cst, first + c, in_slab);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -278,12 +329,12 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, int64_t m0, int64_
   // copies of stages st+1 (complete or in flight) and st+2 (the B tile, in
   // flight: the A tile goes out after this stage's barrier) were issued.
   // The prologue issued all of stages 0 and 1.
-  auto stage = [&](int st, bool refill, bool next) {
+  auto stage = [&](int st, bool refill, bool next, bool in_slab) {
 #pragma unroll
     for (int kk = 0; kk < TK / 16 - 1; ++kk) {
       frag(st, kk + 1, (kk + 1) & 1);
       if (kk == 1) {
-        mma_copies(1, st + 2, S::kIpwA, S::kIpwB, refill);  // B tile of stage st+2
+        mma_copies(1, st + 2, S::kIpwA, S::kIpwB, refill, in_slab);  // B tile of stage st+2
       } else {
         mma(kk & 1);
         order();
@@ -299,7 +350,7 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, int64_t m0, int64_
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
     if (next) frag(st + 1, 0, 0);
-    mma_copies(1, st + 2, 0, S::kIpwA, refill);  // A tile of stage st+2
+    mma_copies(1, st + 2, 0, S::kIpwA, refill, in_slab);  // A tile of stage st+2
   };
   if (nk > 0) issue(0);
   if (nk > 1) issue(1);
@@ -310,9 +361,12 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, int64_t m0, int64_
     frag(0, 0, 0);
   }
   int st = 0;
-  for (; st + 2 < nk; ++st) stage(st, true, true);
-  if (st + 1 < nk) stage(st++, false, true);
-  if (st < nk) stage(st, false, false);
+  if constexpr (MULTI) {  // stages whose copies (for st + 2) come from the main operands, then from the slab
+    for (; st + 2 < nmain; ++st) stage(st, true, true, false);
+  }
+  for (; st + 2 < nk; ++st) stage(st, true, true, true);
+  if (st + 1 < nk) stage(st++, false, true, true);
+  if (st < nk) stage(st, false, false, true);
 
   if constexpr (ADD) {
     // Epilogue with an fp32 addend: each wave stages a quarter of its 128 x 64
@@ -387,14 +441,15 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, int64_t m0, int64_
       const u32x4_t val = *reinterpret_cast<const u32x4_t*>(ep + r * kEpiStride + ch * 8);
       const int64_t row = row_base + h * 32 * RB + r;
       const int64_t col = col_base + ch * 8;
-      if (row < p.M && col < p.N) *reinterpret_cast<u32x4_t*>(p.C + row * p.ldc + col) = val;
+      if (row < p.M && col < p.N)
+        *reinterpret_cast<u32x4_t*>(p.C + (MULTI ? (int64_t)perm[row] : row) * p.ldc + col) = val;
     }
     __builtin_amdgcn_s_waitcnt(0xc07f);  // reads of this half done before the next half overwrites it
   }
 }
 
-template <bool ADD>
-__global__ __launch_bounds__(kThreads, 1) void gemm_nt_kernel(DenseArgs p) {
+template <bool ADD, bool MULTI>
+__device__ __forceinline__ void gemm_nt_body(const DenseArgs& p, const MultiSlab& slab) {
   __shared__ __attribute__((aligned(1024))) uint16_t smem[5 * kStageElems];  // A x 2, B x 3
   const int bid = blockIdx.x;
   const int nfull = p.tiles_m * p.full_n;
@@ -411,7 +466,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_kernel(DenseArgs p) {
     const int tl = t - g * group * p.full_n;
     const int tm = first_m + tl % gm;
     const int tn = tl / gm;
-    gemm_tile<ADD, TM>(p, (int64_t)tm * TM, (int64_t)tn * TN, smem);
+    gemm_tile<ADD, TM, MULTI>(p, slab, (int64_t)tm * TM, (int64_t)tn * TN, smem);
   } else {
     // the tail tile-columns, as half- or quarter-height tiles; dispatched
     // last, they fill the last round of workgroups
@@ -421,10 +476,19 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_kernel(DenseArgs p) {
     if (m0 >= p.M) return;  // a piece of a last tile-row beyond M (uniform per workgroup)
     const int64_t n0 = (int64_t)(p.full_n + h % ncols) * TN;
     if (p.tail_split == 4)
-      gemm_tile<ADD, TM / 4>(p, m0, n0, smem);
+      gemm_tile<ADD, TM / 4, MULTI>(p, slab, m0, n0, smem);
     else
-      gemm_tile<ADD, TM / 2>(p, m0, n0, smem);
+      gemm_tile<ADD, TM / 2, MULTI>(p, slab, m0, n0, smem);
   }
+}
+
+template <bool ADD>
+__global__ __launch_bounds__(kThreads, 1) void gemm_nt_kernel(DenseArgs p) {
+  gemm_nt_body<ADD, false>(p, MultiSlab{});
+}
+
+__global__ __launch_bounds__(kThreads, 1) void gemm_nt_multi_kernel(DenseArgs p, MultiSlab slab) {
+  gemm_nt_body<false, true>(p, slab);
 }
 
 // Wd[n][k] for the forward product, the standalone dequant arithmetic
@@ -521,18 +585,10 @@ hipError_t launch_dequant_cols(const NF4View& W, const NF4Table& tab, uint16_t* 
 
 namespace {
 
-// One launch over all M rows (row offsets of A and A2 below 4 GB).
-hipError_t launch_gemm_nt_rows(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N,
-                               int64_t K, const uint16_t* A2, const uint16_t* B2, int64_t ld2, int64_t K2,
-                               uint16_t* C, int64_t ldc, float alpha, hipStream_t stream, const float* E,
-                               int64_t lde) {
-  DenseArgs p;
-  p.A = A; p.B = B; p.A2 = A2; p.B2 = B2; p.C = C;
-  p.lda = lda; p.ldb = ldb; p.ld2 = ld2; p.ldc = ldc;
-  p.M = M; p.N = N; p.K = K; p.K2 = K2; p.alpha = alpha;
-  p.tiles_m = (int)((M + TM - 1) / TM);
-  p.tiles_n = (int)((N + TN - 1) / TN);
-  p.E = E; p.lde = lde;
+// Tile counts and the tail's split for p's M and N; returns the workgroups.
+int plan_tiles(DenseArgs& p) {
+  p.tiles_m = (int)((p.M + TM - 1) / TM);
+  p.tiles_n = (int)((p.N + TN - 1) / TN);
   // One workgroup per CU at a time. When the last round of tiles would
   // leave at least half of the CUs idle, the last tile-columns that hold
   // those tiles run as quarter-height tiles if those fit in one round, else
@@ -552,7 +608,20 @@ hipError_t launch_gemm_nt_rows(const uint16_t* A, int64_t lda, const uint16_t* B
     }
   }
   p.full_n = p.tiles_n - tail_cols;
-  const int ntiles = p.tiles_m * p.full_n + p.tail_split * p.tiles_m * tail_cols;
+  return p.tiles_m * p.full_n + p.tail_split * p.tiles_m * tail_cols;
+}
+
+// One launch over all M rows (row offsets of A and A2 below 4 GB).
+hipError_t launch_gemm_nt_rows(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N,
+                               int64_t K, const uint16_t* A2, const uint16_t* B2, int64_t ld2, int64_t K2,
+                               uint16_t* C, int64_t ldc, float alpha, hipStream_t stream, const float* E,
+                               int64_t lde) {
+  DenseArgs p;
+  p.A = A; p.B = B; p.A2 = A2; p.B2 = B2; p.C = C;
+  p.lda = lda; p.ldb = ldb; p.ld2 = ld2; p.ldc = ldc;
+  p.M = M; p.N = N; p.K = K; p.K2 = K2; p.alpha = alpha;
+  p.E = E; p.lde = lde;
+  const int ntiles = plan_tiles(p);
   if (E)
     hipLaunchKernelGGL(gemm_nt_kernel<true>, dim3((unsigned)ntiles), dim3(kThreads), 0, stream, p);
   else
@@ -581,6 +650,22 @@ hipError_t launch_gemm_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+hipError_t launch_gemm_nt_multi(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N,
+                                int64_t K, const uint16_t* A2, const uint16_t* B2, int64_t ld2, const MultiSlab& slab,
+                                uint16_t* C, int64_t ldc, hipStream_t stream) {
+  const int64_t two_gb = (int64_t)1 << 31, four_gb = (int64_t)1 << 32;
+  if (N * ldb * 2 >= two_gb || N * ld2 * 2 >= two_gb || M * lda * 2 >= four_gb || (slab.zero_row + 1) * ld2 * 2 >= four_gb)
+    return hipErrorInvalidValue;
+  DenseArgs p;
+  p.A = A; p.B = B; p.A2 = A2; p.B2 = B2; p.C = C;
+  p.lda = lda; p.ldb = ldb; p.ld2 = ld2; p.ldc = ldc;
+  p.M = M; p.N = N; p.K = K; p.K2 = ld2; p.alpha = 1.0f;
+  p.E = nullptr; p.lde = 0;
+  const int ntiles = plan_tiles(p);
+  hipLaunchKernelGGL(gemm_nt_multi_kernel, dim3((unsigned)ntiles), dim3(kThreads), 0, stream, p, slab);
+  return hipGetLastError();
 }
 
 }  // namespace qlora

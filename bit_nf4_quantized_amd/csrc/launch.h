@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "common.h"
+#include "multi.h"
 
 namespace qlora {
 
@@ -258,6 +259,46 @@ hipError_t launch_gemm_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int
                           int64_t K, const uint16_t* A2, const uint16_t* B2, int64_t ld2, int64_t K2, uint16_t* C,
                           int64_t ldc, float alpha, hipStream_t stream, const float* E = nullptr,
                           int64_t lde = 0);
+
+// The same with an adapter per row: A [M] rows in any order, grouped by rv;
+// C[m] = bf16(A[m] B^T + A2[m] B2_a^T) for rows of adapter a, A[m] B^T for the
+// others. A2 [M][ld2], its row zero_row is zeros; B2_a [N][ld2] lies at
+// b2_stride times slot[a] (or times a without slot). K a multiple of 64, ld2
+// too; all rows of A and A2 (the zero row too) below 4 GB, B and B2_a below 2 GB.
+struct MultiSlab {
+  RouteView rv;
+  const int32_t* slot;
+  int64_t zero_row;
+  int64_t b2_stride;
+};
+hipError_t launch_gemm_nt_multi(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N,
+                                int64_t K, const uint16_t* A2, const uint16_t* B2, int64_t ld2, const MultiSlab& slab,
+                                uint16_t* C, int64_t ldc, hipStream_t stream);
+
+// The linear with an adapter per row (multi.hip, multi_small.hip).
+constexpr int64_t kMultiMaxRows = (int64_t)1 << 22;   // 32-bit offsets of the rows' [M][256] rank buffers
+constexpr int kMultiMaxAdapters = 4096;
+struct MultiWorkspace {
+  size_t perm_off, start_off, adapter_off, count_off, slot_off;   // the grouping (RouteView), segment of an adapter
+  size_t perm2_off, start2_off, adapter2_off, count2_off;         // the grouping of a part of the rows
+  size_t st_off;     // bf16 [M + 1][rp]: s T or s U, the last row zero
+  size_t t_off;      // bf16 [M][r]: T, when the caller has none
+  size_t b2_off;     // bf16 per segment: L2^T [N][rp], or L1 [K][rp] with padded columns
+  size_t wd_off;     // bf16 dequantised weight
+  size_t dy_off;     // bf16 [M][N rounded up to 64]: dY, for a ragged N
+  size_t part_off;   // fp32 partials
+  size_t total;
+};
+MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, int A, bool bwd);
+bool multi_dense_supported(int64_t K, int64_t N, int r);            // the paths with a dequantised weight
+bool multi_forward_supported(int64_t M, int64_t K, int64_t N, int r);
+hipError_t multi_forward(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, const int32_t* ids,
+                               int A, const uint16_t* L1, const uint16_t* L2, int r, const float* scale, uint16_t* Y,
+                               uint16_t* T_out, void* ws, hipStream_t stream);
+hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t* X, const uint16_t* dY, int64_t M,
+                          const int32_t* ids, int A, const uint16_t* L1, const uint16_t* L2, int r, const float* scale,
+                          const uint16_t* T, uint16_t* dX, void* dL1, void* dL2, bool grad_bf16, void* ws,
+                          hipStream_t stream);
 
 DropoutParams dropout_params(float p, uint64_t seed);
 hipError_t launch_dropout_input(const uint16_t* X, int64_t numel, const DropoutParams& d, uint16_t* Xd,

@@ -19,6 +19,47 @@ extern "C" {
 #endif
 
 /*
+ * The QLoRA linear with an adapter per row: several adapters of one rank, and
+ * rows without any, beside one frozen weight, in one call. With a =
+ * row_adapter[m],
+ *   Y[m]  = X[m] dequant(Wt)^T + scale[a] (X[m] L1[a]) L2[a]     (the base alone for a outside [0, n_adapters))
+ *   dX[m] = dY[m] dequant(Wt) + scale[a] (dY[m] L2[a]^T) L1[a]^T
+ *   dL1[a] = scale[a] sum over the rows m of a of X[m]^T (dY[m] L2[a]^T)
+ *   dL2[a] = scale[a] sum over the rows m of a of (X[m] L1[a])^T dY[m]
+ * computed as qlora_linear_fwd / _bwd compute them for one adapter (bf16
+ * operands, fp32 accumulation; s T and s U are rounded to bf16 before their
+ * second product, outputs once). Rows may come in any order. An adapter
+ * without rows gets zero gradients. Sums run in a fixed order.
+ *   W            host struct of the quantised weight [N][K].
+ *   X            device bf16 [M][K];  dY device bf16 [M][N].
+ *   row_adapter  device int32 [M].
+ *   n_adapters   A, 1 .. QLORA_MULTI_MAX_ADAPTERS; adapters of a smaller rank
+ *                are padded with zero columns of L1 and rows of L2.
+ *   L1, L2       device bf16 [A][K][r], [A][r][N];  scale device fp32 [A].
+ *   T_out, T     optional device bf16 [M][r] = bf16(X[m] L1[a]), zero for rows
+ *                without an adapter: written by the forward pass, read by the
+ *                backward pass (which computes it when T is NULL).
+ *   dX           device bf16 [M][K], or NULL to skip it.
+ *   dL1, dL2     device, grad_dtype, shaped like L1, L2.
+ *   ws           qlora_linear_multi_workspace(M, K, N, r, A, backward) bytes.
+ * Shape rules as for qlora_linear_fwd (K a multiple of 64, N and r of 8, r in
+ * [8, 256]), M <= QLORA_MULTI_MAX_ROWS; M > 128 and the backward pass need a
+ * dequantised weight below 2 GB. M <= 128 streams the 4-bit weight once, and
+ * a single token (or, for r <= 64, a few) takes the GEMV.
+ */
+#define QLORA_MULTI_MAX_ROWS (1 << 22)
+#define QLORA_MULTI_MAX_ADAPTERS 4096
+int qlora_linear_multi_workspace(int64_t M, int64_t K, int64_t N, int r, int n_adapters, int backward,
+                                 size_t *bytes);
+int qlora_linear_multi_fwd(const qlora_nf4 *W, const uint16_t *X, int64_t M, const int32_t *row_adapter,
+                           int n_adapters, const uint16_t *L1, const uint16_t *L2, int r, const float *scale,
+                           uint16_t *Y, uint16_t *T_out, void *ws, size_t ws_bytes, hipStream_t stream);
+int qlora_linear_multi_bwd(const qlora_nf4 *W, const uint16_t *X, const uint16_t *dY, int64_t M,
+                           const int32_t *row_adapter, int n_adapters, const uint16_t *L1, const uint16_t *L2, int r,
+                           const float *scale, const uint16_t *T, uint16_t *dX, void *dL1, void *dL2,
+                           qlora_dtype grad_dtype, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
  * qlora_preference_loss: a loss over pairs of sequences from the paired log
  * ratios of a policy and a reference, and the gradient of the policy's logits
  * (Rafailov et al., "Direct Preference Optimization", NeurIPS 2023, eq. 7).

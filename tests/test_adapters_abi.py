@@ -137,3 +137,64 @@ def test_preference_refusals(lib):
     for bad in (dict(x=P + 2), dict(dx=P + 1), dict(lab=P + 4), dict(ref=P + 2), dict(lp=P + 1), dict(ws=P + 8),
                 dict(dt=1, x=P + 1)):
         assert call(**bad) == E.QLORA_ERR_ALIGN, bad
+
+
+def multi_weight(N=264, K=256, codes=P, no_dq=0):
+    return api.QNF4(N, K, codes, P, P, P, 0, no_dq, None)
+
+
+def test_multi_workspace(lib):
+    n, m = ctypes.c_size_t(), ctypes.c_size_t()
+    ws = lambda *a: lib.qlora_linear_multi_workspace(*a, ctypes.byref(n))  # noqa: E731
+    for M in (0, 1, 16, 100, 5000, 1 << 22):
+        for back in (0, 1):
+            assert ws(M, 256, 264, 72, 5, back) == api.QLORA_OK and n.value > 0
+    assert lib.qlora_linear_multi_workspace(1, 256, 264, 8, 1, 0, None) == api.QLORA_ERR_ARG
+    for bad in ((1, 256, 264, 8, 0, 0), (1, 256, 264, 8, 4097, 0), (1, 256, 264, 4, 1, 0), (1, 256, 264, 264, 1, 0)):
+        assert ws(*bad) == api.QLORA_ERR_ARG, bad
+    for bad in ((-1, 256, 264, 8, 1, 0), (1, 250, 264, 8, 1, 0), (1, 256, 262, 8, 1, 0), ((1 << 22) + 1, 256, 264, 8, 1, 0)):
+        assert ws(*bad) == api.QLORA_ERR_SHAPE, bad
+    # a larger batch never needs less
+    last = 0
+    for M in (1, 2, 16, 17, 128, 129, 1000, 10000):
+        assert lib.qlora_linear_multi_workspace(M, 512, 512, 16, 7, 1, ctypes.byref(m)) == api.QLORA_OK
+        assert m.value >= M * 16 and m.value >= last // 4
+        last = m.value
+
+
+@pytest.mark.parametrize("M", [1, 9, 100, 500])
+def test_multi_forward_refusals(lib, M):
+    def call(W=multi_weight(), X=P, M=M, ids=P, A=3, L1=P, L2=P, r=16, s=P, Y=P, T=None, ws=P, wsb=1 << 40):
+        return lib.qlora_linear_multi_fwd(ctypes.byref(W), X, M, ids, A, L1, L2, r, s, Y, T, ws, wsb, None)
+
+    E = api
+    assert call(M=0) == E.QLORA_OK
+    for bad in (dict(X=None), dict(ids=None), dict(A=0), dict(A=5000), dict(L1=None), dict(L2=None), dict(r=12),
+                dict(r=264), dict(s=None), dict(Y=None), dict(W=multi_weight(codes=None))):
+        assert call(**bad) == E.QLORA_ERR_ARG, bad
+    for bad in (dict(M=-1), dict(M=(1 << 22) + 1), dict(W=multi_weight(K=250)), dict(W=multi_weight(N=260))):
+        assert call(**bad) == E.QLORA_ERR_SHAPE, bad
+    for bad in (dict(ws=None), dict(wsb=8)):
+        assert call(**bad) == E.QLORA_ERR_WORKSPACE, bad
+    for bad in (dict(X=P + 8), dict(ids=P + 2), dict(L1=P + 8), dict(L2=P + 4), dict(s=P + 1), dict(Y=P + 8),
+                dict(T=P + 8), dict(ws=P + 8)):
+        assert call(**bad) == E.QLORA_ERR_ALIGN, bad
+
+
+def test_multi_backward_refusals(lib):
+    def call(W=multi_weight(), X=P, dY=P, M=50, ids=P, A=3, L1=P, L2=P, r=16, s=P, T=None, dX=P, d1=P, d2=P, dt=0,
+             ws=P, wsb=1 << 40):
+        return lib.qlora_linear_multi_bwd(ctypes.byref(W), X, dY, M, ids, A, L1, L2, r, s, T, dX, d1, d2, dt, ws, wsb,
+                                          None)
+
+    E = api
+    for bad in (dict(X=None), dict(dY=None), dict(ids=None), dict(A=0), dict(L1=None), dict(L2=None), dict(r=0),
+                dict(s=None), dict(d1=None), dict(d2=None), dict(dt=7)):
+        assert call(**bad) == E.QLORA_ERR_ARG, bad
+    for bad in (dict(M=-1), dict(M=(1 << 22) + 1), dict(W=multi_weight(K=1 << 17, N=1 << 14))):
+        assert call(**bad) == E.QLORA_ERR_SHAPE, bad
+    for bad in (dict(ws=None), dict(wsb=8)):
+        assert call(**bad) == E.QLORA_ERR_WORKSPACE, bad
+    for bad in (dict(X=P + 8), dict(dY=P + 2), dict(T=P + 8), dict(dX=P + 8), dict(d1=P + 4), dict(d2=P + 8),
+                dict(ws=P + 8)):
+        assert call(**bad) == E.QLORA_ERR_ALIGN, bad

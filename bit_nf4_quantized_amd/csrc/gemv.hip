@@ -475,6 +475,10 @@ struct FuseT {
 // Fused variants FT = F: lane l loads the 16-byte chunks f 64 + l (f < F)
 // of each of its wave's slices, so M r <= 256 F; a wave takes at most
 // ft_slices(F) slices (the loads stay within 12 registers of 16 bytes).
+// MULTI (an adapter per row, ids[m]): the rows' adapters are numbered by their
+// first row; wave w takes adapters w, w + W, ..., each as one more MFMA pair
+// whose B operand holds the rows of that adapter and zeros. The first one's L2
+// values are loaded behind the first codes and used after the K loop.
 constexpr int ft_slices(int F) { return F == 1 ? 4 : 12 / F; }
 
 template <int D, bool XL>
@@ -483,11 +487,12 @@ struct GlSlot {
   u32x4_t x[XL ? 1 : 2][2];        // X fragments (register path only)
 };
 
-template <int W, int D, bool XL, int FT>
+template <int W, int D, bool XL, int FT, bool MULTI>
 __global__ __launch_bounds__(64 * W) void gemv_lut_kernel(NF4View Wt, NF4Table tab, const uint16_t* __restrict__ X,
                                                           int M, const uint16_t* __restrict__ sT, int ldst,
                                                           const uint16_t* __restrict__ L2, int r,
-                                                          uint16_t* __restrict__ Y, FuseT ft) {
+                                                          uint16_t* __restrict__ Y, FuseT ft, MultiIds mi) {
+  static_assert(!MULTI || FT > 0, "the adapters' products start from the slice partials");
   static_assert(D % 4 == 0, "a round of D steps gives each lane D/4 (row, step) block-constant pairs");
   extern __shared__ __attribute__((aligned(16))) unsigned char gl_smem[];
   constexpr int kThreads = 64 * W;
@@ -511,6 +516,8 @@ __global__ __launch_bounds__(64 * W) void gemv_lut_kernel(NF4View Wt, NF4Table t
   auto ld16 = [](const void* base, uint32_t off) { return *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(base) + off); };
 
   // ---- loads, in the order they are needed: they complete in issue order ----
+  int id = -1;                                   // MULTI: the adapter of X row l%16, or -1
+  if constexpr (MULTI) id = mi.ids[xm];
   // Fused adapter reduction: the slice partials first (the prologue sums
   // them before its barrier). Lane l reads the 16-byte chunks f 64 + l of the
   // [M][r] slab of slices z = wave, wave + W, ...; missing slices and chunks
@@ -536,16 +543,19 @@ __global__ __launch_bounds__(64 * W) void gemv_lut_kernel(NF4View Wt, NF4Table t
   uint32_t la[kLoraChunks][8];
   u32x4_t lb[kLoraChunks];
   const int rp = (r + 31) & ~31;
+  auto load_l2 = [&](const uint16_t* l2) {
 #pragma unroll
-  for (int c = 0; c < kLoraChunks; ++c) {
-    const int j0 = 32 * c + 8 * grp;
-    const int jb = j0 < r ? j0 : 0;              // r % 8 == 0: a chunk of 8 is all in or all out
-    const uint32_t o = (__umul24((uint32_t)jb, (uint32_t)N) + (uint32_t)nrow) * 2u;
+    for (int c = 0; c < kLoraChunks; ++c) {
+      const int j0 = 32 * c + 8 * grp;
+      const int jb = j0 < r ? j0 : 0;            // r % 8 == 0: a chunk of 8 is all in or all out
+      const uint32_t o = (__umul24((uint32_t)jb, (uint32_t)N) + (uint32_t)nrow) * 2u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      la[c][e] = *reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(L2) + o + (uint32_t)(e * N) * 2u);
-    if constexpr (FT == 0) lb[c] = ld16(sT, (__umul24((uint32_t)xm, (uint32_t)ldst) + (uint32_t)jb) * 2u);
-  }
+      for (int e = 0; e < 8; ++e)
+        la[c][e] = *reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(l2) + o + (uint32_t)(e * N) * 2u);
+      if constexpr (FT == 0) lb[c] = ld16(sT, (__umul24((uint32_t)xm, (uint32_t)ldst) + (uint32_t)jb) * 2u);
+    }
+  };
+  if constexpr (!MULTI) load_l2(L2);
   // Block constants, one round of D steps ahead: lane l computes a' of row l%16
   // for the wave's steps base + l/16 + 4k (both 64-blocks of the step).
   // Without double quantisation (Wt.absmax32 set) a' is the fp32 block
@@ -603,6 +613,25 @@ __global__ __launch_bounds__(64 * W) void gemv_lut_kernel(NF4View Wt, NF4Table t
   GlSlot<D, XL> ring[D];
 #pragma unroll
   for (int d = 0; d < D; ++d) load(d, ring[d]);
+  // MULTI: one bit per adapter, at its first row; then this wave's first one
+  uint32_t lead = 0u;
+  int first_a = 0;
+  auto drop = [](uint32_t bits, int n) {         // without the lowest n set bits
+    for (int i = 0; i < n; ++i) bits &= bits - 1u;
+    return bits;
+  };
+  if constexpr (MULTI) {
+    if (row >= M || id < 0 || id >= mi.A) id = -1;
+#pragma unroll
+    for (int m = 0; m < 16; ++m) {
+      const int v = __builtin_amdgcn_readlane(id, m);
+      const uint32_t same = (uint32_t)__ballot(id == v) & 0xFFFFu;   // m's own bit is among them
+      if (v >= 0 && (same & ((1u << m) - 1u)) == 0u) lead |= 1u << m;
+    }
+    lead = drop(lead, wave);
+    if (lead != 0u) first_a = __builtin_amdgcn_readlane(id, (int)__builtin_ctz(lead));
+    load_l2(L2 + (int64_t)first_a * r * N);      // adapter 0's, unused, for a wave without one
+  }
   // keep every use of the loaded values below the last load, so that no wait
   // for an early load delays the issue of the code loads (the empty asm
   // statements after the table build take the loaded registers, and no memory
@@ -630,11 +659,13 @@ __global__ __launch_bounds__(64 * W) void gemv_lut_kernel(NF4View Wt, NF4Table t
 #pragma unroll
     for (int q = 0; q < kLutCopies / 4; ++q) dst[q] = v4;
   }
+  if constexpr (!MULTI) {
 #pragma unroll
-  for (int c = 0; c < kLoraChunks; ++c) {
+    for (int c = 0; c < kLoraChunks; ++c) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(la[c][e]) :: "memory");
-    if constexpr (FT == 0) asm volatile("" : "+v"(lb[c]) :: "memory");
+      for (int e = 0; e < 8; ++e) asm volatile("" : "+v"(la[c][e]) :: "memory");
+      if constexpr (FT == 0) asm volatile("" : "+v"(lb[c]) :: "memory");
+    }
   }
 #pragma unroll
   for (int k = 0; k < kAPairs; ++k) asm volatile("" : "+v"(a16[k]), "+v"(sg0[k]), "+v"(sg1[k]) :: "memory");
@@ -642,15 +673,18 @@ __global__ __launch_bounds__(64 * W) void gemv_lut_kernel(NF4View Wt, NF4Table t
 #pragma unroll
     for (int u = 0; u < kXPer; ++u) asm volatile("" : "+v"(xv[u]) :: "memory");
   }
-  if (wave == 0) {  // packed LoRA fragments, read back by the same lanes after the K loop
+  auto packed = [&](int c) {                     // the A operand of rank chunk c, zero past r
+    const u32x4_t a = {la[c][0] | (la[c][1] << 16), la[c][2] | (la[c][3] << 16), la[c][4] | (la[c][5] << 16),
+                       la[c][6] | (la[c][7] << 16)};
+    return 32 * c + 8 * grp < r ? a : u32x4_t{0u, 0u, 0u, 0u};
+  };
+  if (!MULTI && wave == 0) {  // packed LoRA fragments, read back by the same lanes after the K loop
     u32x4_t* lp = reinterpret_cast<u32x4_t*>(gl_smem + L.lora_off) + lane;
 #pragma unroll
     for (int c = 0; c < kLoraChunks; ++c) {
       const bool in = 32 * c + 8 * grp < r;
       const u32x4_t z = {0u, 0u, 0u, 0u};
-      const u32x4_t a = {la[c][0] | (la[c][1] << 16), la[c][2] | (la[c][3] << 16), la[c][4] | (la[c][5] << 16),
-                         la[c][6] | (la[c][7] << 16)};
-      lp[c * 64] = in ? a : z;
+      lp[c * 64] = packed(c);
       if constexpr (FT == 0) lp[128 + c * 64] = in ? lb[c] : z;
     }
   }
@@ -743,8 +777,57 @@ __global__ __launch_bounds__(64 * W) void gemv_lut_kernel(NF4View Wt, NF4Table t
   for (int d = 0; d < D; ++d)
     if (base + d < mysteps) compute(base + d, ring[d]);
 
+  // MULTI: T[m = l%16][32 c + 8 (l/16) .. +8], the waves' sums added in order
+  auto t_of = [&](int c, float* v) {
+    const int j0 = 32 * c + 8 * grp;
+    const int nw = ft.Z < W ? ft.Z : W;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    const unsigned char* qp = gl_smem + L.q_off + (uint32_t)(xm * r + (j0 < r ? j0 : 0)) * 4u;
+    for (int w = 0; w < nw; ++w) {
+      const f32x4_t t0 = *reinterpret_cast<const f32x4_t*>(qp + (uint32_t)(w * mr) * 4u);
+      const f32x4_t t1 = *reinterpret_cast<const f32x4_t*>(qp + (uint32_t)(w * mr) * 4u + 16u);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] += t0[e];
+        v[4 + e] += t1[e];
+      }
+    }
+  };
+  auto packed8 = [](const float* v) {
+    return u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+  };
+  if constexpr (MULTI) {
+    const u32x4_t none = {0u, 0u, 0u, 0u};
+    if (ft.T_out != nullptr && blockIdx.x == 0 && wave == 0) {
+#pragma unroll
+      for (int c = 0; c < kLoraChunks; ++c) {
+        float v[8];
+        t_of(c, v);
+        const int j0 = 32 * c + 8 * grp;
+        if (row < M && j0 < r) *reinterpret_cast<u32x4_t*>(ft.T_out + row * r + j0) = id >= 0 ? packed8(v) : none;
+      }
+    }
+    for (bool first = true; lead != 0u; lead = drop(lead, W), first = false) {
+      const int a = __builtin_amdgcn_readlane(id, (int)__builtin_ctz(lead));
+      if (!first) load_l2(L2 + (int64_t)a * r * N);
+      const float s = mi.scale[a];
+#pragma unroll
+      for (int c = 0; c < kLoraChunks; ++c) {
+        if (32 * c >= rp) continue;
+        float v[8];
+        t_of(c, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= s;
+        const u32x4_t b = id == a && 32 * c + 8 * grp < r ? packed8(v) : none;   // other rows' T may be unset
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, packed(c)),
+                                                       __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+      }
+    }
+  }
+
   // ---- LoRA term (wave 0): acc += sum_j L2[j][n] sT[m][j] ----
-  if (wave == 0) {
+  if (!MULTI && wave == 0) {
     const u32x4_t* lp = reinterpret_cast<const u32x4_t*>(gl_smem + L.lora_off) + lane;
 #pragma unroll
     for (int c = 0; c < kLoraChunks; ++c) {
@@ -819,19 +902,19 @@ __global__ __launch_bounds__(64 * W) void gemv_lut_kernel(NF4View Wt, NF4Table t
   }
 }
 
-template <int W, int D, bool XL, int FT>
+template <int W, int D, bool XL, int FT, bool MULTI = false>
 hipError_t launch_lut(const NF4View& Wt, const NF4Table& tab, const uint16_t* X, int M, const uint16_t* sT,
                       const uint16_t* L2, int r, uint16_t* Y, const FuseT& ft, int64_t tiles, uint32_t lds,
-                      hipStream_t stream) {
+                      hipStream_t stream, const MultiIds& mi = MultiIds{}) {
   static bool attr_set = false;  // raise the dynamic-LDS limit once per instantiation (idempotent)
   if (!attr_set) {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&gemv_lut_kernel<W, D, XL, FT>),
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&gemv_lut_kernel<W, D, XL, FT, MULTI>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)kGvMaxLds);
     (void)hipGetLastError();  // a refusal shows up as a launch error below
     attr_set = true;
   }
-  hipLaunchKernelGGL((gemv_lut_kernel<W, D, XL, FT>), dim3((unsigned)tiles), dim3(64 * W), lds, stream, Wt, tab, X, M,
-                     sT, r, L2, r, Y, ft);
+  hipLaunchKernelGGL((gemv_lut_kernel<W, D, XL, FT, MULTI>), dim3((unsigned)tiles), dim3(64 * W), lds, stream, Wt, tab, X, M,
+                     sT, r, L2, r, Y, ft, mi);
   return hipGetLastError();
 }
 
@@ -1067,6 +1150,28 @@ hipError_t launch_gemv_fused_t(const NF4View& W, const NF4Table& tab, const uint
                                uint16_t* Y, hipStream_t stream) {
   const FuseT ft{part, Z, s, T_out};
   return launch_gemv_impl(W, tab, X, M, nullptr, L2, r, Y, &ft, stream);
+}
+
+bool gemv_multi_applies(const NF4View& W, int64_t M, int r) { return gemv_fuses_t(W, M, r); }
+
+hipError_t launch_gemv_multi(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, const MultiIds& mi,
+                             const float* part, int Z, const uint16_t* L2, int r, uint16_t* Y, uint16_t* T_out,
+                             hipStream_t stream) {
+  if (!gemv_multi_applies(W, M, r)) return hipErrorInvalidValue;
+  const LutPlan p = lut_plan(W, M, r, true);
+  const FuseT ft{part, Z, 0.0f, T_out};
+  const int64_t tiles = (W.rows + kGvRows - 1) / kGvRows;
+  auto go = [&](auto w, auto xl) -> hipError_t {
+    constexpr int kW = decltype(w)::value;
+    constexpr bool kXL = decltype(xl)::value;
+    if (p.fuse == 1)
+      return launch_lut<kW, 4, kXL, 1, true>(W, tab, X, (int)M, nullptr, L2, r, Y, ft, tiles, p.lds, stream, mi);
+    return launch_lut<kW, 4, kXL, 4, true>(W, tab, X, (int)M, nullptr, L2, r, Y, ft, tiles, p.lds, stream, mi);
+  };
+  using I4 = std::integral_constant<int, 4>;
+  using I8 = std::integral_constant<int, 8>;
+  if (p.waves == 4) return p.xl ? go(I4{}, std::true_type{}) : go(I4{}, std::false_type{});
+  return p.xl ? go(I8{}, std::true_type{}) : go(I8{}, std::false_type{});
 }
 
 }  // namespace qlora

@@ -42,9 +42,13 @@
 // rounds st = bf16(s T[j]) and starts each of its row sums at
 // st * L2[j][row]. The 8 lanes of a row are then added by DPP, the 8 waves'
 // row sums through LDS in a fixed order, and Y is rounded to bf16 once.
+// With an adapter per row (MULTI) the adapter is ids[0]: both kernels start at
+// its L1, L2 and scale; a token without one starts its row sums at 0.
 // Every result is deterministic (fixed orders, no atomics).
 #include "common.h"
 #include "launch.h"
+
+#include <type_traits>
 
 namespace qlora {
 
@@ -80,10 +84,16 @@ typedef __attribute__((address_space(3))) void g1_lds_t;
 
 // part[p][j] = sum_{k in slice p} X[k] L1[k][j], slices of kT1Rows rows;
 // thread t takes the 8 columns (t % 8) * 8 .. +8 of rows t / 8, t / 8 + 32, ...
+template <bool MULTI>
 __global__ __launch_bounds__(256) void t1_partial_kernel(const uint16_t* __restrict__ X, int K,
                                                         const uint16_t* __restrict__ L1, int r,
-                                                        float* __restrict__ part) {
+                                                        float* __restrict__ part, MultiIds mi) {
   __shared__ float red[32][kG1MaxRank];
+  if constexpr (MULTI) {
+    const int a = mi.ids[0];
+    if (a < 0 || a >= mi.A) return;                 // no adapter: the partials are not used
+    L1 += (int64_t)a * K * r;
+  }
   const int t = threadIdx.x, cc = t & 7, ph = t >> 3;
   const int k0 = blockIdx.x * kT1Rows;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -129,13 +139,13 @@ __device__ __forceinline__ float sum8(float v) {
   return v;
 }
 
-template <int NG>
+template <int NG, bool MULTI>
 __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Table tab,
                                                               const uint16_t* __restrict__ X,
                                                               const float* __restrict__ part, int P, float s,
                                                               const uint16_t* __restrict__ L2, int r,
                                                               uint16_t* __restrict__ Y,
-                                                              uint16_t* __restrict__ T_out) {
+                                                              uint16_t* __restrict__ T_out, MultiIds mi) {
   constexpr int DC = NG >= kG1Loads ? 1 : kG1Loads / NG;  // chunks in flight per wave
   __shared__ __attribute__((aligned(256))) uint32_t g1_table[kG1TableBytes / 4];   // at LDS address 0
   extern __shared__ __attribute__((aligned(16))) unsigned char g1_smem[];
@@ -152,6 +162,13 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
   auto ld16 = [](const void* base, uint32_t off) {
     return *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(base) + off);
   };
+  bool has = true;
+  if constexpr (MULTI) {
+    const int a = __builtin_amdgcn_readfirstlane(mi.ids[0]);
+    has = a >= 0 && a < mi.A;
+    L2 += (int64_t)(has ? a : 0) * r * N;
+    s = mi.scale[has ? a : 0];
+  }
 
   // ==== 1. the small operands, issued before any code load (a CU returns
   // load data in issue order, so whatever is queued behind the weight
@@ -295,6 +312,7 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
     t += __shfl_xor(t, 8, 64);
     t += __shfl_xor(t, 16, 64);
     t += __shfl_xor(t, 32, 64);
+    if (MULTI && !has) t = 0.0f;
     if (b == 0 && T_out && lrow == 0 && jw < r) T_out[jw] = f32_to_bf16(t);
     const float st = jw < r ? bf16_to_f32(f32_to_bf16(s * t)) : 0.0f;
 #pragma unroll
@@ -368,19 +386,19 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
   }
 }
 
-template <int NG>
+template <int NG, bool MULTI>
 hipError_t launch_g1(const NF4View& W, const NF4Table& tab, const uint16_t* X, const float* part, int P, float s,
                      const uint16_t* L2, int r, uint16_t* Y, uint16_t* T_out, int G, uint32_t lds,
-                     hipStream_t stream) {
+                     const MultiIds& mi, hipStream_t stream) {
   static bool attr_set = false;  // raise the dynamic-LDS limit once per instantiation (idempotent)
   if (!attr_set) {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&gemv1_kernel<NG>),
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&gemv1_kernel<NG, MULTI>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024 - (int)kG1TableBytes);
     (void)hipGetLastError();  // a refusal shows up as a launch error below
     attr_set = true;
   }
-  hipLaunchKernelGGL((gemv1_kernel<NG>), dim3((unsigned)G), dim3(kG1Threads), lds, stream, W, tab, X, part, P, s,
-                     L2, r, Y, T_out);
+  hipLaunchKernelGGL((gemv1_kernel<NG, MULTI>), dim3((unsigned)G), dim3(kG1Threads), lds, stream, W, tab, X, part, P, s,
+                     L2, r, Y, T_out, mi);
   return hipGetLastError();
 }
 
@@ -424,29 +442,50 @@ size_t gemv1_partial_bytes(int64_t K, int r) { return (size_t)((K + kT1Rows - 1)
 
 bool gemv1_applies(const NF4View& W, int64_t M, int r) { return M == 1 && g1_plan(W, r).ok; }
 
-hipError_t launch_gemv1(const NF4View& W, const NF4Table& tab, const uint16_t* X, const uint16_t* L1,
-                        const uint16_t* L2, int r, float s, uint16_t* Y, uint16_t* T_out, float* part,
-                        hipStream_t stream) {
+namespace {
+
+template <bool MULTI>
+hipError_t run_gemv1(const NF4View& W, const NF4Table& tab, const uint16_t* X, const uint16_t* L1, const uint16_t* L2,
+                     int r, float s, uint16_t* Y, uint16_t* T_out, float* part, const MultiIds& mi,
+                     hipStream_t stream) {
   const G1Plan pl = g1_plan(W, r);
   if (!pl.ok) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(t1_partial_kernel, dim3((unsigned)pl.P), dim3(256), 0, stream, X, (int)W.cols, L1, r, part);
+  hipLaunchKernelGGL(t1_partial_kernel<MULTI>, dim3((unsigned)pl.P), dim3(256), 0, stream, X, (int)W.cols, L1, r, part,
+                     mi);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   return timed(kTimeGemv, stream, [&]() -> hipError_t {
+    auto go = [&](auto ng) {
+      return launch_g1<decltype(ng)::value, MULTI>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, mi, stream);
+    };
     switch (pl.NG) {
-      case 1: return launch_g1<1>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, stream);
-      case 2: return launch_g1<2>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, stream);
-      case 3: return launch_g1<3>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, stream);
-      case 4: return launch_g1<4>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, stream);
-      case 5: return launch_g1<5>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, stream);
-      case 6: return launch_g1<6>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, stream);
-      case 7: return launch_g1<7>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, stream);
-      case 8: return launch_g1<8>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, stream);
-      case 9: return launch_g1<9>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, stream);
-      case 10: return launch_g1<10>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, stream);
-      default: return launch_g1<11>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, stream);
+      case 1: return go(std::integral_constant<int, 1>{});
+      case 2: return go(std::integral_constant<int, 2>{});
+      case 3: return go(std::integral_constant<int, 3>{});
+      case 4: return go(std::integral_constant<int, 4>{});
+      case 5: return go(std::integral_constant<int, 5>{});
+      case 6: return go(std::integral_constant<int, 6>{});
+      case 7: return go(std::integral_constant<int, 7>{});
+      case 8: return go(std::integral_constant<int, 8>{});
+      case 9: return go(std::integral_constant<int, 9>{});
+      case 10: return go(std::integral_constant<int, 10>{});
+      default: return go(std::integral_constant<int, 11>{});
     }
   });
+}
+
+}  // namespace
+
+hipError_t launch_gemv1(const NF4View& W, const NF4Table& tab, const uint16_t* X, const uint16_t* L1,
+                        const uint16_t* L2, int r, float s, uint16_t* Y, uint16_t* T_out, float* part,
+                        hipStream_t stream) {
+  return run_gemv1<false>(W, tab, X, L1, L2, r, s, Y, T_out, part, MultiIds{}, stream);
+}
+
+hipError_t launch_gemv1_multi(const NF4View& W, const NF4Table& tab, const uint16_t* X, const MultiIds& mi,
+                              const uint16_t* L1, const uint16_t* L2, int r, uint16_t* Y, uint16_t* T_out, float* part,
+                              hipStream_t stream) {
+  return run_gemv1<true>(W, tab, X, L1, L2, r, 0.0f, Y, T_out, part, mi, stream);
 }
 
 }  // namespace qlora

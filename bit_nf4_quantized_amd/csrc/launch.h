@@ -141,6 +141,11 @@ bool midm_fits(int64_t M, int64_t K, int64_t N);   // sizes the kernel's 32-bit 
 hipError_t launch_midm(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, const uint16_t* sT,
                        const uint16_t* L2, int r, int rp, float* part, uint16_t* Y, hipStream_t stream);
 
+// The base product alone, as midm_slices(K, N) fp32 partials [S][M][N] (M from 1 on).
+int midm_slices(int64_t K, int64_t N);
+hipError_t launch_midm_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, float* part,
+                            hipStream_t stream);
+
 // Optimiser step (optim.hip). part: 1024 doubles of workspace.
 struct AdamHyper {
   float lr, beta1, beta2, eps, wd;
@@ -287,6 +292,7 @@ struct MultiWorkspace {
   size_t wd_off;     // bf16 dequantised weight
   size_t dy_off;     // bf16 [M][N rounded up to 64]: dY, for a ragged N
   size_t part_off;   // fp32 partials
+  size_t tpart_off;  // fp32 partials of T (M <= 128)
   size_t total;
 };
 MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, int A, bool bwd);
@@ -299,6 +305,30 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
                           const int32_t* ids, int A, const uint16_t* L1, const uint16_t* L2, int r, const float* scale,
                           const uint16_t* T, uint16_t* dX, void* dL1, void* dL2, bool grad_bf16, void* ws,
                           hipStream_t stream);
+
+// M <= 128 (multi_small.hip): T partials [slices][M][r], and the sum of base
+// and adapters.
+struct MultiIds {
+  const int32_t* ids;      // [M]
+  int A;
+  const float* scale;      // [A]
+};
+int64_t multi_small_t_floats(int64_t M, int64_t K, int r);
+int multi_small_t_slices(int64_t K);
+hipError_t launch_multi_small_t(const uint16_t* X, int64_t M, int64_t K, const MultiIds& mi, const uint16_t* L1, int r,
+                                float* part, hipStream_t stream);
+hipError_t launch_multi_small_finish(const float* base, int S, int64_t M, int64_t N, const MultiIds& mi,
+                                     const float* tpart, int Z, int r, const uint16_t* L2, uint16_t* Y,
+                                     uint16_t* T_out, hipStream_t stream);
+// The decode GEMVs with an adapter per row: a single token (gemv1.hip, where
+// gemv1_applies), and up to 16 from the T partials (gemv.hip).
+hipError_t launch_gemv1_multi(const NF4View& W, const NF4Table& tab, const uint16_t* X, const MultiIds& mi,
+                              const uint16_t* L1, const uint16_t* L2, int r, uint16_t* Y, uint16_t* T_out, float* part,
+                              hipStream_t stream);
+bool gemv_multi_applies(const NF4View& W, int64_t M, int r);
+hipError_t launch_gemv_multi(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, const MultiIds& mi,
+                             const float* part, int Z, const uint16_t* L2, int r, uint16_t* Y, uint16_t* T_out,
+                             hipStream_t stream);
 
 DropoutParams dropout_params(float p, uint64_t seed);
 hipError_t launch_dropout_input(const uint16_t* X, int64_t numel, const DropoutParams& d, uint16_t* Xd,

@@ -594,7 +594,14 @@ int64_t gemm_rows(int64_t M, int64_t widest) {
 }  // namespace
 
 MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, int A, bool bwd) {
-  MultiWorkspace L;
+  MultiWorkspace L = {};
+  if (!bwd && M <= kMidMaxM && midm_fits(M, K, N)) {   // the small paths
+    L.part_off = 0;
+    L.tpart_off = align_up((size_t)midm_slices(K, N) * M * N * 4, 256);
+    const size_t t = (size_t)multi_small_t_floats(M, K, r) * 4, one = gemv1_partial_bytes(K, r);
+    L.total = L.tpart_off + align_up((t > one ? t : one) + 1, 256);
+    return L;
+  }
   const int64_t rp = cdiv(r, 64) * 64, segs = A < M ? A : M, np = cdiv(N, 64) * 64;
   size_t off = 0;
   auto take = [&](int64_t bytes) {
@@ -729,7 +736,29 @@ bool multi_dense_supported(int64_t K, int64_t N, int r) {
   return K * np * 2 < two_gb && N * rp * 2 < two_gb && K * rp * 2 < two_gb;
 }
 
-bool multi_forward_supported(int64_t M, int64_t K, int64_t N, int r) { return multi_dense_supported(K, N, r); }
+bool multi_forward_supported(int64_t M, int64_t K, int64_t N, int r) {
+  return (M <= kMidMaxM && midm_fits(M, K, N)) || multi_dense_supported(K, N, r);
+}
+
+// M <= 128: a single token or a few through the GEMVs where they apply, else
+// the one-pass product.
+static hipError_t multi_forward_small(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M,
+                                      const MultiIds& mi, const uint16_t* L1, const uint16_t* L2, int r, uint16_t* Y,
+                                      uint16_t* T_out, float* part, float* tpart, hipStream_t stream) {
+  const int64_t K = W.cols, N = W.rows;
+  if (gemv1_applies(W, M, r)) return launch_gemv1_multi(W, tab, X, mi, L1, L2, r, Y, T_out, tpart, stream);
+  hipError_t e = launch_multi_small_t(X, M, K, mi, L1, r, tpart, stream);
+  if (e != hipSuccess) return e;
+  const int Z = multi_small_t_slices(K);
+  if (gemv_multi_applies(W, M, r))
+    return timed(kTimeGemv, stream,
+                 [&] { return launch_gemv_multi(W, tab, X, M, mi, tpart, Z, L2, r, Y, T_out, stream); });
+  return timed(kTimeMidGemm, stream, [&]() -> hipError_t {
+    const hipError_t b = launch_midm_base(W, tab, X, M, part, stream);
+    if (b != hipSuccess) return b;
+    return launch_multi_small_finish(part, midm_slices(K, N), M, N, mi, tpart, Z, r, L2, Y, T_out, stream);
+  });
+}
 
 hipError_t multi_forward(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, const int32_t* ids,
                                int A, const uint16_t* L1, const uint16_t* L2, int r, const float* scale, uint16_t* Y,
@@ -743,6 +772,9 @@ hipError_t multi_forward(const NF4View& W, const NF4Table& tab, const uint16_t* 
   uint16_t* wd = reinterpret_cast<uint16_t*>(base + L.wd_off);
   int32_t* slot = reinterpret_cast<int32_t*>(base + L.slot_off);
   float* part = reinterpret_cast<float*>(base + L.part_off);
+  if (M <= kMidMaxM && midm_fits(M, K, N))
+    return multi_forward_small(W, tab, X, M, MultiIds{ids, A, scale}, L1, L2, r, Y, T_out, part,
+                               reinterpret_cast<float*>(base + L.tpart_off), stream);
   RouteView rv;
   hipError_t e = route(ids, M, A, base, L.perm_off, L.start_off, L.adapter_off, L.count_off, slot, &rv, stream);
   if (e != hipSuccess) return e;

@@ -85,6 +85,23 @@ __device__ __forceinline__ float block_scale(uint32_t c8, float sigma, float mu)
   return prod + mu;
 }
 
+// fp16 bits of a table value, nearest-even, in integer operations (scalar
+// registers for a kernel argument). Table values are 0 or at least 2^-6 and
+// below 2^15: normal in fp16.
+__device__ __forceinline__ uint32_t table_fp16(float q) {
+  const uint32_t u = __float_as_uint(q), v = u & 0x7FFFFFFFu;
+  const uint32_t h = ((v + 0xFFFu + ((v >> 13) & 1u)) >> 13) - (112u << 10);
+  return ((u >> 16) & 0x8000u) | (v ? h : 0u);
+}
+
+// A pair of fp16 values times an fp32 constant, rounded to bf16: two mixed
+// multiplies (v_fma_mix_f32 widens the halves by itself) and one conversion.
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t h, float a) {
+  const f16x2_t q = __builtin_bit_cast(f16x2_t, h);
+  return pack_bf16x2(__builtin_fmaf((float)q.x, a, 0.0f), __builtin_fmaf((float)q.y, a, 0.0f));
+}
+
 __device__ __forceinline__ float wave_max(float v, int width) {
   for (int o = width / 2; o > 0; o >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, o, 64));
   return v;

@@ -478,7 +478,10 @@ struct FuseT {
 // MULTI (an adapter per row, ids[m]): the rows' adapters are numbered by their
 // first row; wave w takes adapters w, w + W, ..., each as one more MFMA pair
 // whose B operand holds the rows of that adapter and zeros. The first one's L2
-// values are loaded behind the first codes and used after the K loop.
+// values are loaded behind the first codes and used after the K loop. These
+// variants multiply the dequantised weight itself: the table holds fp16 pairs
+// of q (off by at most 2^-12, where bf16(q) is off by 2^-9), each is multiplied
+// by a' in fp32 and rounded to bf16 once, as the standalone dequant rounds.
 constexpr int ft_slices(int F) { return F == 1 ? 4 : 12 / F; }
 
 template <int D, bool XL>
@@ -648,7 +651,7 @@ __global__ __launch_bounds__(64 * W) void gemv_lut_kernel(NF4View Wt, NF4Table t
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const uint32_t u = __float_as_uint(tab.q[j]);       // finite: round to nearest even in scalar integer ops
-      const uint32_t b = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+      const uint32_t b = MULTI ? table_fp16(tab.q[j]) : (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
       asm volatile("v_writelane_b32 %0, %1, %2" : "+v"(qv) : "s"(b), "i"(j));
     }
     const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute((tid & 15) << 2, (int)qv);
@@ -740,8 +743,16 @@ __global__ __launch_bounds__(64 * W) void gemv_lut_kernel(NF4View Wt, NF4Table t
     for (int b = 0; b < 2; ++b) {
       const int blk = 2 * s + b;
       const u32x2_t cw = {b == 0 ? p02[0] : p02[1], b == 0 ? p13[0] : p13[1]};
-      const u32x4_t a0 = {lut(cw.x, 0), lut(cw.x, 1), lut(cw.x, 2), lut(cw.x, 3)};
-      const u32x4_t a1 = {lut(cw.y, 0), lut(cw.y, 1), lut(cw.y, 2), lut(cw.y, 3)};
+      u32x4_t a0 = {lut(cw.x, 0), lut(cw.x, 1), lut(cw.x, 2), lut(cw.x, 3)};
+      u32x4_t a1 = {lut(cw.y, 0), lut(cw.y, 1), lut(cw.y, 2), lut(cw.y, 3)};
+      if constexpr (MULTI) {                       // bf16(q a') of this lane's row
+        const float ap = aw[((i % D) * 2 + b) * 16 + row];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          a0[q] = scaled_pair(a0[q], ap);
+          a1[q] = scaled_pair(a1[q], ap);
+        }
+      }
       u32x4_t x0, x1;
       if constexpr (XL) {
         const unsigned char* xp = gl_smem + L.x_off + (uint32_t)xm * L.xpitch + (uint32_t)(64 * blk + kb) * 2u;
@@ -752,9 +763,14 @@ __global__ __launch_bounds__(64 * W) void gemv_lut_kernel(NF4View Wt, NF4Table t
         x1 = sl.x[b][1];
       }
       f32x4_t p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a0),
-                                                          __builtin_bit_cast(bf16x8_t, x0), zero4, 0, 0, 0);
+                                                          __builtin_bit_cast(bf16x8_t, x0), MULTI ? acc : zero4, 0, 0,
+                                                          0);
       p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a1), __builtin_bit_cast(bf16x8_t, x1),
                                                   p, 0, 0, 0);
+      if constexpr (MULTI) {
+        acc = p;
+        continue;
+      }
       // register q of lane l is row 4 (l/16) + q of the tile
       const f32x4_t s4 = *reinterpret_cast<const f32x4_t*>(aw + ((i % D) * 2 + b) * 16 + 4 * grp);
 #pragma unroll

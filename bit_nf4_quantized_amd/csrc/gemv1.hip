@@ -43,7 +43,10 @@
 // st * L2[j][row]. The 8 lanes of a row are then added by DPP, the 8 waves'
 // row sums through LDS in a fixed order, and Y is rounded to bf16 once.
 // With an adapter per row (MULTI) the adapter is ids[0]: both kernels start at
-// its L1, L2 and scale; a token without one starts its row sums at 0.
+// its L1, L2 and scale; a token without one starts its row sums at 0. These
+// variants multiply the dequantised weight itself: the table holds fp16 pairs
+// of q (off by at most 2^-12, where bf16(q) is off by 2^-9), each is multiplied
+// by a' in fp32 and rounded to bf16 once, as the standalone dequant rounds.
 // Every result is deterministic (fixed orders, no atomics).
 #include "common.h"
 #include "launch.h"
@@ -257,11 +260,12 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
   // bytes. Wave w writes stores 8 w .. 8 w + 7; the entry's low nibble is
   // 4 (i % 4) + l / 16, its high nibble i / 4.
   {
-    uint32_t qb[16];                                // bf16(q[j]), round to nearest even (finite q)
+    uint32_t qb[16];                                // bf16(q[j]), round to nearest even (finite q); MULTI: fp16
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const uint32_t u = __float_as_uint(tab.q[j]);
-      qb[j] = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+      if constexpr (MULTI) qb[j] = table_fp16(tab.q[j]);
+      else qb[j] = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
     }
     const int lq = lane >> 4;
     uint32_t qlo[4];
@@ -347,14 +351,15 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int t = 0; t < 4; ++t) lv[4 * i + t] = lut(words[i], t);
-      float sum = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, lv[k]), __builtin_bit_cast(bf16x2_t, xw[k]),
-                                              sum, false);
       int row = 8 * g + lrow;
       if (row > R - 1) row = R - 1;                  // lanes past the rows read a valid constant (unused)
-      acc[g] = __builtin_fmaf(aw[row * (nblk + 1) + blk], sum, acc[g]);
+      const float ap = aw[row * (nblk + 1) + blk];
+      float sum = MULTI ? acc[g] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, MULTI ? scaled_pair(lv[k], ap) : lv[k]),
+                                              __builtin_bit_cast(bf16x2_t, xw[k]), sum, false);
+      acc[g] = MULTI ? sum : __builtin_fmaf(ap, sum, acc[g]);
     }
   };
   int base = 0;

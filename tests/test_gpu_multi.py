@@ -8,7 +8,7 @@ by element, within the bound that its roundings give: with u = 2^-24, h = 2^-8
 the sum of their magnitudes,
     E(T)   = K u |X| |L1|,     E(sT) = s E(T) + h |sT|     (s T is rounded to bf16)
     E(Y)   = K u |X| |W| + E(sT) |L2| + r u |sT| |L2|      (M <= 16: + 2 h |X| |W|: the
-             GEMV multiplies bf16(q) by the block constant instead of rounding the product)
+             GEMV takes q from fp16, which can move a weight to the neighbouring bf16)
     E(sU)  = s N u |dY| |L2| + h |sU|,  E(dX) = N u |dY| |W| + E(sU) |L1| + r u |sU| |L1|
     E(dL1) = X^T E(sU) + n u |X| |sU|,  E(dL2) = s (E(T) + h |T|)^T |dY| + n u |sT| |dY|
 (products of matrices of magnitudes) and half an ulp of a bf16 output. An RMS

@@ -12,7 +12,6 @@ import ctypes
 import os
 from array import array
 from dataclasses import dataclass
-from operator import attrgetter
 from typing import NamedTuple
 
 import numpy as np
@@ -55,7 +54,6 @@ QLORA_NOALLOC_SCRATCH_BYTES = (2 << 20) + (64 << 10)
 QLORA_QUANT_BATCH_MAX = 16
 QLORA_CLIP_WORKSPACE_BYTES = 8192
 QLORA_ADAM_STATE_BLOCK = 256
-_DTYPE_OF = attrgetter("dtype")
 
 
 class AdamParams(ctypes.Structure):
@@ -250,6 +248,30 @@ def _need(t, dtype, shape, name):
         raise ValueError(f"{name} must be contiguous")
 
 
+_TENSORS = None
+_F32, _BF16, _I32, _I64 = range(4)   # dtype numbers of the tensor module
+
+
+def _tensors():
+    """The compiled tensor checks (address, addresses); raises if they are not built."""
+    global _TENSORS
+    if _TENSORS is None:
+        import torch  # noqa: F401  (its libraries come first)
+
+        try:
+            from bit_nf4_quantized_amd import _tensors as mod
+        except ImportError as e:
+            raise RuntimeError(f"_tensors.so is not built; run `python {os.path.join(HERE, 'build.py')}` ({e})") from e
+        _TENSORS = mod
+    return _TENSORS
+
+
+def _raw_stream(stream):
+    import torch
+
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
 # ---- host-only queries ------------------------------------------------------------
 
 def qlora_nf4_codebook() -> np.ndarray:
@@ -390,32 +412,36 @@ def qlora_preference_loss(logits, labels, ref_logps, beta: float, label_smoothin
     if logits.dim() != 3 or logits.shape[0] % 2:
         raise ValueError("logits must be [2 pairs, T, V]")
     S, T, V = logits.shape
-    dt = {torch.float32: QLORA_F32, torch.bfloat16: QLORA_BF16}.get(logits.dtype)
-    if dt is None:
+    if logits.dtype == torch.bfloat16:
+        dt = QLORA_BF16
+    elif logits.dtype == torch.float32:
+        dt = QLORA_F32
+    else:
         raise TypeError("logits must be float32 or bfloat16")
     if not logits.is_cuda:
         raise ValueError("logits must be a device tensor")
-    dev = logits.device
+    dev = logits.get_device()
     ld = _row_stride(logits, "logits")
-    _need(labels, torch.int64, (S, T), "labels")
-    _need(ref_logps, torch.float32, (S, T), "ref_logps")
-    if need_grad:
-        if dlogits is None:
-            dlogits = torch.empty((S, T, V), dtype=logits.dtype, device=dev)
-        if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or dlogits.device != dev:
-            raise ValueError("dlogits must have the logits' dtype, shape and device")
-        ldd = _row_stride(dlogits, "dlogits")
+    address = _tensors().address
+    yp = address(labels, _I64, (S, T), dev, "labels")
+    rp = address(ref_logps, _F32, (S, T), dev, "ref_logps")
+    ldd, dp = 0, None
+    if not need_grad:
+        dlogits = None
     else:
-        dlogits, ldd = None, 0
-    if labels.device != dev or ref_logps.device != dev:
-        raise ValueError("labels and ref_logps must be on the logits' device")
-    small = torch.empty(1 + S + S * T, dtype=torch.float32, device=dev)   # loss, rewards, logps
+        if dlogits is None:
+            dlogits = logits.new_empty((S, T, V))
+        elif dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or dlogits.get_device() != dev:
+            raise ValueError("dlogits must have the logits' dtype, shape and device")
+        ldd, dp = _row_stride(dlogits, "dlogits"), dlogits.data_ptr()
+    small = ref_logps.new_empty(1 + S + S * T)   # loss, rewards, logps
     loss, rewards, logps = small[:1], small[1:1 + S], small[1 + S:].view(S, T)
-    ws = _workspace(qlora_preference_workspace(S // 2, T, V), dev, workspace)
-    _check(_load().qlora_preference_loss(_ptr(logits), dt, S // 2, T, V, ld, _ptr(labels), _ptr(ref_logps),
-                                         float(beta), float(label_smoothing), float(grad_scale), _ptr(loss),
-                                         _ptr(rewards), _ptr(logps), _ptr(dlogits), ldd, _ptr(ws),
-                                         ws.numel() * ws.element_size(), _stream(stream)), "qlora_preference_loss")
+    ws = _workspace(qlora_preference_workspace(S // 2, T, V), logits.device, workspace)
+    at = small.data_ptr()
+    _check(_load().qlora_preference_loss(logits.data_ptr(), dt, S // 2, T, V, ld, yp, rp, float(beta),
+                                         float(label_smoothing), float(grad_scale), at, at + 4, at + 4 * (1 + S), dp,
+                                         ldd, ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream)),
+           "qlora_preference_loss")
     return PreferenceOut(loss, rewards, logps, dlogits)
 
 
@@ -452,35 +478,13 @@ class AdamWState:
                           z(total, torch.uint8).view(torch.float8_e4m3fn), z(nb, torch.float32), z(nb, torch.float32))
 
 
-def _pointers(tensors, dtype, numel, device, name):
-    """Device addresses of a list of contiguous tensors (array of int64); sizes
-    must match numel. Whole-list calls: a model has hundreds of adapter tensors,
-    and the step on the GPU should not wait for this loop."""
-    import torch
-
-    T = torch.Tensor
-    if list(map(T.numel, tensors)) != numel:
-        raise ValueError(f"{name} must be one tensor of each parameter's size")
-    if set(map(_DTYPE_OF, tensors)) - {dtype}:
-        raise TypeError(f"{name} must all be {dtype}")
-    if set(map(T.get_device, tensors)) - {device.index}:
-        raise ValueError(f"{name} must all be on {device}")
-    if not all(map(T.is_contiguous, tensors)):
-        raise ValueError(f"{name} must be contiguous")
-    return array("q", map(T.data_ptr, tensors))
-
-
-def _array_ptr(a):
-    return None if a is None else a.buffer_info()[0]
-
-
 def _grad_dtype(grads):
     import torch
 
     if not grads or grads[0].dtype == torch.float32:
-        return QLORA_F32, torch.float32
+        return QLORA_F32, _F32
     if grads[0].dtype == torch.bfloat16:
-        return QLORA_BF16, torch.bfloat16
+        return QLORA_BF16, _BF16
     raise TypeError("gradients must be float32 or bfloat16")
 
 
@@ -493,18 +497,15 @@ def qlora_clip_grad_norm_batch(grads, max_norm: float, coef=None, norm=None, wor
     grads = list(grads)
     gd, dtype = _grad_dtype(grads)
     dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
-    if dev.type != "cuda":
-        raise ValueError("grads must be device tensors")
-    numel = list(map(torch.Tensor.numel, grads))
-    gp, sizes = _pointers(grads, dtype, numel, dev, "grads"), array("q", numel)
+    gp, sizes = _tensors().addresses(grads, dtype, dev.index if grads else -1, "grads")
     coef = coef if coef is not None else torch.empty(1, dtype=torch.float32, device=dev)
     norm = norm if norm is not None else torch.empty(1, dtype=torch.float64, device=dev)
     _need(coef, torch.float32, (1,), "coef")
     _need(norm, torch.float64, (1,), "norm")
     ws = _workspace(QLORA_CLIP_WORKSPACE_BYTES, dev, workspace)
-    _check(_load().qlora_clip_grad_norm_batch(len(grads), _array_ptr(gp), gd, _array_ptr(sizes), float(max_norm),
-                                              _ptr(coef), _ptr(norm), _ptr(ws), ws.numel() * ws.element_size(),
-                                              _stream(stream)), "qlora_clip_grad_norm_batch")
+    _check(_load().qlora_clip_grad_norm_batch(len(grads), gp, gd, sizes, float(max_norm), coef.data_ptr(),
+                                              norm.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                              _raw_stream(stream)), "qlora_clip_grad_norm_batch")
     return coef, norm
 
 
@@ -520,16 +521,14 @@ def qlora_adamw_batch(thetas, grads, state: AdamWState, step: int, lr: float, be
     thetas, grads = list(thetas), list(grads)
     n = len(thetas)
     gd, gtype = _grad_dtype(grads)
-    numel = list(map(torch.Tensor.numel, thetas))
-    if numel != list(state.numel):
+    dev = thetas[0].get_device() if n else -1
+    address = _tensors().addresses
+    tp, sizes = address(thetas, _F32, dev, "thetas")
+    if sizes != array("q", state.numel).tobytes():
         raise ValueError("the state belongs to tensors of other sizes")
-    dev = thetas[0].device if n else torch.device("cuda", torch.cuda.current_device())
-    if dev.type != "cuda":
-        raise ValueError("thetas must be device tensors")
-    tp, gp = _pointers(thetas, torch.float32, numel, dev, "thetas"), _pointers(grads, gtype, numel, dev, "grads")
-    bp = None if thetas_bf16 is None else _pointers(list(thetas_bf16), torch.bfloat16, numel, dev, "thetas_bf16")
-    sizes = array("q", numel)
-    total = sum([(k + 255) // 256 * 256 for k in numel])
+    gp, _ = address(grads, gtype, dev, "grads", sizes)
+    bp = None if thetas_bf16 is None else address(list(thetas_bf16), _BF16, dev, "thetas_bf16", sizes)[0]
+    total = sum([(k + 255) // 256 * 256 for k in state.numel])
     held = torch.float32 if state.bits == 32 else torch.float8_e4m3fn
     _need_mem(state.m, held, (total,), "state.m")
     _need_mem(state.v, held, (total,), "state.v")
@@ -542,8 +541,8 @@ def qlora_adamw_batch(thetas, grads, state: AdamWState, step: int, lr: float, be
                     state.m_scale.data_ptr() if state.bits == 8 else None,
                     state.v_scale.data_ptr() if state.bits == 8 else None)
     hp = AdamParams(lr, beta1, beta2, eps, weight_decay, step)
-    _check(_load().qlora_adamw_batch(n, _array_ptr(tp), _array_ptr(gp), gd, _array_ptr(bp), _array_ptr(sizes),
-                                     ctypes.byref(st), ctypes.byref(hp), _ptr(coef), _stream(stream)),
+    _check(_load().qlora_adamw_batch(n, tp, gp, gd, bp, sizes, ctypes.byref(st), ctypes.byref(hp),
+                                     None if coef is None else coef.data_ptr(), _raw_stream(stream)),
            "qlora_adamw_batch")
 
 
@@ -945,22 +944,20 @@ def qlora_linear_multi_workspace(M: int, K: int, N: int, r: int, n_adapters: int
     return out.value
 
 
-def _need_multi(q, X, row_adapter, L1, L2, scale):
-    """Shared argument checks; returns (M, K, N, r, adapters)."""
-    import torch
-
+def _multi_operands(q, X, row_adapter, L1, L2, scale):
+    """The shared arguments, checked: (M, K, N, r, adapters, device), addresses of X, row_adapter, L1, L2, scale."""
     if X.dim() != 2 or L1.dim() != 3:
         raise ValueError("X must be [M, K] and L1 [adapters, K, r]")
     M, K = X.shape
     N, (A, _, r) = q.rows, L1.shape
     if K != q.cols:
         raise ValueError("X columns must equal the weight's in_features")
-    _need(X, torch.bfloat16, (M, K), "X")
-    _need(row_adapter, torch.int32, (M,), "row_adapter")
-    _need(L1, torch.bfloat16, (A, K, r), "L1")
-    _need(L2, torch.bfloat16, (A, r, N), "L2")
-    _need(scale, torch.float32, (A,), "scale")
-    return M, K, N, r, A
+    address = _tensors().address
+    xp = address(X, _BF16, (M, K), -1, "X")
+    dev = X.get_device()
+    return ((M, K, N, r, A, dev), xp, address(row_adapter, _I32, (M,), dev, "row_adapter"),
+            address(L1, _BF16, (A, K, r), dev, "L1"), address(L2, _BF16, (A, r, N), dev, "L2"),
+            address(scale, _F32, (A,), dev, "scale"))
 
 
 @_on_stream
@@ -969,20 +966,19 @@ def qlora_linear_multi_fwd(q: NF4Tensor, X, row_adapter, L1, L2, scale, want_T: 
     """Y[m] = X[m] dequant(Wt)^T + scale[a] (X[m] L1[a]) L2[a], a = row_adapter[m] (int32 [M]; an id outside
     [0, adapters) gives the base alone), L1 [adapters, K, r], L2 [adapters, r, N], scale float32 [adapters];
     returns (Y, T) with T = bf16(X[m] L1[a]) or None."""
-    import torch
-
-    M, K, N, r, A = _need_multi(q, X, row_adapter, L1, L2, scale)
-    Y = Y if Y is not None else torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
-    _need(Y, torch.bfloat16, (M, N), "Y")
+    (M, K, N, r, A, dev), xp, ip, p1, p2, sp = _multi_operands(q, X, row_adapter, L1, L2, scale)
+    address = _tensors().address
+    if Y is None:
+        Y = X.new_empty((M, N))
+    yp = address(Y, _BF16, (M, N), dev, "Y")
     if want_T and T_out is None:
-        T_out = torch.empty((M, r), dtype=torch.bfloat16, device=X.device)
-    if T_out is not None:
-        _need(T_out, torch.bfloat16, (M, r), "T_out")
+        T_out = X.new_empty((M, r))
+    tp = None if T_out is None else address(T_out, _BF16, (M, r), dev, "T_out")
     st = q.struct()
     ws = _workspace(qlora_linear_multi_workspace(M, K, N, r, A), X.device, workspace)
-    _check(_load().qlora_linear_multi_fwd(ctypes.byref(st), _ptr(X), M, _ptr(row_adapter), A, _ptr(L1), _ptr(L2), r,
-                                          _ptr(scale), _ptr(Y), _ptr(T_out), _ptr(ws),
-                                          ws.numel() * ws.element_size(), _stream(stream)), "qlora_linear_multi_fwd")
+    _check(_load().qlora_linear_multi_fwd(ctypes.byref(st), xp, M, ip, A, p1, p2, r, sp, yp, tp, ws.data_ptr(),
+                                          ws.numel() * ws.element_size(), _raw_stream(stream)),
+           "qlora_linear_multi_fwd")
     return Y, T_out
 
 
@@ -996,25 +992,25 @@ def qlora_linear_multi_bwd(q: NF4Tensor, X, dY, row_adapter, L1, L2, scale, T=No
     grad_dtype = torch.float32 if grad_dtype is None else grad_dtype
     if grad_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("grad_dtype must be float32 or bfloat16")
-    M, K, N, r, A = _need_multi(q, X, row_adapter, L1, L2, scale)
-    _need(dY, torch.bfloat16, (M, N), "dY")
-    if T is not None:
-        _need(T, torch.bfloat16, (M, r), "T")
-    if need_dX:
-        dX = dX if dX is not None else torch.empty((M, K), dtype=torch.bfloat16, device=X.device)
-        _need(dX, torch.bfloat16, (M, K), "dX")
-    else:
+    (M, K, N, r, A, dev), xp, ip, p1, p2, sp = _multi_operands(q, X, row_adapter, L1, L2, scale)
+    address = _tensors().address
+    yp = address(dY, _BF16, (M, N), dev, "dY")
+    tp = None if T is None else address(T, _BF16, (M, r), dev, "T")
+    dxp = None
+    if not need_dX:
         dX = None
+    else:
+        if dX is None:
+            dX = X.new_empty((M, K))
+        dxp = address(dX, _BF16, (M, K), dev, "dX")
     dL1 = dL1 if dL1 is not None else torch.empty((A, K, r), dtype=grad_dtype, device=X.device)
     dL2 = dL2 if dL2 is not None else torch.empty((A, r, N), dtype=grad_dtype, device=X.device)
-    _need(dL1, grad_dtype, (A, K, r), "dL1")
-    _need(dL2, grad_dtype, (A, r, N), "dL2")
+    gd, gtype = (QLORA_F32, _F32) if grad_dtype == torch.float32 else (QLORA_BF16, _BF16)
+    d1, d2 = address(dL1, gtype, (A, K, r), dev, "dL1"), address(dL2, gtype, (A, r, N), dev, "dL2")
     st = q.struct()
-    gd = QLORA_F32 if grad_dtype == torch.float32 else QLORA_BF16
     ws = _workspace(qlora_linear_multi_workspace(M, K, N, r, A, True), X.device, workspace)
-    _check(_load().qlora_linear_multi_bwd(ctypes.byref(st), _ptr(X), _ptr(dY), M, _ptr(row_adapter), A, _ptr(L1),
-                                          _ptr(L2), r, _ptr(scale), _ptr(T), _ptr(dX), _ptr(dL1), _ptr(dL2), gd,
-                                          _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+    _check(_load().qlora_linear_multi_bwd(ctypes.byref(st), xp, yp, M, ip, A, p1, p2, r, sp, tp, dxp, d1, d2, gd,
+                                          ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream)),
            "qlora_linear_multi_bwd")
     return dX, dL1, dL2
 

@@ -23,6 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libqlora_nf4.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+# the binding's tensor checks: a CPython module on torch's C++ headers (host code)
+TENSORS_PATH = os.path.join(HERE, "_tensors.so")
 OBJ_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "gemv.hip", "gemv1.hip", "dense_gemm.hip", "skinny_gemm.hip", "int8.hip", "merge.hip", "midm.hip", "multi.hip", "multi_small.hip", "dropout.hip", "optim.hip", "optim_batch.hip", "preference.hip", "convcheck.hip", "probe.hip"]
 ARCH = os.environ.get("QLORA_OFFLOAD_ARCH", "gfx950")
@@ -62,10 +64,32 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_tensors() -> None:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = TENSORS_PATH + ".tmp"
+    cmd = [shutil.which("c++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for path in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", path]
+    cmd += [os.path.join(CSRC, "tensors.cpp"), "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+            f"-Wl,-rpath,{lib}"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"compiling tensors.cpp failed:\n{res.stderr}")
+    os.replace(tmp, TENSORS_PATH)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+        tensors = ex.submit(_build_tensors)
         objs = list(ex.map(_compile, SOURCES))
+        tensors.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     res = subprocess.run(cmd, capture_output=True, text=True)

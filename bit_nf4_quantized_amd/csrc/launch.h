@@ -141,11 +141,6 @@ bool midm_fits(int64_t M, int64_t K, int64_t N);   // sizes the kernel's 32-bit 
 hipError_t launch_midm(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, const uint16_t* sT,
                        const uint16_t* L2, int r, int rp, float* part, uint16_t* Y, hipStream_t stream);
 
-// The base product alone, as midm_slices(K, N) fp32 partials [S][M][N] (M from 1 on).
-int midm_slices(int64_t K, int64_t N);
-hipError_t launch_midm_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, float* part,
-                            hipStream_t stream);
-
 // Optimiser step (optim.hip). part: 1024 doubles of workspace.
 struct AdamHyper {
   float lr, beta1, beta2, eps, wd;
@@ -313,6 +308,10 @@ struct MultiIds {
   int A;
   const float* scale;      // [A]
 };
+bool multi_small_fits(int64_t M, int64_t K, int64_t N);
+int multi_small_slices(int64_t M, int64_t K, int64_t N);   // partials [S][M][N] of the base product
+hipError_t launch_multi_small_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, float* part,
+                                   hipStream_t stream);
 int64_t multi_small_t_floats(int64_t M, int64_t K, int r);
 int multi_small_t_slices(int64_t K);
 hipError_t launch_multi_small_t(const uint16_t* X, int64_t M, int64_t K, const MultiIds& mi, const uint16_t* L1, int r,

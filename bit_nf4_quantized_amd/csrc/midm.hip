@@ -286,33 +286,6 @@ bool midm_fits(int64_t M, int64_t K, int64_t N) {
   return N * K < ((int64_t)1 << 32) && M * K < ((int64_t)1 << 32);
 }
 
-namespace {
-
-// pp: the slices' partials (then Y is not written), else Y
-hipError_t midm_pass(const NF4View& W, const NF4Table& tab, const uint16_t* X, int m, const uint16_t* sT,
-                     const uint16_t* L2, int r, int rp, const MidSplit& p, float* pp, uint16_t* Y,
-                     hipStream_t stream) {
-  const dim3 grid((unsigned)p.tiles, (unsigned)p.S), block(kMidThreads);
-  if (m <= 32)
-    hipLaunchKernelGGL(midm_kernel<32>, grid, block, 0, stream, W, tab, X, m, sT, L2, r, rp, p.kslice, pp, Y);
-  else if (m <= 64)
-    hipLaunchKernelGGL(midm_kernel<64>, grid, block, 0, stream, W, tab, X, m, sT, L2, r, rp, p.kslice, pp, Y);
-  else
-    hipLaunchKernelGGL(midm_kernel<128>, grid, block, 0, stream, W, tab, X, m, sT, L2, r, rp, p.kslice, pp, Y);
-  return hipGetLastError();
-}
-
-}  // namespace
-
-int midm_slices(int64_t K, int64_t N) { return (int)mid_split(K, N).S; }
-
-hipError_t launch_midm_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, float* part,
-                            hipStream_t stream) {
-  if (M < 1 || M > kMidMaxM || (W.cols % 64) != 0 || (W.rows % 8) != 0 || !midm_fits(M, W.cols, W.rows))
-    return hipErrorInvalidValue;
-  return midm_pass(W, tab, X, (int)M, nullptr, nullptr, 0, 0, mid_split(W.cols, W.rows), part, nullptr, stream);
-}
-
 hipError_t launch_midm(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, const uint16_t* sT,
                        const uint16_t* L2, int r, int rp, float* part, uint16_t* Y, hipStream_t stream) {
   if (M <= 16 || M > kMidMaxM || (W.cols % 64) != 0 || (W.rows % 8) != 0 || (rp % 64) != 0 ||
@@ -320,7 +293,15 @@ hipError_t launch_midm(const NF4View& W, const NF4Table& tab, const uint16_t* X,
     return hipErrorInvalidValue;
   const MidSplit p = mid_split(W.cols, W.rows);
   float* pp = p.S > 1 ? part : nullptr;
-  hipError_t e = midm_pass(W, tab, X, (int)M, sT, L2, r, rp, p, pp, Y, stream);
+  const dim3 grid((unsigned)p.tiles, (unsigned)p.S), block(kMidThreads);
+  const int m = (int)M;
+  if (M <= 32)
+    hipLaunchKernelGGL(midm_kernel<32>, grid, block, 0, stream, W, tab, X, m, sT, L2, r, rp, p.kslice, pp, Y);
+  else if (M <= 64)
+    hipLaunchKernelGGL(midm_kernel<64>, grid, block, 0, stream, W, tab, X, m, sT, L2, r, rp, p.kslice, pp, Y);
+  else
+    hipLaunchKernelGGL(midm_kernel<128>, grid, block, 0, stream, W, tab, X, m, sT, L2, r, rp, p.kslice, pp, Y);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.S == 1) return e;
   const int64_t MN = M * W.rows;
   hipLaunchKernelGGL(midm_reduce_kernel, dim3((unsigned)((MN / 4 + 255) / 256)), dim3(256), 0, stream, part,

@@ -595,9 +595,9 @@ int64_t gemm_rows(int64_t M, int64_t widest) {
 
 MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, int A, bool bwd) {
   MultiWorkspace L = {};
-  if (!bwd && M <= kMidMaxM && midm_fits(M, K, N)) {   // the small paths
+  if (!bwd && (M < 1 || multi_small_fits(M, K, N))) {   // the small paths
     L.part_off = 0;
-    L.tpart_off = align_up((size_t)midm_slices(K, N) * M * N * 4, 256);
+    L.tpart_off = align_up((size_t)multi_small_slices(M, K, N) * M * N * 4, 256);
     const size_t t = (size_t)multi_small_t_floats(M, K, r) * 4, one = gemv1_partial_bytes(K, r);
     L.total = L.tpart_off + align_up((t > one ? t : one) + 1, 256);
     return L;
@@ -737,7 +737,7 @@ bool multi_dense_supported(int64_t K, int64_t N, int r) {
 }
 
 bool multi_forward_supported(int64_t M, int64_t K, int64_t N, int r) {
-  return (M <= kMidMaxM && midm_fits(M, K, N)) || multi_dense_supported(K, N, r);
+  return multi_small_fits(M, K, N) || multi_dense_supported(K, N, r);
 }
 
 // M <= 128: a single token or a few through the GEMVs where they apply, else
@@ -754,9 +754,9 @@ static hipError_t multi_forward_small(const NF4View& W, const NF4Table& tab, con
     return timed(kTimeGemv, stream,
                  [&] { return launch_gemv_multi(W, tab, X, M, mi, tpart, Z, L2, r, Y, T_out, stream); });
   return timed(kTimeMidGemm, stream, [&]() -> hipError_t {
-    const hipError_t b = launch_midm_base(W, tab, X, M, part, stream);
+    const hipError_t b = launch_multi_small_base(W, tab, X, M, part, stream);
     if (b != hipSuccess) return b;
-    return launch_multi_small_finish(part, midm_slices(K, N), M, N, mi, tpart, Z, r, L2, Y, T_out, stream);
+    return launch_multi_small_finish(part, multi_small_slices(M, K, N), M, N, mi, tpart, Z, r, L2, Y, T_out, stream);
   });
 }
 
@@ -772,7 +772,7 @@ hipError_t multi_forward(const NF4View& W, const NF4Table& tab, const uint16_t* 
   uint16_t* wd = reinterpret_cast<uint16_t*>(base + L.wd_off);
   int32_t* slot = reinterpret_cast<int32_t*>(base + L.slot_off);
   float* part = reinterpret_cast<float*>(base + L.part_off);
-  if (M <= kMidMaxM && midm_fits(M, K, N))
+  if (multi_small_fits(M, K, N))
     return multi_forward_small(W, tab, X, M, MultiIds{ids, A, scale}, L1, L2, r, Y, T_out, part,
                                reinterpret_cast<float*>(base + L.tpart_off), stream);
   RouteView rv;

@@ -8,18 +8,26 @@
 // path for M > 128 rows and the backward pass; gemv1.hip, gemv.hip and
 // multi_small.hip hold the small ones.
 //
-//   route_kernel      groups the rows by adapter (see multi.h)
-//   multi_nt_kernel   T = X L1_a or U = dY L2_a^T over 128-row pieces of the
-//                     grouped rows, split over the reduction into fp32 partials
-//   multi_tr_kernel   sums them, scales each row by its s_a, rounds to bf16
-//   the dense GEMM    (dense_gemm.hip) walks the grouped rows; its adapter
-//                     stages run over the segments that meet the tile
-//   multi_tn_kernel   dL1_a, dL2_a: per piece of a segment, the product with
-//                     the reduction down the rows
+//   multi_prep_kernel    groups the rows by adapter (see multi.h) and, in its
+//                        other workgroups, dequantises the weight
+//   multi_nt_kernel      T = X L1_a and / or U = dY L2_a^T over 128-row pieces of
+//                        the grouped rows, split over the reduction into fp32
+//                        partials
+//   multi_sum_kernel     sums them, scales each row by its s_a, rounds to bf16;
+//                        its other workgroups lay out L2_a^T or L1_a for the GEMM
+//   the dense GEMM       (dense_gemm.hip) walks the grouped rows; its adapter
+//                        stages run over the segments that meet the tile
+//   multi_tn_kernel      dL1_a and dL2_a: per piece of a segment, the products
+//                        with the reduction down the rows
+//   multi_finish_kernel  the sums over a segment's pieces, and the zeros of
+//                        adapters without rows
+// Launches with independent halves are one launch: at a few hundred rows each
+// kernel takes 4 to 10 us, of which 2 to 4 are its start and end.
 // Rows are gathered where a kernel loads them (a row's 128-byte stage slices
 // are whole cache lines, so the gather costs no bandwidth), and every row
 // buffer stays in the caller's order. All sums run in a fixed order.
 #include "common.h"
+#include "dequant.h"
 #include "launch.h"
 #include "multi.h"
 
@@ -33,10 +41,8 @@ __device__ __attribute__((aligned(16))) uint32_t g_multi_zero[4];  // zero-initi
 
 // ---- route ---------------------------------------------------------------------
 
-constexpr int kRouteThreads = 1024;
-constexpr int kRouteWaves = kRouteThreads / 64;
-
-__device__ __forceinline__ int block_sum(int v, int* s) {   // 1024 threads; s: kRouteWaves ints
+template <int WAVES>
+__device__ __forceinline__ int block_sum(int v, int* s) {   // s: WAVES ints
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
   __syncthreads();
@@ -44,29 +50,38 @@ __device__ __forceinline__ int block_sum(int v, int* s) {   // 1024 threads; s: 
   __syncthreads();
   int t = 0;
 #pragma unroll
-  for (int w = 0; w < kRouteWaves; ++w) t += s[w];
+  for (int w = 0; w < WAVES; ++w) t += s[w];
   return t;
 }
+
+struct RouteArgs {
+  const int32_t* ids;
+  int M, A;
+  int32_t* perm;
+  int32_t* start;
+  int32_t* adapter;
+  int32_t* count;
+  int32_t* slot;          // optional: an adapter's segment
+};
 
 // Workgroup a < A: adapter a; workgroup A: the rows without one. Each reads
 // all ids (from the L2 after the first): it counts the rows and the distinct
 // adapters below its own, which are its place and its segment number, then
-// writes its rows in order. slot (optional) receives an adapter's segment.
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(const int32_t* __restrict__ ids, int M, int A,
-                                                              int32_t* __restrict__ perm, int32_t* __restrict__ start,
-                                                              int32_t* __restrict__ adapter,
-                                                              int32_t* __restrict__ count,
-                                                              int32_t* __restrict__ slot) {
-  extern __shared__ uint32_t seen[];                // A bits
-  __shared__ int s_sum[kRouteWaves], s_wave[kRouteWaves];
+// writes its rows in order.
+template <int WAVES>
+__device__ __forceinline__ void route_body(const RouteArgs& p, int a) {
+  constexpr int kThreads = 64 * WAVES;
+  __shared__ uint32_t seen[kMultiMaxAdapters / 32];
+  __shared__ int s_sum[WAVES], s_wave[WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int a = (int)blockIdx.x;
+  const int M = p.M, A = p.A;
   const int words = (A + 31) / 32;
-  for (int i = tid; i < words; i += kRouteThreads) seen[i] = 0u;
+  for (int i = tid; i < words; i += kThreads) seen[i] = 0u;
   __syncthreads();
   int below = 0, mine = 0;
-  for (int i = tid; i < M; i += kRouteThreads) {
-    const int v = ids[i];
+#pragma unroll 4
+  for (int i = tid; i < M; i += kThreads) {
+    const int v = p.ids[i];
     const bool has = v >= 0 && v < A;
     if (has && v < a) {
       ++below;
@@ -74,26 +89,26 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const int32_t* __r
     }
     mine += a < A ? v == a : !has;
   }
-  below = block_sum(below, s_sum);
-  mine = block_sum(mine, s_sum);                    // its barriers also publish `seen`
+  below = block_sum<WAVES>(below, s_sum);
+  mine = block_sum<WAVES>(mine, s_sum);             // its barriers also publish `seen`
   int rank = 0;
-  for (int i = tid; i < words; i += kRouteThreads) rank += __popc(seen[i]);
-  rank = block_sum(rank, s_sum);
+  for (int i = tid; i < words; i += kThreads) rank += __popc(seen[i]);
+  rank = block_sum<WAVES>(rank, s_sum);
   if (tid == 0) {
     if (a == A) {
-      count[0] = rank;
-      start[rank] = below;
+      p.count[0] = rank;
+      p.start[rank] = below;
     } else if (mine > 0) {
-      adapter[rank] = a;
-      start[rank] = below;
-      if (slot) slot[a] = rank;
+      p.adapter[rank] = a;
+      p.start[rank] = below;
+      if (p.slot) p.slot[a] = rank;
     }
   }
   if (mine == 0) return;                            // uniform
   int at = below;
-  for (int i0 = 0; i0 < M; i0 += kRouteThreads) {
+  for (int i0 = 0; i0 < M; i0 += kThreads) {
     const int i = i0 + tid;
-    const int v = i < M ? ids[i] : 0;
+    const int v = i < M ? p.ids[i] : 0;
     const bool take = i < M && (a < A ? v == a : !(v >= 0 && v < A));
     const unsigned long long b = __ballot(take);
     __syncthreads();
@@ -101,34 +116,57 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const int32_t* __r
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < kRouteWaves; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
       const int c = s_wave[w];
       before += w < wave ? c : 0;
       all += c;
     }
-    if (take) perm[at + before + __popcll(b & ((1ull << lane) - 1ull))] = i;
+    if (take) p.perm[at + before + __popcll(b & ((1ull << lane) - 1ull))] = i;
     at += all;
+  }
+}
+
+__global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) { route_body<16>(p, (int)blockIdx.x); }
+
+// Workgroups 0 .. A group the rows; the others dequantise the weight as stored
+// (COLS = false) or transposed with rows of ldo (gx workgroups along k).
+template <bool COLS>
+__global__ __launch_bounds__(256) void multi_prep_kernel(RouteArgs p, NF4View W, NF4Table tab,
+                                                         uint16_t* __restrict__ out, int64_t ldo, int gx) {
+  const int b = (int)blockIdx.x - (p.A + 1);
+  if (b < 0) {
+    route_body<4>(p, (int)blockIdx.x);
+  } else if constexpr (COLS) {
+    dequant_cols_body(W, tab, out, ldo, b % gx, b / gx);
+  } else {
+    dequant_rows_body(W, tab, out, b, (int)gridDim.x - (p.A + 1));
   }
 }
 
 // ---- adapter operands of the dense GEMM ---------------------------------------------
 
-// out[k] = the transpose of L2 of segment k: [N][rp], columns >= r zero. One
-// workgroup per 64 columns n and 64 ranks of one segment.
-__global__ __launch_bounds__(256) void multi_l2t_kernel(const uint16_t* __restrict__ L2, int64_t N, int r, int rp,
-                                                        RouteView rv, uint16_t* __restrict__ out) {
+struct LayArgs {
+  const uint16_t* src;    // L2 [A][r][W] (transposed into [W][rp]) or L1 [A][W][r] (padded to [W][rp])
+  uint16_t* out;          // per segment [W][rp], columns >= r zero
+  int64_t W;
+  int r, rp, blocks;      // blocks per segment
+  bool transpose;
+};
+
+// L2 of segment k transposed: 64 columns n and 64 ranks per workgroup.
+__device__ __forceinline__ void lay_transposed(const LayArgs& p, const RouteView& rv, int k, int b) {
   __shared__ uint16_t tile[64][64 + 2];
-  const int k = blockIdx.z;
-  if (k >= rv.count[0]) return;                     // uniform
-  const uint16_t* src = L2 + (int64_t)rv.adapter[k] * r * N;
-  const int64_t n0 = (int64_t)blockIdx.x * 64;
-  const int j0 = blockIdx.y * 64;
+  const int64_t N = p.W;
+  const uint16_t* src = p.src + (int64_t)rv.adapter[k] * p.r * N;
+  const int tiles = p.rp / 64;
+  const int64_t n0 = (int64_t)(b / tiles) * 64;
+  const int j0 = (b % tiles) * 64;
   const int t = threadIdx.x;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int j = (t >> 3) + 32 * u, c = (t & 7) * 8;
     u32x4_t v = {0u, 0u, 0u, 0u};
-    if (j0 + j < r && n0 + c < N) v = *reinterpret_cast<const u32x4_t*>(src + (int64_t)(j0 + j) * N + n0 + c);
+    if (j0 + j < p.r && n0 + c < N) v = *reinterpret_cast<const u32x4_t*>(src + (int64_t)(j0 + j) * N + n0 + c);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e) tile[c + e][j] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
@@ -141,24 +179,21 @@ __global__ __launch_bounds__(256) void multi_l2t_kernel(const uint16_t* __restri
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = (uint32_t)tile[n][c + 2 * e] | ((uint32_t)tile[n][c + 2 * e + 1] << 16);
-    *reinterpret_cast<u32x4_t*>(out + ((int64_t)k * N + n0 + n) * rp + j0 + c) = u32x4_t{w[0], w[1], w[2], w[3]};
+    *reinterpret_cast<u32x4_t*>(p.out + ((int64_t)k * N + n0 + n) * p.rp + j0 + c) = u32x4_t{w[0], w[1], w[2], w[3]};
   }
 }
 
-// out[k] = L1 of segment k with its columns padded to rp: [K][rp].
-__global__ __launch_bounds__(256) void multi_l1p_kernel(const uint16_t* __restrict__ L1, int64_t K, int r, int rp,
-                                                        RouteView rv, uint16_t* __restrict__ out) {
-  const int k = blockIdx.y;
-  if (k >= rv.count[0]) return;
-  const uint16_t* src = L1 + (int64_t)rv.adapter[k] * K * r;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // 16-byte piece of the output
-  const int per = rp / 8;
-  if (i >= K * per) return;
+// L1 of segment k with padded columns: 256 16-byte pieces per workgroup.
+__device__ __forceinline__ void lay_padded(const LayArgs& p, const RouteView& rv, int k, int b) {
+  const uint16_t* src = p.src + (int64_t)rv.adapter[k] * p.W * p.r;
+  const int64_t i = (int64_t)b * 256 + threadIdx.x;
+  const int per = p.rp / 8;
+  if (i >= p.W * per) return;
   const int64_t row = i / per;
   const int c = (int)(i - row * per) * 8;
   u32x4_t v = {0u, 0u, 0u, 0u};
-  if (c < r) v = *reinterpret_cast<const u32x4_t*>(src + row * r + c);
-  *reinterpret_cast<u32x4_t*>(out + ((int64_t)k * K + row) * rp + c) = v;
+  if (c < p.r) v = *reinterpret_cast<const u32x4_t*>(src + row * p.r + c);
+  *reinterpret_cast<u32x4_t*>(p.out + ((int64_t)k * p.W + row) * p.rp + c) = v;
 }
 
 // ---- pieces shared by the two adapter products -----------------------------------------
@@ -204,21 +239,27 @@ struct NtArgs {
   RouteView rv;
 };
 
+struct NtLds {
+  __attribute__((aligned(1024))) uint16_t a[kStages][SM * SK];
+  __attribute__((aligned(1024))) uint16_t b[kStages][SJ * SK];
+  int row[SM];
+};
+
 // C[z][m][j] = sum over slice z of A[m][i] B_a[j][i]: 128 grouped rows of one
 // segment by 64 ranks; 4 waves of 32 rows; the copies of two stages are in
 // flight while a third is multiplied. With BT the adapter's operand has its
 // ranks contiguous (L1 as stored) and its fragments come through the LDS
 // transpose read; without, its reduction is contiguous (L2 as stored).
 template <bool BT>
-__global__ __launch_bounds__(kThreads) void multi_nt_kernel(NtArgs p) {
-  __shared__ __attribute__((aligned(1024))) uint16_t sA[kStages][SM * SK];
-  __shared__ __attribute__((aligned(1024))) uint16_t sB[kStages][SJ * SK];
-  __shared__ int s_row[SM];
+__device__ __forceinline__ void nt_body(const NtArgs& p, int z, NtLds& lds) {
+  auto& sA = lds.a;
+  auto& sB = lds.b;
+  auto& s_row = lds.row;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const RoutePiece pc = route_piece(p.rv, (int)blockIdx.x, SM);
   if (pc.hi <= pc.lo) return;                       // uniform: no barrier was reached
   const int j0 = (int)blockIdx.y * SJ;
-  const int64_t z0 = (int64_t)blockIdx.z * p.split;
+  const int64_t z0 = (int64_t)z * p.split;
   const int64_t z1 = z0 + p.split < p.len ? z0 + p.split : p.len;
   const int ns = z0 < z1 ? (int)((z1 - z0 + SK - 1) / SK) : 0;
   if (tid < SM) s_row[tid] = p.rv.perm[pc.lo + tid < pc.hi ? pc.lo + tid : pc.hi - 1];
@@ -303,7 +344,7 @@ __global__ __launch_bounds__(kThreads) void multi_nt_kernel(NtArgs p) {
     }
   }
   // lane l, register v -> row (v%4) + 4(l/32) + 8(v/4), column l%32
-  float* C = p.C + (int64_t)blockIdx.z * p.M * p.rp;
+  float* C = p.C + (int64_t)z * p.M * p.rp;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int j = j0 + t * 32 + (lane & 31);
@@ -315,38 +356,76 @@ __global__ __launch_bounds__(kThreads) void multi_nt_kernel(NtArgs p) {
   }
 }
 
-// From the partials P [Z][M][rp]: scaled [M][rp] = bf16(s_a sum) and plain
-// [M][r] = bf16(sum), either may be null; rows without an adapter and columns
-// >= r are zero. 4 columns per thread.
-__global__ __launch_bounds__(256) void multi_tr_kernel(const float* __restrict__ P, int Z, int64_t M, int r, int rp,
-                                                       const int32_t* __restrict__ ids, int A,
-                                                       const float* __restrict__ scale, uint16_t* __restrict__ scaled,
-                                                       uint16_t* __restrict__ plain) {
-  const int w4 = rp / 4;
+// Slices z < zu: U = dY L2_a^T (arguments u); the others: T = X L1_a (t).
+__global__ __launch_bounds__(kThreads) void multi_nt_kernel(NtArgs u, int zu, NtArgs t) {
+  __shared__ NtLds lds;
+  const int z = (int)blockIdx.z;
+  if (z < zu) nt_body<false>(u, z, lds);
+  else nt_body<true>(t, z - zu, lds);
+}
+
+// scaled [M + 1][rp] = bf16(s_a sum_z S[z]), its last row zero; plain [M][r] =
+// bf16(sum_z P[z]); either may be null. Partials [Z][M][rp]. Rows without an
+// adapter and columns >= r are zero.
+struct SumArgs {
+  const float* S;
+  const float* P;
+  int Zs, Zp;
+  int64_t M;
+  int r, rp;
+  const int32_t* ids;
+  int A;
+  const float* scale;
+  uint16_t* scaled;
+  uint16_t* plain;
+};
+
+__device__ __forceinline__ f32x4_t sum_slices(const float* p, int Z, int64_t pitch) {
+  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+  int z = 0;
+  for (; z + 4 <= Z; z += 4) {  // loads of 4 slices in flight, added in order
+    f32x4_t q[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) q[u] = *reinterpret_cast<const f32x4_t*>(p + (int64_t)(z + u) * pitch);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v += q[u];
+  }
+  for (; z < Z; ++z) v += *reinterpret_cast<const f32x4_t*>(p + (int64_t)z * pitch);
+  return v;
+}
+
+__device__ __forceinline__ u32x2_t pack4(const f32x4_t& v, float s) {
+  return u32x2_t{pack_bf16x2(s * v.x, s * v.y), pack_bf16x2(s * v.z, s * v.w)};
+}
+
+// 4 columns per thread of workgroups below `blocks`; the others lay out the
+// GEMM's adapter operand.
+__global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs p, int blocks, LayArgs lay, RouteView rv) {
+  if ((int)blockIdx.x >= blocks) {
+    const int b = (int)blockIdx.x - blocks, k = b / lay.blocks;
+    if (k >= rv.count[0]) return;                   // uniform
+    if (lay.transpose) lay_transposed(lay, rv, k, b - k * lay.blocks);
+    else lay_padded(lay, rv, k, b - k * lay.blocks);
+    return;
+  }
+  const int w4 = p.rp / 4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= M * w4) return;
   const int64_t m = i / w4;
   const int j = (int)(i - m * w4) * 4;
-  const int a = ids[m];
-  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-  float s = 0.0f;
-  if (a >= 0 && a < A && j < r) {
-    s = scale[a];
-    const float* p = P + m * rp + j;
-    int z = 0;
-    for (; z + 4 <= Z; z += 4) {  // loads of 4 slices in flight, added in order
-      f32x4_t q[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) q[u] = *reinterpret_cast<const f32x4_t*>(p + (int64_t)(z + u) * M * rp);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) v += q[u];
-    }
-    for (; z < Z; ++z) v += *reinterpret_cast<const f32x4_t*>(p + (int64_t)z * M * rp);
+  if (m > p.M) return;
+  const int a = m < p.M ? p.ids[m] : -1;
+  const bool in = a >= 0 && a < p.A && j < p.r;
+  const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t pitch = p.M * p.rp, at = m * p.rp + j;
+  f32x4_t v = zero;
+  if (p.scaled) {
+    if (in) v = sum_slices(p.S + at, p.Zs, pitch);
+    *reinterpret_cast<u32x2_t*>(p.scaled + at) = pack4(v, in ? p.scale[a] : 0.0f);
   }
-  if (plain && j < r)
-    *reinterpret_cast<u32x2_t*>(plain + m * r + j) = u32x2_t{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
-  if (scaled)
-    *reinterpret_cast<u32x2_t*>(scaled + m * rp + j) = u32x2_t{pack_bf16x2(s * v.x, s * v.y), pack_bf16x2(s * v.z, s * v.w)};
+  if (p.plain && m < p.M && j < p.r) {
+    if (!p.scaled || p.P != p.S) v = in ? sum_slices(p.P + at, p.Zp, pitch) : zero;
+    *reinterpret_cast<u32x2_t*>(p.plain + m * p.r + j) = pack4(v, 1.0f);
+  }
 }
 
 struct TnArgs {
@@ -379,14 +458,19 @@ __device__ __forceinline__ int64_t tn_at(int64_t w, int j, int64_t W, int in) {
 // ranks on the lanes (a row of dL1 is r contiguous values), otherwise the
 // columns (a row of dL2 is W contiguous values): the same products with the
 // MFMA operands exchanged.
+struct TnLds {
+  __attribute__((aligned(1024))) char ring[kStages * kTnStageBytes];
+  int row[kTnRows];
+};
+
 template <bool RANKS_IN>
-__global__ __launch_bounds__(kThreads) void multi_tn_kernel(TnArgs p) {
-  __shared__ __attribute__((aligned(1024))) char ring[kStages * kTnStageBytes];
-  __shared__ int s_row[kTnRows];
+__device__ __forceinline__ void tn_body(const TnArgs& p, int bx, TnLds& lds) {
+  char* ring = lds.ring;
+  int* s_row = lds.row;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const RoutePiece pc = route_piece(p.rv, (int)blockIdx.z, p.rows);
   if (pc.hi <= pc.lo) return;                       // uniform: no barrier was reached
-  const int64_t c0 = (int64_t)blockIdx.x * SM;
+  const int64_t c0 = (int64_t)bx * SM;
   const int j0 = (int)blockIdx.y * SJ;
   const int ns = (pc.hi - pc.lo + SK - 1) / SK;
   const char* zero = reinterpret_cast<const char*>(g_multi_zero);
@@ -490,11 +574,19 @@ __global__ __launch_bounds__(kThreads) void multi_tn_kernel(TnArgs p) {
     }
 }
 
+// Column tiles below x1: dL1 (arguments g1); the others: dL2 (g2).
+__global__ __launch_bounds__(kThreads) void multi_tn_kernel(TnArgs g1, int x1, TnArgs g2) {
+  __shared__ TnLds lds;
+  const int x = (int)blockIdx.x;
+  if (x < x1) tn_body<true>(g1, x, lds);
+  else tn_body<false>(g2, x - x1, lds);
+}
+
 // The gradients that multi_tn_kernel left open: the sums of a segment's
-// several pieces, in order, and zeros for adapters without rows. Workgroup
-// (x, a); 4 consecutive output values per thread and step.
+// several pieces, in order, and zeros for adapters without rows. Workgroup bx
+// of `blocks` for adapter blockIdx.y; 4 consecutive values per thread and step.
 template <bool RANKS_IN>
-__global__ __launch_bounds__(256) void multi_tn_reduce_kernel(TnArgs p) {
+__device__ __forceinline__ void finish_body(const TnArgs& p, int bx, int blocks) {
   const int a = (int)blockIdx.y, lane = threadIdx.x & 63;
   const int n = p.rv.count[0];
   int k = -1;
@@ -513,7 +605,7 @@ __global__ __launch_bounds__(256) void multi_tn_reduce_kernel(TnArgs p) {
   }
   const float f = p.scale ? p.scale[a] : 1.0f;
   const int64_t total = p.W * p.r;                  // r % 8 == 0, W % 8 == 0: 4 values never leave a row
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < total; i += (int64_t)gridDim.x * 1024) {
+  for (int64_t i = ((int64_t)bx * 256 + threadIdx.x) * 4; i < total; i += (int64_t)blocks * 1024) {
     f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (pieces > 0) {
       const int64_t w = RANKS_IN ? i / p.r : i % p.W;
@@ -528,6 +620,12 @@ __global__ __launch_bounds__(256) void multi_tn_reduce_kernel(TnArgs p) {
     else
       *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.out) + o) = f32x4_t{f * v.x, f * v.y, f * v.z, f * v.w};
   }
+}
+
+__global__ __launch_bounds__(256) void multi_finish_kernel(TnArgs g1, int x1, TnArgs g2) {
+  const int x = (int)blockIdx.x;
+  if (x < x1) finish_body<true>(g1, x, x1);
+  else finish_body<false>(g2, x - x1, (int)gridDim.x - x1);
 }
 
 __global__ __launch_bounds__(256) void multi_zero_kernel(uint32_t* __restrict__ p, int64_t words) {
@@ -547,6 +645,8 @@ __global__ __launch_bounds__(256) void multi_pad_rows_kernel(const uint16_t* __r
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Workgroups per adapter of multi_finish_kernel: 4 values per thread, a few steps.
+int finish_blocks(int64_t values) { return (int)(cdiv(values, 4096) < 128 ? cdiv(values, 4096) : 128); }
 unsigned capped(int64_t blocks) { return (unsigned)(blocks < 1 ? 1 : blocks > 16384 ? 16384 : blocks); }
 
 // Reduction slices of the NT products: about two workgroups per CU, the
@@ -567,11 +667,11 @@ NtSplit nt_split(int64_t M, int64_t len, int A, int rp) {
   return NtSplit{per * SK, (int)cdiv(steps, per)};
 }
 
-// Rows per piece of the TN products: whole segments up to 2048 rows, so that
-// most gradients are written once; fewer when the launch would not fill the
-// device (128 columns per workgroup).
-int tn_rows(int64_t M, int64_t W, int r) {
-  const int64_t tiles = cdiv(W, SM) * cdiv(r, SJ);
+// Rows per piece of the TN products: whole segments up to kTnRows rows, so
+// that most gradients are written once; fewer when the launch would not fill
+// the device (128 columns of dL1 or dL2 per workgroup).
+int tn_rows(int64_t M, int64_t K, int64_t N, int r) {
+  const int64_t tiles = (cdiv(K, SM) + cdiv(N, SM)) * cdiv(r, SJ);
   const int64_t want = cdiv(2 * (int64_t)device_cu_count(), tiles);   // pieces
   int64_t rows = cdiv(cdiv(M, want), SK) * SK;
   if (rows > kTnRows) rows = kTnRows;
@@ -579,8 +679,8 @@ int tn_rows(int64_t M, int64_t W, int r) {
   return (int)rows;
 }
 
-int64_t tn_part_floats(int64_t M, int64_t W, int r, int A) {
-  const int rows = tn_rows(M, W, r);
+int64_t tn_part_floats(int64_t M, int64_t K, int64_t N, int64_t W, int r, int A) {
+  const int rows = tn_rows(M, K, N, r);
   if (M <= rows) return 0;                          // one piece per segment
   return (M / rows + (A < M ? A : M)) * W * cdiv(r, SJ) * SJ;
 }
@@ -625,12 +725,11 @@ MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, in
   L.wd_off = take(K * np * 2);
   L.dy_off = take(bwd && N % 64 ? M * np * 2 : 0);
   const NtSplit t = nt_split(M, K, A, (int)rp), u = nt_split(M, N, A, (int)rp);
-  int64_t part = t.Z * M * rp;
+  int64_t part = t.Z * M * rp;                       // T's, then U's; later dL1's, then dL2's
   if (bwd) {
-    if (u.Z * M * rp > part) part = u.Z * M * rp;
-    const int64_t a = tn_part_floats(M, K, r, A), b = tn_part_floats(M, N, r, A);
-    if (a > part) part = a;
-    if (b > part) part = b;
+    part += u.Z * M * rp;
+    const int64_t grads = tn_part_floats(M, K, N, K, r, A) + tn_part_floats(M, K, N, N, r, A);
+    if (grads > part) part = grads;
   }
   L.part_off = take(part * 4);
   L.total = off;
@@ -639,36 +738,45 @@ MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, in
 
 namespace {
 
-hipError_t route(const int32_t* ids, int64_t M, int A, char* ws, size_t perm, size_t start, size_t adapter,
-                 size_t count, int32_t* slot, RouteView* rv, hipStream_t stream) {
-  int32_t* p = reinterpret_cast<int32_t*>(ws + perm);
-  int32_t* s = reinterpret_cast<int32_t*>(ws + start);
-  int32_t* a = reinterpret_cast<int32_t*>(ws + adapter);
-  int32_t* c = reinterpret_cast<int32_t*>(ws + count);
-  hipLaunchKernelGGL(route_kernel, dim3((unsigned)(A + 1)), dim3(kRouteThreads), (size_t)(A + 31) / 32 * 4, stream,
-                     ids, (int)M, A, p, s, a, c, slot);
-  *rv = RouteView{p, s, a, c};
+RouteArgs route_args(const int32_t* ids, int64_t M, int A, char* ws, size_t perm, size_t start, size_t adapter,
+                     size_t count, int32_t* slot) {
+  RouteArgs p;
+  p.ids = ids;
+  p.M = (int)M;
+  p.A = A;
+  p.perm = reinterpret_cast<int32_t*>(ws + perm);
+  p.start = reinterpret_cast<int32_t*>(ws + start);
+  p.adapter = reinterpret_cast<int32_t*>(ws + adapter);
+  p.count = reinterpret_cast<int32_t*>(ws + count);
+  p.slot = slot;
+  return p;
+}
+
+RouteView view_of(const RouteArgs& p) { return RouteView{p.perm, p.start, p.adapter, p.count}; }
+
+// Arguments of T = X L1_a (b_t) or U = dY L2_a^T over rows of `len` values.
+NtArgs nt_args(const uint16_t* rows, int64_t len, const uint16_t* B, int64_t b_stride, int64_t M, int r, int rp,
+               const NtSplit& sp, const RouteView& rv, float* part) {
+  NtArgs a;
+  a.A = rows; a.B = B; a.C = part;
+  a.lda = len; a.ldb = len; a.b_stride = b_stride;
+  a.M = M; a.len = len; a.split = sp.len;
+  a.r = r; a.rp = rp; a.rv = rv;
+  return a;
+}
+
+hipError_t launch_nt(const NtArgs* u, int zu, const NtArgs* t, int zt, int64_t M, int A, hipStream_t stream) {
+  const NtArgs& any = u ? *u : *t;
+  const int64_t pieces = M / SM + (A < M ? A : M);
+  hipLaunchKernelGGL(multi_nt_kernel, dim3((unsigned)pieces, (unsigned)(any.rp / SJ), (unsigned)(zu + zt)),
+                     dim3(kThreads), 0, stream, u ? *u : any, zu, t ? *t : any);
   return hipGetLastError();
 }
 
-// scaled [M][rp] and/or plain [M][r] of rows times their adapters' operand.
-template <bool BT>
-hipError_t rows_by_adapter(const uint16_t* X, int64_t len, const uint16_t* B, int64_t ldb, int64_t b_stride, int64_t M,
-                           int r, int rp, int A, const int32_t* ids, const float* scale, const RouteView& rv,
-                           float* part, uint16_t* scaled, uint16_t* plain, hipStream_t stream) {
-  const NtSplit sp = nt_split(M, len, A, rp);
-  NtArgs a;
-  a.A = X; a.B = B; a.C = part;
-  a.lda = len; a.ldb = ldb; a.b_stride = b_stride;
-  a.M = M; a.len = len; a.split = sp.len;
-  a.r = r; a.rp = rp; a.rv = rv;
-  const int64_t pieces = M / SM + (A < M ? A : M);
-  hipLaunchKernelGGL(multi_nt_kernel<BT>, dim3((unsigned)pieces, (unsigned)(rp / SJ), (unsigned)sp.Z), dim3(kThreads),
-                     0, stream, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(multi_tr_kernel, dim3((unsigned)cdiv(M * rp / 4, 256)), dim3(256), 0, stream, part, sp.Z, M, r, rp,
-                     ids, A, scale, scaled, plain);
+hipError_t launch_sum(const SumArgs& s, const LayArgs& lay, int64_t segs, const RouteView& rv, hipStream_t stream) {
+  const int64_t blocks = cdiv((s.M + 1) * s.rp / 4, 256);
+  hipLaunchKernelGGL(multi_sum_kernel, dim3((unsigned)(blocks + segs * lay.blocks)), dim3(256), 0, stream, s, (int)blocks,
+                     lay, rv);
   return hipGetLastError();
 }
 
@@ -685,9 +793,12 @@ hipError_t gemm_by_adapter(const uint16_t* X, int64_t K, const uint16_t* B, int6
     MultiSlab slab;
     slab.rv = rv;
     if (rows < M) {
-      const hipError_t e = route(ids + r0, rows, A, ws, L.perm2_off, L.start2_off, L.adapter2_off, L.count2_off,
-                                 nullptr, &slab.rv, stream);
+      const RouteArgs p =
+          route_args(ids + r0, rows, A, ws, L.perm2_off, L.start2_off, L.adapter2_off, L.count2_off, nullptr);
+      hipLaunchKernelGGL(route_kernel, dim3((unsigned)(A + 1)), dim3(1024), 0, stream, p);
+      const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
+      slab.rv = view_of(p);
     }
     slab.slot = slot;
     slab.zero_row = M - r0;
@@ -706,27 +817,17 @@ hipError_t zero_words(void* p, int64_t bytes, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool RANKS_IN>
-hipError_t gradient(const uint16_t* L, int64_t W, const uint16_t* S, int64_t lds, int64_t M, int r, int A,
-                    const float* scale, const RouteView& rv, float* part, void* out, bool out_bf16,
-                    hipStream_t stream) {
+TnArgs tn_args(const uint16_t* L, int64_t W, const uint16_t* S, int64_t lds, int r, int rows, const float* scale,
+               const RouteView& rv, float* part, void* out, bool out_bf16) {
   TnArgs a;
   a.L = L; a.S = S; a.out = out; a.part = part; a.scale = scale;
   a.ldl = W; a.lds = lds; a.W = W;
   a.slab = W * cdiv(r, SJ) * SJ;
   a.r = r;
-  a.rows = tn_rows(M, W, r);
+  a.rows = rows;
   a.out_bf16 = out_bf16;
   a.rv = rv;
-  const int64_t pieces = M / a.rows + (A < M ? A : M);
-  hipLaunchKernelGGL(multi_tn_kernel<RANKS_IN>, dim3((unsigned)cdiv(W, SM), (unsigned)cdiv(r, SJ), (unsigned)pieces),
-                     dim3(kThreads), 0, stream, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  int64_t blocks = cdiv(W * r, 4096);
-  if (blocks > 256) blocks = 256;
-  hipLaunchKernelGGL(multi_tn_reduce_kernel<RANKS_IN>, dim3((unsigned)blocks, (unsigned)A), dim3(256), 0, stream, a);
-  return hipGetLastError();
+  return a;
 }
 
 }  // namespace
@@ -775,18 +876,19 @@ hipError_t multi_forward(const NF4View& W, const NF4Table& tab, const uint16_t* 
   if (multi_small_fits(M, K, N))
     return multi_forward_small(W, tab, X, M, MultiIds{ids, A, scale}, L1, L2, r, Y, T_out, part,
                                reinterpret_cast<float*>(base + L.tpart_off), stream);
-  RouteView rv;
-  hipError_t e = route(ids, M, A, base, L.perm_off, L.start_off, L.adapter_off, L.count_off, slot, &rv, stream);
+  const RouteArgs ra = route_args(ids, M, A, base, L.perm_off, L.start_off, L.adapter_off, L.count_off, slot);
+  const RouteView rv = view_of(ra);
+  hipLaunchKernelGGL(multi_prep_kernel<false>, dim3((unsigned)(A + 1 + dequant_rows_blocks(W))), dim3(256), 0, stream, ra,
+                     W, tab, wd, (int64_t)0, 1);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  e = rows_by_adapter<true>(X, K, L1, 0, K * r, M, r, rp, A, ids, scale, rv, part, sT, T_out, stream);
+  const NtSplit sp = nt_split(M, K, A, rp);
+  const NtArgs t = nt_args(X, K, L1, K * r, M, r, rp, sp, rv, part);
+  e = launch_nt(nullptr, 0, &t, sp.Z, M, A, stream);
   if (e != hipSuccess) return e;
-  e = zero_words(sT + M * rp, rp * 2, stream);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(multi_l2t_kernel, dim3((unsigned)cdiv(N, 64), (unsigned)(rp / 64), (unsigned)segs), dim3(256), 0,
-                     stream, L2, N, r, rp, rv, l2t);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  e = launch_dequant_rows(W, tab, wd, stream);
+  const SumArgs s{part, part, sp.Z, sp.Z, M, r, rp, ids, A, scale, sT, T_out};
+  const LayArgs lay{L2, l2t, N, r, rp, (int)(cdiv(N, 64) * (rp / 64)), true};
+  e = launch_sum(s, lay, segs, rv, stream);
   if (e != hipSuccess) return e;
   return gemm_by_adapter(X, K, wd, M, N, sT, l2t, rp, N * rp, slot, Y, ids, A, rv, base, L, kTimeFwdGemm, stream);
 }
@@ -807,26 +909,33 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
   uint16_t* sU = reinterpret_cast<uint16_t*>(base + L.st_off);
   int32_t* slot = reinterpret_cast<int32_t*>(base + L.slot_off);
   float* part = reinterpret_cast<float*>(base + L.part_off);
-  RouteView rv;
-  hipError_t e = route(ids, M, A, base, L.perm_off, L.start_off, L.adapter_off, L.count_off, slot, &rv, stream);
+  const RouteArgs ra = route_args(ids, M, A, base, L.perm_off, L.start_off, L.adapter_off, L.count_off, slot);
+  const RouteView rv = view_of(ra);
+  // the GEMM reduces over whole stages of 64: a ragged N is padded with zeros
+  const int64_t np = cdiv(N, 64) * 64;
+  uint16_t* wdt = reinterpret_cast<uint16_t*>(base + L.wd_off);
+  const int gx = (int)cdiv(K, 128);
+  const int64_t dequant_blocks = dX ? gx * cdiv(np, 128) : 0;
+  hipLaunchKernelGGL(multi_prep_kernel<true>, dim3((unsigned)(A + 1 + dequant_blocks)), dim3(256), 0, stream, ra, W, tab,
+                     wdt, np, gx);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  e = rows_by_adapter<false>(dY, N, L2, N, N * r, M, r, rp, A, ids, scale, rv, part, sU, nullptr, stream);
+
+  const NtSplit su = nt_split(M, N, A, rp), st = nt_split(M, K, A, rp);
+  float* upart = part + (int64_t)st.Z * M * rp;
+  const NtArgs u = nt_args(dY, N, L2, N * r, M, r, rp, su, rv, upart), t = nt_args(X, K, L1, K * r, M, r, rp, st, rv, part);
+  e = launch_nt(&u, su.Z, T ? nullptr : &t, T ? 0 : st.Z, M, A, stream);
   if (e != hipSuccess) return e;
+  uint16_t* tbuf = T ? nullptr : reinterpret_cast<uint16_t*>(base + L.t_off);
+  uint16_t* l1p = reinterpret_cast<uint16_t*>(base + L.b2_off);
+  const bool padded = dX && rp != r;
+  const SumArgs s{upart, part, su.Z, st.Z, M, r, rp, ids, A, scale, sU, tbuf};
+  const LayArgs lay{L1, l1p, K, r, rp, (int)cdiv(K * rp / 8, 256), false};
+  e = launch_sum(s, lay, padded ? segs : 0, rv, stream);
+  if (e != hipSuccess) return e;
+  if (!T) T = tbuf;
+
   if (dX) {
-    e = zero_words(sU + M * rp, rp * 2, stream);
-    if (e != hipSuccess) return e;
-    const uint16_t* b2 = L1;
-    const bool padded = rp != r;
-    if (padded) {
-      uint16_t* l1p = reinterpret_cast<uint16_t*>(base + L.b2_off);
-      hipLaunchKernelGGL(multi_l1p_kernel, dim3((unsigned)cdiv(K * rp / 8, 256), (unsigned)segs), dim3(256), 0, stream,
-                         L1, K, r, rp, rv, l1p);
-      e = hipGetLastError();
-      if (e != hipSuccess) return e;
-      b2 = l1p;
-    }
-    // the GEMM reduces over whole stages of 64: pad a ragged N with zeros
-    const int64_t np = cdiv(N, 64) * 64;
     const uint16_t* dYp = dY;
     if (np != N) {
       uint16_t* p = reinterpret_cast<uint16_t*>(base + L.dy_off);
@@ -836,22 +945,23 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
       if (e != hipSuccess) return e;
       dYp = p;
     }
-    uint16_t* wdt = reinterpret_cast<uint16_t*>(base + L.wd_off);
-    e = launch_dequant_cols(W, tab, wdt, np, stream);
-    if (e != hipSuccess) return e;
-    e = gemm_by_adapter(dYp, np, wdt, M, K, sU, b2, rp, K * rp, padded ? slot : nullptr, dX, ids, A, rv, base, L,
-                        kTimeDxGemm, stream);
+    e = gemm_by_adapter(dYp, np, wdt, M, K, sU, padded ? l1p : L1, rp, K * rp, padded ? slot : nullptr, dX, ids, A, rv,
+                        base, L, kTimeDxGemm, stream);
     if (e != hipSuccess) return e;
   }
-  if (!T) {
-    uint16_t* t = reinterpret_cast<uint16_t*>(base + L.t_off);
-    e = rows_by_adapter<true>(X, K, L1, 0, K * r, M, r, rp, A, ids, scale, rv, part, nullptr, t, stream);
-    if (e != hipSuccess) return e;
-    T = t;
-  }
-  e = gradient<true>(X, K, sU, rp, M, r, A, nullptr, rv, part, dL1, grad_bf16, stream);
+
+  const int rows = tn_rows(M, K, N, r);
+  float* part2 = part + tn_part_floats(M, K, N, K, r, A);
+  const TnArgs g1 = tn_args(X, K, sU, rp, r, rows, nullptr, rv, part, dL1, grad_bf16);
+  const TnArgs g2 = tn_args(dY, N, T, r, r, rows, scale, rv, part2, dL2, grad_bf16);
+  const int64_t pieces = M / rows + segs;
+  hipLaunchKernelGGL(multi_tn_kernel, dim3((unsigned)(cdiv(K, SM) + cdiv(N, SM)), (unsigned)cdiv(r, SJ), (unsigned)pieces),
+                     dim3(kThreads), 0, stream, g1, (int)cdiv(K, SM), g2);
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return gradient<false>(dY, N, T, r, M, r, A, scale, rv, part, dL2, grad_bf16, stream);
+  const int b1 = finish_blocks(K * r), b2 = finish_blocks(N * r);
+  hipLaunchKernelGGL(multi_finish_kernel, dim3((unsigned)(b1 + b2), (unsigned)A), dim3(256), 0, stream, g1, b1, g2);
+  return hipGetLastError();
 }
 
 }  // namespace qlora

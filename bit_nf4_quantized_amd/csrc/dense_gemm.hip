@@ -157,10 +157,12 @@ __device__ __forceinline__ void stage_load_one(const uint16_t* __restrict__ P, c
                :: "v"(o.off[j]), "s"(base), "s"(m0) : "memory", "m0");
 }
 
+// The same copy from a 64-bit address per lane.
 template <int NI>
-__device__ __forceinline__ void stage_load(const uint16_t* __restrict__ P, const StageOffsets<NI>& o, uint16_t* lds) {
-#pragma unroll
-  for (int j = 0; j < NI; ++j) stage_load_one(P, o, lds, j);
+__device__ __forceinline__ void stage_load_wide(const uint16_t* src, uint16_t* lds, int j) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t*)(lds + (wave * NI + j) * RPI * TK));
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(src), "s"(m0) : "memory", "m0");
 }
 
 // A wave-uniform address in scalar registers, as the copies take it.
@@ -176,9 +178,9 @@ __device__ __forceinline__ int lds_off(int row, int chunk) { return row * TK + (
 // One TMX x TN output tile at (m0, n0). smem holds the stage tiles: two A
 // buffers, then three B buffers, kStageElems elements each. MULTI: the tile's
 // rows are rows m0 .. of the grouped order, and the slab has the K2 columns of
-// every segment that meets them, with zeros (slab.zero_row) in the place of
-// the other segments' rows.
-template <bool ADD, int TMX, bool MULTI>
+// every group of segments that meets them, with zeros (slab.zero_row) in the
+// place of the other groups' rows. WIDE: A's rows span more than 32-bit offsets.
+template <bool ADD, int TMX, bool MULTI, bool WIDE>
 __device__ __forceinline__ void gemm_tile(const DenseArgs& p, const MultiSlab& slab, int64_t m0, int64_t n0,
                                           uint16_t* smem) {
   using S = TileShape<TMX>;
@@ -186,12 +188,13 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, const MultiSlab& s
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave / WGN, wn = wave % WGN;
   const int nmain = (int)(p.K / TK);
-  int nslab = (int)(p.K2 / TK), seg0 = 0;
-  const int per_seg = nslab;                        // slab stages per segment (MULTI)
+  int nslab = (int)(p.K2 / TK), group0 = 0, segs = 0;
+  const int per_group = nslab;                      // slab stages per group (MULTI)
   if constexpr (MULTI) {
     const RouteRange rg = route_range(slab.rv, (int)m0, (int)m0 + TMX);
-    seg0 = rg.lo;
-    nslab = (rg.hi > rg.lo ? rg.hi - rg.lo : 0) * per_seg;
+    group0 = rg.lo / slab.pack;
+    nslab = rg.hi > rg.lo ? ((rg.hi - 1) / slab.pack - group0 + 1) * per_group : 0;
+    segs = rg.hi;
   }
   const int nk = nmain + nslab;
   const int32_t* perm = MULTI ? slab.rv.perm : nullptr;
@@ -211,25 +214,35 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, const MultiSlab& s
   // Stage st covers columns [64 st, 64 st + 64) of (A, B) for st < nmain,
   // then the slab (A2, B2). Operand selection is branch-free so that the
   // copy can be scheduled among the MFMAs of the same block.
-  // MULTI: slab stage i's segment and first column, A2's copy instruction j
-  // of it, and its operand B2
+  // MULTI: slab stage i's group and first column, A2's copy instruction j of
+  // it, and its operand B2
   auto slab_at = [&](int i, int* col) {
-    const int s = __builtin_amdgcn_readfirstlane(i / per_seg);
-    *col = (i - s * per_seg) * TK;
-    return seg0 + s;
+    const int s = __builtin_amdgcn_readfirstlane(i / per_group);
+    *col = (i - s * per_group) * TK;
+    return group0 + s;
   };
-  auto slab_a = [&](int k, int j) -> uint32_t {
+  auto slab_a = [&](int g, int j) -> uint32_t {
     const int rloc = (wave * S::kIpwA + j) * RPI + (lane >> 3);
     const int row = (int)m0 + rloc;
-    const bool in = row >= slab.rv.start[k] && row < slab.rv.start[k + 1];
+    const int k = g * slab.pack, end = k + slab.pack < segs ? k + slab.pack : segs;   // segs: past the tile's last
+    const bool in = row >= slab.rv.start[k] && row < slab.rv.start[end];
     const uint32_t chunk = (uint32_t)((lane & 7) ^ swz(rloc));
     return in ? offA2.off[j] : (uint32_t)((slab.zero_row * p.ld2 + chunk * 8) * 2);
   };
-  auto slab_b = [&](int k) -> const uint16_t* {
-    int a = __builtin_amdgcn_readfirstlane(slab.rv.adapter[k]);
-    if (slab.slot) a = __builtin_amdgcn_readfirstlane(slab.slot[a]);
-    return p.B2 + (int64_t)a * slab.b2_stride;
+  auto slab_b = [&](int g) -> const uint16_t* {
+    const int i = slab.by_adapter ? __builtin_amdgcn_readfirstlane(slab.rv.adapter[g]) : g;
+    return p.B2 + (int64_t)i * slab.b2_stride;
   };
+  // WIDE: the lane's rows of A
+  const uint16_t* rowA[WIDE ? S::kIpwA : 1];
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int j = 0; j < S::kIpwA; ++j) {
+      const int rloc = (wave * S::kIpwA + j) * RPI + (lane >> 3);
+      const int64_t row = m0 + rloc < p.M ? m0 + rloc : p.M - 1;
+      rowA[j] = p.A + (int64_t)perm[row] * p.lda + ((lane & 7) ^ swz(rloc)) * 8;
+    }
+  }
   auto a_buf = [&](int st) { return smem + (st & 1) * kStageElems; };
   auto b_buf = [&](int st) { return smem + (2 + st % 3) * kStageElems; };
   // copy instruction q of stage st: q < kIpwA are the A tile's, the rest
@@ -239,7 +252,9 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, const MultiSlab& s
     if constexpr (MULTI) {
       int k = 0, k0 = st * TK;
       if (in_slab) k = slab_at(st - nmain, &k0);
-      if (q < S::kIpwA) {
+      if (WIDE && !in_slab && q < S::kIpwA) {
+        stage_load_wide<S::kIpwA>(rowA[q] + k0, a_buf(st), q);
+      } else if (q < S::kIpwA) {
         StageOffsets<S::kIpwA> oa;
         oa.off[q] = in_slab ? slab_a(k, q) : offA.off[q];
         stage_load_one(uniform((in_slab ? p.A2 : p.A) + k0), oa, a_buf(st), q);
@@ -449,7 +464,7 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, const MultiSlab& s
   }
 }
 
-template <bool ADD, bool MULTI>
+template <bool ADD, bool MULTI, bool WIDE>
 __device__ __forceinline__ void gemm_nt_body(const DenseArgs& p, const MultiSlab& slab) {
   __shared__ __attribute__((aligned(1024))) uint16_t smem[5 * kStageElems];  // A x 2, B x 3
   const int bid = blockIdx.x;
@@ -467,7 +482,7 @@ __device__ __forceinline__ void gemm_nt_body(const DenseArgs& p, const MultiSlab
     const int tl = t - g * group * p.full_n;
     const int tm = first_m + tl % gm;
     const int tn = tl / gm;
-    gemm_tile<ADD, TM, MULTI>(p, slab, (int64_t)tm * TM, (int64_t)tn * TN, smem);
+    gemm_tile<ADD, TM, MULTI, WIDE>(p, slab, (int64_t)tm * TM, (int64_t)tn * TN, smem);
   } else {
     // the tail tile-columns, as half- or quarter-height tiles; dispatched
     // last, they fill the last round of workgroups
@@ -477,19 +492,20 @@ __device__ __forceinline__ void gemm_nt_body(const DenseArgs& p, const MultiSlab
     if (m0 >= p.M) return;  // a piece of a last tile-row beyond M (uniform per workgroup)
     const int64_t n0 = (int64_t)(p.full_n + h % ncols) * TN;
     if (p.tail_split == 4)
-      gemm_tile<ADD, TM / 4, MULTI>(p, slab, m0, n0, smem);
+      gemm_tile<ADD, TM / 4, MULTI, WIDE>(p, slab, m0, n0, smem);
     else
-      gemm_tile<ADD, TM / 2, MULTI>(p, slab, m0, n0, smem);
+      gemm_tile<ADD, TM / 2, MULTI, WIDE>(p, slab, m0, n0, smem);
   }
 }
 
 template <bool ADD>
 __global__ __launch_bounds__(kThreads, 1) void gemm_nt_kernel(DenseArgs p) {
-  gemm_nt_body<ADD, false>(p, MultiSlab{});
+  gemm_nt_body<ADD, false, false>(p, MultiSlab{});
 }
 
+template <bool WIDE>
 __global__ __launch_bounds__(kThreads, 1) void gemm_nt_multi_kernel(DenseArgs p, MultiSlab slab) {
-  gemm_nt_body<false, true>(p, slab);
+  gemm_nt_body<false, true, WIDE>(p, slab);
 }
 
 __global__ __launch_bounds__(256) void dequant_rows_kernel(NF4View W, NF4Table tab, uint16_t* __restrict__ out) {
@@ -588,7 +604,7 @@ hipError_t launch_gemm_nt_multi(const uint16_t* A, int64_t lda, const uint16_t* 
                                 int64_t K, const uint16_t* A2, const uint16_t* B2, int64_t ld2, const MultiSlab& slab,
                                 uint16_t* C, int64_t ldc, hipStream_t stream) {
   const int64_t two_gb = (int64_t)1 << 31, four_gb = (int64_t)1 << 32;
-  if (N * ldb * 2 >= two_gb || N * ld2 * 2 >= two_gb || M * lda * 2 >= four_gb || (slab.zero_row + 1) * ld2 * 2 >= four_gb)
+  if (N * ldb * 2 >= two_gb || N * ld2 * 2 >= two_gb || (slab.zero_row + 1) * ld2 * 2 >= four_gb)
     return hipErrorInvalidValue;
   DenseArgs p;
   p.A = A; p.B = B; p.A2 = A2; p.B2 = B2; p.C = C;
@@ -596,7 +612,10 @@ hipError_t launch_gemm_nt_multi(const uint16_t* A, int64_t lda, const uint16_t* 
   p.M = M; p.N = N; p.K = K; p.K2 = ld2; p.alpha = 1.0f;
   p.E = nullptr; p.lde = 0;
   const int ntiles = plan_tiles(p);
-  hipLaunchKernelGGL(gemm_nt_multi_kernel, dim3((unsigned)ntiles), dim3(kThreads), 0, stream, p, slab);
+  if (M * lda * 2 >= four_gb)
+    hipLaunchKernelGGL(gemm_nt_multi_kernel<true>, dim3((unsigned)ntiles), dim3(kThreads), 0, stream, p, slab);
+  else
+    hipLaunchKernelGGL(gemm_nt_multi_kernel<false>, dim3((unsigned)ntiles), dim3(kThreads), 0, stream, p, slab);
   return hipGetLastError();
 }
 

@@ -261,13 +261,16 @@ hipError_t launch_gemm_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int
                           int64_t lde = 0);
 
 // The same with an adapter per row: A [M] rows in any order, grouped by rv;
-// C[m] = bf16(A[m] B^T + A2[m] B2_a^T) for rows of adapter a, A[m] B^T for the
-// others. A2 [M][ld2], its row zero_row is zeros; B2_a [N][ld2] lies at
-// b2_stride times slot[a] (or times a without slot). K a multiple of 64, ld2
-// too; all rows of A and A2 (the zero row too) below 4 GB, B and B2_a below 2 GB.
+// C[m] = bf16(A[m] B^T + A2[m] B2_g^T) for rows of segment k, A[m] B^T for rows
+// of none. Segments are packed `pack` to a group g = k / pack: A2 [M][ld2] holds
+// a row's values in its segment's columns and zeros in the others', B2_g [N][ld2]
+// the operands of the group's segments side by side, at g b2_stride (by_adapter,
+// with pack = 1: at a b2_stride). Row zero_row of A2 is zeros. K and ld2 are
+// multiples of 64; A2 (the zero row too) below 4 GB, B and B2_g below 2 GB.
 struct MultiSlab {
   RouteView rv;
-  const int32_t* slot;
+  int pack;
+  bool by_adapter;
   int64_t zero_row;
   int64_t b2_stride;
 };
@@ -280,10 +283,9 @@ constexpr int64_t kMultiMaxRows = (int64_t)1 << 22;   // 32-bit offsets of the r
 constexpr int kMultiMaxAdapters = 4096;
 struct MultiWorkspace {
   size_t perm_off, start_off, adapter_off, count_off, slot_off;   // the grouping (RouteView), segment of an adapter
-  size_t perm2_off, start2_off, adapter2_off, count2_off;         // the grouping of a part of the rows
-  size_t st_off;     // bf16 [M + 1][rp]: s T or s U, the last row zero
+  size_t st_off;     // bf16 [M + 1][rp]: s T or s U in the segment's columns, the last row zero
   size_t t_off;      // bf16 [M][r]: T, when the caller has none
-  size_t b2_off;     // bf16 per segment: L2^T [N][rp], or L1 [K][rp] with padded columns
+  size_t b2_off;     // bf16 per group of segments: L2^T [N][rp], or L1 [K][rp] with padded columns
   size_t wd_off;     // bf16 dequantised weight
   size_t dy_off;     // bf16 [M][N rounded up to 64]: dY, for a ragged N
   size_t part_off;   // fp32 partials

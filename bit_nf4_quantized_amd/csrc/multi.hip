@@ -41,8 +41,9 @@ __device__ __attribute__((aligned(16))) uint32_t g_multi_zero[4];  // zero-initi
 
 // ---- route ---------------------------------------------------------------------
 
-template <int WAVES>
-__device__ __forceinline__ int block_sum(int v, int* s) {   // s: WAVES ints
+constexpr int kRouteWaves = 4;
+
+__device__ __forceinline__ int block_sum(int v, int* s) {   // 256 threads; s: kRouteWaves ints
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
   __syncthreads();
@@ -50,7 +51,7 @@ __device__ __forceinline__ int block_sum(int v, int* s) {   // s: WAVES ints
   __syncthreads();
   int t = 0;
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) t += s[w];
+  for (int w = 0; w < kRouteWaves; ++w) t += s[w];
   return t;
 }
 
@@ -61,18 +62,17 @@ struct RouteArgs {
   int32_t* start;
   int32_t* adapter;
   int32_t* count;
-  int32_t* slot;          // optional: an adapter's segment
+  int32_t* slot;          // an adapter's segment, where it has rows
 };
 
 // Workgroup a < A: adapter a; workgroup A: the rows without one. Each reads
 // all ids (from the L2 after the first): it counts the rows and the distinct
 // adapters below its own, which are its place and its segment number, then
 // writes its rows in order.
-template <int WAVES>
 __device__ __forceinline__ void route_body(const RouteArgs& p, int a) {
-  constexpr int kThreads = 64 * WAVES;
+  constexpr int kThreads = 64 * kRouteWaves;
   __shared__ uint32_t seen[kMultiMaxAdapters / 32];
-  __shared__ int s_sum[WAVES], s_wave[WAVES];
+  __shared__ int s_sum[kRouteWaves], s_wave[kRouteWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int M = p.M, A = p.A;
   const int words = (A + 31) / 32;
@@ -89,11 +89,11 @@ __device__ __forceinline__ void route_body(const RouteArgs& p, int a) {
     }
     mine += a < A ? v == a : !has;
   }
-  below = block_sum<WAVES>(below, s_sum);
-  mine = block_sum<WAVES>(mine, s_sum);             // its barriers also publish `seen`
+  below = block_sum(below, s_sum);
+  mine = block_sum(mine, s_sum);             // its barriers also publish `seen`
   int rank = 0;
   for (int i = tid; i < words; i += kThreads) rank += __popc(seen[i]);
-  rank = block_sum<WAVES>(rank, s_sum);
+  rank = block_sum(rank, s_sum);
   if (tid == 0) {
     if (a == A) {
       p.count[0] = rank;
@@ -101,7 +101,7 @@ __device__ __forceinline__ void route_body(const RouteArgs& p, int a) {
     } else if (mine > 0) {
       p.adapter[rank] = a;
       p.start[rank] = below;
-      if (p.slot) p.slot[a] = rank;
+      p.slot[a] = rank;
     }
   }
   if (mine == 0) return;                            // uniform
@@ -116,7 +116,7 @@ __device__ __forceinline__ void route_body(const RouteArgs& p, int a) {
     __syncthreads();
     int before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
+    for (int w = 0; w < kRouteWaves; ++w) {
       const int c = s_wave[w];
       before += w < wave ? c : 0;
       all += c;
@@ -126,8 +126,6 @@ __device__ __forceinline__ void route_body(const RouteArgs& p, int a) {
   }
 }
 
-__global__ __launch_bounds__(1024) void route_kernel(RouteArgs p) { route_body<16>(p, (int)blockIdx.x); }
-
 // Workgroups 0 .. A group the rows; the others dequantise the weight as stored
 // (COLS = false) or transposed with rows of ldo (gx workgroups along k).
 template <bool COLS>
@@ -135,7 +133,7 @@ __global__ __launch_bounds__(256) void multi_prep_kernel(RouteArgs p, NF4View W,
                                                          uint16_t* __restrict__ out, int64_t ldo, int gx) {
   const int b = (int)blockIdx.x - (p.A + 1);
   if (b < 0) {
-    route_body<4>(p, (int)blockIdx.x);
+    route_body(p, (int)blockIdx.x);
   } else if constexpr (COLS) {
     dequant_cols_body(W, tab, out, ldo, b % gx, b / gx);
   } else {
@@ -145,19 +143,33 @@ __global__ __launch_bounds__(256) void multi_prep_kernel(RouteArgs p, NF4View W,
 
 // ---- adapter operands of the dense GEMM ---------------------------------------------
 
+// Segments of small ranks share the 64 columns of a stage: rank r takes `width`
+// columns (8, 16, 32, or whole stages), segment k the columns from
+// (k % pack) width of group k / pack.
+struct Packing {
+  int width, pack;
+};
+
+__host__ __device__ inline Packing packing_of(int r) {
+  const int w = r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : (r + 63) / 64 * 64;
+  return Packing{w, w < 64 ? 64 / w : 1};
+}
+
 struct LayArgs {
   const uint16_t* src;    // L2 [A][r][W] (transposed into [W][rp]) or L1 [A][W][r] (padded to [W][rp])
-  uint16_t* out;          // per segment [W][rp], columns >= r zero
+  uint16_t* out;          // per group [W][rp]; columns past a segment's r, and of segments that are none, zero
   int64_t W;
   int r, rp, blocks;      // blocks per segment
   bool transpose;
 };
 
-// L2 of segment k transposed: 64 columns n and 64 ranks per workgroup.
-__device__ __forceinline__ void lay_transposed(const LayArgs& p, const RouteView& rv, int k, int b) {
+// L2 of segment k transposed into its columns: 64 output rows n and 64 ranks
+// per workgroup (none: zeros).
+__device__ __forceinline__ void lay_transposed(const LayArgs& p, const RouteView& rv, int k, bool none, int b) {
   __shared__ uint16_t tile[64][64 + 2];
   const int64_t N = p.W;
-  const uint16_t* src = p.src + (int64_t)rv.adapter[k] * p.r * N;
+  const uint16_t* src = p.src + (none ? 0 : (int64_t)rv.adapter[k] * p.r * N);
+  const Packing pk = packing_of(p.r);
   const int tiles = p.rp / 64;
   const int64_t n0 = (int64_t)(b / tiles) * 64;
   const int j0 = (b % tiles) * 64;
@@ -166,34 +178,36 @@ __device__ __forceinline__ void lay_transposed(const LayArgs& p, const RouteView
   for (int u = 0; u < 2; ++u) {
     const int j = (t >> 3) + 32 * u, c = (t & 7) * 8;
     u32x4_t v = {0u, 0u, 0u, 0u};
-    if (j0 + j < p.r && n0 + c < N) v = *reinterpret_cast<const u32x4_t*>(src + (int64_t)(j0 + j) * N + n0 + c);
+    if (!none && j0 + j < p.r && n0 + c < N) v = *reinterpret_cast<const u32x4_t*>(src + (int64_t)(j0 + j) * N + n0 + c);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e) tile[c + e][j] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
   }
   __syncthreads();
+  uint16_t* out = p.out + (int64_t)(k / pk.pack) * N * p.rp + (k % pk.pack) * pk.width;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int n = (t >> 3) + 32 * u, c = (t & 7) * 8;
-    if (n0 + n >= N) continue;
+    if (n0 + n >= N || c >= pk.width) continue;
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = (uint32_t)tile[n][c + 2 * e] | ((uint32_t)tile[n][c + 2 * e + 1] << 16);
-    *reinterpret_cast<u32x4_t*>(p.out + ((int64_t)k * N + n0 + n) * p.rp + j0 + c) = u32x4_t{w[0], w[1], w[2], w[3]};
+    *reinterpret_cast<u32x4_t*>(out + (n0 + n) * p.rp + j0 + c) = u32x4_t{w[0], w[1], w[2], w[3]};
   }
 }
 
-// L1 of segment k with padded columns: 256 16-byte pieces per workgroup.
-__device__ __forceinline__ void lay_padded(const LayArgs& p, const RouteView& rv, int k, int b) {
-  const uint16_t* src = p.src + (int64_t)rv.adapter[k] * p.W * p.r;
+// L1 of segment k into its columns: 256 16-byte pieces per workgroup.
+__device__ __forceinline__ void lay_padded(const LayArgs& p, const RouteView& rv, int k, bool none, int b) {
+  const uint16_t* src = p.src + (none ? 0 : (int64_t)rv.adapter[k] * p.W * p.r);
+  const Packing pk = packing_of(p.r);
   const int64_t i = (int64_t)b * 256 + threadIdx.x;
-  const int per = p.rp / 8;
+  const int per = pk.width / 8;
   if (i >= p.W * per) return;
   const int64_t row = i / per;
   const int c = (int)(i - row * per) * 8;
   u32x4_t v = {0u, 0u, 0u, 0u};
-  if (c < p.r) v = *reinterpret_cast<const u32x4_t*>(src + row * p.r + c);
-  *reinterpret_cast<u32x4_t*>(p.out + ((int64_t)k * p.W + row) * p.rp + c) = v;
+  if (!none && c < p.r) v = *reinterpret_cast<const u32x4_t*>(src + row * p.r + c);
+  *reinterpret_cast<u32x4_t*>(p.out + ((int64_t)(k / pk.pack) * p.W + row) * p.rp + (k % pk.pack) * pk.width + c) = v;
 }
 
 // ---- pieces shared by the two adapter products -----------------------------------------
@@ -364,9 +378,9 @@ __global__ __launch_bounds__(kThreads) void multi_nt_kernel(NtArgs u, int zu, Nt
   else nt_body<true>(t, z - zu, lds);
 }
 
-// scaled [M + 1][rp] = bf16(s_a sum_z S[z]), its last row zero; plain [M][r] =
-// bf16(sum_z P[z]); either may be null. Partials [Z][M][rp]. Rows without an
-// adapter and columns >= r are zero.
+// scaled [M + 1][rp] = bf16(s_a sum_z S[z]) in the columns of the row's segment,
+// its other columns and the last row zero; plain [M][r] = bf16(sum_z P[z]).
+// Either may be null. Partials [Z][M][rp]. Rows without an adapter are zero.
 struct SumArgs {
   const float* S;
   const float* P;
@@ -376,6 +390,7 @@ struct SumArgs {
   const int32_t* ids;
   int A;
   const float* scale;
+  const int32_t* slot;
   uint16_t* scaled;
   uint16_t* plain;
 };
@@ -403,9 +418,10 @@ __device__ __forceinline__ u32x2_t pack4(const f32x4_t& v, float s) {
 __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs p, int blocks, LayArgs lay, RouteView rv) {
   if ((int)blockIdx.x >= blocks) {
     const int b = (int)blockIdx.x - blocks, k = b / lay.blocks;
-    if (k >= rv.count[0]) return;                   // uniform
-    if (lay.transpose) lay_transposed(lay, rv, k, b - k * lay.blocks);
-    else lay_padded(lay, rv, k, b - k * lay.blocks);
+    const int n = rv.count[0], pack = packing_of(lay.r).pack;
+    if (k >= (n + pack - 1) / pack * pack) return;  // uniform; the last group's missing segments are zeros
+    if (lay.transpose) lay_transposed(lay, rv, k, k >= n, b - k * lay.blocks);
+    else lay_padded(lay, rv, k, k >= n, b - k * lay.blocks);
     return;
   }
   const int w4 = p.rp / 4;
@@ -414,18 +430,18 @@ __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs p, int blocks, L
   const int j = (int)(i - m * w4) * 4;
   if (m > p.M) return;
   const int a = m < p.M ? p.ids[m] : -1;
-  const bool in = a >= 0 && a < p.A && j < p.r;
+  const bool has = a >= 0 && a < p.A;
   const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  const int64_t pitch = p.M * p.rp, at = m * p.rp + j;
-  f32x4_t v = zero;
+  const int64_t pitch = p.M * p.rp, at = m * p.rp;
   if (p.scaled) {
-    if (in) v = sum_slices(p.S + at, p.Zs, pitch);
-    *reinterpret_cast<u32x2_t*>(p.scaled + at) = pack4(v, in ? p.scale[a] : 0.0f);
+    const Packing pk = packing_of(p.r);
+    const int c = has ? j - p.slot[a] % pk.pack * pk.width : -1;   // 4 columns are inside a segment's, or all outside
+    const bool in = c >= 0 && c < p.r;
+    *reinterpret_cast<u32x2_t*>(p.scaled + at + j) =
+        pack4(in ? sum_slices(p.S + at + c, p.Zs, pitch) : zero, in ? p.scale[a] : 0.0f);
   }
-  if (p.plain && m < p.M && j < p.r) {
-    if (!p.scaled || p.P != p.S) v = in ? sum_slices(p.P + at, p.Zp, pitch) : zero;
-    *reinterpret_cast<u32x2_t*>(p.plain + m * p.r + j) = pack4(v, 1.0f);
-  }
+  if (p.plain && m < p.M && j < p.r)
+    *reinterpret_cast<u32x2_t*>(p.plain + m * p.r + j) = pack4(has ? sum_slices(p.P + at + j, p.Zp, pitch) : zero, 1.0f);
 }
 
 struct TnArgs {
@@ -436,6 +452,7 @@ struct TnArgs {
   const float* scale;     // factor per adapter, or null
   int64_t ldl, lds, W, slab;   // slab: floats per piece (all its rank tiles)
   int r, rows;            // rows per piece
+  bool packed;            // S holds a segment's ranks in its own columns
   bool out_bf16;
   RouteView rv;
 };
@@ -472,6 +489,8 @@ __device__ __forceinline__ void tn_body(const TnArgs& p, int bx, TnLds& lds) {
   if (pc.hi <= pc.lo) return;                       // uniform: no barrier was reached
   const int64_t c0 = (int64_t)bx * SM;
   const int j0 = (int)blockIdx.y * SJ;
+  const Packing pk = packing_of(p.r);
+  const uint16_t* S = p.S + (p.packed ? pc.k % pk.pack * pk.width : 0);
   const int ns = (pc.hi - pc.lo + SK - 1) / SK;
   const char* zero = reinterpret_cast<const char*>(g_multi_zero);
 
@@ -507,7 +526,7 @@ __device__ __forceinline__ void tn_body(const TnArgs& p, int bx, TnLds& lds) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = st * SK + 8 * (2 * wave + i) + (lane >> 3);
-      copy16(m < n && s_in[i] ? reinterpret_cast<const char*>(p.S + (int64_t)s_row[m < n ? m : 0] * p.lds + s_col[i]) : zero,
+      copy16(m < n && s_in[i] ? reinterpret_cast<const char*>(S + (int64_t)s_row[m < n ? m : 0] * p.lds + s_col[i]) : zero,
              buf + kTnLBytes + (2 * wave + i) * 1024);
     }
   };
@@ -685,12 +704,6 @@ int64_t tn_part_floats(int64_t M, int64_t K, int64_t N, int64_t W, int r, int A)
   return (M / rows + (A < M ? A : M)) * W * cdiv(r, SJ) * SJ;
 }
 
-// Per-lane offsets of the GEMM are 32-bit: rows per launch.
-int64_t gemm_rows(int64_t M, int64_t widest) {
-  const int64_t most = (((int64_t)1 << 31) - 1) / (widest * 2) / 256 * 256;
-  return M < most ? M : most;
-}
-
 }  // namespace
 
 MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, int A, bool bwd) {
@@ -714,13 +727,10 @@ MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, in
   L.adapter_off = take(segs * 4);
   L.count_off = take(4);
   L.slot_off = take(A * 4);
-  L.perm2_off = take(M * 4);        // the grouping of a part of the rows (more rows than one GEMM launch takes)
-  L.start2_off = take((segs + 1) * 4);
-  L.adapter2_off = take(segs * 4);
-  L.count2_off = take(4);
   L.st_off = take((M + 1) * rp * 2);   // s T or s U, and a row of zeros
   L.t_off = take(bwd ? M * r * 2 : 0);
-  const int64_t wide = bwd ? (r % 64 ? segs * K * rp * 2 : 0) : segs * N * rp * 2;
+  const int64_t groups = cdiv(segs, packing_of(r).pack);
+  const int64_t wide = bwd ? (r % 64 ? groups * K * rp * 2 : 0) : groups * N * rp * 2;
   L.b2_off = take(wide);
   L.wd_off = take(K * np * 2);
   L.dy_off = take(bwd && N % 64 ? M * np * 2 : 0);
@@ -738,17 +748,16 @@ MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, in
 
 namespace {
 
-RouteArgs route_args(const int32_t* ids, int64_t M, int A, char* ws, size_t perm, size_t start, size_t adapter,
-                     size_t count, int32_t* slot) {
+RouteArgs route_args(const int32_t* ids, int64_t M, int A, char* ws, const MultiWorkspace& L) {
   RouteArgs p;
   p.ids = ids;
   p.M = (int)M;
   p.A = A;
-  p.perm = reinterpret_cast<int32_t*>(ws + perm);
-  p.start = reinterpret_cast<int32_t*>(ws + start);
-  p.adapter = reinterpret_cast<int32_t*>(ws + adapter);
-  p.count = reinterpret_cast<int32_t*>(ws + count);
-  p.slot = slot;
+  p.perm = reinterpret_cast<int32_t*>(ws + L.perm_off);
+  p.start = reinterpret_cast<int32_t*>(ws + L.start_off);
+  p.adapter = reinterpret_cast<int32_t*>(ws + L.adapter_off);
+  p.count = reinterpret_cast<int32_t*>(ws + L.count_off);
+  p.slot = reinterpret_cast<int32_t*>(ws + L.slot_off);
   return p;
 }
 
@@ -775,40 +784,10 @@ hipError_t launch_nt(const NtArgs* u, int zu, const NtArgs* t, int zt, int64_t M
 
 hipError_t launch_sum(const SumArgs& s, const LayArgs& lay, int64_t segs, const RouteView& rv, hipStream_t stream) {
   const int64_t blocks = cdiv((s.M + 1) * s.rp / 4, 256);
+  if (lay.blocks > 0) segs = cdiv(segs, packing_of(lay.r).pack) * packing_of(lay.r).pack;   // whole groups
   hipLaunchKernelGGL(multi_sum_kernel, dim3((unsigned)(blocks + segs * lay.blocks)), dim3(256), 0, stream, s, (int)blocks,
                      lay, rv);
   return hipGetLastError();
-}
-
-// C = X B^T + S_a B2_a^T, in launches of as many rows as 32-bit offsets reach.
-// B2's operands lie b2_stride apart, by adapter or (slot) by segment.
-hipError_t gemm_by_adapter(const uint16_t* X, int64_t K, const uint16_t* B, int64_t M, int64_t N, const uint16_t* S,
-                           const uint16_t* B2, int64_t rp, int64_t b2_stride, const int32_t* slot, uint16_t* C,
-                           const int32_t* ids, int A, const RouteView& rv, char* ws, const MultiWorkspace& L,
-                           int timing, hipStream_t stream) {
-  const int64_t most = gemm_rows(M, K > rp ? K : rp);
-  if (most < 1) return hipErrorInvalidValue;
-  for (int64_t r0 = 0; r0 < M; r0 += most) {
-    const int64_t rows = M - r0 < most ? M - r0 : most;
-    MultiSlab slab;
-    slab.rv = rv;
-    if (rows < M) {
-      const RouteArgs p =
-          route_args(ids + r0, rows, A, ws, L.perm2_off, L.start2_off, L.adapter2_off, L.count2_off, nullptr);
-      hipLaunchKernelGGL(route_kernel, dim3((unsigned)(A + 1)), dim3(1024), 0, stream, p);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-      slab.rv = view_of(p);
-    }
-    slab.slot = slot;
-    slab.zero_row = M - r0;
-    slab.b2_stride = b2_stride;
-    const hipError_t e = timed(timing, stream, [&] {
-      return launch_gemm_nt_multi(X + r0 * K, K, B, K, rows, N, K, S + r0 * rp, B2, rp, slab, C + r0 * N, N, stream);
-    });
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
 }
 
 hipError_t zero_words(void* p, int64_t bytes, hipStream_t stream) {
@@ -817,14 +796,15 @@ hipError_t zero_words(void* p, int64_t bytes, hipStream_t stream) {
   return hipGetLastError();
 }
 
-TnArgs tn_args(const uint16_t* L, int64_t W, const uint16_t* S, int64_t lds, int r, int rows, const float* scale,
-               const RouteView& rv, float* part, void* out, bool out_bf16) {
+TnArgs tn_args(const uint16_t* L, int64_t W, const uint16_t* S, int64_t lds, bool packed, int r, int rows,
+               const float* scale, const RouteView& rv, float* part, void* out, bool out_bf16) {
   TnArgs a;
   a.L = L; a.S = S; a.out = out; a.part = part; a.scale = scale;
   a.ldl = W; a.lds = lds; a.W = W;
   a.slab = W * cdiv(r, SJ) * SJ;
   a.r = r;
   a.rows = rows;
+  a.packed = packed;
   a.out_bf16 = out_bf16;
   a.rv = rv;
   return a;
@@ -871,12 +851,11 @@ hipError_t multi_forward(const NF4View& W, const NF4Table& tab, const uint16_t* 
   uint16_t* sT = reinterpret_cast<uint16_t*>(base + L.st_off);
   uint16_t* l2t = reinterpret_cast<uint16_t*>(base + L.b2_off);
   uint16_t* wd = reinterpret_cast<uint16_t*>(base + L.wd_off);
-  int32_t* slot = reinterpret_cast<int32_t*>(base + L.slot_off);
   float* part = reinterpret_cast<float*>(base + L.part_off);
   if (multi_small_fits(M, K, N))
     return multi_forward_small(W, tab, X, M, MultiIds{ids, A, scale}, L1, L2, r, Y, T_out, part,
                                reinterpret_cast<float*>(base + L.tpart_off), stream);
-  const RouteArgs ra = route_args(ids, M, A, base, L.perm_off, L.start_off, L.adapter_off, L.count_off, slot);
+  const RouteArgs ra = route_args(ids, M, A, base, L);
   const RouteView rv = view_of(ra);
   hipLaunchKernelGGL(multi_prep_kernel<false>, dim3((unsigned)(A + 1 + dequant_rows_blocks(W))), dim3(256), 0, stream, ra,
                      W, tab, wd, (int64_t)0, 1);
@@ -886,11 +865,13 @@ hipError_t multi_forward(const NF4View& W, const NF4Table& tab, const uint16_t* 
   const NtArgs t = nt_args(X, K, L1, K * r, M, r, rp, sp, rv, part);
   e = launch_nt(nullptr, 0, &t, sp.Z, M, A, stream);
   if (e != hipSuccess) return e;
-  const SumArgs s{part, part, sp.Z, sp.Z, M, r, rp, ids, A, scale, sT, T_out};
+  const SumArgs s{part, part, sp.Z, sp.Z, M, r, rp, ids, A, scale, ra.slot, sT, T_out};
   const LayArgs lay{L2, l2t, N, r, rp, (int)(cdiv(N, 64) * (rp / 64)), true};
   e = launch_sum(s, lay, segs, rv, stream);
   if (e != hipSuccess) return e;
-  return gemm_by_adapter(X, K, wd, M, N, sT, l2t, rp, N * rp, slot, Y, ids, A, rv, base, L, kTimeFwdGemm, stream);
+  const MultiSlab slab{rv, packing_of(r).pack, false, M, N * rp};
+  return timed(kTimeFwdGemm, stream,
+               [&] { return launch_gemm_nt_multi(X, K, wd, K, M, N, K, sT, l2t, rp, slab, Y, N, stream); });
 }
 
 hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t* X, const uint16_t* dY, int64_t M,
@@ -907,9 +888,8 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
   const MultiWorkspace L = multi_workspace_layout(M, K, N, r, A, true);
   char* base = static_cast<char*>(ws);
   uint16_t* sU = reinterpret_cast<uint16_t*>(base + L.st_off);
-  int32_t* slot = reinterpret_cast<int32_t*>(base + L.slot_off);
   float* part = reinterpret_cast<float*>(base + L.part_off);
-  const RouteArgs ra = route_args(ids, M, A, base, L.perm_off, L.start_off, L.adapter_off, L.count_off, slot);
+  const RouteArgs ra = route_args(ids, M, A, base, L);
   const RouteView rv = view_of(ra);
   // the GEMM reduces over whole stages of 64: a ragged N is padded with zeros
   const int64_t np = cdiv(N, 64) * 64;
@@ -929,8 +909,8 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
   uint16_t* tbuf = T ? nullptr : reinterpret_cast<uint16_t*>(base + L.t_off);
   uint16_t* l1p = reinterpret_cast<uint16_t*>(base + L.b2_off);
   const bool padded = dX && rp != r;
-  const SumArgs s{upart, part, su.Z, st.Z, M, r, rp, ids, A, scale, sU, tbuf};
-  const LayArgs lay{L1, l1p, K, r, rp, (int)cdiv(K * rp / 8, 256), false};
+  const SumArgs s{upart, part, su.Z, st.Z, M, r, rp, ids, A, scale, ra.slot, sU, tbuf};
+  const LayArgs lay{L1, l1p, K, r, rp, (int)cdiv(K * packing_of(r).width / 8, 256), false};
   e = launch_sum(s, lay, padded ? segs : 0, rv, stream);
   if (e != hipSuccess) return e;
   if (!T) T = tbuf;
@@ -945,15 +925,17 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
       if (e != hipSuccess) return e;
       dYp = p;
     }
-    e = gemm_by_adapter(dYp, np, wdt, M, K, sU, padded ? l1p : L1, rp, K * rp, padded ? slot : nullptr, dX, ids, A, rv,
-                        base, L, kTimeDxGemm, stream);
+    const MultiSlab slab{rv, packing_of(r).pack, !padded, M, K * rp};
+    e = timed(kTimeDxGemm, stream, [&] {
+      return launch_gemm_nt_multi(dYp, np, wdt, np, M, K, np, sU, padded ? l1p : L1, rp, slab, dX, K, stream);
+    });
     if (e != hipSuccess) return e;
   }
 
   const int rows = tn_rows(M, K, N, r);
   float* part2 = part + tn_part_floats(M, K, N, K, r, A);
-  const TnArgs g1 = tn_args(X, K, sU, rp, r, rows, nullptr, rv, part, dL1, grad_bf16);
-  const TnArgs g2 = tn_args(dY, N, T, r, r, rows, scale, rv, part2, dL2, grad_bf16);
+  const TnArgs g1 = tn_args(X, K, sU, rp, true, r, rows, nullptr, rv, part, dL1, grad_bf16);
+  const TnArgs g2 = tn_args(dY, N, T, r, false, r, rows, scale, rv, part2, dL2, grad_bf16);
   const int64_t pieces = M / rows + segs;
   hipLaunchKernelGGL(multi_tn_kernel, dim3((unsigned)(cdiv(K, SM) + cdiv(N, SM)), (unsigned)cdiv(r, SJ), (unsigned)pieces),
                      dim3(kThreads), 0, stream, g1, (int)cdiv(K, SM), g2);

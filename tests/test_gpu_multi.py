@@ -180,6 +180,9 @@ FWD = [
     (513, 256, 512, 64, 2, "few"),
     (600, 256, 264, 16, 4, "none"),
     (1030, 256, 4160, 16, 3, "one"),
+    (320, 256, 264, 8, 45, "rows"),        # eight segments to a group, several groups to a tile
+    (300, 256, 136, 16, 3, "rows"),        # a group that is not full
+    (260, 128, 264, 24, 33, "rows"),
 ]
 
 
@@ -202,6 +205,9 @@ BWD = [
     (2500, 256, 512, 64, 2, "few"),        # a segment of several pieces, and adapters without rows
     (4200, 320, 256, 16, 3, "one"),
     (1000, 512, 520, 64, 300, "rows"),
+    (320, 256, 264, 8, 45, "rows"),
+    (300, 192, 136, 24, 7, "rows"),
+    (260, 128, 192, 32, 33, "few"),
 ]
 
 
@@ -301,19 +307,19 @@ def test_stream_and_graph(api, M):
 
 
 def test_rows_beyond_32_bit_offsets(api):
-    """More rows than one launch of the dense GEMM addresses (2 GB): parts, each grouped by itself."""
+    """Rows that span more than 4 GB: the dense GEMM's variant with 64-bit addresses."""
     import torch
 
-    M, K, N, r, A = 270000, 4096, 64, 8, 3
+    M, K, N, r, A = 540000, 4096, 64, 8, 3
     say(f"multi M={M} K={K}: {M * K * 2 / 2 ** 30:.1f} GiB of rows")
     c = Case(api, 300, K, N, r, A, "rows")
     X = c.d["X"].repeat(M // 300, 1)
     ids = c.d["ids"].repeat(M // 300)
     Y = api.qlora_linear_multi_fwd(c.q, X, ids, c.d["L1"], c.d["L2"], c.d["scale"])[0]
     blocks = Y.view(M // 300, 300, N)
-    assert torch.equal(blocks, blocks[:1].expand(M // 300, 300, N))     # the same 300 rows in every part
+    assert torch.equal(blocks, blocks[:1].expand(M // 300, 300, N))     # the same 300 rows over and over
     Yr, Tr = multi.multi_fwd(c.X, c.W, c.ids, c.L1, c.L2, c.scale)
-    within("rows beyond 2 GB", "Y", api.to_host_bits(blocks[0]), Yr, Bounds(c, Tr).Y)
+    within("rows beyond 4 GB", "Y", api.to_host_bits(blocks[0]), Yr, Bounds(c, Tr).Y)
 
 
 def test_refusals(api):

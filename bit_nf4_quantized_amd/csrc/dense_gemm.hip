@@ -107,6 +107,8 @@ struct DenseArgs {
   int tail_split;   // 2 or 4
   const float* E;   // ADD: fp32 addend [M][N] (row stride lde), C = bf16(alpha acc + E)
   int64_t lde;
+  float* part;      // SPLIT: fp32 partials [slices][M][N] of main stages z per_slice .. (the slab with the last)
+  int per_slice;
 };
 
 // One stage of one operand: rows [row0, row0+256) x columns [k0, k0+64).
@@ -180,9 +182,19 @@ __device__ __forceinline__ int lds_off(int row, int chunk) { return row * TK + (
 // rows are rows m0 .. of the grouped order, and the slab has the K2 columns of
 // every group of segments that meets them, with zeros (slab.zero_row) in the
 // place of the other groups' rows. WIDE: A's rows span more than 32-bit offsets.
-template <bool ADD, int TMX, bool MULTI, bool WIDE>
-__device__ __forceinline__ void gemm_tile(const DenseArgs& p, const MultiSlab& slab, int64_t m0, int64_t n0,
-                                          uint16_t* smem) {
+// SPLIT: slice z of the main stages only, into fp32 partials.
+template <bool ADD, int TMX, bool MULTI, bool WIDE, bool SPLIT = false>
+__device__ __forceinline__ void gemm_tile(const DenseArgs& p_all, const MultiSlab& slab, int64_t m0, int64_t n0,
+                                          uint16_t* smem, int z = 0) {
+  DenseArgs p = p_all;
+  if constexpr (SPLIT) {
+    const int64_t k0 = (int64_t)z * p.per_slice * TK, len = (int64_t)p.per_slice * TK;
+    const bool last = k0 + len >= p.K;
+    p.A += k0;
+    p.B += k0;
+    p.K = last ? p.K - k0 : len;
+    if (!last) p.K2 = 0;
+  }
   using S = TileShape<TMX>;
   constexpr int WTM = S::kWtm, MI = S::kMi;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -193,7 +205,7 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, const MultiSlab& s
   if constexpr (MULTI) {
     const RouteRange rg = route_range(slab.rv, (int)m0, (int)m0 + TMX);
     group0 = rg.lo / slab.pack;
-    nslab = rg.hi > rg.lo ? ((rg.hi - 1) / slab.pack - group0 + 1) * per_group : 0;
+    nslab = rg.hi > rg.lo ? ((rg.hi - 1) / slab.pack - group0 + 1) * per_group : 0;   // per_group 0: another slice's
     segs = rg.hi;
   }
   const int nk = nmain + nslab;
@@ -384,8 +396,8 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, const MultiSlab& s
   if (st + 1 < nk) stage(st++, false, true, true);
   if (st < nk) stage(st, false, false, true);
 
-  if constexpr (ADD) {
-    // Epilogue with an fp32 addend: each wave stages a quarter of its 128 x 64
+  if constexpr (ADD || SPLIT) {
+    // Epilogue in fp32 (with an addend, or as partials): each wave stages a quarter of its 128 x 64
     // sub-tile (32 rows, one accumulator row-block) as fp32 in its own padded
     // LDS slice; then each lane takes 8 consecutive columns of a row, adds the
     // matching 32 bytes of E and stores 16 bytes of bf16.
@@ -410,6 +422,14 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p, const MultiSlab& s
         const f32x4_t a1 = *reinterpret_cast<const f32x4_t*>(ef + r * kAddStride + cc + 4);
         const int64_t row = row_base + i * 32 + r, col = col_base + cc;
         const bool in = row < p.M && col < p.N;
+        if constexpr (SPLIT) {
+          float* out = p.part + ((int64_t)z * p.M + (in ? (int64_t)perm[row] : 0)) * p.N + col;
+          if (in) {
+            *reinterpret_cast<f32x4_t*>(out) = a0;
+            *reinterpret_cast<f32x4_t*>(out + 4) = a1;
+          }
+          continue;
+        }
         const float* ep = p.E + (in ? row * p.lde + col : 0);
         const f32x4_t e0 = *reinterpret_cast<const f32x4_t*>(ep);
         const f32x4_t e1 = *reinterpret_cast<const f32x4_t*>(ep + 4);
@@ -503,6 +523,40 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_kernel(DenseArgs p) {
   gemm_nt_body<ADD, false, false>(p, MultiSlab{});
 }
 
+// Half-height tiles, each in slices of the reduction. Workgroup b runs on XCD
+// b % 8: each XCD gets a contiguous range of (slice, column, row) numbers, so
+// that the row tiles which share B's columns read them through one L2.
+__global__ __launch_bounds__(kThreads, 1) void gemm_nt_multi_split_kernel(DenseArgs p, MultiSlab slab) {
+  __shared__ __attribute__((aligned(1024))) uint16_t smem[5 * kStageElems];
+  const int tiles_m = (int)((p.M + TM / 2 - 1) / (TM / 2)), tiles = tiles_m * p.tiles_n;
+  const int bid = (int)blockIdx.x, n = (int)gridDim.x, xcd = bid % 8, q = n / 8, rem = n % 8;
+  const int w = xcd * q + (xcd < rem ? xcd : rem) + bid / 8;
+  const int z = w / tiles, t = w - z * tiles;
+  gemm_tile<false, TM / 2, true, false, true>(p, slab, (int64_t)(t % tiles_m) * (TM / 2), (int64_t)(t / tiles_m) * TN, smem, z);
+}
+
+// C = bf16(sum of the slices' partials, in order); 8 values per thread.
+__global__ __launch_bounds__(256) void gemm_split_sum_kernel(const float* __restrict__ part, int S, int64_t values,
+                                                             uint16_t* __restrict__ C) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= values) return;
+  f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
+  int z = 0;
+  for (; z + 2 <= S; z += 2) {
+    const float* q = part + (int64_t)z * values + i;
+    const f32x4_t a0 = *reinterpret_cast<const f32x4_t*>(q), b0 = *reinterpret_cast<const f32x4_t*>(q + 4);
+    const f32x4_t a1 = *reinterpret_cast<const f32x4_t*>(q + values), b1 = *reinterpret_cast<const f32x4_t*>(q + values + 4);
+    a += a0; b += b0;
+    a += a1; b += b1;
+  }
+  if (z < S) {
+    a += *reinterpret_cast<const f32x4_t*>(part + (int64_t)z * values + i);
+    b += *reinterpret_cast<const f32x4_t*>(part + (int64_t)z * values + i + 4);
+  }
+  *reinterpret_cast<u32x4_t*>(C + i) =
+      u32x4_t{pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w)};
+}
+
 template <bool WIDE>
 __global__ __launch_bounds__(kThreads, 1) void gemm_nt_multi_kernel(DenseArgs p, MultiSlab slab) {
   gemm_nt_body<false, true, WIDE>(p, slab);
@@ -569,6 +623,7 @@ hipError_t launch_gemm_nt_rows(const uint16_t* A, int64_t lda, const uint16_t* B
   p.lda = lda; p.ldb = ldb; p.ld2 = ld2; p.ldc = ldc;
   p.M = M; p.N = N; p.K = K; p.K2 = K2; p.alpha = alpha;
   p.E = E; p.lde = lde;
+  p.part = nullptr; p.per_slice = 0;
   const int ntiles = plan_tiles(p);
   if (E)
     hipLaunchKernelGGL(gemm_nt_kernel<true>, dim3((unsigned)ntiles), dim3(kThreads), 0, stream, p);
@@ -600,17 +655,64 @@ hipError_t launch_gemm_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int
   return hipSuccess;
 }
 
+namespace {
+
+// Reduction slices for a product whose full tiles leave more than half of the
+// CUs idle: half-height tiles in as many slices as fill the device once, of at
+// least 16 stages, at most 8. Their partials cost S M N 8 bytes of traffic, so
+// two or three slices are taken only where that is less than the weight's 2 N K.
+// Whole forward call, split against quarter-height tiles without (rank 16, us):
+// 150 x 4096 -> 4096 46 / 60, 391 rows 54 / 59; 256 x 4096 -> 11008 70 / 89;
+// 300 x 11008 -> 4096 80 / 117; and where the rule keeps one slice, 700 x 4096 ->
+// 4096 62 / 58, 1000 rows 69 / 65.
+struct GemmSplit {
+  int S, per;
+};
+
+GemmSplit gemm_split(int64_t M, int64_t N, int64_t K) {
+  const int64_t cus = device_cu_count(), nk = K / TK;
+  const int64_t full = ((M + TM - 1) / TM) * ((N + TN - 1) / TN);
+  if (full < 1 || 2 * full > cus) return GemmSplit{1, (int)nk};
+  const int64_t half = ((M + TM / 2 - 1) / (TM / 2)) * ((N + TN - 1) / TN);
+  int64_t S = cus / half;
+  if (S > nk / 16) S = nk / 16;
+  if (S > 8) S = 8;
+  if (S < 2 || (S < 4 && 8 * S * M * N > 2 * N * K)) return GemmSplit{1, (int)nk};
+  const int64_t per = (nk + S - 1) / S;
+  return GemmSplit{(int)((nk + per - 1) / per), (int)per};
+}
+
+}  // namespace
+
+size_t gemm_multi_partial_bytes(int64_t M, int64_t N, int64_t K) {
+  const GemmSplit sp = gemm_split(M, N, K);
+  return sp.S > 1 ? (size_t)sp.S * M * N * 4 : 0;
+}
+
 hipError_t launch_gemm_nt_multi(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N,
                                 int64_t K, const uint16_t* A2, const uint16_t* B2, int64_t ld2, const MultiSlab& slab,
-                                uint16_t* C, int64_t ldc, hipStream_t stream) {
+                                uint16_t* C, float* part, hipStream_t stream) {
   const int64_t two_gb = (int64_t)1 << 31, four_gb = (int64_t)1 << 32;
   if (N * ldb * 2 >= two_gb || N * ld2 * 2 >= two_gb || (slab.zero_row + 1) * ld2 * 2 >= four_gb)
     return hipErrorInvalidValue;
   DenseArgs p;
   p.A = A; p.B = B; p.A2 = A2; p.B2 = B2; p.C = C;
-  p.lda = lda; p.ldb = ldb; p.ld2 = ld2; p.ldc = ldc;
+  p.lda = lda; p.ldb = ldb; p.ld2 = ld2; p.ldc = N;
   p.M = M; p.N = N; p.K = K; p.K2 = ld2; p.alpha = 1.0f;
   p.E = nullptr; p.lde = 0;
+  const GemmSplit sp = gemm_split(M, N, K);
+  p.part = part;
+  p.per_slice = sp.per;
+  if (sp.S > 1 && M * lda * 2 < four_gb) {
+    p.tiles_n = (int)((N + TN - 1) / TN);
+    const int64_t tiles = ((M + TM / 2 - 1) / (TM / 2)) * p.tiles_n;
+    hipLaunchKernelGGL(gemm_nt_multi_split_kernel, dim3((unsigned)(tiles * sp.S)), dim3(kThreads), 0, stream, p, slab);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(gemm_split_sum_kernel, dim3((unsigned)((M * N / 8 + 255) / 256)), dim3(256), 0, stream, part, sp.S,
+                       M * N, C);
+    return hipGetLastError();
+  }
   const int ntiles = plan_tiles(p);
   if (M * lda * 2 >= four_gb)
     hipLaunchKernelGGL(gemm_nt_multi_kernel<true>, dim3((unsigned)ntiles), dim3(kThreads), 0, stream, p, slab);

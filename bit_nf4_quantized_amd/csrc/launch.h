@@ -266,7 +266,8 @@ hipError_t launch_gemm_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int
 // a row's values in its segment's columns and zeros in the others', B2_g [N][ld2]
 // the operands of the group's segments side by side, at g b2_stride (by_adapter,
 // with pack = 1: at a b2_stride). Row zero_row of A2 is zeros. K and ld2 are
-// multiples of 64; A2 (the zero row too) below 4 GB, B and B2_g below 2 GB.
+// multiples of 64; A2 (the zero row too) below 4 GB, B and B2_g below 2 GB. C is
+// dense [M][N].
 struct MultiSlab {
   RouteView rv;
   int pack;
@@ -276,7 +277,8 @@ struct MultiSlab {
 };
 hipError_t launch_gemm_nt_multi(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N,
                                 int64_t K, const uint16_t* A2, const uint16_t* B2, int64_t ld2, const MultiSlab& slab,
-                                uint16_t* C, int64_t ldc, hipStream_t stream);
+                                uint16_t* C, float* part, hipStream_t stream);
+size_t gemm_multi_partial_bytes(int64_t M, int64_t N, int64_t K);   // of part, in launch_gemm_nt_multi
 
 // The linear with an adapter per row (multi.hip, multi_small.hip).
 constexpr int64_t kMultiMaxRows = (int64_t)1 << 22;   // 32-bit offsets of the rows' [M][256] rank buffers

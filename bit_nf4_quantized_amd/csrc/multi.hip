@@ -735,12 +735,14 @@ MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, in
   L.wd_off = take(K * np * 2);
   L.dy_off = take(bwd && N % 64 ? M * np * 2 : 0);
   const NtSplit t = nt_split(M, K, A, (int)rp), u = nt_split(M, N, A, (int)rp);
-  int64_t part = t.Z * M * rp;                       // T's, then U's; later dL1's, then dL2's
+  int64_t part = t.Z * M * rp;                       // T's, then U's; then the GEMM's; then dL1's and dL2's
   if (bwd) {
     part += u.Z * M * rp;
     const int64_t grads = tn_part_floats(M, K, N, K, r, A) + tn_part_floats(M, K, N, N, r, A);
     if (grads > part) part = grads;
   }
+  const size_t gemm = bwd ? gemm_multi_partial_bytes(M, K, np) : gemm_multi_partial_bytes(M, N, K);
+  if ((int64_t)gemm > part * 4) part = (int64_t)gemm / 4;
   L.part_off = take(part * 4);
   L.total = off;
   return L;
@@ -871,7 +873,7 @@ hipError_t multi_forward(const NF4View& W, const NF4Table& tab, const uint16_t* 
   if (e != hipSuccess) return e;
   const MultiSlab slab{rv, packing_of(r).pack, false, M, N * rp};
   return timed(kTimeFwdGemm, stream,
-               [&] { return launch_gemm_nt_multi(X, K, wd, K, M, N, K, sT, l2t, rp, slab, Y, N, stream); });
+               [&] { return launch_gemm_nt_multi(X, K, wd, K, M, N, K, sT, l2t, rp, slab, Y, part, stream); });
 }
 
 hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t* X, const uint16_t* dY, int64_t M,
@@ -927,7 +929,7 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
     }
     const MultiSlab slab{rv, packing_of(r).pack, !padded, M, K * rp};
     e = timed(kTimeDxGemm, stream, [&] {
-      return launch_gemm_nt_multi(dYp, np, wdt, np, M, K, np, sU, padded ? l1p : L1, rp, slab, dX, K, stream);
+      return launch_gemm_nt_multi(dYp, np, wdt, np, M, K, np, sU, padded ? l1p : L1, rp, slab, dX, part, stream);
     });
     if (e != hipSuccess) return e;
   }

@@ -30,6 +30,8 @@ SIZES = {
     "edges": [0, 1, 3, 4, 255, 256, 257, 0, 4095, 4096, 4097, 12289],
     "many": [17 * k % 700 + 1 for k in range(150)],
     "empties": [0] * 70 + [5],
+    "launches": [17 * k % 700 + 1 for k in range(300)],                          # more than any launch's table
+    "gaps": [0] * 70 + [5, 4096, 0] + [0] * 300 + [8192, 3, 0],
 }
 
 

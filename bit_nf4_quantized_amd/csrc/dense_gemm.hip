@@ -535,27 +535,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_multi_split_kernel(DenseA
   gemm_tile<false, TM / 2, true, false, true>(p, slab, (int64_t)(t % tiles_m) * (TM / 2), (int64_t)(t / tiles_m) * TN, smem, z);
 }
 
-// C = bf16(sum of the slices' partials, in order); 8 values per thread.
-__global__ __launch_bounds__(256) void gemm_split_sum_kernel(const float* __restrict__ part, int S, int64_t values,
-                                                             uint16_t* __restrict__ C) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (i >= values) return;
-  f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
-  int z = 0;
-  for (; z + 2 <= S; z += 2) {
-    const float* q = part + (int64_t)z * values + i;
-    const f32x4_t a0 = *reinterpret_cast<const f32x4_t*>(q), b0 = *reinterpret_cast<const f32x4_t*>(q + 4);
-    const f32x4_t a1 = *reinterpret_cast<const f32x4_t*>(q + values), b1 = *reinterpret_cast<const f32x4_t*>(q + values + 4);
-    a += a0; b += b0;
-    a += a1; b += b1;
-  }
-  if (z < S) {
-    a += *reinterpret_cast<const f32x4_t*>(part + (int64_t)z * values + i);
-    b += *reinterpret_cast<const f32x4_t*>(part + (int64_t)z * values + i + 4);
-  }
-  *reinterpret_cast<u32x4_t*>(C + i) =
-      u32x4_t{pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w)};
-}
+__global__ __launch_bounds__(256) void gemm_split_sum_kernel(SplitSum s) { split_sum_body(s, (int64_t)blockIdx.x * 256 + threadIdx.x); }
 
 template <bool WIDE>
 __global__ __launch_bounds__(kThreads, 1) void gemm_nt_multi_kernel(DenseArgs p, MultiSlab slab) {
@@ -691,7 +671,7 @@ size_t gemm_multi_partial_bytes(int64_t M, int64_t N, int64_t K) {
 
 hipError_t launch_gemm_nt_multi(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N,
                                 int64_t K, const uint16_t* A2, const uint16_t* B2, int64_t ld2, const MultiSlab& slab,
-                                uint16_t* C, float* part, hipStream_t stream) {
+                                uint16_t* C, float* part, SplitSum* later, hipStream_t stream) {
   const int64_t two_gb = (int64_t)1 << 31, four_gb = (int64_t)1 << 32;
   if (N * ldb * 2 >= two_gb || N * ld2 * 2 >= two_gb || (slab.zero_row + 1) * ld2 * 2 >= four_gb)
     return hipErrorInvalidValue;
@@ -709,8 +689,12 @@ hipError_t launch_gemm_nt_multi(const uint16_t* A, int64_t lda, const uint16_t* 
     hipLaunchKernelGGL(gemm_nt_multi_split_kernel, dim3((unsigned)(tiles * sp.S)), dim3(kThreads), 0, stream, p, slab);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(gemm_split_sum_kernel, dim3((unsigned)((M * N / 8 + 255) / 256)), dim3(256), 0, stream, part, sp.S,
-                       M * N, C);
+    const SplitSum sum{part, C, M * N, sp.S};
+    if (later) {
+      *later = sum;
+      return hipSuccess;
+    }
+    hipLaunchKernelGGL(gemm_split_sum_kernel, dim3((unsigned)((M * N / 8 + 255) / 256)), dim3(256), 0, stream, sum);
     return hipGetLastError();
   }
   const int ntiles = plan_tiles(p);

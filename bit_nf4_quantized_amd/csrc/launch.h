@@ -275,9 +275,11 @@ struct MultiSlab {
   int64_t zero_row;
   int64_t b2_stride;
 };
+// `later`: what is left of a product that is cut into reduction slices (S > 1)
+// goes there for the caller to add beside other work; NULL: added here.
 hipError_t launch_gemm_nt_multi(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N,
                                 int64_t K, const uint16_t* A2, const uint16_t* B2, int64_t ld2, const MultiSlab& slab,
-                                uint16_t* C, float* part, hipStream_t stream);
+                                uint16_t* C, float* part, SplitSum* later, hipStream_t stream);
 size_t gemm_multi_partial_bytes(int64_t M, int64_t N, int64_t K);   // of part, in launch_gemm_nt_multi
 
 // The linear with an adapter per row (multi.hip, multi_small.hip).
@@ -292,6 +294,7 @@ struct MultiWorkspace {
   size_t dy_off;     // bf16 [M][N rounded up to 64]: dY, for a ragged N
   size_t part_off;   // fp32 partials
   size_t tpart_off;  // fp32 partials of T (M <= 128)
+  size_t gpart_off;  // fp32 partials of a split dX
   size_t total;
 };
 MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, int A, bool bwd);

@@ -60,4 +60,33 @@ __device__ __forceinline__ RouteRange route_range(const RouteView& r, int m0, in
   return RouteRange{__builtin_amdgcn_readfirstlane(before), __builtin_amdgcn_readfirstlane(begun)};
 }
 
+// A product cut into S reduction slices: C = bf16(part[0] + part[1] + ...).
+struct SplitSum {
+  const float* part;   // [S][values]
+  uint16_t* C;
+  int64_t values;      // a multiple of 8
+  int S;
+};
+
+// Its values 8 i .. 8 i + 8.
+__device__ __forceinline__ void split_sum_body(const SplitSum& s, int64_t i) {
+  i *= 8;
+  if (i >= s.values) return;
+  f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
+  int z = 0;
+  for (; z + 2 <= s.S; z += 2) {
+    const float* q = s.part + (int64_t)z * s.values + i;
+    const f32x4_t a0 = *reinterpret_cast<const f32x4_t*>(q), b0 = *reinterpret_cast<const f32x4_t*>(q + 4);
+    const f32x4_t a1 = *reinterpret_cast<const f32x4_t*>(q + s.values), b1 = *reinterpret_cast<const f32x4_t*>(q + s.values + 4);
+    a += a0; b += b0;
+    a += a1; b += b1;
+  }
+  if (z < s.S) {
+    a += *reinterpret_cast<const f32x4_t*>(s.part + (int64_t)z * s.values + i);
+    b += *reinterpret_cast<const f32x4_t*>(s.part + (int64_t)z * s.values + i + 4);
+  }
+  *reinterpret_cast<u32x4_t*>(s.C + i) =
+      u32x4_t{pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w)};
+}
+
 }  // namespace qlora

@@ -593,10 +593,18 @@ __device__ __forceinline__ void tn_body(const TnArgs& p, int bx, TnLds& lds) {
     }
 }
 
-// Column tiles below x1: dL1 (arguments g1); the others: dL2 (g2).
-__global__ __launch_bounds__(kThreads) void multi_tn_kernel(TnArgs g1, int x1, TnArgs g2) {
+// Planes below z1: the pieces; column tiles below x1: dL1 (arguments g1), the
+// others: dL2 (g2). The planes from z1 on add the slices of a split dX: alone
+// that was a launch of 5.8 us after the GEMM (391 rows of 4096).
+__global__ __launch_bounds__(kThreads) void multi_tn_kernel(TnArgs g1, int x1, TnArgs g2, int z1, SplitSum sum) {
   __shared__ TnLds lds;
   const int x = (int)blockIdx.x;
+  if ((int)blockIdx.z >= z1) {
+    const int64_t plane = (int64_t)gridDim.x * gridDim.y;
+    const int64_t b = ((int64_t)blockIdx.z - z1) * plane + (int64_t)blockIdx.y * gridDim.x + x;
+    split_sum_body(sum, b * kThreads + threadIdx.x);
+    return;
+  }
   if (x < x1) tn_body<true>(g1, x, lds);
   else tn_body<false>(g2, x - x1, lds);
 }
@@ -735,15 +743,18 @@ MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, in
   L.wd_off = take(K * np * 2);
   L.dy_off = take(bwd && N % 64 ? M * np * 2 : 0);
   const NtSplit t = nt_split(M, K, A, (int)rp), u = nt_split(M, N, A, (int)rp);
-  int64_t part = t.Z * M * rp;                       // T's, then U's; then the GEMM's; then dL1's and dL2's
+  int64_t part = t.Z * M * rp;                       // T's, then U's; then dL1's and dL2's, or the forward GEMM's
   if (bwd) {
     part += u.Z * M * rp;
     const int64_t grads = tn_part_floats(M, K, N, K, r, A) + tn_part_floats(M, K, N, N, r, A);
     if (grads > part) part = grads;
   }
-  const size_t gemm = bwd ? gemm_multi_partial_bytes(M, K, np) : gemm_multi_partial_bytes(M, N, K);
-  if ((int64_t)gemm > part * 4) part = (int64_t)gemm / 4;
+  if (!bwd) {
+    const int64_t gemm = (int64_t)gemm_multi_partial_bytes(M, N, K) / 4;
+    if (gemm > part) part = gemm;
+  }
   L.part_off = take(part * 4);
+  L.gpart_off = take(bwd ? (int64_t)gemm_multi_partial_bytes(M, K, np) : 0);   // dX's, added while dL1 and dL2 are computed
   L.total = off;
   return L;
 }
@@ -873,7 +884,7 @@ hipError_t multi_forward(const NF4View& W, const NF4Table& tab, const uint16_t* 
   if (e != hipSuccess) return e;
   const MultiSlab slab{rv, packing_of(r).pack, false, M, N * rp};
   return timed(kTimeFwdGemm, stream,
-               [&] { return launch_gemm_nt_multi(X, K, wd, K, M, N, K, sT, l2t, rp, slab, Y, part, stream); });
+               [&] { return launch_gemm_nt_multi(X, K, wd, K, M, N, K, sT, l2t, rp, slab, Y, part, nullptr, stream); });
 }
 
 hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t* X, const uint16_t* dY, int64_t M,
@@ -917,7 +928,9 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
   if (e != hipSuccess) return e;
   if (!T) T = tbuf;
 
+  SplitSum sum{nullptr, nullptr, 0, 0};
   if (dX) {
+    float* gpart = reinterpret_cast<float*>(base + L.gpart_off);
     const uint16_t* dYp = dY;
     if (np != N) {
       uint16_t* p = reinterpret_cast<uint16_t*>(base + L.dy_off);
@@ -929,7 +942,7 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
     }
     const MultiSlab slab{rv, packing_of(r).pack, !padded, M, K * rp};
     e = timed(kTimeDxGemm, stream, [&] {
-      return launch_gemm_nt_multi(dYp, np, wdt, np, M, K, np, sU, padded ? l1p : L1, rp, slab, dX, part, stream);
+      return launch_gemm_nt_multi(dYp, np, wdt, np, M, K, np, sU, padded ? l1p : L1, rp, slab, dX, gpart, &sum, stream);
     });
     if (e != hipSuccess) return e;
   }
@@ -938,9 +951,10 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
   float* part2 = part + tn_part_floats(M, K, N, K, r, A);
   const TnArgs g1 = tn_args(X, K, sU, rp, true, r, rows, nullptr, rv, part, dL1, grad_bf16);
   const TnArgs g2 = tn_args(dY, N, T, r, false, r, rows, scale, rv, part2, dL2, grad_bf16);
-  const int64_t pieces = M / rows + segs;
-  hipLaunchKernelGGL(multi_tn_kernel, dim3((unsigned)(cdiv(K, SM) + cdiv(N, SM)), (unsigned)cdiv(r, SJ), (unsigned)pieces),
-                     dim3(kThreads), 0, stream, g1, (int)cdiv(K, SM), g2);
+  const int64_t pieces = M / rows + segs, tiles = cdiv(K, SM) + cdiv(N, SM);
+  const int64_t planes = cdiv(sum.values / 8, kThreads * tiles * cdiv(r, SJ));
+  hipLaunchKernelGGL(multi_tn_kernel, dim3((unsigned)tiles, (unsigned)cdiv(r, SJ), (unsigned)(pieces + planes)),
+                     dim3(kThreads), 0, stream, g1, (int)cdiv(K, SM), g2, (int)pieces, sum);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int b1 = finish_blocks(K * r), b2 = finish_blocks(N * r);

@@ -200,16 +200,20 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// One workgroup per pair: waves 0 and 1 add the preferred sequence's positions
-// in float64 (lane l of wave w: positions 64 w + l, + 128, ...), waves 2 and 3
-// the other's; then the lanes, then the waves.
-__global__ __launch_bounds__(256) void pair_loss_kernel(PrefArgs p) {
-  __shared__ double part[4];
+// One workgroup per pair: half of the waves add the preferred sequence's
+// positions in float64 (lane l of wave w: positions 64 w + l, + 512, ...), half
+// the other's; then the lanes, then the waves. Latency-bound: 16 waves so that
+// a sequence of some thousand positions is one or two round trips.
+constexpr int kPairWaves = 16;
+
+__global__ __launch_bounds__(64 * kPairWaves) void pair_loss_kernel(PrefArgs p) {
+  constexpr int kHalf = kPairWaves / 2;
+  __shared__ double part[kPairWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, P = p.S / 2, q = (int)blockIdx.x;
-  const int64_t base = (int64_t)(q + (wave >> 1) * P) * p.T;
+  const int64_t base = (int64_t)(q + (wave / kHalf) * P) * p.T;
   double v = 0.0;
 #pragma unroll 4
-  for (int i = 64 * (wave & 1) + lane; i < p.T; i += 128) {
+  for (int i = 64 * (wave % kHalf) + lane; i < p.T; i += 64 * kHalf) {
     const int64_t y = p.labels[base + i];
     const double d = (double)p.lp[base + i] - (double)p.ref[base + i];
     v += y >= 0 && y < p.V ? d : 0.0;
@@ -218,7 +222,12 @@ __global__ __launch_bounds__(256) void pair_loss_kernel(PrefArgs p) {
   if (lane == 0) part[wave] = v;
   __syncthreads();
   if (threadIdx.x == 0) {
-    const double ra = (double)p.beta * (part[0] + part[1]), rb = (double)p.beta * (part[2] + part[3]), h = ra - rb;
+    double sa = part[0], sb = part[kHalf];
+    for (int k = 1; k < kHalf; ++k) {
+      sa += part[k];
+      sb += part[kHalf + k];
+    }
+    const double ra = (double)p.beta * sa, rb = (double)p.beta * sb, h = ra - rb;
     const double w = -(double)p.gscale * ((double)p.beta / P) * (1.0 / (1.0 + exp(h)) - (double)p.eps);
     p.pair[q] = (1.0 - (double)p.eps) * softplus(-h) + (double)p.eps * softplus(h);
     p.reward[q] = (float)ra;
@@ -293,6 +302,22 @@ __global__ __launch_bounds__(kRowThreads) void row_grad_kernel(PrefArgs p) {
   }
 }
 
+template <typename T>
+hipError_t run_preference(PrefArgs& p, bool grad, hipStream_t stream) {
+  hipError_t e = hipSuccess;
+  if (p.rows > 0) {
+    hipLaunchKernelGGL((row_stats_kernel<T>), dim3((unsigned)p.rows), dim3(kRowThreads), 0, stream, p);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (p.S > 0) {
+    hipLaunchKernelGGL(pair_loss_kernel, dim3((unsigned)(p.S / 2)), dim3(64 * kPairWaves), 0, stream, p);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (!grad) p.rows = 0;   // only the mean's workgroup
+  hipLaunchKernelGGL((row_grad_kernel<T>), dim3((unsigned)(p.rows + 1)), dim3(kRowThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_preference(const PrefCall& c, hipStream_t stream) {
@@ -308,26 +333,8 @@ hipError_t launch_preference(const PrefCall& c, hipStream_t stream) {
   p.ld = c.ld; p.ldd = c.ldd;
   p.S = c.S; p.T = c.T; p.V = c.V;
   p.beta = c.beta; p.eps = c.eps; p.gscale = c.gscale;
-  const dim3 block(kRowThreads);
-  if (p.rows > 0) {
-    if (c.bf16)
-      hipLaunchKernelGGL(row_stats_kernel<uint16_t>, dim3((unsigned)p.rows), block, 0, stream, p);
-    else
-      hipLaunchKernelGGL(row_stats_kernel<float>, dim3((unsigned)p.rows), block, 0, stream, p);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (c.S > 0) {
-    hipLaunchKernelGGL(pair_loss_kernel, dim3((unsigned)(c.S / 2)), dim3(256), 0, stream, p);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (!c.dlogits) p.rows = 0;   // only the mean's workgroup
-  if (c.bf16)
-    hipLaunchKernelGGL(row_grad_kernel<uint16_t>, dim3((unsigned)(p.rows + 1)), block, 0, stream, p);
-  else
-    hipLaunchKernelGGL(row_grad_kernel<float>, dim3((unsigned)(p.rows + 1)), block, 0, stream, p);
-  return hipGetLastError();
+  const bool grad = c.dlogits != nullptr;
+  return c.bf16 ? run_preference<uint16_t>(p, grad, stream) : run_preference<float>(p, grad, stream);
 }
 
 }  // namespace qlora

@@ -249,7 +249,7 @@ def _need(t, dtype, shape, name):
 
 
 _TENSORS = None
-_F32, _BF16, _I32, _I64 = range(4)   # dtype numbers of the tensor module
+_F32, _BF16, _I32, _I64, _F64 = range(5)   # dtype numbers of the tensor module
 
 
 def _tensors():
@@ -267,9 +267,7 @@ def _tensors():
 
 
 def _raw_stream(stream):
-    import torch
-
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    return _tensors().stream() if stream is None else stream.cuda_stream
 
 
 # ---- host-only queries ------------------------------------------------------------
@@ -434,13 +432,12 @@ def qlora_preference_loss(logits, labels, ref_logps, beta: float, label_smoothin
         elif dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or dlogits.get_device() != dev:
             raise ValueError("dlogits must have the logits' dtype, shape and device")
         ldd, dp = _row_stride(dlogits, "dlogits"), dlogits.data_ptr()
-    small = ref_logps.new_empty(1 + S + S * T)   # loss, rewards, logps
-    loss, rewards, logps = small[:1], small[1:1 + S], small[1 + S:].view(S, T)
+    loss, rewards, logps = ref_logps.new_empty(1), ref_logps.new_empty(S), ref_logps.new_empty((S, T))
     ws = _workspace(qlora_preference_workspace(S // 2, T, V), logits.device, workspace)
-    at = small.data_ptr()
     _check(_load().qlora_preference_loss(logits.data_ptr(), dt, S // 2, T, V, ld, yp, rp, float(beta),
-                                         float(label_smoothing), float(grad_scale), at, at + 4, at + 4 * (1 + S), dp,
-                                         ldd, ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream)),
+                                         float(label_smoothing), float(grad_scale), loss.data_ptr(),
+                                         rewards.data_ptr(), logps.data_ptr(), dp, ldd, ws.data_ptr(),
+                                         ws.numel() * ws.element_size(), _raw_stream(stream)),
            "qlora_preference_loss")
     return PreferenceOut(loss, rewards, logps, dlogits)
 
@@ -500,12 +497,12 @@ def qlora_clip_grad_norm_batch(grads, max_norm: float, coef=None, norm=None, wor
     gp, sizes = _tensors().addresses(grads, dtype, dev.index if grads else -1, "grads")
     coef = coef if coef is not None else torch.empty(1, dtype=torch.float32, device=dev)
     norm = norm if norm is not None else torch.empty(1, dtype=torch.float64, device=dev)
-    _need(coef, torch.float32, (1,), "coef")
-    _need(norm, torch.float64, (1,), "norm")
+    address = _tensors().address
+    cp, np_ = address(coef, _F32, (1,), dev.index, "coef"), address(norm, _F64, (1,), dev.index, "norm")
     ws = _workspace(QLORA_CLIP_WORKSPACE_BYTES, dev, workspace)
-    _check(_load().qlora_clip_grad_norm_batch(len(grads), gp, gd, sizes, float(max_norm), coef.data_ptr(),
-                                              norm.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                              _raw_stream(stream)), "qlora_clip_grad_norm_batch")
+    _check(_load().qlora_clip_grad_norm_batch(len(grads), gp, gd, sizes, float(max_norm), cp, np_, ws.data_ptr(),
+                                              ws.numel() * ws.element_size(), _raw_stream(stream)),
+           "qlora_clip_grad_norm_batch")
     return coef, norm
 
 
@@ -535,15 +532,13 @@ def qlora_adamw_batch(thetas, grads, state: AdamWState, step: int, lr: float, be
     if state.bits == 8:
         _need_mem(state.m_scale, torch.float32, (total // QLORA_ADAM_STATE_BLOCK,), "state.m_scale")
         _need_mem(state.v_scale, torch.float32, (total // QLORA_ADAM_STATE_BLOCK,), "state.v_scale")
-    if coef is not None:
-        _need(coef, torch.float32, (1,), "coef")
+    cp = None if coef is None else _tensors().address(coef, _F32, (1,), dev, "coef")
     st = QAdamState(state.bits, state.m.data_ptr(), state.v.data_ptr(),
                     state.m_scale.data_ptr() if state.bits == 8 else None,
                     state.v_scale.data_ptr() if state.bits == 8 else None)
     hp = AdamParams(lr, beta1, beta2, eps, weight_decay, step)
     _check(_load().qlora_adamw_batch(n, tp, gp, gd, bp, sizes, ctypes.byref(st), ctypes.byref(hp),
-                                     None if coef is None else coef.data_ptr(), _raw_stream(stream)),
-           "qlora_adamw_batch")
+                                     cp, _raw_stream(stream)), "qlora_adamw_batch")
 
 
 @_on_stream

@@ -74,9 +74,11 @@ def _build_tensors() -> None:
     tmp = TENSORS_PATH + ".tmp"
     cmd = [shutil.which("c++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
-    for path in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]:
+    cmd += ["-D__HIP_PLATFORM_AMD__=1"]
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    for path in cpp_extension.include_paths() + [os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]:
         cmd += ["-isystem", path]
-    cmd += [os.path.join(CSRC, "tensors.cpp"), "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+    cmd += [os.path.join(CSRC, "tensors.cpp"), "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10",
             f"-Wl,-rpath,{lib}"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:

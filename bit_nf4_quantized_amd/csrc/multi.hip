@@ -216,7 +216,6 @@ constexpr int SK = 64;       // reduction per stage
 constexpr int SJ = 64;       // ranks per tile
 constexpr int SM = 128;      // rows (nt) or columns (tn) per tile
 constexpr int kThreads = 256;
-constexpr int kStages = 3;
 
 // 16-byte chunk c of a 128-byte LDS row sits at c ^ swz(row): 16 consecutive
 // rows' fragment reads fall on distinct bank groups.
@@ -253,15 +252,18 @@ struct NtArgs {
   RouteView rv;
 };
 
+constexpr int kNtStages = 2;
+
 struct NtLds {
-  __attribute__((aligned(1024))) uint16_t a[kStages][SM * SK];
-  __attribute__((aligned(1024))) uint16_t b[kStages][SJ * SK];
+  __attribute__((aligned(1024))) uint16_t a[kNtStages][SM * SK];
+  __attribute__((aligned(1024))) uint16_t b[kNtStages][SJ * SK];
   int row[SM];
 };
 
 // C[z][m][j] = sum over slice z of A[m][i] B_a[j][i]: 128 grouped rows of one
-// segment by 64 ranks; 4 waves of 32 rows; the copies of two stages are in
-// flight while a third is multiplied. With BT the adapter's operand has its
+// segment by 64 ranks; 4 waves of 32 rows; one stage's copies are in flight
+// while another is multiplied, and three workgroups fit in a CU's LDS (with
+// three stages two would: 4096 rows of 4096 18.1 us against 14.4). With BT the adapter's operand has its
 // ranks contiguous (L1 as stored) and its fragments come through the LDS
 // transpose read; without, its reduction is contiguous (L2 as stored).
 template <bool BT>
@@ -270,9 +272,9 @@ __device__ __forceinline__ void nt_body(const NtArgs& p, int z, NtLds& lds) {
   auto& sB = lds.b;
   auto& s_row = lds.row;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const RoutePiece pc = route_piece(p.rv, (int)blockIdx.x, SM);
+  const RoutePiece pc = route_piece(p.rv, (int)blockIdx.y, SM);
   if (pc.hi <= pc.lo) return;                       // uniform: no barrier was reached
-  const int j0 = (int)blockIdx.y * SJ;
+  const int j0 = (int)blockIdx.z * SJ;
   const int64_t z0 = (int64_t)z * p.split;
   const int64_t z1 = z0 + p.split < p.len ? z0 + p.split : p.len;
   const int ns = z0 < z1 ? (int)((z1 - z0 + SK - 1) / SK) : 0;
@@ -309,7 +311,7 @@ __device__ __forceinline__ void nt_body(const NtArgs& p, int z, NtLds& lds) {
   }
   auto issue = [&](int st) {
     const int64_t left = z1 - z0 - (int64_t)st * SK;   // reduction left from this stage on
-    const int buf = st % kStages;
+    const int buf = st % kNtStages;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       copy16(a_col[q] < left ? reinterpret_cast<const char*>(a_src[q] + (int64_t)st * SK) : zero,
@@ -335,14 +337,13 @@ __device__ __forceinline__ void nt_body(const NtArgs& p, int z, NtLds& lds) {
   };
 
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s)
+  for (int s = 0; s < kNtStages - 1; ++s)
     if (s < ns) issue(s);
   for (int st = 0; st < ns; ++st) {
-    const int buf = st % kStages;
-    if (st + 1 < ns) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");  // the next stage's 6 copies may stay in flight
-    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const int buf = st % kNtStages;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (st + kStages - 1 < ns) issue(st + kStages - 1);
+    if (st + kNtStages - 1 < ns) issue(st + kNtStages - 1);
     const char* bb = reinterpret_cast<const char*>(sB[buf]);
 #pragma unroll
     for (int kk = 0; kk < SK / 16; ++kk) {
@@ -373,7 +374,7 @@ __device__ __forceinline__ void nt_body(const NtArgs& p, int z, NtLds& lds) {
 // Slices z < zu: U = dY L2_a^T (arguments u); the others: T = X L1_a (t).
 __global__ __launch_bounds__(kThreads) void multi_nt_kernel(NtArgs u, int zu, NtArgs t) {
   __shared__ NtLds lds;
-  const int z = (int)blockIdx.z;
+  const int z = (int)blockIdx.x;
   if (z < zu) nt_body<false>(u, z, lds);
   else nt_body<true>(t, z - zu, lds);
 }
@@ -475,8 +476,14 @@ __device__ __forceinline__ int64_t tn_at(int64_t w, int j, int64_t W, int in) {
 // ranks on the lanes (a row of dL1 is r contiguous values), otherwise the
 // columns (a row of dL2 is W contiguous values): the same products with the
 // MFMA operands exchanged.
+// Three stages, two workgroups per CU. With two stages and three workgroups the
+// kernel took 73 instead of 86 us (8192 rows, 16 adapters) and 11.4 instead of
+// 9.8 us (391 rows), but the whole backward call 747 instead of 750 us and 67.6
+// instead of 67.0: at the larger size the card's power sets the call's time.
+constexpr int kTnStages = 3;
+
 struct TnLds {
-  __attribute__((aligned(1024))) char ring[kStages * kTnStageBytes];
+  __attribute__((aligned(1024))) char ring[kTnStages * kTnStageBytes];
   int row[kTnRows];
 };
 
@@ -516,7 +523,7 @@ __device__ __forceinline__ void tn_body(const TnArgs& p, int bx, TnLds& lds) {
   __syncthreads();
   const int n = pc.hi - pc.lo;
   auto issue = [&](int st) {
-    char* buf = ring + (st % kStages) * kTnStageBytes;
+    char* buf = ring + (st % kTnStages) * kTnStageBytes;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int m = st * SK + 4 * (4 * wave + i) + (lane >> 4);
@@ -548,14 +555,14 @@ __device__ __forceinline__ void tn_body(const TnArgs& p, int bx, TnLds& lds) {
     return b + kTnLBytes + row * kTnSRow + (((c >> 3) ^ tr_swz128(row)) << 4) + ((c & 7) << 1);
   };
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s)
+  for (int s = 0; s < kTnStages - 1; ++s)
     if (s < ns) issue(s);
   for (int st = 0; st < ns; ++st) {
-    if (st + 1 < ns) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+    if (st + 1 < ns) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");   // the next stage's 6 copies may stay in flight
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (st + kStages - 1 < ns) issue(st + kStages - 1);
-    const char* buf = ring + (st % kStages) * kTnStageBytes;
+    if (st + kTnStages - 1 < ns) issue(st + kTnStages - 1);
+    const char* buf = ring + (st % kTnStages) * kTnStageBytes;
 #pragma unroll
     for (int kk = 0; kk < SK / 16; ++kk) {
       const int r0 = 16 * kk + rb;
@@ -676,8 +683,10 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int finish_blocks(int64_t values) { return (int)(cdiv(values, 4096) < 128 ? cdiv(values, 4096) : 128); }
 unsigned capped(int64_t blocks) { return (unsigned)(blocks < 1 ? 1 : blocks > 16384 ? 16384 : blocks); }
 
-// Reduction slices of the NT products: about two workgroups per CU, the
-// number that is resident at once.
+// Reduction slices of the NT products: about two workgroups per CU, from five
+// slices on in eights: consecutive workgroups run on the 8 XCDs in turn, and
+// then an XCD's L2 holds one slice of the adapters' operands instead of all
+// (dY of 8192 x 11008, 16 adapters: 61.9 -> 58.9 us; X of 4096 x 4096: 15.9 -> 14.4).
 struct NtSplit {
   int64_t len;
   int Z;
@@ -687,7 +696,7 @@ NtSplit nt_split(int64_t M, int64_t len, int A, int rp) {
   if (tiles < 1) tiles = 1;
   const int64_t steps = cdiv(len, SK);
   int64_t z = 2 * (int64_t)device_cu_count() / tiles;
-  if (z > 16) z = 16;
+  if (z > 4) z = z > 8 ? 16 : 8;
   if (z > steps) z = steps;
   if (z < 1) z = 1;
   const int64_t per = cdiv(steps, z);
@@ -790,7 +799,7 @@ NtArgs nt_args(const uint16_t* rows, int64_t len, const uint16_t* B, int64_t b_s
 hipError_t launch_nt(const NtArgs* u, int zu, const NtArgs* t, int zt, int64_t M, int A, hipStream_t stream) {
   const NtArgs& any = u ? *u : *t;
   const int64_t pieces = M / SM + (A < M ? A : M);
-  hipLaunchKernelGGL(multi_nt_kernel, dim3((unsigned)pieces, (unsigned)(any.rp / SJ), (unsigned)(zu + zt)),
+  hipLaunchKernelGGL(multi_nt_kernel, dim3((unsigned)(zu + zt), (unsigned)pieces, (unsigned)(any.rp / SJ)),
                      dim3(kThreads), 0, stream, u ? *u : any, zu, t ? *t : any);
   return hipGetLastError();
 }
@@ -953,8 +962,8 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
   const TnArgs g2 = tn_args(dY, N, T, r, false, r, rows, scale, rv, part2, dL2, grad_bf16);
   const int64_t pieces = M / rows + segs, tiles = cdiv(K, SM) + cdiv(N, SM);
   const int64_t planes = cdiv(sum.values / 8, kThreads * tiles * cdiv(r, SJ));
-  hipLaunchKernelGGL(multi_tn_kernel, dim3((unsigned)tiles, (unsigned)cdiv(r, SJ), (unsigned)(pieces + planes)),
-                     dim3(kThreads), 0, stream, g1, (int)cdiv(K, SM), g2, (int)pieces, sum);
+  const dim3 grid((unsigned)tiles, (unsigned)cdiv(r, SJ), (unsigned)(pieces + planes));
+  hipLaunchKernelGGL(multi_tn_kernel, grid, dim3(kThreads), 0, stream, g1, (int)cdiv(K, SM), g2, (int)pieces, sum);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int b1 = finish_blocks(K * r), b2 = finish_blocks(N * r);

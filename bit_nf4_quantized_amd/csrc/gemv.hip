@@ -482,6 +482,8 @@ struct FuseT {
 // variants multiply the dequantised weight itself: the table holds fp16 pairs
 // of q (off by at most 2^-12, where bf16(q) is off by 2^-9), each is multiplied
 // by a' in fp32 and rounded to bf16 once, as the standalone dequant rounds.
+// 13 rows of 32 rank-16 adapters, 11008 -> 4096 (29 MB): 17.8 us after T's 5.5, the
+// call 21.5 (a single adapter's 19.3); bound by the table lookups and latency.
 constexpr int ft_slices(int F) { return F == 1 ? 4 : 12 / F; }
 
 template <int D, bool XL>

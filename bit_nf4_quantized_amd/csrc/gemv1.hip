@@ -47,6 +47,9 @@
 // variants multiply the dequantised weight itself: the table holds fp16 pairs
 // of q (off by at most 2^-12, where bf16(q) is off by 2^-9), each is multiplied
 // by a' in fp32 and rounded to bf16 once, as the standalone dequant rounds.
+// One token of 8 resident rank-64 adapters, 4096 -> 11008 (25 MB): 5.1 + 12.3 us,
+// the call 16.3 (1.5 TB/s; a single adapter's 15.9), bound by two launches and the
+// prologue's latency.
 // Every result is deterministic (fixed orders, no atomics).
 #include "common.h"
 #include "launch.h"

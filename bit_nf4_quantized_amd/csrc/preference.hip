@@ -23,10 +23,11 @@
 // The weight needs every row of its pair, so a counted logit is read twice and
 // its gradient written once: both row kernels are bound by HBM. For 16
 // sequences of 1024 x 32000 bf16 (72 % of the rows count: 0.75 GB read twice,
-// 1.05 GB written) the call takes 0.47 ms, 5.4 TB/s, a large copy's rate.
+// 1.05 GB written) the call takes 0.45 ms, 5.6 TB/s, more than a large copy's rate:
+// row_stats 133 us, pair_loss 5.5, row_grad 311.
 // row_grad walks the rows backwards, so that the rows read last are still in
 // the last-level cache, and stores past it (nontemporal): 0.50 ms without
-// either, 0.495 ms with one of them. Launching both row kernels over groups of
+// either, 0.495 ms with one of them, 0.47 with both. Launching both row kernels over groups of
 // pairs that fit that cache was slower (0.54 ms for two groups, 0.62 ms for
 // eight): each group adds three launches' ends.
 // A row's first element need not be 16-byte aligned

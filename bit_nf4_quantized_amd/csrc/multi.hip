@@ -170,17 +170,27 @@ struct LayArgs {
   const uint16_t* src;    // L2 [A][r][W] (transposed into [W][rp]) or L1 [A][W][r] (padded to [W][rp])
   uint16_t* out;          // per group [W][rp]; columns past a segment's r, and of segments that are none, zero
   int64_t W;
-  int r, rp, blocks;      // blocks per segment
+  int r, rp, blocks;      // blocks per group
   bool transpose;
 };
 
-// L2 of segment k transposed into its columns: 64 output rows n and 64 ranks
-// per workgroup (none: zeros).
-__device__ __forceinline__ void lay_transposed(const LayArgs& p, const RouteView& rv, int k, bool none, int b) {
+// Column c of group g's operand: its segment and rank (none: zeros).
+struct LayColumn {
+  int segment, rank;
+  bool none;
+};
+__device__ __forceinline__ LayColumn lay_column(const LayArgs& p, const RouteView& rv, int g, int c) {
+  const Packing pk = packing_of(p.r);
+  const int s = c / pk.width, k = g * pk.pack + s, j = c - s * pk.width;
+  return LayColumn{k, j, k >= rv.count[0] || j >= p.r};
+}
+
+// L2 of group g's segments transposed side by side: 64 output rows n and 64
+// columns per workgroup, so that whole lines are written (one segment per
+// workgroup: 13.3 against 6.7 us for 32 of rank 16, N = 11008).
+__device__ __forceinline__ void lay_transposed(const LayArgs& p, const RouteView& rv, int g, int b) {
   __shared__ uint16_t tile[64][64 + 2];
   const int64_t N = p.W;
-  const uint16_t* src = p.src + (none ? 0 : (int64_t)rv.adapter[k] * p.r * N);
-  const Packing pk = packing_of(p.r);
   const int tiles = p.rp / 64;
   const int64_t n0 = (int64_t)(b / tiles) * 64;
   const int j0 = (b % tiles) * 64;
@@ -188,18 +198,20 @@ __device__ __forceinline__ void lay_transposed(const LayArgs& p, const RouteView
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int j = (t >> 3) + 32 * u, c = (t & 7) * 8;
+    const LayColumn col = lay_column(p, rv, g, j0 + j);
     u32x4_t v = {0u, 0u, 0u, 0u};
-    if (!none && j0 + j < p.r && n0 + c < N) v = *reinterpret_cast<const u32x4_t*>(src + (int64_t)(j0 + j) * N + n0 + c);
+    if (!col.none && n0 + c < N)
+      v = *reinterpret_cast<const u32x4_t*>(p.src + ((int64_t)rv.adapter[col.segment] * p.r + col.rank) * N + n0 + c);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e) tile[c + e][j] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
   }
   __syncthreads();
-  uint16_t* out = p.out + (int64_t)(k / pk.pack) * N * p.rp + (k % pk.pack) * pk.width;
+  uint16_t* out = p.out + (int64_t)g * N * p.rp;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int n = (t >> 3) + 32 * u, c = (t & 7) * 8;
-    if (n0 + n >= N || c >= pk.width) continue;
+    if (n0 + n >= N) continue;
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = (uint32_t)tile[n][c + 2 * e] | ((uint32_t)tile[n][c + 2 * e + 1] << 16);
@@ -207,18 +219,18 @@ __device__ __forceinline__ void lay_transposed(const LayArgs& p, const RouteView
   }
 }
 
-// L1 of segment k into its columns: 256 16-byte pieces per workgroup.
-__device__ __forceinline__ void lay_padded(const LayArgs& p, const RouteView& rv, int k, bool none, int b) {
-  const uint16_t* src = p.src + (none ? 0 : (int64_t)rv.adapter[k] * p.W * p.r);
-  const Packing pk = packing_of(p.r);
+// L1 of group g's segments side by side: 256 16-byte pieces per workgroup.
+__device__ __forceinline__ void lay_padded(const LayArgs& p, const RouteView& rv, int g, int b) {
   const int64_t i = (int64_t)b * 256 + threadIdx.x;
-  const int per = pk.width / 8;
+  const int per = p.rp / 8;
   if (i >= p.W * per) return;
   const int64_t row = i / per;
-  const int c = (int)(i - row * per) * 8;
+  const int c = (int)(i - row * per) * 8;           // 8 columns are one segment's (r % 8 == 0)
+  const LayColumn col = lay_column(p, rv, g, c);
   u32x4_t v = {0u, 0u, 0u, 0u};
-  if (!none && c < p.r) v = *reinterpret_cast<const u32x4_t*>(src + row * p.r + c);
-  *reinterpret_cast<u32x4_t*>(p.out + ((int64_t)(k / pk.pack) * p.W + row) * p.rp + (k % pk.pack) * pk.width + c) = v;
+  if (!col.none)
+    v = *reinterpret_cast<const u32x4_t*>(p.src + ((int64_t)rv.adapter[col.segment] * p.W + row) * p.r + col.rank);
+  *reinterpret_cast<u32x4_t*>(p.out + ((int64_t)g * p.W + row) * p.rp + c) = v;
 }
 
 // ---- pieces shared by the two adapter products -----------------------------------------
@@ -429,11 +441,10 @@ __device__ __forceinline__ u32x2_t pack4(const f32x4_t& v, float s) {
 // GEMM's adapter operand.
 __global__ __launch_bounds__(256) void multi_sum_kernel(SumArgs p, int blocks, LayArgs lay, RouteView rv) {
   if ((int)blockIdx.x >= blocks) {
-    const int b = (int)blockIdx.x - blocks, k = b / lay.blocks;
-    const int n = rv.count[0], pack = packing_of(lay.r).pack;
-    if (k >= (n + pack - 1) / pack * pack) return;  // uniform; the last group's missing segments are zeros
-    if (lay.transpose) lay_transposed(lay, rv, k, k >= n, b - k * lay.blocks);
-    else lay_padded(lay, rv, k, k >= n, b - k * lay.blocks);
+    const int b = (int)blockIdx.x - blocks, g = b / lay.blocks;
+    if (g * packing_of(lay.r).pack >= rv.count[0]) return;  // uniform
+    if (lay.transpose) lay_transposed(lay, rv, g, b - g * lay.blocks);
+    else lay_padded(lay, rv, g, b - g * lay.blocks);
     return;
   }
   const int w4 = p.rp / 4;
@@ -463,7 +474,7 @@ struct TnArgs {
   float* part;            // per piece and rank tile: [W][64] or [64][W]
   const float* scale;     // factor per adapter, or null
   int64_t ldl, lds, W, slab;   // slab: floats per piece (all its rank tiles)
-  int r, rows;            // rows per piece
+  int r, rows, ring;      // rows per piece, bytes of the ring
   bool packed;            // S holds a segment's ranks in its own columns
   bool out_bf16;
   RouteView rv;
@@ -493,15 +504,16 @@ __device__ __forceinline__ int64_t tn_at(int64_t w, int j, int64_t W, int in) {
 // instead of 67.0: at the larger size the card's power sets the call's time.
 constexpr int kTnStages = 3;
 
-struct TnLds {
-  __attribute__((aligned(1024))) char ring[kTnStages * kTnStageBytes];
-  int row[kTnRows];
-};
+// Dynamic LDS: the ring, then the piece's rows; for few rows M the stages and
+// rows that a piece of M rows has, so that more workgroups fit in a CU. With
+// that, and only the rows of a short piece copied and multiplied: 88 rows of 44
+// rank-8 adapters, 9280 -> 3776, 37.6 -> 28.8 us.
+int tn_stages(int64_t rows) { return (int)(rows <= SK ? 1 : rows <= 2 * SK ? 2 : kTnStages); }
+int tn_lds(int64_t rows) { return tn_stages(rows) * kTnStageBytes + (int)(rows < kTnRows ? rows : kTnRows) * 4; }
 
 template <bool RANKS_IN>
-__device__ __forceinline__ void tn_body(const TnArgs& p, int bx, TnLds& lds) {
-  char* ring = lds.ring;
-  int* s_row = lds.row;
+__device__ __forceinline__ void tn_body(const TnArgs& p, int bx, char* ring) {
+  int* s_row = reinterpret_cast<int*>(ring + p.ring);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const RoutePiece pc = route_piece(p.rv, (int)blockIdx.z, p.rows);
   if (pc.hi <= pc.lo) return;                       // uniform: no barrier was reached
@@ -533,16 +545,19 @@ __device__ __forceinline__ void tn_body(const TnArgs& p, int bx, TnLds& lds) {
   for (int i = tid; i < pc.hi - pc.lo; i += kThreads) s_row[i] = p.rv.perm[pc.lo + i];
   __syncthreads();
   const int n = pc.hi - pc.lo;
-  auto issue = [&](int st) {
+  // a single stage: only the MFMA steps that have rows
+  auto issue = [&](int st, int end) {
     char* buf = ring + (st % kTnStages) * kTnStageBytes;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      if (4 * (4 * wave + i) >= end) continue;        // uniform
       const int m = st * SK + 4 * (4 * wave + i) + (lane >> 4);
       copy16(m < n ? reinterpret_cast<const char*>(p.L + (int64_t)s_row[m < n ? m : 0] * p.ldl + l_col[i]) : zero,
              buf + (4 * wave + i) * 1024);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      if (8 * (2 * wave + i) >= end) continue;
       const int m = st * SK + 8 * (2 * wave + i) + (lane >> 3);
       copy16(m < n && s_in[i] ? reinterpret_cast<const char*>(S + (int64_t)s_row[m < n ? m : 0] * p.lds + s_col[i]) : zero,
              buf + kTnLBytes + (2 * wave + i) * 1024);
@@ -565,25 +580,33 @@ __device__ __forceinline__ void tn_body(const TnArgs& p, int bx, TnLds& lds) {
     const int c = 32 * t + cs;
     return b + kTnLBytes + row * kTnSRow + (((c >> 3) ^ tr_swz128(row)) << 4) + ((c & 7) << 1);
   };
+  auto multiply = [&](const char* buf, int kk) {
+    const int r0 = 16 * kk + rb;
+    const bf16x8_t l = frag_tr(l_at(buf, r0), l_at(buf, r0 + 4));
 #pragma unroll
-  for (int s = 0; s < kTnStages - 1; ++s)
-    if (s < ns) issue(s);
-  for (int st = 0; st < ns; ++st) {
-    if (st + 1 < ns) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");   // the next stage's 6 copies may stay in flight
-    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    for (int t = 0; t < 2; ++t) {
+      const bf16x8_t s = frag_tr(s_at(buf, r0, t), s_at(buf, r0 + 4, t));
+      acc[t] = RANKS_IN ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(l, s, acc[t], 0, 0, 0)
+                        : __builtin_amdgcn_mfma_f32_32x32x16_bf16(s, l, acc[t], 0, 0, 0);
+    }
+  };
+  if (ns == 1) {
+    issue(0, (n + 15) & ~15);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (st + kTnStages - 1 < ns) issue(st + kTnStages - 1);
-    const char* buf = ring + (st % kTnStages) * kTnStageBytes;
+    for (int kk = 0; 16 * kk < n; ++kk) multiply(ring, kk);
+  } else {
 #pragma unroll
-    for (int kk = 0; kk < SK / 16; ++kk) {
-      const int r0 = 16 * kk + rb;
-      const bf16x8_t l = frag_tr(l_at(buf, r0), l_at(buf, r0 + 4));
+    for (int s = 0; s < kTnStages - 1; ++s)
+      if (s < ns) issue(s, SK);
+    for (int st = 0; st < ns; ++st) {
+      if (st + 1 < ns) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");   // the next stage's 6 copies may stay in flight
+      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      if (st + kTnStages - 1 < ns) issue(st + kTnStages - 1, SK);
+      const char* buf = ring + (st % kTnStages) * kTnStageBytes;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const bf16x8_t s = frag_tr(s_at(buf, r0, t), s_at(buf, r0 + 4, t));
-        acc[t] = RANKS_IN ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(l, s, acc[t], 0, 0, 0)
-                          : __builtin_amdgcn_mfma_f32_32x32x16_bf16(s, l, acc[t], 0, 0, 0);
-      }
+      for (int kk = 0; kk < SK / 16; ++kk) multiply(buf, kk);
     }
   }
   const int s0 = p.rv.start[pc.k], s1 = p.rv.start[pc.k + 1];
@@ -615,7 +638,7 @@ __device__ __forceinline__ void tn_body(const TnArgs& p, int bx, TnLds& lds) {
 // others: dL2 (g2). The planes from z1 on add the slices of a split dX: alone
 // that was a launch of 5.8 us after the GEMM (391 rows of 4096).
 __global__ __launch_bounds__(kThreads) void multi_tn_kernel(TnArgs g1, int x1, TnArgs g2, int z1, SplitSum sum) {
-  __shared__ TnLds lds;
+  extern __shared__ __attribute__((aligned(1024))) char tn_smem[];
   const int x = (int)blockIdx.x;
   if ((int)blockIdx.z >= z1) {
     const int64_t plane = (int64_t)gridDim.x * gridDim.y;
@@ -623,8 +646,8 @@ __global__ __launch_bounds__(kThreads) void multi_tn_kernel(TnArgs g1, int x1, T
     split_sum_body(sum, b * kThreads + threadIdx.x);
     return;
   }
-  if (x < x1) tn_body<true>(g1, x, lds);
-  else tn_body<false>(g2, x - x1, lds);
+  if (x < x1) tn_body<true>(g1, x, tn_smem);
+  else tn_body<false>(g2, x - x1, tn_smem);
 }
 
 // The gradients that multi_tn_kernel left open: the sums of a segment's
@@ -817,8 +840,8 @@ hipError_t launch_nt(const NtArgs* u, int zu, const NtArgs* t, int zt, int64_t M
 
 hipError_t launch_sum(const SumArgs& s, const LayArgs& lay, int64_t segs, const RouteView& rv, hipStream_t stream) {
   const int64_t blocks = cdiv((s.M + 1) * s.rp / 4, 256);
-  if (lay.blocks > 0) segs = cdiv(segs, packing_of(lay.r).pack) * packing_of(lay.r).pack;   // whole groups
-  hipLaunchKernelGGL(multi_sum_kernel, dim3((unsigned)(blocks + segs * lay.blocks)), dim3(256), 0, stream, s, (int)blocks,
+  const int64_t groups = cdiv(segs, packing_of(lay.r).pack);
+  hipLaunchKernelGGL(multi_sum_kernel, dim3((unsigned)(blocks + groups * lay.blocks)), dim3(256), 0, stream, s, (int)blocks,
                      lay, rv);
   return hipGetLastError();
 }
@@ -829,7 +852,7 @@ hipError_t zero_words(void* p, int64_t bytes, hipStream_t stream) {
   return hipGetLastError();
 }
 
-TnArgs tn_args(const uint16_t* L, int64_t W, const uint16_t* S, int64_t lds, bool packed, int r, int rows,
+TnArgs tn_args(const uint16_t* L, int64_t W, const uint16_t* S, int64_t lds, bool packed, int r, int rows, int ring,
                const float* scale, const RouteView& rv, float* part, void* out, bool out_bf16) {
   TnArgs a;
   a.L = L; a.S = S; a.out = out; a.part = part; a.scale = scale;
@@ -837,6 +860,7 @@ TnArgs tn_args(const uint16_t* L, int64_t W, const uint16_t* S, int64_t lds, boo
   a.slab = W * cdiv(r, SJ) * SJ;
   a.r = r;
   a.rows = rows;
+  a.ring = ring;
   a.packed = packed;
   a.out_bf16 = out_bf16;
   a.rv = rv;
@@ -943,7 +967,7 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
   uint16_t* l1p = reinterpret_cast<uint16_t*>(base + L.b2_off);
   const bool padded = dX && rp != r;
   const SumArgs s{upart, part, su.Z, st.Z, M, r, rp, ids, A, scale, ra.slot, sU, tbuf};
-  const LayArgs lay{L1, l1p, K, r, rp, (int)cdiv(K * packing_of(r).width / 8, 256), false};
+  const LayArgs lay{L1, l1p, K, r, rp, (int)cdiv(K * rp / 8, 256), false};
   e = launch_sum(s, lay, padded ? segs : 0, rv, stream);
   if (e != hipSuccess) return e;
   if (!T) T = tbuf;
@@ -969,12 +993,21 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
 
   const int rows = tn_rows(M, K, N, r);
   float* part2 = part + tn_part_floats(M, K, N, K, r, A);
-  const TnArgs g1 = tn_args(X, K, sU, rp, true, r, rows, nullptr, rv, part, dL1, grad_bf16);
-  const TnArgs g2 = tn_args(dY, N, T, r, false, r, rows, scale, rv, part2, dL2, grad_bf16);
+  const int64_t most = M < rows ? M : rows;          // rows of a piece
+  const int ring = tn_stages(most) * kTnStageBytes;
+  const TnArgs g1 = tn_args(X, K, sU, rp, true, r, rows, ring, nullptr, rv, part, dL1, grad_bf16);
+  const TnArgs g2 = tn_args(dY, N, T, r, false, r, rows, ring, scale, rv, part2, dL2, grad_bf16);
   const int64_t pieces = M / rows + segs, tiles = cdiv(K, SM) + cdiv(N, SM);
   const int64_t planes = cdiv(sum.values / 8, kThreads * tiles * cdiv(r, SJ));
   const dim3 grid((unsigned)tiles, (unsigned)cdiv(r, SJ), (unsigned)(pieces + planes));
-  hipLaunchKernelGGL(multi_tn_kernel, grid, dim3(kThreads), 0, stream, g1, (int)cdiv(K, SM), g2, (int)pieces, sum);
+  static bool attr_set = false;  // raise the dynamic-LDS limit once (idempotent)
+  if (!attr_set) {
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&multi_tn_kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                              tn_lds(kTnRows));
+    (void)hipGetLastError();  // a refusal shows up as a launch error below
+    attr_set = true;
+  }
+  hipLaunchKernelGGL(multi_tn_kernel, grid, dim3(kThreads), tn_lds(most), stream, g1, (int)cdiv(K, SM), g2, (int)pieces, sum);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int b1 = finish_blocks(K * r), b2 = finish_blocks(N * r);

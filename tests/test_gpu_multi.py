@@ -219,6 +219,27 @@ def test_backward(api, M, K, N, r, A, kind):
     c.check_bwd(label, c.check_fwd(label))
 
 
+# a few rows per adapter: pieces that end inside an MFMA step, one and two stages of rows, groups of small ranks
+FEW = [(2, 8, 2), (15, 8, 9), (16, 64, 1), (17, 64, 1), (31, 16, 5), (33, 64, 33), (63, 24, 2), (65, 64, 1), (88, 8, 44),
+       (127, 32, 1), (128, 16, 128), (129, 64, 1), (190, 40, 1)]
+
+
+@pytest.mark.parametrize("M,r,A", FEW)
+def test_backward_of_few_rows(api, M, r, A):
+    label = f"multi bwd of few rows M={M} r={r} A={A}"
+    say(label)
+    c = Case(api, M, 320, 264, r, A, "rows" if A > 1 else "one")
+    c.check_bwd(label, c.check_fwd(label))
+
+
+@pytest.mark.parametrize("M,K", [(20, 4096), (30, 1088), (50, 2048), (17, 640)])
+def test_many_slices(api, M, K):
+    """Narrow weights: the base product of up to 128 rows in many slices of the reduction."""
+    label = f"multi fwd many slices M={M} K={K}"
+    say(label)
+    Case(api, M, K, 136, 16, 3, "rows").check_fwd(label)
+
+
 @pytest.mark.parametrize("qtype,dq", [("nf4", False), ("int4", True), ("fp4_e2m1", False)])
 @pytest.mark.parametrize("M", [1, 6, 50, 200])
 def test_other_weight_formats(api, M, qtype, dq):

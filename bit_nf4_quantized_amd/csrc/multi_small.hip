@@ -465,13 +465,13 @@ hipError_t run_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, in
 
 // ---- the sum ---------------------------------------------------------------------------
 
-// Y = bf16(sum_z base[z][m][n] + sum_j bf16(s_a T[m][j]) L2_a[j][n]): 512
-// columns, 8 per lane, up to 16 rows of one group: wave w takes rows w, w + 4,
-// ... The slices of T and of the base are added in order; workgroup column 0
-// writes T_out.
-constexpr int kFinCols = 512;
+// Y = bf16(sum_z base[z][m][n] + sum_j bf16(s_a T[m][j]) L2_a[j][n]) for up to
+// 16 rows of one group and 8 LANES columns, 8 per lane: a wave takes 64 / LANES
+// rows at a time. The slices of T and of the base are added in order; workgroup
+// column 0 writes T_out.
 constexpr int kFinRank = 256;
 
+template <int LANES>
 __global__ __launch_bounds__(256) void small_multi_finish_kernel(const float* __restrict__ base, int S, int M, int N,
                                                                  const int32_t* __restrict__ ids, int A,
                                                                  const float* __restrict__ tpart, int Z, int r,
@@ -480,11 +480,13 @@ __global__ __launch_bounds__(256) void small_multi_finish_kernel(const float* __
                                                                  uint16_t* __restrict__ Y,
                                                                  uint16_t* __restrict__ T_out) {
   __shared__ int rows[kGroup];
-  __shared__ float sT[kGroup][kFinRank];
+  constexpr int kPer = 64 / LANES, kQ = kGroup / (4 * kPer);   // rows per wave at a time, and times
+  __shared__ float sT[kGroup][kFinRank + 4];          // rows of one wave in different banks
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const SmallGroup g = small_group<256>(ids, M, A, (int)blockIdx.y, rows);
   if (g.n == 0) return;                               // uniform
-  const int n = (int)blockIdx.x * kFinCols + 8 * lane;
+  const int n = (int)blockIdx.x * (8 * LANES) + 8 * (lane % LANES);
+  const int first = wave * kPer;                      // row i of time q: first + lane / LANES + 4 kPer q
   const bool in = n < N;                              // N % 8 == 0
   const int nc = in ? n : 0;
   // L2 rows in batches; the first one's loads go out before anything waits
@@ -497,21 +499,33 @@ __global__ __launch_bounds__(256) void small_multi_finish_kernel(const float* __
       l2[u] = *reinterpret_cast<const u32x4_t*>(B + (int64_t)(j0 + u < r ? j0 + u : 0) * N);
   };
   load_l2(0);
-  float acc[4][8];
+  constexpr int kSlices = 4;
+  float acc[kQ][8];
+  int at[kQ];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int i = wave + 4 * q;
+  for (int q = 0; q < kQ; ++q) {
+    at[q] = first + lane / LANES + 4 * kPer * q;
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[q][e] = 0.0f;
-    if (i >= g.n) continue;                           // uniform per wave
-    const int64_t row = rows[i];
-    for (int z = 0; z < S; ++z) {
-      const float* p = base + ((int64_t)z * M + row) * N + nc;
-      const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(p + 4);
+    if (first + 4 * kPer * q >= g.n) continue;        // uniform per wave
+    const float* p = base + (int64_t)rows[at[q] < g.n ? at[q] : 0] * N + nc;
+    const int64_t pitch = (int64_t)M * N;
+    for (int z = 0; z < S; z += kSlices) {            // that many slices' loads in flight, added in order
+      f32x4_t a[kSlices], b[kSlices];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[q][e] += a[e];
-        acc[q][4 + e] += b[e];
+      for (int u = 0; u < kSlices; ++u) {
+        const float* s = p + (z + u < S ? z + u : z) * pitch;
+        a[u] = *reinterpret_cast<const f32x4_t*>(s);
+        b[u] = *reinterpret_cast<const f32x4_t*>(s + 4);
+      }
+#pragma unroll
+      for (int u = 0; u < kSlices; ++u) {
+        if (z + u >= S) break;                        // uniform
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[q][e] += a[u][e];
+          acc[q][4 + e] += b[u][e];
+        }
       }
     }
   }
@@ -521,15 +535,13 @@ __global__ __launch_bounds__(256) void small_multi_finish_kernel(const float* __
       const int k = i / r, j = i - k * r;
       const float* p = tpart + (int64_t)rows[k] * r + j;
       float v = 0.0f;
-      int z = 0;
-      for (; z + 8 <= Z; z += 8) {  // loads of 8 slices in flight, added in order
+      for (int z = 0; z < Z; z += 8) {  // loads of 8 slices in flight, added in order
         float b[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) b[u] = p[(int64_t)(z + u) * M * r];
+        for (int u = 0; u < 8; ++u) b[u] = p[(int64_t)(z + u < Z ? z + u : z) * M * r];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v += b[u];
+        for (int u = 0; u < 8; ++u) v += z + u < Z ? b[u] : 0.0f;
       }
-      for (; z < Z; ++z) v += p[(int64_t)z * M * r];
       sT[k][j] = bf16_to_f32(f32_to_bf16(s * v));
       if (T_out && blockIdx.x == 0) T_out[(int64_t)rows[k] * r + j] = f32_to_bf16(v);
     }
@@ -537,7 +549,7 @@ __global__ __launch_bounds__(256) void small_multi_finish_kernel(const float* __
     for (int i = tid; i < g.n * r; i += 256) T_out[(int64_t)rows[i / r] * r + i % r] = 0;
   }
   __syncthreads();
-  if (g.has && wave < g.n) {
+  if (g.has && first < g.n) {
     for (int j0 = 0; j0 < r; j0 += kBatch) {
       if (j0 > 0) load_l2(j0);
 #pragma unroll
@@ -551,9 +563,9 @@ __global__ __launch_bounds__(256) void small_multi_finish_kernel(const float* __
           l[2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (wave + 4 * q >= g.n) continue;
-          const float t = sT[wave + 4 * q][j0 + u];
+        for (int q = 0; q < kQ; ++q) {
+          if (first + 4 * kPer * q >= g.n) continue;
+          const float t = sT[at[q]][j0 + u];          // rows past the group: not stored
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[q][e] = __builtin_fmaf(t, l[e], acc[q][e]);
         }
@@ -561,10 +573,9 @@ __global__ __launch_bounds__(256) void small_multi_finish_kernel(const float* __
     }
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int i = wave + 4 * q;
-    if (i < g.n && in)
-      *reinterpret_cast<u32x4_t*>(Y + (int64_t)rows[i] * N + n) =
+  for (int q = 0; q < kQ; ++q) {
+    if (at[q] < g.n && in)
+      *reinterpret_cast<u32x4_t*>(Y + (int64_t)rows[at[q]] * N + n) =
           u32x4_t{pack_bf16x2(acc[q][0], acc[q][1]), pack_bf16x2(acc[q][2], acc[q][3]),
                   pack_bf16x2(acc[q][4], acc[q][5]), pack_bf16x2(acc[q][6], acc[q][7])};
   }
@@ -601,8 +612,16 @@ hipError_t launch_multi_small_t(const uint16_t* X, int64_t M, int64_t K, const M
 hipError_t launch_multi_small_finish(const float* base, int S, int64_t M, int64_t N, const MultiIds& mi,
                                      const float* tpart, int Z, int r, const uint16_t* L2, uint16_t* Y,
                                      uint16_t* T_out, hipStream_t stream) {
-  hipLaunchKernelGGL(small_multi_finish_kernel, dim3((unsigned)((N + kFinCols - 1) / kFinCols), (unsigned)M), dim3(256),
-                     0, stream, base, S, (int)M, (int)N, mi.ids, mi.A, tpart, Z, r, L2, mi.scale, Y, T_out);
+  // Workgroups of 512 columns, or of 128 where those would leave CUs idle: 34
+  // rows of 8 rank-64 adapters 2944 -> 2392 26.2 instead of 39 us, 51 rows of one
+  // 4608 -> 1128 23.0 / 33.9; 96 rows of 24, 4096 -> 11008 44.8 / 39.5.
+  const int64_t groups = M < mi.A + 1 + M / kGroup ? M : mi.A + 1 + M / kGroup;   // at most
+  if ((N + 511) / 512 * groups <= device_cu_count())
+    hipLaunchKernelGGL(small_multi_finish_kernel<16>, dim3((unsigned)((N + 127) / 128), (unsigned)M), dim3(256), 0, stream,
+                       base, S, (int)M, (int)N, mi.ids, mi.A, tpart, Z, r, L2, mi.scale, Y, T_out);
+  else
+    hipLaunchKernelGGL(small_multi_finish_kernel<64>, dim3((unsigned)((N + 511) / 512), (unsigned)M), dim3(256), 0, stream,
+                       base, S, (int)M, (int)N, mi.ids, mi.A, tpart, Z, r, L2, mi.scale, Y, T_out);
   return hipGetLastError();
 }
 

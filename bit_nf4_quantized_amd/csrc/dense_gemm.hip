@@ -107,8 +107,8 @@ struct DenseArgs {
   int tail_split;   // 2 or 4
   const float* E;   // ADD: fp32 addend [M][N] (row stride lde), C = bf16(alpha acc + E)
   int64_t lde;
-  float* part;      // SPLIT: fp32 partials [slices][M][N] of main stages z per_slice .. (the slab with the last)
-  int per_slice;
+  float* part;      // SPLIT: fp32 partials [slices][M][N] of main stages z per_slice ..
+  int per_slice, slices;
 };
 
 // One stage of one operand: rows [row0, row0+256) x columns [k0, k0+64).
@@ -189,11 +189,9 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p_all, const MultiSla
   DenseArgs p = p_all;
   if constexpr (SPLIT) {
     const int64_t k0 = (int64_t)z * p.per_slice * TK, len = (int64_t)p.per_slice * TK;
-    const bool last = k0 + len >= p.K;
     p.A += k0;
     p.B += k0;
-    p.K = last ? p.K - k0 : len;
-    if (!last) p.K2 = 0;
+    p.K = k0 + len >= p.K ? p.K - k0 : len;
   }
   using S = TileShape<TMX>;
   constexpr int WTM = S::kWtm, MI = S::kMi;
@@ -205,7 +203,13 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p_all, const MultiSla
   if constexpr (MULTI) {
     const RouteRange rg = route_range(slab.rv, (int)m0, (int)m0 + TMX);
     group0 = rg.lo / slab.pack;
-    nslab = rg.hi > rg.lo ? ((rg.hi - 1) / slab.pack - group0 + 1) * per_group : 0;   // per_group 0: another slice's
+    int groups = rg.hi > rg.lo ? (rg.hi - 1) / slab.pack - group0 + 1 : 0;
+    if constexpr (SPLIT) {  // group g goes to slice g mod S: the same sums wherever a row lies
+      const int skip = (z - group0 % p.slices + p.slices) % p.slices;
+      groups = groups > skip ? (groups - skip - 1) / p.slices + 1 : 0;
+      group0 += skip;
+    }
+    nslab = groups * per_group;
     segs = rg.hi;
   }
   const int nk = nmain + nslab;
@@ -231,7 +235,7 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p_all, const MultiSla
   auto slab_at = [&](int i, int* col) {
     const int s = __builtin_amdgcn_readfirstlane(i / per_group);
     *col = (i - s * per_group) * TK;
-    return group0 + s;
+    return group0 + s * (SPLIT ? p.slices : 1);
   };
   auto slab_a = [&](int g, int j) -> uint32_t {
     const int rloc = (wave * S::kIpwA + j) * RPI + (lane >> 3);
@@ -603,7 +607,7 @@ hipError_t launch_gemm_nt_rows(const uint16_t* A, int64_t lda, const uint16_t* B
   p.lda = lda; p.ldb = ldb; p.ld2 = ld2; p.ldc = ldc;
   p.M = M; p.N = N; p.K = K; p.K2 = K2; p.alpha = alpha;
   p.E = E; p.lde = lde;
-  p.part = nullptr; p.per_slice = 0;
+  p.part = nullptr; p.per_slice = 0; p.slices = 1;
   const int ntiles = plan_tiles(p);
   if (E)
     hipLaunchKernelGGL(gemm_nt_kernel<true>, dim3((unsigned)ntiles), dim3(kThreads), 0, stream, p);
@@ -683,6 +687,7 @@ hipError_t launch_gemm_nt_multi(const uint16_t* A, int64_t lda, const uint16_t* 
   const GemmSplit sp = gemm_split(M, N, K);
   p.part = part;
   p.per_slice = sp.per;
+  p.slices = sp.S;
   if (sp.S > 1 && M * lda * 2 < four_gb) {
     p.tiles_n = (int)((N + TN - 1) / TN);
     const int64_t tiles = ((M + TM / 2 - 1) / (TM / 2)) * p.tiles_n;

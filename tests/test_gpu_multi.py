@@ -268,6 +268,30 @@ def test_order_of_rows(api, M):
     assert torch.equal(c.bwd(T=T2)[0], dX[p])
 
 
+@pytest.mark.parametrize("M,r,A", [(150, 24, 40), (300, 72, 3), (260, 8, 130)])
+def test_order_of_rows_in_slices(api, M, r, A):
+    """The same where the reduction is cut into slices, against the oracle too."""
+    import torch
+
+    label = f"multi order in slices M={M} r={r} A={A}"
+    say(label)
+    c = Case(api, M, 4096, 264, r, A, "rows")
+    c.check_fwd(label)
+    Y = c.fwd()[0]
+    p = torch.from_numpy(np.random.default_rng(2).permutation(M)).cuda()
+    for k in ("X", "ids"):
+        c.d[k] = c.d[k][p].contiguous()
+    assert torch.equal(c.fwd()[0], Y[p])
+
+
+@pytest.mark.parametrize("M,r,A", [(150, 24, 40), (200, 72, 3), (330, 8, 130)])
+def test_backward_in_slices(api, M, r, A):
+    label = f"multi bwd in slices M={M} r={r} A={A}"
+    say(label)
+    c = Case(api, M, 256, 4096, r, A, "rows")
+    c.check_bwd(label, c.check_fwd(label))
+
+
 @pytest.mark.parametrize("M", [1, 7, 16, 40, 128, 200])
 def test_rows_without_an_adapter(api, M):
     """They equal the layer whose second factor is zero, whatever the other rows do."""

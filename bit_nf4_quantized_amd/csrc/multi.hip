@@ -504,12 +504,18 @@ __device__ __forceinline__ int64_t tn_at(int64_t w, int j, int64_t W, int in) {
 // instead of 67.0: at the larger size the card's power sets the call's time.
 constexpr int kTnStages = 3;
 
-// Dynamic LDS: the ring, then the piece's rows; for few rows M the stages and
-// rows that a piece of M rows has, so that more workgroups fit in a CU. With
-// that, and only the rows of a short piece copied and multiplied: 88 rows of 44
-// rank-8 adapters, 9280 -> 3776, 37.6 -> 28.8 us.
-int tn_stages(int64_t rows) { return (int)(rows <= SK ? 1 : rows <= 2 * SK ? 2 : kTnStages); }
-int tn_lds(int64_t rows) { return tn_stages(rows) * kTnStageBytes + (int)(rows < kTnRows ? rows : kTnRows) * 4; }
+// Dynamic LDS: the ring, then the piece's rows. The ring has the stages that a
+// piece of `rows` rows has, and one where segments of one stage are expected
+// (adapters enough for all rows at 64 each): then more workgroups fit in a CU,
+// which hides what a short piece waits for. A longer piece is right with it too.
+// 88 rows of 44 rank-8 adapters, 9280 -> 3776, 37.6 -> 23.7 us (with only the rows
+// of a short piece copied and multiplied); 926 rows of 32 rank-120 adapters,
+// 3264 -> 7360, 88 -> 54.
+int tn_stages(int64_t rows, int64_t M, int64_t segs) {
+  if (rows <= SK || M <= SK * segs) return 1;
+  return rows <= 2 * SK ? 2 : kTnStages;
+}
+int tn_lds(int64_t rows, int stages) { return stages * kTnStageBytes + (int)(rows < kTnRows ? rows : kTnRows) * 4; }
 
 template <bool RANKS_IN>
 __device__ __forceinline__ void tn_body(const TnArgs& p, int bx, char* ring) {
@@ -546,8 +552,7 @@ __device__ __forceinline__ void tn_body(const TnArgs& p, int bx, char* ring) {
   __syncthreads();
   const int n = pc.hi - pc.lo;
   // a single stage: only the MFMA steps that have rows
-  auto issue = [&](int st, int end) {
-    char* buf = ring + (st % kTnStages) * kTnStageBytes;
+  auto copy_stage = [&](int st, int end, char* buf) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (4 * (4 * wave + i) >= end) continue;        // uniform
@@ -563,6 +568,7 @@ __device__ __forceinline__ void tn_body(const TnArgs& p, int bx, char* ring) {
              buf + kTnLBytes + (2 * wave + i) * 1024);
     }
   };
+  auto issue = [&](int st, int end) { copy_stage(st, end, ring + (st % kTnStages) * kTnStageBytes); };
 
   f32x16_t acc[2];
 #pragma unroll
@@ -590,7 +596,16 @@ __device__ __forceinline__ void tn_body(const TnArgs& p, int bx, char* ring) {
                         : __builtin_amdgcn_mfma_f32_32x32x16_bf16(s, l, acc[t], 0, 0, 0);
     }
   };
-  if (ns == 1) {
+  if (p.ring == kTnStageBytes) {                    // one stage in LDS
+    for (int st = 0; st < ns; ++st) {
+      const int left = n - st * SK, end = left < SK ? (left + 15) & ~15 : SK;
+      if (st > 0) __syncthreads();                  // the stage before has been read
+      copy_stage(st, end, ring);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      for (int kk = 0; 16 * kk < end; ++kk) multiply(ring, kk);
+    }
+  } else if (ns == 1) {
     issue(0, (n + 15) & ~15);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
@@ -994,7 +1009,7 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
   const int rows = tn_rows(M, K, N, r);
   float* part2 = part + tn_part_floats(M, K, N, K, r, A);
   const int64_t most = M < rows ? M : rows;          // rows of a piece
-  const int ring = tn_stages(most) * kTnStageBytes;
+  const int ring = tn_stages(most, M, segs) * kTnStageBytes;
   const TnArgs g1 = tn_args(X, K, sU, rp, true, r, rows, ring, nullptr, rv, part, dL1, grad_bf16);
   const TnArgs g2 = tn_args(dY, N, T, r, false, r, rows, ring, scale, rv, part2, dL2, grad_bf16);
   const int64_t pieces = M / rows + segs, tiles = cdiv(K, SM) + cdiv(N, SM);
@@ -1003,11 +1018,11 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
   static bool attr_set = false;  // raise the dynamic-LDS limit once (idempotent)
   if (!attr_set) {
     (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&multi_tn_kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                              tn_lds(kTnRows));
+                              tn_lds(kTnRows, kTnStages));
     (void)hipGetLastError();  // a refusal shows up as a launch error below
     attr_set = true;
   }
-  hipLaunchKernelGGL(multi_tn_kernel, grid, dim3(kThreads), tn_lds(most), stream, g1, (int)cdiv(K, SM), g2, (int)pieces, sum);
+  hipLaunchKernelGGL(multi_tn_kernel, grid, dim3(kThreads), tn_lds(most, ring / kTnStageBytes), stream, g1, (int)cdiv(K, SM), g2, (int)pieces, sum);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int b1 = finish_blocks(K * r), b2 = finish_blocks(N * r);

@@ -430,8 +430,8 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
 
 // K-slices: as many workgroups as are resident at once (one or two per CU by
 // LDS), in slices of whole stages; at most 8, whose sum in the finish costs what
-// more would save here (whole call: 24 rows 4096 -> 4096 23.9 us with 8, 30.5 with
-// 16; 15 rows 6080 -> 1368 25.3 / 27.0, with 4 27.8).
+// more would save here (whole call with 8 / 16: 24 rows 4096 -> 4096 18.8 / 22.4 us,
+// 82 rows 5760 -> 1288 28.0 / 28.9, 121 rows 10432 -> 1104 42.6 / 40.5).
 struct BaseSplit {
   int slice, S;
 };

@@ -249,7 +249,7 @@ def _need(t, dtype, shape, name):
 
 
 _TENSORS = None
-_F32, _BF16, _I32, _I64, _F64 = range(5)   # dtype numbers of the tensor module
+_F32, _BF16, _I32, _I64, _F64, _U8 = range(6)   # dtype numbers of the tensor module
 
 
 def _tensors():
@@ -264,6 +264,21 @@ def _tensors():
             raise RuntimeError(f"_tensors.so is not built; run `python {os.path.join(HERE, 'build.py')}` ({e})") from e
         _TENSORS = mod
     return _TENSORS
+
+
+def _fill(dev, tensors, specs):
+    """``tensors`` with a new one of (dtype number, shape) from ``specs`` for each None."""
+    want = [x for t, s in zip(tensors, specs) if t is None for x in s]
+    new = iter(_tensors().empties(dev, *want)) if want else None
+    return [next(new) if t is None else t for t in tensors]
+
+
+def _workspace_of(ws, nbytes):
+    """The address and size of a workspace, which must hold ``nbytes``."""
+    size = ws.numel() * ws.element_size()
+    if size < nbytes:
+        raise ValueError("workspace too small")
+    return ws.data_ptr(), size
 
 
 def _raw_stream(stream):
@@ -432,12 +447,13 @@ def qlora_preference_loss(logits, labels, ref_logps, beta: float, label_smoothin
         elif dlogits.dtype != logits.dtype or dlogits.shape != logits.shape or dlogits.get_device() != dev:
             raise ValueError("dlogits must have the logits' dtype, shape and device")
         ldd, dp = _row_stride(dlogits, "dlogits"), dlogits.data_ptr()
-    loss, rewards, logps = ref_logps.new_empty(1), ref_logps.new_empty(S), ref_logps.new_empty((S, T))
-    ws = _workspace(qlora_preference_workspace(S // 2, T, V), logits.device, workspace)
+    need = qlora_preference_workspace(S // 2, T, V)
+    loss, rewards, logps, ws = _fill(dev, (None, None, None, workspace),
+                                     ((_F32, (1,)), (_F32, (S,)), (_F32, (S, T)), (_U8, (max(need, 256),))))
     _check(_load().qlora_preference_loss(logits.data_ptr(), dt, S // 2, T, V, ld, yp, rp, float(beta),
                                          float(label_smoothing), float(grad_scale), loss.data_ptr(),
-                                         rewards.data_ptr(), logps.data_ptr(), dp, ldd, ws.data_ptr(),
-                                         ws.numel() * ws.element_size(), _raw_stream(stream)),
+                                         rewards.data_ptr(), logps.data_ptr(), dp, ldd,
+                                         *_workspace_of(ws, need), _raw_stream(stream)),
            "qlora_preference_loss")
     return PreferenceOut(loss, rewards, logps, dlogits)
 
@@ -495,13 +511,12 @@ def qlora_clip_grad_norm_batch(grads, max_norm: float, coef=None, norm=None, wor
     gd, dtype = _grad_dtype(grads)
     dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
     gp, sizes = _tensors().addresses(grads, dtype, dev.index if grads else -1, "grads")
-    coef = coef if coef is not None else torch.empty(1, dtype=torch.float32, device=dev)
-    norm = norm if norm is not None else torch.empty(1, dtype=torch.float64, device=dev)
+    need = QLORA_CLIP_WORKSPACE_BYTES
+    coef, norm, ws = _fill(dev.index, (coef, norm, workspace), ((_F32, (1,)), (_F64, (1,)), (_U8, (need,))))
     address = _tensors().address
     cp, np_ = address(coef, _F32, (1,), dev.index, "coef"), address(norm, _F64, (1,), dev.index, "norm")
-    ws = _workspace(QLORA_CLIP_WORKSPACE_BYTES, dev, workspace)
-    _check(_load().qlora_clip_grad_norm_batch(len(grads), gp, gd, sizes, float(max_norm), cp, np_, ws.data_ptr(),
-                                              ws.numel() * ws.element_size(), _raw_stream(stream)),
+    _check(_load().qlora_clip_grad_norm_batch(len(grads), gp, gd, sizes, float(max_norm), cp, np_,
+                                              *_workspace_of(ws, need), _raw_stream(stream)),
            "qlora_clip_grad_norm_batch")
     return coef, norm
 
@@ -963,17 +978,15 @@ def qlora_linear_multi_fwd(q: NF4Tensor, X, row_adapter, L1, L2, scale, want_T: 
     returns (Y, T) with T = bf16(X[m] L1[a]) or None."""
     (M, K, N, r, A, dev), xp, ip, p1, p2, sp = _multi_operands(q, X, row_adapter, L1, L2, scale)
     address = _tensors().address
-    if Y is None:
-        Y = X.new_empty((M, N))
-    yp = address(Y, _BF16, (M, N), dev, "Y")
+    need = qlora_linear_multi_workspace(M, K, N, r, A)
     if want_T and T_out is None:
         T_out = X.new_empty((M, r))
+    Y, ws = _fill(dev, (Y, workspace), ((_BF16, (M, N)), (_U8, (max(need, 256),))))
+    yp = address(Y, _BF16, (M, N), dev, "Y")
     tp = None if T_out is None else address(T_out, _BF16, (M, r), dev, "T_out")
     st = q.struct()
-    ws = _workspace(qlora_linear_multi_workspace(M, K, N, r, A), X.device, workspace)
-    _check(_load().qlora_linear_multi_fwd(ctypes.byref(st), xp, M, ip, A, p1, p2, r, sp, yp, tp, ws.data_ptr(),
-                                          ws.numel() * ws.element_size(), _raw_stream(stream)),
-           "qlora_linear_multi_fwd")
+    _check(_load().qlora_linear_multi_fwd(ctypes.byref(st), xp, M, ip, A, p1, p2, r, sp, yp, tp,
+                                          *_workspace_of(ws, need), _raw_stream(stream)), "qlora_linear_multi_fwd")
     return Y, T_out
 
 

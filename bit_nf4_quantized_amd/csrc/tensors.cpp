@@ -12,7 +12,10 @@
 //       the addresses and element counts of a list of tensors, as arrays of
 //       int64; with numel (such an array) the counts must equal it
 //
-// dtype: 0 float32, 1 bfloat16, 2 int32, 3 int64, 4 float64. Failed checks raise TypeError
+//   empties(device, dtype, shape, dtype, shape, ...) -> tuple
+//       new device tensors (1.3 us each from Python)
+//
+// dtype: 0 float32, 1 bfloat16, 2 int32, 3 int64, 4 float64, 5 uint8. Failed checks raise TypeError
 // or ValueError; C++ exceptions end here as RuntimeError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -23,14 +26,16 @@
 #include <string>
 #include <vector>
 
+#include <ATen/ops/empty.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 namespace {
 
 const c10::ScalarType kTypes[] = {c10::ScalarType::Float, c10::ScalarType::BFloat16, c10::ScalarType::Int,
-                                  c10::ScalarType::Long, c10::ScalarType::Double};
-constexpr int kTypeCount = 5;
+                                  c10::ScalarType::Long, c10::ScalarType::Double,   c10::ScalarType::Byte};
+constexpr int kTypeCount = 6;
 
 // nullptr after setting a Python error
 const at::Tensor* tensor_of(PyObject* o, int dtype, long device, const char* name) {
@@ -149,11 +154,40 @@ PyObject* stream(PyObject*, PyObject*) {
   }
 }
 
+PyObject* empties(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS   // an allocator's error stays torch's own
+  if (n % 2 == 0) throw torch::TypeError("empties(device, dtype, shape, ...)");
+  const long device = PyLong_AsLong(args[0]);
+  if (PyErr_Occurred()) throw python_error();
+  const auto on = c10::TensorOptions().device(c10::Device(c10::DeviceType::CUDA, (c10::DeviceIndex)device));
+  std::vector<at::Tensor> made;
+  std::vector<int64_t> sizes;
+  for (Py_ssize_t i = 1; i < n; i += 2) {
+    const long dtype = PyLong_AsLong(args[i]);
+    if (PyErr_Occurred()) throw python_error();
+    if (dtype < 0 || dtype >= kTypeCount || !PyTuple_Check(args[i + 1]))
+      throw torch::TypeError("empties(device, dtype, shape, ...)");
+    sizes.clear();
+    for (Py_ssize_t k = 0; k < PyTuple_GET_SIZE(args[i + 1]); ++k) {
+      sizes.push_back(PyLong_AsLongLong(PyTuple_GET_ITEM(args[i + 1], k)));
+      if (PyErr_Occurred()) throw python_error();
+    }
+    made.push_back(at::empty(sizes, on.dtype(kTypes[dtype])));
+  }
+  PyObject* out = PyTuple_New((Py_ssize_t)made.size());
+  if (!out) throw python_error();
+  for (size_t i = 0; i < made.size(); ++i) PyTuple_SET_ITEM(out, (Py_ssize_t)i, THPVariable_Wrap(made[i]));
+  return out;
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef kMethods[] = {
     {"address", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(address)), METH_FASTCALL,
      "address(tensor, dtype, shape, device, name): the checked device address"},
     {"addresses", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(addresses)), METH_FASTCALL,
      "addresses(list, dtype, device, name, numel=None): checked addresses and sizes"},
+    {"empties", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(empties)), METH_FASTCALL,
+     "empties(device, dtype, shape, ...): new device tensors"},
     {"stream", stream, METH_NOARGS, "stream(): the current stream of the current device"},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -18,7 +18,7 @@
 //                              an adapter's L2 is read once per 16 rows
 // At these sizes the weight stream (0.52 B per weight) and the live adapters
 // are all there is to read; the launches' latency is the rest. 96 rows of 24
-// rank-16 adapters and of none, 4096 -> 11008: T 5.6 us, base 27.9, finish 8.1;
+// rank-16 adapters and of none, 4096 -> 11008: T 5.3 us, base 27.7, finish 8.3;
 // the call 40 us. (In the finish, loading the base's first two slices before T's
 // took 10.3 us: 186 registers leave two waves per SIMD.)
 #include "common.h"

@@ -38,7 +38,7 @@
 // That case: adamw_batch_kernel 4 x 152 us (18 B a value, 4.7 TB/s),
 // sumsq_batch_kernel 2 x 70 us (4.6 TB/s), clip_finalize_kernel 5 us. 14
 // tensors of 0.62 M values in all (fp32 state): 7.1 + 4.5 + 2.3 us of kernels
-// in 21 us, which the host's two calls and three launches bound. A maximum
+// in 20 us, which the host's two calls and three launches bound. A maximum
 // without LDS exchanges (lane rotations) changed neither (683 / 688 us).
 #include "adam.h"
 #include "common.h"

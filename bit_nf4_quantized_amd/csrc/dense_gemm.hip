@@ -177,6 +177,35 @@ __device__ __forceinline__ const uint16_t* uniform(const uint16_t* p) {
 
 __device__ __forceinline__ int lds_off(int row, int chunk) { return row * TK + ((chunk ^ swz(row)) << 3); }
 
+// The products with an adapter's infinities and NaN, for its rows of a tile
+// whose sums are stored (see MultiSlab). Rare, and slow. The whole workgroup.
+template <typename C>
+__device__ __forceinline__ void add_bad(const DenseArgs& p, const MultiSlab& slab, int64_t m0, int64_t m1, int64_t n0,
+                                        int seg0, int seg1, C* out, int64_t ldc) {
+  __syncthreads();                                    // the tile is stored
+  const int pack = slab.pack;
+  for (int k = seg0; k < seg1; ++k) {
+    if (slab.bad[k] == 0) continue;
+    const int64_t lo = slab.rv.start[k] > m0 ? slab.rv.start[k] : m0;
+    const int64_t hi = slab.rv.start[k + 1] < m1 ? slab.rv.start[k + 1] : m1;
+    const uint16_t* raw = slab.raw + (int64_t)slab.rv.adapter[k] * slab.raw_stride;
+    for (int64_t i = threadIdx.x; i < (hi - lo) * TN; i += kThreads) {
+      const int64_t row = slab.rv.perm[lo + i / TN], col = n0 + i % TN;
+      if (col >= p.N) continue;
+      const uint16_t* t = p.A2 + row * p.ld2 + k % pack * slab.width;
+      float sum = 0.0f;
+      for (int j = 0; j < slab.r; ++j) {
+        const uint16_t b = raw[col * slab.raw_col + j * slab.raw_j];
+        if ((b & 0x7F80u) == 0x7F80u) sum += bf16_to_f32(t[j]) * bf16_to_f32(b);
+      }
+      if (sum == 0.0f) continue;                      // no such value in this column
+      C* c = out + row * ldc + col;
+      if constexpr (sizeof(C) == 2) *c = f32_to_bf16(bf16_to_f32(*c) + sum);
+      else *c += sum;
+    }
+  }
+}
+
 // One TMX x TN output tile at (m0, n0). smem holds the stage tiles: two A
 // buffers, then three B buffers, kStageElems elements each. MULTI: the tile's
 // rows are rows m0 .. of the grouped order, and the slab has the K2 columns of
@@ -200,9 +229,16 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p_all, const MultiSla
   const int nmain = (int)(p.K / TK);
   int nslab = (int)(p.K2 / TK), group0 = 0, segs = 0;
   const int per_group = nslab;                      // slab stages per group (MULTI)
+  int first_seg = 0;
+  bool any_bad = false;                             // uniform
   if constexpr (MULTI) {
     const RouteRange rg = route_range(slab.rv, (int)m0, (int)m0 + TMX);
     group0 = rg.lo / slab.pack;
+    first_seg = rg.lo;
+    for (int base = rg.lo; base < rg.hi; base += 64) {
+      const int k = base + lane;
+      any_bad = any_bad || __ballot(k < rg.hi && slab.bad[k < rg.hi ? k : rg.lo] != 0) != 0;
+    }
     int groups = rg.hi > rg.lo ? (rg.hi - 1) / slab.pack - group0 + 1 : 0;
     if constexpr (SPLIT) {  // group g goes to slice g mod S: the same sums wherever a row lies
       const int skip = (z - group0 % p.slices + p.slices) % p.slices;
@@ -246,8 +282,7 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p_all, const MultiSla
     return in ? offA2.off[j] : (uint32_t)((slab.zero_row * p.ld2 + chunk * 8) * 2);
   };
   auto slab_b = [&](int g) -> const uint16_t* {
-    const int i = slab.by_adapter ? __builtin_amdgcn_readfirstlane(slab.rv.adapter[g]) : g;
-    return p.B2 + (int64_t)i * slab.b2_stride;
+    return p.B2 + (int64_t)g * slab.b2_stride;
   };
   // WIDE: the lane's rows of A
   const uint16_t* rowA[WIDE ? S::kIpwA : 1];
@@ -443,6 +478,9 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p_all, const MultiSla
       }
       __builtin_amdgcn_s_waitcnt(0xc07f);  // reads of this quarter done before the next overwrites it
     }
+    if constexpr (SPLIT) {
+      if (any_bad && z == 0) add_bad(p, slab, m0, m0 + TMX, n0, first_seg, segs, p.part, p.N);
+    }
     return;
   }
 
@@ -485,6 +523,9 @@ __device__ __forceinline__ void gemm_tile(const DenseArgs& p_all, const MultiSla
         *reinterpret_cast<u32x4_t*>(p.C + (MULTI ? (int64_t)perm[row] : row) * p.ldc + col) = val;
     }
     __builtin_amdgcn_s_waitcnt(0xc07f);  // reads of this half done before the next half overwrites it
+  }
+  if constexpr (MULTI) {
+    if (any_bad) add_bad(p, slab, m0, m0 + TMX, n0, first_seg, segs, p.C, p.ldc);
   }
 }
 

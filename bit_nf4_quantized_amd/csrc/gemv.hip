@@ -830,6 +830,7 @@ __global__ __launch_bounds__(64 * W) void gemv_lut_kernel(NF4View Wt, NF4Table t
       const int a = __builtin_amdgcn_readlane(id, (int)__builtin_ctz(lead));
       if (!first) load_l2(L2 + (int64_t)a * r * N);
       const float s = mi.scale[a];
+      f32x4_t own = {0.0f, 0.0f, 0.0f, 0.0f};        // apart: another row's zeros times an infinity of this L2 are NaN
 #pragma unroll
       for (int c = 0; c < kLoraChunks; ++c) {
         if (32 * c >= rp) continue;
@@ -838,9 +839,10 @@ __global__ __launch_bounds__(64 * W) void gemv_lut_kernel(NF4View Wt, NF4Table t
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= s;
         const u32x4_t b = id == a && 32 * c + 8 * grp < r ? packed8(v) : none;   // other rows' T may be unset
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, packed(c)),
-                                                       __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+        own = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, packed(c)),
+                                                       __builtin_bit_cast(bf16x8_t, b), own, 0, 0, 0);
       }
+      if (id == a) acc += own;
     }
   }
 

@@ -264,16 +264,22 @@ hipError_t launch_gemm_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int
 // C[m] = bf16(A[m] B^T + A2[m] B2_g^T) for rows of segment k, A[m] B^T for rows
 // of none. Segments are packed `pack` to a group g = k / pack: A2 [M][ld2] holds
 // a row's values in its segment's columns and zeros in the others', B2_g [N][ld2]
-// the operands of the group's segments side by side, at g b2_stride (by_adapter,
-// with pack = 1: at a b2_stride). Row zero_row of A2 is zeros. K and ld2 are
+// the operands of the group's segments side by side, at g b2_stride. Row zero_row of A2 is zeros. K and ld2 are
 // multiples of 64; A2 (the zero row too) below 4 GB, B and B2_g below 2 GB. C is
 // dense [M][N].
 struct MultiSlab {
   RouteView rv;
   int pack;
-  bool by_adapter;
   int64_t zero_row;
   int64_t b2_stride;
+  // Infinities and NaN of an adapter: its operand in B2 has zeros instead (a
+  // zero of another segment's row times them would be NaN), bad[k] says that
+  // segment k has some, and its rows get them from the adapter itself:
+  // raw[a raw_stride + column raw_col + j raw_j], columns of width values in A2.
+  const int32_t* bad;
+  const uint16_t* raw;
+  int64_t raw_stride, raw_col, raw_j;
+  int r, width;
 };
 // `later`: what is left of a product that is cut into reduction slices (S > 1)
 // goes there for the caller to add beside other work; NULL: added here.
@@ -286,7 +292,7 @@ size_t gemm_multi_partial_bytes(int64_t M, int64_t N, int64_t K);   // of part, 
 constexpr int64_t kMultiMaxRows = (int64_t)1 << 22;   // 32-bit offsets of the rows' [M][256] rank buffers
 constexpr int kMultiMaxAdapters = 4096;
 struct MultiWorkspace {
-  size_t perm_off, start_off, adapter_off, count_off, slot_off;   // the grouping (RouteView), segment of an adapter
+  size_t perm_off, start_off, adapter_off, count_off, slot_off, bad_off;   // the grouping (RouteView), segment of an adapter, its flag
   size_t st_off;     // bf16 [M + 1][rp]: s T or s U in the segment's columns, the last row zero
   size_t t_off;      // bf16 [M][r]: T, when the caller has none
   size_t b2_off;     // bf16 per group of segments: L2^T [N][rp], or L1 [K][rp] with padded columns

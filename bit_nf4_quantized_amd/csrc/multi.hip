@@ -34,7 +34,7 @@
 //   360 (1.04 PFLOP/s); the call 370
 //   8192 rows of 16, backward: prep 45 (113 MB, 2.5 TB/s), NT 54 (180 MB, 3.3
 //   TB/s), sum 5.8, GEMM 588 (1.26 PFLOP/s), TN 86 (247 MB, 2.9 TB/s), finish
-//   5.5; the call 724 to 731
+//   5.5; the call 744
 //   391 rows of 4 rank-32 adapters, 4096 -> 4096, backward: prep 12, NT 7.4,
 //   sum 6.1, GEMM 27 (0.49 PFLOP/s), TN 9.9, finish 5.4; the call 65
 #include "common.h"
@@ -74,6 +74,7 @@ struct RouteArgs {
   int32_t* adapter;
   int32_t* count;
   int32_t* slot;          // an adapter's segment, where it has rows
+  int32_t* bad;           // per segment: its adapter's laid-out operand has infinities or NaN
 };
 
 // Workgroup a < A: adapter a; workgroup A: the rows without one. Each reads
@@ -113,6 +114,7 @@ __device__ __forceinline__ void route_body(const RouteArgs& p, int a) {
       p.adapter[rank] = a;
       p.start[rank] = below;
       p.slot[a] = rank;
+      p.bad[rank] = 0;
     }
   }
   if (mine == 0) return;                            // uniform
@@ -171,6 +173,7 @@ struct LayArgs {
   uint16_t* out;          // per group [W][rp]; columns past a segment's r, and of segments that are none, zero
   int64_t W;
   int r, rp, blocks;      // blocks per group
+  int32_t* bad;           // set where a segment has infinities or NaN; they are laid out as zeros
   bool transpose;
 };
 
@@ -183,6 +186,19 @@ __device__ __forceinline__ LayColumn lay_column(const LayArgs& p, const RouteVie
   const Packing pk = packing_of(p.r);
   const int s = c / pk.width, k = g * pk.pack + s, j = c - s * pk.width;
   return LayColumn{k, j, k >= rv.count[0] || j >= p.r};
+}
+
+// Eight values of segment k with infinities and NaN noted and zeroed.
+__device__ __forceinline__ u32x4_t lay_finite(const LayArgs& p, int k, u32x4_t v) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool lo = (v[i] & 0x7F80u) == 0x7F80u, hi = (v[i] & 0x7F800000u) == 0x7F800000u;
+    v[i] = (lo ? 0u : v[i] & 0xFFFFu) | (hi ? 0u : v[i] & 0xFFFF0000u);
+    bad = bad || lo || hi;
+  }
+  if (bad) p.bad[k] = 1;                            // the same value from every thread
+  return v;
 }
 
 // L2 of group g's segments transposed side by side: 64 output rows n and 64
@@ -201,7 +217,8 @@ __device__ __forceinline__ void lay_transposed(const LayArgs& p, const RouteView
     const LayColumn col = lay_column(p, rv, g, j0 + j);
     u32x4_t v = {0u, 0u, 0u, 0u};
     if (!col.none && n0 + c < N)
-      v = *reinterpret_cast<const u32x4_t*>(p.src + ((int64_t)rv.adapter[col.segment] * p.r + col.rank) * N + n0 + c);
+      v = lay_finite(p, col.segment, *reinterpret_cast<const u32x4_t*>(
+              p.src + ((int64_t)rv.adapter[col.segment] * p.r + col.rank) * N + n0 + c));
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e) tile[c + e][j] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
@@ -229,7 +246,8 @@ __device__ __forceinline__ void lay_padded(const LayArgs& p, const RouteView& rv
   const LayColumn col = lay_column(p, rv, g, c);
   u32x4_t v = {0u, 0u, 0u, 0u};
   if (!col.none)
-    v = *reinterpret_cast<const u32x4_t*>(p.src + ((int64_t)rv.adapter[col.segment] * p.W + row) * p.r + col.rank);
+    v = lay_finite(p, col.segment, *reinterpret_cast<const u32x4_t*>(
+            p.src + ((int64_t)rv.adapter[col.segment] * p.W + row) * p.r + col.rank));
   *reinterpret_cast<u32x4_t*>(p.out + ((int64_t)g * p.W + row) * p.rp + c) = v;
 }
 
@@ -793,10 +811,11 @@ MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, in
   L.adapter_off = take(segs * 4);
   L.count_off = take(4);
   L.slot_off = take(A * 4);
+  L.bad_off = take(segs * 4);
   L.st_off = take((M + 1) * rp * 2);   // s T or s U, and a row of zeros
   L.t_off = take(bwd ? M * r * 2 : 0);
   const int64_t groups = cdiv(segs, packing_of(r).pack);
-  const int64_t wide = bwd ? (r % 64 ? groups * K * rp * 2 : 0) : groups * N * rp * 2;
+  const int64_t wide = bwd ? groups * K * rp * 2 : groups * N * rp * 2;
   L.b2_off = take(wide);
   L.wd_off = take(K * np * 2);
   L.dy_off = take(bwd && N % 64 ? M * np * 2 : 0);
@@ -829,6 +848,7 @@ RouteArgs route_args(const int32_t* ids, int64_t M, int A, char* ws, const Multi
   p.adapter = reinterpret_cast<int32_t*>(ws + L.adapter_off);
   p.count = reinterpret_cast<int32_t*>(ws + L.count_off);
   p.slot = reinterpret_cast<int32_t*>(ws + L.slot_off);
+  p.bad = reinterpret_cast<int32_t*>(ws + L.bad_off);
   return p;
 }
 
@@ -938,10 +958,10 @@ hipError_t multi_forward(const NF4View& W, const NF4Table& tab, const uint16_t* 
   e = launch_nt(nullptr, 0, &t, sp.Z, M, A, stream);
   if (e != hipSuccess) return e;
   const SumArgs s{part, part, sp.Z, sp.Z, M, r, rp, ids, A, scale, ra.slot, sT, T_out};
-  const LayArgs lay{L2, l2t, N, r, rp, (int)(cdiv(N, 64) * (rp / 64)), true};
+  const LayArgs lay{L2, l2t, N, r, rp, (int)(cdiv(N, 64) * (rp / 64)), ra.bad, true};
   e = launch_sum(s, lay, segs, rv, stream);
   if (e != hipSuccess) return e;
-  const MultiSlab slab{rv, packing_of(r).pack, false, M, N * rp};
+  const MultiSlab slab{rv, packing_of(r).pack, M, N * rp, ra.bad, L2, N * r, 1, N, r, packing_of(r).width};
   return timed(kTimeFwdGemm, stream,
                [&] { return launch_gemm_nt_multi(X, K, wd, K, M, N, K, sT, l2t, rp, slab, Y, part, nullptr, stream); });
 }
@@ -980,10 +1000,9 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
   if (e != hipSuccess) return e;
   uint16_t* tbuf = T ? nullptr : reinterpret_cast<uint16_t*>(base + L.t_off);
   uint16_t* l1p = reinterpret_cast<uint16_t*>(base + L.b2_off);
-  const bool padded = dX && rp != r;
   const SumArgs s{upart, part, su.Z, st.Z, M, r, rp, ids, A, scale, ra.slot, sU, tbuf};
-  const LayArgs lay{L1, l1p, K, r, rp, (int)cdiv(K * rp / 8, 256), false};
-  e = launch_sum(s, lay, padded ? segs : 0, rv, stream);
+  const LayArgs lay{L1, l1p, K, r, rp, (int)cdiv(K * rp / 8, 256), ra.bad, false};
+  e = launch_sum(s, lay, dX ? segs : 0, rv, stream);
   if (e != hipSuccess) return e;
   if (!T) T = tbuf;
 
@@ -999,9 +1018,9 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
       if (e != hipSuccess) return e;
       dYp = p;
     }
-    const MultiSlab slab{rv, packing_of(r).pack, !padded, M, K * rp};
+    const MultiSlab slab{rv, packing_of(r).pack, M, K * rp, ra.bad, L1, K * r, r, 1, r, packing_of(r).width};
     e = timed(kTimeDxGemm, stream, [&] {
-      return launch_gemm_nt_multi(dYp, np, wdt, np, M, K, np, sU, padded ? l1p : L1, rp, slab, dX, gpart, &sum, stream);
+      return launch_gemm_nt_multi(dYp, np, wdt, np, M, K, np, sU, l1p, rp, slab, dX, gpart, &sum, stream);
     });
     if (e != hipSuccess) return e;
   }

@@ -29,7 +29,8 @@ extern "C" {
  * computed as qlora_linear_fwd / _bwd compute them for one adapter (bf16
  * operands, fp32 accumulation; s T and s U are rounded to bf16 before their
  * second product, outputs once). Rows may come in any order. An adapter
- * without rows gets zero gradients. Sums run in a fixed order.
+ * without rows gets zero gradients. Sums run in a fixed order. Infinities and
+ * NaN of one row or one adapter reach no other row.
  *   W            host struct of the quantised weight [N][K].
  *   X            device bf16 [M][K];  dY device bf16 [M][N].
  *   row_adapter  device int32 [M].

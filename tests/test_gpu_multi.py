@@ -308,6 +308,48 @@ def test_rows_without_an_adapter(api, M):
     assert torch.equal(c.fwd()[0][bare], Y[bare])
 
 
+@pytest.mark.parametrize("M,K,r", [(1, 512, 16), (7, 512, 16), (16, 512, 64), (13, 640, 24), (60, 512, 16), (128, 320, 72),
+                                   (200, 512, 8), (300, 512, 64), (150, 4096, 16), (700, 256, 72)])
+def test_an_adapter_that_diverged(api, M, K, r):
+    """Infinities and NaN of one adapter's second factor reach its own rows alone, and there their own columns."""
+    import torch
+
+    say(f"multi diverged M={M} K={K} r={r}")
+    c = Case(api, M, K, 264, r, 4, "rows")
+    c.d["ids"][0] = 1
+    Y = c.fwd()[0]
+    c.d["L2"][1, 3, 5] = float("inf")
+    c.d["L2"][1, 2, 9] = float("nan")
+    c.d["L2"][1, 0, 200] = float("-inf")
+    Y2 = c.fwd()[0]
+    own = c.d["ids"] == 1
+    assert torch.equal(Y2[~own], Y[~own])
+    hit = torch.zeros(264, dtype=torch.bool, device="cuda")
+    hit[[5, 9, 200]] = True
+    assert torch.equal(Y2[:, ~hit], Y[:, ~hit])
+    assert not torch.isfinite(Y2[own][:, hit]).any() and torch.isnan(Y2[own][:, 9]).all()
+
+
+@pytest.mark.parametrize("M,N,r", [(5, 264, 16), (200, 264, 64), (300, 512, 8), (150, 4096, 16), (150, 4096, 64), (700, 256, 72)])
+def test_an_adapter_that_diverged_backward(api, M, N, r):
+    import torch
+
+    say(f"multi diverged bwd M={M} N={N} r={r}")
+    c = Case(api, M, 320, N, r, 4, "rows")
+    c.d["ids"][0] = 1
+    T = c.fwd(want_T=True)[1]
+    dX = c.bwd(T=T)[0]
+    c.d["L1"][1, 6, 3] = float("inf")
+    c.d["L1"][1, 70, 2] = float("nan")
+    dX2 = c.bwd(T=T)[0]
+    own = c.d["ids"] == 1
+    assert torch.equal(dX2[~own], dX[~own])
+    hit = torch.zeros(320, dtype=torch.bool, device="cuda")
+    hit[[6, 70]] = True
+    assert torch.equal(dX2[:, ~hit], dX[:, ~hit])
+    assert not torch.isfinite(dX2[own][:, hit]).any() and torch.isnan(dX2[own][:, 70]).all()
+
+
 def test_no_rows(api):
     import torch
 

@@ -43,7 +43,8 @@
 // st * L2[j][row]. The 8 lanes of a row are then added by DPP, the 8 waves'
 // row sums through LDS in a fixed order, and Y is rounded to bf16 once.
 // With an adapter per row (MULTI) the adapter is ids[0]: both kernels start at
-// its L1, L2 and scale; a token without one starts its row sums at 0. These
+// its L1, L2 and scale; a token without one starts its row sums at 0 (it reads
+// adapter 0's L2 and scale, and uses neither). These
 // variants multiply the dequantised weight itself: the table holds fp16 pairs
 // of q (off by at most 2^-12, where bf16(q) is off by 2^-9), each is multiplied
 // by a' in fp32 and rounded to bf16 once, as the standalone dequant rounds.
@@ -323,7 +324,8 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
     if (b == 0 && T_out && lrow == 0 && jw < r) T_out[jw] = f32_to_bf16(t);
     const float st = jw < r ? bf16_to_f32(f32_to_bf16(s * t)) : 0.0f;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) acc[g] = st * bf16_to_f32(l2g[g]);
+    for (int g = 0; g < NG; ++g)  // a select: st = 0 times an infinity or NaN of the L2 that was read is NaN
+      acc[g] = MULTI && !has ? 0.0f : st * bf16_to_f32(l2g[g]);
   }
   // the X copies (issued first) have landed once all but the code loads are done
   asm volatile("s_waitcnt vmcnt(%0)" :: "n"(DC * NG) : "memory");

@@ -322,10 +322,10 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
     t += __shfl_xor(t, 32, 64);
     if (MULTI && !has) t = 0.0f;
     if (b == 0 && T_out && lrow == 0 && jw < r) T_out[jw] = f32_to_bf16(t);
-    const float st = jw < r ? bf16_to_f32(f32_to_bf16(s * t)) : 0.0f;
+    const float st = bf16_to_f32(f32_to_bf16(s * t));
 #pragma unroll
-    for (int g = 0; g < NG; ++g)  // a select: st = 0 times an infinity or NaN of the L2 that was read is NaN
-      acc[g] = MULTI && !has ? 0.0f : st * bf16_to_f32(l2g[g]);
+    for (int g = 0; g < NG; ++g)  // a select: 0 times an infinity or NaN of the (clamped) L2 that was read is NaN
+      acc[g] = jw >= r || (MULTI && !has) ? 0.0f : st * bf16_to_f32(l2g[g]);
   }
   // the X copies (issued first) have landed once all but the code loads are done
   asm volatile("s_waitcnt vmcnt(%0)" :: "n"(DC * NG) : "memory");

@@ -50,3 +50,33 @@ def test_bare_token_beside_a_diverged_adapter(api, K, N, r, bare, what):
             c.d[what][2, ::3, ::5] = value
         Y2, T2 = c.fwd(want_T=True)
         assert torch.equal(Y2, Y) and (T2 == 0).all(), value
+
+
+@pytest.mark.parametrize("M,K,N,r", [(1, 512, 512, 24), (1, 512, 512, 64), (1, 320, 72, 8), (7, 512, 264, 16),
+                                     (16, 640, 264, 40), (60, 512, 264, 24), (200, 512, 264, 24), (300, 512, 264, 72)])
+def test_an_infinity_of_the_last_rank(api, M, K, N, r):
+    """Ranks past r add nothing: an infinity in the last rank is an infinity of the product's sign."""
+    import torch
+
+    say(f"multi last rank M={M} K={K} N={N} r={r}")
+    c = Case(api, M, K, N, r, 2, "one")
+    T = c.fwd(want_T=True)[1]
+    assert (T[:, r - 1] != 0).all()
+    c.d["L2"][1, r - 1, 5] = INF
+    c.d["L2"][1, r - 1, 40] = -INF
+    Y = c.fwd()[0].float()
+    sign = torch.sign(T[:, r - 1].float())
+    assert torch.equal(Y[:, 5], sign * INF) and torch.equal(Y[:, 40], sign * -INF)
+
+
+@pytest.mark.parametrize("r", [8, 24, 64])
+def test_an_infinity_of_the_last_rank_of_one_adapter(api, r):
+    """The same for the single-adapter linear's token."""
+    import torch
+
+    c = Case(api, 1, 512, 512, r, 1, "one")
+    L1, L2 = c.d["L1"][0], c.d["L2"][0]
+    T = api.qlora_linear_fwd(c.q, c.d["X"], L1, L2, 0.5, want_T=True)[1]
+    L2[r - 1, 5] = INF
+    Y = api.qlora_linear_fwd(c.q, c.d["X"], L1, L2, 0.5)[0]
+    assert torch.equal(Y[:, 5].float(), torch.sign(T[:, r - 1].float()) * INF)

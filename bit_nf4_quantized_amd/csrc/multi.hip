@@ -704,7 +704,7 @@ __device__ __forceinline__ void finish_body(const TnArgs& p, int bx, int blocks)
     first = s0 / p.rows + k;
     if (pieces == 1) return;
   }
-  const float f = p.scale ? p.scale[a] : 1.0f;
+  const float f = pieces > 0 && p.scale ? p.scale[a] : 1.0f;   // not times the zeros: an idle adapter's scale may be anything
   const int64_t total = p.W * p.r;                  // r % 8 == 0, W % 8 == 0: 4 values never leave a row
   for (int64_t i = ((int64_t)bx * 256 + threadIdx.x) * 4; i < total; i += (int64_t)blocks * 1024) {
     f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};

@@ -80,3 +80,26 @@ def test_an_infinity_of_the_last_rank_of_one_adapter(api, r):
     L2[r - 1, 5] = INF
     Y = api.qlora_linear_fwd(c.q, c.d["X"], L1, L2, 0.5)[0]
     assert torch.equal(Y[:, 5].float(), torch.sign(T[:, r - 1].float()) * INF)
+
+
+# ---- adapters without rows ----------------------------------------------------------------
+
+@pytest.mark.parametrize("M,r,A", [(5, 16, 4), (300, 24, 5), (2500, 64, 3)])
+@pytest.mark.parametrize("value", [INF, -INF, NAN, -2.0])
+def test_gradients_of_an_idle_adapter(api, M, r, A, value):
+    """Zeros, whatever its scale and factors hold."""
+    import torch
+
+    say(f"multi idle adapter M={M} r={r} A={A} scale={value}")
+    c = Case(api, M, 256, 264, r, A, "rows")
+    set_ids(c, np.where(c.ids == 1, 0, c.ids))
+    want = c.bwd()
+    c.d["scale"][1] = value
+    c.d["L1"][1, :, 0] = value
+    c.d["L2"][1, 0] = value
+    for dt in (torch.float32, torch.bfloat16):
+        got = c.bwd(grad_dtype=dt)
+        assert torch.equal(got[0], want[0])
+        for g, w in zip(got[1:], want[1:]):
+            assert torch.equal(g, w.to(dt))
+            assert not g[1].view(torch.int16 if dt == torch.bfloat16 else torch.int32).any()

@@ -138,11 +138,24 @@ struct PrefArgs {
   float beta, eps, gscale;
 };
 
+// One workgroup per row, numbered over a grid of lines: one dimension of a
+// launch holds fewer than 2^32 work-items, which 2^24 rows would reach.
+// Workgroups past the last row end at once.
+constexpr int64_t kRowsPerLine = 1 << 23;
+
+dim3 row_grid(int64_t rows) {
+  const int64_t line = rows < kRowsPerLine ? rows : kRowsPerLine;
+  return dim3((unsigned)line, (unsigned)((rows + line - 1) / line));
+}
+
+__device__ __forceinline__ int64_t row_number() { return (int64_t)blockIdx.y * kRowsPerLine + blockIdx.x; }
+
 template <typename T>
 __global__ __launch_bounds__(kRowThreads) void row_stats_kernel(PrefArgs p) {
   __shared__ MaxSum part[kRowThreads / 64];
   const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x;
+  const int64_t row = row_number();
+  if (row >= p.rows) return;                        // uniform: no barrier was reached
   const int64_t y = p.labels[row];
   if (y < 0 || y >= p.V) {
     if (tid == 0) p.lp[row] = 0.0f;
@@ -250,11 +263,11 @@ __device__ __forceinline__ void mean_loss(const PrefArgs& p) {
 template <typename T>
 __global__ __launch_bounds__(kRowThreads) void row_grad_kernel(PrefArgs p) {
   const int tid = threadIdx.x;
-  if ((int64_t)blockIdx.x == p.rows) {   // one more workgroup than rows
-    if (tid < 64) mean_loss(p);
+  const int64_t row = p.rows - 1 - row_number();
+  if (row < 0) {                         // one more workgroup than rows
+    if (row == -1 && tid < 64) mean_loss(p);
     return;
   }
-  const int64_t row = p.rows - 1 - (int64_t)blockIdx.x;
   const int64_t y = p.labels[row];
   constexpr int N = Vec<T>::kN;
   T* dx = static_cast<T*>(p.dx) + row * p.ldd;
@@ -307,7 +320,7 @@ template <typename T>
 hipError_t run_preference(PrefArgs& p, bool grad, hipStream_t stream) {
   hipError_t e = hipSuccess;
   if (p.rows > 0) {
-    hipLaunchKernelGGL((row_stats_kernel<T>), dim3((unsigned)p.rows), dim3(kRowThreads), 0, stream, p);
+    hipLaunchKernelGGL((row_stats_kernel<T>), row_grid(p.rows), dim3(kRowThreads), 0, stream, p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (p.S > 0) {
@@ -315,7 +328,7 @@ hipError_t run_preference(PrefArgs& p, bool grad, hipStream_t stream) {
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (!grad) p.rows = 0;   // only the mean's workgroup
-  hipLaunchKernelGGL((row_grad_kernel<T>), dim3((unsigned)(p.rows + 1)), dim3(kRowThreads), 0, stream, p);
+  hipLaunchKernelGGL((row_grad_kernel<T>), row_grid(p.rows + 1), dim3(kRowThreads), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -103,3 +103,45 @@ def test_gradients_of_an_idle_adapter(api, M, r, A, value):
         for g, w in zip(got[1:], want[1:]):
             assert torch.equal(g, w.to(dt))
             assert not g[1].view(torch.int16 if dt == torch.bfloat16 else torch.int32).any()
+
+
+# ---- rows past a launch's reach ----------------------------------------------------------------
+
+@pytest.mark.parametrize("T", [(1 << 23) - 1, 1 << 23, (1 << 23) + 3])
+def test_preference_of_more_than_2_24_rows(api, T):
+    """One pair of long sequences over a tiny vocabulary, against float64 sums on the device."""
+    import torch
+
+    U, V, beta = 2.0 ** -24, 3, 1e-3
+    say(f"preference 2 x {T} rows of {V}")
+    gen = torch.Generator("cuda").manual_seed(T)
+    x = torch.randn(2, T, V, generator=gen, device="cuda")
+    y = torch.randint(-1, V, (2, T), generator=gen, device="cuda")
+    ref = -1.0 + 0.1 * torch.randn(2, T, generator=gen, device="cuda")
+    out = api.qlora_preference_loss(x, y, ref, beta)
+    only = api.qlora_preference_loss(x, y, ref, beta, need_grad=False)
+    d = x.double()
+    q = d.exp()
+    total = q.sum(2, keepdim=True)
+    on, at = y >= 0, y.clamp(min=0)[..., None]
+    lp = torch.where(on, d.gather(2, at)[..., 0] - total[..., 0].log(), 0.0)
+    q /= total
+    rho = U * (V / 256 + 48 + 8 * x.abs().amax(2).double())      # as in test_gpu_preference.py
+    e_lp = torch.where(on, rho + 2 * U * lp.abs(), 0.0)
+    assert ((out.logps - lp).abs() <= e_lp).all()
+    reward = beta * torch.where(on, lp - ref, 0.0).sum(1)
+    e_r = beta * e_lp.sum(1) + 2 * U * reward.abs()
+    assert ((out.rewards - reward).abs() <= e_r).all()
+    h = reward[0] - reward[1]
+    loss = torch.nn.functional.softplus(-h)
+    assert (out.loss - loss).abs() <= e_r.sum() + 2 * U * loss
+    w = -beta * torch.sigmoid(-h) * torch.tensor([1.0, -1.0], dtype=torch.float64, device="cuda")
+    e_w = beta * e_r.sum() / 4 + 4 * U * w.abs()
+    hot = torch.zeros_like(q).scatter_(2, at, 1.0)
+    grad = torch.where(on[..., None], w[:, None, None] * (hot - q), 0.0)
+    tol = w.abs()[:, None, None] * q * 2 * rho[..., None] + e_w[:, None, None] * (hot - q).abs()
+    tol = tol * 1.01 + 4 * U * grad.abs() + 2.0 ** -133
+    tol = torch.where(on[..., None], tol, 0.0)
+    assert ((out.dlogits - grad).abs() <= tol).all()
+    for a, b in zip(out[:3], only[:3]):
+        assert torch.equal(a, b)

@@ -158,6 +158,8 @@ constexpr int kCodeBytes = kBaseRows * kBaseK / 2;
 
 typedef __attribute__((address_space(3))) void lds_void_t;
 
+__device__ __attribute__((aligned(16))) uint32_t g_base_zero[4];  // zero-initialised copy source
+
 // One 16-byte copy per lane into 1 KB of LDS (uniform base, the lane's 32-bit
 // offset), not visible to the compiler: the caller waits for it with a counted
 // vmcnt.
@@ -210,9 +212,9 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
   // stages ahead, would hold up X, from the L2 and two stages ahead).
   // Code instruction q of wave 4 + w: rows 16 (2 w + q) .. +16, lane -> row lane / 4, chunk lane % 4;
   // X instruction q of wave w: 8 rows of one half, lane -> row lane / 8, chunk lane % 8. Rows past N or M
-  // repeat the last one; k past the slice (the second half of a last stage) reads its first half (its
-  // constants are 0). Stage numbers past the last repeat its addresses: every stage issues the same number
-  // of copies, and their data is not used.
+  // repeat the last one; k past the slice (the second half of a last stage) reads the first half's codes with
+  // constants of 0, and zeros for X (0 times a copied infinity would be NaN). Stage numbers past the last repeat
+  // its addresses: every stage issues the same number of copies, and their data is not used.
   constexpr int kXPer = 2 * MT, kCPer = 2;
   const bool brings_x = wave < 4;
   const char* base = brings_x ? reinterpret_cast<const char*>(X + k0) : reinterpret_cast<const char*>(W.codes + (n0 * K + k0) / 2);
@@ -225,7 +227,7 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
       const uint32_t row = (uint32_t)(rl < M ? rl : M - 1) * (uint32_t)K;
       const uint32_t k = 8u * ((lane & 7) ^ x_swz(rl));
       off[q] = 2u * (row + 64u * (t / (4 * MT)) + k);
-      off_half[q] = 2u * (row + k);
+      off_half[q] = t < 4 * MT ? off[q] : 0u;
     } else {
       const int rl = 16 * (2 * (wave - 4) + (q & 1)) + (lane >> 2);
       const uint32_t row = (uint32_t)(n0 + rl < N ? rl : N - 1 - n0) * (uint32_t)(K / 2);
@@ -235,6 +237,7 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
     }
   }
   const bool ragged = (k1 - k0) % kBaseK != 0;           // the last stage has 64 k
+  const char* zeros = reinterpret_cast<const char*>(g_base_zero);
   // copies q0 .. q1 of the wave's share of X of stage st, and of the codes
   auto issue_x = [&](int st, int q0, int q1) {
     char* buf = smem + (st % kBaseStages) * L::kXBytes + kXPer * wave * 1024;
@@ -242,7 +245,8 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
     const char* from = base + (int64_t)at * (2 * kBaseK);
     const bool h = ragged && at == ns - 1;
 #pragma unroll
-    for (int q = q0; q < q1; ++q) copy16(from, h ? off_half[q] : off[q], buf + q * 1024);
+    for (int q = q0; q < q1; ++q)                        // a wave's instruction is of one half
+      copy16(h && kXPer * wave + q >= 4 * MT ? zeros : from, h ? off_half[q] : off[q], buf + q * 1024);
   };
   auto issue_c = [&](int st, int q0, int q1) {
     char* buf = smem + L::kCodes + (st % L::kC) * kCodeBytes + kCPer * (wave - 4) * 1024;

@@ -105,6 +105,33 @@ def test_gradients_of_an_idle_adapter(api, M, r, A, value):
             assert not g[1].view(torch.int16 if dt == torch.bfloat16 else torch.int32).any()
 
 
+# ---- infinities of a row ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [1, 7, 17, 60, 96, 128, 200])
+@pytest.mark.parametrize("K", [320, 64, 512])
+def test_an_infinity_in_a_bare_row(api, M, K):
+    """Y[m][n] is an infinity with the weight's sign where only one x is infinite, and NaN where that weight is 0."""
+    import torch
+
+    say(f"multi infinity in a bare row M={M} K={K}")
+    c = Case(api, M, K, 264, 16, 3, "rows")
+    m = M // 2
+    ids = c.ids.copy()
+    ids[m] = -1
+    set_ids(c, ids)
+    Y = c.fwd()[0]
+    W = api.qlora_dequantize(c.q).float()
+    others = torch.arange(M, device="cuda") != m
+    for k in (0, K // 2 + 3, K - 64, K - 33, K - 1):
+        x = c.d["X"][m, k].clone()
+        c.d["X"][m, k] = -INF
+        Y2 = c.fwd()[0]
+        c.d["X"][m, k] = x
+        want = W[:, k] * -INF
+        assert torch.equal(Y2[others], Y[others]), k
+        assert torch.equal(Y2[m].float().nan_to_num(nan=7.0), want.nan_to_num(nan=7.0)), k
+
+
 # ---- rows past a launch's reach ----------------------------------------------------------------
 
 @pytest.mark.parametrize("T", [(1 << 23) - 1, 1 << 23, (1 << 23) + 3])

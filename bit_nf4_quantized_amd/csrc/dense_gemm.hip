@@ -709,9 +709,13 @@ GemmSplit gemm_split(int64_t M, int64_t N, int64_t K) {
 
 }  // namespace
 
+// Of any split product of up to M rows: its half-height tiles times its slices
+// are at most one per CU.
 size_t gemm_multi_partial_bytes(int64_t M, int64_t N, int64_t K) {
-  const GemmSplit sp = gemm_split(M, N, K);
-  return sp.S > 1 ? (size_t)sp.S * M * N * 4 : 0;
+  const int64_t nk = K / TK, most = nk / 16 < 8 ? nk / 16 : 8;
+  if (most < 2) return 0;
+  const int64_t filled = device_cu_count() / ((N + TN - 1) / TN) * (TM / 2), rows = most * M;
+  return (size_t)(rows < filled ? rows : filled) * N * 4;
 }
 
 hipError_t launch_gemm_nt_multi(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N,

@@ -286,7 +286,7 @@ struct MultiSlab {
 hipError_t launch_gemm_nt_multi(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t N,
                                 int64_t K, const uint16_t* A2, const uint16_t* B2, int64_t ld2, const MultiSlab& slab,
                                 uint16_t* C, float* part, SplitSum* later, hipStream_t stream);
-size_t gemm_multi_partial_bytes(int64_t M, int64_t N, int64_t K);   // of part, in launch_gemm_nt_multi
+size_t gemm_multi_partial_bytes(int64_t M, int64_t N, int64_t K);   // of part, in launch_gemm_nt_multi, for up to M rows
 
 // The linear with an adapter per row (multi.hip, multi_small.hip).
 constexpr int64_t kMultiMaxRows = (int64_t)1 << 22;   // 32-bit offsets of the rows' [M][256] rank buffers
@@ -321,8 +321,10 @@ struct MultiIds {
   int A;
   const float* scale;      // [A]
 };
+constexpr int64_t kMultiSmallRows = 128;
 bool multi_small_fits(int64_t M, int64_t K, int64_t N);
 int multi_small_slices(int64_t M, int64_t K, int64_t N);   // partials [S][M][N] of the base product
+int64_t multi_small_partial_floats(int64_t M, int64_t K, int64_t N);   // theirs for any batch of up to M rows
 hipError_t launch_multi_small_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, float* part,
                                    hipStream_t stream);
 int64_t multi_small_t_floats(int64_t M, int64_t K, int r);

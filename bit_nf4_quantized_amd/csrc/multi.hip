@@ -770,31 +770,57 @@ NtSplit nt_split(int64_t M, int64_t len, int A, int rp) {
   return NtSplit{per * SK, (int)cdiv(steps, per)};
 }
 
-// Rows per piece of the TN products: whole segments up to kTnRows rows, so
-// that most gradients are written once; fewer when the launch would not fill
-// the device (128 columns of dL1 or dL2 per workgroup).
-int tn_rows(int64_t M, int64_t K, int64_t N, int r) {
+// The most rows times slices of nt_split for any batch of up to M rows: z
+// slices are taken for at most 2 CUs / `least` tiles.
+int64_t nt_partial_rows(int64_t M, int64_t len, int rp) {
+  struct Slices {
+    int64_t z, least;
+  };
+  int64_t most = M;
+  for (const Slices& s : {Slices{16, 9}, Slices{8, 5}, Slices{4, 4}, Slices{3, 3}, Slices{2, 2}}) {
+    const int64_t rows = 2 * (int64_t)device_cu_count() / (s.least * (rp / SJ)) * SM;
+    const int64_t z = s.z < cdiv(len, SK) ? s.z : cdiv(len, SK), v = z * (rows < M ? rows : M);
+    if (v > most) most = v;
+  }
+  return most;
+}
+
+// Pieces of the TN products that fill the device (128 columns of dL1 or dL2 per workgroup).
+int64_t tn_wanted(int64_t K, int64_t N, int r) {
   const int64_t tiles = (cdiv(K, SM) + cdiv(N, SM)) * cdiv(r, SJ);
-  const int64_t want = cdiv(2 * (int64_t)device_cu_count(), tiles);   // pieces
-  int64_t rows = cdiv(cdiv(M, want), SK) * SK;
+  return cdiv(2 * (int64_t)device_cu_count(), tiles);
+}
+
+// Rows per piece: whole segments up to kTnRows rows, so that most gradients are
+// written once; fewer when the launch would not fill the device.
+constexpr int kTnLeast = 256;
+
+int tn_rows(int64_t M, int64_t K, int64_t N, int r) {
+  int64_t rows = cdiv(cdiv(M, tn_wanted(K, N, r)), SK) * SK;
   if (rows > kTnRows) rows = kTnRows;
-  if (rows < 256) rows = 256;
+  if (rows < kTnLeast) rows = kTnLeast;
   return (int)rows;
 }
 
+// Partials of dL1 or dL2 for any batch of up to M rows: at most M / rows + the
+// segments, none where every segment is one piece.
 int64_t tn_part_floats(int64_t M, int64_t K, int64_t N, int64_t W, int r, int A) {
-  const int rows = tn_rows(M, K, N, r);
-  if (M <= rows) return 0;                          // one piece per segment
-  return (M / rows + (A < M ? A : M)) * W * cdiv(r, SJ) * SJ;
+  const int64_t want = tn_wanted(K, N, r);
+  if (M <= (want > 1 ? kTnLeast : kTnRows)) return 0;
+  int64_t pieces = want > M / kTnRows ? want : M / kTnRows;
+  if (pieces > M / kTnLeast) pieces = M / kTnLeast;
+  return (pieces + (A < M ? A : M)) * W * cdiv(r, SJ) * SJ;
 }
 
 }  // namespace
 
+// No part is smaller for more rows, so that a workspace for the largest batch
+// serves the smaller ones too.
 MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, int A, bool bwd) {
   MultiWorkspace L = {};
   if (!bwd && (M < 1 || multi_small_fits(M, K, N))) {   // the small paths
     L.part_off = 0;
-    L.tpart_off = align_up((size_t)multi_small_slices(M, K, N) * M * N * 4, 256);
+    L.tpart_off = align_up((size_t)multi_small_partial_floats(M, K, N) * 4, 256);
     const size_t t = (size_t)multi_small_t_floats(M, K, r) * 4, one = gemv1_partial_bytes(K, r);
     L.total = L.tpart_off + align_up((t > one ? t : one) + 1, 256);
     return L;
@@ -819,10 +845,9 @@ MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, in
   L.b2_off = take(wide);
   L.wd_off = take(K * np * 2);
   L.dy_off = take(bwd && N % 64 ? M * np * 2 : 0);
-  const NtSplit t = nt_split(M, K, A, (int)rp), u = nt_split(M, N, A, (int)rp);
-  int64_t part = t.Z * M * rp;                       // T's, then U's; then dL1's and dL2's, or the forward GEMM's
+  int64_t part = nt_partial_rows(M, K, (int)rp) * rp;   // T's, then U's; then dL1's and dL2's, or the forward GEMM's
   if (bwd) {
-    part += u.Z * M * rp;
+    part += nt_partial_rows(M, N, (int)rp) * rp;
     const int64_t grads = tn_part_floats(M, K, N, K, r, A) + tn_part_floats(M, K, N, N, r, A);
     if (grads > part) part = grads;
   }
@@ -833,6 +858,10 @@ MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, in
   L.part_off = take(part * 4);
   L.gpart_off = take(bwd ? (int64_t)gemm_multi_partial_bytes(M, K, np) : 0);   // dX's, added while dL1 and dL2 are computed
   L.total = off;
+  if (!bwd && multi_small_fits(kMultiSmallRows, K, N)) {
+    const size_t small = multi_workspace_layout(kMultiSmallRows, K, N, r, A, false).total;
+    if (small > L.total) L.total = small;
+  }
   return L;
 }
 

@@ -436,13 +436,15 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
 // LDS), in slices of whole stages; at most 8, whose sum in the finish costs what
 // more would save here (whole call with 8 / 16: 24 rows 4096 -> 4096 18.8 / 22.4 us,
 // 82 rows 5760 -> 1288 28.0 / 28.9, 121 rows 10432 -> 1104 42.6 / 40.5).
+constexpr int kBaseTwoPerCu = 32;            // rows up to which two workgroups fit in a CU's LDS
+
 struct BaseSplit {
   int slice, S;
 };
 
 BaseSplit base_split(int64_t M, int64_t K, int64_t N) {
   const int64_t tiles = (N + kBaseRows - 1) / kBaseRows, steps = (K + kBaseK - 1) / kBaseK;
-  const int64_t resident = (M <= 32 ? 2 : 1) * (int64_t)device_cu_count();
+  const int64_t resident = (M <= kBaseTwoPerCu ? 2 : 1) * (int64_t)device_cu_count();
   int64_t S = resident / tiles;
   if (S > steps / 2) S = steps / 2;
   if (S > 8) S = 8;
@@ -591,10 +593,16 @@ int64_t multi_small_t_floats(int64_t M, int64_t K, int r) { return (K + kTK - 1)
 int multi_small_t_slices(int64_t K) { return (int)((K + kTK - 1) / kTK); }
 
 bool multi_small_fits(int64_t M, int64_t K, int64_t N) {
-  return M >= 1 && M <= 128 && K < ((int64_t)1 << 23) && N <= ((int64_t)1 << 31) - 256;   // 32-bit offsets of 128 rows
+  return M >= 1 && M <= kMultiSmallRows && K < ((int64_t)1 << 23) && N <= ((int64_t)1 << 31) - 256;   // 32-bit offsets of 128 rows
 }
 
 int multi_small_slices(int64_t M, int64_t K, int64_t N) { return base_split(M, K, N).S; }
+
+int64_t multi_small_partial_floats(int64_t M, int64_t K, int64_t N) {
+  const int64_t few = M < kBaseTwoPerCu ? M : kBaseTwoPerCu;   // the slices depend on M only through this bound
+  const int64_t a = base_split(few, K, N).S * few, b = base_split(M, K, N).S * M;
+  return (a > b ? a : b) * N;
+}
 
 hipError_t launch_multi_small_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, float* part,
                                    hipStream_t stream) {

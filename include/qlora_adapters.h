@@ -42,7 +42,9 @@ extern "C" {
  *                backward pass (which computes it when T is NULL).
  *   dX           device bf16 [M][K], or NULL to skip it.
  *   dL1, dL2     device, grad_dtype, shaped like L1, L2.
- *   ws           qlora_linear_multi_workspace(M, K, N, r, A, backward) bytes.
+ *   ws           qlora_linear_multi_workspace(M, K, N, r, A, backward) bytes,
+ *                which never shrink as M grows: one of the largest batch's
+ *                size serves smaller batches.
  * Shape rules as for qlora_linear_fwd (K a multiple of 64, N and r of 8, r in
  * [8, 256]), M <= QLORA_MULTI_MAX_ROWS; M > 128 and the backward pass need a
  * dequantised weight below 2 GB. M <= 128 streams the 4-bit weight once, and

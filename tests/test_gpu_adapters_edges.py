@@ -172,3 +172,28 @@ def test_preference_of_more_than_2_24_rows(api, T):
     assert ((out.dlogits - grad).abs() <= tol).all()
     for a, b in zip(out[:3], only[:3]):
         assert torch.equal(a, b)
+
+
+# ---- workspaces ------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M,K,N,r,A", [(1, 512, 512, 16, 3), (13, 512, 264, 16, 5), (33, 4096, 136, 16, 3), (128, 320, 1032, 72, 9),
+                                       (129, 512, 264, 64, 4), (150, 4096, 264, 24, 40), (300, 256, 4096, 72, 3),
+                                       (513, 512, 512, 16, 7), (2500, 256, 512, 64, 2)])
+def test_nothing_beyond_the_workspace(api, M, K, N, r, A):
+    """A workspace of the query's size for this batch or a larger one is enough, and nothing past the former is written."""
+    import torch
+
+    say(f"multi workspace M={M} K={K} N={N} r={r} A={A}")
+    c = Case(api, M, K, N, r, A, "rows")
+    for back, call in ((False, lambda **kw: c.fwd(want_T=True, **kw)), (True, c.bwd)):
+        want = call()
+        need = api.qlora_linear_multi_workspace(M, K, N, r, A, back)
+        ws = torch.full((need + 4096,), 171, dtype=torch.uint8, device="cuda")
+        got = call(workspace=ws)
+        assert (ws[need:] == 171).all()
+        large = torch.empty(api.qlora_linear_multi_workspace(3 * M + 500, K, N, r, A, back), dtype=torch.uint8, device="cuda")
+        for other in (got, call(workspace=ws[:need]), call(workspace=large)):
+            for a, b in zip(other, want):
+                assert torch.equal(a, b)
+        with pytest.raises(ValueError):
+            call(workspace=ws[:need - 1])

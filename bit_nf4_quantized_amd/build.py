@@ -86,18 +86,22 @@ def _build_tensors() -> None:
     os.replace(tmp, TENSORS_PATH)
 
 
-def build(verbose: bool = False) -> str:
-    os.makedirs(OBJ_DIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
-        tensors = ex.submit(_build_tensors)
-        objs = list(ex.map(_compile, SOURCES))
-        tensors.result()
+def _link(objs: list[str]) -> None:
     tmp = LIB_PATH + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
+
+
+def build(verbose: bool = False) -> str:
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+        tensors = ex.submit(_build_tensors)
+        objs = list(ex.map(_compile, SOURCES))
+    _link(objs)
+    tensors.result()   # needs torch and the Python headers; the library does not
     if verbose:
         print(f"built {LIB_PATH}")
     return LIB_PATH

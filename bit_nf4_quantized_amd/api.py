@@ -273,12 +273,25 @@ def _fill(dev, tensors, specs):
     return [next(new) if t is None else t for t in tensors]
 
 
-def _workspace_of(ws, nbytes):
-    """The address and size of a workspace, which must hold ``nbytes``."""
-    size = ws.numel() * ws.element_size()
-    if size < nbytes:
+def _need_workspace(ws, nbytes, dev):
+    """A caller's workspace: memory of device ``dev`` in one piece of at least ``nbytes``."""
+    import torch
+
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("workspace must be a torch tensor")
+    if not ws.is_cuda:
+        raise ValueError("workspace must be a device tensor")
+    if ws.get_device() != dev:
+        raise ValueError(f"workspace must be on device {dev}, got {ws.get_device()}")
+    if not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if ws.numel() * ws.element_size() < nbytes:
         raise ValueError("workspace too small")
-    return ws.data_ptr(), size
+
+
+def _memory(t):
+    """Address and size of a tensor's memory."""
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _raw_stream(stream):
@@ -448,12 +461,14 @@ def qlora_preference_loss(logits, labels, ref_logps, beta: float, label_smoothin
             raise ValueError("dlogits must have the logits' dtype, shape and device")
         ldd, dp = _row_stride(dlogits, "dlogits"), dlogits.data_ptr()
     need = qlora_preference_workspace(S // 2, T, V)
+    if workspace is not None:
+        _need_workspace(workspace, need, dev)
     loss, rewards, logps, ws = _fill(dev, (None, None, None, workspace),
                                      ((_F32, (1,)), (_F32, (S,)), (_F32, (S, T)), (_U8, (max(need, 256),))))
     _check(_load().qlora_preference_loss(logits.data_ptr(), dt, S // 2, T, V, ld, yp, rp, float(beta),
                                          float(label_smoothing), float(grad_scale), loss.data_ptr(),
                                          rewards.data_ptr(), logps.data_ptr(), dp, ldd,
-                                         *_workspace_of(ws, need), _raw_stream(stream)),
+                                         *_memory(ws), _raw_stream(stream)),
            "qlora_preference_loss")
     return PreferenceOut(loss, rewards, logps, dlogits)
 
@@ -512,11 +527,13 @@ def qlora_clip_grad_norm_batch(grads, max_norm: float, coef=None, norm=None, wor
     dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
     gp, sizes = _tensors().addresses(grads, dtype, dev.index if grads else -1, "grads")
     need = QLORA_CLIP_WORKSPACE_BYTES
+    if workspace is not None:
+        _need_workspace(workspace, need, dev.index)
     coef, norm, ws = _fill(dev.index, (coef, norm, workspace), ((_F32, (1,)), (_F64, (1,)), (_U8, (need,))))
     address = _tensors().address
     cp, np_ = address(coef, _F32, (1,), dev.index, "coef"), address(norm, _F64, (1,), dev.index, "norm")
     _check(_load().qlora_clip_grad_norm_batch(len(grads), gp, gd, sizes, float(max_norm), cp, np_,
-                                              *_workspace_of(ws, need), _raw_stream(stream)),
+                                              *_memory(ws), _raw_stream(stream)),
            "qlora_clip_grad_norm_batch")
     return coef, norm
 
@@ -981,12 +998,14 @@ def qlora_linear_multi_fwd(q: NF4Tensor, X, row_adapter, L1, L2, scale, want_T: 
     need = qlora_linear_multi_workspace(M, K, N, r, A)
     if want_T and T_out is None:
         T_out = X.new_empty((M, r))
+    if workspace is not None:
+        _need_workspace(workspace, need, dev)
     Y, ws = _fill(dev, (Y, workspace), ((_BF16, (M, N)), (_U8, (max(need, 256),))))
     yp = address(Y, _BF16, (M, N), dev, "Y")
     tp = None if T_out is None else address(T_out, _BF16, (M, r), dev, "T_out")
     st = q.struct()
     _check(_load().qlora_linear_multi_fwd(ctypes.byref(st), xp, M, ip, A, p1, p2, r, sp, yp, tp,
-                                          *_workspace_of(ws, need), _raw_stream(stream)), "qlora_linear_multi_fwd")
+                                          *_memory(ws), _raw_stream(stream)), "qlora_linear_multi_fwd")
     return Y, T_out
 
 
@@ -1016,9 +1035,12 @@ def qlora_linear_multi_bwd(q: NF4Tensor, X, dY, row_adapter, L1, L2, scale, T=No
     gd, gtype = (QLORA_F32, _F32) if grad_dtype == torch.float32 else (QLORA_BF16, _BF16)
     d1, d2 = address(dL1, gtype, (A, K, r), dev, "dL1"), address(dL2, gtype, (A, r, N), dev, "dL2")
     st = q.struct()
-    ws = _workspace(qlora_linear_multi_workspace(M, K, N, r, A, True), X.device, workspace)
+    need = qlora_linear_multi_workspace(M, K, N, r, A, True)
+    if workspace is not None:
+        _need_workspace(workspace, need, dev)
+    ws, = _fill(dev, (workspace,), ((_U8, (max(need, 256),)),))
     _check(_load().qlora_linear_multi_bwd(ctypes.byref(st), xp, yp, M, ip, A, p1, p2, r, sp, tp, dxp, d1, d2, gd,
-                                          ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream)),
+                                          *_memory(ws), _raw_stream(stream)),
            "qlora_linear_multi_bwd")
     return dX, dL1, dL2
 

@@ -197,3 +197,26 @@ def test_nothing_beyond_the_workspace(api, M, K, N, r, A):
                 assert torch.equal(a, b)
         with pytest.raises(ValueError):
             call(workspace=ws[:need - 1])
+
+
+def test_refused_workspaces(api):
+    """A workspace in host memory, or one whose values do not lie in a row, is refused before anything is enqueued."""
+    import torch
+
+    c = Case(api, 20, 256, 264, 16, 3, "rows")
+    z = torch.zeros(2, 3, 8, device="cuda")
+    lab = torch.zeros(2, 3, dtype=torch.int64, device="cuda")
+    calls = [lambda ws: c.fwd(workspace=ws), lambda ws: c.bwd(workspace=ws),
+             lambda ws: api.qlora_preference_loss(z, lab, z[:, :, 0].contiguous(), 0.1, workspace=ws),
+             lambda ws: api.qlora_clip_grad_norm_batch([z], 1.0, workspace=ws)]
+    n = 1 << 24
+    for call in calls:
+        for bad in (torch.empty(n, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(n),
+                    torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+            with pytest.raises(ValueError):
+                call(bad)
+        with pytest.raises(TypeError):
+            call(n)
+        call(torch.empty(n, dtype=torch.uint8, device="cuda"))
+        call(torch.empty(n // 4, device="cuda"))
+    torch.cuda.synchronize()

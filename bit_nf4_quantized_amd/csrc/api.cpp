@@ -673,7 +673,7 @@ int qlora_linear_multi_fwd(const qlora_nf4* W, const uint16_t* X, int64_t M, con
   if (!Y) return QLORA_ERR_ARG;
   if (!ws) return QLORA_ERR_WORKSPACE;
   if (!aligned16(Y) || !aligned16(T_out) || !aligned16(ws)) return QLORA_ERR_ALIGN;
-  if (!qlora::multi_forward_supported(M, W->cols, W->rows, r)) return QLORA_ERR_SHAPE;
+  if (!qlora::multi_forward_supported(M, W->cols, W->rows, r, n_adapters)) return QLORA_ERR_SHAPE;
   if (ws_bytes < qlora::multi_workspace_layout(M, W->cols, W->rows, r, n_adapters, false).total)
     return QLORA_ERR_WORKSPACE;
   (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
@@ -694,6 +694,7 @@ int qlora_linear_multi_bwd(const qlora_nf4* W, const uint16_t* X, const uint16_t
   if (!aligned16(dY) || !aligned16(T) || !aligned16(dX) || !aligned16(dL1) || !aligned16(dL2) || !aligned16(ws))
     return QLORA_ERR_ALIGN;
   if (!qlora::multi_dense_supported(W->cols, W->rows, r)) return QLORA_ERR_SHAPE;
+  if (dX && !qlora::multi_lay_supported(M, W->cols, r, n_adapters, false)) return QLORA_ERR_SHAPE;
   if (ws_bytes < qlora::multi_workspace_layout(M, W->cols, W->rows, r, n_adapters, true).total)
     return QLORA_ERR_WORKSPACE;
   (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call

@@ -305,7 +305,10 @@ struct MultiWorkspace {
 };
 MultiWorkspace multi_workspace_layout(int64_t M, int64_t K, int64_t N, int r, int A, bool bwd);
 bool multi_dense_supported(int64_t K, int64_t N, int r);            // the paths with a dequantised weight
-bool multi_forward_supported(int64_t M, int64_t K, int64_t N, int r);
+// the adapters' sums and the layout of the GEMM's adapter operand (L2^T: W = N, transposed; L1: W = K) are one launch,
+// whose single dimension holds fewer than 2^32 work-items
+bool multi_lay_supported(int64_t M, int64_t W, int r, int A, bool transpose);
+bool multi_forward_supported(int64_t M, int64_t K, int64_t N, int r, int A);
 hipError_t multi_forward(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, const int32_t* ids,
                                int A, const uint16_t* L1, const uint16_t* L2, int r, const float* scale, uint16_t* Y,
                                uint16_t* T_out, void* ws, hipStream_t stream);

@@ -902,8 +902,12 @@ hipError_t launch_nt(const NtArgs* u, int zu, const NtArgs* t, int zt, int64_t M
   return hipGetLastError();
 }
 
+// Workgroups of multi_sum_kernel: the sums, and the layout of one group's operand.
+int64_t sum_blocks(int64_t M, int64_t rp) { return cdiv((M + 1) * rp / 4, 256); }
+int64_t lay_blocks(int64_t W, int64_t rp, bool transpose) { return transpose ? cdiv(W, 64) * (rp / 64) : cdiv(W * rp / 8, 256); }
+
 hipError_t launch_sum(const SumArgs& s, const LayArgs& lay, int64_t segs, const RouteView& rv, hipStream_t stream) {
-  const int64_t blocks = cdiv((s.M + 1) * s.rp / 4, 256);
+  const int64_t blocks = sum_blocks(s.M, s.rp);
   const int64_t groups = cdiv(segs, packing_of(lay.r).pack);
   hipLaunchKernelGGL(multi_sum_kernel, dim3((unsigned)(blocks + groups * lay.blocks)), dim3(256), 0, stream, s, (int)blocks,
                      lay, rv);
@@ -938,8 +942,13 @@ bool multi_dense_supported(int64_t K, int64_t N, int r) {
   return K * np * 2 < two_gb && N * rp * 2 < two_gb && K * rp * 2 < two_gb;
 }
 
-bool multi_forward_supported(int64_t M, int64_t K, int64_t N, int r) {
-  return multi_small_fits(M, K, N) || multi_dense_supported(K, N, r);
+bool multi_lay_supported(int64_t M, int64_t W, int r, int A, bool transpose) {
+  const int64_t rp = cdiv(r, 64) * 64, groups = cdiv(A < M ? A : M, packing_of(r).pack);
+  return sum_blocks(M, rp) + groups * lay_blocks(W, rp, transpose) < (int64_t)1 << 24;
+}
+
+bool multi_forward_supported(int64_t M, int64_t K, int64_t N, int r, int A) {
+  return multi_small_fits(M, K, N) || (multi_dense_supported(K, N, r) && multi_lay_supported(M, N, r, A, true));
 }
 
 // M <= 128: a single token or a few through the GEMVs where they apply, else
@@ -987,7 +996,7 @@ hipError_t multi_forward(const NF4View& W, const NF4Table& tab, const uint16_t* 
   e = launch_nt(nullptr, 0, &t, sp.Z, M, A, stream);
   if (e != hipSuccess) return e;
   const SumArgs s{part, part, sp.Z, sp.Z, M, r, rp, ids, A, scale, ra.slot, sT, T_out};
-  const LayArgs lay{L2, l2t, N, r, rp, (int)(cdiv(N, 64) * (rp / 64)), ra.bad, true};
+  const LayArgs lay{L2, l2t, N, r, rp, (int)lay_blocks(N, rp, true), ra.bad, true};
   e = launch_sum(s, lay, segs, rv, stream);
   if (e != hipSuccess) return e;
   const MultiSlab slab{rv, packing_of(r).pack, M, N * rp, ra.bad, L2, N * r, 1, N, r, packing_of(r).width};
@@ -1030,7 +1039,7 @@ hipError_t multi_backward(const NF4View& W, const NF4Table& tab, const uint16_t*
   uint16_t* tbuf = T ? nullptr : reinterpret_cast<uint16_t*>(base + L.t_off);
   uint16_t* l1p = reinterpret_cast<uint16_t*>(base + L.b2_off);
   const SumArgs s{upart, part, su.Z, st.Z, M, r, rp, ids, A, scale, ra.slot, sU, tbuf};
-  const LayArgs lay{L1, l1p, K, r, rp, (int)cdiv(K * rp / 8, 256), ra.bad, false};
+  const LayArgs lay{L1, l1p, K, r, rp, (int)lay_blocks(K, rp, false), ra.bad, false};
   e = launch_sum(s, lay, dX ? segs : 0, rv, stream);
   if (e != hipSuccess) return e;
   if (!T) T = tbuf;

@@ -47,8 +47,10 @@ extern "C" {
  *                size serves smaller batches.
  * Shape rules as for qlora_linear_fwd (K a multiple of 64, N and r of 8, r in
  * [8, 256]), M <= QLORA_MULTI_MAX_ROWS; M > 128 and the backward pass need a
- * dequantised weight below 2 GB. M <= 128 streams the 4-bit weight once, and
- * a single token (or, for r <= 64, a few) takes the GEMV.
+ * dequantised weight below 2 GB, and the factor that the GEMM lays out for the
+ * adapters with rows (L2 in the forward pass, L1 for dX) below about 64 GB, its
+ * rank rounded up to 64: QLORA_ERR_SHAPE otherwise. M <= 128 streams the 4-bit
+ * weight once, and a single token (or, for r <= 64, a few) takes the GEMV.
  */
 #define QLORA_MULTI_MAX_ROWS (1 << 22)
 #define QLORA_MULTI_MAX_ADAPTERS 4096

@@ -29,3 +29,24 @@ def test_a_larger_batch_never_needs_less(lib, K, N, r, A, back):
         assert lib.qlora_linear_multi_workspace(M, K, N, r, A, back, ctypes.byref(n)) == api.QLORA_OK
         assert n.value >= last, (M, n.value, last)
         last = n.value
+
+
+P = 4096   # a 16-byte aligned address that is never dereferenced
+
+
+def test_operands_beyond_one_launch(lib):
+    """Adapters whose laid-out factor would take 2^32 work-items or more are refused before anything is enqueued."""
+    def call(back, M, K, N, r, A, dX=P):
+        W = api.QNF4(N, K, P, P, P, P, 0, 0, None)
+        if back:
+            return lib.qlora_linear_multi_bwd(ctypes.byref(W), P, P, M, P, A, P, P, r, P, None, dX, P, P, 0, P, 0, None)
+        return lib.qlora_linear_multi_fwd(ctypes.byref(W), P, M, P, A, P, P, r, P, P, None, P, 0, None)
+
+    # 4096 adapters of [32768][256] are 2^35 values: 2^32 work-items of 8; the workspace of 0 bytes is checked later
+    assert call(True, 5000, 32768, 64, 256, 4096) == api.QLORA_ERR_SHAPE
+    assert call(True, 5000, 32768, 64, 256, 4096, dX=None) == api.QLORA_ERR_WORKSPACE
+    assert call(True, 5000, 32768, 64, 256, 2048) == api.QLORA_ERR_WORKSPACE
+    assert call(True, 1000, 32768, 64, 256, 4096) == api.QLORA_ERR_WORKSPACE          # 1000 rows: at most 1000 adapters
+    assert call(False, 5000, 64, 1 << 17, 256, 4096) == api.QLORA_ERR_SHAPE            # 2^37 values, 16 a work-item
+    assert call(False, 5000, 64, 1 << 15, 256, 4096) == api.QLORA_ERR_WORKSPACE
+    assert call(False, 100, 64, 1 << 17, 256, 4096) == api.QLORA_ERR_WORKSPACE

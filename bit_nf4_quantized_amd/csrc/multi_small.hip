@@ -24,6 +24,8 @@
 #include "common.h"
 #include "launch.h"
 
+#include <type_traits>
+
 namespace qlora {
 
 namespace {
@@ -158,8 +160,6 @@ constexpr int kCodeBytes = kBaseRows * kBaseK / 2;
 
 typedef __attribute__((address_space(3))) void lds_void_t;
 
-__device__ __attribute__((aligned(16))) uint32_t g_base_zero[4];  // zero-initialised copy source
-
 // One 16-byte copy per lane into 1 KB of LDS (uniform base, the lane's 32-bit
 // offset), not visible to the compiler: the caller waits for it with a counted
 // vmcnt.
@@ -189,7 +189,11 @@ struct BaseLds {
   static_assert(kOut <= kConst, "the output tiles fit over the rings");
 };
 
-template <int MT>
+// RAGGED: K is an odd multiple of 64; the last stage is then compiled apart. A
+// check in the loop of one variant for all took 0.4 to 1.5 us of every call (60
+// rows 4096 -> 11008 35.2 -> 36.7); so it costs K = 4160 0.4 to 0.8 us (60 rows
+// -> 11008 37.7 -> 38.2) and nothing where K is a multiple of 128.
+template <int MT, bool RAGGED>
 __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4Table tab,
                                                                   const uint16_t* __restrict__ X, int M, int slice,
                                                                   float* __restrict__ part) {
@@ -212,9 +216,9 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
   // stages ahead, would hold up X, from the L2 and two stages ahead).
   // Code instruction q of wave 4 + w: rows 16 (2 w + q) .. +16, lane -> row lane / 4, chunk lane % 4;
   // X instruction q of wave w: 8 rows of one half, lane -> row lane / 8, chunk lane % 8. Rows past N or M
-  // repeat the last one; k past the slice (the second half of a last stage) reads the first half's codes with
-  // constants of 0, and zeros for X (0 times a copied infinity would be NaN). Stage numbers past the last repeat
-  // its addresses: every stage issues the same number of copies, and their data is not used.
+  // repeat the last one; k past the slice (the second half of a last stage) reads its first half: the constants
+  // there are 0, and X is cleared before it is used (0 times a copied infinity would be NaN). Stage numbers past
+  // the last repeat its addresses: every stage issues the same number of copies, and their data is not used.
   constexpr int kXPer = 2 * MT, kCPer = 2;
   const bool brings_x = wave < 4;
   const char* base = brings_x ? reinterpret_cast<const char*>(X + k0) : reinterpret_cast<const char*>(W.codes + (n0 * K + k0) / 2);
@@ -227,7 +231,7 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
       const uint32_t row = (uint32_t)(rl < M ? rl : M - 1) * (uint32_t)K;
       const uint32_t k = 8u * ((lane & 7) ^ x_swz(rl));
       off[q] = 2u * (row + 64u * (t / (4 * MT)) + k);
-      off_half[q] = t < 4 * MT ? off[q] : 0u;
+      off_half[q] = 2u * (row + k);
     } else {
       const int rl = 16 * (2 * (wave - 4) + (q & 1)) + (lane >> 2);
       const uint32_t row = (uint32_t)(n0 + rl < N ? rl : N - 1 - n0) * (uint32_t)(K / 2);
@@ -236,8 +240,7 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
       off_half[q] = row + 16u * (c & 1u);
     }
   }
-  const bool ragged = (k1 - k0) % kBaseK != 0;           // the last stage has 64 k
-  const char* zeros = reinterpret_cast<const char*>(g_base_zero);
+  const bool ragged = RAGGED && k1 == K;                 // the last stage has 64 k
   // copies q0 .. q1 of the wave's share of X of stage st, and of the codes
   auto issue_x = [&](int st, int q0, int q1) {
     char* buf = smem + (st % kBaseStages) * L::kXBytes + kXPer * wave * 1024;
@@ -245,8 +248,7 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
     const char* from = base + (int64_t)at * (2 * kBaseK);
     const bool h = ragged && at == ns - 1;
 #pragma unroll
-    for (int q = q0; q < q1; ++q)                        // a wave's instruction is of one half
-      copy16(h && kXPer * wave + q >= 4 * MT ? zeros : from, h ? off_half[q] : off[q], buf + q * 1024);
+    for (int q = q0; q < q1; ++q) copy16(from, h ? off_half[q] : off[q], buf + q * 1024);
   };
   auto issue_c = [&](int st, int q0, int q1) {
     char* buf = smem + L::kCodes + (st % L::kC) * kCodeBytes + kCPer * (wave - 4) * 1024;
@@ -361,7 +363,7 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
   // of st, part by part: the table reads of part p, the MFMAs of part p, the
   // conversion of part p - 1. The order is pinned: the scheduler would
   // otherwise gather all table reads before the first MFMA.
-  auto stage = [&](int st, const u32x4_t* cur, u32x4_t* next) {
+  auto stage = [&](int st, const u32x4_t* cur, u32x4_t* next, auto clear) {
     if ((st + 1) % kConstStages == 0 && st + 1 < ns) {  // uniform; long slices only: every wave has read stage st's
       __syncthreads();
       constants(st + 1);
@@ -369,7 +371,12 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
     if (brings_x) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(kXPer) : "memory");
     else asm volatile("s_waitcnt vmcnt(%0)" :: "n"(kCPer * (L::kC - 2)) : "memory");
     __syncthreads();
-    const char* x = smem + (st % kBaseStages) * L::kXBytes;
+    char* x = smem + (st % kBaseStages) * L::kXBytes;
+    if constexpr (decltype(clear)::value) {               // every copy of this stage has landed
+      for (int i = tid; i < 32 * MT * 128 / 16; i += kBaseThreads)
+        reinterpret_cast<u32x4_t*>(x + 32 * MT * 128)[i] = u32x4_t{0u, 0u, 0u, 0u};
+      __syncthreads();
+    }
     const Codes d = codes_of(st + 1);
     bf16x8_t b[2][MT];
 #pragma unroll
@@ -394,12 +401,21 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
     }
     next[3] = convert(d, 3, f[1]);
   };
+  const std::false_type whole;
+  const int n = ragged ? ns - 1 : ns;
   int st = 0;
-  for (; st + 1 < ns; st += 2) {
-    stage(st, w0, w1);
-    stage(st + 1, w1, w0);
+  for (; st + 1 < n; st += 2) {
+    stage(st, w0, w1, whole);
+    stage(st + 1, w1, w0, whole);
   }
-  if (st < ns) stage(st, w0, w1);
+  if (st < n) {
+    stage(st, w0, w1, whole);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) w0[p] = w1[p];
+  }
+  if constexpr (RAGGED) {
+    if (ragged) stage(n, w0, w1, std::true_type{});
+  }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // no copy may land in the output tile
   // register v of lane l: weight row 64 wn + 32 g + (v%4) + 4 (l/32) + 8 (v/4), column m = 32 t + l%32
   constexpr int kPitch = kBaseRows + 4, kTile = 32 * MT * kPitch;
@@ -453,18 +469,18 @@ BaseSplit base_split(int64_t M, int64_t K, int64_t N) {
   return BaseSplit{(int)(per * kBaseK), (int)((steps + per - 1) / per)};
 }
 
-template <int MT>
+template <int MT, bool RAGGED>
 hipError_t run_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, int M, const BaseSplit& sp, float* part,
                     hipStream_t stream) {
   static bool attr_set = false;  // raise the dynamic-LDS limit once per instantiation (idempotent)
   if (!attr_set) {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&small_base_kernel<MT>),
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&small_base_kernel<MT, RAGGED>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, BaseLds<MT>::kTotal);
     (void)hipGetLastError();  // a refusal shows up as a launch error below
     attr_set = true;
   }
   const dim3 grid((unsigned)((W.rows + kBaseRows - 1) / kBaseRows), (unsigned)sp.S);
-  hipLaunchKernelGGL(small_base_kernel<MT>, grid, dim3(kBaseThreads), BaseLds<MT>::kTotal, stream, W, tab, X, M,
+  hipLaunchKernelGGL((small_base_kernel<MT, RAGGED>), grid, dim3(kBaseThreads), BaseLds<MT>::kTotal, stream, W, tab, X, M,
                      sp.slice, part);
   return hipGetLastError();
 }
@@ -607,10 +623,14 @@ int64_t multi_small_partial_floats(int64_t M, int64_t K, int64_t N) {
 hipError_t launch_multi_small_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, float* part,
                                    hipStream_t stream) {
   const BaseSplit sp = base_split(M, W.cols, W.rows);
-  if (M <= 32) return run_base<1>(W, tab, X, (int)M, sp, part, stream);
-  if (M <= 64) return run_base<2>(W, tab, X, (int)M, sp, part, stream);
-  if (M <= 96) return run_base<3>(W, tab, X, (int)M, sp, part, stream);
-  return run_base<4>(W, tab, X, (int)M, sp, part, stream);
+  auto run = [&](auto ragged) -> hipError_t {
+    constexpr bool kRagged = decltype(ragged)::value;
+    if (M <= 32) return run_base<1, kRagged>(W, tab, X, (int)M, sp, part, stream);
+    if (M <= 64) return run_base<2, kRagged>(W, tab, X, (int)M, sp, part, stream);
+    if (M <= 96) return run_base<3, kRagged>(W, tab, X, (int)M, sp, part, stream);
+    return run_base<4, kRagged>(W, tab, X, (int)M, sp, part, stream);
+  };
+  return W.cols % kBaseK ? run(std::true_type{}) : run(std::false_type{});
 }
 
 hipError_t launch_multi_small_t(const uint16_t* X, int64_t M, int64_t K, const MultiIds& mi, const uint16_t* L1, int r,

@@ -524,14 +524,14 @@ def qlora_clip_grad_norm_batch(grads, max_norm: float, coef=None, norm=None, wor
 
     grads = list(grads)
     gd, dtype = _grad_dtype(grads)
-    dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
-    gp, sizes = _tensors().addresses(grads, dtype, dev.index if grads else -1, "grads")
+    dev = grads[0].get_device() if grads else torch.cuda.current_device()
+    gp, sizes = _tensors().addresses(grads, dtype, dev, "grads")
     need = QLORA_CLIP_WORKSPACE_BYTES
     if workspace is not None:
-        _need_workspace(workspace, need, dev.index)
-    coef, norm, ws = _fill(dev.index, (coef, norm, workspace), ((_F32, (1,)), (_F64, (1,)), (_U8, (need,))))
+        _need_workspace(workspace, need, dev)
+    coef, norm, ws = _fill(dev, (coef, norm, workspace), ((_F32, (1,)), (_F64, (1,)), (_U8, (need,))))
     address = _tensors().address
-    cp, np_ = address(coef, _F32, (1,), dev.index, "coef"), address(norm, _F64, (1,), dev.index, "norm")
+    cp, np_ = address(coef, _F32, (1,), dev, "coef"), address(norm, _F64, (1,), dev, "norm")
     _check(_load().qlora_clip_grad_norm_batch(len(grads), gp, gd, sizes, float(max_norm), cp, np_,
                                               *_memory(ws), _raw_stream(stream)),
            "qlora_clip_grad_norm_batch")

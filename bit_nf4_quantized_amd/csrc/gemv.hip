@@ -479,11 +479,14 @@ struct FuseT {
 // first row; wave w takes adapters w, w + W, ..., each as one more MFMA pair
 // whose B operand holds the rows of that adapter and zeros. The first one's L2
 // values are loaded behind the first codes and used after the K loop. These
-// variants multiply the dequantised weight itself: the table holds fp16 pairs
-// of q (off by at most 2^-12, where bf16(q) is off by 2^-9), each is multiplied
-// by a' in fp32 and rounded to bf16 once, as the standalone dequant rounds.
-// 13 rows of 32 rank-16 adapters, 11008 -> 4096 (29 MB): 17.8 us after T's 5.5, the
-// call 21.5 (a single adapter's 19.3); bound by the table lookups and latency.
+// variants come closer to the dequantised weight: the table holds fp16 pairs of
+// q (off by at most 2^-12, where bf16(q) is off by 2^-9), each is multiplied by
+// a' in fp32 and rounded to bf16 once. Against the standalone dequant, whose q
+// is fp32, 2.7 % of NF4 weights are the neighbouring bf16.
+// 13 rows of 32 rank-16 adapters, 11008 -> 4096 (29 MB): 18.6 us after T's 5.1, the
+// call 21.4 (a single adapter's 19.3). By count, the codes stream in 4.3 us, the
+// lookups take 1.3 and the VALU about 4, so none of them bounds it alone; where
+// the rest goes has not been measured.
 constexpr int ft_slices(int F) { return F == 1 ? 4 : 12 / F; }
 
 template <int D, bool XL>

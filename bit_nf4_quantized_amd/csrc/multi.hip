@@ -30,11 +30,11 @@
 // Measured, kernel times in us. The streaming kernels are bound by HBM, the GEMM
 // by the matrix cores at the card's power limit:
 //   4096 rows of 12 rank-64 adapters and of none, 4096 -> 11008, forward: prep
-//   29 (113 MB, 3.9 TB/s), NT 14.4 (34 MB of X and its share of L1), sum 9.7, GEMM
+//   29 (113 MB, 3.9 TB/s), NT 14.4 (34 MB of X and its share of L1), sum 10.6, GEMM
 //   360 (1.04 PFLOP/s); the call 370
-//   8192 rows of 16, backward: prep 45 (113 MB, 2.5 TB/s), NT 54 (180 MB, 3.3
-//   TB/s), sum 5.8, GEMM 588 (1.26 PFLOP/s), TN 86 (247 MB, 2.9 TB/s), finish
-//   5.5; the call 744
+//   8192 rows of 16, backward: prep 44 (113 MB, 2.6 TB/s), NT 54 (180 MB, 3.3
+//   TB/s), sum 8.7, GEMM 588 (1.26 PFLOP/s), TN 84 (247 MB, 2.9 TB/s), finish
+//   5.7; the call 744
 //   391 rows of 4 rank-32 adapters, 4096 -> 4096, backward: prep 12, NT 7.4,
 //   sum 6.1, GEMM 27 (0.49 PFLOP/s), TN 9.9, finish 5.4; the call 65
 #include "common.h"

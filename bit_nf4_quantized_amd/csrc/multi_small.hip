@@ -18,8 +18,8 @@
 //                              an adapter's L2 is read once per 16 rows
 // At these sizes the weight stream (0.52 B per weight) and the live adapters
 // are all there is to read; the launches' latency is the rest. 96 rows of 24
-// rank-16 adapters and of none, 4096 -> 11008: T 5.3 us, base 27.7, finish 8.3;
-// the call 40 us. (In the finish, loading the base's first two slices before T's
+// rank-16 adapters and of none, 4096 -> 11008: T 5.3 us, base 27.4, finish 8.2;
+// the call 39 us. (In the finish, loading the base's first two slices before T's
 // took 10.3 us: 186 registers leave two waves per SIMD.)
 #include "common.h"
 #include "launch.h"
@@ -147,7 +147,7 @@ __global__ __launch_bounds__(64 * kTWaves) void small_multi_t_kernel(const uint1
 //     where the partials are written in whole rows.
 // Against 64-row workgroups with X staged through registers (the single
 // adapter's one-pass kernel) X is read half as often from the L2 and the LDS
-// reads per MFMA are half as many: M = 96, 4096 -> 11008 27.9 us (0.31 PFLOP/s,
+// reads per MFMA are half as many: M = 96, 4096 -> 11008 27.4 us (0.32 PFLOP/s,
 // 0.8 TB/s of weights) against 47. A stage takes about 2600 clocks, where its
 // MFMAs need 770, its LDS accesses 1200 and its dequantisation 1200 clocks of a
 // SIMD: two waves per SIMD overlap them in part.

@@ -30,7 +30,12 @@ extern "C" {
  * operands, fp32 accumulation; s T and s U are rounded to bf16 before their
  * second product, outputs once). Rows may come in any order. An adapter
  * without rows gets zero gradients. Sums run in a fixed order. Infinities and
- * NaN of one row or one adapter reach no other row.
+ * NaN of one row or one adapter reach no other row and no other adapter's
+ * gradients. (Within a row whose s T or s U holds an infinity, its product with
+ * an infinity of the adapter's second factor may come out as NaN.) Up to 16
+ * rows may take paths that hold the code values in fp16, so that some weights
+ * are the neighbouring bf16 of the dequantised ones (2.7 % for NF4). There is no
+ * LoRA dropout here.
  *   W            host struct of the quantised weight [N][K].
  *   X            device bf16 [M][K];  dY device bf16 [M][N].
  *   row_adapter  device int32 [M].
@@ -122,7 +127,8 @@ int qlora_preference_loss(const void *logits, qlora_dtype dtype, int64_t pairs, 
  *
  * qlora_clip_grad_norm_batch: qlora_clip_grad_norm's norm and coef over all
  * tensors' gradients (float64 sums in a fixed order; bf16 gradients are
- * squared exactly). coef, norm, ws as there, in device memory.
+ * squared exactly). coef, norm, ws as there, in device memory. Gradients with
+ * NaN have norm NaN and, as there, coef 1.
  *
  * qlora_adamw_batch: qlora_adam_step's update of every tensor, element by
  * element with the same arithmetic (weight decay decoupled from the moments);

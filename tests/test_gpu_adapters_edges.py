@@ -220,3 +220,92 @@ def test_refused_workspaces(api):
         call(torch.empty(n, dtype=torch.uint8, device="cuda"))
         call(torch.empty(n // 4, device="cuda"))
     torch.cuda.synchronize()
+
+
+# ---- one adapter or one row beside the others -----------------------------------------------------
+
+def diverged(c, what, a):
+    """Infinities and NaN in parts of adapter a."""
+    if what == "scale":
+        c.d["scale"][a] = NAN
+    else:
+        t = c.d[what][a]
+        t[t.shape[0] // 2, 3] = INF
+        t[0, t.shape[1] - 1] = -INF
+        t[t.shape[0] - 1, 0] = NAN
+
+
+def mixed_ids(M, A, skip=None):
+    """Every adapter but `skip`, and rows without one (or -1 alone)."""
+    pool = [-1] + [a for a in range(A) if a != skip] + [A]
+    return [pool[i % len(pool)] for i in range(M)] if M > 1 else [pool[1]]
+
+
+SIZES = [(1, 512, 512, 64), (1, 320, 264, 16), (6, 512, 264, 16), (16, 512, 512, 64), (13, 640, 264, 24), (33, 512, 264, 16),
+         (128, 320, 264, 72), (200, 512, 264, 8), (300, 512, 264, 64), (150, 4096, 264, 16), (150, 256, 4096, 16),
+         (700, 256, 264, 72)]
+
+
+@pytest.mark.parametrize("M,K,N,r", SIZES)
+@pytest.mark.parametrize("bad", [0, 2])
+@pytest.mark.parametrize("what", ["L1", "L2", "scale"])
+def test_a_diverged_adapter_stays_alone(api, M, K, N, r, bad, what):
+    """Outputs and gradients of the others' rows and of the others keep their bits, beside its rows or without any."""
+    import torch
+
+    say(f"multi alone M={M} K={K} N={N} r={r} adapter {bad} {what}")
+    for idle in (False, True):
+        c = Case(api, M, K, N, r, 4, "rows")
+        set_ids(c, mixed_ids(M, 4, bad if idle or M == 1 else None))
+        Y, T = c.fwd(want_T=True)
+        back = c.bwd()
+        diverged(c, what, bad)
+        Y2, T2 = c.fwd(want_T=True)
+        back2 = c.bwd()
+        back3 = c.bwd(T=T2)
+        other = c.d["ids"] != bad
+        assert other.any()
+        assert torch.equal(Y2[other], Y[other]) and torch.equal(T2[other], T[other])
+        for b in (back2, back3):
+            assert torch.equal(b[0][other], back[0][other])
+            for a in range(4):
+                if a != bad or idle:
+                    assert torch.equal(b[1][a], back[1][a]) and torch.equal(b[2][a], back[2][a]), a
+
+
+@pytest.mark.parametrize("M,K,N,r", [s for s in SIZES if s[0] > 1])
+@pytest.mark.parametrize("value", [INF, NAN])
+def test_a_row_that_is_not_finite_stays_alone(api, M, K, N, r, value):
+    import torch
+
+    say(f"multi row alone M={M} K={K} N={N} r={r} {value}")
+    c = Case(api, M, K, N, r, 4, "rows")
+    set_ids(c, mixed_ids(M, 4))
+    Y, T = c.fwd(want_T=True)
+    back = c.bwd()
+    for m in (0, 1, M - 1):              # a row without an adapter, one of adapter 0, the last one
+        a = int(c.ids[m])
+        other = torch.arange(M, device="cuda") != m
+        x, dy = c.d["X"][m].clone(), c.d["dY"][m].clone()
+        c.d["X"][m, [0, K // 2, K - 1]] = value
+        c.d["dY"][m, [1, N // 2, N - 1]] = value
+        Y2, T2 = c.fwd(want_T=True)
+        b = c.bwd()
+        c.d["X"][m], c.d["dY"][m] = x, dy
+        assert torch.equal(Y2[other], Y[other]) and torch.equal(T2[other], T[other])
+        assert torch.equal(b[0][other], back[0][other])
+        for k in range(4):
+            if k != a:
+                assert torch.equal(b[1][k], back[1][k]) and torch.equal(b[2][k], back[2][k]), (m, k)
+
+
+def test_norm_of_gradients_with_nan(api):
+    """As the flat call: norm NaN, coef 1; an infinity gives norm inf and coef 0."""
+    import torch
+
+    for value, coef in ((NAN, 1.0), (INF, 0.0)):
+        g = torch.ones(300, device="cuda")
+        g[7] = value
+        flat, both = api.qlora_clip_grad_norm(g, 0.3), api.qlora_clip_grad_norm_batch([g, g.clone()], 0.3)
+        for c, n in (flat, both):
+            assert c.item() == coef and str(n.item()) == str(value)

@@ -50,6 +50,13 @@ ADAPTER_EXPORTS = (
     "qlora_preference_workspace", "qlora_preference_loss",
     "qlora_adam_state_numel", "qlora_clip_grad_norm_batch", "qlora_adamw_batch",
 )
+# every symbol declared in include/qlora_layers.h
+LAYER_EXPORTS = (
+    "qlora_gated_workspace", "qlora_gated_fwd", "qlora_gated_bwd", "qlora_linear_bwd_int8_workspace",
+    "qlora_linear_bwd_int8", "qlora_norm_workspace", "qlora_norm_fwd", "qlora_norm_bwd", "qlora_head_workspace",
+    "qlora_head_loss",
+)
+QLORA_ACTS = {"silu": 0, "gelu": 1}
 QLORA_NOALLOC_SCRATCH_BYTES = (2 << 20) + (64 << 10)
 QLORA_QUANT_BATCH_MAX = 16
 QLORA_CLIP_WORKSPACE_BYTES = 8192
@@ -91,6 +98,12 @@ class QAdamState(ctypes.Structure):
 
     _fields_ = [("bits", ctypes.c_int32), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class QInt8Values(ctypes.Structure):
+    """Mirror of the C struct qlora_int8_values (host struct of device pointers)."""
+
+    _fields_ = [("codes", ctypes.c_void_p), ("absmax", ctypes.c_void_p)]
 
 
 class QLoRAError(RuntimeError):
@@ -182,7 +195,19 @@ def _load():
     lib.qlora_adam_state_numel.argtypes = [ctypes.c_int, P(i64), P(i64)]
     lib.qlora_clip_grad_norm_batch.argtypes = [ctypes.c_int, vp, ctypes.c_int, vp, ctypes.c_float, vp, vp, vp, sz, vp]
     lib.qlora_adamw_batch.argtypes = [ctypes.c_int, vp, vp, ctypes.c_int, vp, vp, P(QAdamState), P(AdamParams), vp, vp]
-    for name in ADAPTER_EXPORTS:
+    ci, P8 = ctypes.c_int, P(QInt8Values)
+    lib.qlora_gated_workspace.argtypes = [i64, i64, i64, ci, ci, P(sz)]
+    lib.qlora_gated_fwd.argtypes = [P(QNF4), P(QNF4), vp, i64, vp, vp, ci, f32, ci, vp, vp, P8, P8, vp, sz, vp]
+    lib.qlora_gated_bwd.argtypes = [P(QNF4), P(QNF4), vp, P8, vp, i64, vp, vp, ci, f32, ci, vp, P8, P8, vp, vp, vp, ci,
+                                    vp, sz, vp]
+    lib.qlora_linear_bwd_int8_workspace.argtypes = [i64, i64, i64, ci, P(sz)]
+    lib.qlora_linear_bwd_int8.argtypes = [P(QNF4), P8, vp, i64, vp, vp, ci, f32, vp, vp, vp, vp, ci, vp, sz, vp]
+    lib.qlora_norm_workspace.argtypes = [i64, i64, P(sz)]
+    lib.qlora_norm_fwd.argtypes = [vp, ci, vp, ci, vp, ci, i64, i64, f32, vp, P8, vp, vp, vp]
+    lib.qlora_norm_bwd.argtypes = [vp, vp, ci, vp, vp, ci, vp, i64, i64, vp, vp, vp, vp, sz, vp]
+    lib.qlora_head_workspace.argtypes = [i64, i64, i64, ci, ci, ci, P(sz)]
+    lib.qlora_head_loss.argtypes = [vp, vp, vp, vp, i64, i64, i64, f32, f32, vp, vp, vp, vp, ci, vp, sz, vp]
+    for name in ADAPTER_EXPORTS + LAYER_EXPORTS:
         getattr(lib, name).restype = ctypes.c_int
     _LIB = lib
     return lib
@@ -249,7 +274,7 @@ def _need(t, dtype, shape, name):
 
 
 _TENSORS = None
-_F32, _BF16, _I32, _I64, _F64, _U8 = range(6)   # dtype numbers of the tensor module
+_F32, _BF16, _I32, _I64, _F64, _U8, _I8 = range(7)   # dtype numbers of the tensor module
 
 
 def _tensors():
@@ -1043,6 +1068,401 @@ def qlora_linear_multi_bwd(q: NF4Tensor, X, dY, row_adapter, L1, L2, scale, T=No
                                           *_memory(ws), _raw_stream(stream)),
            "qlora_linear_multi_bwd")
     return dX, dL1, dL2
+
+
+# ---- the rest of a training step ----------------------------------------------------
+
+def _on_device(fn):
+    """Run a wrapper with the device of its first tensor argument as the current one (the kernels, the stream
+    and the memory allocated here then belong to it); a ``stream`` has to be of that device."""
+    import functools
+
+    @functools.wraps(fn)
+    def wrapper(*args, **kwargs):
+        import torch
+
+        dev = next((a.get_device() for a in args if isinstance(a, torch.Tensor)), -1)
+        stream = kwargs.get("stream")
+        if stream is not None and dev >= 0 and stream.device.index != dev:
+            raise ValueError(f"stream must be of device {dev}, got {stream.device.index}")
+        if dev < 0 or dev == torch.cuda.current_device():
+            return fn(*args, **kwargs)
+        with torch.cuda.device(dev):
+            return fn(*args, **kwargs)
+
+    return wrapper
+
+
+def _int8_values(v, numel, dev, name):
+    """(codes, absmax) of blocks of 64, checked, as a C struct."""
+    if not isinstance(v, (tuple, list)) or len(v) != 2:
+        raise TypeError(f"{name} must be a (codes, absmax) pair")
+    address = _tensors().address
+    return QInt8Values(address(v[0], _I8, (numel,), dev, name + " codes"),
+                       address(v[1], _F32, (numel // QLORA_BLOCK,), dev, name + " absmax"))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def _float_type(t, name):
+    """(qlora_dtype, dtype number) of a float32 or bfloat16 tensor."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype == torch.float32:
+        return QLORA_F32, _F32
+    if t.dtype == torch.bfloat16:
+        return QLORA_BF16, _BF16
+    raise TypeError(f"{name} must be float32 or bfloat16")
+
+
+def _grad_type(grad_dtype):
+    import torch
+
+    grad_dtype = torch.float32 if grad_dtype is None else grad_dtype
+    if grad_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("grad_dtype must be float32 or bfloat16")
+    return (QLORA_F32, _F32) if grad_dtype == torch.float32 else (QLORA_BF16, _BF16)
+
+
+def _ready_workspace(workspace, need, dev):
+    """The caller's workspace, checked, or a new one: address and size."""
+    if workspace is not None:
+        _need_workspace(workspace, need, dev)
+    else:
+        workspace, = _tensors().empties(dev, _U8, (max(need, 256),))
+    return workspace
+
+
+class GatedOut(NamedTuple):
+    """Result of qlora_gated_fwd; T, gate8 and up8 are None unless asked for."""
+
+    A: "torch.Tensor"       # bf16 [M, F]
+    T: "torch.Tensor"       # bf16 [2, M, r]
+    gate8: tuple            # (int8 codes [M * F], float32 absmax [M * F / 64])
+    up8: tuple
+
+
+def qlora_gated_workspace(M: int, K: int, F: int, r: int, backward: bool = False) -> int:
+    out = ctypes.c_size_t()
+    _check(_load().qlora_gated_workspace(M, K, F, r, int(backward), ctypes.byref(out)), "qlora_gated_workspace")
+    return out.value
+
+
+def _act(act):
+    if act not in QLORA_ACTS:
+        raise ValueError(f"act must be one of {sorted(QLORA_ACTS)}")
+    return QLORA_ACTS[act]
+
+
+def _gated_operands(gate, up, L1, L2, dev):
+    """(K, F, r), addresses of L1 and L2."""
+    K, F = gate.cols, gate.rows
+    if (up.rows, up.cols) != (F, K):
+        raise ValueError("gate and up must have one shape")
+    if L1.dim() != 3:
+        raise ValueError("L1 must be [2, K, r]")
+    if gate.codes.get_device() != dev or up.codes.get_device() != dev:
+        raise ValueError(f"the weights must be on device {dev}")
+    r = L1.shape[2]
+    address = _tensors().address
+    return (K, F, r), address(L1, _BF16, (2, K, r), dev, "L1"), address(L2, _BF16, (2, r, F), dev, "L2")
+
+
+@_on_device
+@_on_stream
+def _gated_fwd(X, gate, up, L1, L2, scale, act, want_T, want_int8, A, T_out, workspace, stream=None):
+    if X.dim() != 2:
+        raise ValueError("X must be [M, K]")
+    dev = X.get_device()
+    (K, F, r), p1, p2 = _gated_operands(gate, up, L1, L2, dev)
+    M = X.shape[0]
+    address = _tensors().address
+    xp = address(X, _BF16, (M, K), dev, "X")
+    act = _act(act)
+    if want_int8 and F % QLORA_BLOCK:
+        raise ValueError("int8 values need F to be a multiple of 64")
+    need = qlora_gated_workspace(M, K, F, r)
+    ws = _ready_workspace(workspace, need, dev)
+    A, = _fill(dev, (A,), ((_BF16, (M, F)),))
+    if want_T and T_out is None:
+        T_out, = _tensors().empties(dev, _BF16, (2, M, r))
+    g8 = u8 = gs = us = None
+    if want_int8:
+        n = M * F
+        gc, ga, uc, ua = _tensors().empties(dev, _I8, (n,), _F32, (n // QLORA_BLOCK,), _I8, (n,), _F32, (n // QLORA_BLOCK,))
+        g8, u8 = (gc, ga), (uc, ua)
+        gs, us = QInt8Values(gc.data_ptr(), ga.data_ptr()), QInt8Values(uc.data_ptr(), ua.data_ptr())
+    ap = address(A, _BF16, (M, F), dev, "A")
+    tp = None if T_out is None else address(T_out, _BF16, (2, M, r), dev, "T_out")
+    sg, su = gate.struct(), up.struct()
+    _check(_load().qlora_gated_fwd(ctypes.byref(sg), ctypes.byref(su), xp, M, p1, p2, r, float(scale), act, ap, tp,
+                                   _ref(gs), _ref(us), *_memory(ws), _raw_stream(stream)), "qlora_gated_fwd")
+    return GatedOut(A, T_out, g8, u8)
+
+
+def qlora_gated_fwd(gate: NF4Tensor, up: NF4Tensor, X, L1, L2, scale: float, act: str = "silu", want_T: bool = False,
+                    want_int8: bool = False, A=None, T_out=None, workspace=None, stream=None) -> GatedOut:
+    """A = act(G) * U, G = X dequant(gate)^T + scale (X L1[0]) L2[0], U likewise from ``up`` and L1[1], L2[1];
+    L1 [2, K, r], L2 [2, r, F] bf16, act "silu" or "gelu" (its tanh form). ``want_T``: T = bf16(X L1[i]);
+    ``want_int8``: G and U as int8 values (codes, absmax of 64) for the backward pass."""
+    return _gated_fwd(X, gate, up, L1, L2, scale, act, want_T, want_int8, A, T_out, workspace, stream=stream)
+
+
+@_on_device
+@_on_stream
+def _gated_bwd(dA, gate, up, X, L1, L2, scale, act, T, gate8, up8, need_dX, grad_dtype, dX, dL1, dL2, workspace,
+               stream=None):
+    if dA.dim() != 2:
+        raise ValueError("dA must be [M, F]")
+    dev = dA.get_device()
+    (K, F, r), p1, p2 = _gated_operands(gate, up, L1, L2, dev)
+    M = dA.shape[0]
+    gd, gtype = _grad_type(grad_dtype)
+    address = _tensors().address
+    ap = address(dA, _BF16, (M, F), dev, "dA")
+    act = _act(act)
+    xp = x8 = None
+    if isinstance(X, (tuple, list)):
+        x8 = _int8_values(X, M * K, dev, "X")
+    else:
+        xp = address(X, _BF16, (M, K), dev, "X")
+    if (gate8 is None) != (up8 is None):
+        raise ValueError("gate8 and up8 come together")
+    gs = us = None
+    if gate8 is not None:
+        gs, us = _int8_values(gate8, M * F, dev, "gate8"), _int8_values(up8, M * F, dev, "up8")
+    tp = None if T is None else address(T, _BF16, (2, M, r), dev, "T")
+    need = qlora_gated_workspace(M, K, F, r, True)
+    ws = _ready_workspace(workspace, need, dev)
+    dxp = None
+    if not need_dX:
+        dX = None
+    else:
+        dX, = _fill(dev, (dX,), ((_BF16, (M, K)),))
+        dxp = address(dX, _BF16, (M, K), dev, "dX")
+    dL1, dL2 = _fill(dev, (dL1, dL2), ((gtype, (2, K, r)), (gtype, (2, r, F))))
+    d1, d2 = address(dL1, gtype, (2, K, r), dev, "dL1"), address(dL2, gtype, (2, r, F), dev, "dL2")
+    sg, su = gate.struct(), up.struct()
+    _check(_load().qlora_gated_bwd(ctypes.byref(sg), ctypes.byref(su), xp, _ref(x8), ap, M, p1, p2, r, float(scale), act,
+                                   tp, _ref(gs), _ref(us), dxp, d1, d2, gd, *_memory(ws), _raw_stream(stream)),
+           "qlora_gated_bwd")
+    return dX, dL1, dL2
+
+
+def qlora_gated_bwd(gate: NF4Tensor, up: NF4Tensor, X, dA, L1, L2, scale: float, act: str = "silu", T=None, gate8=None,
+                    up8=None, need_dX: bool = True, grad_dtype=None, dX=None, dL1=None, dL2=None, workspace=None,
+                    stream=None):
+    """Returns (dX or None, dL1 [2, K, r], dL2 [2, r, F]) of qlora_gated_fwd for upstream gradient dA. X: bf16
+    [M, K], or its int8 values (codes, absmax). ``gate8``, ``up8``: those of G and U from the forward pass; without
+    them both are computed again from X."""
+    return _gated_bwd(dA, gate, up, X, L1, L2, scale, act, T, gate8, up8, need_dX, grad_dtype, dX, dL1, dL2, workspace,
+                      stream=stream)
+
+
+def qlora_linear_bwd_int8_workspace(M: int, K: int, N: int, r: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_load().qlora_linear_bwd_int8_workspace(M, K, N, r, ctypes.byref(out)), "qlora_linear_bwd_int8_workspace")
+    return out.value
+
+
+@_on_device
+@_on_stream
+def _linear_bwd_int8(dY, q, X8, L1, L2, scale, T, need_dX, grad_dtype, dX, dL1, dL2, workspace, stream=None):
+    if dY.dim() != 2 or L1.dim() != 2:
+        raise ValueError("dY must be [M, N] and L1 [K, r]")
+    dev = dY.get_device()
+    M, K, N, r = dY.shape[0], q.cols, q.rows, L1.shape[1]
+    if q.codes.get_device() != dev:
+        raise ValueError(f"the weight must be on device {dev}")
+    gd, gtype = _grad_type(grad_dtype)
+    address = _tensors().address
+    yp = address(dY, _BF16, (M, N), dev, "dY")
+    x8 = _int8_values(X8, M * K, dev, "X8")
+    p1, p2 = address(L1, _BF16, (K, r), dev, "L1"), address(L2, _BF16, (r, N), dev, "L2")
+    tp = None if T is None else address(T, _BF16, (M, r), dev, "T")
+    need = qlora_linear_bwd_int8_workspace(M, K, N, r)
+    ws = _ready_workspace(workspace, need, dev)
+    dxp = None
+    if not need_dX:
+        dX = None
+    else:
+        dX, = _fill(dev, (dX,), ((_BF16, (M, K)),))
+        dxp = address(dX, _BF16, (M, K), dev, "dX")
+    dL1, dL2 = _fill(dev, (dL1, dL2), ((gtype, (K, r)), (gtype, (r, N))))
+    d1, d2 = address(dL1, gtype, (K, r), dev, "dL1"), address(dL2, gtype, (r, N), dev, "dL2")
+    st = q.struct()
+    _check(_load().qlora_linear_bwd_int8(ctypes.byref(st), ctypes.byref(x8), yp, M, p1, p2, r, float(scale), tp, dxp, d1,
+                                         d2, gd, *_memory(ws), _raw_stream(stream)), "qlora_linear_bwd_int8")
+    return dX, dL1, dL2
+
+
+def qlora_linear_bwd_int8(q: NF4Tensor, X8, dY, L1, L2, scale: float, T=None, need_dX: bool = True, grad_dtype=None,
+                          dX=None, dL1=None, dL2=None, workspace=None, stream=None):
+    """qlora_linear_bwd with the input as int8 values: X8 = (codes [M * K], absmax [M * K / 64]), as
+    qlora_int8_quantize(X) or qlora_norm_fwd(..., want_int8=True) give them."""
+    return _linear_bwd_int8(dY, q, X8, L1, L2, scale, T, need_dX, grad_dtype, dX, dL1, dL2, workspace, stream=stream)
+
+
+class NormOut(NamedTuple):
+    """Result of qlora_norm_fwd."""
+
+    y: "torch.Tensor"       # bf16 [M, K], or None
+    h: "torch.Tensor"       # x + residual, the residual's type; x itself without a residual
+    rstd: "torch.Tensor"    # float32 [M]
+    int8: tuple             # y's (codes, absmax), or None
+
+
+class NormGrads(NamedTuple):
+    """Result of qlora_norm_bwd."""
+
+    dh: "torch.Tensor"       # h's type [M, K]: of x and of the residual
+    dx16: "torch.Tensor"     # bf16 [M, K], or None
+    dweight: "torch.Tensor"  # float32 [K], or None
+
+
+def qlora_norm_workspace(M: int, K: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_load().qlora_norm_workspace(M, K, ctypes.byref(out)), "qlora_norm_workspace")
+    return out.value
+
+
+@_on_device
+@_on_stream
+def qlora_norm_fwd(x, weight=None, eps: float = 1e-6, residual=None, want_y: bool = True, want_int8: bool = False,
+                   y=None, h=None, rstd=None, stream=None) -> NormOut:
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight for float32 or bfloat16 [M, K] (each tensor its own);
+    y in bf16, with ``want_int8`` also as int8 values. ``h`` may be the residual's own tensor."""
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    dev = x.get_device()
+    address = _tensors().address
+    xd, xt = _float_type(x, "x")
+    xp = address(x, xt, (M, K), -1, "x")
+    rp = hp = wp = None
+    rd = wd = QLORA_F32
+    if residual is not None:
+        rd, rt = _float_type(residual, "residual")
+        rp = address(residual, rt, (M, K), dev, "residual")
+    elif h is not None:
+        raise ValueError("h comes with a residual")
+    if weight is not None:
+        wd, wt = _float_type(weight, "weight")
+        wp = address(weight, wt, (K,), dev, "weight")
+    if want_int8 and K % QLORA_BLOCK:
+        raise ValueError("int8 values need K to be a multiple of 64")
+    if residual is not None:
+        h, = _fill(dev, (h,), ((rt, (M, K)),))
+        hp = address(h, rt, (M, K), dev, "h")
+    rstd, = _fill(dev, (rstd,), ((_F32, (M,)),))
+    yp = q = qs = None
+    if want_y:
+        y, = _fill(dev, (y,), ((_BF16, (M, K)),))
+        yp = address(y, _BF16, (M, K), dev, "y")
+    else:
+        y = None
+    if want_int8:
+        q = tuple(_tensors().empties(dev, _I8, (M * K,), _F32, (M * K // QLORA_BLOCK,)))
+        qs = QInt8Values(q[0].data_ptr(), q[1].data_ptr())
+    _check(_load().qlora_norm_fwd(xp, xd, rp, rd, wp, wd, M, K, float(eps), yp, _ref(qs), hp,
+                                  address(rstd, _F32, (M,), dev, "rstd"), _raw_stream(stream)), "qlora_norm_fwd")
+    return NormOut(y, x if h is None else h, rstd, q)
+
+
+@_on_device
+@_on_stream
+def qlora_norm_bwd(dy, h, rstd, weight=None, dres=None, need_dweight: bool = True, want_dx16: bool = False, dh=None,
+                   dx16=None, dweight=None, workspace=None, stream=None) -> NormGrads:
+    """The gradient dh of x and of the residual for upstream gradients dy (of y, bf16) and dres (of h, its type, or
+    None), and of the weight; h and rstd as qlora_norm_fwd returned them."""
+    if h.dim() != 2:
+        raise ValueError("h must be [M, K]")
+    M, K = h.shape
+    dev = h.get_device()
+    address = _tensors().address
+    hd, ht = _float_type(h, "h")
+    hp = address(h, ht, (M, K), -1, "h")
+    yp = address(dy, _BF16, (M, K), dev, "dy")
+    sp = address(rstd, _F32, (M,), dev, "rstd")
+    wp = rp = xp = gp = None
+    wd = QLORA_F32
+    if weight is not None:
+        wd, wt = _float_type(weight, "weight")
+        wp = address(weight, wt, (K,), dev, "weight")
+    if dres is not None:
+        rp = address(dres, ht, (M, K), dev, "dres")
+    dh, = _fill(dev, (dh,), ((ht, (M, K)),))
+    if want_dx16:
+        dx16, = _fill(dev, (dx16,), ((_BF16, (M, K)),))
+        xp = address(dx16, _BF16, (M, K), dev, "dx16")
+    else:
+        dx16 = None
+    mem = (None, 0)
+    if need_dweight:
+        dweight, = _fill(dev, (dweight,), ((_F32, (K,)),))
+        gp = address(dweight, _F32, (K,), dev, "dweight")
+        ws = _ready_workspace(workspace, qlora_norm_workspace(M, K), dev)
+        mem = _memory(ws)
+    else:
+        dweight = None
+    _check(_load().qlora_norm_bwd(yp, hp, hd, sp, wp, wd, rp, M, K, address(dh, ht, (M, K), dev, "dh"), xp, gp, *mem,
+                                  _raw_stream(stream)), "qlora_norm_bwd")
+    return NormGrads(dh, dx16, dweight)
+
+
+class HeadLoss(NamedTuple):
+    """Result of qlora_head_loss."""
+
+    loss: "torch.Tensor"    # float32 [1]
+    nll: "torch.Tensor"     # float32 [M]
+    dH: "torch.Tensor"      # bf16 [M, K], or None
+    dW: "torch.Tensor"      # grad_dtype [V, K], or None
+
+
+def qlora_head_workspace(M: int, K: int, V: int, dH: bool = True, dW: bool = False, grad_dtype: int = QLORA_F32) -> int:
+    out = ctypes.c_size_t()
+    _check(_load().qlora_head_workspace(M, K, V, int(dH), int(dW), grad_dtype, ctypes.byref(out)),
+           "qlora_head_workspace")
+    return out.value
+
+
+@_on_device
+@_on_stream
+def qlora_head_loss(H, W, labels, weights=None, divisor: float = 0.0, grad_scale: float = 1.0, need_dH: bool = True,
+                    need_dW: bool = False, grad_dtype=None, dH=None, dW=None, workspace=None, stream=None) -> HeadLoss:
+    """Softmax cross entropy of the logits H W^T (bf16 [M, K], [V, K]; the logits are not stored) against int64
+    labels [M]: rows with a label in [0, V) count, with float32 ``weights`` [M] or 1; the sum is divided by
+    ``divisor`` (0: the number of counted rows). Returns the loss, each row's, and grad_scale times the gradients
+    dH (bf16) and, with ``need_dW``, dW (grad_dtype)."""
+    if H.dim() != 2 or W.dim() != 2:
+        raise ValueError("H must be [M, K] and W [V, K]")
+    (M, K), V = H.shape, W.shape[0]
+    dev = H.get_device()
+    gd, gtype = _grad_type(grad_dtype)
+    address = _tensors().address
+    hp, wp = address(H, _BF16, (M, K), -1, "H"), address(W, _BF16, (V, K), dev, "W")
+    lp = address(labels, _I64, (M,), dev, "labels")
+    sp = None if weights is None else address(weights, _F32, (M,), dev, "weights")
+    loss, nll = _tensors().empties(dev, _F32, (1,), _F32, (M,))
+    dhp = dwp = None
+    if need_dH:
+        dH, = _fill(dev, (dH,), ((_BF16, (M, K)),))
+        dhp = address(dH, _BF16, (M, K), dev, "dH")
+    else:
+        dH = None
+    if need_dW:
+        dW, = _fill(dev, (dW,), ((gtype, (V, K)),))
+        dwp = address(dW, gtype, (V, K), dev, "dW")
+    else:
+        dW = None
+    ws = _ready_workspace(workspace, qlora_head_workspace(M, K, V, need_dH, need_dW, gd), dev)
+    _check(_load().qlora_head_loss(hp, wp, lp, sp, M, K, V, float(divisor), float(grad_scale), loss.data_ptr(),
+                                   nll.data_ptr(), dhp, dwp, gd, *_memory(ws), _raw_stream(stream)), "qlora_head_loss")
+    return HeadLoss(loss, nll, dH, dW)
 
 
 # ---- helpers for moving numpy data (bf16 as uint16 bits) ------------------------------

@@ -1,7 +1,8 @@
 // C ABI of the QLoRA NF4 library: host-side validation, sizes, the NF4
-// codebook, and stream-ordered kernel launches. See include/qlora_nf4.h
-// and include/qlora_adapters.h.
+// codebook, and stream-ordered kernel launches. See include/qlora_nf4.h,
+// include/qlora_adapters.h and include/qlora_layers.h.
 #include "qlora_adapters.h"
+#include "qlora_layers.h"
 #include "qlora_nf4.h"
 
 #include <math.h>
@@ -27,6 +28,9 @@ int hip_fail(hipError_t e) {
 }
 
 static_assert(qlora::kMultiMaxRows == QLORA_MULTI_MAX_ROWS && qlora::kMultiMaxAdapters == QLORA_MULTI_MAX_ADAPTERS,
+              "limits of the header and of the kernels");
+static_assert(qlora::kLayerMaxRows == QLORA_LAYER_MAX_ROWS && qlora::kNormMaxK == QLORA_NORM_MAX_COLS &&
+                  qlora::kHeadMaxVocab == QLORA_HEAD_MAX_VOCAB && qlora::kGatedMaxCols == QLORA_GATED_MAX_COLS,
               "limits of the header and of the kernels");
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -764,6 +768,270 @@ int qlora_preference_loss(const void* logits, qlora_dtype dtype, int64_t pairs, 
   c.ws = ws;
   (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
   const hipError_t e = qlora::launch_preference(c, stream);
+  return e == hipSuccess ? QLORA_OK : hip_fail(e);
+}
+
+// ---- the rest of a training step (qlora_layers.h) ----------------------------------------------
+
+static bool off_by(const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
+
+// Optional int8 values: absent, or both buffers there (QLORA_OK), aligned.
+static int check_int8(const qlora_int8_values* v, bool rows) {
+  if (!v || !rows) return QLORA_OK;
+  if (!v->codes || !v->absmax) return QLORA_ERR_ARG;
+  return aligned16(v->codes) && !off_by(v->absmax, 3u) ? QLORA_OK : QLORA_ERR_ALIGN;
+}
+
+static qlora::Int8Values int8_of(const qlora_int8_values* v) {
+  return v ? qlora::Int8Values{v->codes, v->absmax} : qlora::Int8Values{nullptr, nullptr};
+}
+
+static int check_gated_shape(int64_t M, int64_t K, int64_t F, int r) {
+  if (r < 8 || r > QLORA_MAX_RANK || (r % 8) != 0) return QLORA_ERR_ARG;
+  if (M < 0 || K <= 0 || F <= 0 || (K % QLORA_BLOCK) != 0 || (F % 8) != 0) return QLORA_ERR_SHAPE;
+  if (M > QLORA_LAYER_MAX_ROWS || K >= QLORA_GATED_MAX_COLS || F >= QLORA_GATED_MAX_COLS) return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
+int qlora_gated_workspace(int64_t M, int64_t K, int64_t F, int r, int backward, size_t* bytes) {
+  if (!bytes) return QLORA_ERR_ARG;
+  const int st = check_gated_shape(M, K, F, r);
+  if (st != QLORA_OK) return st;
+  *bytes = qlora::gated_workspace_layout(M, K, F, r, backward != 0).total;
+  return QLORA_OK;
+}
+
+// The arguments that both passes share.
+static int check_gated(const qlora_nf4* gate, const qlora_nf4* up, int64_t M, const void* L1, const void* L2, int r,
+                       float scale, qlora_act act, const void* T, const qlora_int8_values* gate8,
+                       const qlora_int8_values* up8) {
+  if (!valid_nf4(gate) || !valid_nf4(up) || !isfinite(scale)) return QLORA_ERR_ARG;
+  if (act != QLORA_ACT_SILU && act != QLORA_ACT_GELU_TANH) return QLORA_ERR_ARG;
+  if (gate->rows != up->rows || gate->cols != up->cols) return QLORA_ERR_SHAPE;
+  int st = check_gated_shape(M, gate->cols, gate->rows, r);
+  if (st != QLORA_OK) return st;
+  if (!L1 || !L2 || (gate8 == nullptr) != (up8 == nullptr)) return QLORA_ERR_ARG;
+  if (gate8 && gate->rows % QLORA_BLOCK != 0) return QLORA_ERR_SHAPE;
+  st = check_int8(gate8, M > 0);
+  if (st == QLORA_OK) st = check_int8(up8, M > 0);
+  if (st != QLORA_OK) return st;
+  if (!aligned16(gate->codes) || !aligned16(up->codes) || !aligned16(L1) || !aligned16(L2) || !aligned16(T))
+    return QLORA_ERR_ALIGN;
+  return QLORA_OK;
+}
+
+static qlora::GatedBase gated_base(const qlora_nf4* gate, const qlora_nf4* up) {
+  return qlora::GatedBase{view_of(gate), view_of(up), tables(gate->qtype).tab, tables(up->qtype).tab};
+}
+
+int qlora_gated_fwd(const qlora_nf4* gate, const qlora_nf4* up, const uint16_t* X, int64_t M, const uint16_t* L1,
+                    const uint16_t* L2, int r, float scale, qlora_act act, uint16_t* A, uint16_t* T_out,
+                    const qlora_int8_values* gate8, const qlora_int8_values* up8, void* ws, size_t ws_bytes,
+                    hipStream_t stream) {
+  const int st = check_gated(gate, up, M, L1, L2, r, scale, act, T_out, gate8, up8);
+  if (st != QLORA_OK) return st;
+  if (M == 0) return QLORA_OK;
+  if (!X || !A) return QLORA_ERR_ARG;
+  if (!ws) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(X) || !aligned16(A) || !aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (ws_bytes < qlora::gated_workspace_layout(M, gate->cols, gate->rows, r, false).total) return QLORA_ERR_WORKSPACE;
+  const qlora::Int8Values g8 = int8_of(gate8), u8 = int8_of(up8);
+  (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
+  const hipError_t e = qlora::gated_forward(gated_base(gate, up), X, M, L1, L2, r, scale, (int)act, A, T_out,
+                                            gate8 ? &g8 : nullptr, up8 ? &u8 : nullptr, ws, stream);
+  return e == hipSuccess ? QLORA_OK : hip_fail(e);
+}
+
+int qlora_gated_bwd(const qlora_nf4* gate, const qlora_nf4* up, const uint16_t* X, const qlora_int8_values* X8,
+                    const uint16_t* dA, int64_t M, const uint16_t* L1, const uint16_t* L2, int r, float scale,
+                    qlora_act act, const uint16_t* T, const qlora_int8_values* gate8, const qlora_int8_values* up8,
+                    uint16_t* dX, void* dL1, void* dL2, qlora_dtype grad_dtype, void* ws, size_t ws_bytes,
+                    hipStream_t stream) {
+  int st = check_gated(gate, up, M, L1, L2, r, scale, act, T, gate8, up8);
+  if (st != QLORA_OK) return st;
+  if (grad_dtype != QLORA_F32 && grad_dtype != QLORA_BF16) return QLORA_ERR_ARG;
+  if (!dL1 || !dL2 || (M > 0 && (!dA || (X == nullptr) == (X8 == nullptr)))) return QLORA_ERR_ARG;
+  st = check_int8(X8, M > 0);
+  if (st != QLORA_OK) return st;
+  if (!ws) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(X) || !aligned16(dA) || !aligned16(dX) || !aligned16(dL1) || !aligned16(dL2) || !aligned16(ws))
+    return QLORA_ERR_ALIGN;
+  if (ws_bytes < qlora::gated_workspace_layout(M, gate->cols, gate->rows, r, true).total) return QLORA_ERR_WORKSPACE;
+  const qlora::Int8Values g8 = int8_of(gate8), u8 = int8_of(up8), x8 = int8_of(X8);
+  (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
+  const hipError_t e = qlora::gated_backward(gated_base(gate, up), X, X8 ? &x8 : nullptr, dA, M, L1, L2, r, scale,
+                                             (int)act, T, gate8 ? &g8 : nullptr, up8 ? &u8 : nullptr, dX, dL1, dL2,
+                                             grad_dtype == QLORA_BF16, ws, stream);
+  return e == hipSuccess ? QLORA_OK : hip_fail(e);
+}
+
+int qlora_linear_bwd_int8_workspace(int64_t M, int64_t K, int64_t N, int r, size_t* bytes) {
+  if (M > QLORA_LAYER_MAX_ROWS) return QLORA_ERR_SHAPE;
+  const int st = qlora_linear_workspace(M, K, N, r, bytes);
+  if (st != QLORA_OK) return st;
+  if (M > 0 && M * K > QLORA_INT8_MAX_NUMEL) return QLORA_ERR_SHAPE;
+  *bytes = qlora::align_up(*bytes, 256) + qlora::align_up((size_t)M * (size_t)K * 2, 256);
+  return QLORA_OK;
+}
+
+int qlora_linear_bwd_int8(const qlora_nf4* W, const qlora_int8_values* X8, const uint16_t* dY, int64_t M,
+                          const uint16_t* L1, const uint16_t* L2, int r, float scale, const uint16_t* T, uint16_t* dX,
+                          void* dL1, void* dL2, qlora_dtype grad_dtype, void* ws, size_t ws_bytes,
+                          hipStream_t stream) {
+  int st = check_linear(W, M, r, scale);
+  if (st != QLORA_OK) return st;
+  if (M > 0 && !X8) return QLORA_ERR_ARG;
+  st = check_int8(X8, M > 0);
+  if (st != QLORA_OK) return st;
+  size_t need = 0;
+  st = qlora_linear_bwd_int8_workspace(M, W->cols, W->rows, r, &need);
+  if (st != QLORA_OK) return st;
+  if (!ws) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  if (ws_bytes < need) return QLORA_ERR_WORKSPACE;
+  uint16_t* X = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + need -
+                                            qlora::align_up((size_t)M * (size_t)W->cols * 2, 256));
+  // every check of the linear first, so that nothing is enqueued for a refused call
+  if (grad_dtype != QLORA_F32 && grad_dtype != QLORA_BF16) return QLORA_ERR_ARG;
+  if (!L1 || !L2 || !dL1 || !dL2 || (M > 0 && !dY)) return QLORA_ERR_ARG;
+  if (!aligned16(dY) || !aligned16(L1) || !aligned16(L2) || !aligned16(T) || !aligned16(dX) || !aligned16(dL1) ||
+      !aligned16(dL2))
+    return QLORA_ERR_ALIGN;
+  if (M > 0) {
+    (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
+    const hipError_t e = qlora::launch_int8_dequantize(X8->codes, X8->absmax, M * W->cols, 6, X, true, stream);
+    if (e != hipSuccess) return hip_fail(e);
+  }
+  return linear_bwd_impl(W, X, dY, M, L1, L2, r, scale, T, dX, dL1, dL2, grad_dtype, ws, ws_bytes, stream, nullptr);
+}
+
+static int check_norm(int64_t M, int64_t K, qlora_dtype a, qlora_dtype b, qlora_dtype c) {
+  for (qlora_dtype t : {a, b, c})
+    if (t != QLORA_F32 && t != QLORA_BF16) return QLORA_ERR_ARG;
+  if (M < 0 || M > QLORA_LAYER_MAX_ROWS || K < 8 || K > QLORA_NORM_MAX_COLS || (K % 8) != 0) return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
+int qlora_norm_workspace(int64_t M, int64_t K, size_t* bytes) {
+  if (!bytes) return QLORA_ERR_ARG;
+  const int st = check_norm(M, K, QLORA_F32, QLORA_F32, QLORA_F32);
+  if (st != QLORA_OK) return st;
+  *bytes = qlora::align_up((size_t)qlora::norm_slices(M) * (size_t)K * 4 + 1, 256);
+  return QLORA_OK;
+}
+
+int qlora_norm_fwd(const void* x, qlora_dtype x_dtype, const void* residual, qlora_dtype stream_dtype,
+                   const void* weight, qlora_dtype weight_dtype, int64_t M, int64_t K, float eps, uint16_t* y,
+                   const qlora_int8_values* y8, void* h, float* rstd, hipStream_t stream) {
+  int st = check_norm(M, K, x_dtype, residual ? stream_dtype : x_dtype, weight ? weight_dtype : x_dtype);
+  if (st != QLORA_OK) return st;
+  if (!isfinite(eps) || eps < 0.0f) return QLORA_ERR_ARG;
+  if (y8 && K % QLORA_BLOCK != 0) return QLORA_ERR_SHAPE;
+  if (M == 0) return QLORA_OK;
+  if (!x || (residual == nullptr) != (h == nullptr)) return QLORA_ERR_ARG;
+  st = check_int8(y8, true);
+  if (st != QLORA_OK) return st;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(y) || !aligned16(h) || off_by(rstd, 3u))
+    return QLORA_ERR_ALIGN;
+  qlora::NormFwd c{};
+  c.x = x;
+  c.res = residual;
+  c.x_bf16 = x_dtype == QLORA_BF16;
+  c.res_bf16 = stream_dtype == QLORA_BF16;
+  c.w = weight;
+  c.w_bf16 = weight_dtype == QLORA_BF16;
+  c.M = M;
+  c.K = K;
+  c.eps = eps;
+  c.y = y;
+  c.codes = y8 ? y8->codes : nullptr;
+  c.absmax = y8 ? y8->absmax : nullptr;
+  c.h = h;
+  c.rstd = rstd;
+  (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
+  const hipError_t e = qlora::launch_norm_fwd(c, stream);
+  return e == hipSuccess ? QLORA_OK : hip_fail(e);
+}
+
+int qlora_norm_bwd(const uint16_t* dy, const void* h, qlora_dtype stream_dtype, const float* rstd, const void* weight,
+                   qlora_dtype weight_dtype, const void* dres, int64_t M, int64_t K, void* dh, uint16_t* dx16,
+                   float* dweight, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const int st = check_norm(M, K, stream_dtype, stream_dtype, weight ? weight_dtype : stream_dtype);
+  if (st != QLORA_OK) return st;
+  if (M > 0 && (!dy || !h || !rstd || !dh)) return QLORA_ERR_ARG;
+  if (!aligned16(dy) || !aligned16(h) || off_by(rstd, 3u) || !aligned16(weight) || !aligned16(dres) || !aligned16(dh) ||
+      !aligned16(dx16) || off_by(dweight, 3u) || !aligned16(ws))
+    return QLORA_ERR_ALIGN;
+  if (dweight) {
+    size_t need = 0;
+    qlora_norm_workspace(M, K, &need);
+    if (!ws || ws_bytes < need) return QLORA_ERR_WORKSPACE;
+  }
+  qlora::NormBwd c{};
+  c.dy = dy;
+  c.h = h;
+  c.h_bf16 = stream_dtype == QLORA_BF16;
+  c.rstd = rstd;
+  c.w = weight;
+  c.w_bf16 = weight_dtype == QLORA_BF16;
+  c.dres = dres;
+  c.M = M;
+  c.K = K;
+  c.dh = dh;
+  c.dx16 = dx16;
+  c.dw = dweight;
+  c.part = static_cast<float*>(ws);
+  (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
+  const hipError_t e = qlora::launch_norm_bwd(c, stream);
+  return e == hipSuccess ? QLORA_OK : hip_fail(e);
+}
+
+static int check_head(int64_t M, int64_t K, int64_t V, qlora_dtype grad_dtype) {
+  if (grad_dtype != QLORA_F32 && grad_dtype != QLORA_BF16) return QLORA_ERR_ARG;
+  if (M < 0 || M > QLORA_LAYER_MAX_ROWS || K <= 0 || (K % 64) != 0 || K >= ((int64_t)1 << 23) || V < 1 ||
+      V > QLORA_HEAD_MAX_VOCAB)
+    return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
+int qlora_head_workspace(int64_t M, int64_t K, int64_t V, int dH, int dW, qlora_dtype grad_dtype, size_t* bytes) {
+  if (!bytes) return QLORA_ERR_ARG;
+  const int st = check_head(M, K, V, grad_dtype);
+  if (st != QLORA_OK) return st;
+  *bytes = qlora::head_workspace_layout(M, K, V, dH != 0, dW != 0, grad_dtype == QLORA_BF16).total;
+  return QLORA_OK;
+}
+
+int qlora_head_loss(const uint16_t* H, const uint16_t* W, const int64_t* labels, const float* weights, int64_t M,
+                    int64_t K, int64_t V, float divisor, float grad_scale, float* loss, float* nll, uint16_t* dH,
+                    void* dW, qlora_dtype grad_dtype, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const int st = check_head(M, K, V, grad_dtype);
+  if (st != QLORA_OK) return st;
+  if (!isfinite(divisor) || divisor < 0.0f || !isfinite(grad_scale)) return QLORA_ERR_ARG;
+  if (!W || !loss || (M > 0 && (!H || !labels || !nll))) return QLORA_ERR_ARG;
+  if (!aligned16(H) || !aligned16(W) || off_by(labels, 7u) || off_by(weights, 3u) || off_by(loss, 3u) || off_by(nll, 3u) ||
+      !aligned16(dH) || !aligned16(dW) || !aligned16(ws))
+    return QLORA_ERR_ALIGN;
+  if (!ws || ws_bytes < qlora::head_workspace_layout(M, K, V, dH != nullptr, dW != nullptr, grad_dtype == QLORA_BF16).total)
+    return QLORA_ERR_WORKSPACE;
+  qlora::HeadCall c{};
+  c.H = H;
+  c.W = W;
+  c.labels = labels;
+  c.weights = weights;
+  c.M = M;
+  c.K = K;
+  c.V = V;
+  c.divisor = divisor;
+  c.grad_scale = grad_scale;
+  c.loss = loss;
+  c.nll = nll;
+  c.dH = dH;
+  c.dW = dW;
+  c.dw_bf16 = grad_dtype == QLORA_BF16;
+  c.ws = ws;
+  (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
+  const hipError_t e = qlora::launch_head_loss(c, stream);
   return e == hipSuccess ? QLORA_OK : hip_fail(e);
 }
 

@@ -1,0 +1,629 @@
+// The gated feed-forward block over two quantised bases with adapters, for
+// gfx950:
+//
+//   G = X Wg^T + s (X L1g) L2g,   U = X Wu^T + s (X L1u) L2u,   A = act(G) U
+//   dU = dA act(G),  dG = dA U act'(G)
+//   dX = dG Wg + dU Wu + s (dG L2g^T) L1g^T + s (dU L2u^T) L1u^T,  dL1, dL2 as for the linear
+//
+// with act(g) = g sigma(z): z = g (SiLU) or z = sqrt(8 / pi) (g + 0.044715 g^3)
+// (GELU in its tanh form), act'(g) = sigma + g sigma (1 - sigma) dz/dg.
+//
+// Both weights are dequantised into one matrix [2 Fp][K] (Fp: F rounded up to
+// 64) whose rows alternate in blocks of 32, gate and up, so that the 64 columns
+// of a GEMM wave hold G and U of the same 32 features in the same lanes and
+// registers: the product act(G) U is made from the accumulators, and only A is
+// written. The backward pass without kept activations runs the same product,
+// with an epilogue that reads dA and writes dG and dU; with G and U kept in 8
+// bits an elementwise kernel makes them. dX is one product over both, [dG dU]
+// against the same matrix read down its rows.
+#include "common.h"
+#include "launch.h"
+#include "tile_gemm.h"
+
+namespace qlora {
+
+namespace {
+
+int64_t gd_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// act and its derivative. sigma (1 - sigma) is 0 for large |z|, where z's derivative may be infinite.
+template <int ACT>
+__device__ __forceinline__ float act_of(float g) {
+  const float z = ACT == kActSilu ? g : 1.5957691216057308f * (g + 0.044715f * (g * g * g));
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_both(float g, float* a, float* d) {
+  const float z = ACT == kActSilu ? g : 1.5957691216057308f * (g + 0.044715f * (g * g * g));
+  const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+  const float q = p * (1.0f - p);
+  const float dz = ACT == kActSilu ? 1.0f : 1.5957691216057308f * (1.0f + 0.134145f * (g * g));
+  *a = g * p;
+  *d = q == 0.0f ? p : p + g * q * dz;
+}
+
+// ---- operands ------------------------------------------------------------------------------
+
+// Feature f of weight which (0 gate, 1 up) is row 64 (f / 32) + 32 which + f % 32; rows of f in [F, Fp) are zeros.
+__global__ __launch_bounds__(256) void dequant_pair_kernel(NF4View Wg, NF4View Wu, NF4Table tg, NF4Table tu, int64_t Fp,
+                                                           uint16_t* __restrict__ out) {
+  __shared__ float s_q[2][16];
+  const int which = (int)blockIdx.y;
+  const NF4View& W = which ? Wu : Wg;
+  if (threadIdx.x < 16) s_q[which][threadIdx.x] = which ? tu.q[threadIdx.x] : tg.q[threadIdx.x];
+  __syncthreads();
+  const float mu = tensor_mean(W);
+  const int64_t K8 = W.cols / 8, nunits = W.rows * K8, all = Fp * K8;
+  const uint32_t* codes = reinterpret_cast<const uint32_t*>(W.codes);
+  constexpr int kUnits = 4;
+  for (int64_t base = (int64_t)blockIdx.x * 256 * kUnits + threadIdx.x; base < all; base += (int64_t)gridDim.x * 256 * kUnits) {
+    uint32_t c[kUnits];
+    float ap[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int64_t un = base + (int64_t)u * 256, uc = un < nunits ? un : nunits - 1;
+      c[u] = codes[uc];
+      ap[u] = block_const(W, uc >> 3, mu);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int64_t un = base + (int64_t)u * 256;
+      if (un >= all) continue;
+      const int64_t f = un / K8, k8 = un - f * K8;
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t byte = (c[u] >> (8 * i)) & 0xFFu;
+        o[i] = un < nunits ? pack_bf16x2(s_q[which][byte & 15u] * ap[u], s_q[which][byte >> 4] * ap[u]) : 0u;
+      }
+      const int64_t row = 64 * (f >> 5) + 32 * which + (f & 31);
+      *reinterpret_cast<u32x4_t*>(out + row * W.cols + k8 * 8) = u32x4_t{o[0], o[1], o[2], o[3]};
+    }
+  }
+}
+
+// The adapters as the products take them; 32 x 32 tiles, transposed through LDS.
+//   l1t [2][rp][K] = L1^T, rows from r on zero
+//   l2i [2 Fp][2 rp] (forward): L2^T in the weight's row order, each weight's r columns at rp which, zeros elsewhere
+//   l2p [2][rp][Fp] (backward): L2, zeros from row r and column F on
+struct GatedAdapters {
+  const uint16_t* L1;
+  const uint16_t* L2;
+  int64_t K, F, Fp;
+  int r, rp;
+  uint16_t* l1t;
+  uint16_t* l2i;      // or nullptr
+  uint16_t* l2p;      // or nullptr
+  int tiles1, tiles2;  // workgroups of each part
+};
+
+__global__ __launch_bounds__(256) void gated_adapters_kernel(GatedAdapters g) {
+  __shared__ uint16_t tile[32][33];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int which = (int)blockIdx.y;
+  int id = (int)blockIdx.x;
+  const int nr = g.rp / 32;
+  if (id < g.tiles1) {
+    const int64_t k0 = (int64_t)(id / nr) * 32;
+    const int j0 = (id % nr) * 32;
+    const uint16_t* src = g.L1 + (int64_t)which * g.K * g.r;
+    for (int y = ty; y < 32; y += 8) tile[y][tx] = j0 + tx < g.r ? src[(k0 + y) * g.r + j0 + tx] : 0;
+    __syncthreads();
+    uint16_t* dst = g.l1t + (int64_t)which * g.rp * g.K;
+    for (int y = ty; y < 32; y += 8) dst[(int64_t)(j0 + y) * g.K + k0 + tx] = tile[tx][y];
+    return;
+  }
+  id -= g.tiles1;
+  const int64_t f0 = (int64_t)(id / nr) * 32;
+  const int j0 = (id % nr) * 32;
+  const uint16_t* src = g.L2 + (int64_t)which * g.r * g.F;
+  for (int y = ty; y < 32; y += 8) {
+    const uint16_t v = j0 + y < g.r && f0 + tx < g.F ? src[(int64_t)(j0 + y) * g.F + f0 + tx] : 0;
+    tile[y][tx] = v;
+    if (g.l2p) g.l2p[((int64_t)which * g.rp + j0 + y) * g.Fp + f0 + tx] = v;
+  }
+  if (!g.l2i) return;
+  __syncthreads();
+  for (int y = ty; y < 32; y += 8) {
+    uint16_t* row = g.l2i + (2 * f0 + 32 * which + y) * (2 * g.rp);
+    row[which * g.rp + j0 + tx] = tile[tx][y];
+    row[(1 - which) * g.rp + j0 + tx] = 0;
+  }
+}
+
+// ---- the product with its epilogues ------------------------------------------------------
+
+// Epilogue tile in LDS: one 32-row block of every wave at a time, gate and up as fp32, 64 rows (both wave rows) x 128
+// features; the threads then take 8 features of a row each.
+constexpr int kEpPitch = 128 + 4;
+
+struct GatedOut {
+  uint16_t* A;
+  int8_t* codes[2];    // gate, up; nullptr: not kept
+  float* absmax[2];
+  int64_t M, F;
+};
+
+__device__ __forceinline__ uint32_t code4(const float* v, float c) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(v[i] * c), -127.0f), 127.0f);
+    w |= ((uint32_t)((int32_t)x) & 0xFFu) << (8 * i);
+  }
+  return w;
+}
+
+// 8 of a block's 64 values per lane, 8 neighbouring lanes per block: the codec's codes and absmax.
+__device__ __forceinline__ void store_int8(const float* v, int8_t* codes, float* absmax, int64_t at) {
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = __builtin_fmaxf(m, __builtin_fabsf(v[e]));
+  m = wave_max(m, 8);
+  const float c = m < 0x1p-120f ? 0.0f : 127.0f / m;
+  *reinterpret_cast<u32x2_t*>(codes + at) = u32x2_t{code4(v, c), code4(v + 4, c)};
+  if ((threadIdx.x & 7) == 0) absmax[at >> 6] = m;
+}
+
+// A = act(G) U, and the 8-bit values of G and U.
+template <int ACT, bool SAVE>
+struct GatedFwdEpi {
+  GatedOut o;
+  template <int MI>
+  __device__ __forceinline__ void operator()(f32x16_t (&acc)[MI][2], int64_t m0, int64_t n0, int wm, int wn, int z,
+                                             uint16_t* smem) const {
+    const int lane = threadIdx.x & 63, tid = threadIdx.x;
+    const int64_t f0 = n0 / 2;
+    if constexpr (!SAVE) {
+      // a wave's 32 rows x 32 features as bf16 in its own padded LDS slice, then 16-byte stores
+      constexpr int kPitch = 32 + 8;
+      uint16_t* ep = smem + (wm * 4 + wn) * (32 * kPitch);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          ep[((v & 3) + 4 * (lane >> 5) + 8 * (v >> 2)) * kPitch + (lane & 31)] =
+              f32_to_bf16(act_of<ACT>(acc[i][0][v]) * acc[i][1][v]);
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave's writes to its own slice
+#pragma unroll
+        for (int it = 0; it < 2; ++it) {
+          const int r = 16 * it + (lane >> 2), c = 8 * (lane & 3);
+          const u32x4_t val = *reinterpret_cast<const u32x4_t*>(ep + r * kPitch + c);
+          const int64_t row = m0 + (wm * MI + i) * 32 + r, f = f0 + 32 * wn + c;
+          if (row < o.M && f < o.F) *reinterpret_cast<u32x4_t*>(o.A + row * o.F + f) = val;
+        }
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+      }
+    } else {
+      float* eg = reinterpret_cast<float*>(smem);
+      float* eu = eg + 64 * kEpPitch;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        if (i > 0) __syncthreads();
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int at = (32 * wm + (v & 3) + 4 * (lane >> 5) + 8 * (v >> 2)) * kEpPitch + 32 * wn + (lane & 31);
+          eg[at] = acc[i][0][v];
+          eu[at] = acc[i][1][v];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int it = 0; it < 2; ++it) {
+          const int rl = 32 * it + (tid >> 4), c = 8 * (tid & 15);
+          const int64_t row = m0 + ((rl >> 5) * MI + i) * 32 + (rl & 31), f = f0 + c;
+          float g[8], u[8], a[8];
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            const f32x4_t gv = *reinterpret_cast<const f32x4_t*>(eg + rl * kEpPitch + c + e);
+            const f32x4_t uv = *reinterpret_cast<const f32x4_t*>(eu + rl * kEpPitch + c + e);
+            g[e] = gv.x; g[e + 1] = gv.y; g[e + 2] = gv.z; g[e + 3] = gv.w;
+            u[e] = uv.x; u[e + 1] = uv.y; u[e + 2] = uv.z; u[e + 3] = uv.w;
+          }
+          if (row < o.M && f < o.F) {     // F % 64 == 0: the 8 lanes of a block agree
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[e] = act_of<ACT>(g[e]) * u[e];
+            const int64_t at = row * o.F + f;
+            *reinterpret_cast<u32x4_t*>(o.A + at) = u32x4_t{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                                                            pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7])};
+            store_int8(g, o.codes[0], o.absmax[0], at);
+            store_int8(u, o.codes[1], o.absmax[1], at);
+          }
+        }
+      }
+    }
+  }
+};
+
+// dG = dA U act'(G), dU = dA act(G) of the recomputed G and U, rounded to bf16 once: they are the operands of the
+// products that follow.
+template <int ACT>
+struct GatedBwdEpi {
+  const uint16_t* dA;
+  uint16_t* dgu;         // [M][2 Fp]
+  int64_t M, F, Fp;
+  template <int MI>
+  __device__ __forceinline__ void operator()(f32x16_t (&acc)[MI][2], int64_t m0, int64_t n0, int wm, int wn, int z,
+                                             uint16_t* smem) const {
+    const int lane = threadIdx.x & 63;
+    const int64_t f0 = n0 / 2 + 32 * wn;
+    constexpr int kPitch = 32 + 8;
+    uint16_t* eg = smem + (wm * 4 + wn) * (2 * 32 * kPitch);
+    uint16_t* eu = eg + 32 * kPitch;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int64_t row0 = m0 + (wm * MI + i) * 32;
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {          // dA through the slice
+        const int r = 16 * it + (lane >> 2), c = 8 * (lane & 3);
+        const bool in = row0 + r < M && f0 + c < F;
+        u32x4_t val = {0u, 0u, 0u, 0u};
+        if (in) val = *reinterpret_cast<const u32x4_t*>(dA + (row0 + r) * F + f0 + c);
+        *reinterpret_cast<u32x4_t*>(eg + r * kPitch + c) = val;
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int at = ((v & 3) + 4 * (lane >> 5) + 8 * (v >> 2)) * kPitch + (lane & 31);
+        const float d = bf16_to_f32(eg[at]);
+        float a, da;
+        act_both<ACT>(acc[i][0][v], &a, &da);
+        // columns from F on: zeros, also where the weights' padding gave 0 / 0
+        eg[at] = f32_to_bf16(d * acc[i][1][v] * da);
+        eu[at] = f32_to_bf16(d * a);
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {
+        const int r = 16 * it + (lane >> 2), c = 8 * (lane & 3);
+        const int64_t row = row0 + r, f = f0 + c;
+        if (row < M && f < Fp) {
+          *reinterpret_cast<u32x4_t*>(dgu + row * (2 * Fp) + f) = *reinterpret_cast<const u32x4_t*>(eg + r * kPitch + c);
+          *reinterpret_cast<u32x4_t*>(dgu + row * (2 * Fp) + Fp + f) = *reinterpret_cast<const u32x4_t*>(eu + r * kPitch + c);
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+    }
+  }
+};
+
+// bf16 output, rows of `ld`.
+struct StoreEpi {
+  uint16_t* C;
+  int64_t ld, M, N;
+  template <int MI>
+  __device__ __forceinline__ void operator()(f32x16_t (&acc)[MI][2], int64_t m0, int64_t n0, int wm, int wn, int z,
+                                             uint16_t* smem) const {
+    const int lane = threadIdx.x & 63;
+    constexpr int kPitch = 64 + 8;
+    uint16_t* ep = smem + (wm * 4 + wn) * (32 * kPitch);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          ep[((v & 3) + 4 * (lane >> 5) + 8 * (v >> 2)) * kPitch + 32 * j + (lane & 31)] = f32_to_bf16(acc[i][j][v]);
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const int r = 8 * it + (lane >> 3), c = 8 * (lane & 7);
+        const u32x4_t val = *reinterpret_cast<const u32x4_t*>(ep + r * kPitch + c);
+        const int64_t row = m0 + (wm * MI + i) * 32 + r, col = n0 + 64 * wn + c;
+        if (row < M && col < N) *reinterpret_cast<u32x4_t*>(C + row * ld + col) = val;
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+    }
+  }
+};
+
+template <class L, class E>
+__global__ __launch_bounds__(kTgThreads, 1) void gated_gemm_kernel(TgArgs p, E epi, TgPlan pl) {
+  __shared__ __attribute__((aligned(1024))) uint16_t smem[kTgSmem];
+  int64_t m0, n0;
+  int z;
+  if (!tg_where(pl, 1, (int)blockIdx.x, &m0, &n0, &z)) return;
+  if (pl.half) tg_tile<128, L>(p, epi, m0, n0, smem, z);
+  else tg_tile<256, L>(p, epi, m0, n0, smem, z);
+}
+
+template <class L, class E>
+hipError_t run_tiles(const TgArgs& p, const E& epi, int64_t M, int64_t N, hipStream_t stream) {
+  const TgPlan pl = tg_plan(M, N, 1, device_cu_count());
+  hipLaunchKernelGGL((gated_gemm_kernel<L, E>), dim3((unsigned)(pl.tiles_m * pl.tiles_n)), dim3(kTgThreads), 0, stream, p, epi, pl);
+  return hipGetLastError();
+}
+
+using RowRow = TgLayout<false, false, true, false>;
+using RowPaired = TgLayout<false, true, true, true>;
+
+// ---- elementwise parts -----------------------------------------------------------------------
+
+__device__ __forceinline__ void load_int8(const int8_t* codes, const float* absmax, int64_t at, float* v) {
+  const u32x2_t w = *reinterpret_cast<const u32x2_t*>(codes + at);
+  const float s = absmax[at >> 6] / 127.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3))) * s;
+}
+
+__device__ __forceinline__ void load_bf16(const uint16_t* p, float* v) {
+  const u32x4_t w = *reinterpret_cast<const u32x4_t*>(p);
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __uint_as_float(x[e] << 16);
+    v[2 * e + 1] = __uint_as_float(x[e] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ u32x4_t pack8(const float* v) {
+  return u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
+// dG and dU from the kept 8-bit G and U (F a multiple of 64), 8 features per thread.
+template <int ACT>
+__global__ __launch_bounds__(256) void gated_dgu_kernel(const uint16_t* __restrict__ dA, Int8Values G, Int8Values U,
+                                                        int64_t M, int64_t F, uint16_t* __restrict__ dgu) {
+  const int64_t n = M * F / 8, per = F / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per, f = (i - row * per) * 8;
+    float g[8], u[8], d[8], dg[8], du[8];
+    load_int8(G.codes, G.absmax, i * 8, g);
+    load_int8(U.codes, U.absmax, i * 8, u);
+    load_bf16(dA + i * 8, d);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float a, da;
+      act_both<ACT>(g[e], &a, &da);
+      dg[e] = d[e] * u[e] * da;
+      du[e] = d[e] * a;
+    }
+    *reinterpret_cast<u32x4_t*>(dgu + row * 2 * F + f) = pack8(dg);
+    *reinterpret_cast<u32x4_t*>(dgu + row * 2 * F + F + f) = pack8(du);
+  }
+}
+
+// ---- few rows ------------------------------------------------------------------------------------
+
+// A (and the 8-bit values) from the base products' partials [S][M][F] of each weight and sT [M][2 rp]: one row and 8
+// features per thread, 128 features and 16 rows per workgroup. Slices and ranks are added in order.
+template <int ACT>
+__global__ __launch_bounds__(256) void gated_finish_kernel(const float* __restrict__ pg, const float* __restrict__ pu, int S,
+                                                           const uint16_t* __restrict__ sT, int rp, int r,
+                                                           const uint16_t* __restrict__ L2, GatedOut o) {
+  const int64_t f = (int64_t)blockIdx.x * 128 + 8 * (threadIdx.x & 15);
+  const int64_t row = (int64_t)blockIdx.y * 16 + (threadIdx.x >> 4);
+  if (row >= o.M || f >= o.F) return;
+  const int64_t at = row * o.F + f, all = o.M * o.F;
+  float v[2][8] = {};
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const float* p = (w ? pu : pg) + at;
+    for (int z = 0; z < S; ++z) {
+      const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p + z * all), b = *reinterpret_cast<const f32x4_t*>(p + z * all + 4);
+      v[w][0] += a.x; v[w][1] += a.y; v[w][2] += a.z; v[w][3] += a.w;
+      v[w][4] += b.x; v[w][5] += b.y; v[w][6] += b.z; v[w][7] += b.w;
+    }
+    const uint16_t* t = sT + row * (2 * rp) + w * rp;
+    const uint16_t* l = L2 + (int64_t)w * r * o.F + f;
+    for (int j = 0; j < r; j += 8) {               // r % 8 == 0
+      float x[8];
+      load_bf16(t + j, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float y[8];
+        load_bf16(l + (int64_t)(j + i) * o.F, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[w][e] = __builtin_fmaf(x[i], y[e], v[w][e]);
+      }
+    }
+  }
+  float a[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) a[e] = act_of<ACT>(v[0][e]) * v[1][e];
+  *reinterpret_cast<u32x4_t*>(o.A + at) = pack8(a);
+  if (o.codes[0]) {                                // F % 64 == 0: whole blocks per 8 lanes
+    store_int8(v[0], o.codes[0], o.absmax[0], at);
+    store_int8(v[1], o.codes[1], o.absmax[1], at);
+  }
+}
+
+}  // namespace
+
+GatedWorkspace gated_workspace_layout(int64_t M, int64_t K, int64_t F, int r, bool bwd) {
+  const int64_t Fp = gd_cdiv(F, 64) * 64, rp = gd_cdiv(r, 64) * 64;
+  GatedWorkspace L;
+  size_t off = 0;
+  auto take = [&](int64_t bytes) { const size_t at = off; off += align_up((size_t)bytes, 256); return at; };
+  const bool dense = bwd || M > kMultiSmallRows;
+  L.wd_off = take(dense ? 2 * Fp * K * 2 : 0);
+  L.l1t_off = take(dense ? 2 * rp * K * 2 : 0);
+  L.l2_off = take(dense ? (2 * Fp) * (2 * rp) * 2 : 0);
+  L.st_off = take(M * 2 * rp * 2);
+  L.t_off = take(bwd ? 2 * M * r * 2 : 0);
+  L.dgu_off = take(bwd ? M * 2 * Fp * 2 : 0);
+  L.x_off = take(bwd ? M * K * 2 : 0);
+  L.part_off = take((int64_t)adapter_partial_bytes(M, K, Fp, r));
+  const int64_t few = M < kMultiSmallRows ? M : kMultiSmallRows;
+  L.part2_off = take(bwd ? 0 : 2 * multi_small_partial_floats(few, K, F) * 4);
+  L.total = off > 0 ? off : 256;
+  return L;
+}
+
+namespace {
+
+struct GatedBuffers {
+  uint16_t *wd, *l1t, *l2, *st, *t, *dgu, *x;
+  float *part, *part2;
+  GatedBuffers(const GatedWorkspace& L, void* ws) {
+    char* b = static_cast<char*>(ws);
+    wd = reinterpret_cast<uint16_t*>(b + L.wd_off);
+    l1t = reinterpret_cast<uint16_t*>(b + L.l1t_off);
+    l2 = reinterpret_cast<uint16_t*>(b + L.l2_off);
+    st = reinterpret_cast<uint16_t*>(b + L.st_off);
+    t = reinterpret_cast<uint16_t*>(b + L.t_off);
+    dgu = reinterpret_cast<uint16_t*>(b + L.dgu_off);
+    x = reinterpret_cast<uint16_t*>(b + L.x_off);
+    part = reinterpret_cast<float*>(b + L.part_off);
+    part2 = reinterpret_cast<float*>(b + L.part2_off);
+  }
+};
+
+hipError_t launch_dequant_pair(const GatedBase& W, int64_t Fp, uint16_t* wd, hipStream_t stream) {
+  int64_t blocks = gd_cdiv(Fp * W.gate.cols / 8, 1024);
+  if (blocks > 4 * device_cu_count()) blocks = 4 * device_cu_count();
+  hipLaunchKernelGGL(dequant_pair_kernel, dim3((unsigned)blocks, 2), dim3(256), 0, stream, W.gate, W.up, W.tab_gate, W.tab_up,
+                     Fp, wd);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_adapters(const uint16_t* L1, const uint16_t* L2, int64_t K, int64_t F, int r, uint16_t* l1t,
+                                 uint16_t* l2i, uint16_t* l2p, hipStream_t stream) {
+  const int rp = (int)gd_cdiv(r, 64) * 64;
+  GatedAdapters g{L1, L2, K, F, gd_cdiv(F, 64) * 64, r, rp, l1t, l2i, l2p, 0, 0};
+  g.tiles1 = (int)(K / 32) * (rp / 32);
+  g.tiles2 = (int)(g.Fp / 32) * (rp / 32);
+  hipLaunchKernelGGL(gated_adapters_kernel, dim3((unsigned)(g.tiles1 + g.tiles2), 2), dim3(256), 0, stream, g);
+  return hipGetLastError();
+}
+
+// The product of X with both weights and their adapters, into `epi`.
+template <class E>
+hipError_t gated_product(const GatedBuffers& b, const uint16_t* X, int64_t M, int64_t K, int64_t Fp, int64_t rp, const E& epi,
+                         hipStream_t stream) {
+  TgArgs p{};
+  p.A = {X, K, M};
+  p.B = {b.wd, K, 2 * Fp};
+  p.A2 = {b.st, 2 * rp, M};
+  p.B2 = {b.l2, 2 * rp, 2 * Fp};
+  p.kmain = K;
+  p.kslab = 2 * rp;
+  p.per_slice = (int)((p.kmain + p.kslab) / kTgK);
+  p.slices = 1;
+  return run_tiles<RowRow>(p, epi, M, 2 * Fp, stream);
+}
+
+template <typename F1, typename F2>
+hipError_t by_act(int act, F1&& silu, F2&& gelu) { return act == kActSilu ? silu() : gelu(); }
+
+}  // namespace
+
+#define GD_TRY(call)                       \
+  do {                                     \
+    const hipError_t e_ = (call);          \
+    if (e_ != hipSuccess) return e_;       \
+  } while (0)
+
+hipError_t gated_forward(const GatedBase& W, const uint16_t* X, int64_t M, const uint16_t* L1, const uint16_t* L2, int r,
+                         float s, int act, uint16_t* A, uint16_t* T_out, const Int8Values* gate8, const Int8Values* up8,
+                         void* ws, hipStream_t stream) {
+  const int64_t K = W.gate.cols, F = W.gate.rows, Fp = gd_cdiv(F, 64) * 64, rp = gd_cdiv(r, 64) * 64;
+  if (M == 0) return hipSuccess;
+  const GatedWorkspace L = gated_workspace_layout(M, K, F, r, false);
+  const GatedBuffers b(L, ws);
+  GatedOut o{A, {gate8 ? gate8->codes : nullptr, up8 ? up8->codes : nullptr},
+             {gate8 ? gate8->absmax : nullptr, up8 ? up8->absmax : nullptr}, M, F};
+  if (M <= kMultiSmallRows) {      // one pass over the 4-bit weights
+    for (int w = 0; w < 2; ++w)
+      GD_TRY(launch_small_lora_down(X, M, K, L1 + w * K * r, r, s, b.st + w * rp, 2 * rp, T_out ? T_out + w * M * r : nullptr,
+                                    b.part, stream));
+    const int S = multi_small_slices(M, K, F);
+    float* pu = b.part2 + (int64_t)S * M * F;
+    GD_TRY(launch_multi_small_base(W.gate, W.tab_gate, X, M, b.part2, stream));
+    GD_TRY(launch_multi_small_base(W.up, W.tab_up, X, M, pu, stream));
+    const dim3 grid((unsigned)gd_cdiv(F, 128), (unsigned)gd_cdiv(M, 16));
+    if (act == kActSilu)
+      hipLaunchKernelGGL(gated_finish_kernel<kActSilu>, grid, dim3(256), 0, stream, b.part2, pu, S, b.st, (int)rp, r, L2, o);
+    else
+      hipLaunchKernelGGL(gated_finish_kernel<kActGelu>, grid, dim3(256), 0, stream, b.part2, pu, S, b.st, (int)rp, r, L2, o);
+    return hipGetLastError();
+  }
+  GD_TRY(launch_gated_adapters(L1, L2, K, F, r, b.l1t, b.l2, nullptr, stream));
+  for (int w = 0; w < 2; ++w)
+    GD_TRY(adapter_down(X, M, K, L1 + w * K * r, b.l1t + w * rp * K, r, s, b.st + w * rp, rp, 2 * rp,
+                        T_out ? T_out + w * M * r : nullptr, b.part, stream));
+  GD_TRY(launch_dequant_pair(W, Fp, b.wd, stream));
+  if (gate8)
+    return by_act(
+        act, [&] { return gated_product(b, X, M, K, Fp, rp, GatedFwdEpi<kActSilu, true>{o}, stream); },
+        [&] { return gated_product(b, X, M, K, Fp, rp, GatedFwdEpi<kActGelu, true>{o}, stream); });
+  return by_act(
+      act, [&] { return gated_product(b, X, M, K, Fp, rp, GatedFwdEpi<kActSilu, false>{o}, stream); },
+      [&] { return gated_product(b, X, M, K, Fp, rp, GatedFwdEpi<kActGelu, false>{o}, stream); });
+}
+
+namespace {
+
+__global__ __launch_bounds__(256) void zero_kernel(uint32_t* __restrict__ p, int64_t words) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256) p[i] = 0u;
+}
+
+}  // namespace
+
+hipError_t gated_backward(const GatedBase& W, const uint16_t* X, const Int8Values* X8, const uint16_t* dA, int64_t M,
+                          const uint16_t* L1, const uint16_t* L2, int r, float s, int act, const uint16_t* T,
+                          const Int8Values* gate8, const Int8Values* up8, uint16_t* dX, void* dL1, void* dL2,
+                          bool grad_bf16, void* ws, hipStream_t stream) {
+  const int64_t K = W.gate.cols, F = W.gate.rows, Fp = gd_cdiv(F, 64) * 64, rp = gd_cdiv(r, 64) * 64;
+  const int64_t e = grad_bf16 ? 2 : 4;
+  if (M == 0) {
+    hipLaunchKernelGGL(zero_kernel, dim3(256), dim3(256), 0, stream, static_cast<uint32_t*>(dL1), 2 * K * r * e / 4);
+    hipLaunchKernelGGL(zero_kernel, dim3(256), dim3(256), 0, stream, static_cast<uint32_t*>(dL2), 2 * r * F * e / 4);
+    return hipGetLastError();
+  }
+  const GatedWorkspace L = gated_workspace_layout(M, K, F, r, true);
+  const GatedBuffers b(L, ws);
+  if (X8) {
+    GD_TRY(launch_int8_dequantize(X8->codes, X8->absmax, M * K, 6, b.x, true, stream));
+    X = b.x;
+  }
+  // the forward product needs L2^T in b.l2; afterwards the same place holds L2 padded for dY L2^T
+  if (!gate8 || dX) GD_TRY(launch_dequant_pair(W, Fp, b.wd, stream));
+  uint16_t* t = b.t;
+  if (!gate8) {
+    GD_TRY(launch_gated_adapters(L1, L2, K, F, r, b.l1t, b.l2, nullptr, stream));
+    for (int w = 0; w < 2; ++w)
+      GD_TRY(adapter_down(X, M, K, L1 + w * K * r, b.l1t + w * rp * K, r, s, b.st + w * rp, rp, 2 * rp,
+                          T ? nullptr : t + w * M * r, b.part, stream));
+    GD_TRY(by_act(
+        act, [&] { return gated_product(b, X, M, K, Fp, rp, GatedBwdEpi<kActSilu>{dA, b.dgu, M, F, Fp}, stream); },
+        [&] { return gated_product(b, X, M, K, Fp, rp, GatedBwdEpi<kActGelu>{dA, b.dgu, M, F, Fp}, stream); }));
+    GD_TRY(launch_gated_adapters(L1, L2, K, F, r, b.l1t, nullptr, b.l2, stream));
+  } else {
+    GD_TRY(launch_gated_adapters(L1, L2, K, F, r, b.l1t, nullptr, b.l2, stream));
+    if (!T)
+      for (int w = 0; w < 2; ++w)
+        GD_TRY(adapter_down(X, M, K, L1 + w * K * r, b.l1t + w * rp * K, r, s, b.st + w * rp, rp, 2 * rp, t + w * M * r,
+                            b.part, stream));
+    int64_t blocks = gd_cdiv(M * F / 8, 256);
+    if (blocks > 16 * device_cu_count()) blocks = 16 * device_cu_count();
+    if (act == kActSilu)
+      hipLaunchKernelGGL(gated_dgu_kernel<kActSilu>, dim3((unsigned)blocks), dim3(256), 0, stream, dA, *gate8, *up8, M, F, b.dgu);
+    else
+      hipLaunchKernelGGL(gated_dgu_kernel<kActGelu>, dim3((unsigned)blocks), dim3(256), 0, stream, dA, *gate8, *up8, M, F, b.dgu);
+    GD_TRY(hipGetLastError());
+  }
+  if (T) t = const_cast<uint16_t*>(T);
+  for (int w = 0; w < 2; ++w)
+    GD_TRY(adapter_up(b.dgu + w * Fp, 2 * Fp, M, F, b.l2 + w * rp * Fp, Fp, r, s, b.st + w * rp, rp, 2 * rp, b.part, stream));
+  if (dX) {
+    TgArgs p{};
+    p.A = {b.dgu, 2 * Fp, M};
+    p.B = {b.wd, K, K};
+    p.A2 = {b.st, 2 * rp, M};
+    p.B2 = {b.l1t, K, K};
+    p.kmain = 2 * Fp;
+    p.kslab = 2 * rp;
+    p.krows_b = 2 * Fp;
+    p.per_slice = (int)((p.kmain + p.kslab) / kTgK);
+    p.slices = 1;
+    GD_TRY(run_tiles<RowPaired>(p, StoreEpi{dX, K, M, K}, M, K, stream));
+  }
+  for (int w = 0; w < 2; ++w)
+    GD_TRY(adapter_grads(X, K, b.dgu + w * Fp, 2 * Fp, F, M, b.st + w * rp, 2 * rp, t + w * M * r, r, s,
+                         static_cast<char*>(dL1) + w * K * r * e, static_cast<char*>(dL2) + w * r * F * e, grad_bf16, b.part,
+                         stream));
+  return hipSuccess;
+}
+
+}  // namespace qlora

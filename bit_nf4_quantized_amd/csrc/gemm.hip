@@ -289,28 +289,29 @@ __global__ __launch_bounds__(NT) void gemm_kernel(GemmArgs p) {
 }
 
 // Fixed-order split-K reduction of partials P[z][rows][cols]:
-//   out[m][j]  = alpha  * sum_z P[z][m][j]   (bf16 or fp32, row stride ldo;
+//   out[m][j]  = alpha  * sum_z P[z][m][j]   (bf16 or fp32, row stride pitch;
 //                columns [cols, ldo) of a bf16 out are zero-filled)
 //   out2[m][j] = bf16(alpha2 * sum)          (optional, row stride cols)
 __global__ __launch_bounds__(256) void splitk_reduce_kernel(const float* __restrict__ P, int Z, int64_t rows,
                                                             int64_t cols, float alpha, void* __restrict__ out,
                                                             int out_bf16, int64_t ldo, float alpha2,
-                                                            uint16_t* __restrict__ out2) {
+                                                            uint16_t* __restrict__ out2, int64_t pitch) {
   const int64_t count = rows * cols;
   const int64_t total = rows * ldo;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t m = i / ldo, j = i - m * ldo;
+    const int64_t o = m * pitch + j;
     if (j >= cols) {  // padding columns of a bf16 slab operand
-      static_cast<uint16_t*>(out)[i] = 0;
+      static_cast<uint16_t*>(out)[o] = 0;
       continue;
     }
     const int64_t src = m * cols + j;
     float acc = 0.0f;
     for (int z = 0; z < Z; ++z) acc += P[(int64_t)z * count + src];
     const float v = alpha * acc;
-    if (out_bf16) static_cast<uint16_t*>(out)[i] = f32_to_bf16(v);
-    else static_cast<float*>(out)[i] = v;
+    if (out_bf16) static_cast<uint16_t*>(out)[o] = f32_to_bf16(v);
+    else static_cast<float*>(out)[o] = v;
     if (out2) out2[src] = f32_to_bf16(alpha2 * acc);
   }
 }
@@ -419,12 +420,12 @@ Split choose_split(int64_t tiles, int64_t klen) {
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 hipError_t reduce(const float* P, int Z, int64_t rows, int64_t cols, float alpha, void* out, bool out_bf16,
-                  int64_t ldo, float alpha2, uint16_t* out2, hipStream_t stream) {
+                  int64_t ldo, float alpha2, uint16_t* out2, hipStream_t stream, int64_t pitch = 0) {
   int64_t blocks = cdiv(rows * ldo, 256);
   if (blocks > 4096) blocks = 4096;
   if (blocks < 1) blocks = 1;
   hipLaunchKernelGGL(splitk_reduce_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, P, Z, rows, cols, alpha,
-                     out, out_bf16 ? 1 : 0, ldo, alpha2, out2);
+                     out, out_bf16 ? 1 : 0, ldo, alpha2, out2, pitch ? pitch : ldo);
   return hipGetLastError();
 }
 
@@ -800,6 +801,87 @@ hipError_t linear_backward(const NF4View& W, const NF4Table& tab, const uint16_t
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+// ---- the adapter products of one of several adapters beside a product of their own --------
+//
+// As in linear_forward and linear_backward: the skinny kernels for rank <= 64
+// where their 32-bit offsets reach, else the 128 x 128 GEMM in reduction slices.
+
+size_t adapter_partial_bytes(int64_t M, int64_t K, int64_t N, int r) {
+  const Split sT = choose_split(cdiv(M, BM) * cdiv(r, BN), K), sU = choose_split(cdiv(M, BM) * cdiv(r, BN), N);
+  const Split s1 = choose_split(cdiv(K, BM) * cdiv(r, BN), M), s2 = choose_split(cdiv(r, BM) * cdiv(N, BN), M);
+  size_t part = 0;
+  auto upd = [&](int64_t b) { part = (size_t)b > part ? (size_t)b : part; };
+  upd((int64_t)sT.Z * M * r * 4);
+  upd((int64_t)sU.Z * M * r * 4);
+  upd((int64_t)s1.Z * K * r * 4);
+  upd((int64_t)s2.Z * r * N * 4);
+  if (r <= 64) upd((int64_t)skinny_partial_bytes(M, K, N));
+  if (M <= kMidMaxM) upd((int64_t)small_t_partial_bytes(M, K, r));
+  return align_up(part, 256);
+}
+
+hipError_t adapter_down(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, const uint16_t* l1t, int r, float s,
+                        uint16_t* sT, int64_t width, int64_t pitch, uint16_t* T_out, float* part, hipStream_t stream) {
+  if (skinny_ok(r, M, K)) return skinny_nt(X, K, l1t, K, M, K, r, part, s, sT, width, 1.0f, T_out, stream, nullptr, pitch);
+  GemmArgs a = base_args();
+  a.M = M; a.N = r; a.K = K;
+  a.A = X; a.lda = K;
+  a.B = L1; a.ldb = r;
+  const Split sp = choose_split(cdiv(M, BM) * cdiv(r, BN), K);
+  a.k_split = sp.k_split;
+  a.C = part; a.ldc = r;
+  const hipError_t e = run_gemm<A_ROW, B_COL, EPI_F32, false>(a, sp.Z, stream);
+  if (e != hipSuccess) return e;
+  return reduce(part, sp.Z, M, r, s, sT, true, width, 1.0f, T_out, stream, pitch);
+}
+
+hipError_t adapter_up(const uint16_t* dY, int64_t ldy, int64_t M, int64_t N, const uint16_t* l2p, int64_t ldl, int r,
+                      float s, uint16_t* sU, int64_t width, int64_t pitch, float* part, hipStream_t stream) {
+  if (r <= 64 && fits_dense({M * ldy * 2}))
+    return skinny_nt(dY, ldy, l2p, ldl, M, ldl, r, part, s, sU, width, 0.0f, nullptr, stream, nullptr, pitch);
+  GemmArgs a = base_args();
+  a.M = M; a.N = r; a.K = N;
+  a.A = dY; a.lda = ldy;
+  a.B = l2p; a.ldb = ldl;
+  const Split sp = choose_split(cdiv(M, BM) * cdiv(r, BN), N);
+  a.k_split = sp.k_split;
+  a.C = part; a.ldc = r;
+  const hipError_t e = run_gemm<A_ROW, B_ROW, EPI_F32, false>(a, sp.Z, stream);
+  if (e != hipSuccess) return e;
+  return reduce(part, sp.Z, M, r, s, sU, true, width, 0.0f, nullptr, stream, pitch);
+}
+
+hipError_t adapter_grads(const uint16_t* X, int64_t K, const uint16_t* dY, int64_t ldy, int64_t N, int64_t M,
+                         const uint16_t* sU, int64_t ldu, const uint16_t* T, int r, float s, void* dL1, void* dL2,
+                         bool grad_bf16, float* part, hipStream_t stream) {
+  if (r <= 64) {
+    const hipError_t e = skinny_tn(X, K, K, sU, ldu, M, r, part, 1.0f, false, grad_bf16, dL1, stream);
+    if (e != hipSuccess) return e;
+    return skinny_tn(dY, ldy, N, T, r, M, r, part, s, true, grad_bf16, dL2, stream);
+  }
+  GemmArgs a = base_args();
+  a.M = K; a.N = r; a.K = M;
+  a.A = X; a.lda = K;
+  a.B = sU; a.ldb = ldu;
+  const Split s1 = choose_split(cdiv(K, BM) * cdiv(r, BN), M);
+  a.k_split = s1.k_split;
+  a.C = part; a.ldc = r;
+  hipError_t e = run_gemm<A_COL, B_COL, EPI_F32, false>(a, s1.Z, stream);
+  if (e != hipSuccess) return e;
+  e = reduce(part, s1.Z, K, r, 1.0f, dL1, grad_bf16, r, 0.0f, nullptr, stream);
+  if (e != hipSuccess) return e;
+  a = base_args();
+  a.M = r; a.N = N; a.K = M;
+  a.A = T; a.lda = r;
+  a.B = dY; a.ldb = ldy;
+  const Split s2 = choose_split(cdiv(r, BM) * cdiv(N, BN), M);
+  a.k_split = s2.k_split;
+  a.C = part; a.ldc = N;
+  e = run_gemm<A_COL, B_COL, EPI_F32, false>(a, s2.Z, stream);
+  if (e != hipSuccess) return e;
+  return reduce(part, s2.Z, r, N, s, dL2, grad_bf16, N, 0.0f, nullptr, stream);
 }
 
 }  // namespace qlora

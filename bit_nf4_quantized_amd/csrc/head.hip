@@ -1,0 +1,651 @@
+// Softmax cross entropy over a large vocabulary from hidden states H [M][K] and
+// the head's weight W [V][K], without the logits S = H W^T in memory, and its
+// gradients, for gfx950:
+//
+//   nll_m = log sum_v exp(S_mv) - S_my,   y = labels[m];   loss = sum_m w_m nll_m / divisor
+//   dH_m = g_m (sum_v p_mv W_v - W_y),   dW_v = sum_m g_m (p_mv - [v = y]) H_m,   g_m = grad_scale w_m / divisor
+//
+// The exponentials are taken against the row's own label logit, which a dot
+// product per row gives beforehand: with P_mv = exp(S_mv - S_my) for v != y and
+// l_m = sum of them, nll = log(1 + l), p_mv = P_mv / (1 + l), and the label's
+// gradient p_my - 1 = -l / (1 + l) has no cancellation. So no pass for the row's
+// maximum is needed: P goes to bf16 (whose exponents are fp32's) straight from the
+// logits' accumulators, with one rounding, and dH is one product of P with W, its
+// rows scaled by g / (1 + l) at the end. A label with less than about e^-40 of the
+// largest probability would let P overflow: where a logit of a 256-column tile is
+// more than 40 above the label's, the tile takes its row's maximum out (its shift),
+// and the rows' statistics bring the tiles to one shift.
+//
+//   head_rows_kernel     the list of counted rows (one workgroup; labels outside [0, V) do not count)
+//   head_gather_kernel   their rows of H side by side, their label logits; zero rows of dH for the others
+//   head_prob_kernel     the GEMM H W^T in 256 x 256 tiles, P and the tiles' row sums from its accumulators
+//   head_stat_kernel     l, nll, the rows' scales; P_my = -l
+//   head_dh_kernel       the GEMM P W, W read down its rows
+//   head_dw_kernel       the GEMM P^T (scale H), both operands read down their rows
+//   head_loss_kernel     the weighted sum in fp64
+// Rows are taken in pieces whose P fits a gigabyte. The number of counted rows is
+// known on the device only: the GEMMs plan their tiles there, from a grid for all rows.
+#include "common.h"
+#include "launch.h"
+#include "tile_gemm.h"
+
+namespace qlora {
+
+namespace {
+
+int64_t hd_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr float kShiftAbove = 40.0f;
+
+// ---- rows --------------------------------------------------------------------------------
+
+// rows[0 .. count): the counted rows in order; slot[m]: a row's place among them, or -1.
+__global__ __launch_bounds__(1024) void head_rows_kernel(const int64_t* __restrict__ labels, int64_t M, int64_t V,
+                                                         int32_t* __restrict__ rows, int32_t* __restrict__ slot,
+                                                         int32_t* __restrict__ count) {
+  __shared__ int s_n[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int n = 0;
+  for (int64_t base = 0; base < M; base += 1024) {
+    const int64_t m = base + tid;
+    const int64_t y = m < M ? labels[m] : -1;
+    const bool on = y >= 0 && y < V;
+    const unsigned long long b = __ballot(on);
+    if (lane == 0) s_n[wave] = __popcll(b);
+    __syncthreads();
+    int before = n, all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      before += w < wave ? s_n[w] : 0;
+      all += s_n[w];
+    }
+    const int at = before + __popcll(b & ((1ull << lane) - 1ull));
+    if (on) rows[at] = (int32_t)m;
+    if (m < M) slot[m] = on ? at : -1;
+    n += all;
+    __syncthreads();
+  }
+  if (tid == 0) count[0] = n;
+}
+
+struct HeadRows {
+  const int32_t* rows;
+  const int32_t* count;
+  const float* ref;       // the exponentials' reference: the label's logit (0 where that is not finite)
+  const float* logit;     // the label's logit
+  const int32_t* label;
+};
+
+__global__ __launch_bounds__(256) void head_gather_kernel(const uint16_t* __restrict__ H, const uint16_t* __restrict__ W,
+                                                          const int64_t* __restrict__ labels, int64_t K,
+                                                          const int32_t* __restrict__ slot, uint16_t* __restrict__ Hc,
+                                                          float* __restrict__ ref, float* __restrict__ logit,
+                                                          int32_t* __restrict__ label, float* __restrict__ nll,
+                                                          uint16_t* __restrict__ dH) {
+  __shared__ float red[4];
+  const int64_t m = blockIdx.x;
+  const int at = slot[m];
+  if (at < 0) {
+    if (threadIdx.x == 0) nll[m] = 0.0f;
+    if (dH)
+      for (int64_t k = threadIdx.x * 8; k < K; k += 2048) *reinterpret_cast<u32x4_t*>(dH + m * K + k) = u32x4_t{0u, 0u, 0u, 0u};
+    return;
+  }
+  const int64_t y = labels[m];
+  float sum = 0.0f;
+  for (int64_t k = threadIdx.x * 8; k < K; k += 2048) {
+    const u32x4_t h = *reinterpret_cast<const u32x4_t*>(H + m * K + k), w = *reinterpret_cast<const u32x4_t*>(W + y * K + k);
+    *reinterpret_cast<u32x4_t*>(Hc + (int64_t)at * K + k) = h;
+    const uint32_t a[4] = {h.x, h.y, h.z, h.w}, b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sum = __builtin_fmaf(__uint_as_float(a[e] << 16), __uint_as_float(b[e] << 16), sum);
+      sum = __builtin_fmaf(__uint_as_float(a[e] & 0xFFFF0000u), __uint_as_float(b[e] & 0xFFFF0000u), sum);
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    sum = (red[0] + red[1]) + (red[2] + red[3]);
+    logit[at] = sum;
+    ref[at] = __builtin_isfinite(sum) ? sum : 0.0f;
+    label[at] = (int32_t)y;
+  }
+}
+
+// Rows of a piece that starts at row0: how many there are.
+__device__ __forceinline__ int64_t piece_rows(const int32_t* count, int64_t row0, int64_t piece) {
+  const int64_t n = (int64_t)__builtin_amdgcn_readfirstlane(count[0]) - row0;
+  return n < 0 ? 0 : n < piece ? n : piece;
+}
+
+// ---- P -----------------------------------------------------------------------------------
+
+__device__ __forceinline__ float sum16(float v) {   // over each 16 lanes, in every lane
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, false));   // quad_perm 1,0,3,2
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, false));   // quad_perm 2,3,0,1
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, false));  // row_half_mirror
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, false));  // row_mirror
+  return v;
+}
+
+__device__ __forceinline__ float max16(float v) {
+  v = __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, false)));
+  v = __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, false)));
+  v = __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, false)));
+  v = __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, false)));
+  return v;
+}
+
+// P and the tile's sums and shifts [tile][piece]. Columns from V on and rows past the counted ones: zeros.
+struct ProbEpi {
+  const float* ref;       // of the piece's first row
+  const int32_t* label;
+  int64_t rows;           // counted rows of the piece
+  int64_t V, ldp, piece;
+  uint16_t* P;
+  float* sum;
+  float* shift;
+  template <int MI>
+  __device__ __forceinline__ void operator()(f32x16_t (&acc)[MI][2], int64_t m0, int64_t n0, int wm, int wn, int z,
+                                             uint16_t* smem) const {
+    constexpr int TM = 64 * MI;
+    const int tid = threadIdx.x, lane = tid & 63;
+    float* s_ref = reinterpret_cast<float*>(smem);
+    int* s_label = reinterpret_cast<int*>(s_ref + 256);
+    float* s_shift = s_ref + 512;
+    float* s_part = s_ref + 768;                    // [8][256]
+    int* s_over = reinterpret_cast<int*>(s_ref + 768 + 2048);
+    uint16_t* ep = smem + 2 * (768 + 2048 + 64) + (wm * 4 + wn) * (32 * 72);
+    if (tid == 0) *s_over = 0;
+    if (tid < TM) {
+      const bool in = m0 + tid < rows;
+      s_ref[tid] = in ? ref[m0 + tid] : 0.0f;
+      s_label[tid] = in ? (int)(label[m0 + tid] - n0) : -1;    // column in the tile
+      s_shift[tid] = 0.0f;
+    }
+    __syncthreads();
+    const int c0 = 64 * wn + (lane & 31);
+    const bool in0 = n0 + c0 < V, in1 = n0 + c0 + 32 < V;
+    auto row_of = [&](int i, int v) { return wm * (32 * MI) + 32 * i + (v & 3) + 4 * (lane >> 5) + 8 * (v >> 2); };
+    bool over = false;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int r = row_of(i, v);
+        const float f = s_ref[r];
+        const int y = s_label[r];
+        const bool live = m0 + r < rows;
+        // masked entries: -inf, whose exponential is 0
+        acc[i][0][v] = live && in0 && c0 != y ? acc[i][0][v] - f : -__builtin_inff();
+        acc[i][1][v] = live && in1 && c0 + 32 != y ? acc[i][1][v] - f : -__builtin_inff();
+        over = over || acc[i][0][v] > kShiftAbove || acc[i][1][v] > kShiftAbove;
+      }
+    if (__any(over) && lane == 0) *s_over = 1;
+    __syncthreads();
+    if (*s_over) {                                  // uniform
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const float m = max16(__builtin_fmaxf(acc[i][0][v], acc[i][1][v]));
+          if ((lane & 15) == 0) s_part[(2 * wn + ((lane >> 4) & 1)) * 256 + row_of(i, v)] = m;
+        }
+      __syncthreads();
+      if (tid < TM) {
+        float m = s_part[tid];
+#pragma unroll
+        for (int q = 1; q < 8; ++q) m = __builtin_fmaxf(m, s_part[q * 256 + tid]);
+        s_shift[tid] = m > kShiftAbove ? m : 0.0f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const float d = s_shift[row_of(i, v)];
+          acc[i][0][v] -= d;
+          acc[i][1][v] -= d;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      float mine = 0.0f;                            // of the lane's row: register v = lane % 16
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const float a = __expf(acc[i][0][v]), b = __expf(acc[i][1][v]);
+        const float s = sum16(a + b);
+        mine = (lane & 15) == v ? s : mine;
+        const int at = ((v & 3) + 4 * (lane >> 5) + 8 * (v >> 2)) * 72 + (lane & 31);
+        ep[at] = f32_to_bf16(a);
+        ep[at + 32] = f32_to_bf16(b);
+      }
+      {
+        const int v = lane & 15;
+        s_part[(2 * wn + ((lane >> 4) & 1)) * 256 + row_of(i, v)] = mine;
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);           // lgkmcnt(0): the wave's own slice
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const int r = 8 * it + (lane >> 3), c = 8 * (lane & 7);
+        const u32x4_t val = *reinterpret_cast<const u32x4_t*>(ep + r * 72 + c);
+        const int64_t row = m0 + wm * (32 * MI) + 32 * i + r, col = n0 + 64 * wn + c;
+        if (row < piece && col < ldp) *reinterpret_cast<u32x4_t*>(P + row * ldp + col) = val;
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+    }
+    __syncthreads();
+    if (tid < TM && m0 + tid < rows) {
+      float s = s_part[tid];
+#pragma unroll
+      for (int q = 1; q < 8; ++q) s += s_part[q * 256 + tid];
+      const int64_t at = (n0 / kTgN) * piece + m0 + tid;
+      sum[at] = s;
+      shift[at] = s_shift[tid];
+    }
+  }
+};
+
+__global__ __launch_bounds__(kTgThreads, 1) void head_prob_kernel(TgArgs p, ProbEpi epi, const int32_t* count, int64_t row0,
+                                                                  int64_t N, int cus) {
+  __shared__ __attribute__((aligned(1024))) uint16_t smem[kTgSmem];
+  epi.rows = piece_rows(count, row0, epi.piece);
+  const TgPlan pl = tg_plan(epi.rows, N, 1, cus);
+  int64_t m0, n0;
+  int z;
+  if (!tg_where(pl, 1, (int)blockIdx.x, &m0, &n0, &z)) return;
+  using L = TgLayout<false, false, false, false>;
+  if (pl.half) tg_tile<128, L>(p, epi, m0, n0, smem, z);
+  else tg_tile<256, L>(p, epi, m0, n0, smem, z);
+}
+
+// ---- statistics ----------------------------------------------------------------------------
+
+// 64 rows per workgroup, one per lane; wave w joins the tiles w, w + 16, ... with its rows' sums, then the waves in
+// order. A row's tiles are brought to its largest shift D: l = sum_t sum_t e^(shift_t - D), and with e_y = e^-D
+// (0 where the label's logit is -inf) nll = D + log(e_y + l) (+ reference - label's logit) and scale = g / (e_y + l).
+struct StatArgs {
+  const float* sum;
+  const float* shift;
+  int tiles;
+  int64_t row0, piece, ldp;
+  HeadRows r;
+  const float* weights;
+  float divisor, grad_scale;
+  uint16_t* P;             // nullptr: the loss alone
+  float* scale;            // of the piece
+  float* nll;              // by row
+  uint16_t* Hc;            // dW: the piece's rows, scaled here; else nullptr
+  int64_t K;
+};
+
+__global__ __launch_bounds__(1024) void head_stat_kernel(StatArgs a) {
+  __shared__ float s_d[16][64], s_l[16][64], s_scale[64], s_top[64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t n = piece_rows(a.r.count, a.row0, a.piece), r0 = (int64_t)blockIdx.x * 64;
+  if (r0 >= n) return;                              // uniform
+  const bool in = r0 + lane < n;
+  const int64_t row = in ? r0 + lane : n - 1;
+  float d = 0.0f, l = 0.0f;
+  bool moved = false;
+  for (int t = wave; t < a.tiles; t += 16) {
+    const float s = a.sum[t * a.piece + row], h = a.shift[t * a.piece + row];
+    moved = moved || h != 0.0f;
+    if (h > d) {
+      l *= __expf(d - h);
+      d = h;
+    }
+    l += h == d ? s : s * __expf(h - d);
+  }
+  s_d[wave][lane] = d;
+  s_l[wave][lane] = l;
+  __syncthreads();
+  d = s_d[0][lane];
+#pragma unroll
+  for (int w = 1; w < 16; ++w) d = __builtin_fmaxf(d, s_d[w][lane]);
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) l += s_d[w][lane] == d ? s_l[w][lane] : s_l[w][lane] * __expf(s_d[w][lane] - d);
+  const int64_t at = a.row0 + row;
+  if (wave == 0) {
+    const float logit = a.r.logit[at], ref = a.r.ref[at];
+    const float ey = logit == ref ? __expf(-d) : __expf(logit);   // reference 0: e^-inf = 0, or not a number
+    const float total = ey + l;
+    const int32_t m = a.r.rows[at];
+    const float nll = (logit == ref && d == 0.0f ? log1pf(l) : d + __logf(total)) + (ref - logit);
+    const float w = a.weights ? a.weights[m] : 1.0f;
+    const float div = a.divisor != 0.0f ? a.divisor : (float)a.r.count[0];
+    const float scale = a.grad_scale * w / div / total;
+    s_scale[lane] = scale;
+    s_top[lane] = d;
+    if (in) {
+      a.nll[m] = nll;
+      a.scale[row] = scale;
+    }
+  }
+  if (!a.P) return;
+  __syncthreads();
+  const bool any = __syncthreads_or(moved || d != 0.0f);
+  if (any) {                                        // rare: rows whose tiles have different shifts
+    for (int q = 0; q < 64 && r0 + q < n; ++q) {
+      const float top = s_top[q];
+      if (top == 0.0f) continue;
+      uint16_t* p = a.P + (r0 + q) * a.ldp;
+      for (int64_t c = tid; c < a.ldp; c += 1024) {
+        const float h = a.shift[(c / kTgN) * a.piece + r0 + q];
+        if (h != top) p[c] = f32_to_bf16(bf16_to_f32(p[c]) * __expf(h - top));
+      }
+    }
+    __syncthreads();
+  }
+  if (wave == 0 && in) a.P[row * a.ldp + a.r.label[at]] = f32_to_bf16(-l);
+  if (a.Hc) {
+    for (int64_t i = tid; i < 64 * (a.K / 8); i += 1024) {
+      const int64_t q = i / (a.K / 8), k = (i - q * (a.K / 8)) * 8;
+      if (r0 + q >= n) break;
+      uint16_t* h = a.Hc + (r0 + q) * a.K + k;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(h);
+      const float s = s_scale[q];
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(s * __uint_as_float(x[e] << 16), s * __uint_as_float(x[e] & 0xFFFF0000u));
+      *reinterpret_cast<u32x4_t*>(h) = u32x4_t{o[0], o[1], o[2], o[3]};
+    }
+  }
+}
+
+// ---- gradients --------------------------------------------------------------------------------
+
+// dH rows, scaled, at their places; or, in reduction slices, fp32 partials [slices][piece][K].
+struct DhEpi {
+  const float* scale;      // of the piece
+  const int32_t* rows;
+  int64_t n, K, piece;
+  uint16_t* dH;
+  float* part;
+  template <int MI>
+  __device__ __forceinline__ void operator()(f32x16_t (&acc)[MI][2], int64_t m0, int64_t n0, int wm, int wn, int z,
+                                             uint16_t* smem) const {
+    const int lane = threadIdx.x & 63;
+    if (part) {
+      float* out = part + (int64_t)z * piece * K;
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int64_t row = m0 + wm * (32 * MI) + 32 * i + (v & 3) + 4 * (lane >> 5) + 8 * (v >> 2);
+          if (row >= n) continue;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int64_t col = n0 + 64 * wn + 32 * j + (lane & 31);
+            if (col < K) out[row * K + col] = acc[i][j][v];
+          }
+        }
+      return;
+    }
+    constexpr int kPitch = 64 + 8;
+    uint16_t* ep = smem + (wm * 4 + wn) * (32 * kPitch);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int r = (v & 3) + 4 * (lane >> 5) + 8 * (v >> 2);
+        const int64_t row = m0 + wm * (32 * MI) + 32 * i + r;
+        const float s = scale[row < n ? row : n - 1];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) ep[r * kPitch + 32 * j + (lane & 31)] = f32_to_bf16(s * acc[i][j][v]);
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const int r = 8 * it + (lane >> 3), c = 8 * (lane & 7);
+        const u32x4_t val = *reinterpret_cast<const u32x4_t*>(ep + r * kPitch + c);
+        const int64_t row = m0 + wm * (32 * MI) + 32 * i + r, col = n0 + 64 * wn + c;
+        if (row < n && col < K) *reinterpret_cast<u32x4_t*>(dH + (int64_t)rows[row] * K + col) = val;
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+    }
+  }
+};
+
+__global__ __launch_bounds__(kTgThreads, 1) void head_dh_kernel(TgArgs p, DhEpi epi, const int32_t* count, int64_t row0, int cus) {
+  __shared__ __attribute__((aligned(1024))) uint16_t smem[kTgSmem];
+  epi.n = piece_rows(count, row0, epi.piece);
+  const TgPlan pl = tg_plan(epi.n, epi.K, p.slices, cus);
+  int64_t m0, n0;
+  int z;
+  if (!tg_where(pl, p.slices, (int)blockIdx.x, &m0, &n0, &z)) return;
+  using L = TgLayout<false, true, false, false>;
+  if (pl.half) tg_tile<128, L>(p, epi, m0, n0, smem, z);
+  else tg_tile<256, L>(p, epi, m0, n0, smem, z);
+}
+
+// dH from its slices, added in order.
+__global__ __launch_bounds__(256) void head_dh_sum_kernel(const float* __restrict__ part, int S, int64_t piece, int64_t K,
+                                                          const int32_t* count, int64_t row0, const float* __restrict__ scale,
+                                                          const int32_t* __restrict__ rows, uint16_t* __restrict__ dH) {
+  const int64_t n = piece_rows(count, row0, piece), per = K / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = i / per, k = (i - row * per) * 8;
+  if (row >= n) return;
+  f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
+  for (int z = 0; z < S; ++z) {
+    const float* q = part + ((int64_t)z * piece + row) * K + k;
+    a += *reinterpret_cast<const f32x4_t*>(q);
+    b += *reinterpret_cast<const f32x4_t*>(q + 4);
+  }
+  const float s = scale[row];
+  *reinterpret_cast<u32x4_t*>(dH + (int64_t)rows[row] * K + k) =
+      u32x4_t{pack_bf16x2(s * a.x, s * a.y), pack_bf16x2(s * a.z, s * a.w), pack_bf16x2(s * b.x, s * b.y), pack_bf16x2(s * b.z, s * b.w)};
+}
+
+// dW tile, with the sum of the pieces before in E (fp32; nullptr: none), to fp32 or bf16.
+struct DwEpi {
+  const float* E;
+  void* out;
+  bool bf16;
+  int64_t V, K;
+  template <int MI>
+  __device__ __forceinline__ void operator()(f32x16_t (&acc)[MI][2], int64_t m0, int64_t n0, int wm, int wn, int z,
+                                             uint16_t* smem) const {
+    constexpr int kPitch = 64 + 4;
+    const int lane = threadIdx.x & 63;
+    float* ep = reinterpret_cast<float*>(smem) + (wm * 4 + wn) * (32 * kPitch);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int r = (v & 3) + 4 * (lane >> 5) + 8 * (v >> 2);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) ep[r * kPitch + 32 * j + (lane & 31)] = acc[i][j][v];
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const int r = 8 * it + (lane >> 3), c = 8 * (lane & 7);
+        f32x4_t a = *reinterpret_cast<const f32x4_t*>(ep + r * kPitch + c);
+        f32x4_t b = *reinterpret_cast<const f32x4_t*>(ep + r * kPitch + c + 4);
+        const int64_t row = m0 + wm * (32 * MI) + 32 * i + r, col = n0 + 64 * wn + c;
+        if (row < V && col < K) {
+          const int64_t at = row * K + col;
+          if (E) {
+            a += *reinterpret_cast<const f32x4_t*>(E + at);
+            b += *reinterpret_cast<const f32x4_t*>(E + at + 4);
+          }
+          if (bf16) {
+            *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + at) =
+                u32x4_t{pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w)};
+          } else {
+            *reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + at) = a;
+            *reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + at + 4) = b;
+          }
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+    }
+  }
+};
+
+__global__ __launch_bounds__(kTgThreads, 1) void head_dw_kernel(TgArgs p, DwEpi epi, TgPlan pl, const int32_t* count, int64_t row0,
+                                                                int64_t piece) {
+  __shared__ __attribute__((aligned(1024))) uint16_t smem[kTgSmem];
+  const int64_t n = piece_rows(count, row0, piece);
+  p.kmain = (n + kTgK - 1) / kTgK * kTgK;           // P's rows up to there are zeros, H's repeat its last row
+  p.krows_a = p.kmain > 0 ? p.kmain : 1;
+  p.krows_b = n > 0 ? n : 1;
+  p.per_slice = (int)(p.kmain / kTgK);
+  int64_t m0, n0;
+  int z;
+  if (!tg_where(pl, 1, (int)blockIdx.x, &m0, &n0, &z)) return;
+  using L = TgLayout<true, true, false, false>;
+  if (pl.half) tg_tile<128, L>(p, epi, m0, n0, smem, z);
+  else tg_tile<256, L>(p, epi, m0, n0, smem, z);
+}
+
+__global__ __launch_bounds__(1024) void head_loss_kernel(const float* __restrict__ nll, const float* __restrict__ weights,
+                                                         const int32_t* __restrict__ rows, const int32_t* __restrict__ count,
+                                                         float divisor, float* __restrict__ loss) {
+  __shared__ double red[16];
+  const int n = count[0], tid = threadIdx.x;
+  double s = 0.0;
+  for (int i = tid; i < n; i += 1024) {
+    const int32_t m = rows[i];
+    s += (double)nll[m] * (weights ? (double)weights[m] : 1.0);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  if ((tid & 63) == 0) red[tid >> 6] = s;
+  __syncthreads();
+  if (tid == 0) {
+    s = 0.0;
+    for (int w = 0; w < 16; ++w) s += red[w];
+    const double div = divisor != 0.0f ? (double)divisor : (double)(n > 0 ? n : 1);
+    loss[0] = (float)(s / div);
+  }
+}
+
+// Rows of a piece: P of at most 2^29 values, at least 256 rows.
+int64_t head_piece(int64_t M, int64_t ldp) {
+  int64_t most = ((int64_t)1 << 29) / ldp / 256 * 256;
+  if (most < 256) most = 256;
+  const int64_t all = M > 256 ? hd_cdiv(M, 256) * 256 : 256;
+  return all < most ? all : most;
+}
+
+// Slices of dH's reduction (over the vocabulary) where the tiles leave CUs idle, of at least 8 stages.
+int head_slices(int64_t rows, int64_t K, int64_t ldp) {
+  const int64_t cus = device_cu_count(), nk = ldp / kTgK;
+  const int64_t tiles = hd_cdiv(rows > 0 ? rows : 1, 128) * hd_cdiv(K, kTgN);
+  int64_t S = cus / tiles;
+  if (S > nk / 8) S = nk / 8;
+  if (S > 16) S = 16;
+  if (S < 2) return 1;
+  const int64_t per = hd_cdiv(nk, S);
+  return (int)hd_cdiv(nk, per);
+}
+
+}  // namespace
+
+HeadWorkspace head_workspace_layout(int64_t M, int64_t K, int64_t V, bool dH, bool dW, bool dw_bf16) {
+  const int64_t ldp = hd_cdiv(V, 64) * 64;
+  HeadWorkspace L;
+  L.piece = head_piece(M, ldp);
+  size_t off = 0;
+  auto take = [&](int64_t bytes) { const size_t at = off; off += align_up((size_t)bytes, 256); return at; };
+  L.rows_off = take(8 * M);                         // rows, then slots
+  L.count_off = take(4);
+  L.ref_off = take(8 * M);                          // references, then label logits
+  L.label_off = take(4 * M);
+  L.scale_off = take(4 * L.piece);
+  L.stat_off = take(8 * hd_cdiv(V, kTgN) * L.piece);
+  L.h_off = take(2 * M * K);
+  L.p_off = take(2 * L.piece * ldp);
+  const int S = dH ? head_slices(L.piece < M ? L.piece : M, K, ldp) : 1;
+  L.part_off = take(S > 1 ? 4 * (int64_t)S * L.piece * K : 0);
+  L.dw_off = take(dW && dw_bf16 && M > L.piece ? 4 * V * K : 0);
+  L.total = off > 0 ? off : 256;
+  return L;
+}
+
+hipError_t launch_head_loss(const HeadCall& c, hipStream_t stream) {
+  const int64_t M = c.M, K = c.K, V = c.V, ldp = hd_cdiv(V, 64) * 64;
+  const HeadWorkspace L = head_workspace_layout(M, K, V, c.dH != nullptr, c.dW != nullptr, c.dw_bf16);
+  char* b = static_cast<char*>(c.ws);
+  int32_t* rows = reinterpret_cast<int32_t*>(b + L.rows_off);
+  int32_t* slot = rows + M;
+  int32_t* count = reinterpret_cast<int32_t*>(b + L.count_off);
+  float* ref = reinterpret_cast<float*>(b + L.ref_off);
+  float* logit = ref + M;
+  int32_t* label = reinterpret_cast<int32_t*>(b + L.label_off);
+  float* scale = reinterpret_cast<float*>(b + L.scale_off);
+  float* sum = reinterpret_cast<float*>(b + L.stat_off);
+  const int64_t tiles = hd_cdiv(V, kTgN);
+  float* shift = sum + tiles * L.piece;
+  uint16_t* Hc = reinterpret_cast<uint16_t*>(b + L.h_off);
+  uint16_t* P = reinterpret_cast<uint16_t*>(b + L.p_off);
+  float* part = reinterpret_cast<float*>(b + L.part_off);
+  float* dwsum = reinterpret_cast<float*>(b + L.dw_off);
+  const int cus = device_cu_count();
+  const bool grad = c.dH || c.dW;
+
+  hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(1024), 0, stream, c.labels, M, V, rows, slot, count);
+  if (M > 0)
+    hipLaunchKernelGGL(head_gather_kernel, dim3((unsigned)M), dim3(256), 0, stream, c.H, c.W, c.labels, K, slot, Hc, ref, logit,
+                       label, c.nll, c.dH);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int S = c.dH ? head_slices(L.piece < M ? L.piece : M, K, ldp) : 1;
+  const HeadRows hr{rows, count, ref, logit, label};
+  for (int64_t r0 = 0; r0 < M || r0 == 0; r0 += L.piece) {
+    const int64_t most = M - r0 < L.piece ? M - r0 : L.piece;     // rows there may be
+    const bool last = r0 + L.piece >= M;
+    if (most > 0) {
+      TgArgs p{};
+      p.A = {Hc + r0 * K, K, most};
+      p.B = {c.W, K, V};
+      p.kmain = K;
+      p.per_slice = (int)(K / kTgK);
+      p.slices = 1;
+      const ProbEpi pe{ref + r0, label + r0, 0, V, ldp, L.piece, P, sum, shift};
+      hipLaunchKernelGGL(head_prob_kernel, dim3((unsigned)tg_grid(most, V, 1)), dim3(kTgThreads), 0, stream, p, pe, count, r0, V, cus);
+      const StatArgs sa{sum, shift, (int)tiles, r0, L.piece, ldp, hr, c.weights, c.divisor, c.grad_scale, grad ? P : nullptr,
+                        scale, c.nll, c.dW ? Hc + r0 * K : nullptr, K};
+      hipLaunchKernelGGL(head_stat_kernel, dim3((unsigned)hd_cdiv(most, 64)), dim3(1024), 0, stream, sa);
+    }
+    if (c.dH && most > 0) {
+      TgArgs p{};
+      p.A = {P, ldp, L.piece};
+      p.B = {c.W, K, K};
+      p.kmain = ldp;
+      p.krows_b = V;
+      p.per_slice = (int)hd_cdiv(ldp / kTgK, S);
+      p.slices = S;
+      const DhEpi de{scale, rows + r0, 0, K, L.piece, c.dH, S > 1 ? part : nullptr};
+      hipLaunchKernelGGL(head_dh_kernel, dim3((unsigned)tg_grid(most, K, S)), dim3(kTgThreads), 0, stream, p, de, count, r0, cus);
+      if (S > 1)
+        hipLaunchKernelGGL(head_dh_sum_kernel, dim3((unsigned)hd_cdiv(most * K / 8, 256)), dim3(256), 0, stream, part, S, L.piece, K,
+                           count, r0, scale, rows + r0, c.dH);
+    }
+    if (c.dW) {
+      TgArgs p{};
+      p.A = {P, ldp, ldp};
+      p.B = {Hc + r0 * K, K, K};
+      p.slices = 1;
+      const TgPlan pl = tg_plan(V, K, 1, cus);
+      float* f32 = c.dw_bf16 ? dwsum : static_cast<float*>(c.dW);
+      const DwEpi we{r0 > 0 ? f32 : nullptr, last ? c.dW : f32, last && c.dw_bf16, V, K};
+      hipLaunchKernelGGL(head_dw_kernel, dim3((unsigned)(pl.tiles_m * pl.tiles_n)), dim3(kTgThreads), 0, stream, p, we, pl, count, r0,
+                         L.piece);
+    }
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(head_loss_kernel, dim3(1), dim3(1024), 0, stream, c.nll, c.weights, rows, count, c.divisor, c.loss);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

@@ -225,7 +225,8 @@ size_t skinny_partial_bytes(int64_t M, int64_t K, int64_t N);
 // dr: A is the adapter input X ([M][K], lda == K), dropped in registers.
 hipError_t skinny_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t K, int r,
                      float* part, float alpha, uint16_t* out, int64_t ldo, float alpha2, uint16_t* out2,
-                     hipStream_t stream, const DropoutParams* dr = nullptr);
+                     hipStream_t stream, const DropoutParams* dr = nullptr, int64_t pitch = 0);
+// (pitch: elements between rows of out, ldo where 0)
 // dr: L is the adapter input X ([M][W], ldl == W), dropped in registers.
 hipError_t skinny_tn(const uint16_t* L, int64_t ldl, int64_t W, const uint16_t* S, int64_t lds, int64_t M, int r,
                      float* part, float alpha, bool transpose, bool out_bf16, void* out, hipStream_t stream,
@@ -405,5 +406,115 @@ hipError_t linear_backward(const NF4View& W, const NF4Table& tab, const uint16_t
                            int64_t M, const uint16_t* L1, const uint16_t* L2, int r, float s,
                            const uint16_t* T, uint16_t* dX, void* dL1, void* dL2, bool grad_bf16,
                            void* ws, hipStream_t stream, const DropoutParams* dr = nullptr);
+
+// The adapter products beside another kernel's product (gemm.hip). width, pitch:
+// columns written (zeros from r on) and elements between rows of sT and sU.
+//   down: sT = bf16(s X L1), T_out (or NULL) = bf16(X L1); l1t: L1^T [rank rounded up to 64][K], zero rows from r on
+//   up:   sU = bf16(s dY L2^T); l2p: L2 [rank rounded up to 64][ldl], zeros from row r and column N on, ldl a multiple
+//         of 64 up to which dY's rows (ldy apart) can be read
+//   grads: dL1 = X^T sU, dL2 = s T^T dY
+size_t adapter_partial_bytes(int64_t M, int64_t K, int64_t N, int r);
+hipError_t adapter_down(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, const uint16_t* l1t, int r, float s,
+                        uint16_t* sT, int64_t width, int64_t pitch, uint16_t* T_out, float* part, hipStream_t stream);
+hipError_t adapter_up(const uint16_t* dY, int64_t ldy, int64_t M, int64_t N, const uint16_t* l2p, int64_t ldl, int r,
+                      float s, uint16_t* sU, int64_t width, int64_t pitch, float* part, hipStream_t stream);
+hipError_t adapter_grads(const uint16_t* X, int64_t K, const uint16_t* dY, int64_t ldy, int64_t N, int64_t M,
+                         const uint16_t* sU, int64_t ldu, const uint16_t* T, int r, float s, void* dL1, void* dL2,
+                         bool grad_bf16, float* part, hipStream_t stream);
+hipError_t launch_small_lora_down(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r, float s,
+                                  uint16_t* sT, int64_t ldst, uint16_t* T_out, float* part, hipStream_t stream);
+
+// The gated feed-forward block (gated.hip): two bases [F][K], adapters stacked
+// gate first: L1 [2][K][r], L2 [2][r][F], T [2][M][r].
+struct GatedBase {
+  NF4View gate, up;
+  NF4Table tab_gate, tab_up;
+};
+struct Int8Values {              // blocks of 64 (the blockwise Int8 codec)
+  int8_t* codes;
+  float* absmax;
+};
+enum GatedAct { kActSilu = 0, kActGelu = 1 };
+struct GatedWorkspace {
+  size_t wd_off;     // bf16 [2 Fp][K]: both dequantised weights, rows in pairs of blocks of 32 (Fp: F rounded up to 64)
+  size_t l1t_off;    // bf16 [2][rp][K]: L1^T
+  size_t l2_off;     // forward: bf16 [2 Fp][2 rp], L2^T in the rows' order; backward: bf16 [2][rp][Fp], L2
+  size_t st_off;     // bf16 [M][2 rp]: s T, or s U
+  size_t t_off;      // bf16 [2][M][r]: T, when the caller has none
+  size_t dgu_off;    // backward: bf16 [M][2 Fp]: dG, then dU
+  size_t x_off;      // backward: bf16 [M][K]: X from its 8-bit values
+  size_t part_off;   // fp32 partials
+  size_t part2_off;  // few rows: fp32 partials of both base products
+  size_t total;
+};
+constexpr int64_t kLayerMaxRows = (int64_t)1 << 21;   // of the entry points of qlora_layers.h
+constexpr int64_t kGatedMaxCols = (int64_t)1 << 22;   // K and F: 32-bit offsets inside a tile
+GatedWorkspace gated_workspace_layout(int64_t M, int64_t K, int64_t F, int r, bool bwd);
+hipError_t gated_forward(const GatedBase& W, const uint16_t* X, int64_t M, const uint16_t* L1, const uint16_t* L2, int r,
+                         float s, int act, uint16_t* A, uint16_t* T_out, const Int8Values* gate8, const Int8Values* up8,
+                         void* ws, hipStream_t stream);
+hipError_t gated_backward(const GatedBase& W, const uint16_t* X, const Int8Values* X8, const uint16_t* dA, int64_t M,
+                          const uint16_t* L1, const uint16_t* L2, int r, float s, int act, const uint16_t* T,
+                          const Int8Values* gate8, const Int8Values* up8, uint16_t* dX, void* dL1, void* dL2,
+                          bool grad_bf16, void* ws, hipStream_t stream);
+
+// The norm with the residual's addition (norm.hip).
+struct NormFwd {
+  const void* x;
+  const void* res;          // or nullptr
+  bool x_bf16, res_bf16;
+  const void* w;            // or nullptr
+  bool w_bf16;
+  int64_t M, K;
+  float eps;
+  uint16_t* y;              // or nullptr
+  int8_t* codes;            // or nullptr
+  float* absmax;
+  void* h;                  // the residual's type; nullptr without a residual
+  float* rstd;              // or nullptr
+};
+struct NormBwd {
+  const uint16_t* dy;
+  const void* h;
+  bool h_bf16;
+  const float* rstd;
+  const void* w;            // or nullptr
+  bool w_bf16;
+  const void* dres;         // h's type, or nullptr
+  int64_t M, K;
+  void* dh;                 // h's type
+  uint16_t* dx16;           // or nullptr
+  float* dw;                // or nullptr
+  float* part;              // fp32 [norm_slices][K], for dw
+};
+constexpr int64_t kNormMaxK = 16384;
+int norm_slices(int64_t M);
+hipError_t launch_norm_fwd(const NormFwd& c, hipStream_t stream);
+hipError_t launch_norm_bwd(const NormBwd& c, hipStream_t stream);
+
+// The loss over the vocabulary (head.hip).
+struct HeadWorkspace {
+  int64_t piece;            // rows whose probabilities are held at once
+  size_t rows_off, count_off, ref_off, label_off, scale_off, stat_off, h_off, p_off, part_off, dw_off;
+  size_t total;
+};
+constexpr int64_t kHeadMaxVocab = (int64_t)1 << 22;
+HeadWorkspace head_workspace_layout(int64_t M, int64_t K, int64_t V, bool dH, bool dW, bool dw_bf16);
+struct HeadCall {
+  const uint16_t* H;
+  const uint16_t* W;
+  const int64_t* labels;
+  const float* weights;     // or nullptr
+  int64_t M, K, V;
+  float divisor;            // 0: the number of counted rows
+  float grad_scale;
+  float* loss;
+  float* nll;
+  uint16_t* dH;             // or nullptr
+  void* dW;                 // or nullptr
+  bool dw_bf16;
+  void* ws;
+};
+hipError_t launch_head_loss(const HeadCall& c, hipStream_t stream);
 
 }  // namespace qlora

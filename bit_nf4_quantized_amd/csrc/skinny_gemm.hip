@@ -418,15 +418,17 @@ __global__ __launch_bounds__(kSkThreads) void skinny_tn_dma_kernel(TnArgs p) {
 }
 
 // out = alpha * sum_z P[z] over a [rows][SJ] slab, columns j < r:
-//   mode 0: out[m][j] (row stride ldo; columns [r, ldo) zero) in bf16, plus
+//   mode 0: out[m][j] (columns [r, ldo) zero) in bf16, plus
 //           optional out2[m][j] = bf16(alpha2 * sum) with row stride r
-//   mode 1: out[m][j] fp32 or bf16, row stride r
+//   mode 1: out[m][j] fp32 or bf16
+// out's rows are `pitch` elements apart.
 // Four consecutive columns per thread (r % 8 == 0 and ldo % 4 == 0, so a
 // group of four is all below r or all at or above it): 16-byte partial loads,
 // the sum over z in order, 8- or 16-byte stores.
 __global__ __launch_bounds__(256) void skinny_reduce_kernel(const float* __restrict__ P, int Z, int64_t rows, int r,
                                                             float alpha, int mode, int out_bf16, void* __restrict__ out,
-                                                            int64_t ldo, float alpha2, uint16_t* __restrict__ out2) {
+                                                            int64_t ldo, float alpha2, uint16_t* __restrict__ out2,
+                                                            int64_t pitch) {
   const int64_t width = (mode == 0) ? ldo : r;
   const int64_t w4 = width / 4;
   const int64_t total = rows * w4;
@@ -434,7 +436,7 @@ __global__ __launch_bounds__(256) void skinny_reduce_kernel(const float* __restr
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t m = i / w4, j = (i - m * w4) * 4;
-    const int64_t o = m * width + j;
+    const int64_t o = m * pitch + j;
     if (j >= r) {
       *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(out) + o) = u32x2_t{0u, 0u};
       continue;
@@ -535,7 +537,7 @@ size_t skinny_partial_bytes(int64_t M, int64_t K, int64_t N) {
 // C = A B^T over K with B [64][ldb] (rows >= r zero), then reduce.
 hipError_t skinny_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t K, int r,
                      float* part, float alpha, uint16_t* out, int64_t ldo, float alpha2, uint16_t* out2,
-                     hipStream_t stream, const DropoutParams* dr) {
+                     hipStream_t stream, const DropoutParams* dr, int64_t pitch) {
   if (dr && lda != K) return hipErrorInvalidValue;  // the mask indexes a contiguous [M][K] input
   // 72 KB of LDS: two workgroups per CU
   const SkinnySplit sp = skinny_split(sk_cdiv(M, SM), K, 2 * (int64_t)device_cu_count());
@@ -550,7 +552,7 @@ hipError_t skinny_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t 
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(skinny_reduce_kernel, dim3((unsigned)sk_grid(M * ldo / 4)), dim3(256), 0, stream, part, sp.Z, M, r,
-                     alpha, 0, 1, (void*)out, ldo, alpha2, out2);
+                     alpha, 0, 1, (void*)out, ldo, alpha2, out2, pitch ? pitch : ldo);
   return hipGetLastError();
 }
 
@@ -576,7 +578,7 @@ hipError_t skinny_tn(const uint16_t* L, int64_t ldl, int64_t W, const uint16_t* 
                        alpha, out_bf16 ? 1 : 0, out);
   else
     hipLaunchKernelGGL(skinny_reduce_kernel, dim3((unsigned)sk_grid(W * (int64_t)r / 4)), dim3(256), 0, stream, part, sp.Z,
-                       W, r, alpha, 1, out_bf16 ? 1 : 0, out, (int64_t)r, 0.0f, (uint16_t*)nullptr);
+                       W, r, alpha, 1, out_bf16 ? 1 : 0, out, (int64_t)r, 0.0f, (uint16_t*)nullptr, (int64_t)r);
   return hipGetLastError();
 }
 

@@ -15,7 +15,7 @@
 //   empties(device, dtype, shape, dtype, shape, ...) -> tuple
 //       new device tensors (1.3 us each from Python)
 //
-// dtype: 0 float32, 1 bfloat16, 2 int32, 3 int64, 4 float64, 5 uint8. Failed checks raise TypeError
+// dtype: 0 float32, 1 bfloat16, 2 int32, 3 int64, 4 float64, 5 uint8, 6 int8. Failed checks raise TypeError
 // or ValueError; C++ exceptions end here as RuntimeError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -34,8 +34,9 @@
 namespace {
 
 const c10::ScalarType kTypes[] = {c10::ScalarType::Float, c10::ScalarType::BFloat16, c10::ScalarType::Int,
-                                  c10::ScalarType::Long, c10::ScalarType::Double,   c10::ScalarType::Byte};
-constexpr int kTypeCount = 6;
+                                  c10::ScalarType::Long, c10::ScalarType::Double,   c10::ScalarType::Byte,
+                                  c10::ScalarType::Char};
+constexpr int kTypeCount = 7;
 
 // nullptr after setting a Python error
 const at::Tensor* tensor_of(PyObject* o, int dtype, long device, const char* name) {

@@ -1,0 +1,350 @@
+// Core of the bf16 MFMA products with an epilogue of their own (gated.hip,
+// head.hip), for gfx950: one workgroup of 8 waves computes a TM x 256 tile of
+//
+//   C[m][n] = sum_k A[m][k] B[n][k]  (+ sum_j A2[m][j] B2[n][j])
+//
+// in fp32 accumulators and hands them to the caller's epilogue. Each operand is
+// either row-major (the reduction contiguous in a row) or k-major (the reduction
+// down the rows: B stored [k][n]); a k-major tile lies in LDS as it lies in
+// memory, and its fragments are read with the LDS transpose read.
+//
+// Schedule (that of the dense linear's GEMM): stages of 64 k, copied global ->
+// LDS without registers, A double- and B triple-buffered (160 KB); fragments of
+// k-step kk + 1 are read while the MFMAs of kk run; the copies of stage st + 2
+// go out one instruction at a time among the MFMAs of stage st. A wave owns
+// TM / 2 x 64 outputs as 32 x 32 x 16 MFMA accumulators.
+//
+// Copies take a uniform 64-bit base per tile and stage and a 32-bit offset per
+// lane (inside the tile; k-major: inside 96 rows, so rows of up to 2^24 elements),
+// so operands of any number of rows can be read. Rows past the end of
+// an operand are read from its last row: what they give is never stored, or, down
+// a reduction, meets zeros of the other operand.
+#pragma once
+
+#include "common.h"
+#include "launch.h"
+
+namespace qlora {
+
+typedef __attribute__((address_space(3))) void tg_lds_t;
+typedef short tg_v4i16 __attribute__((ext_vector_type(4)));
+
+constexpr int kTgN = 256, kTgK = 64, kTgWaves = 8, kTgThreads = 64 * kTgWaves;
+constexpr int kTgStage = 256 * kTgK;               // LDS elements per operand and stage
+constexpr int kTgSmem = 5 * kTgStage;              // A x 2, B x 3
+
+struct TgOperand {
+  const uint16_t* p;
+  int64_t ld;      // elements between rows
+  int64_t n;       // row-major: rows; k-major: columns (a multiple of 8)
+};
+
+struct TgArgs {
+  TgOperand A, B, A2, B2;
+  int64_t kmain, kslab;        // reductions, multiples of 64 (kslab 0: none)
+  int64_t krows_a, krows_b;    // k-major operands: rows that exist (the last one stands for those past it)
+  int per_slice, slices;       // stages per reduction slice
+};
+
+// The operands' layouts and what a stage means.
+//   AK, BK  the operand is k-major
+//   SLAB    there is a second pair of operands, in the same layouts
+//   PAIRED  B (k-major, main) has its rows in pairs of blocks: block b of 32 rows
+//           of the first half at 64 b, of the second half at 64 b + 32
+template <bool AK, bool BK, bool SLAB, bool PAIRED>
+struct TgLayout {
+  static constexpr bool kAK = AK, kBK = BK, kSlab = SLAB, kPaired = PAIRED;
+};
+
+__device__ __forceinline__ int tg_swz(int row) { return (row >> 1) & 7; }     // row-major stage rows (128 bytes)
+
+// One stage of an operand, W rows (row-major) or columns (k-major) wide: this
+// wave's copy instruction j of NI. Lane i of an instruction writes 16 bytes at
+// 16 i of a 1 KB slice.
+//   row-major: 8 rows of 128 bytes; chunk c of row r at c ^ tg_swz(r)
+//   k-major: 512 / W rows of 2 W bytes; chunk c of row k at c ^ 4 (k % 4): the
+//   four rows that a transpose read touches lie in different banks
+__device__ __forceinline__ void tg_copy(const char* base, uint32_t off, uint16_t* lds, int slice) {
+  const uint64_t v = reinterpret_cast<uint64_t>(base);
+  const uint64_t b = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v) |
+                     (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32;
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(tg_lds_t*)(lds + slice * 512));
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" :: "v"(off), "s"(b), "s"(m0)
+               : "memory", "m0");
+}
+
+// The lane's place in copy instruction j: its row in the stage (row-major: tile row, k-major: k) and 16-byte chunk.
+template <int W, bool KMAJOR, int NI>
+__device__ __forceinline__ void tg_place(int j, int* row, int* chunk) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int slice = wave * NI + j;
+  if constexpr (KMAJOR) {
+    constexpr int kLanes = W / 8;                     // per k row
+    *row = slice * (64 / kLanes) + lane / kLanes;
+    *chunk = (lane % kLanes) ^ ((*row & 3) << 2);
+  } else {
+    *row = slice * 8 + (lane >> 3);
+    *chunk = (lane & 7) ^ tg_swz(*row);
+  }
+}
+
+// One operand's copies of a tile.
+template <int W, bool KMAJOR>
+struct TgSource {
+  static constexpr int kNi = W / 8 / kTgWaves;        // copy instructions per wave and stage
+  uint32_t off[kNi];       // row-major: the lane's offset from the tile's first row; k-major: from column 0
+  __device__ __forceinline__ void init(const TgOperand& o, int64_t first) {
+#pragma unroll
+    for (int j = 0; j < kNi; ++j) {
+      int row, chunk;
+      tg_place<W, KMAJOR, kNi>(j, &row, &chunk);
+      if constexpr (KMAJOR) {
+        int64_t col = first + chunk * 8;
+        if (col > o.n - 8) col = o.n - 8;
+        off[j] = (uint32_t)(col * 2);
+      } else {
+        const int64_t r = first + row < o.n ? row : o.n - 1 - first;
+        off[j] = (uint32_t)((r * o.ld + chunk * 8) * 2);
+      }
+    }
+  }
+};
+
+// Epilogue: a struct E with
+//   template <int MI> __device__ void operator()(f32x16_t (&acc)[MI][2], int64_t m0, int64_t n0, int wm, int wn,
+//                                                int z, uint16_t* smem) const;
+// called by all waves after a barrier; register v of lane l of acc[i][j] is row
+// m0 + wm 32 MI + 32 i + (v % 4) + 4 (l / 32) + 8 (v / 4), column n0 + 64 wn + 32 j + l % 32.
+template <int TM, class L, class E>
+__device__ __forceinline__ void tg_tile(const TgArgs& p, const E& epi, int64_t m0, int64_t n0, uint16_t* smem, int z) {
+  constexpr int MI = TM / 64, NJ = 2;
+  using SA = TgSource<TM, L::kAK>;
+  using SB = TgSource<kTgN, L::kBK>;
+  constexpr int NA = SA::kNi, NB = SB::kNi;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int nmain = (int)(p.kmain / kTgK);
+  const int nall = nmain + (L::kSlab ? (int)(p.kslab / kTgK) : 0);
+  const int s0 = z * p.per_slice;
+  const int nk = (s0 + p.per_slice < nall ? s0 + p.per_slice : nall) - s0;   // stages of this slice (may be 0)
+
+  f32x16_t acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+  SA a1, a2;
+  SB b1, b2;
+  a1.init(p.A, m0);
+  b1.init(p.B, n0);
+  if constexpr (L::kSlab) {
+    a2.init(p.A2, m0);
+    b2.init(p.B2, n0);
+  }
+  const char* const A1 = reinterpret_cast<const char*>(p.A.p + (L::kAK ? 0 : m0 * p.A.ld));
+  const char* const B1 = reinterpret_cast<const char*>(p.B.p + (L::kBK ? 0 : n0 * p.B.ld));
+  const char* const A2 = L::kSlab ? reinterpret_cast<const char*>(p.A2.p + (L::kAK ? 0 : m0 * p.A2.ld)) : nullptr;
+  const char* const B2 = L::kSlab ? reinterpret_cast<const char*>(p.B2.p + (L::kBK ? 0 : n0 * p.B2.ld)) : nullptr;
+
+  auto a_buf = [&](int st) { return smem + (st & 1) * kTgStage; };
+  auto b_buf = [&](int st) { return smem + (2 + st % 3) * kTgStage; };
+  // copy instruction q of stage st of the slice: q < NA are the A tile's, the rest the B tile's
+  auto issue_one = [&](int st, int q) {
+    const int at = s0 + st;
+    const bool slab = L::kSlab && at >= nmain;        // uniform
+    const int64_t k0 = (int64_t)(slab ? at - nmain : at) * kTgK;
+    int row, chunk;
+    if (q < NA) {
+      const int64_t ld = slab ? p.A2.ld : p.A.ld;
+      uint32_t off = slab ? a2.off[q] : a1.off[q];
+      const char* base = slab ? A2 : A1;
+      if constexpr (L::kAK) {
+        tg_place<TM, true, NA>(q, &row, &chunk);
+        const int64_t last = p.krows_a - 1 - k0;
+        if (row > last) row = (int)last;
+        off += (uint32_t)row * (uint32_t)(ld * 2);
+        base += k0 * ld * 2;
+      } else {
+        base += k0 * 2;
+      }
+      tg_copy(base, off, a_buf(st), wave * NA + q);
+    } else {
+      const int j = q - NA;
+      const int64_t ld = slab ? p.B2.ld : p.B.ld;
+      uint32_t off = slab ? b2.off[j] : b1.off[j];
+      const char* base = slab ? B2 : B1;
+      if constexpr (L::kBK) {
+        tg_place<kTgN, true, NB>(j, &row, &chunk);
+        int64_t first = k0;
+        if (L::kPaired && !slab) {
+          const int half = (int)(p.kmain / 2 / kTgK);
+          const bool second = at >= half;
+          first = 2 * (k0 - (second ? p.kmain / 2 : 0)) + (second ? 32 : 0);
+          row += row & 32;
+        } else if (!slab) {
+          const int64_t last = p.krows_b - 1 - k0;
+          if (row > last) row = (int)last;
+        }
+        off += (uint32_t)row * (uint32_t)(ld * 2);
+        base += first * ld * 2;
+      } else {
+        base += k0 * 2;
+      }
+      tg_copy(base, off, b_buf(st), wave * NB + j);
+    }
+  };
+  bf16x8_t fa[2][MI], fb[2][NJ];                      // two register sets of k-step fragments
+  // k-major fragments: two transpose reads of 4 k each. Lane j of a group of 16 addresses row 16 kk + 8 (lane / 32)
+  // + 4 h + j / 4, columns c + 4 (j % 4) .. +4, and receives column c + j of the four rows.
+  const int jl = lane & 15, krow = 8 * (lane >> 5) + (jl >> 2), kcol = 16 * ((lane >> 4) & 1) + 4 * (jl & 3);
+  const int kx = (jl >> 2) << 2;                      // chunk swizzle of the lane's rows
+  auto frag_k = [&](const uint16_t* buf, int w, int col, int kk) {
+    const int c = col + kcol;
+    const char* at = reinterpret_cast<const char*>(buf) + (((c >> 3) ^ kx) << 4) + ((c & 7) << 1) + (krow + 16 * kk) * (2 * w);
+    const tg_v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tg_v4i16*)(tg_lds_t*)at);
+    const tg_v4i16 hi =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tg_v4i16*)(tg_lds_t*)(at + 8 * w));
+    return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto frag_r = [&](const uint16_t* buf, int row, int kk) {
+    const int ch = 2 * kk + (lane >> 5);
+    row += lane & 31;
+    return *reinterpret_cast<const bf16x8_t*>(buf + row * kTgK + ((ch ^ tg_swz(row)) << 3));
+  };
+  auto frag = [&](int st, int kk, int set) {
+    const uint16_t* As = a_buf(st);
+    const uint16_t* Bs = b_buf(st);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      if constexpr (L::kAK) fa[set][i] = frag_k(As, TM, wm * (TM / 2) + 32 * i, kk);
+      else fa[set][i] = frag_r(As, wm * (TM / 2) + 32 * i, kk);
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      if constexpr (L::kBK) fb[set][j] = frag_k(Bs, kTgN, 64 * wn + 32 * j, kk);
+      else fb[set][j] = frag_r(Bs, 64 * wn + 32 * j, kk);
+    }
+  };
+  auto mma = [&](int set) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
+  };
+  // the next k-step's reads one by one between this k-step's MFMAs
+  auto order = [&]() {
+    constexpr int nr = MI * (L::kAK ? 2 : 1) + NJ * (L::kBK ? 2 : 1), nm = MI * NJ;
+    if constexpr (nm >= nr) {
+      constexpr int per = nm / nr, left = nm - nr * per;
+#pragma unroll
+      for (int q = 0; q < nr; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, per, 0);
+      }
+      if constexpr (left > 0) __builtin_amdgcn_sched_group_barrier(0x008, left, 0);
+    } else {
+      constexpr int per = nr / nm, left = nr - nm * per;
+#pragma unroll
+      for (int q = 0; q < nm; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x100, per, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      }
+      if constexpr (left > 0) __builtin_amdgcn_sched_group_barrier(0x100, left, 0);
+    }
+  };
+  auto mma_copies = [&](int set, int cst, int first, int cnt, bool on) {
+    constexpr int nm = MI * NJ;
+#pragma unroll
+    for (int q = 0; q < nm; ++q) {
+      acc[q / NJ][q % NJ] =
+          __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][q / NJ], fb[set][q % NJ], acc[q / NJ][q % NJ], 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < cnt; ++c)
+        if (on && (c * nm) / cnt == q) issue_one(cst, first + c);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // On entry the fragments of k-step 0 are in set 0 and the copies of stage st + 1 are complete or in flight, as
+  // are those of B of stage st + 2; its A tile goes out after this stage's barrier.
+  auto stage = [&](int st, bool refill, bool next) {
+#pragma unroll
+    for (int kk = 0; kk < kTgK / 16 - 1; ++kk) {
+      frag(st, kk + 1, (kk + 1) & 1);
+      if (kk == 1) {
+        mma_copies(1, st + 2, NA, NB, refill);
+      } else {
+        mma(kk & 1);
+        order();
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (refill) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(NB) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    if (next) frag(st + 1, 0, 0);
+    mma_copies(1, st + 2, 0, NA, refill);
+  };
+  auto issue = [&](int st) {
+#pragma unroll
+    for (int q = 0; q < NA + NB; ++q) issue_one(st, q);
+  };
+  if (nk > 0) issue(0);
+  if (nk > 1) issue(1);
+  if (nk > 0) {
+    if (nk > 1) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(NA + NB) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    frag(0, 0, 0);
+  }
+  int st = 0;
+  for (; st + 2 < nk; ++st) stage(st, true, true);
+  if (st + 1 < nk) stage(st++, false, true);
+  if (st < nk) stage(st, false, false);
+  __syncthreads();
+  epi.template operator()<MI>(acc, m0, n0, wm, wn, z, smem);
+}
+
+// How a launch's tiles cover M x N on `cus` compute units, one workgroup each at
+// a time: tiles of 256 or 128 rows, whichever ends sooner (a half-height tile
+// takes a little more than half the time; 0.56 measured on both products of the
+// loss at 4096 hidden columns). Also used on the device, where M is known there only.
+struct TgPlan {
+  int tiles_m, tiles_n, half;     // half: tiles of 128 rows
+};
+
+__host__ __device__ inline TgPlan tg_plan(int64_t M, int64_t N, int slices, int cus) {
+  const int tn = (int)((N + kTgN - 1) / kTgN), t1 = (int)((M + 255) / 256), t2 = (int)((M + 127) / 128);
+  const int64_t r1 = ((int64_t)t1 * tn * slices + cus - 1) / cus, r2 = ((int64_t)t2 * tn * slices + cus - 1) / cus;
+  const bool half = 100 * r1 > 56 * r2;
+  return TgPlan{half ? t2 : t1, tn, half ? 1 : 0};
+}
+
+// Workgroups that cover either choice for any M' <= M.
+inline int64_t tg_grid(int64_t M, int64_t N, int slices) {
+  return ((M + 127) / 128) * ((N + kTgN - 1) / kTgN) * slices;
+}
+
+// Tile and slice of workgroup bid: each of the 8 XCDs (bid % 8) takes a contiguous
+// range of the tiles, ordered in groups of 4 tile-rows, so that concurrent tiles
+// share rows of A and columns of B in one L2.
+__device__ __forceinline__ bool tg_where(const TgPlan& pl, int slices, int bid, int64_t* m0, int64_t* n0, int* z) {
+  const int per = pl.tiles_m * pl.tiles_n, n = per * slices;
+  if (bid >= n) return false;
+  const int xcd = bid % 8, q = n / 8, rem = n % 8;
+  const int w = xcd * q + (xcd < rem ? xcd : rem) + bid / 8;
+  *z = w / per;
+  const int t = w - *z * per;
+  const int g = t / (4 * pl.tiles_n), first = 4 * g;
+  const int gm = pl.tiles_m - first < 4 ? pl.tiles_m - first : 4;
+  const int tl = t - g * 4 * pl.tiles_n;
+  *m0 = (int64_t)(first + tl % gm) * (pl.half ? 128 : 256);
+  *n0 = (int64_t)(tl / gm) * kTgN;
+  return true;
+}
+
+}  // namespace qlora

@@ -16,6 +16,7 @@
 // with an epilogue that reads dA and writes dG and dU; with G and U kept in 8
 // bits an elementwise kernel makes them. dX is one product over both, [dG dU]
 // against the same matrix read down its rows.
+#include "act.h"
 #include "common.h"
 #include "launch.h"
 #include "tile_gemm.h"
@@ -25,23 +26,6 @@ namespace qlora {
 namespace {
 
 int64_t gd_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// act and its derivative. sigma (1 - sigma) is 0 for large |z|, where z's derivative may be infinite.
-template <int ACT>
-__device__ __forceinline__ float act_of(float g) {
-  const float z = ACT == kActSilu ? g : 1.5957691216057308f * (g + 0.044715f * (g * g * g));
-  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
-}
-
-template <int ACT>
-__device__ __forceinline__ void act_both(float g, float* a, float* d) {
-  const float z = ACT == kActSilu ? g : 1.5957691216057308f * (g + 0.044715f * (g * g * g));
-  const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-z));
-  const float q = p * (1.0f - p);
-  const float dz = ACT == kActSilu ? 1.0f : 1.5957691216057308f * (1.0f + 0.134145f * (g * g));
-  *a = g * p;
-  *d = q == 0.0f ? p : p + g * q * dz;
-}
 
 // ---- operands ------------------------------------------------------------------------------
 
@@ -287,14 +271,19 @@ struct GatedBwdEpi {
   }
 };
 
-// bf16 output, rows of `ld`.
+// bf16 output, dense [M][N]; or, in reduction slices, fp32 partials [slices][M][N].
 struct StoreEpi {
   uint16_t* C;
-  int64_t ld, M, N;
+  float* part;
+  int64_t M, N;
   template <int MI>
   __device__ __forceinline__ void operator()(f32x16_t (&acc)[MI][2], int64_t m0, int64_t n0, int wm, int wn, int z,
                                              uint16_t* smem) const {
     const int lane = threadIdx.x & 63;
+    if (part) {
+      tg_store_partial(acc, part + (int64_t)z * M * N, M, N, m0, n0, wm, wn);
+      return;
+    }
     constexpr int kPitch = 64 + 8;
     uint16_t* ep = smem + (wm * 4 + wn) * (32 * kPitch);
 #pragma unroll
@@ -310,7 +299,7 @@ struct StoreEpi {
         const int r = 8 * it + (lane >> 3), c = 8 * (lane & 7);
         const u32x4_t val = *reinterpret_cast<const u32x4_t*>(ep + r * kPitch + c);
         const int64_t row = m0 + (wm * MI + i) * 32 + r, col = n0 + 64 * wn + c;
-        if (row < M && col < N) *reinterpret_cast<u32x4_t*>(C + row * ld + col) = val;
+        if (row < M && col < N) *reinterpret_cast<u32x4_t*>(C + row * N + col) = val;
       }
       __builtin_amdgcn_s_waitcnt(0xc07f);
     }
@@ -322,15 +311,16 @@ __global__ __launch_bounds__(kTgThreads, 1) void gated_gemm_kernel(TgArgs p, E e
   __shared__ __attribute__((aligned(1024))) uint16_t smem[kTgSmem];
   int64_t m0, n0;
   int z;
-  if (!tg_where(pl, 1, (int)blockIdx.x, &m0, &n0, &z)) return;
+  if (!tg_where(pl, p.slices, (int)blockIdx.x, &m0, &n0, &z)) return;
   if (pl.half) tg_tile<128, L>(p, epi, m0, n0, smem, z);
   else tg_tile<256, L>(p, epi, m0, n0, smem, z);
 }
 
 template <class L, class E>
 hipError_t run_tiles(const TgArgs& p, const E& epi, int64_t M, int64_t N, hipStream_t stream) {
-  const TgPlan pl = tg_plan(M, N, 1, device_cu_count());
-  hipLaunchKernelGGL((gated_gemm_kernel<L, E>), dim3((unsigned)(pl.tiles_m * pl.tiles_n)), dim3(kTgThreads), 0, stream, p, epi, pl);
+  const TgPlan pl = tg_plan(M, N, p.slices, device_cu_count());
+  hipLaunchKernelGGL((gated_gemm_kernel<L, E>), dim3((unsigned)(pl.tiles_m * pl.tiles_n * p.slices)), dim3(kTgThreads), 0, stream,
+                     p, epi, pl);
   return hipGetLastError();
 }
 
@@ -385,39 +375,89 @@ __global__ __launch_bounds__(256) void gated_dgu_kernel(const uint16_t* __restri
 
 // ---- few rows ------------------------------------------------------------------------------------
 
-// A (and the 8-bit values) from the base products' partials [S][M][F] of each weight and sT [M][2 rp]: one row and 8
-// features per thread, 128 features and 16 rows per workgroup. Slices and ranks are added in order.
+// A (and the 8-bit values) from the base products' partials [S][M][F] of each weight and the adapters' T partials
+// [2][Z][M][r]: 16 rows and 128 features per workgroup, one row and 8 features per thread. The adapters' second factors
+// come through LDS in pieces of 64 ranks (all loads of a piece in flight; read rank by rank from memory, one token of
+// rank 64 took 39 us here). Slices and ranks are added in order.
+constexpr int kFinRanks = 64;
+
 template <int ACT>
-__global__ __launch_bounds__(256) void gated_finish_kernel(const float* __restrict__ pg, const float* __restrict__ pu, int S,
-                                                           const uint16_t* __restrict__ sT, int rp, int r,
-                                                           const uint16_t* __restrict__ L2, GatedOut o) {
-  const int64_t f = (int64_t)blockIdx.x * 128 + 8 * (threadIdx.x & 15);
-  const int64_t row = (int64_t)blockIdx.y * 16 + (threadIdx.x >> 4);
-  if (row >= o.M || f >= o.F) return;
-  const int64_t at = row * o.F + f, all = o.M * o.F;
+__global__ __launch_bounds__(256) void gated_finish_kernel(const float* __restrict__ part, int S,
+                                                           const float* __restrict__ tpart, int Z, int r, float s,
+                                                           const uint16_t* __restrict__ L2, uint16_t* __restrict__ T_out,
+                                                           GatedOut o) {
+  __shared__ float sT[2][16][kFinRanks + 4];
+  __shared__ __attribute__((aligned(16))) uint16_t sL[2][kFinRanks][128];
+  const int tid = threadIdx.x, lr = tid >> 4;
+  const int64_t f0 = (int64_t)blockIdx.x * 128, f = f0 + 8 * (tid & 15);
+  const int64_t row0 = (int64_t)blockIdx.y * 16, row = row0 + lr;
+  const bool in = row < o.M && f < o.F;
+  const int64_t at = in ? row * o.F + f : 0, all = o.M * o.F;
+  const int rows = (int)(o.M - row0 < 16 ? o.M - row0 : 16);
   float v[2][8] = {};
+  constexpr int kSlices = 4;                       // that many slices' loads in flight
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const float* p = (w ? pu : pg) + at;
-    for (int z = 0; z < S; ++z) {
-      const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p + z * all), b = *reinterpret_cast<const f32x4_t*>(p + z * all + 4);
-      v[w][0] += a.x; v[w][1] += a.y; v[w][2] += a.z; v[w][3] += a.w;
-      v[w][4] += b.x; v[w][5] += b.y; v[w][6] += b.z; v[w][7] += b.w;
-    }
-    const uint16_t* t = sT + row * (2 * rp) + w * rp;
-    const uint16_t* l = L2 + (int64_t)w * r * o.F + f;
-    for (int j = 0; j < r; j += 8) {               // r % 8 == 0
-      float x[8];
-      load_bf16(t + j, x);
+    const float* p = part + (int64_t)w * S * all + at;
+    for (int z = 0; z < S; z += kSlices) {
+      f32x4_t a[kSlices], b[kSlices];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float y[8];
-        load_bf16(l + (int64_t)(j + i) * o.F, y);
+      for (int u = 0; u < kSlices; ++u) {
+        const float* q = p + (z + u < S ? z + u : z) * all;
+        a[u] = *reinterpret_cast<const f32x4_t*>(q);
+        b[u] = *reinterpret_cast<const f32x4_t*>(q + 4);
+      }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[w][e] = __builtin_fmaf(x[i], y[e], v[w][e]);
+      for (int u = 0; u < kSlices; ++u) {
+        if (z + u >= S) break;                     // uniform
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[w][e] += a[u][e];
+          v[w][4 + e] += b[u][e];
+        }
       }
     }
   }
+  for (int j0 = 0; j0 < r; j0 += kFinRanks) {
+    const int n = r - j0 < kFinRanks ? r - j0 : kFinRanks;      // a multiple of 8
+    if (j0 > 0) __syncthreads();
+    // L2 [2][n][128 features]: 16 chunks of 16 bytes per rank
+#pragma unroll
+    for (int i = 0; i < 2 * kFinRanks * 16 / 256; ++i) {
+      const int c = tid + 256 * i, w = c / (kFinRanks * 16), j = c / 16 % kFinRanks, ch = c % 16;
+      if (j < n && f0 + 8 * ch < o.F)
+        *reinterpret_cast<u32x4_t*>(&sL[w][j][8 * ch]) =
+            *reinterpret_cast<const u32x4_t*>(L2 + ((int64_t)w * r + j0 + j) * o.F + f0 + 8 * ch);
+    }
+    for (int i = tid; i < 2 * rows * n; i += 256) {
+      const int w = i / (rows * n), k = i / n % rows, j = i % n;
+      const float* p = tpart + (((int64_t)w * Z) * o.M + row0 + k) * r + j0 + j;
+      float t = 0.0f;
+      for (int z = 0; z < Z; z += 8) {             // loads of 8 slices in flight, added in order
+        float b[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) b[u] = p[(int64_t)(z + u < Z ? z + u : z) * o.M * r];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) t += z + u < Z ? b[u] : 0.0f;
+      }
+      sT[w][k][j] = bf16_to_f32(f32_to_bf16(s * t));
+      if (T_out && blockIdx.x == 0) T_out[((int64_t)w * o.M + row0 + k) * r + j0 + j] = f32_to_bf16(t);
+    }
+    __syncthreads();
+    if (in) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+          const float x = sT[w][lr][j];
+          float y[8];
+          load_bf16(&sL[w][j][8 * (tid & 15)], y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[w][e] = __builtin_fmaf(x, y[e], v[w][e]);
+        }
+    }
+  }
+  if (!in) return;
   float a[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) a[e] = act_of<ACT>(v[0][e]) * v[1][e];
@@ -443,9 +483,13 @@ GatedWorkspace gated_workspace_layout(int64_t M, int64_t K, int64_t F, int r, bo
   L.t_off = take(bwd ? 2 * M * r * 2 : 0);
   L.dgu_off = take(bwd ? M * 2 * Fp * 2 : 0);
   L.x_off = take(bwd ? M * K * 2 : 0);
-  L.part_off = take((int64_t)adapter_partial_bytes(M, K, Fp, r));
+  int64_t part = (int64_t)adapter_partial_bytes(AdapterShape{2, M, K, Fp, r, 0.0f});
+  const int64_t S = bwd ? tg_slices(M, K, (2 * Fp + 2 * rp) / kTgK, device_cu_count()) : 1;
+  if (S > 1 && S * M * K * 4 > part) part = S * M * K * 4;
+  if (2 * (int64_t)gemv1_partial_bytes(K, r) > part) part = 2 * gemv1_partial_bytes(K, r);
+  L.part_off = take(part);
   const int64_t few = M < kMultiSmallRows ? M : kMultiSmallRows;
-  L.part2_off = take(bwd ? 0 : 2 * multi_small_partial_floats(few, K, F) * 4);
+  L.part2_off = take(bwd ? 0 : small_pair_partial_floats(few, K, F) * 4);
   L.total = off > 0 ? off : 256;
   return L;
 }
@@ -523,25 +567,20 @@ hipError_t gated_forward(const GatedBase& W, const uint16_t* X, int64_t M, const
   const GatedBuffers b(L, ws);
   GatedOut o{A, {gate8 ? gate8->codes : nullptr, up8 ? up8->codes : nullptr},
              {gate8 ? gate8->absmax : nullptr, up8 ? up8->absmax : nullptr}, M, F};
+  if (!gate8 && gemv1_pair_applies(W, M, r)) return launch_gemv1_pair(W, X, L1, L2, r, s, act, A, T_out, b.part, stream);
   if (M <= kMultiSmallRows) {      // one pass over the 4-bit weights
-    for (int w = 0; w < 2; ++w)
-      GD_TRY(launch_small_lora_down(X, M, K, L1 + w * K * r, r, s, b.st + w * rp, 2 * rp, T_out ? T_out + w * M * r : nullptr,
-                                    b.part, stream));
-    const int S = multi_small_slices(M, K, F);
-    float* pu = b.part2 + (int64_t)S * M * F;
-    GD_TRY(launch_multi_small_base(W.gate, W.tab_gate, X, M, b.part2, stream));
-    GD_TRY(launch_multi_small_base(W.up, W.tab_up, X, M, pu, stream));
+    GD_TRY(launch_small_t_partial(X, M, K, L1, r, b.part, stream, 2));
+    GD_TRY(launch_small_pair_base(W, X, M, b.part2, stream));
+    const int S = small_pair_slices(M, K, F), Z = small_t_slices(K);
     const dim3 grid((unsigned)gd_cdiv(F, 128), (unsigned)gd_cdiv(M, 16));
     if (act == kActSilu)
-      hipLaunchKernelGGL(gated_finish_kernel<kActSilu>, grid, dim3(256), 0, stream, b.part2, pu, S, b.st, (int)rp, r, L2, o);
+      hipLaunchKernelGGL(gated_finish_kernel<kActSilu>, grid, dim3(256), 0, stream, b.part2, S, b.part, Z, r, s, L2, T_out, o);
     else
-      hipLaunchKernelGGL(gated_finish_kernel<kActGelu>, grid, dim3(256), 0, stream, b.part2, pu, S, b.st, (int)rp, r, L2, o);
+      hipLaunchKernelGGL(gated_finish_kernel<kActGelu>, grid, dim3(256), 0, stream, b.part2, S, b.part, Z, r, s, L2, T_out, o);
     return hipGetLastError();
   }
   GD_TRY(launch_gated_adapters(L1, L2, K, F, r, b.l1t, b.l2, nullptr, stream));
-  for (int w = 0; w < 2; ++w)
-    GD_TRY(adapter_down(X, M, K, L1 + w * K * r, b.l1t + w * rp * K, r, s, b.st + w * rp, rp, 2 * rp,
-                        T_out ? T_out + w * M * r : nullptr, b.part, stream));
+  GD_TRY(adapter_down(AdapterShape{2, M, K, F, r, s}, X, L1, b.l1t, b.st, T_out, b.part, stream));
   GD_TRY(launch_dequant_pair(W, Fp, b.wd, stream));
   if (gate8)
     return by_act(
@@ -553,6 +592,8 @@ hipError_t gated_forward(const GatedBase& W, const uint16_t* X, int64_t M, const
 }
 
 namespace {
+
+__global__ __launch_bounds__(256) void gated_sum_kernel(SplitSum s) { split_sum_body(s, (int64_t)blockIdx.x * 256 + threadIdx.x); }
 
 __global__ __launch_bounds__(256) void zero_kernel(uint32_t* __restrict__ p, int64_t words) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256) p[i] = 0u;
@@ -573,6 +614,7 @@ hipError_t gated_backward(const GatedBase& W, const uint16_t* X, const Int8Value
   }
   const GatedWorkspace L = gated_workspace_layout(M, K, F, r, true);
   const GatedBuffers b(L, ws);
+  const AdapterShape sh{2, M, K, F, r, s};
   if (X8) {
     GD_TRY(launch_int8_dequantize(X8->codes, X8->absmax, M * K, 6, b.x, true, stream));
     X = b.x;
@@ -582,19 +624,14 @@ hipError_t gated_backward(const GatedBase& W, const uint16_t* X, const Int8Value
   uint16_t* t = b.t;
   if (!gate8) {
     GD_TRY(launch_gated_adapters(L1, L2, K, F, r, b.l1t, b.l2, nullptr, stream));
-    for (int w = 0; w < 2; ++w)
-      GD_TRY(adapter_down(X, M, K, L1 + w * K * r, b.l1t + w * rp * K, r, s, b.st + w * rp, rp, 2 * rp,
-                          T ? nullptr : t + w * M * r, b.part, stream));
+    GD_TRY(adapter_down(sh, X, L1, b.l1t, b.st, T ? nullptr : t, b.part, stream));
     GD_TRY(by_act(
         act, [&] { return gated_product(b, X, M, K, Fp, rp, GatedBwdEpi<kActSilu>{dA, b.dgu, M, F, Fp}, stream); },
         [&] { return gated_product(b, X, M, K, Fp, rp, GatedBwdEpi<kActGelu>{dA, b.dgu, M, F, Fp}, stream); }));
     GD_TRY(launch_gated_adapters(L1, L2, K, F, r, b.l1t, nullptr, b.l2, stream));
   } else {
     GD_TRY(launch_gated_adapters(L1, L2, K, F, r, b.l1t, nullptr, b.l2, stream));
-    if (!T)
-      for (int w = 0; w < 2; ++w)
-        GD_TRY(adapter_down(X, M, K, L1 + w * K * r, b.l1t + w * rp * K, r, s, b.st + w * rp, rp, 2 * rp, t + w * M * r,
-                            b.part, stream));
+    if (!T) GD_TRY(adapter_down(sh, X, L1, b.l1t, b.st, t, b.part, stream));
     int64_t blocks = gd_cdiv(M * F / 8, 256);
     if (blocks > 16 * device_cu_count()) blocks = 16 * device_cu_count();
     if (act == kActSilu)
@@ -604,8 +641,7 @@ hipError_t gated_backward(const GatedBase& W, const uint16_t* X, const Int8Value
     GD_TRY(hipGetLastError());
   }
   if (T) t = const_cast<uint16_t*>(T);
-  for (int w = 0; w < 2; ++w)
-    GD_TRY(adapter_up(b.dgu + w * Fp, 2 * Fp, M, F, b.l2 + w * rp * Fp, Fp, r, s, b.st + w * rp, rp, 2 * rp, b.part, stream));
+  GD_TRY(adapter_up(sh, b.dgu, 2 * Fp, Fp, b.l2, Fp, b.st, b.part, stream));
   if (dX) {
     TgArgs p{};
     p.A = {b.dgu, 2 * Fp, M};
@@ -615,15 +651,17 @@ hipError_t gated_backward(const GatedBase& W, const uint16_t* X, const Int8Value
     p.kmain = 2 * Fp;
     p.kslab = 2 * rp;
     p.krows_b = 2 * Fp;
-    p.per_slice = (int)((p.kmain + p.kslab) / kTgK);
-    p.slices = 1;
-    GD_TRY(run_tiles<RowPaired>(p, StoreEpi{dX, K, M, K}, M, K, stream));
+    const int64_t nk = (p.kmain + p.kslab) / kTgK;
+    p.slices = tg_slices(M, K, nk, device_cu_count());
+    p.per_slice = (int)gd_cdiv(nk, p.slices);
+    GD_TRY(run_tiles<RowPaired>(p, StoreEpi{dX, p.slices > 1 ? b.part : nullptr, M, K}, M, K, stream));
+    if (p.slices > 1) {
+      const SplitSum sum{b.part, dX, M * K, p.slices};
+      hipLaunchKernelGGL(gated_sum_kernel, dim3((unsigned)gd_cdiv(M * K / 8, 256)), dim3(256), 0, stream, sum);
+      GD_TRY(hipGetLastError());
+    }
   }
-  for (int w = 0; w < 2; ++w)
-    GD_TRY(adapter_grads(X, K, b.dgu + w * Fp, 2 * Fp, F, M, b.st + w * rp, 2 * rp, t + w * M * r, r, s,
-                         static_cast<char*>(dL1) + w * K * r * e, static_cast<char*>(dL2) + w * r * F * e, grad_bf16, b.part,
-                         stream));
-  return hipSuccess;
+  return adapter_grads(sh, X, b.dgu, 2 * Fp, Fp, b.st, t, dL1, dL2, grad_bf16, b.part, stream);
 }
 
 }  // namespace qlora

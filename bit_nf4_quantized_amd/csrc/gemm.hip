@@ -443,14 +443,10 @@ GemmArgs base_args() {
 
 }  // namespace
 
-size_t small_t_partial_bytes(int64_t M, int64_t K, int r);
 hipError_t launch_small_lora_down(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r, float s,
                                   uint16_t* sT, int64_t ldst, uint16_t* T_out, float* part, hipStream_t stream);
 hipError_t launch_gemv(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M,
                        const uint16_t* sT, const uint16_t* L2, int r, uint16_t* Y, hipStream_t stream);
-int small_t_slices(int64_t K);
-hipError_t launch_small_t_partial(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r, float* part,
-                                  hipStream_t stream);
 bool gemv_fuses_t(const NF4View& W, int64_t M, int r);
 hipError_t launch_gemv_fused_t(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M,
                                const float* part, int Z, float s, uint16_t* T_out, const uint16_t* L2, int r,
@@ -803,85 +799,105 @@ hipError_t linear_backward(const NF4View& W, const NF4Table& tab, const uint16_t
   return hipSuccess;
 }
 
-// ---- the adapter products of one of several adapters beside a product of their own --------
-//
-// As in linear_forward and linear_backward: the skinny kernels for rank <= 64
-// where their 32-bit offsets reach, else the 128 x 128 GEMM in reduction slices.
+// ---- adapter products beside another kernel's product --------------------------------------
 
-size_t adapter_partial_bytes(int64_t M, int64_t K, int64_t N, int r) {
+size_t adapter_partial_bytes(const AdapterShape& a) {
+  const int64_t M = a.M, K = a.K, N = a.N, r = a.r;
   const Split sT = choose_split(cdiv(M, BM) * cdiv(r, BN), K), sU = choose_split(cdiv(M, BM) * cdiv(r, BN), N);
   const Split s1 = choose_split(cdiv(K, BM) * cdiv(r, BN), M), s2 = choose_split(cdiv(r, BM) * cdiv(N, BN), M);
-  size_t part = 0;
-  auto upd = [&](int64_t b) { part = (size_t)b > part ? (size_t)b : part; };
+  int64_t part = 0;
+  auto upd = [&](int64_t b) { part = b > part ? b : part; };
   upd((int64_t)sT.Z * M * r * 4);
   upd((int64_t)sU.Z * M * r * 4);
   upd((int64_t)s1.Z * K * r * 4);
   upd((int64_t)s2.Z * r * N * 4);
-  if (r <= 64) upd((int64_t)skinny_partial_bytes(M, K, N));
-  if (M <= kMidMaxM) upd((int64_t)small_t_partial_bytes(M, K, r));
-  return align_up(part, 256);
+  if (r <= 64) upd(a.n * (int64_t)skinny_partial_bytes(M, K, N));
+  if (M <= kMidMaxM) upd(a.n * (int64_t)small_t_partial_bytes(M, K, (int)r));
+  return align_up((size_t)part, 256);
 }
 
-hipError_t adapter_down(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, const uint16_t* l1t, int r, float s,
-                        uint16_t* sT, int64_t width, int64_t pitch, uint16_t* T_out, float* part, hipStream_t stream) {
-  if (skinny_ok(r, M, K)) return skinny_nt(X, K, l1t, K, M, K, r, part, s, sT, width, 1.0f, T_out, stream, nullptr, pitch);
-  GemmArgs a = base_args();
-  a.M = M; a.N = r; a.K = K;
-  a.A = X; a.lda = K;
-  a.B = L1; a.ldb = r;
-  const Split sp = choose_split(cdiv(M, BM) * cdiv(r, BN), K);
-  a.k_split = sp.k_split;
-  a.C = part; a.ldc = r;
-  const hipError_t e = run_gemm<A_ROW, B_COL, EPI_F32, false>(a, sp.Z, stream);
-  if (e != hipSuccess) return e;
-  return reduce(part, sp.Z, M, r, s, sT, true, width, 1.0f, T_out, stream, pitch);
-}
-
-hipError_t adapter_up(const uint16_t* dY, int64_t ldy, int64_t M, int64_t N, const uint16_t* l2p, int64_t ldl, int r,
-                      float s, uint16_t* sU, int64_t width, int64_t pitch, float* part, hipStream_t stream) {
-  if (r <= 64 && fits_dense({M * ldy * 2}))
-    return skinny_nt(dY, ldy, l2p, ldl, M, ldl, r, part, s, sU, width, 0.0f, nullptr, stream, nullptr, pitch);
-  GemmArgs a = base_args();
-  a.M = M; a.N = r; a.K = N;
-  a.A = dY; a.lda = ldy;
-  a.B = l2p; a.ldb = ldl;
-  const Split sp = choose_split(cdiv(M, BM) * cdiv(r, BN), N);
-  a.k_split = sp.k_split;
-  a.C = part; a.ldc = r;
-  const hipError_t e = run_gemm<A_ROW, B_ROW, EPI_F32, false>(a, sp.Z, stream);
-  if (e != hipSuccess) return e;
-  return reduce(part, sp.Z, M, r, s, sU, true, width, 0.0f, nullptr, stream, pitch);
-}
-
-hipError_t adapter_grads(const uint16_t* X, int64_t K, const uint16_t* dY, int64_t ldy, int64_t N, int64_t M,
-                         const uint16_t* sU, int64_t ldu, const uint16_t* T, int r, float s, void* dL1, void* dL2,
-                         bool grad_bf16, float* part, hipStream_t stream) {
-  if (r <= 64) {
-    const hipError_t e = skinny_tn(X, K, K, sU, ldu, M, r, part, 1.0f, false, grad_bf16, dL1, stream);
-    if (e != hipSuccess) return e;
-    return skinny_tn(dY, ldy, N, T, r, M, r, part, s, true, grad_bf16, dL2, stream);
+hipError_t adapter_down(const AdapterShape& a, const uint16_t* X, const uint16_t* L1, const uint16_t* l1t, uint16_t* sT,
+                        uint16_t* T_out, float* part, hipStream_t stream) {
+  const int64_t rp = cdiv(a.r, 64) * 64, pitch = a.n * rp;
+  if (skinny_ok(a.r, a.M, a.K)) {
+    const SkinnyBatch b{a.n, 0, rp * a.K, rp, a.M * a.r};
+    return skinny_nt(X, a.K, l1t, a.K, a.M, a.K, a.r, part, a.s, sT, rp, 1.0f, T_out, stream, nullptr, pitch, &b);
   }
-  GemmArgs a = base_args();
-  a.M = K; a.N = r; a.K = M;
-  a.A = X; a.lda = K;
-  a.B = sU; a.ldb = ldu;
-  const Split s1 = choose_split(cdiv(K, BM) * cdiv(r, BN), M);
-  a.k_split = s1.k_split;
-  a.C = part; a.ldc = r;
-  hipError_t e = run_gemm<A_COL, B_COL, EPI_F32, false>(a, s1.Z, stream);
-  if (e != hipSuccess) return e;
-  e = reduce(part, s1.Z, K, r, 1.0f, dL1, grad_bf16, r, 0.0f, nullptr, stream);
-  if (e != hipSuccess) return e;
-  a = base_args();
-  a.M = r; a.N = N; a.K = M;
-  a.A = T; a.lda = r;
-  a.B = dY; a.ldb = ldy;
-  const Split s2 = choose_split(cdiv(r, BM) * cdiv(N, BN), M);
-  a.k_split = s2.k_split;
-  a.C = part; a.ldc = N;
-  e = run_gemm<A_COL, B_COL, EPI_F32, false>(a, s2.Z, stream);
-  if (e != hipSuccess) return e;
-  return reduce(part, s2.Z, r, N, s, dL2, grad_bf16, N, 0.0f, nullptr, stream);
+  for (int k = 0; k < a.n; ++k) {
+    GemmArgs g = base_args();
+    g.M = a.M; g.N = a.r; g.K = a.K;
+    g.A = X; g.lda = a.K;
+    g.B = L1 + k * a.K * a.r; g.ldb = a.r;
+    const Split sp = choose_split(cdiv(a.M, BM) * cdiv(a.r, BN), a.K);
+    g.k_split = sp.k_split;
+    g.C = part; g.ldc = a.r;
+    hipError_t e = run_gemm<A_ROW, B_COL, EPI_F32, false>(g, sp.Z, stream);
+    if (e != hipSuccess) return e;
+    e = reduce(part, sp.Z, a.M, a.r, a.s, sT + k * rp, true, rp, 1.0f, T_out ? T_out + k * a.M * a.r : nullptr, stream, pitch);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t adapter_up(const AdapterShape& a, const uint16_t* dY, int64_t ldy, int64_t y_step, const uint16_t* l2p,
+                      int64_t ldl, uint16_t* sU, float* part, hipStream_t stream) {
+  const int64_t rp = cdiv(a.r, 64) * 64, pitch = a.n * rp;
+  if (a.r <= 64 && fits_dense({a.M * ldy * 2})) {
+    const SkinnyBatch b{a.n, y_step, rp * ldl, rp, 0};
+    return skinny_nt(dY, ldy, l2p, ldl, a.M, ldl, a.r, part, a.s, sU, rp, 0.0f, nullptr, stream, nullptr, pitch, &b);
+  }
+  for (int k = 0; k < a.n; ++k) {
+    GemmArgs g = base_args();
+    g.M = a.M; g.N = a.r; g.K = a.N;
+    g.A = dY + k * y_step; g.lda = ldy;
+    g.B = l2p + k * rp * ldl; g.ldb = ldl;
+    const Split sp = choose_split(cdiv(a.M, BM) * cdiv(a.r, BN), a.N);
+    g.k_split = sp.k_split;
+    g.C = part; g.ldc = a.r;
+    hipError_t e = run_gemm<A_ROW, B_ROW, EPI_F32, false>(g, sp.Z, stream);
+    if (e != hipSuccess) return e;
+    e = reduce(part, sp.Z, a.M, a.r, a.s, sU + k * rp, true, rp, 0.0f, nullptr, stream, pitch);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t adapter_grads(const AdapterShape& a, const uint16_t* X, const uint16_t* dY, int64_t ldy, int64_t y_step,
+                         const uint16_t* sU, const uint16_t* T, void* dL1, void* dL2, bool grad_bf16, float* part,
+                         hipStream_t stream) {
+  const int64_t rp = cdiv(a.r, 64) * 64, pitch = a.n * rp, r = a.r;
+  if (r <= 64) {
+    const SkinnyBatch b1{a.n, 0, rp, a.K * r, 0}, b2{a.n, y_step, a.M * r, r * a.N, 0};
+    const hipError_t e = skinny_tn(X, a.K, a.K, sU, pitch, a.M, a.r, part, 1.0f, false, grad_bf16, dL1, stream, nullptr, &b1);
+    if (e != hipSuccess) return e;
+    return skinny_tn(dY, ldy, a.N, T, r, a.M, a.r, part, a.s, true, grad_bf16, dL2, stream, nullptr, &b2);
+  }
+  const int64_t w = grad_bf16 ? 2 : 4;
+  for (int k = 0; k < a.n; ++k) {
+    GemmArgs g = base_args();
+    g.M = a.K; g.N = r; g.K = a.M;
+    g.A = X; g.lda = a.K;
+    g.B = sU + k * rp; g.ldb = pitch;
+    const Split s1 = choose_split(cdiv(a.K, BM) * cdiv(r, BN), a.M);
+    g.k_split = s1.k_split;
+    g.C = part; g.ldc = r;
+    hipError_t e = run_gemm<A_COL, B_COL, EPI_F32, false>(g, s1.Z, stream);
+    if (e != hipSuccess) return e;
+    e = reduce(part, s1.Z, a.K, r, 1.0f, static_cast<char*>(dL1) + k * a.K * r * w, grad_bf16, r, 0.0f, nullptr, stream);
+    if (e != hipSuccess) return e;
+    g = base_args();
+    g.M = r; g.N = a.N; g.K = a.M;
+    g.A = T + k * a.M * r; g.lda = r;
+    g.B = dY + k * y_step; g.ldb = ldy;
+    const Split s2 = choose_split(cdiv(r, BM) * cdiv(a.N, BN), a.M);
+    g.k_split = s2.k_split;
+    g.C = part; g.ldc = a.N;
+    e = run_gemm<A_COL, B_COL, EPI_F32, false>(g, s2.Z, stream);
+    if (e != hipSuccess) return e;
+    e = reduce(part, s2.Z, r, a.N, a.s, static_cast<char*>(dL2) + k * r * a.N * w, grad_bf16, a.N, 0.0f, nullptr, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace qlora

@@ -52,9 +52,17 @@
 // One token of 8 resident rank-64 adapters, 4096 -> 11008 (25 MB): 5.1 + 12.3 us,
 // the call 16.3 (1.5 TB/s; a single adapter's 15.9), bound by two launches and the
 // prologue's latency.
+// For the gated block (PAIR) a workgroup owns the same features of two weights:
+// its row r < R / 2 is feature r of gate, r + R / 2 of up, with the block
+// constants, adapter columns and partials of both, and the product act(G) U is
+// made where the waves' row sums are joined, so neither G nor U is written. Its
+// arithmetic is that of MULTI.
 // Every result is deterministic (fixed orders, no atomics).
 #include "common.h"
+#include "act.h"
 #include "launch.h"
+
+#include <string.h>
 
 #include <type_traits>
 
@@ -92,7 +100,8 @@ typedef __attribute__((address_space(3))) void g1_lds_t;
 
 // part[p][j] = sum_{k in slice p} X[k] L1[k][j], slices of kT1Rows rows;
 // thread t takes the 8 columns (t % 8) * 8 .. +8 of rows t / 8, t / 8 + 32, ...
-template <bool MULTI>
+// PAIR: adapter blockIdx.y of two.
+template <bool MULTI, bool PAIR>
 __global__ __launch_bounds__(256) void t1_partial_kernel(const uint16_t* __restrict__ X, int K,
                                                         const uint16_t* __restrict__ L1, int r,
                                                         float* __restrict__ part, MultiIds mi) {
@@ -101,6 +110,10 @@ __global__ __launch_bounds__(256) void t1_partial_kernel(const uint16_t* __restr
     const int a = mi.ids[0];
     if (a < 0 || a >= mi.A) return;                 // no adapter: the partials are not used
     L1 += (int64_t)a * K * r;
+  }
+  if constexpr (PAIR) {
+    L1 += (int64_t)blockIdx.y * K * r;
+    part += (int64_t)blockIdx.y * gridDim.x * r;
   }
   const int t = threadIdx.x, cc = t & 7, ph = t >> 3;
   const int k0 = blockIdx.x * kT1Rows;
@@ -147,13 +160,21 @@ __device__ __forceinline__ float sum8(float v) {
   return v;
 }
 
-template <int NG, bool MULTI>
+struct PairArgs {
+  NF4View up;
+  int act;
+};
+
+template <int NG, bool MULTI, bool PAIR>
 __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Table tab,
                                                               const uint16_t* __restrict__ X,
                                                               const float* __restrict__ part, int P, float s,
                                                               const uint16_t* __restrict__ L2, int r,
                                                               uint16_t* __restrict__ Y,
-                                                              uint16_t* __restrict__ T_out, MultiIds mi) {
+                                                              uint16_t* __restrict__ T_out, MultiIds mi,
+                                                              PairArgs pa) {
+  constexpr bool FP16 = MULTI || PAIR;             // the table's values in fp16
+  constexpr int NW = PAIR ? 2 : 1;                 // weights
   constexpr int DC = NG >= kG1Loads ? 1 : kG1Loads / NG;  // chunks in flight per wave
   __shared__ __attribute__((aligned(256))) uint32_t g1_table[kG1TableBytes / 4];   // at LDS address 0
   extern __shared__ __attribute__((aligned(16))) unsigned char g1_smem[];
@@ -162,7 +183,8 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
   const int K = (int)Wt.cols, N = (int)Wt.rows;
   const int G = (int)gridDim.x, b = (int)blockIdx.x;
   const int n_lo = (int)((int64_t)b * N / G), n_hi = (int)((int64_t)(b + 1) * N / G);
-  const int R = n_hi - n_lo;                       // 8 <= R <= 8 NG (the launcher checks)
+  const int R1 = n_hi - n_lo;                      // rows of a weight
+  const int R = NW * R1;                           // R <= 8 NG (the launcher checks)
   const int nblk = K / kBlock, NC = K / kG1Chunk;
   const G1Layout L = g1_layout(K, R, nblk, NG);
   const int sub = lane & 7, lrow = lane >> 3;
@@ -200,36 +222,45 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
   // the 16-aligned run of 16 blocks at gb_a + 16 t (and + 16 x 512), one
   // 16-byte load, with the run's group scale (a group of 256 blocks holds
   // the whole run; N nblk % 16 == 0 keeps the last run inside the array)
-  const int gb_lo = n_lo * nblk, gb_hi = gb_lo + R * nblk;
+  // (PAIR: run tid of each weight's same range)
+  const int gb_lo = n_lo * nblk, gb_hi = gb_lo + R1 * nblk;
   const int gb_a = gb_lo & ~15;
   const int nruns = (gb_hi - gb_a + 15) / 16;
   u32x4_t a16[kRunsPerThread];
   float sg[kRunsPerThread];
 #pragma unroll
   for (int q = 0; q < kRunsPerThread; ++q) {
-    int run = tid + q * kG1Threads;
+    int run = PAIR ? tid : tid + q * kG1Threads;
     if (run > nruns - 1) run = nruns - 1;           // past the range: a valid run (not stored)
     const uint32_t gb = (uint32_t)(gb_a + 16 * run);
-    a16[q] = ld16(Wt.absmax8, gb);
-    sg[q] = Wt.scale2[gb >> 8];
+    a16[q] = ld16(PAIR && q ? pa.up.absmax8 : Wt.absmax8, gb);
+    sg[q] = (PAIR && q ? pa.up.scale2 : Wt.scale2)[gb >> 8];
   }
   const float mu = Wt.mean[0];
+  const float mu2 = PAIR ? pa.up.mean[0] : 0.0f;
   // The LoRA term is split over the waves by adapter column: lane (lrow,
   // sub) of wave w owns column j = 8 w + sub. It loads the slice partials
   // part[p][j] for p = lrow, lrow + 8, ... and L2[j][row] of its row in
   // each row group (clamped addresses; the extras are masked below).
   const int jw = 8 * wave + sub, jc = jw < r ? jw : r - 1;
-  float pt[kG1MaxSlices / 8];
+  float pt[NW][kG1MaxSlices / 8];
   uint32_t l2g[NG];
 #pragma unroll
-  for (int m = 0; m < kG1MaxSlices / 8; ++m) {
-    const int p = lrow + 8 * m;
-    pt[m] = part[(uint32_t)(p < P ? p : P - 1) * (uint32_t)r + (uint32_t)jc];
-  }
+  for (int w = 0; w < NW; ++w)
+#pragma unroll
+    for (int m = 0; m < kG1MaxSlices / 8; ++m) {
+      const int p = lrow + 8 * m;
+      pt[w][m] = part[(uint32_t)((p < P ? p : P - 1) + w * P) * (uint32_t)r + (uint32_t)jc];
+    }
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     const int row = 8 * g + lrow;
-    l2g[g] = L2[(uint32_t)jc * (uint32_t)N + (uint32_t)(n_lo + (row < R ? row : R - 1))];
+    if constexpr (PAIR) {
+      const int rc = row < R ? row : R - 1, up = rc >= R1;
+      l2g[g] = L2[((int64_t)up * r + jc) * N + n_lo + rc - up * R1];
+    } else {
+      l2g[g] = L2[(uint32_t)jc * (uint32_t)N + (uint32_t)(n_lo + (row < R ? row : R - 1))];
+    }
   }
   __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_barrier();                     // every wave's small loads are queued
@@ -240,18 +271,25 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
   //   row * K/2 + 128 c + 16 sub (rows clamped into the workgroup's range,
   //   chunks clamped into the row: those lanes and chunks are not used)
   uint32_t roff[NG];
+  const uint8_t* rcode[PAIR ? NG : 1];              // PAIR: the lane's weight
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     int n = n_lo + 8 * g + lrow;
-    if (n > n_hi - 1) n = n_hi - 1;
-    roff[g] = __umul24((uint32_t)n, (uint32_t)(K >> 1)) + 16u * (uint32_t)sub;
+    if constexpr (PAIR) {
+      const int rc = 8 * g + lrow < R ? 8 * g + lrow : R - 1, up = rc >= R1;
+      rcode[g] = (up ? pa.up.codes : Wt.codes) + __umul24((uint32_t)(n_lo + rc - up * R1), (uint32_t)(K >> 1)) + 16u * (uint32_t)sub;
+      roff[g] = 0;
+    } else {
+      if (n > n_hi - 1) n = n_hi - 1;
+      roff[g] = __umul24((uint32_t)n, (uint32_t)(K >> 1)) + 16u * (uint32_t)sub;
+    }
   }
   auto chunk_of = [&](int ci) { const int c = wave + kG1Waves * ci; return c < NC ? c : (wave < NC ? wave : 0); };
   u32x4_t ring[DC][NG];
   auto load_chunk = [&](int ci, u32x4_t* slot) {
     const uint32_t cb = 128u * (uint32_t)chunk_of(ci);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) slot[g] = ld16(Wt.codes, roff[g] + cb);
+    for (int g = 0; g < NG; ++g) slot[g] = PAIR ? ld16(rcode[PAIR ? g : 0], cb) : ld16(Wt.codes, roff[g] + cb);
   };
 #pragma unroll
   for (int d = 0; d < DC; ++d) load_chunk(d, ring[d]);
@@ -265,11 +303,11 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
   // bytes. Wave w writes stores 8 w .. 8 w + 7; the entry's low nibble is
   // 4 (i % 4) + l / 16, its high nibble i / 4.
   {
-    uint32_t qb[16];                                // bf16(q[j]), round to nearest even (finite q); MULTI: fp16
+    uint32_t qb[16];                                // bf16(q[j]), round to nearest even (finite q); FP16: fp16
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const uint32_t u = __float_as_uint(tab.q[j]);
-      if constexpr (MULTI) qb[j] = table_fp16(tab.q[j]);
+      if constexpr (FP16) qb[j] = table_fp16(tab.q[j]);
       else qb[j] = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
     }
     const int lq = lane >> 4;
@@ -294,7 +332,7 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
   const uint32_t mB = 0xFFFFFFFFu / (uint32_t)nblk + 1u;    // e / nblk by a multiply-high, exact for e < 2^16
 #pragma unroll
   for (int q = 0; q < kRunsPerThread; ++q) {
-    const int run = tid + q * kG1Threads;
+    const int run = PAIR ? tid : tid + q * kG1Threads;
     if (run < nruns) {
       const uint32_t bytes[4] = {a16[q].x, a16[q].y, a16[q].z, a16[q].w};
 #pragma unroll
@@ -302,7 +340,8 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
         const int rel = gb_a + 16 * run + e - gb_lo;   // block, relative to gb_lo
         if (rel >= 0 && rel < gb_hi - gb_lo) {
           const int rr = (int)__umulhi((uint32_t)rel, mB);
-          aw[rel + rr] = block_scale((bytes[e >> 2] >> (8 * (e & 3))) & 0xFFu, sg[q], mu);
+          aw[rel + rr + (PAIR ? q * R1 * (nblk + 1) : 0)] =
+              block_scale((bytes[e >> 2] >> (8 * (e & 3))) & 0xFFu, sg[q], PAIR && q ? mu2 : mu);
         }
       }
     }
@@ -314,19 +353,24 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
   // together add every column once.
   float acc[NG];
   {
-    float t = 0.0f;
+    float st[NW];
 #pragma unroll
-    for (int m = 0; m < kG1MaxSlices / 8; ++m)
-      if (lrow + 8 * m < P) t += pt[m];
-    t += __shfl_xor(t, 8, 64);
-    t += __shfl_xor(t, 16, 64);
-    t += __shfl_xor(t, 32, 64);
-    if (MULTI && !has) t = 0.0f;
-    if (b == 0 && T_out && lrow == 0 && jw < r) T_out[jw] = f32_to_bf16(t);
-    const float st = bf16_to_f32(f32_to_bf16(s * t));
+    for (int w = 0; w < NW; ++w) {
+      float t = 0.0f;
+#pragma unroll
+      for (int m = 0; m < kG1MaxSlices / 8; ++m)
+        if (lrow + 8 * m < P) t += pt[w][m];
+      t += __shfl_xor(t, 8, 64);
+      t += __shfl_xor(t, 16, 64);
+      t += __shfl_xor(t, 32, 64);
+      if (MULTI && !has) t = 0.0f;
+      if (b == 0 && T_out && lrow == 0 && jw < r) T_out[w * r + jw] = f32_to_bf16(t);
+      st[w] = bf16_to_f32(f32_to_bf16(s * t));
+    }
 #pragma unroll
     for (int g = 0; g < NG; ++g)  // a select: 0 times an infinity or NaN of the (clamped) L2 that was read is NaN
-      acc[g] = jw >= r || (MULTI && !has) ? 0.0f : st * bf16_to_f32(l2g[g]);
+      acc[g] = jw >= r || (MULTI && !has) ? 0.0f
+                                          : (PAIR && 8 * g + lrow >= R1 ? st[NW - 1] : st[0]) * bf16_to_f32(l2g[g]);
   }
   // the X copies (issued first) have landed once all but the code loads are done
   asm volatile("s_waitcnt vmcnt(%0)" :: "n"(DC * NG) : "memory");
@@ -360,12 +404,12 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
       int row = 8 * g + lrow;
       if (row > R - 1) row = R - 1;                  // lanes past the rows read a valid constant (unused)
       const float ap = aw[row * (nblk + 1) + blk];
-      float sum = MULTI ? acc[g] : 0.0f;
+      float sum = FP16 ? acc[g] : 0.0f;
 #pragma unroll
       for (int k = 0; k < 16; ++k)
-        sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, MULTI ? scaled_pair(lv[k], ap) : lv[k]),
+        sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, FP16 ? scaled_pair(lv[k], ap) : lv[k]),
                                               __builtin_bit_cast(bf16x2_t, xw[k]), sum, false);
-      acc[g] = MULTI ? sum : __builtin_fmaf(ap, sum, acc[g]);
+      acc[g] = FP16 ? sum : __builtin_fmaf(ap, sum, acc[g]);
     }
   };
   int base = 0;
@@ -389,27 +433,33 @@ __global__ __launch_bounds__(kG1Threads, 1) void gemv1_kernel(NF4View Wt, NF4Tab
     if (sub == 0) red[wave * (8 * NG) + 8 * g + lrow] = v;
   }
   __syncthreads();
-  if (tid < R) {
+  if (tid < R1) {
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kG1Waves; ++w) v += red[w * (8 * NG) + tid];
+    if constexpr (PAIR) {
+      float u = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kG1Waves; ++w) u += red[w * (8 * NG) + R1 + tid];
+      v = (pa.act == kActSilu ? act_of<kActSilu>(v) : act_of<kActGelu>(v)) * u;
+    }
     Y[n_lo + tid] = f32_to_bf16(v);
   }
 }
 
-template <int NG, bool MULTI>
+template <int NG, bool MULTI, bool PAIR>
 hipError_t launch_g1(const NF4View& W, const NF4Table& tab, const uint16_t* X, const float* part, int P, float s,
                      const uint16_t* L2, int r, uint16_t* Y, uint16_t* T_out, int G, uint32_t lds,
-                     const MultiIds& mi, hipStream_t stream) {
+                     const MultiIds& mi, const PairArgs& pa, hipStream_t stream) {
   static bool attr_set = false;  // raise the dynamic-LDS limit once per instantiation (idempotent)
   if (!attr_set) {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&gemv1_kernel<NG, MULTI>),
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&gemv1_kernel<NG, MULTI, PAIR>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024 - (int)kG1TableBytes);
     (void)hipGetLastError();  // a refusal shows up as a launch error below
     attr_set = true;
   }
-  hipLaunchKernelGGL((gemv1_kernel<NG, MULTI>), dim3((unsigned)G), dim3(kG1Threads), lds, stream, W, tab, X, part, P, s,
-                     L2, r, Y, T_out, mi);
+  hipLaunchKernelGGL((gemv1_kernel<NG, MULTI, PAIR>), dim3((unsigned)G), dim3(kG1Threads), lds, stream, W, tab, X, part, P, s,
+                     L2, r, Y, T_out, mi, pa);
   return hipGetLastError();
 }
 
@@ -421,19 +471,31 @@ struct G1Plan {
   bool ok;
 };
 
-G1Plan g1_plan(const NF4View& W, int r) {
+// `pair`: features of two weights, so many rounds of workgroups that the rows fit.
+G1Plan g1_plan(const NF4View& W, int r, bool pair = false) {
   G1Plan p{0, 0, 0, 0u, false};
   const int64_t K = W.cols, N = W.rows;
   if (r > kG1MaxRank || K % kG1Chunk != 0 || K > 16384 || N < 8) return p;   // P = K / 256 <= 64
   if (W.absmax32 != nullptr || r % 8 != 0) return p;   // double-quantised weights only
   if (N * K / 2 >= ((int64_t)1 << 32) || N >= (1 << 24)) return p;   // 32-bit byte offsets, 24-bit products
   int G = device_cu_count();
-  if (G > N / 8) G = (int)(N / 8);
-  const int64_t R = (N + G - 1) / G;
+  const int nblk = (int)(K / kBlock);
+  int64_t R;
+  if (pair) {
+    int64_t most = 16 * kG1Threads / nblk - 1;       // of a weight: one run of block codes per thread
+    if (most > 44) most = 44;
+    if (most < 1) return p;
+    const int64_t rounds = (N + most * G - 1) / (most * G);
+    G = (int)(rounds * G < N / 8 ? rounds * G : N / 8);
+    R = 2 * ((N + G - 1) / G);
+    if (R > 2 * most) return p;
+  } else {
+    if (G > N / 8) G = (int)(N / 8);
+    R = (N + G - 1) / G;
+  }
   const int NG = (int)((R + 7) / 8);
   if (NG > 11) return p;
-  const int nblk = (int)(K / kBlock);
-  if (R * nblk > 16 * kRunsPerThread * kG1Threads - 16) return p;   // runs of block codes per thread
+  if ((pair ? R / 2 : R) * nblk > 16 * (pair ? 1 : kRunsPerThread) * kG1Threads - 16) return p;   // runs of block codes per thread
   if ((N * nblk) % 16 != 0) return p;                              // whole runs of 16 block codes
   const G1Layout L = g1_layout((int)K, (int)R, nblk, NG);
   if (L.total + kG1TableBytes > 160u * 1024u) return p;
@@ -455,19 +517,19 @@ bool gemv1_applies(const NF4View& W, int64_t M, int r) { return M == 1 && g1_pla
 
 namespace {
 
-template <bool MULTI>
+template <bool MULTI, bool PAIR = false>
 hipError_t run_gemv1(const NF4View& W, const NF4Table& tab, const uint16_t* X, const uint16_t* L1, const uint16_t* L2,
-                     int r, float s, uint16_t* Y, uint16_t* T_out, float* part, const MultiIds& mi,
+                     int r, float s, uint16_t* Y, uint16_t* T_out, float* part, const MultiIds& mi, const PairArgs& pa,
                      hipStream_t stream) {
-  const G1Plan pl = g1_plan(W, r);
+  const G1Plan pl = g1_plan(W, r, PAIR);
   if (!pl.ok) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(t1_partial_kernel<MULTI>, dim3((unsigned)pl.P), dim3(256), 0, stream, X, (int)W.cols, L1, r, part,
-                     mi);
+  hipLaunchKernelGGL((t1_partial_kernel<MULTI, PAIR>), dim3((unsigned)pl.P, PAIR ? 2 : 1), dim3(256), 0, stream, X, (int)W.cols,
+                     L1, r, part, mi);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return timed(kTimeGemv, stream, [&]() -> hipError_t {
+  auto launch = [&]() -> hipError_t {
     auto go = [&](auto ng) {
-      return launch_g1<decltype(ng)::value, MULTI>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, mi, stream);
+      return launch_g1<decltype(ng)::value, MULTI, PAIR>(W, tab, X, part, pl.P, s, L2, r, Y, T_out, pl.G, pl.lds, mi, pa, stream);
     };
     switch (pl.NG) {
       case 1: return go(std::integral_constant<int, 1>{});
@@ -482,7 +544,9 @@ hipError_t run_gemv1(const NF4View& W, const NF4Table& tab, const uint16_t* X, c
       case 10: return go(std::integral_constant<int, 10>{});
       default: return go(std::integral_constant<int, 11>{});
     }
-  });
+  };
+  if constexpr (PAIR) return launch();
+  else return timed(kTimeGemv, stream, launch);
 }
 
 }  // namespace
@@ -490,13 +554,23 @@ hipError_t run_gemv1(const NF4View& W, const NF4Table& tab, const uint16_t* X, c
 hipError_t launch_gemv1(const NF4View& W, const NF4Table& tab, const uint16_t* X, const uint16_t* L1,
                         const uint16_t* L2, int r, float s, uint16_t* Y, uint16_t* T_out, float* part,
                         hipStream_t stream) {
-  return run_gemv1<false>(W, tab, X, L1, L2, r, s, Y, T_out, part, MultiIds{}, stream);
+  return run_gemv1<false>(W, tab, X, L1, L2, r, s, Y, T_out, part, MultiIds{}, PairArgs{}, stream);
 }
 
 hipError_t launch_gemv1_multi(const NF4View& W, const NF4Table& tab, const uint16_t* X, const MultiIds& mi,
                               const uint16_t* L1, const uint16_t* L2, int r, uint16_t* Y, uint16_t* T_out, float* part,
                               hipStream_t stream) {
-  return run_gemv1<true>(W, tab, X, L1, L2, r, 0.0f, Y, T_out, part, mi, stream);
+  return run_gemv1<true>(W, tab, X, L1, L2, r, 0.0f, Y, T_out, part, mi, PairArgs{}, stream);
+}
+
+// Both weights double-quantised in one data type (one table).
+bool gemv1_pair_applies(const GatedBase& W, int64_t M, int r) {
+  return M == 1 && W.up.absmax32 == nullptr && memcmp(&W.tab_gate, &W.tab_up, sizeof(NF4Table)) == 0 && g1_plan(W.gate, r, true).ok;
+}
+
+hipError_t launch_gemv1_pair(const GatedBase& W, const uint16_t* X, const uint16_t* L1, const uint16_t* L2, int r, float s,
+                             int act, uint16_t* A, uint16_t* T_out, float* part, hipStream_t stream) {
+  return run_gemv1<false, true>(W.gate, W.tab_gate, X, L1, L2, r, s, A, T_out, part, MultiIds{}, PairArgs{W.up, act}, stream);
 }
 
 }  // namespace qlora

@@ -76,15 +76,42 @@ struct HeadRows {
   const int32_t* label;
 };
 
+// FEW (up to kFewRows rows): each workgroup counts the rows before its own itself, and the last one writes the count:
+// one launch less (48 rows: 10.2 -> ? us).
+constexpr int64_t kFewRows = 2048;
+
+template <bool FEW>
 __global__ __launch_bounds__(256) void head_gather_kernel(const uint16_t* __restrict__ H, const uint16_t* __restrict__ W,
-                                                          const int64_t* __restrict__ labels, int64_t K,
+                                                          const int64_t* __restrict__ labels, int64_t K, int64_t M, int64_t V,
+                                                          int32_t* __restrict__ rows, int32_t* __restrict__ count,
                                                           const int32_t* __restrict__ slot, uint16_t* __restrict__ Hc,
                                                           float* __restrict__ ref, float* __restrict__ logit,
                                                           int32_t* __restrict__ label, float* __restrict__ nll,
                                                           uint16_t* __restrict__ dH) {
   __shared__ float red[4];
   const int64_t m = blockIdx.x;
-  const int at = slot[m];
+  int at;
+  if constexpr (FEW) {
+    __shared__ int s_n[4];
+    int n = 0;                                      // counted rows up to this one
+    for (int64_t i = threadIdx.x; i <= m; i += 256) {
+      const int64_t y = labels[i];
+      n += y >= 0 && y < V;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, 64);
+    if ((threadIdx.x & 63) == 0) s_n[threadIdx.x >> 6] = n;
+    __syncthreads();
+    n = (s_n[0] + s_n[1]) + (s_n[2] + s_n[3]);
+    const int64_t y = labels[m];
+    at = y >= 0 && y < V ? n - 1 : -1;
+    if (threadIdx.x == 0) {
+      if (at >= 0) rows[at] = (int32_t)m;
+      if (m == M - 1) count[0] = n;
+    }
+  } else {
+    at = slot[m];
+  }
   if (at < 0) {
     if (threadIdx.x == 0) nll[m] = 0.0f;
     if (dH)
@@ -278,12 +305,10 @@ struct StatArgs {
   uint16_t* P;             // nullptr: the loss alone
   float* scale;            // of the piece
   float* nll;              // by row
-  uint16_t* Hc;            // dW: the piece's rows, scaled here; else nullptr
-  int64_t K;
 };
 
 __global__ __launch_bounds__(1024) void head_stat_kernel(StatArgs a) {
-  __shared__ float s_d[16][64], s_l[16][64], s_scale[64], s_top[64];
+  __shared__ float s_d[16][64], s_l[16][64], s_top[64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t n = piece_rows(a.r.count, a.row0, a.piece), r0 = (int64_t)blockIdx.x * 64;
   if (r0 >= n) return;                              // uniform
@@ -291,14 +316,26 @@ __global__ __launch_bounds__(1024) void head_stat_kernel(StatArgs a) {
   const int64_t row = in ? r0 + lane : n - 1;
   float d = 0.0f, l = 0.0f;
   bool moved = false;
-  for (int t = wave; t < a.tiles; t += 16) {
-    const float s = a.sum[t * a.piece + row], h = a.shift[t * a.piece + row];
-    moved = moved || h != 0.0f;
-    if (h > d) {
-      l *= __expf(d - h);
-      d = h;
+  constexpr int kBatch = 8;                         // tiles whose loads are in flight
+  for (int t0 = wave; t0 < a.tiles; t0 += 16 * kBatch) {
+    float sv[kBatch], hv[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t t = t0 + 16 * u < a.tiles ? t0 + 16 * u : t0;
+      sv[u] = a.sum[t * a.piece + row];
+      hv[u] = a.shift[t * a.piece + row];
     }
-    l += h == d ? s : s * __expf(h - d);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (t0 + 16 * u >= a.tiles) break;            // uniform
+      const float s = sv[u], h = hv[u];
+      moved = moved || h != 0.0f;
+      if (h > d) {
+        l *= __expf(d - h);
+        d = h;
+      }
+      l += h == d ? s : s * __expf(h - d);
+    }
   }
   s_d[wave][lane] = d;
   s_l[wave][lane] = l;
@@ -319,7 +356,6 @@ __global__ __launch_bounds__(1024) void head_stat_kernel(StatArgs a) {
     const float w = a.weights ? a.weights[m] : 1.0f;
     const float div = a.divisor != 0.0f ? a.divisor : (float)a.r.count[0];
     const float scale = a.grad_scale * w / div / total;
-    s_scale[lane] = scale;
     s_top[lane] = d;
     if (in) {
       a.nll[m] = nll;
@@ -342,20 +378,22 @@ __global__ __launch_bounds__(1024) void head_stat_kernel(StatArgs a) {
     __syncthreads();
   }
   if (wave == 0 && in) a.P[row * a.ldp + a.r.label[at]] = f32_to_bf16(-l);
-  if (a.Hc) {
-    for (int64_t i = tid; i < 64 * (a.K / 8); i += 1024) {
-      const int64_t q = i / (a.K / 8), k = (i - q * (a.K / 8)) * 8;
-      if (r0 + q >= n) break;
-      uint16_t* h = a.Hc + (r0 + q) * a.K + k;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(h);
-      const float s = s_scale[q];
-      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-      uint32_t o[4];
+}
+
+// dW's operand: the piece's rows of H, scaled.
+__global__ __launch_bounds__(256) void head_scale_kernel(uint16_t* __restrict__ Hc, const float* __restrict__ scale,
+                                                         const int32_t* count, int64_t row0, int64_t piece, int64_t K) {
+  const int64_t n = piece_rows(count, row0, piece), per = K / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / per;
+  if (row >= n) return;
+  uint16_t* h = Hc + i * 8;
+  const u32x4_t v = *reinterpret_cast<const u32x4_t*>(h);
+  const float s = scale[row];
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(s * __uint_as_float(x[e] << 16), s * __uint_as_float(x[e] & 0xFFFF0000u));
-      *reinterpret_cast<u32x4_t*>(h) = u32x4_t{o[0], o[1], o[2], o[3]};
-    }
-  }
+  for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(s * __uint_as_float(x[e] << 16), s * __uint_as_float(x[e] & 0xFFFF0000u));
+  *reinterpret_cast<u32x4_t*>(h) = u32x4_t{o[0], o[1], o[2], o[3]};
 }
 
 // ---- gradients --------------------------------------------------------------------------------
@@ -372,19 +410,7 @@ struct DhEpi {
                                              uint16_t* smem) const {
     const int lane = threadIdx.x & 63;
     if (part) {
-      float* out = part + (int64_t)z * piece * K;
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int64_t row = m0 + wm * (32 * MI) + 32 * i + (v & 3) + 4 * (lane >> 5) + 8 * (v >> 2);
-          if (row >= n) continue;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int64_t col = n0 + 64 * wn + 32 * j + (lane & 31);
-            if (col < K) out[row * K + col] = acc[i][j][v];
-          }
-        }
+      tg_store_partial(acc, part + (int64_t)z * piece * K, n, K, m0, n0, wm, wn);
       return;
     }
     constexpr int kPitch = 64 + 8;
@@ -536,18 +562,6 @@ int64_t head_piece(int64_t M, int64_t ldp) {
   return all < most ? all : most;
 }
 
-// Slices of dH's reduction (over the vocabulary) where the tiles leave CUs idle, of at least 8 stages.
-int head_slices(int64_t rows, int64_t K, int64_t ldp) {
-  const int64_t cus = device_cu_count(), nk = ldp / kTgK;
-  const int64_t tiles = hd_cdiv(rows > 0 ? rows : 1, 128) * hd_cdiv(K, kTgN);
-  int64_t S = cus / tiles;
-  if (S > nk / 8) S = nk / 8;
-  if (S > 16) S = 16;
-  if (S < 2) return 1;
-  const int64_t per = hd_cdiv(nk, S);
-  return (int)hd_cdiv(nk, per);
-}
-
 }  // namespace
 
 HeadWorkspace head_workspace_layout(int64_t M, int64_t K, int64_t V, bool dH, bool dW, bool dw_bf16) {
@@ -564,7 +578,7 @@ HeadWorkspace head_workspace_layout(int64_t M, int64_t K, int64_t V, bool dH, bo
   L.stat_off = take(8 * hd_cdiv(V, kTgN) * L.piece);
   L.h_off = take(2 * M * K);
   L.p_off = take(2 * L.piece * ldp);
-  const int S = dH ? head_slices(L.piece < M ? L.piece : M, K, ldp) : 1;
+  const int S = dH ? tg_slices(L.piece < M ? L.piece : M, K, ldp / kTgK, device_cu_count()) : 1;
   L.part_off = take(S > 1 ? 4 * (int64_t)S * L.piece * K : 0);
   L.dw_off = take(dW && dw_bf16 && M > L.piece ? 4 * V * K : 0);
   L.total = off > 0 ? off : 256;
@@ -592,13 +606,18 @@ hipError_t launch_head_loss(const HeadCall& c, hipStream_t stream) {
   const int cus = device_cu_count();
   const bool grad = c.dH || c.dW;
 
-  hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(1024), 0, stream, c.labels, M, V, rows, slot, count);
-  if (M > 0)
-    hipLaunchKernelGGL(head_gather_kernel, dim3((unsigned)M), dim3(256), 0, stream, c.H, c.W, c.labels, K, slot, Hc, ref, logit,
-                       label, c.nll, c.dH);
+  if (M > 0 && M <= kFewRows) {
+    hipLaunchKernelGGL(head_gather_kernel<true>, dim3((unsigned)M), dim3(256), 0, stream, c.H, c.W, c.labels, K, M, V, rows, count,
+                       slot, Hc, ref, logit, label, c.nll, c.dH);
+  } else {
+    hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(1024), 0, stream, c.labels, M, V, rows, slot, count);
+    if (M > 0)
+      hipLaunchKernelGGL(head_gather_kernel<false>, dim3((unsigned)M), dim3(256), 0, stream, c.H, c.W, c.labels, K, M, V, rows,
+                         count, slot, Hc, ref, logit, label, c.nll, c.dH);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int S = c.dH ? head_slices(L.piece < M ? L.piece : M, K, ldp) : 1;
+  const int S = c.dH ? tg_slices(L.piece < M ? L.piece : M, K, ldp / kTgK, device_cu_count()) : 1;
   const HeadRows hr{rows, count, ref, logit, label};
   for (int64_t r0 = 0; r0 < M || r0 == 0; r0 += L.piece) {
     const int64_t most = M - r0 < L.piece ? M - r0 : L.piece;     // rows there may be
@@ -613,8 +632,11 @@ hipError_t launch_head_loss(const HeadCall& c, hipStream_t stream) {
       const ProbEpi pe{ref + r0, label + r0, 0, V, ldp, L.piece, P, sum, shift};
       hipLaunchKernelGGL(head_prob_kernel, dim3((unsigned)tg_grid(most, V, 1)), dim3(kTgThreads), 0, stream, p, pe, count, r0, V, cus);
       const StatArgs sa{sum, shift, (int)tiles, r0, L.piece, ldp, hr, c.weights, c.divisor, c.grad_scale, grad ? P : nullptr,
-                        scale, c.nll, c.dW ? Hc + r0 * K : nullptr, K};
+                        scale, c.nll};
       hipLaunchKernelGGL(head_stat_kernel, dim3((unsigned)hd_cdiv(most, 64)), dim3(1024), 0, stream, sa);
+      if (c.dW)
+        hipLaunchKernelGGL(head_scale_kernel, dim3((unsigned)hd_cdiv(most * K / 8, 256)), dim3(256), 0, stream, Hc + r0 * K, scale,
+                           count, r0, L.piece, K);
     }
     if (c.dH && most > 0) {
       TgArgs p{};

@@ -220,17 +220,25 @@ struct SkinnySplit {
   int Z;        // reduction slices
   int64_t len;  // reduction length per slice (multiple of 64)
 };
+// n equal products in one launch (no dropout): elements between their large
+// operands, small operands, results and second results; the partials take n
+// times skinny_partial_bytes.
+struct SkinnyBatch {
+  int n;
+  int64_t a_step, b_step, o_step, o2_step;
+};
 SkinnySplit skinny_split(int64_t tiles, int64_t klen, int64_t fit = 0);
 size_t skinny_partial_bytes(int64_t M, int64_t K, int64_t N);
 // dr: A is the adapter input X ([M][K], lda == K), dropped in registers.
 hipError_t skinny_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t K, int r,
                      float* part, float alpha, uint16_t* out, int64_t ldo, float alpha2, uint16_t* out2,
-                     hipStream_t stream, const DropoutParams* dr = nullptr, int64_t pitch = 0);
+                     hipStream_t stream, const DropoutParams* dr = nullptr, int64_t pitch = 0,
+                     const SkinnyBatch* batch = nullptr);
 // (pitch: elements between rows of out, ldo where 0)
 // dr: L is the adapter input X ([M][W], ldl == W), dropped in registers.
 hipError_t skinny_tn(const uint16_t* L, int64_t ldl, int64_t W, const uint16_t* S, int64_t lds, int64_t M, int r,
                      float* part, float alpha, bool transpose, bool out_bf16, void* out, hipStream_t stream,
-                     const DropoutParams* dr = nullptr);
+                     const DropoutParams* dr = nullptr, const SkinnyBatch* batch = nullptr);
 
 // Workspace of the linear layer (shared by forward and backward).
 struct LinearWorkspace {
@@ -407,22 +415,33 @@ hipError_t linear_backward(const NF4View& W, const NF4Table& tab, const uint16_t
                            const uint16_t* T, uint16_t* dX, void* dL1, void* dL2, bool grad_bf16,
                            void* ws, hipStream_t stream, const DropoutParams* dr = nullptr);
 
-// The adapter products beside another kernel's product (gemm.hip). width, pitch:
-// columns written (zeros from r on) and elements between rows of sT and sU.
-//   down: sT = bf16(s X L1), T_out (or NULL) = bf16(X L1); l1t: L1^T [rank rounded up to 64][K], zero rows from r on
-//   up:   sU = bf16(s dY L2^T); l2p: L2 [rank rounded up to 64][ldl], zeros from row r and column N on, ldl a multiple
-//         of 64 up to which dY's rows (ldy apart) can be read
-//   grads: dL1 = X^T sU, dL2 = s T^T dY
-size_t adapter_partial_bytes(int64_t M, int64_t K, int64_t N, int r);
-hipError_t adapter_down(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, const uint16_t* l1t, int r, float s,
-                        uint16_t* sT, int64_t width, int64_t pitch, uint16_t* T_out, float* part, hipStream_t stream);
-hipError_t adapter_up(const uint16_t* dY, int64_t ldy, int64_t M, int64_t N, const uint16_t* l2p, int64_t ldl, int r,
-                      float s, uint16_t* sU, int64_t width, int64_t pitch, float* part, hipStream_t stream);
-hipError_t adapter_grads(const uint16_t* X, int64_t K, const uint16_t* dY, int64_t ldy, int64_t N, int64_t M,
-                         const uint16_t* sU, int64_t ldu, const uint16_t* T, int r, float s, void* dL1, void* dL2,
-                         bool grad_bf16, float* part, hipStream_t stream);
-hipError_t launch_small_lora_down(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r, float s,
-                                  uint16_t* sT, int64_t ldst, uint16_t* T_out, float* part, hipStream_t stream);
+// The adapter products of n adapters beside another kernel's product (gemm.hip), as in linear_forward and
+// linear_backward: the skinny kernels, all adapters in one launch, for rank <= 64 where their 32-bit offsets reach,
+// else the 128 x 128 GEMM in reduction slices, adapter by adapter. rp: rank rounded up to 64; adapter k's part of sT
+// and sU is columns [k rp, (k + 1) rp) of [M][n rp] (zeros behind its rank).
+//   down: sT = bf16(s X L1_k), T_out (or NULL) [n][M][r] = bf16(X L1_k); L1 [n][K][r], l1t [n][rp][K]: L1^T, zero rows
+//   up:   sU = bf16(s dY_k L2_k^T); dY_k [M] rows ldy apart, k y_step; l2p [n][rp][ldl]: L2, zeros behind rank and N,
+//         ldl a multiple of 64 up to which dY's rows can be read
+//   grads: dL1 [n][K][r] = X^T sU_k, dL2 [n][r][N] = s T_k^T dY_k; T [n][M][r]
+struct AdapterShape {
+  int n;
+  int64_t M, K, N;
+  int r;
+  float s;
+};
+size_t adapter_partial_bytes(const AdapterShape& a);
+hipError_t adapter_down(const AdapterShape& a, const uint16_t* X, const uint16_t* L1, const uint16_t* l1t, uint16_t* sT,
+                        uint16_t* T_out, float* part, hipStream_t stream);
+hipError_t adapter_up(const AdapterShape& a, const uint16_t* dY, int64_t ldy, int64_t y_step, const uint16_t* l2p,
+                      int64_t ldl, uint16_t* sU, float* part, hipStream_t stream);
+hipError_t adapter_grads(const AdapterShape& a, const uint16_t* X, const uint16_t* dY, int64_t ldy, int64_t y_step,
+                         const uint16_t* sU, const uint16_t* T, void* dL1, void* dL2, bool grad_bf16, float* part,
+                         hipStream_t stream);
+// T partials [slices][M][r] for M <= 128 (gemv.hip), of `adapters` adapters one after another
+size_t small_t_partial_bytes(int64_t M, int64_t K, int r);
+int small_t_slices(int64_t K);
+hipError_t launch_small_t_partial(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r, float* part,
+                                  hipStream_t stream, int adapters = 1);
 
 // The gated feed-forward block (gated.hip): two bases [F][K], adapters stacked
 // gate first: L1 [2][K][r], L2 [2][r][F], T [2][M][r].
@@ -457,6 +476,15 @@ hipError_t gated_backward(const GatedBase& W, const uint16_t* X, const Int8Value
                           const uint16_t* L1, const uint16_t* L2, int r, float s, int act, const uint16_t* T,
                           const Int8Values* gate8, const Int8Values* up8, uint16_t* dX, void* dL1, void* dL2,
                           bool grad_bf16, void* ws, hipStream_t stream);
+
+// Up to 128 rows (multi_small.hip): the base products' partials [slices][M][F] of gate, then of up
+int small_pair_slices(int64_t M, int64_t K, int64_t N);
+int64_t small_pair_partial_floats(int64_t M, int64_t K, int64_t N);   // of any batch of up to M rows
+hipError_t launch_small_pair_base(const GatedBase& W, const uint16_t* X, int64_t M, float* part, hipStream_t stream);
+// A single token (gemv1.hip); part: two times gemv1_partial_bytes.
+bool gemv1_pair_applies(const GatedBase& W, int64_t M, int r);
+hipError_t launch_gemv1_pair(const GatedBase& W, const uint16_t* X, const uint16_t* L1, const uint16_t* L2, int r, float s,
+                             int act, uint16_t* A, uint16_t* T_out, float* part, hipStream_t stream);
 
 // The norm with the residual's addition (norm.hip).
 struct NormFwd {

@@ -193,10 +193,23 @@ struct BaseLds {
 // check in the loop of one variant for all took 0.4 to 1.5 us of every call (60
 // rows 4096 -> 11008 35.2 -> 36.7); so it costs K = 4160 0.4 to 0.8 us (60 rows
 // -> 11008 37.7 -> 38.2) and nothing where K is a multiple of 128.
-template <int MT, bool RAGGED>
+// PAIR: weight blockIdx.z of two (of one shape), whose partials follow the first one's.
+struct SecondBase {
+  NF4View W;
+  NF4Table tab;
+};
+
+template <int MT, bool RAGGED, bool PAIR>
 __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4Table tab,
                                                                   const uint16_t* __restrict__ X, int M, int slice,
-                                                                  float* __restrict__ part) {
+                                                                  float* __restrict__ part, SecondBase other) {
+  if constexpr (PAIR) {
+    if (blockIdx.z) {
+      W = other.W;
+      tab = other.tab;
+      part += (int64_t)gridDim.y * M * W.rows;
+    }
+  }
   using L = BaseLds<MT>;
   __shared__ float s_q[16];                            // a fixed address: table reads need no base
   extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -458,8 +471,8 @@ struct BaseSplit {
   int slice, S;
 };
 
-BaseSplit base_split(int64_t M, int64_t K, int64_t N) {
-  const int64_t tiles = (N + kBaseRows - 1) / kBaseRows, steps = (K + kBaseK - 1) / kBaseK;
+BaseSplit base_split(int64_t M, int64_t K, int64_t N, int weights = 1) {
+  const int64_t tiles = weights * ((N + kBaseRows - 1) / kBaseRows), steps = (K + kBaseK - 1) / kBaseK;
   const int64_t resident = (M <= kBaseTwoPerCu ? 2 : 1) * (int64_t)device_cu_count();
   int64_t S = resident / tiles;
   if (S > steps / 2) S = steps / 2;
@@ -469,19 +482,19 @@ BaseSplit base_split(int64_t M, int64_t K, int64_t N) {
   return BaseSplit{(int)(per * kBaseK), (int)((steps + per - 1) / per)};
 }
 
-template <int MT, bool RAGGED>
+template <int MT, bool RAGGED, bool PAIR>
 hipError_t run_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, int M, const BaseSplit& sp, float* part,
-                    hipStream_t stream) {
+                    const SecondBase& other, hipStream_t stream) {
   static bool attr_set = false;  // raise the dynamic-LDS limit once per instantiation (idempotent)
   if (!attr_set) {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&small_base_kernel<MT, RAGGED>),
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&small_base_kernel<MT, RAGGED, PAIR>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, BaseLds<MT>::kTotal);
     (void)hipGetLastError();  // a refusal shows up as a launch error below
     attr_set = true;
   }
-  const dim3 grid((unsigned)((W.rows + kBaseRows - 1) / kBaseRows), (unsigned)sp.S);
-  hipLaunchKernelGGL((small_base_kernel<MT, RAGGED>), grid, dim3(kBaseThreads), BaseLds<MT>::kTotal, stream, W, tab, X, M,
-                     sp.slice, part);
+  const dim3 grid((unsigned)((W.rows + kBaseRows - 1) / kBaseRows), (unsigned)sp.S, PAIR ? 2 : 1);
+  hipLaunchKernelGGL((small_base_kernel<MT, RAGGED, PAIR>), grid, dim3(kBaseThreads), BaseLds<MT>::kTotal, stream, W, tab, X, M,
+                     sp.slice, part, other);
   return hipGetLastError();
 }
 
@@ -620,17 +633,39 @@ int64_t multi_small_partial_floats(int64_t M, int64_t K, int64_t N) {
   return (a > b ? a : b) * N;
 }
 
-hipError_t launch_multi_small_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, float* part,
-                                   hipStream_t stream) {
-  const BaseSplit sp = base_split(M, W.cols, W.rows);
+namespace {
+
+template <bool PAIR>
+hipError_t launch_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, const BaseSplit& sp, float* part,
+                       const SecondBase& other, hipStream_t stream) {
   auto run = [&](auto ragged) -> hipError_t {
     constexpr bool kRagged = decltype(ragged)::value;
-    if (M <= 32) return run_base<1, kRagged>(W, tab, X, (int)M, sp, part, stream);
-    if (M <= 64) return run_base<2, kRagged>(W, tab, X, (int)M, sp, part, stream);
-    if (M <= 96) return run_base<3, kRagged>(W, tab, X, (int)M, sp, part, stream);
-    return run_base<4, kRagged>(W, tab, X, (int)M, sp, part, stream);
+    if (M <= 32) return run_base<1, kRagged, PAIR>(W, tab, X, (int)M, sp, part, other, stream);
+    if (M <= 64) return run_base<2, kRagged, PAIR>(W, tab, X, (int)M, sp, part, other, stream);
+    if (M <= 96) return run_base<3, kRagged, PAIR>(W, tab, X, (int)M, sp, part, other, stream);
+    return run_base<4, kRagged, PAIR>(W, tab, X, (int)M, sp, part, other, stream);
   };
   return W.cols % kBaseK ? run(std::true_type{}) : run(std::false_type{});
+}
+
+}  // namespace
+
+hipError_t launch_multi_small_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, int64_t M, float* part,
+                                   hipStream_t stream) {
+  return launch_base<false>(W, tab, X, M, base_split(M, W.cols, W.rows), part, SecondBase{}, stream);
+}
+
+int small_pair_slices(int64_t M, int64_t K, int64_t N) { return base_split(M, K, N, 2).S; }
+
+int64_t small_pair_partial_floats(int64_t M, int64_t K, int64_t N) {
+  const int64_t few = M < kBaseTwoPerCu ? M : kBaseTwoPerCu;   // the slices depend on M only through this bound
+  const int64_t a = base_split(few, K, N, 2).S * few, b = base_split(M, K, N, 2).S * M;
+  return 2 * (a > b ? a : b) * N;
+}
+
+hipError_t launch_small_pair_base(const GatedBase& W, const uint16_t* X, int64_t M, float* part, hipStream_t stream) {
+  return launch_base<true>(W.gate, W.tab_gate, X, M, base_split(M, W.gate.cols, W.gate.rows, 2), part,
+                           SecondBase{W.up, W.tab_up}, stream);
 }
 
 hipError_t launch_multi_small_t(const uint16_t* X, int64_t M, int64_t K, const MultiIds& mi, const uint16_t* L1, int r,

@@ -133,8 +133,27 @@ __global__ __launch_bounds__(NormShape<WAVES>::kThreads) void norm_fwd_kernel(No
   }
 }
 
-// Rows first, first + rows in flight, ...: each group of WAVES waves sums dw over its rows into part[group].
-template <int WAVES, int NV, bool DW>
+// 8 values as they lie in memory.
+template <bool BF16>
+struct Raw8 {
+  u32x4_t a[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    const char* c = static_cast<const char*>(p) + at * (BF16 ? 2 : 4);
+    a[0] = *reinterpret_cast<const u32x4_t*>(c);
+    if constexpr (!BF16) a[1] = *reinterpret_cast<const u32x4_t*>(c + 16);
+  }
+  __device__ __forceinline__ float get(int e) const {
+    const u32x4_t& q = a[BF16 ? 0 : e >> 2];
+    const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+    if constexpr (BF16) return (e & 1) ? __uint_as_float(x[e >> 1] & 0xFFFF0000u) : __uint_as_float(x[e >> 1] << 16);
+    else return __uint_as_float(x[e & 3]);
+  }
+};
+
+// Rows group, group + groups, ...: each group of WAVES waves sums dw over its rows into part[group]. A row's values
+// stay in their memory format between the sum and the output (as floats, 6656 bf16 columns took 229 registers, 2
+// waves per SIMD).
+template <int WAVES, int NV, bool H16, bool W16, bool DW>
 __global__ __launch_bounds__(NormShape<WAVES>::kThreads) void norm_bwd_kernel(NormBwd c) {
   using S = NormShape<WAVES>;
   __shared__ float red[16];
@@ -142,35 +161,37 @@ __global__ __launch_bounds__(NormShape<WAVES>::kThreads) void norm_bwd_kernel(No
   const int64_t group = (int64_t)blockIdx.x * S::kRows + threadIdx.x / (64 * WAVES);
   const int64_t groups = (int64_t)gridDim.x * S::kRows;
   float dw[DW ? NV : 1][8];
-  float w[NV][8];
+  if constexpr (DW) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t k = (int64_t)(i * 64 * WAVES + t) * 8;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[i][e] = 1.0f;
-      if constexpr (DW) dw[i][e] = 0.0f;
-    }
-    if (c.w && k < c.K) nm_load(c.w, c.w_bf16, k, w[i]);
+      for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
   }
   for (int64_t row = group; row < c.M; row += groups) {   // uniform for the waves of a row
     const int64_t base = row * c.K;
+    Raw8<H16> h[NV], dr[NV];
+    Raw8<true> dy[NV];
+    Raw8<W16> w[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t k = (int64_t)(i * 64 * WAVES + t) * 8;
+      if (k >= c.K) continue;
+      h[i].load(c.h, base + k);
+      dy[i].load(c.dy, base + k);
+      if (c.w) w[i].load(c.w, k);
+      if (c.dres) dr[i].load(c.dres, base + k);
+    }
     const float rstd = c.rstd[row];
-    float xh[NV][8], dy[NV][8], dr[NV][8];
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t k = (int64_t)(i * 64 * WAVES + t) * 8;
       if (k >= c.K) continue;
-      nm_load(c.h, c.h_bf16, base + k, xh[i]);
-      nm_load(c.dy, true, base + k, dy[i]);
-      if (c.dres) nm_load(c.dres, c.h_bf16, base + k, dr[i]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        xh[i][e] *= rstd;
-        if constexpr (DW) dw[i][e] = __builtin_fmaf(dy[i][e], xh[i][e], dw[i][e]);
-        dy[i][e] *= w[i][e];
-        sum = __builtin_fmaf(dy[i][e], xh[i][e], sum);
+        const float xh = h[i].get(e) * rstd, y = dy[i].get(e);
+        if constexpr (DW) dw[i][e] = __builtin_fmaf(y, xh, dw[i][e]);
+        sum = __builtin_fmaf(c.w ? y * w[i].get(e) : y, xh, sum);
       }
     }
     const float mean = row_sum<WAVES>(sum, red) / (float)c.K;
@@ -181,10 +202,11 @@ __global__ __launch_bounds__(NormShape<WAVES>::kThreads) void norm_bwd_kernel(No
       float d[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        d[e] = rstd * (dy[i][e] - xh[i][e] * mean);
-        if (c.dres) d[e] += dr[i][e];
+        const float y = dy[i].get(e);
+        d[e] = rstd * ((c.w ? y * w[i].get(e) : y) - h[i].get(e) * rstd * mean);
+        if (c.dres) d[e] += dr[i].get(e);
       }
-      nm_store(c.dh, c.h_bf16, base + k, d);
+      nm_store(c.dh, H16, base + k, d);
       if (c.dx16) nm_store(c.dx16, true, base + k, d);
     }
   }
@@ -197,7 +219,8 @@ __global__ __launch_bounds__(NormShape<WAVES>::kThreads) void norm_bwd_kernel(No
   }
 }
 
-// dw[k] = the groups' sums, 16 parts of the groups in order, then the parts in order. 64 columns per workgroup.
+// dw[k] = the groups' sums, 16 parts of the groups in order (8 loads in flight), then the parts in order. 64 columns
+// per workgroup.
 __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__ part, int groups, int64_t K, float* __restrict__ dw) {
   __shared__ float red[16][64];
   const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
@@ -205,7 +228,13 @@ __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__
   const int per = (groups + 15) / 16, lo = q * per, hi = lo + per < groups ? lo + per : groups;
   float v = 0.0f;
   if (k < K)
-    for (int g = lo; g < hi; ++g) v += part[(int64_t)g * K + k];
+    for (int g = lo; g < hi; g += 8) {
+      float b[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) b[u] = part[(int64_t)(g + u < hi ? g + u : g) * K + k];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v += g + u < hi ? b[u] : 0.0f;
+    }
   red[q][c] = v;
   __syncthreads();
   if (q == 0 && k < K) {
@@ -246,24 +275,33 @@ hipError_t launch_norm_fwd(const NormFwd& c, hipStream_t stream) {
   });
 }
 
-// Groups of waves that sum dw: four workgroups per CU.
+// Groups of waves that sum dw: of at least 4 rows where that leaves one per CU (their sums of K floats are written and
+// read once more), at most four per CU.
 int norm_slices(int64_t M) {
-  const int64_t most = 4 * (int64_t)device_cu_count();
-  return (int)((M < most ? M : most) + 3) / 4 * 4;
+  const int64_t cus = device_cu_count();
+  int64_t n = M / 4;
+  if (n < cus) n = M < cus ? M : cus;
+  if (n > 4 * cus) n = 4 * cus;
+  return (int)(n + 3) / 4 * 4;
 }
 
 hipError_t launch_norm_bwd(const NormBwd& c, hipStream_t stream) {
   const int groups = norm_slices(c.M);
   hipError_t e = hipSuccess;
-  if (c.M > 0) e = by_shape(c.K, [&](auto waves, auto nv) {
-    using S = NormShape<decltype(waves)::value>;
-    const dim3 grid((unsigned)((groups + S::kRows - 1) / S::kRows));
-    if (c.dw)
-      hipLaunchKernelGGL((norm_bwd_kernel<decltype(waves)::value, decltype(nv)::value, true>), grid, dim3(S::kThreads), 0, stream, c);
-    else
-      hipLaunchKernelGGL((norm_bwd_kernel<decltype(waves)::value, decltype(nv)::value, false>), grid, dim3(S::kThreads), 0, stream, c);
-    return hipGetLastError();
-  });
+  if (c.M > 0)
+    e = by_shape(c.K, [&](auto waves, auto nv) {
+      using S = NormShape<decltype(waves)::value>;
+      const dim3 grid((unsigned)((groups + S::kRows - 1) / S::kRows));
+      auto go = [&](auto h16, auto w16, auto dw) {
+        hipLaunchKernelGGL((norm_bwd_kernel<decltype(waves)::value, decltype(nv)::value, decltype(h16)::value,
+                                            decltype(w16)::value, decltype(dw)::value>),
+                           grid, dim3(S::kThreads), 0, stream, c);
+      };
+      auto by_w = [&](auto h16, auto dw) { c.w_bf16 ? go(h16, std::true_type{}, dw) : go(h16, std::false_type{}, dw); };
+      auto by_h = [&](auto dw) { c.h_bf16 ? by_w(std::true_type{}, dw) : by_w(std::false_type{}, dw); };
+      c.dw ? by_h(std::true_type{}) : by_h(std::false_type{});
+      return hipGetLastError();
+    });
   if (e != hipSuccess || !c.dw) return e;
   hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((c.K + 63) / 64)), dim3(1024), 0, stream, c.part, groups, c.K, c.dw);
   return hipGetLastError();

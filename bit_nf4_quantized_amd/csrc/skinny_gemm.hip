@@ -66,10 +66,14 @@ struct NtArgs {
   uint32_t thr;       // DROP: keep iff the element's Philox word >= thr; kept values scaled by c
   float c;
   uint64_t seed;
+  int64_t a_step, b_step;  // product blockIdx.y of a batch: elements between the operands; its C follows the others'
 };
 
 template <bool DROP>
 __global__ __launch_bounds__(kSkThreads) void skinny_nt_kernel(NtArgs p) {
+  p.A += blockIdx.y * p.a_step;
+  p.B += blockIdx.y * p.b_step;
+  p.C += (int64_t)blockIdx.y * gridDim.z * p.M * SJ;
   __shared__ __attribute__((aligned(1024))) uint16_t sA[kNtStages][SM * SK];
   __shared__ __attribute__((aligned(1024))) uint16_t sB[kNtStages][SJ * SK];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -174,6 +178,7 @@ struct TnArgs {
   uint32_t thr;       // DROP: keep iff the element's Philox word >= thr; kept values scaled by c
   float c;
   uint64_t seed;
+  int64_t l_step, s_step;  // product blockIdx.y of a batch, as in NtArgs (without DROP)
 };
 
 template <bool DROP>
@@ -312,6 +317,9 @@ __device__ __forceinline__ tn_v4i16 tn_read_tr(const char* lds_byte) {
 
 __global__ __launch_bounds__(kSkThreads) void skinny_tn_dma_kernel(TnArgs p) {
   __shared__ __attribute__((aligned(1024))) char ring[kTnStages * kTnStageBytes];
+  p.L += blockIdx.y * p.l_step;
+  p.S += blockIdx.y * p.s_step;
+  p.C += (int64_t)blockIdx.y * gridDim.z * p.W * SJ;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t c0 = (int64_t)blockIdx.x * SM;
   const int64_t mz0 = (int64_t)blockIdx.z * p.m_split;
@@ -417,6 +425,22 @@ __global__ __launch_bounds__(kSkThreads) void skinny_tn_dma_kernel(TnArgs p) {
   }
 }
 
+// sum_z P[z slab .. +4], in order, 8 slices' loads in flight (one at a time, the
+// sum of 32 slices of 391 rows took 10 us).
+__device__ __forceinline__ f32x4_t sum_slices(const float* __restrict__ P, int Z, int64_t slab) {
+  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  int z = 0;
+  for (; z + 8 <= Z; z += 8) {
+    f32x4_t v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const f32x4_t*>(P + (int64_t)(z + u) * slab);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) acc += v[u];
+  }
+  for (; z < Z; ++z) acc += *reinterpret_cast<const f32x4_t*>(P + (int64_t)z * slab);
+  return acc;
+}
+
 // out = alpha * sum_z P[z] over a [rows][SJ] slab, columns j < r:
 //   mode 0: out[m][j] (columns [r, ldo) zero) in bf16, plus
 //           optional out2[m][j] = bf16(alpha2 * sum) with row stride r
@@ -428,7 +452,10 @@ __global__ __launch_bounds__(kSkThreads) void skinny_tn_dma_kernel(TnArgs p) {
 __global__ __launch_bounds__(256) void skinny_reduce_kernel(const float* __restrict__ P, int Z, int64_t rows, int r,
                                                             float alpha, int mode, int out_bf16, void* __restrict__ out,
                                                             int64_t ldo, float alpha2, uint16_t* __restrict__ out2,
-                                                            int64_t pitch) {
+                                                            int64_t pitch, int64_t o_step, int64_t o2_step) {
+  P += (int64_t)blockIdx.y * Z * rows * SJ;
+  out = out_bf16 ? (void*)(static_cast<uint16_t*>(out) + blockIdx.y * o_step) : (void*)(static_cast<float*>(out) + blockIdx.y * o_step);
+  if (out2) out2 += blockIdx.y * o2_step;
   const int64_t width = (mode == 0) ? ldo : r;
   const int64_t w4 = width / 4;
   const int64_t total = rows * w4;
@@ -441,8 +468,7 @@ __global__ __launch_bounds__(256) void skinny_reduce_kernel(const float* __restr
       *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(out) + o) = u32x2_t{0u, 0u};
       continue;
     }
-    f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int z = 0; z < Z; ++z) acc += *reinterpret_cast<const f32x4_t*>(P + (int64_t)z * slab + m * SJ + j);
+    const f32x4_t acc = sum_slices(P + m * SJ + j, Z, slab);
     const f32x4_t v = {alpha * acc.x, alpha * acc.y, alpha * acc.z, alpha * acc.w};
     if (out_bf16)
       *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(out) + o) = u32x2_t{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
@@ -461,8 +487,11 @@ __global__ __launch_bounds__(256) void skinny_reduce_kernel(const float* __restr
 // 64 x 16 result is transposed through LDS, and each output row segment is
 // written 4 columns per thread.
 __global__ __launch_bounds__(256) void skinny_reduce_t_kernel(const float* __restrict__ P, int Z, int64_t W, int r,
-                                                              float alpha, int out_bf16, void* __restrict__ out) {
+                                                              float alpha, int out_bf16, void* __restrict__ out,
+                                                              int64_t o_step) {
   __shared__ float tile[64][16 + 1];
+  P += (int64_t)blockIdx.z * Z * W * SJ;
+  out = out_bf16 ? (void*)(static_cast<uint16_t*>(out) + blockIdx.z * o_step) : (void*)(static_cast<float*>(out) + blockIdx.z * o_step);
   const int t = threadIdx.x;
   const int64_t c0 = (int64_t)blockIdx.x * 64;
   const int j0 = blockIdx.y * 16;
@@ -470,10 +499,7 @@ __global__ __launch_bounds__(256) void skinny_reduce_t_kernel(const float* __res
   const int cl = t >> 2, jq = (t & 3) * 4;     // column c0 + cl, ranks j0 + jq .. +4
   const int64_t c = c0 + cl;
   f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (c < W) {
-    const int64_t slab = W * SJ;
-    for (int z = 0; z < Z; ++z) acc += *reinterpret_cast<const f32x4_t*>(P + (int64_t)z * slab + c * SJ + j0 + jq);
-  }
+  if (c < W) acc = sum_slices(P + c * SJ + j0 + jq, Z, W * SJ);
 #pragma unroll
   for (int e = 0; e < 4; ++e) tile[cl][jq + e] = acc[e];
   __syncthreads();
@@ -537,36 +563,40 @@ size_t skinny_partial_bytes(int64_t M, int64_t K, int64_t N) {
 // C = A B^T over K with B [64][ldb] (rows >= r zero), then reduce.
 hipError_t skinny_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t K, int r,
                      float* part, float alpha, uint16_t* out, int64_t ldo, float alpha2, uint16_t* out2,
-                     hipStream_t stream, const DropoutParams* dr, int64_t pitch) {
-  if (dr && lda != K) return hipErrorInvalidValue;  // the mask indexes a contiguous [M][K] input
+                     hipStream_t stream, const DropoutParams* dr, int64_t pitch, const SkinnyBatch* batch) {
+  if (dr && (lda != K || batch)) return hipErrorInvalidValue;  // the mask indexes a contiguous [M][K] input
   // 72 KB of LDS: two workgroups per CU
   const SkinnySplit sp = skinny_split(sk_cdiv(M, SM), K, 2 * (int64_t)device_cu_count());
   NtArgs a;
   a.A = A; a.B = B; a.C = part; a.lda = lda; a.ldb = ldb; a.M = M; a.K = K; a.k_split = sp.len;
   a.thr = dr ? dr->thr : 0u; a.c = dr ? dr->c : 1.0f; a.seed = dr ? dr->seed : 0u;
-  const dim3 grid((unsigned)sk_cdiv(M, SM), 1, (unsigned)sp.Z);
+  const SkinnyBatch bt = batch ? *batch : SkinnyBatch{1, 0, 0, 0, 0};
+  a.a_step = bt.a_step; a.b_step = bt.b_step;
+  const dim3 grid((unsigned)sk_cdiv(M, SM), (unsigned)bt.n, (unsigned)sp.Z);
   if (dr)
     hipLaunchKernelGGL(skinny_nt_kernel<true>, grid, dim3(kSkThreads), 0, stream, a);
   else
     hipLaunchKernelGGL(skinny_nt_kernel<false>, grid, dim3(kSkThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(skinny_reduce_kernel, dim3((unsigned)sk_grid(M * ldo / 4)), dim3(256), 0, stream, part, sp.Z, M, r,
-                     alpha, 0, 1, (void*)out, ldo, alpha2, out2, pitch ? pitch : ldo);
+  hipLaunchKernelGGL(skinny_reduce_kernel, dim3((unsigned)sk_grid(M * ldo / 4), (unsigned)bt.n), dim3(256), 0, stream, part,
+                     sp.Z, M, r, alpha, 0, 1, (void*)out, ldo, alpha2, out2, pitch ? pitch : ldo, bt.o_step, bt.o2_step);
   return hipGetLastError();
 }
 
 // C[c][j] = sum_m L[m][c] S[m][j], then reduce to out (transposed if `transpose`).
 hipError_t skinny_tn(const uint16_t* L, int64_t ldl, int64_t W, const uint16_t* S, int64_t lds, int64_t M, int r,
                      float* part, float alpha, bool transpose, bool out_bf16, void* out, hipStream_t stream,
-                     const DropoutParams* dr) {
-  if (dr && (ldl != W || W % 64)) return hipErrorInvalidValue;  // the mask indexes a contiguous [M][W] input
+                     const DropoutParams* dr, const SkinnyBatch* batch) {
+  if (dr && (ldl != W || W % 64 || batch)) return hipErrorInvalidValue;  // the mask indexes a contiguous [M][W] input
   // the copy-ring kernel (72 KB of LDS) fits two workgroups per CU
   const SkinnySplit sp = skinny_split(sk_cdiv(W, SM), M, dr ? 0 : 2 * (int64_t)device_cu_count());
   TnArgs a;
   a.L = L; a.S = S; a.C = part; a.ldl = ldl; a.lds = lds; a.M = M; a.W = W; a.r = r; a.m_split = sp.len;
   a.thr = dr ? dr->thr : 0u; a.c = dr ? dr->c : 1.0f; a.seed = dr ? dr->seed : 0u;
-  const dim3 grid((unsigned)sk_cdiv(W, SM), 1, (unsigned)sp.Z);
+  const SkinnyBatch bt = batch ? *batch : SkinnyBatch{1, 0, 0, 0, 0};
+  a.l_step = bt.a_step; a.s_step = bt.b_step;
+  const dim3 grid((unsigned)sk_cdiv(W, SM), (unsigned)bt.n, (unsigned)sp.Z);
   if (dr)
     hipLaunchKernelGGL(skinny_tn_kernel<true>, grid, dim3(kSkThreads), 0, stream, a);
   else
@@ -574,11 +604,12 @@ hipError_t skinny_tn(const uint16_t* L, int64_t ldl, int64_t W, const uint16_t* 
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (transpose)
-    hipLaunchKernelGGL(skinny_reduce_t_kernel, dim3((unsigned)sk_cdiv(W, 64), SJ / 16), dim3(256), 0, stream, part, sp.Z, W, r,
-                       alpha, out_bf16 ? 1 : 0, out);
+    hipLaunchKernelGGL(skinny_reduce_t_kernel, dim3((unsigned)sk_cdiv(W, 64), SJ / 16, (unsigned)bt.n), dim3(256), 0, stream, part,
+                       sp.Z, W, r, alpha, out_bf16 ? 1 : 0, out, bt.o_step);
   else
-    hipLaunchKernelGGL(skinny_reduce_kernel, dim3((unsigned)sk_grid(W * (int64_t)r / 4)), dim3(256), 0, stream, part, sp.Z,
-                       W, r, alpha, 1, out_bf16 ? 1 : 0, out, (int64_t)r, 0.0f, (uint16_t*)nullptr, (int64_t)r);
+    hipLaunchKernelGGL(skinny_reduce_kernel, dim3((unsigned)sk_grid(W * (int64_t)r / 4), (unsigned)bt.n), dim3(256), 0, stream,
+                       part, sp.Z, W, r, alpha, 1, out_bf16 ? 1 : 0, out, (int64_t)r, 0.0f, (uint16_t*)nullptr, (int64_t)r,
+                       bt.o_step, (int64_t)0);
   return hipGetLastError();
 }
 

@@ -324,6 +324,37 @@ __host__ __device__ inline TgPlan tg_plan(int64_t M, int64_t N, int slices, int 
   return TgPlan{half ? t2 : t1, tn, half ? 1 : 0};
 }
 
+// Slices of the reduction (nk stages) where the tiles leave half of the CUs or more idle: as many as fill them once,
+// of at least 8 stages, at most 16.
+inline int tg_slices(int64_t M, int64_t N, int64_t nk, int64_t cus) {
+  const int64_t tiles = ((M > 0 ? M : 1) + 127) / 128 * ((N + kTgN - 1) / kTgN);
+  int64_t S = cus / tiles;
+  if (S > nk / 8) S = nk / 8;
+  if (S > 16) S = 16;
+  if (S < 2) return 1;
+  const int64_t per = (nk + S - 1) / S;
+  return (int)((nk + per - 1) / per);
+}
+
+// fp32 partials of a tile, straight from the accumulators (128-byte rows per half wave).
+template <int MI>
+__device__ __forceinline__ void tg_store_partial(f32x16_t (&acc)[MI][2], float* out, int64_t M, int64_t N, int64_t m0,
+                                                 int64_t n0, int wm, int wn) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int64_t row = m0 + wm * (32 * MI) + 32 * i + (v & 3) + 4 * (lane >> 5) + 8 * (v >> 2);
+      if (row >= M) continue;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t col = n0 + 64 * wn + 32 * j + (lane & 31);
+        if (col < N) out[row * N + col] = acc[i][j][v];
+      }
+    }
+}
+
 // Workgroups that cover either choice for any M' <= M.
 inline int64_t tg_grid(int64_t M, int64_t N, int slices) {
   return ((M + 127) / 128) * ((N + kTgN - 1) / kTgN) * slices;

@@ -309,31 +309,43 @@ __device__ __forceinline__ void tg_tile(const TgArgs& p, const E& epi, int64_t m
   epi.template operator()<MI>(acc, m0, n0, wm, wn, z, smem);
 }
 
-// How a launch's tiles cover M x N on `cus` compute units, one workgroup each at
-// a time: tiles of 256 or 128 rows, whichever ends sooner (a half-height tile
-// takes a little more than half the time; 0.56 measured on both products of the
-// loss at 4096 hidden columns). Also used on the device, where M is known there only.
+// How a launch's tiles cover M x N on `cus` compute units, one workgroup each at a time: tiles of 256 or 128 rows,
+// whichever ends sooner. A stage of a half-height tile took 1.0 us beside 1.65 of a full one (P W of 6144 rows, H W^T
+// of 6144 rows); both choices where they matter: P W of 777 rows 264 us in half tiles, ? in full ones. Also used on the
+// device, where M may be known there only.
+constexpr int kTgFullCost = 165, kTgHalfCost = 105;
+
 struct TgPlan {
   int tiles_m, tiles_n, half;     // half: tiles of 128 rows
 };
 
+__host__ __device__ inline int64_t tg_rounds(int64_t M, int64_t N, int rows, int slices, int cus) {
+  return ((M + rows - 1) / rows * ((N + kTgN - 1) / kTgN) * slices + cus - 1) / cus;
+}
+
 __host__ __device__ inline TgPlan tg_plan(int64_t M, int64_t N, int slices, int cus) {
   const int tn = (int)((N + kTgN - 1) / kTgN), t1 = (int)((M + 255) / 256), t2 = (int)((M + 127) / 128);
-  const int64_t r1 = ((int64_t)t1 * tn * slices + cus - 1) / cus, r2 = ((int64_t)t2 * tn * slices + cus - 1) / cus;
-  const bool half = 100 * r1 > 56 * r2;
+  const bool half = kTgFullCost * tg_rounds(M, N, 256, slices, cus) > kTgHalfCost * tg_rounds(M, N, 128, slices, cus);
   return TgPlan{half ? t2 : t1, tn, half ? 1 : 0};
 }
 
-// Slices of the reduction (nk stages) where the tiles leave half of the CUs or more idle: as many as fill them once,
-// of at least 8 stages, at most 16.
-inline int tg_slices(int64_t M, int64_t N, int64_t nk, int64_t cus) {
-  const int64_t tiles = ((M > 0 ? M : 1) + 127) / 128 * ((N + kTgN - 1) / kTgN);
-  int64_t S = cus / tiles;
-  if (S > nk / 8) S = nk / 8;
-  if (S > 16) S = 16;
-  if (S < 2) return 1;
-  const int64_t per = (nk + S - 1) / S;
-  return (int)((nk + per - 1) / per);
+// Slices of the reduction (nk stages): what ends soonest by the stages' times above, the partials written and read
+// once (S M N 8 bytes at 4.5 TB/s) and one launch more; of at least 8 stages, at most 16.
+inline int tg_slices(int64_t M, int64_t N, int64_t nk, int cus) {
+  if (M < 1) return 1;
+  int best = 1;
+  double least = 0.0;
+  for (int S = 1; S <= 16 && (S == 1 || nk / S >= 8); ++S) {
+    const int64_t per = (nk + S - 1) / S;
+    if ((nk + per - 1) / per != S) continue;         // a slice would be empty
+    const double full = 0.01 * kTgFullCost * tg_rounds(M, N, 256, S, cus), half = 0.01 * kTgHalfCost * tg_rounds(M, N, 128, S, cus);
+    const double t = per * (full < half ? full : half) + (S > 1 ? 3.0 + 8e-6 / 4.5 * S * M * N : 0.0);
+    if (S == 1 || t < least) {
+      best = S;
+      least = t;
+    }
+  }
+  return best;
 }
 
 // fp32 partials of a tile, straight from the accumulators (128-byte rows per half wave).

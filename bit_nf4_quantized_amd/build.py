@@ -26,7 +26,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 # the binding's tensor checks: a CPython module on torch's C++ headers (host code)
 TENSORS_PATH = os.path.join(HERE, "_tensors.so")
 OBJ_DIR = os.path.join(ROOT, "_build")
-SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "gemv.hip", "gemv1.hip", "dense_gemm.hip", "skinny_gemm.hip", "int8.hip", "merge.hip", "midm.hip", "multi.hip", "multi_small.hip", "dropout.hip", "optim.hip", "optim_batch.hip", "preference.hip", "gated.hip", "norm.hip", "head.hip", "convcheck.hip", "probe.hip"]
+SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "gemv.hip", "gemv1.hip", "dense_gemm.hip", "skinny_gemm.hip", "int8.hip", "merge.hip", "midm.hip", "multi.hip", "multi_small.hip", "dropout.hip", "optim.hip", "optim_batch.hip", "preference.hip", "prep.hip", "gated.hip", "norm.hip", "head.hip", "convcheck.hip", "probe.hip"]
 ARCH = os.environ.get("QLORA_OFFLOAD_ARCH", "gfx950")
 
 

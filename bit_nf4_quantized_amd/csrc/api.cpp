@@ -786,7 +786,7 @@ static qlora::Int8Values int8_of(const qlora_int8_values* v) {
   return v ? qlora::Int8Values{v->codes, v->absmax} : qlora::Int8Values{nullptr, nullptr};
 }
 
-static int check_gated_shape(int64_t M, int64_t K, int64_t F, int r) {
+static int check_layer_shape(int64_t M, int64_t K, int64_t F, int r) {
   if (r < 8 || r > QLORA_MAX_RANK || (r % 8) != 0) return QLORA_ERR_ARG;
   if (M < 0 || K <= 0 || F <= 0 || (K % QLORA_BLOCK) != 0 || (F % 8) != 0) return QLORA_ERR_SHAPE;
   if (M > QLORA_LAYER_MAX_ROWS || K >= QLORA_GATED_MAX_COLS || F >= QLORA_GATED_MAX_COLS) return QLORA_ERR_SHAPE;
@@ -795,7 +795,7 @@ static int check_gated_shape(int64_t M, int64_t K, int64_t F, int r) {
 
 int qlora_gated_workspace(int64_t M, int64_t K, int64_t F, int r, int backward, size_t* bytes) {
   if (!bytes) return QLORA_ERR_ARG;
-  const int st = check_gated_shape(M, K, F, r);
+  const int st = check_layer_shape(M, K, F, r);
   if (st != QLORA_OK) return st;
   *bytes = qlora::gated_workspace_layout(M, K, F, r, backward != 0).total;
   return QLORA_OK;
@@ -808,7 +808,7 @@ static int check_gated(const qlora_nf4* gate, const qlora_nf4* up, int64_t M, co
   if (!valid_nf4(gate) || !valid_nf4(up) || !isfinite(scale)) return QLORA_ERR_ARG;
   if (act != QLORA_ACT_SILU && act != QLORA_ACT_GELU_TANH) return QLORA_ERR_ARG;
   if (gate->rows != up->rows || gate->cols != up->cols) return QLORA_ERR_SHAPE;
-  int st = check_gated_shape(M, gate->cols, gate->rows, r);
+  int st = check_layer_shape(M, gate->cols, gate->rows, r);
   if (st != QLORA_OK) return st;
   if (!L1 || !L2 || (gate8 == nullptr) != (up8 == nullptr)) return QLORA_ERR_ARG;
   if (gate8 && gate->rows % QLORA_BLOCK != 0) return QLORA_ERR_SHAPE;
@@ -866,11 +866,10 @@ int qlora_gated_bwd(const qlora_nf4* gate, const qlora_nf4* up, const uint16_t* 
 }
 
 int qlora_linear_bwd_int8_workspace(int64_t M, int64_t K, int64_t N, int r, size_t* bytes) {
-  if (M > QLORA_LAYER_MAX_ROWS) return QLORA_ERR_SHAPE;
-  const int st = qlora_linear_workspace(M, K, N, r, bytes);
+  if (!bytes) return QLORA_ERR_ARG;
+  const int st = check_layer_shape(M, K, N, r);
   if (st != QLORA_OK) return st;
-  if (M > 0 && M * K > QLORA_INT8_MAX_NUMEL) return QLORA_ERR_SHAPE;
-  *bytes = qlora::align_up(*bytes, 256) + qlora::align_up((size_t)M * (size_t)K * 2, 256);
+  *bytes = qlora::linear_int8_workspace_layout(M, K, N, r).total;
   return QLORA_OK;
 }
 
@@ -879,30 +878,21 @@ int qlora_linear_bwd_int8(const qlora_nf4* W, const qlora_int8_values* X8, const
                           void* dL1, void* dL2, qlora_dtype grad_dtype, void* ws, size_t ws_bytes,
                           hipStream_t stream) {
   int st = check_linear(W, M, r, scale);
+  if (st == QLORA_OK) st = check_layer_shape(M, W->cols, W->rows, r);
   if (st != QLORA_OK) return st;
-  if (M > 0 && !X8) return QLORA_ERR_ARG;
+  if (grad_dtype != QLORA_F32 && grad_dtype != QLORA_BF16) return QLORA_ERR_ARG;
+  if (!L1 || !L2 || !dL1 || !dL2 || (M > 0 && (!X8 || !dY))) return QLORA_ERR_ARG;
   st = check_int8(X8, M > 0);
   if (st != QLORA_OK) return st;
-  size_t need = 0;
-  st = qlora_linear_bwd_int8_workspace(M, W->cols, W->rows, r, &need);
-  if (st != QLORA_OK) return st;
   if (!ws) return QLORA_ERR_WORKSPACE;
-  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
-  if (ws_bytes < need) return QLORA_ERR_WORKSPACE;
-  uint16_t* X = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + need -
-                                            qlora::align_up((size_t)M * (size_t)W->cols * 2, 256));
-  // every check of the linear first, so that nothing is enqueued for a refused call
-  if (grad_dtype != QLORA_F32 && grad_dtype != QLORA_BF16) return QLORA_ERR_ARG;
-  if (!L1 || !L2 || !dL1 || !dL2 || (M > 0 && !dY)) return QLORA_ERR_ARG;
   if (!aligned16(dY) || !aligned16(L1) || !aligned16(L2) || !aligned16(T) || !aligned16(dX) || !aligned16(dL1) ||
-      !aligned16(dL2))
+      !aligned16(dL2) || !aligned16(ws))
     return QLORA_ERR_ALIGN;
-  if (M > 0) {
-    (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
-    const hipError_t e = qlora::launch_int8_dequantize(X8->codes, X8->absmax, M * W->cols, 6, X, true, stream);
-    if (e != hipSuccess) return hip_fail(e);
-  }
-  return linear_bwd_impl(W, X, dY, M, L1, L2, r, scale, T, dX, dL1, dL2, grad_dtype, ws, ws_bytes, stream, nullptr);
+  if (ws_bytes < qlora::linear_int8_workspace_layout(M, W->cols, W->rows, r).total) return QLORA_ERR_WORKSPACE;
+  (void)hipGetLastError();  // drop an error left by an earlier, unrelated runtime call
+  const hipError_t e = qlora::linear_backward_int8(view_of(W), tables(W->qtype).tab, int8_of(X8), dY, M, L1, L2, r, scale, T,
+                                                   dX, dL1, dL2, grad_dtype == QLORA_BF16, ws, stream);
+  return e == hipSuccess ? QLORA_OK : hip_fail(e);
 }
 
 static int check_norm(int64_t M, int64_t K, qlora_dtype a, qlora_dtype b, qlora_dtype c) {

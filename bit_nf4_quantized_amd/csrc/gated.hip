@@ -27,95 +27,6 @@ namespace {
 
 int64_t gd_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// ---- operands ------------------------------------------------------------------------------
-
-// Feature f of weight which (0 gate, 1 up) is row 64 (f / 32) + 32 which + f % 32; rows of f in [F, Fp) are zeros.
-__global__ __launch_bounds__(256) void dequant_pair_kernel(NF4View Wg, NF4View Wu, NF4Table tg, NF4Table tu, int64_t Fp,
-                                                           uint16_t* __restrict__ out) {
-  __shared__ float s_q[2][16];
-  const int which = (int)blockIdx.y;
-  const NF4View& W = which ? Wu : Wg;
-  if (threadIdx.x < 16) s_q[which][threadIdx.x] = which ? tu.q[threadIdx.x] : tg.q[threadIdx.x];
-  __syncthreads();
-  const float mu = tensor_mean(W);
-  const int64_t K8 = W.cols / 8, nunits = W.rows * K8, all = Fp * K8;
-  const uint32_t* codes = reinterpret_cast<const uint32_t*>(W.codes);
-  constexpr int kUnits = 4;
-  for (int64_t base = (int64_t)blockIdx.x * 256 * kUnits + threadIdx.x; base < all; base += (int64_t)gridDim.x * 256 * kUnits) {
-    uint32_t c[kUnits];
-    float ap[kUnits];
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int64_t un = base + (int64_t)u * 256, uc = un < nunits ? un : nunits - 1;
-      c[u] = codes[uc];
-      ap[u] = block_const(W, uc >> 3, mu);
-    }
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int64_t un = base + (int64_t)u * 256;
-      if (un >= all) continue;
-      const int64_t f = un / K8, k8 = un - f * K8;
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t byte = (c[u] >> (8 * i)) & 0xFFu;
-        o[i] = un < nunits ? pack_bf16x2(s_q[which][byte & 15u] * ap[u], s_q[which][byte >> 4] * ap[u]) : 0u;
-      }
-      const int64_t row = 64 * (f >> 5) + 32 * which + (f & 31);
-      *reinterpret_cast<u32x4_t*>(out + row * W.cols + k8 * 8) = u32x4_t{o[0], o[1], o[2], o[3]};
-    }
-  }
-}
-
-// The adapters as the products take them; 32 x 32 tiles, transposed through LDS.
-//   l1t [2][rp][K] = L1^T, rows from r on zero
-//   l2i [2 Fp][2 rp] (forward): L2^T in the weight's row order, each weight's r columns at rp which, zeros elsewhere
-//   l2p [2][rp][Fp] (backward): L2, zeros from row r and column F on
-struct GatedAdapters {
-  const uint16_t* L1;
-  const uint16_t* L2;
-  int64_t K, F, Fp;
-  int r, rp;
-  uint16_t* l1t;
-  uint16_t* l2i;      // or nullptr
-  uint16_t* l2p;      // or nullptr
-  int tiles1, tiles2;  // workgroups of each part
-};
-
-__global__ __launch_bounds__(256) void gated_adapters_kernel(GatedAdapters g) {
-  __shared__ uint16_t tile[32][33];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int which = (int)blockIdx.y;
-  int id = (int)blockIdx.x;
-  const int nr = g.rp / 32;
-  if (id < g.tiles1) {
-    const int64_t k0 = (int64_t)(id / nr) * 32;
-    const int j0 = (id % nr) * 32;
-    const uint16_t* src = g.L1 + (int64_t)which * g.K * g.r;
-    for (int y = ty; y < 32; y += 8) tile[y][tx] = j0 + tx < g.r ? src[(k0 + y) * g.r + j0 + tx] : 0;
-    __syncthreads();
-    uint16_t* dst = g.l1t + (int64_t)which * g.rp * g.K;
-    for (int y = ty; y < 32; y += 8) dst[(int64_t)(j0 + y) * g.K + k0 + tx] = tile[tx][y];
-    return;
-  }
-  id -= g.tiles1;
-  const int64_t f0 = (int64_t)(id / nr) * 32;
-  const int j0 = (id % nr) * 32;
-  const uint16_t* src = g.L2 + (int64_t)which * g.r * g.F;
-  for (int y = ty; y < 32; y += 8) {
-    const uint16_t v = j0 + y < g.r && f0 + tx < g.F ? src[(int64_t)(j0 + y) * g.F + f0 + tx] : 0;
-    tile[y][tx] = v;
-    if (g.l2p) g.l2p[((int64_t)which * g.rp + j0 + y) * g.Fp + f0 + tx] = v;
-  }
-  if (!g.l2i) return;
-  __syncthreads();
-  for (int y = ty; y < 32; y += 8) {
-    uint16_t* row = g.l2i + (2 * f0 + 32 * which + y) * (2 * g.rp);
-    row[which * g.rp + j0 + tx] = tile[tx][y];
-    row[(1 - which) * g.rp + j0 + tx] = 0;
-  }
-}
-
 // ---- the product with its epilogues ------------------------------------------------------
 
 // Epilogue tile in LDS: one 32-row block of every wave at a time, gate and up as fp32, 64 rows (both wave rows) x 128
@@ -326,6 +237,7 @@ hipError_t run_tiles(const TgArgs& p, const E& epi, int64_t M, int64_t N, hipStr
 
 using RowRow = TgLayout<false, false, true, false>;
 using RowPaired = TgLayout<false, true, true, true>;
+using RowDown = TgLayout<false, true, true, false>;
 
 // ---- elementwise parts -----------------------------------------------------------------------
 
@@ -470,87 +382,106 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(const float* __restri
 
 }  // namespace
 
-GatedWorkspace gated_workspace_layout(int64_t M, int64_t K, int64_t F, int r, bool bwd) {
+LayerWorkspace gated_workspace_layout(int64_t M, int64_t K, int64_t F, int r, bool bwd) {
   const int64_t Fp = gd_cdiv(F, 64) * 64, rp = gd_cdiv(r, 64) * 64;
-  GatedWorkspace L;
+  LayerWorkspace L;
   size_t off = 0;
   auto take = [&](int64_t bytes) { const size_t at = off; off += align_up((size_t)bytes, 256); return at; };
   const bool dense = bwd || M > kMultiSmallRows;
   L.wd_off = take(dense ? 2 * Fp * K * 2 : 0);
   L.l1t_off = take(dense ? 2 * rp * K * 2 : 0);
-  L.l2_off = take(dense ? (2 * Fp) * (2 * rp) * 2 : 0);
+  L.l2i_off = take(dense ? (2 * Fp) * (2 * rp) * 2 : 0);
+  L.l2p_off = take(bwd ? 2 * rp * Fp * 2 : 0);
   L.st_off = take(M * 2 * rp * 2);
   L.t_off = take(bwd ? 2 * M * r * 2 : 0);
-  L.dgu_off = take(bwd ? M * 2 * Fp * 2 : 0);
+  L.dy_off = take(bwd ? M * 2 * Fp * 2 : 0);
   L.x_off = take(bwd ? M * K * 2 : 0);
   int64_t part = (int64_t)adapter_partial_bytes(AdapterShape{2, M, K, Fp, r, 0.0f});
-  const int64_t S = bwd ? tg_slices(M, K, (2 * Fp + 2 * rp) / kTgK, device_cu_count()) : 1;
-  if (S > 1 && S * M * K * 4 > part) part = S * M * K * 4;
   if (2 * (int64_t)gemv1_partial_bytes(K, r) > part) part = 2 * gemv1_partial_bytes(K, r);
   L.part_off = take(part);
   const int64_t few = M < kMultiSmallRows ? M : kMultiSmallRows;
-  L.part2_off = take(bwd ? 0 : small_pair_partial_floats(few, K, F) * 4);
+  const int64_t S = bwd ? tg_slices(M, K, (2 * Fp + 2 * rp) / kTgK, device_cu_count()) : 1;
+  L.part2_off = take(bwd ? (S > 1 ? S * M * K * 4 : 0) : small_pair_partial_floats(few, K, F) * 4);
+  L.total = off > 0 ? off : 256;
+  return L;
+}
+
+LayerWorkspace linear_int8_workspace_layout(int64_t M, int64_t K, int64_t N, int r) {
+  const int64_t Np = gd_cdiv(N, 64) * 64, rp = gd_cdiv(r, 64) * 64;
+  LayerWorkspace L;
+  size_t off = 0;
+  auto take = [&](int64_t bytes) { const size_t at = off; off += align_up((size_t)bytes, 256); return at; };
+  L.wd_off = take(Np * K * 2);
+  L.l1t_off = take(rp * K * 2);
+  L.l2i_off = off;
+  L.l2p_off = take(rp * Np * 2);
+  L.st_off = take(M * rp * 2);
+  L.t_off = take(M * r * 2);
+  L.dy_off = take(Np != N ? M * Np * 2 : 0);
+  L.x_off = take(M * K * 2);
+  L.part_off = take((int64_t)adapter_partial_bytes(AdapterShape{1, M, K, Np, r, 0.0f}));
+  const int64_t S = tg_slices(M, K, (Np + rp) / kTgK, device_cu_count());
+  L.part2_off = take(S > 1 ? S * M * K * 4 : 0);
   L.total = off > 0 ? off : 256;
   return L;
 }
 
 namespace {
 
-struct GatedBuffers {
-  uint16_t *wd, *l1t, *l2, *st, *t, *dgu, *x;
+struct LayerBuffers {
+  uint16_t *wd, *l1t, *l2i, *l2p, *st, *t, *dy, *x;
   float *part, *part2;
-  GatedBuffers(const GatedWorkspace& L, void* ws) {
+  LayerBuffers(const LayerWorkspace& L, void* ws) {
     char* b = static_cast<char*>(ws);
-    wd = reinterpret_cast<uint16_t*>(b + L.wd_off);
-    l1t = reinterpret_cast<uint16_t*>(b + L.l1t_off);
-    l2 = reinterpret_cast<uint16_t*>(b + L.l2_off);
-    st = reinterpret_cast<uint16_t*>(b + L.st_off);
-    t = reinterpret_cast<uint16_t*>(b + L.t_off);
-    dgu = reinterpret_cast<uint16_t*>(b + L.dgu_off);
-    x = reinterpret_cast<uint16_t*>(b + L.x_off);
+    auto at = [&](size_t off) { return reinterpret_cast<uint16_t*>(b + off); };
+    wd = at(L.wd_off);
+    l1t = at(L.l1t_off);
+    l2i = at(L.l2i_off);
+    l2p = at(L.l2p_off);
+    st = at(L.st_off);
+    t = at(L.t_off);
+    dy = at(L.dy_off);
+    x = at(L.x_off);
     part = reinterpret_cast<float*>(b + L.part_off);
     part2 = reinterpret_cast<float*>(b + L.part2_off);
   }
 };
 
-hipError_t launch_dequant_pair(const GatedBase& W, int64_t Fp, uint16_t* wd, hipStream_t stream) {
-  int64_t blocks = gd_cdiv(Fp * W.gate.cols / 8, 1024);
-  if (blocks > 4 * device_cu_count()) blocks = 4 * device_cu_count();
-  hipLaunchKernelGGL(dequant_pair_kernel, dim3((unsigned)blocks, 2), dim3(256), 0, stream, W.gate, W.up, W.tab_gate, W.tab_up,
-                     Fp, wd);
-  return hipGetLastError();
-}
-
-hipError_t launch_gated_adapters(const uint16_t* L1, const uint16_t* L2, int64_t K, int64_t F, int r, uint16_t* l1t,
-                                 uint16_t* l2i, uint16_t* l2p, hipStream_t stream) {
-  const int rp = (int)gd_cdiv(r, 64) * 64;
-  GatedAdapters g{L1, L2, K, F, gd_cdiv(F, 64) * 64, r, rp, l1t, l2i, l2p, 0, 0};
-  g.tiles1 = (int)(K / 32) * (rp / 32);
-  g.tiles2 = (int)(g.Fp / 32) * (rp / 32);
-  hipLaunchKernelGGL(gated_adapters_kernel, dim3((unsigned)(g.tiles1 + g.tiles2), 2), dim3(256), 0, stream, g);
-  return hipGetLastError();
+LayerPrep gated_prep(const GatedBase& W, int64_t M, const uint16_t* L1, const uint16_t* L2, int r) {
+  LayerPrep p{};
+  p.n = 2;
+  p.M = M;
+  p.K = W.gate.cols;
+  p.N = W.gate.rows;
+  p.Np = gd_cdiv(p.N, 64) * 64;
+  p.r = r;
+  p.rp = (int)gd_cdiv(r, 64) * 64;
+  p.W[0] = W.gate;
+  p.W[1] = W.up;
+  p.tab[0] = W.tab_gate;
+  p.tab[1] = W.tab_up;
+  p.L1 = L1;
+  p.L2 = L2;
+  return p;
 }
 
 // The product of X with both weights and their adapters, into `epi`.
 template <class E>
-hipError_t gated_product(const GatedBuffers& b, const uint16_t* X, int64_t M, int64_t K, int64_t Fp, int64_t rp, const E& epi,
-                         hipStream_t stream) {
+hipError_t gated_product(const LayerBuffers& b, const uint16_t* X, const LayerPrep& s, const E& epi, hipStream_t stream) {
   TgArgs p{};
-  p.A = {X, K, M};
-  p.B = {b.wd, K, 2 * Fp};
-  p.A2 = {b.st, 2 * rp, M};
-  p.B2 = {b.l2, 2 * rp, 2 * Fp};
-  p.kmain = K;
-  p.kslab = 2 * rp;
+  p.A = {X, s.K, s.M};
+  p.B = {b.wd, s.K, 2 * s.Np};
+  p.A2 = {b.st, 2 * s.rp, s.M};
+  p.B2 = {b.l2i, 2 * s.rp, 2 * s.Np};
+  p.kmain = s.K;
+  p.kslab = 2 * s.rp;
   p.per_slice = (int)((p.kmain + p.kslab) / kTgK);
   p.slices = 1;
-  return run_tiles<RowRow>(p, epi, M, 2 * Fp, stream);
+  return run_tiles<RowRow>(p, epi, s.M, 2 * s.Np, stream);
 }
 
 template <typename F1, typename F2>
 hipError_t by_act(int act, F1&& silu, F2&& gelu) { return act == kActSilu ? silu() : gelu(); }
-
-}  // namespace
 
 #define GD_TRY(call)                       \
   do {                                     \
@@ -558,13 +489,55 @@ hipError_t by_act(int act, F1&& silu, F2&& gelu) { return act == kActSilu ? silu
     if (e_ != hipSuccess) return e_;       \
   } while (0)
 
+// dX (unless NULL), dL1 and dL2 of s.n linears of one input from their upstream gradients, side by side in rows of
+// n Np: s U (and T_out, where T is not there yet), dX with the weights read down their rows, the adapters' gradients
+// beside the sums of dX's slices.
+template <class L>
+hipError_t layer_grads(const LayerPrep& s, const LayerBuffers& b, const uint16_t* X, const uint16_t* dY, float scale,
+                       const uint16_t* T, bool have_t, uint16_t* dX, void* dL1, void* dL2, bool grad_bf16,
+                       hipStream_t stream) {
+  const int64_t ldy = s.n * s.Np;
+  const AdapterShape sh{s.n, s.M, s.K, s.N, s.r, scale};
+  const AdapterOperands o{X, s.L1, b.l1t, dY, ldy, s.Np, b.l2p, s.Np};
+  GD_TRY(adapter_up(sh, o, b.st, have_t ? nullptr : b.t, b.part, stream));
+  SplitSum sum{b.part2, dX, s.M * s.K, 1};
+  if (dX) {
+    TgArgs p{};
+    p.A = {dY, ldy, s.M};
+    p.B = {b.wd, s.K, s.K};
+    p.A2 = {b.st, s.n * s.rp, s.M};
+    p.B2 = {b.l1t, s.K, s.K};
+    p.kmain = ldy;
+    p.kslab = s.n * s.rp;
+    p.krows_b = ldy;
+    const int64_t nk = (p.kmain + p.kslab) / kTgK;
+    p.slices = sum.S = tg_slices(s.M, s.K, nk, device_cu_count());
+    p.per_slice = (int)gd_cdiv(nk, p.slices);
+    GD_TRY(run_tiles<L>(p, StoreEpi{dX, p.slices > 1 ? b.part2 : nullptr, s.M, s.K}, s.M, s.K, stream));
+  }
+  return adapter_grads(sh, o, b.st, have_t ? T : b.t, dL1, dL2, grad_bf16, b.part, dX && sum.S > 1 ? &sum : nullptr, stream);
+}
+
+__global__ __launch_bounds__(256) void zero_kernel(uint32_t* __restrict__ p, int64_t words) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256) p[i] = 0u;
+}
+
+// The gradients of an empty batch (a fill kernel: the call may be captured).
+hipError_t zero_grads(int64_t n1, int64_t n2, void* dL1, void* dL2, bool grad_bf16, hipStream_t stream) {
+  const int64_t per = grad_bf16 ? 2 : 1;             // values per word; both counts are multiples of 8
+  hipLaunchKernelGGL(zero_kernel, dim3(256), dim3(256), 0, stream, static_cast<uint32_t*>(dL1), n1 / per);
+  hipLaunchKernelGGL(zero_kernel, dim3(256), dim3(256), 0, stream, static_cast<uint32_t*>(dL2), n2 / per);
+  return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t gated_forward(const GatedBase& W, const uint16_t* X, int64_t M, const uint16_t* L1, const uint16_t* L2, int r,
                          float s, int act, uint16_t* A, uint16_t* T_out, const Int8Values* gate8, const Int8Values* up8,
                          void* ws, hipStream_t stream) {
-  const int64_t K = W.gate.cols, F = W.gate.rows, Fp = gd_cdiv(F, 64) * 64, rp = gd_cdiv(r, 64) * 64;
+  const int64_t K = W.gate.cols, F = W.gate.rows;
   if (M == 0) return hipSuccess;
-  const GatedWorkspace L = gated_workspace_layout(M, K, F, r, false);
-  const GatedBuffers b(L, ws);
+  const LayerBuffers b(gated_workspace_layout(M, K, F, r, false), ws);
   GatedOut o{A, {gate8 ? gate8->codes : nullptr, up8 ? up8->codes : nullptr},
              {gate8 ? gate8->absmax : nullptr, up8 ? up8->absmax : nullptr}, M, F};
   if (!gate8 && gemv1_pair_applies(W, M, r)) return launch_gemv1_pair(W, X, L1, L2, r, s, act, A, T_out, b.part, stream);
@@ -579,89 +552,93 @@ hipError_t gated_forward(const GatedBase& W, const uint16_t* X, int64_t M, const
       hipLaunchKernelGGL(gated_finish_kernel<kActGelu>, grid, dim3(256), 0, stream, b.part2, S, b.part, Z, r, s, L2, T_out, o);
     return hipGetLastError();
   }
-  GD_TRY(launch_gated_adapters(L1, L2, K, F, r, b.l1t, b.l2, nullptr, stream));
-  GD_TRY(adapter_down(AdapterShape{2, M, K, F, r, s}, X, L1, b.l1t, b.st, T_out, b.part, stream));
-  GD_TRY(launch_dequant_pair(W, Fp, b.wd, stream));
+  LayerPrep p = gated_prep(W, M, L1, L2, r);
+  p.wd = b.wd;
+  p.l1t = b.l1t;
+  p.l2i = b.l2i;
+  GD_TRY(launch_layer_prep(p, stream));
+  GD_TRY(adapter_down(AdapterShape{2, M, K, F, r, s}, AdapterOperands{X, L1, b.l1t, nullptr, 0, 0, nullptr, 0}, b.st, T_out,
+                      b.part, stream));
   if (gate8)
     return by_act(
-        act, [&] { return gated_product(b, X, M, K, Fp, rp, GatedFwdEpi<kActSilu, true>{o}, stream); },
-        [&] { return gated_product(b, X, M, K, Fp, rp, GatedFwdEpi<kActGelu, true>{o}, stream); });
+        act, [&] { return gated_product(b, X, p, GatedFwdEpi<kActSilu, true>{o}, stream); },
+        [&] { return gated_product(b, X, p, GatedFwdEpi<kActGelu, true>{o}, stream); });
   return by_act(
-      act, [&] { return gated_product(b, X, M, K, Fp, rp, GatedFwdEpi<kActSilu, false>{o}, stream); },
-      [&] { return gated_product(b, X, M, K, Fp, rp, GatedFwdEpi<kActGelu, false>{o}, stream); });
+      act, [&] { return gated_product(b, X, p, GatedFwdEpi<kActSilu, false>{o}, stream); },
+      [&] { return gated_product(b, X, p, GatedFwdEpi<kActGelu, false>{o}, stream); });
 }
-
-namespace {
-
-__global__ __launch_bounds__(256) void gated_sum_kernel(SplitSum s) { split_sum_body(s, (int64_t)blockIdx.x * 256 + threadIdx.x); }
-
-__global__ __launch_bounds__(256) void zero_kernel(uint32_t* __restrict__ p, int64_t words) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256) p[i] = 0u;
-}
-
-}  // namespace
 
 hipError_t gated_backward(const GatedBase& W, const uint16_t* X, const Int8Values* X8, const uint16_t* dA, int64_t M,
                           const uint16_t* L1, const uint16_t* L2, int r, float s, int act, const uint16_t* T,
                           const Int8Values* gate8, const Int8Values* up8, uint16_t* dX, void* dL1, void* dL2,
                           bool grad_bf16, void* ws, hipStream_t stream) {
-  const int64_t K = W.gate.cols, F = W.gate.rows, Fp = gd_cdiv(F, 64) * 64, rp = gd_cdiv(r, 64) * 64;
-  const int64_t e = grad_bf16 ? 2 : 4;
-  if (M == 0) {
-    hipLaunchKernelGGL(zero_kernel, dim3(256), dim3(256), 0, stream, static_cast<uint32_t*>(dL1), 2 * K * r * e / 4);
-    hipLaunchKernelGGL(zero_kernel, dim3(256), dim3(256), 0, stream, static_cast<uint32_t*>(dL2), 2 * r * F * e / 4);
-    return hipGetLastError();
-  }
-  const GatedWorkspace L = gated_workspace_layout(M, K, F, r, true);
-  const GatedBuffers b(L, ws);
-  const AdapterShape sh{2, M, K, F, r, s};
+  const int64_t K = W.gate.cols, F = W.gate.rows;
+  if (M == 0) return zero_grads(2 * K * r, 2 * r * F, dL1, dL2, grad_bf16, stream);
+  const LayerBuffers b(gated_workspace_layout(M, K, F, r, true), ws);
+  LayerPrep p = gated_prep(W, M, L1, L2, r);
+  p.wd = !gate8 || dX ? b.wd : nullptr;
+  p.l1t = b.l1t;
+  p.l2i = gate8 ? nullptr : b.l2i;
+  p.l2p = b.l2p;
   if (X8) {
-    GD_TRY(launch_int8_dequantize(X8->codes, X8->absmax, M * K, 6, b.x, true, stream));
+    p.x8 = *X8;
+    p.x = b.x;
     X = b.x;
   }
-  // the forward product needs L2^T in b.l2; afterwards the same place holds L2 padded for dY L2^T
-  if (!gate8 || dX) GD_TRY(launch_dequant_pair(W, Fp, b.wd, stream));
-  uint16_t* t = b.t;
+  GD_TRY(launch_layer_prep(p, stream));
+  bool have_t = T != nullptr;
   if (!gate8) {
-    GD_TRY(launch_gated_adapters(L1, L2, K, F, r, b.l1t, b.l2, nullptr, stream));
-    GD_TRY(adapter_down(sh, X, L1, b.l1t, b.st, T ? nullptr : t, b.part, stream));
+    GD_TRY(adapter_down(AdapterShape{2, M, K, F, r, s}, AdapterOperands{X, L1, b.l1t, nullptr, 0, 0, nullptr, 0}, b.st,
+                        T ? nullptr : b.t, b.part, stream));
     GD_TRY(by_act(
-        act, [&] { return gated_product(b, X, M, K, Fp, rp, GatedBwdEpi<kActSilu>{dA, b.dgu, M, F, Fp}, stream); },
-        [&] { return gated_product(b, X, M, K, Fp, rp, GatedBwdEpi<kActGelu>{dA, b.dgu, M, F, Fp}, stream); }));
-    GD_TRY(launch_gated_adapters(L1, L2, K, F, r, b.l1t, nullptr, b.l2, stream));
+        act, [&] { return gated_product(b, X, p, GatedBwdEpi<kActSilu>{dA, b.dy, M, F, p.Np}, stream); },
+        [&] { return gated_product(b, X, p, GatedBwdEpi<kActGelu>{dA, b.dy, M, F, p.Np}, stream); }));
+    if (!have_t) {
+      T = b.t;
+      have_t = true;
+    }
   } else {
-    GD_TRY(launch_gated_adapters(L1, L2, K, F, r, b.l1t, nullptr, b.l2, stream));
-    if (!T) GD_TRY(adapter_down(sh, X, L1, b.l1t, b.st, t, b.part, stream));
     int64_t blocks = gd_cdiv(M * F / 8, 256);
     if (blocks > 16 * device_cu_count()) blocks = 16 * device_cu_count();
     if (act == kActSilu)
-      hipLaunchKernelGGL(gated_dgu_kernel<kActSilu>, dim3((unsigned)blocks), dim3(256), 0, stream, dA, *gate8, *up8, M, F, b.dgu);
+      hipLaunchKernelGGL(gated_dgu_kernel<kActSilu>, dim3((unsigned)blocks), dim3(256), 0, stream, dA, *gate8, *up8, M, F, b.dy);
     else
-      hipLaunchKernelGGL(gated_dgu_kernel<kActGelu>, dim3((unsigned)blocks), dim3(256), 0, stream, dA, *gate8, *up8, M, F, b.dgu);
+      hipLaunchKernelGGL(gated_dgu_kernel<kActGelu>, dim3((unsigned)blocks), dim3(256), 0, stream, dA, *gate8, *up8, M, F, b.dy);
     GD_TRY(hipGetLastError());
   }
-  if (T) t = const_cast<uint16_t*>(T);
-  GD_TRY(adapter_up(sh, b.dgu, 2 * Fp, Fp, b.l2, Fp, b.st, b.part, stream));
-  if (dX) {
-    TgArgs p{};
-    p.A = {b.dgu, 2 * Fp, M};
-    p.B = {b.wd, K, K};
-    p.A2 = {b.st, 2 * rp, M};
-    p.B2 = {b.l1t, K, K};
-    p.kmain = 2 * Fp;
-    p.kslab = 2 * rp;
-    p.krows_b = 2 * Fp;
-    const int64_t nk = (p.kmain + p.kslab) / kTgK;
-    p.slices = tg_slices(M, K, nk, device_cu_count());
-    p.per_slice = (int)gd_cdiv(nk, p.slices);
-    GD_TRY(run_tiles<RowPaired>(p, StoreEpi{dX, p.slices > 1 ? b.part : nullptr, M, K}, M, K, stream));
-    if (p.slices > 1) {
-      const SplitSum sum{b.part, dX, M * K, p.slices};
-      hipLaunchKernelGGL(gated_sum_kernel, dim3((unsigned)gd_cdiv(M * K / 8, 256)), dim3(256), 0, stream, sum);
-      GD_TRY(hipGetLastError());
-    }
+  return layer_grads<RowPaired>(p, b, X, b.dy, s, T, have_t, dX, dL1, dL2, grad_bf16, stream);
+}
+
+hipError_t linear_backward_int8(const NF4View& W, const NF4Table& tab, const Int8Values& X8, const uint16_t* dY, int64_t M,
+                                const uint16_t* L1, const uint16_t* L2, int r, float s, const uint16_t* T, uint16_t* dX,
+                                void* dL1, void* dL2, bool grad_bf16, void* ws, hipStream_t stream) {
+  const int64_t K = W.cols, N = W.rows;
+  if (M == 0) return zero_grads(K * r, r * N, dL1, dL2, grad_bf16, stream);
+  const LayerBuffers b(linear_int8_workspace_layout(M, K, N, r), ws);
+  LayerPrep p{};
+  p.n = 1;
+  p.M = M;
+  p.K = K;
+  p.N = N;
+  p.Np = gd_cdiv(N, 64) * 64;
+  p.r = r;
+  p.rp = (int)gd_cdiv(r, 64) * 64;
+  p.W[0] = W;
+  p.tab[0] = tab;
+  p.wd = dX ? b.wd : nullptr;
+  p.L1 = L1;
+  p.L2 = L2;
+  p.l1t = b.l1t;
+  p.l2p = b.l2p;
+  p.x8 = X8;
+  p.x = b.x;
+  if (p.Np != N) {
+    p.dy = dY;
+    p.dyp = b.dy;
+    dY = b.dy;
   }
-  return adapter_grads(sh, X, b.dgu, 2 * Fp, Fp, b.st, t, dL1, dL2, grad_bf16, b.part, stream);
+  GD_TRY(launch_layer_prep(p, stream));
+  return layer_grads<RowDown>(p, b, b.x, dY, s, T, T != nullptr, dX, dL1, dL2, grad_bf16, stream);
 }
 
 }  // namespace qlora

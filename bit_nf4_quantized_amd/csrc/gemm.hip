@@ -811,46 +811,66 @@ size_t adapter_partial_bytes(const AdapterShape& a) {
   upd((int64_t)sU.Z * M * r * 4);
   upd((int64_t)s1.Z * K * r * 4);
   upd((int64_t)s2.Z * r * N * 4);
-  if (r <= 64) upd(a.n * (int64_t)skinny_partial_bytes(M, K, N));
+  if (r <= 64) upd(2 * a.n * (int64_t)skinny_partial_bytes(M, K, N));   // two jobs
   if (M <= kMidMaxM) upd(a.n * (int64_t)small_t_partial_bytes(M, K, (int)r));
   return align_up((size_t)part, 256);
 }
 
-hipError_t adapter_down(const AdapterShape& a, const uint16_t* X, const uint16_t* L1, const uint16_t* l1t, uint16_t* sT,
-                        uint16_t* T_out, float* part, hipStream_t stream) {
+namespace {
+
+SkinnyNt down_job(const AdapterShape& a, const AdapterOperands& o, uint16_t* sT, uint16_t* T_out) {
+  const int64_t rp = cdiv(a.r, 64) * 64;
+  const SkinnyBatch b{a.n, 0, rp * a.K, sT ? rp : a.M * a.r, a.M * a.r};
+  // without sT the sum is T_out itself
+  return sT ? SkinnyNt{o.X, a.K, o.l1t, a.K, a.M, a.K, a.r, a.s, sT, rp, a.n * rp, 1.0f, T_out, b}
+            : SkinnyNt{o.X, a.K, o.l1t, a.K, a.M, a.K, a.r, 1.0f, T_out, a.r, 0, 0.0f, nullptr, b};
+}
+
+}  // namespace
+
+hipError_t adapter_down(const AdapterShape& a, const AdapterOperands& o, uint16_t* sT, uint16_t* T_out, float* part,
+                        hipStream_t stream) {
   const int64_t rp = cdiv(a.r, 64) * 64, pitch = a.n * rp;
   if (skinny_ok(a.r, a.M, a.K)) {
-    const SkinnyBatch b{a.n, 0, rp * a.K, rp, a.M * a.r};
-    return skinny_nt(X, a.K, l1t, a.K, a.M, a.K, a.r, part, a.s, sT, rp, 1.0f, T_out, stream, nullptr, pitch, &b);
+    const SkinnyNt j = down_job(a, o, sT, T_out);
+    return skinny_nt_jobs(&j, 1, part, stream);
   }
   for (int k = 0; k < a.n; ++k) {
     GemmArgs g = base_args();
     g.M = a.M; g.N = a.r; g.K = a.K;
-    g.A = X; g.lda = a.K;
-    g.B = L1 + k * a.K * a.r; g.ldb = a.r;
+    g.A = o.X; g.lda = a.K;
+    g.B = o.L1 + k * a.K * a.r; g.ldb = a.r;
     const Split sp = choose_split(cdiv(a.M, BM) * cdiv(a.r, BN), a.K);
     g.k_split = sp.k_split;
     g.C = part; g.ldc = a.r;
     hipError_t e = run_gemm<A_ROW, B_COL, EPI_F32, false>(g, sp.Z, stream);
     if (e != hipSuccess) return e;
-    e = reduce(part, sp.Z, a.M, a.r, a.s, sT + k * rp, true, rp, 1.0f, T_out ? T_out + k * a.M * a.r : nullptr, stream, pitch);
+    uint16_t* t = T_out ? T_out + k * a.M * a.r : nullptr;
+    e = sT ? reduce(part, sp.Z, a.M, a.r, a.s, sT + k * rp, true, rp, 1.0f, t, stream, pitch)
+           : reduce(part, sp.Z, a.M, a.r, 1.0f, t, true, a.r, 0.0f, nullptr, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-hipError_t adapter_up(const AdapterShape& a, const uint16_t* dY, int64_t ldy, int64_t y_step, const uint16_t* l2p,
-                      int64_t ldl, uint16_t* sU, float* part, hipStream_t stream) {
+hipError_t adapter_up(const AdapterShape& a, const AdapterOperands& o, uint16_t* sU, uint16_t* T_out, float* part,
+                      hipStream_t stream) {
   const int64_t rp = cdiv(a.r, 64) * 64, pitch = a.n * rp;
-  if (a.r <= 64 && fits_dense({a.M * ldy * 2})) {
-    const SkinnyBatch b{a.n, y_step, rp * ldl, rp, 0};
-    return skinny_nt(dY, ldy, l2p, ldl, a.M, ldl, a.r, part, a.s, sU, rp, 0.0f, nullptr, stream, nullptr, pitch, &b);
+  if (a.r <= 64 && fits_dense({a.M * o.ldy * 2, a.M * a.K * 2})) {
+    const SkinnyNt j[2] = {SkinnyNt{o.dY, o.ldy, o.l2p, o.ldl, a.M, o.ldl, a.r, a.s, sU, rp, pitch, 0.0f, nullptr,
+                                    SkinnyBatch{a.n, o.y_step, rp * o.ldl, rp, 0}},
+                           T_out ? down_job(a, o, nullptr, T_out) : SkinnyNt{}};
+    return skinny_nt_jobs(j, T_out ? 2 : 1, part, stream);
+  }
+  if (T_out) {
+    const hipError_t e = adapter_down(a, o, nullptr, T_out, part, stream);
+    if (e != hipSuccess) return e;
   }
   for (int k = 0; k < a.n; ++k) {
     GemmArgs g = base_args();
     g.M = a.M; g.N = a.r; g.K = a.N;
-    g.A = dY + k * y_step; g.lda = ldy;
-    g.B = l2p + k * rp * ldl; g.ldb = ldl;
+    g.A = o.dY + k * o.y_step; g.lda = o.ldy;
+    g.B = o.l2p + k * rp * o.ldl; g.ldb = o.ldl;
     const Split sp = choose_split(cdiv(a.M, BM) * cdiv(a.r, BN), a.N);
     g.k_split = sp.k_split;
     g.C = part; g.ldc = a.r;
@@ -862,21 +882,31 @@ hipError_t adapter_up(const AdapterShape& a, const uint16_t* dY, int64_t ldy, in
   return hipSuccess;
 }
 
-hipError_t adapter_grads(const AdapterShape& a, const uint16_t* X, const uint16_t* dY, int64_t ldy, int64_t y_step,
-                         const uint16_t* sU, const uint16_t* T, void* dL1, void* dL2, bool grad_bf16, float* part,
-                         hipStream_t stream) {
+namespace {
+
+__global__ __launch_bounds__(256) void split_sum_kernel(SplitSum s) { split_sum_body(s, (int64_t)blockIdx.x * 256 + threadIdx.x); }
+
+}  // namespace
+
+hipError_t adapter_grads(const AdapterShape& a, const AdapterOperands& o, const uint16_t* sU, const uint16_t* T, void* dL1,
+                         void* dL2, bool grad_bf16, float* part, const SplitSum* split, hipStream_t stream) {
   const int64_t rp = cdiv(a.r, 64) * 64, pitch = a.n * rp, r = a.r;
   if (r <= 64) {
-    const SkinnyBatch b1{a.n, 0, rp, a.K * r, 0}, b2{a.n, y_step, a.M * r, r * a.N, 0};
-    const hipError_t e = skinny_tn(X, a.K, a.K, sU, pitch, a.M, a.r, part, 1.0f, false, grad_bf16, dL1, stream, nullptr, &b1);
+    const SkinnyTn j[2] = {
+        SkinnyTn{o.X, a.K, a.K, sU, pitch, a.M, a.r, 1.0f, false, grad_bf16, dL1, SkinnyBatch{a.n, 0, rp, a.K * r, 0}},
+        SkinnyTn{o.dY, o.ldy, a.N, T, r, a.M, a.r, a.s, true, grad_bf16, dL2, SkinnyBatch{a.n, o.y_step, a.M * r, r * a.N, 0}}};
+    return skinny_tn_jobs(j, 2, part, split, stream);
+  }
+  if (split) {
+    hipLaunchKernelGGL(split_sum_kernel, dim3((unsigned)cdiv(split->values / 8, 256)), dim3(256), 0, stream, *split);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    return skinny_tn(dY, ldy, a.N, T, r, a.M, a.r, part, a.s, true, grad_bf16, dL2, stream, nullptr, &b2);
   }
   const int64_t w = grad_bf16 ? 2 : 4;
   for (int k = 0; k < a.n; ++k) {
     GemmArgs g = base_args();
     g.M = a.K; g.N = r; g.K = a.M;
-    g.A = X; g.lda = a.K;
+    g.A = o.X; g.lda = a.K;
     g.B = sU + k * rp; g.ldb = pitch;
     const Split s1 = choose_split(cdiv(a.K, BM) * cdiv(r, BN), a.M);
     g.k_split = s1.k_split;
@@ -888,7 +918,7 @@ hipError_t adapter_grads(const AdapterShape& a, const uint16_t* X, const uint16_
     g = base_args();
     g.M = r; g.N = a.N; g.K = a.M;
     g.A = T + k * a.M * r; g.lda = r;
-    g.B = dY + k * y_step; g.ldb = ldy;
+    g.B = o.dY + k * o.y_step; g.ldb = o.ldy;
     const Split s2 = choose_split(cdiv(r, BM) * cdiv(a.N, BN), a.M);
     g.k_split = s2.k_split;
     g.C = part; g.ldc = a.N;

@@ -220,25 +220,50 @@ struct SkinnySplit {
   int Z;        // reduction slices
   int64_t len;  // reduction length per slice (multiple of 64)
 };
-// n equal products in one launch (no dropout): elements between their large
-// operands, small operands, results and second results; the partials take n
-// times skinny_partial_bytes.
-struct SkinnyBatch {
-  int n;
-  int64_t a_step, b_step, o_step, o2_step;
-};
 SkinnySplit skinny_split(int64_t tiles, int64_t klen, int64_t fit = 0);
 size_t skinny_partial_bytes(int64_t M, int64_t K, int64_t N);
 // dr: A is the adapter input X ([M][K], lda == K), dropped in registers.
 hipError_t skinny_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t K, int r,
                      float* part, float alpha, uint16_t* out, int64_t ldo, float alpha2, uint16_t* out2,
-                     hipStream_t stream, const DropoutParams* dr = nullptr, int64_t pitch = 0,
-                     const SkinnyBatch* batch = nullptr);
-// (pitch: elements between rows of out, ldo where 0)
+                     hipStream_t stream, const DropoutParams* dr = nullptr);
 // dr: L is the adapter input X ([M][W], ldl == W), dropped in registers.
 hipError_t skinny_tn(const uint16_t* L, int64_t ldl, int64_t W, const uint16_t* S, int64_t lds, int64_t M, int r,
                      float* part, float alpha, bool transpose, bool out_bf16, void* out, hipStream_t stream,
-                     const DropoutParams* dr = nullptr, const SkinnyBatch* batch = nullptr);
+                     const DropoutParams* dr = nullptr);
+// One or two such jobs, each n equal products (elements between their large operands, small operands, results and
+// second results), in one launch, and their sums in another. The partials of a job take batch.n Z rows 64 floats
+// (skinny_partial_bytes per product at most), one job's after the other's.
+struct SkinnyBatch {
+  int n;
+  int64_t a_step, b_step, o_step, o2_step;
+};
+struct SkinnyNt {          // out [M][ldo columns, rows pitch apart (0: ldo)] = bf16(alpha A B^T), out2 [M][r] = bf16(alpha2 A B^T)
+  const uint16_t* A;
+  int64_t lda;
+  const uint16_t* B;
+  int64_t ldb, M, K;
+  int r;
+  float alpha;
+  uint16_t* out;
+  int64_t ldo, pitch;
+  float alpha2;
+  uint16_t* out2;
+  SkinnyBatch batch;
+};
+struct SkinnyTn {          // out [W][r] (transposed: [r][W]) = alpha L^T S
+  const uint16_t* L;
+  int64_t ldl, W;
+  const uint16_t* S;
+  int64_t lds, M;
+  int r;
+  float alpha;
+  bool transpose, out_bf16;
+  void* out;
+  SkinnyBatch batch;
+};
+hipError_t skinny_nt_jobs(const SkinnyNt* jobs, int n, float* part, hipStream_t stream);
+// split: another product's slices, added in the same launch as the sums (or NULL)
+hipError_t skinny_tn_jobs(const SkinnyTn* jobs, int n, float* part, const SplitSum* split, hipStream_t stream);
 
 // Workspace of the linear layer (shared by forward and backward).
 struct LinearWorkspace {
@@ -416,27 +441,35 @@ hipError_t linear_backward(const NF4View& W, const NF4Table& tab, const uint16_t
                            void* ws, hipStream_t stream, const DropoutParams* dr = nullptr);
 
 // The adapter products of n adapters beside another kernel's product (gemm.hip), as in linear_forward and
-// linear_backward: the skinny kernels, all adapters in one launch, for rank <= 64 where their 32-bit offsets reach,
-// else the 128 x 128 GEMM in reduction slices, adapter by adapter. rp: rank rounded up to 64; adapter k's part of sT
-// and sU is columns [k rp, (k + 1) rp) of [M][n rp] (zeros behind its rank).
-//   down: sT = bf16(s X L1_k), T_out (or NULL) [n][M][r] = bf16(X L1_k); L1 [n][K][r], l1t [n][rp][K]: L1^T, zero rows
-//   up:   sU = bf16(s dY_k L2_k^T); dY_k [M] rows ldy apart, k y_step; l2p [n][rp][ldl]: L2, zeros behind rank and N,
-//         ldl a multiple of 64 up to which dY's rows can be read
-//   grads: dL1 [n][K][r] = X^T sU_k, dL2 [n][r][N] = s T_k^T dY_k; T [n][M][r]
+// linear_backward: the skinny kernels, all products of a call in one launch and their sums in another, for rank <= 64
+// where their 32-bit offsets reach, else the 128 x 128 GEMM in reduction slices, one after another. rp: rank rounded
+// up to 64; adapter k's part of sT and sU is columns [k rp, (k + 1) rp) of [M][n rp] (zeros behind its rank).
+//   down: sT = bf16(s X L1_k) and T_out [n][M][r] = bf16(X L1_k) (either may be NULL)
+//   up:   sU = bf16(s dY_k L2_k^T)
+//   grads: dL1 [n][K][r] = X^T sU_k, dL2 [n][r][N] = s T_k^T dY_k; split as in skinny_tn_jobs
 struct AdapterShape {
   int n;
   int64_t M, K, N;
   int r;
   float s;
 };
+struct AdapterOperands {
+  const uint16_t* X;        // [M][K]
+  const uint16_t* L1;       // [n][K][r]
+  const uint16_t* l1t;      // [n][rp][K]: L1^T, zero rows behind the rank
+  const uint16_t* dY;       // of adapter k at k y_step, rows ldy apart, readable up to column ldl
+  int64_t ldy, y_step;
+  const uint16_t* l2p;      // [n][rp][ldl]: L2, zeros behind rank and N; ldl a multiple of 64
+  int64_t ldl;
+};
 size_t adapter_partial_bytes(const AdapterShape& a);
-hipError_t adapter_down(const AdapterShape& a, const uint16_t* X, const uint16_t* L1, const uint16_t* l1t, uint16_t* sT,
-                        uint16_t* T_out, float* part, hipStream_t stream);
-hipError_t adapter_up(const AdapterShape& a, const uint16_t* dY, int64_t ldy, int64_t y_step, const uint16_t* l2p,
-                      int64_t ldl, uint16_t* sU, float* part, hipStream_t stream);
-hipError_t adapter_grads(const AdapterShape& a, const uint16_t* X, const uint16_t* dY, int64_t ldy, int64_t y_step,
-                         const uint16_t* sU, const uint16_t* T, void* dL1, void* dL2, bool grad_bf16, float* part,
-                         hipStream_t stream);
+hipError_t adapter_down(const AdapterShape& a, const AdapterOperands& o, uint16_t* sT, uint16_t* T_out, float* part,
+                        hipStream_t stream);
+// up, and T_out as in down where it is not NULL
+hipError_t adapter_up(const AdapterShape& a, const AdapterOperands& o, uint16_t* sU, uint16_t* T_out, float* part,
+                      hipStream_t stream);
+hipError_t adapter_grads(const AdapterShape& a, const AdapterOperands& o, const uint16_t* sU, const uint16_t* T, void* dL1,
+                         void* dL2, bool grad_bf16, float* part, const SplitSum* split, hipStream_t stream);
 // T partials [slices][M][r] for M <= 128 (gemv.hip), of `adapters` adapters one after another
 size_t small_t_partial_bytes(int64_t M, int64_t K, int r);
 int small_t_slices(int64_t K);
@@ -454,21 +487,43 @@ struct Int8Values {              // blocks of 64 (the blockwise Int8 codec)
   float* absmax;
 };
 enum GatedAct { kActSilu = 0, kActGelu = 1 };
-struct GatedWorkspace {
-  size_t wd_off;     // bf16 [2 Fp][K]: both dequantised weights, rows in pairs of blocks of 32 (Fp: F rounded up to 64)
-  size_t l1t_off;    // bf16 [2][rp][K]: L1^T
-  size_t l2_off;     // forward: bf16 [2 Fp][2 rp], L2^T in the rows' order; backward: bf16 [2][rp][Fp], L2
-  size_t st_off;     // bf16 [M][2 rp]: s T, or s U
-  size_t t_off;      // bf16 [2][M][r]: T, when the caller has none
-  size_t dgu_off;    // backward: bf16 [M][2 Fp]: dG, then dU
-  size_t x_off;      // backward: bf16 [M][K]: X from its 8-bit values
-  size_t part_off;   // fp32 partials
-  size_t part2_off;  // few rows: fp32 partials of both base products
+
+// What a layer's products need beforehand, in one launch (prep.hip, which says what each part is). NULL outputs: not
+// computed.
+struct LayerPrep {
+  int n;                     // weights and adapters: 1 or 2
+  int64_t M, K, N, Np;       // Np: N rounded up to 64
+  int r, rp;                 // rp: r rounded up to 64
+  NF4View W[2];
+  NF4Table tab[2];
+  uint16_t* wd;
+  const uint16_t* L1;        // [n][K][r]
+  const uint16_t* L2;        // [n][r][N]
+  uint16_t *l1t, *l2i, *l2p;
+  Int8Values x8;
+  uint16_t* x;
+  const uint16_t* dy;
+  uint16_t* dyp;
+  int blocks[5];             // set by the launch
+};
+hipError_t launch_layer_prep(LayerPrep p, hipStream_t stream);
+
+struct LayerWorkspace {
+  size_t wd_off;     // bf16 [n Np][K]: the dequantised weights
+  size_t l1t_off;    // bf16 [n][rp][K]: L1^T
+  size_t l2i_off;    // bf16 [2 Np][2 rp]: L2^T in the paired rows' order (the gated product)
+  size_t l2p_off;    // bf16 [n][rp][Np]: L2 (backward)
+  size_t st_off;     // bf16 [M][n rp]: s T, or s U
+  size_t t_off;      // bf16 [n][M][r]: T, when the caller has none
+  size_t dy_off;     // bf16 [M][n Np]: dG, then dU; or dY of a ragged N
+  size_t x_off;      // bf16 [M][K]: X from its 8-bit values
+  size_t part_off;   // fp32 partials of the adapter products
+  size_t part2_off;  // fp32 partials of dX's slices; few rows forward: of both base products
   size_t total;
 };
 constexpr int64_t kLayerMaxRows = (int64_t)1 << 21;   // of the entry points of qlora_layers.h
 constexpr int64_t kGatedMaxCols = (int64_t)1 << 22;   // K and F: 32-bit offsets inside a tile
-GatedWorkspace gated_workspace_layout(int64_t M, int64_t K, int64_t F, int r, bool bwd);
+LayerWorkspace gated_workspace_layout(int64_t M, int64_t K, int64_t F, int r, bool bwd);
 hipError_t gated_forward(const GatedBase& W, const uint16_t* X, int64_t M, const uint16_t* L1, const uint16_t* L2, int r,
                          float s, int act, uint16_t* A, uint16_t* T_out, const Int8Values* gate8, const Int8Values* up8,
                          void* ws, hipStream_t stream);
@@ -476,6 +531,12 @@ hipError_t gated_backward(const GatedBase& W, const uint16_t* X, const Int8Value
                           const uint16_t* L1, const uint16_t* L2, int r, float s, int act, const uint16_t* T,
                           const Int8Values* gate8, const Int8Values* up8, uint16_t* dX, void* dL1, void* dL2,
                           bool grad_bf16, void* ws, hipStream_t stream);
+
+// The linear's backward pass from 8-bit values of X (gated.hip)
+LayerWorkspace linear_int8_workspace_layout(int64_t M, int64_t K, int64_t N, int r);
+hipError_t linear_backward_int8(const NF4View& W, const NF4Table& tab, const Int8Values& X8, const uint16_t* dY, int64_t M,
+                                const uint16_t* L1, const uint16_t* L2, int r, float s, const uint16_t* T, uint16_t* dX,
+                                void* dL1, void* dL2, bool grad_bf16, void* ws, hipStream_t stream);
 
 // Up to 128 rows (multi_small.hip): the base products' partials [slices][M][F] of gate, then of up
 int small_pair_slices(int64_t M, int64_t K, int64_t N);

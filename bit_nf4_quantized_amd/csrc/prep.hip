@@ -1,0 +1,146 @@
+// What the products of a layer's pass need beforehand, as one launch of
+// independent parts (each workgroup takes a piece of one part): apart, the parts
+// of a short batch were mostly launch latency (a linear's backward pass of 200
+// rows 101 -> ? us with this and the joined sums).
+//
+//   weights   one or two quantised weights [N][K] -> bf16 rows; two of them in
+//             pairs of blocks of 32 rows (row n of weight w at 64 (n / 32) + 32 w
+//             + n % 32), rows N .. Np zeros. 2.5 B per weight: 90 M weights 50 us.
+//   adapters  32 x 32 tiles, transposed through LDS:
+//             l1t [n][rp][K] = L1^T, rows behind the rank zero
+//             l2i [2 Np][2 rp] = L2^T in the paired rows' order, weight w's columns
+//             at rp w, zeros elsewhere
+//             l2p [n][rp][Np] = L2, zeros behind rank and N
+//   x         int8 values -> bf16
+//   dY        [M][N] -> [M][Np], zeros behind N
+#include "common.h"
+#include "launch.h"
+
+namespace qlora {
+
+namespace {
+
+__device__ __forceinline__ void prep_weights(const LayerPrep& p, int which, int block, int blocks, float* s_q) {
+  const NF4View& W = which ? p.W[1] : p.W[0];
+  if (threadIdx.x < 16) s_q[threadIdx.x] = which ? p.tab[1].q[threadIdx.x] : p.tab[0].q[threadIdx.x];
+  __syncthreads();
+  const float mu = tensor_mean(W);
+  const int64_t K8 = W.cols / 8, nunits = W.rows * K8, all = p.Np * K8;
+  const uint32_t* codes = reinterpret_cast<const uint32_t*>(W.codes);
+  constexpr int kUnits = 4;                          // 8 weights each, 256 units apart, all loads first
+  for (int64_t base = (int64_t)block * 256 * kUnits + threadIdx.x; base < all; base += (int64_t)blocks * 256 * kUnits) {
+    uint32_t c[kUnits];
+    float ap[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int64_t un = base + (int64_t)u * 256, uc = un < nunits ? un : nunits - 1;
+      c[u] = codes[uc];
+      ap[u] = block_const(W, uc >> 3, mu);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int64_t un = base + (int64_t)u * 256;
+      if (un >= all) continue;
+      const int64_t n = un / K8, k8 = un - n * K8;
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t byte = (c[u] >> (8 * i)) & 0xFFu;
+        o[i] = un < nunits ? pack_bf16x2(s_q[byte & 15u] * ap[u], s_q[byte >> 4] * ap[u]) : 0u;
+      }
+      const int64_t row = p.n == 2 ? 64 * (n >> 5) + 32 * which + (n & 31) : n;
+      *reinterpret_cast<u32x4_t*>(p.wd + row * W.cols + k8 * 8) = u32x4_t{o[0], o[1], o[2], o[3]};
+    }
+  }
+}
+
+__device__ __forceinline__ void prep_l1(const LayerPrep& p, int id, uint16_t (*tile)[33]) {
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, nr = p.rp / 32, per = (int)(p.K / 32) * nr;
+  const int which = id / per, i = id - which * per;
+  const int64_t k0 = (int64_t)(i / nr) * 32;
+  const int j0 = (i % nr) * 32;
+  const uint16_t* src = p.L1 + (int64_t)which * p.K * p.r;
+  for (int y = ty; y < 32; y += 8) tile[y][tx] = j0 + tx < p.r ? src[(k0 + y) * p.r + j0 + tx] : 0;
+  __syncthreads();
+  uint16_t* dst = p.l1t + (int64_t)which * p.rp * p.K;
+  for (int y = ty; y < 32; y += 8) dst[(int64_t)(j0 + y) * p.K + k0 + tx] = tile[tx][y];
+}
+
+__device__ __forceinline__ void prep_l2(const LayerPrep& p, int id, uint16_t (*tile)[33]) {
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, nr = p.rp / 32, per = (int)(p.Np / 32) * nr;
+  const int which = id / per, i = id - which * per;
+  const int64_t n0 = (int64_t)(i / nr) * 32;
+  const int j0 = (i % nr) * 32;
+  const uint16_t* src = p.L2 + (int64_t)which * p.r * p.N;
+  for (int y = ty; y < 32; y += 8) {
+    const uint16_t v = j0 + y < p.r && n0 + tx < p.N ? src[(int64_t)(j0 + y) * p.N + n0 + tx] : 0;
+    tile[y][tx] = v;
+    if (p.l2p) p.l2p[((int64_t)which * p.rp + j0 + y) * p.Np + n0 + tx] = v;
+  }
+  if (!p.l2i) return;
+  __syncthreads();
+  for (int y = ty; y < 32; y += 8) {
+    uint16_t* row = p.l2i + (2 * n0 + 32 * which + y) * (2 * p.rp);
+    row[which * p.rp + j0 + tx] = tile[tx][y];
+    row[(1 - which) * p.rp + j0 + tx] = 0;
+  }
+}
+
+__global__ __launch_bounds__(256) void layer_prep_kernel(LayerPrep p) {
+  __shared__ float s_q[16];
+  __shared__ uint16_t tile[32][33];
+  int id = (int)blockIdx.x;
+  if (id < p.blocks[0]) {                            // the longest part first
+    const int per = p.blocks[0] / p.n;
+    prep_weights(p, id / per, id % per, per, s_q);
+    return;
+  }
+  id -= p.blocks[0];
+  if (id < p.blocks[1]) {
+    const int64_t n8 = p.M * p.K / 8;
+    for (int64_t i = (int64_t)id * 256 + threadIdx.x; i < n8; i += (int64_t)p.blocks[1] * 256) {
+      const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p.x8.codes + i * 8);
+      const float s = p.x8.absmax[i >> 3] / 127.0f;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3))) * s;
+      *reinterpret_cast<u32x4_t*>(p.x + i * 8) =
+          u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    }
+    return;
+  }
+  id -= p.blocks[1];
+  if (id < p.blocks[2]) return prep_l1(p, id, tile);
+  id -= p.blocks[2];
+  if (id < p.blocks[3]) return prep_l2(p, id, tile);
+  id -= p.blocks[3];
+  const int64_t per = p.Np / 8, n8 = p.M * per;
+  for (int64_t i = (int64_t)id * 256 + threadIdx.x; i < n8; i += (int64_t)p.blocks[4] * 256) {
+    const int64_t m = i / per, c = (i - m * per) * 8;   // N % 8 == 0
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if (c < p.N) v = *reinterpret_cast<const u32x4_t*>(p.dy + m * p.N + c);
+    *reinterpret_cast<u32x4_t*>(p.dyp + m * p.Np + c) = v;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_layer_prep(LayerPrep p, hipStream_t stream) {
+  const int64_t cus = device_cu_count();
+  auto blocks = [&](int64_t units, int64_t most) {
+    const int64_t b = (units + 255) / 256;
+    return (int)(b < most ? b : most);
+  };
+  p.blocks[0] = p.wd ? p.n * blocks(p.Np * p.K / 32, 8 * cus / p.n) : 0;
+  p.blocks[1] = p.x ? blocks(p.M * p.K / 8, 8 * cus) : 0;
+  p.blocks[2] = p.l1t ? p.n * (int)(p.K / 32) * (p.rp / 32) : 0;
+  p.blocks[3] = p.l2i || p.l2p ? p.n * (int)(p.Np / 32) * (p.rp / 32) : 0;
+  p.blocks[4] = p.dyp ? blocks(p.M * p.Np / 8, 8 * cus) : 0;
+  int64_t all = 0;
+  for (int b : p.blocks) all += b;
+  if (all == 0) return hipSuccess;
+  hipLaunchKernelGGL(layer_prep_kernel, dim3((unsigned)all), dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

@@ -69,16 +69,17 @@ struct NtArgs {
   int64_t a_step, b_step;  // product blockIdx.y of a batch: elements between the operands; its C follows the others'
 };
 
+// Row tile bx and slice bz of nz of product by.
 template <bool DROP>
-__global__ __launch_bounds__(kSkThreads) void skinny_nt_kernel(NtArgs p) {
-  p.A += blockIdx.y * p.a_step;
-  p.B += blockIdx.y * p.b_step;
-  p.C += (int64_t)blockIdx.y * gridDim.z * p.M * SJ;
+__device__ __forceinline__ void skinny_nt_body(NtArgs p, int bx, int by, int bz, int nz) {
+  p.A += by * p.a_step;
+  p.B += by * p.b_step;
+  p.C += (int64_t)by * nz * p.M * SJ;
   __shared__ __attribute__((aligned(1024))) uint16_t sA[kNtStages][SM * SK];
   __shared__ __attribute__((aligned(1024))) uint16_t sB[kNtStages][SJ * SK];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m0 = (int64_t)blockIdx.x * SM;
-  const int64_t kz0 = (int64_t)blockIdx.z * p.k_split;
+  const int64_t m0 = (int64_t)bx * SM;
+  const int64_t kz0 = (int64_t)bz * p.k_split;
   const int64_t kz1 = (kz0 + p.k_split < p.K) ? kz0 + p.k_split : p.K;
   const int nk = kz0 < kz1 ? (int)((kz1 - kz0) / SK) : 0;
 
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(kSkThreads) void skinny_nt_kernel(NtArgs p) {
     }
   }
   // C[z][m][j]: lane l, register v -> row (v%4) + 4(l/32) + 8(v/4), column l%32
-  float* Cz = p.C + (int64_t)blockIdx.z * p.M * SJ;
+  float* Cz = p.C + (int64_t)bz * p.M * SJ;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int j = t * 32 + (lane & 31);
@@ -166,6 +167,25 @@ __global__ __launch_bounds__(kSkThreads) void skinny_nt_kernel(NtArgs p) {
       if (m < p.M) Cz[m * SJ + j] = acc[t][v];
     }
   }
+}
+
+template <bool DROP>
+__global__ __launch_bounds__(kSkThreads) void skinny_nt_kernel(NtArgs p) {
+  skinny_nt_body<DROP>(p, (int)blockIdx.x, 0, (int)blockIdx.z, (int)gridDim.z);
+}
+
+// Where workgroups of a job in a launch of several begin, and its grid.
+struct JobGrid {
+  int first, x, y, z;
+  int end() const { return first + x * y * z; }
+};
+
+__global__ __launch_bounds__(kSkThreads) void skinny_nt_jobs_kernel(NtArgs a, NtArgs b, JobGrid ga, JobGrid gb) {
+  const bool second = (int)blockIdx.x >= gb.first;
+  const NtArgs& p = second ? b : a;
+  const JobGrid& g = second ? gb : ga;
+  const int id = (int)blockIdx.x - g.first, xy = g.x * g.y;
+  skinny_nt_body<false>(p, id % g.x, id / g.x % g.y, id / xy, g.z);
 }
 
 // ---- TN: both operands run the reduction down their rows ----------------------------
@@ -315,14 +335,15 @@ __device__ __forceinline__ tn_v4i16 tn_read_tr(const char* lds_byte) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tn_v4i16*)(lds_void_t*)lds_byte);
 }
 
-__global__ __launch_bounds__(kSkThreads) void skinny_tn_dma_kernel(TnArgs p) {
+// Column tile bx and slice bz of nz of product by.
+__device__ __forceinline__ void skinny_tn_body(TnArgs p, int bx, int by, int bz, int nz) {
   __shared__ __attribute__((aligned(1024))) char ring[kTnStages * kTnStageBytes];
-  p.L += blockIdx.y * p.l_step;
-  p.S += blockIdx.y * p.s_step;
-  p.C += (int64_t)blockIdx.y * gridDim.z * p.W * SJ;
+  p.L += by * p.l_step;
+  p.S += by * p.s_step;
+  p.C += (int64_t)by * nz * p.W * SJ;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t c0 = (int64_t)blockIdx.x * SM;
-  const int64_t mz0 = (int64_t)blockIdx.z * p.m_split;
+  const int64_t c0 = (int64_t)bx * SM;
+  const int64_t mz0 = (int64_t)bz * p.m_split;
   const int64_t mz1 = (mz0 + p.m_split < p.M) ? mz0 + p.m_split : p.M;
   const int ns = mz0 < mz1 ? (int)((mz1 - mz0 + SK - 1) / SK) : 0;
   const char* zero = reinterpret_cast<const char*>(g_tn_zero);
@@ -413,7 +434,7 @@ __global__ __launch_bounds__(kSkThreads) void skinny_tn_dma_kernel(TnArgs p) {
       }
     }
   }
-  float* Cz = p.C + (int64_t)blockIdx.z * p.W * SJ;
+  float* Cz = p.C + (int64_t)bz * p.W * SJ;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int j = t * 32 + (lane & 31);
@@ -423,6 +444,18 @@ __global__ __launch_bounds__(kSkThreads) void skinny_tn_dma_kernel(TnArgs p) {
       if (c < p.W) Cz[c * SJ + j] = acc[t][v];
     }
   }
+}
+
+__global__ __launch_bounds__(kSkThreads) void skinny_tn_dma_kernel(TnArgs p) {
+  skinny_tn_body(p, (int)blockIdx.x, 0, (int)blockIdx.z, (int)gridDim.z);
+}
+
+__global__ __launch_bounds__(kSkThreads) void skinny_tn_jobs_kernel(TnArgs a, TnArgs b, JobGrid ga, JobGrid gb) {
+  const bool second = (int)blockIdx.x >= gb.first;
+  const TnArgs& p = second ? b : a;
+  const JobGrid& g = second ? gb : ga;
+  const int id = (int)blockIdx.x - g.first, xy = g.x * g.y;
+  skinny_tn_body(p, id % g.x, id / g.x % g.y, id / xy, g.z);
 }
 
 // sum_z P[z slab .. +4], in order, 8 slices' loads in flight (one at a time, the
@@ -449,35 +482,52 @@ __device__ __forceinline__ f32x4_t sum_slices(const float* __restrict__ P, int Z
 // Four consecutive columns per thread (r % 8 == 0 and ldo % 4 == 0, so a
 // group of four is all below r or all at or above it): 16-byte partial loads,
 // the sum over z in order, 8- or 16-byte stores.
-__global__ __launch_bounds__(256) void skinny_reduce_kernel(const float* __restrict__ P, int Z, int64_t rows, int r,
-                                                            float alpha, int mode, int out_bf16, void* __restrict__ out,
-                                                            int64_t ldo, float alpha2, uint16_t* __restrict__ out2,
-                                                            int64_t pitch, int64_t o_step, int64_t o2_step) {
-  P += (int64_t)blockIdx.y * Z * rows * SJ;
-  out = out_bf16 ? (void*)(static_cast<uint16_t*>(out) + blockIdx.y * o_step) : (void*)(static_cast<float*>(out) + blockIdx.y * o_step);
-  if (out2) out2 += blockIdx.y * o2_step;
-  const int64_t width = (mode == 0) ? ldo : r;
+struct ReduceArgs {
+  const float* P;
+  int Z;
+  int64_t rows;
+  int r;
+  float alpha;
+  int mode, out_bf16;
+  void* out;
+  int64_t ldo;
+  float alpha2;
+  uint16_t* out2;
+  int64_t pitch;
+  int64_t o_step, o2_step;   // elements between the results of a batch
+};
+
+// Workgroup bx of nx of product by.
+__device__ __forceinline__ void skinny_reduce_body(const ReduceArgs& a, int bx, int nx, int by) {
+  const int r = a.r;
+  const float* P = a.P + (int64_t)by * a.Z * a.rows * SJ;
+  void* out = a.out_bf16 ? (void*)(static_cast<uint16_t*>(a.out) + by * a.o_step) : (void*)(static_cast<float*>(a.out) + by * a.o_step);
+  uint16_t* out2 = a.out2 ? a.out2 + by * a.o2_step : nullptr;
+  const int64_t width = (a.mode == 0) ? a.ldo : r;
   const int64_t w4 = width / 4;
-  const int64_t total = rows * w4;
-  const int64_t slab = rows * SJ;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * blockDim.x) {
+  const int64_t total = a.rows * w4;
+  const int64_t slab = a.rows * SJ;
+  for (int64_t i = (int64_t)bx * 256 + threadIdx.x; i < total; i += (int64_t)nx * 256) {
     const int64_t m = i / w4, j = (i - m * w4) * 4;
-    const int64_t o = m * pitch + j;
+    const int64_t o = m * a.pitch + j;
     if (j >= r) {
       *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(out) + o) = u32x2_t{0u, 0u};
       continue;
     }
-    const f32x4_t acc = sum_slices(P + m * SJ + j, Z, slab);
-    const f32x4_t v = {alpha * acc.x, alpha * acc.y, alpha * acc.z, alpha * acc.w};
-    if (out_bf16)
+    const f32x4_t acc = sum_slices(P + m * SJ + j, a.Z, slab);
+    const f32x4_t v = {a.alpha * acc.x, a.alpha * acc.y, a.alpha * acc.z, a.alpha * acc.w};
+    if (a.out_bf16)
       *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(out) + o) = u32x2_t{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
     else
       *reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + o) = v;
-    if (mode == 0 && out2)
+    if (a.mode == 0 && out2)
       *reinterpret_cast<u32x2_t*>(out2 + m * r + j) =
-          u32x2_t{pack_bf16x2(alpha2 * acc.x, alpha2 * acc.y), pack_bf16x2(alpha2 * acc.z, alpha2 * acc.w)};
+          u32x2_t{pack_bf16x2(a.alpha2 * acc.x, a.alpha2 * acc.y), pack_bf16x2(a.alpha2 * acc.z, a.alpha2 * acc.w)};
   }
+}
+
+__global__ __launch_bounds__(256) void skinny_reduce_kernel(ReduceArgs a) {
+  skinny_reduce_body(a, (int)blockIdx.x, (int)gridDim.x, 0);
 }
 
 // Transposed reduction: out[j][c] = alpha * sum_z P[z][c][j] for j < r, c < W,
@@ -486,20 +536,21 @@ __global__ __launch_bounds__(256) void skinny_reduce_kernel(const float* __restr
 // column over the Z partial tiles in a fixed z order (16-byte loads), the
 // 64 x 16 result is transposed through LDS, and each output row segment is
 // written 4 columns per thread.
-__global__ __launch_bounds__(256) void skinny_reduce_t_kernel(const float* __restrict__ P, int Z, int64_t W, int r,
-                                                              float alpha, int out_bf16, void* __restrict__ out,
-                                                              int64_t o_step) {
+// (ReduceArgs: rows is W.) Columns 64 bx .. of rank block by of product bz.
+__device__ __forceinline__ void skinny_reduce_t_body(const ReduceArgs& a, int bx, int by, int bz) {
   __shared__ float tile[64][16 + 1];
-  P += (int64_t)blockIdx.z * Z * W * SJ;
-  out = out_bf16 ? (void*)(static_cast<uint16_t*>(out) + blockIdx.z * o_step) : (void*)(static_cast<float*>(out) + blockIdx.z * o_step);
+  const int64_t W = a.rows;
+  const int r = a.r;
+  const float* P = a.P + (int64_t)bz * a.Z * W * SJ;
+  void* out = a.out_bf16 ? (void*)(static_cast<uint16_t*>(a.out) + bz * a.o_step) : (void*)(static_cast<float*>(a.out) + bz * a.o_step);
   const int t = threadIdx.x;
-  const int64_t c0 = (int64_t)blockIdx.x * 64;
-  const int j0 = blockIdx.y * 16;
+  const int64_t c0 = (int64_t)bx * 64;
+  const int j0 = by * 16;
   if (j0 >= r) return;                         // uniform per workgroup
   const int cl = t >> 2, jq = (t & 3) * 4;     // column c0 + cl, ranks j0 + jq .. +4
   const int64_t c = c0 + cl;
   f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (c < W) acc = sum_slices(P + c * SJ + j0 + jq, Z, W * SJ);
+  if (c < W) acc = sum_slices(P + c * SJ + j0 + jq, a.Z, W * SJ);
 #pragma unroll
   for (int e = 0; e < 4; ++e) tile[cl][jq + e] = acc[e];
   __syncthreads();
@@ -510,12 +561,35 @@ __global__ __launch_bounds__(256) void skinny_reduce_t_kernel(const float* __res
     for (int e = 0; e < 4; ++e) {
       const int64_t cc = c0 + cq + e;
       if (cc < W) {
-        const float v = alpha * tile[cq + e][jl];
-        if (out_bf16) static_cast<uint16_t*>(out)[(int64_t)j * W + cc] = f32_to_bf16(v);
+        const float v = a.alpha * tile[cq + e][jl];
+        if (a.out_bf16) static_cast<uint16_t*>(out)[(int64_t)j * W + cc] = f32_to_bf16(v);
         else static_cast<float*>(out)[(int64_t)j * W + cc] = v;
       }
     }
   }
+}
+
+__global__ __launch_bounds__(256) void skinny_reduce_t_kernel(ReduceArgs a) {
+  skinny_reduce_t_body(a, (int)blockIdx.x, (int)blockIdx.y, 0);
+}
+
+// The sums of two jobs and of a product cut into slices (values 0: none), in one launch.
+struct SumJob {
+  ReduceArgs a;
+  int transpose;
+  JobGrid g;
+};
+
+__global__ __launch_bounds__(256) void skinny_sums_kernel(SumJob p, SumJob q, SplitSum s, int first_split) {
+  const int id = (int)blockIdx.x;
+  if (id >= first_split) {
+    split_sum_body(s, (int64_t)(id - first_split) * 256 + threadIdx.x);
+    return;
+  }
+  const SumJob& j = id >= q.g.first ? q : p;
+  const int i = id - j.g.first;
+  if (j.transpose) skinny_reduce_t_body(j.a, i % j.g.x, i / j.g.x % j.g.y, i / (j.g.x * j.g.y));
+  else skinny_reduce_body(j.a, i % j.g.x, j.g.x, i / j.g.x);
 }
 
 int64_t sk_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -560,56 +634,157 @@ size_t skinny_partial_bytes(int64_t M, int64_t K, int64_t N) {
   return m * SJ * sizeof(float);
 }
 
+namespace {
+
+NtArgs nt_args(const SkinnyNt& j, const SkinnySplit& sp, float* part) {
+  NtArgs a{};
+  a.A = j.A; a.B = j.B; a.C = part; a.lda = j.lda; a.ldb = j.ldb; a.M = j.M; a.K = j.K; a.k_split = sp.len;
+  a.c = 1.0f;
+  a.a_step = j.batch.a_step; a.b_step = j.batch.b_step;
+  return a;
+}
+
+SkinnySplit nt_split(const SkinnyNt& j) {
+  // 72 KB of LDS: two workgroups per CU
+  return skinny_split(sk_cdiv(j.M, SM), j.K, 2 * (int64_t)device_cu_count());
+}
+
+ReduceArgs nt_reduce(const SkinnyNt& j, const SkinnySplit& sp, const float* part) {
+  return ReduceArgs{part, sp.Z, j.M, j.r, j.alpha, 0, 1, j.out, j.ldo, j.alpha2, j.out2, j.pitch ? j.pitch : j.ldo,
+                    j.batch.o_step, j.batch.o2_step};
+}
+
+TnArgs tn_args(const SkinnyTn& j, const SkinnySplit& sp, float* part) {
+  TnArgs a{};
+  a.L = j.L; a.S = j.S; a.C = part; a.ldl = j.ldl; a.lds = j.lds; a.M = j.M; a.W = j.W; a.r = j.r; a.m_split = sp.len;
+  a.c = 1.0f;
+  a.l_step = j.batch.a_step; a.s_step = j.batch.b_step;
+  return a;
+}
+
+SkinnySplit tn_split(const SkinnyTn& j) {
+  // the copy-ring kernel (72 KB of LDS) fits two workgroups per CU
+  return skinny_split(sk_cdiv(j.W, SM), j.M, 2 * (int64_t)device_cu_count());
+}
+
+ReduceArgs tn_reduce(const SkinnyTn& j, const SkinnySplit& sp, const float* part) {
+  return ReduceArgs{part, sp.Z, j.W, j.r, j.alpha, 1, j.out_bf16 ? 1 : 0, j.out, (int64_t)j.r, 0.0f, nullptr, (int64_t)j.r,
+                    j.batch.o_step, 0};
+}
+
+SumJob sum_job(const ReduceArgs& a, bool transpose, int n, int first) {
+  SumJob s{a, transpose ? 1 : 0, JobGrid{first, 0, 1, n}};
+  if (transpose) {
+    s.g.x = (int)sk_cdiv(a.rows, 64);
+    s.g.y = (a.r + 15) / 16;
+  } else {
+    s.g.x = (int)sk_grid(a.rows * (a.mode == 0 ? a.ldo : a.r) / 4);
+    if (s.g.x > 1024) s.g.x = 1024;
+  }
+  return s;
+}
+
+hipError_t launch_sums(const SumJob& p, const SumJob& q, const SplitSum* split, hipStream_t stream) {
+  const int first = q.g.end();
+  const SplitSum s = split ? *split : SplitSum{nullptr, nullptr, 0, 0};
+  const int64_t blocks = first + (s.values / 8 + 255) / 256;
+  hipLaunchKernelGGL(skinny_sums_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, p, q, s, first);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t skinny_nt_jobs(const SkinnyNt* jobs, int n, float* part, hipStream_t stream) {
+  const SkinnyNt& ja = jobs[0];
+  const SkinnySplit sa = nt_split(ja);
+  const JobGrid ga{0, (int)sk_cdiv(ja.M, SM), ja.batch.n, sa.Z};
+  const NtArgs a = nt_args(ja, sa, part);
+  NtArgs b = a;
+  JobGrid gb{ga.end(), 1, 1, 0};                // no second job: no workgroups
+  SumJob p = sum_job(nt_reduce(ja, sa, part), false, ja.batch.n, 0), q = p;
+  q.g = JobGrid{p.g.end(), 1, 1, 0};
+  if (n > 1) {
+    const SkinnyNt& jb = jobs[1];
+    const SkinnySplit sb = nt_split(jb);
+    float* more = part + (int64_t)ja.batch.n * sa.Z * ja.M * SJ;
+    gb = JobGrid{ga.end(), (int)sk_cdiv(jb.M, SM), jb.batch.n, sb.Z};
+    b = nt_args(jb, sb, more);
+    q = sum_job(nt_reduce(jb, sb, more), false, jb.batch.n, p.g.end());
+  }
+  hipLaunchKernelGGL(skinny_nt_jobs_kernel, dim3((unsigned)gb.end()), dim3(kSkThreads), 0, stream, a, b, ga, gb);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_sums(p, q, nullptr, stream);
+}
+
+hipError_t skinny_tn_jobs(const SkinnyTn* jobs, int n, float* part, const SplitSum* split, hipStream_t stream) {
+  const SkinnyTn& ja = jobs[0];
+  const SkinnySplit sa = tn_split(ja);
+  const JobGrid ga{0, (int)sk_cdiv(ja.W, SM), ja.batch.n, sa.Z};
+  const TnArgs a = tn_args(ja, sa, part);
+  TnArgs b = a;
+  JobGrid gb{ga.end(), 1, 1, 0};
+  SumJob p = sum_job(tn_reduce(ja, sa, part), ja.transpose, ja.batch.n, 0), q = p;
+  q.g = JobGrid{p.g.end(), 1, 1, 0};
+  if (n > 1) {
+    const SkinnyTn& jb = jobs[1];
+    const SkinnySplit sb = tn_split(jb);
+    float* more = part + (int64_t)ja.batch.n * sa.Z * ja.W * SJ;
+    gb = JobGrid{ga.end(), (int)sk_cdiv(jb.W, SM), jb.batch.n, sb.Z};
+    b = tn_args(jb, sb, more);
+    q = sum_job(tn_reduce(jb, sb, more), jb.transpose, jb.batch.n, p.g.end());
+  }
+  hipLaunchKernelGGL(skinny_tn_jobs_kernel, dim3((unsigned)gb.end()), dim3(kSkThreads), 0, stream, a, b, ga, gb);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_sums(p, q, split, stream);
+}
+
 // C = A B^T over K with B [64][ldb] (rows >= r zero), then reduce.
 hipError_t skinny_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t K, int r,
                      float* part, float alpha, uint16_t* out, int64_t ldo, float alpha2, uint16_t* out2,
-                     hipStream_t stream, const DropoutParams* dr, int64_t pitch, const SkinnyBatch* batch) {
-  if (dr && (lda != K || batch)) return hipErrorInvalidValue;  // the mask indexes a contiguous [M][K] input
-  // 72 KB of LDS: two workgroups per CU
-  const SkinnySplit sp = skinny_split(sk_cdiv(M, SM), K, 2 * (int64_t)device_cu_count());
-  NtArgs a;
-  a.A = A; a.B = B; a.C = part; a.lda = lda; a.ldb = ldb; a.M = M; a.K = K; a.k_split = sp.len;
-  a.thr = dr ? dr->thr : 0u; a.c = dr ? dr->c : 1.0f; a.seed = dr ? dr->seed : 0u;
-  const SkinnyBatch bt = batch ? *batch : SkinnyBatch{1, 0, 0, 0, 0};
-  a.a_step = bt.a_step; a.b_step = bt.b_step;
-  const dim3 grid((unsigned)sk_cdiv(M, SM), (unsigned)bt.n, (unsigned)sp.Z);
+                     hipStream_t stream, const DropoutParams* dr) {
+  if (dr && lda != K) return hipErrorInvalidValue;  // the mask indexes a contiguous [M][K] input
+  const SkinnyNt j{A, lda, B, ldb, M, K, r, alpha, out, ldo, 0, alpha2, out2, SkinnyBatch{1, 0, 0, 0, 0}};
+  const SkinnySplit sp = nt_split(j);
+  NtArgs a = nt_args(j, sp, part);
+  if (dr) {
+    a.thr = dr->thr; a.c = dr->c; a.seed = dr->seed;
+  }
+  const dim3 grid((unsigned)sk_cdiv(M, SM), 1, (unsigned)sp.Z);
   if (dr)
     hipLaunchKernelGGL(skinny_nt_kernel<true>, grid, dim3(kSkThreads), 0, stream, a);
   else
     hipLaunchKernelGGL(skinny_nt_kernel<false>, grid, dim3(kSkThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(skinny_reduce_kernel, dim3((unsigned)sk_grid(M * ldo / 4), (unsigned)bt.n), dim3(256), 0, stream, part,
-                     sp.Z, M, r, alpha, 0, 1, (void*)out, ldo, alpha2, out2, pitch ? pitch : ldo, bt.o_step, bt.o2_step);
+  hipLaunchKernelGGL(skinny_reduce_kernel, dim3((unsigned)sk_grid(M * ldo / 4)), dim3(256), 0, stream, nt_reduce(j, sp, part));
   return hipGetLastError();
 }
 
 // C[c][j] = sum_m L[m][c] S[m][j], then reduce to out (transposed if `transpose`).
 hipError_t skinny_tn(const uint16_t* L, int64_t ldl, int64_t W, const uint16_t* S, int64_t lds, int64_t M, int r,
                      float* part, float alpha, bool transpose, bool out_bf16, void* out, hipStream_t stream,
-                     const DropoutParams* dr, const SkinnyBatch* batch) {
-  if (dr && (ldl != W || W % 64 || batch)) return hipErrorInvalidValue;  // the mask indexes a contiguous [M][W] input
-  // the copy-ring kernel (72 KB of LDS) fits two workgroups per CU
-  const SkinnySplit sp = skinny_split(sk_cdiv(W, SM), M, dr ? 0 : 2 * (int64_t)device_cu_count());
-  TnArgs a;
-  a.L = L; a.S = S; a.C = part; a.ldl = ldl; a.lds = lds; a.M = M; a.W = W; a.r = r; a.m_split = sp.len;
-  a.thr = dr ? dr->thr : 0u; a.c = dr ? dr->c : 1.0f; a.seed = dr ? dr->seed : 0u;
-  const SkinnyBatch bt = batch ? *batch : SkinnyBatch{1, 0, 0, 0, 0};
-  a.l_step = bt.a_step; a.s_step = bt.b_step;
-  const dim3 grid((unsigned)sk_cdiv(W, SM), (unsigned)bt.n, (unsigned)sp.Z);
+                     const DropoutParams* dr) {
+  if (dr && (ldl != W || W % 64)) return hipErrorInvalidValue;  // the mask indexes a contiguous [M][W] input
+  const SkinnyTn j{L, ldl, W, S, lds, M, r, alpha, transpose, out_bf16, out, SkinnyBatch{1, 0, 0, 0, 0}};
+  const SkinnySplit sp = dr ? skinny_split(sk_cdiv(W, SM), M, 0) : tn_split(j);
+  TnArgs a = tn_args(j, sp, part);
+  if (dr) {
+    a.thr = dr->thr; a.c = dr->c; a.seed = dr->seed;
+  }
+  const dim3 grid((unsigned)sk_cdiv(W, SM), 1, (unsigned)sp.Z);
   if (dr)
     hipLaunchKernelGGL(skinny_tn_kernel<true>, grid, dim3(kSkThreads), 0, stream, a);
   else
     hipLaunchKernelGGL(skinny_tn_dma_kernel, grid, dim3(kSkThreads), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  const ReduceArgs ra = tn_reduce(j, sp, part);
   if (transpose)
-    hipLaunchKernelGGL(skinny_reduce_t_kernel, dim3((unsigned)sk_cdiv(W, 64), SJ / 16, (unsigned)bt.n), dim3(256), 0, stream, part,
-                       sp.Z, W, r, alpha, out_bf16 ? 1 : 0, out, bt.o_step);
+    hipLaunchKernelGGL(skinny_reduce_t_kernel, dim3((unsigned)sk_cdiv(W, 64), SJ / 16), dim3(256), 0, stream, ra);
   else
-    hipLaunchKernelGGL(skinny_reduce_kernel, dim3((unsigned)sk_grid(W * (int64_t)r / 4), (unsigned)bt.n), dim3(256), 0, stream,
-                       part, sp.Z, W, r, alpha, 1, out_bf16 ? 1 : 0, out, (int64_t)r, 0.0f, (uint16_t*)nullptr, (int64_t)r,
-                       bt.o_step, (int64_t)0);
+    hipLaunchKernelGGL(skinny_reduce_kernel, dim3((unsigned)sk_grid(W * (int64_t)r / 4)), dim3(256), 0, stream, ra);
   return hipGetLastError();
 }
 

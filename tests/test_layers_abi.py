@@ -122,7 +122,7 @@ def test_linear_bwd_int8_refusals(lib):
                 dict(T=P + 2), dict(ws=P + 2)):
         assert call(**bad) == E.QLORA_ERR_ALIGN, bad
     need = size(lib.qlora_linear_bwd_int8_workspace, 4, 64, 128, 8)
-    assert need >= size(lib.qlora_linear_workspace, 4, 64, 128, 8) + 4 * 64 * 2
+    assert need >= 128 * 64 * 2 + 4 * 64 * 2            # the dequantised weight and X
     assert call(ws=None) == E.QLORA_ERR_WORKSPACE and call(wsb=need - 1) == E.QLORA_ERR_WORKSPACE
 
 

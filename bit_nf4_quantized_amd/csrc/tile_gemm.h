@@ -24,6 +24,8 @@
 #include "common.h"
 #include "launch.h"
 
+#include <type_traits>
+
 namespace qlora {
 
 typedef __attribute__((address_space(3))) void tg_lds_t;
@@ -65,11 +67,8 @@ __device__ __forceinline__ int tg_swz(int row) { return (row >> 1) & 7; }     //
 //   k-major: 512 / W rows of 2 W bytes; chunk c of row k at c ^ 4 (k % 4): the
 //   four rows that a transpose read touches lie in different banks
 __device__ __forceinline__ void tg_copy(const char* base, uint32_t off, uint16_t* lds, int slice) {
-  const uint64_t v = reinterpret_cast<uint64_t>(base);
-  const uint64_t b = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v) |
-                     (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32;
   const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(tg_lds_t*)(lds + slice * 512));
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" :: "v"(off), "s"(b), "s"(m0)
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" :: "v"(off), "s"(base), "s"(m0)
                : "memory", "m0");
 }
 
@@ -88,27 +87,37 @@ __device__ __forceinline__ void tg_place(int j, int* row, int* chunk) {
   }
 }
 
-// One operand's copies of a tile.
+// One operand's copies of a tile: the lane's byte offsets.
+//   row-major: off, from the tile's first row (main and slab operands apart: their ld differ)
+//   k-major: row, of the lane's k row in a stage, and off, of its columns from column 0; main and slab operands have
+//   one ld and one width
 template <int W, bool KMAJOR>
 struct TgSource {
   static constexpr int kNi = W / 8 / kTgWaves;        // copy instructions per wave and stage
-  uint32_t off[kNi];       // row-major: the lane's offset from the tile's first row; k-major: from column 0
+  uint32_t off[kNi], row[KMAJOR ? kNi : 1];
   __device__ __forceinline__ void init(const TgOperand& o, int64_t first) {
 #pragma unroll
     for (int j = 0; j < kNi; ++j) {
-      int row, chunk;
-      tg_place<W, KMAJOR, kNi>(j, &row, &chunk);
+      int r, chunk;
+      tg_place<W, KMAJOR, kNi>(j, &r, &chunk);
       if constexpr (KMAJOR) {
         int64_t col = first + chunk * 8;
         if (col > o.n - 8) col = o.n - 8;
         off[j] = (uint32_t)(col * 2);
+        row[j] = (uint32_t)(r * o.ld * 2);
       } else {
-        const int64_t r = first + row < o.n ? row : o.n - 1 - first;
-        off[j] = (uint32_t)((r * o.ld + chunk * 8) * 2);
+        const int64_t in = first + r < o.n ? r : o.n - 1 - first;
+        off[j] = (uint32_t)((in * o.ld + chunk * 8) * 2);
       }
     }
   }
 };
+
+// The byte offset of the last k row that a stage at k0 may read, or of its row 63.
+__device__ __forceinline__ uint32_t tg_limit(int64_t krows, int64_t k0, int64_t ld) {
+  const int64_t last = krows - 1 - k0;
+  return (uint32_t)((last < kTgK - 1 ? last : kTgK - 1) * ld * 2);
+}
 
 // Epilogue: a struct E with
 //   template <int MI> __device__ void operator()(f32x16_t (&acc)[MI][2], int64_t m0, int64_t n0, int wm, int wn,
@@ -140,9 +149,17 @@ __device__ __forceinline__ void tg_tile(const TgArgs& p, const E& epi, int64_t m
   SB b1, b2;
   a1.init(p.A, m0);
   b1.init(p.B, n0);
-  if constexpr (L::kSlab) {
-    a2.init(p.A2, m0);
-    b2.init(p.B2, n0);
+  if constexpr (L::kSlab && !L::kAK) a2.init(p.A2, m0);
+  if constexpr (L::kSlab && !L::kBK) b2.init(p.B2, n0);
+  // PAIRED: k row 32 .. 63 of a main stage lies 32 rows further
+  uint32_t pair[L::kPaired ? NB : 1];
+  if constexpr (L::kPaired) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      int r, chunk;
+      tg_place<kTgN, true, NB>(j, &r, &chunk);
+      pair[j] = b1.row[j] + (uint32_t)((r & 32) * p.B.ld * 2);
+    }
   }
   const char* const A1 = reinterpret_cast<const char*>(p.A.p + (L::kAK ? 0 : m0 * p.A.ld));
   const char* const B1 = reinterpret_cast<const char*>(p.B.p + (L::kBK ? 0 : n0 * p.B.ld));
@@ -151,46 +168,41 @@ __device__ __forceinline__ void tg_tile(const TgArgs& p, const E& epi, int64_t m
 
   auto a_buf = [&](int st) { return smem + (st & 1) * kTgStage; };
   auto b_buf = [&](int st) { return smem + (2 + st % 3) * kTgStage; };
-  // copy instruction q of stage st of the slice: q < NA are the A tile's, the rest the B tile's
-  auto issue_one = [&](int st, int q) {
+  // copy instruction q of stage st of the slice: q < NA are the A tile's, the rest the B tile's. Main and slab stages'
+  // copies run in loops of their own: selected in one loop, they cut it into branches between the MFMAs.
+  auto issue_one = [&](int st, int q, auto of_slab) {
+    constexpr bool slab = L::kSlab && decltype(of_slab)::value;
     const int at = s0 + st;
-    const bool slab = L::kSlab && at >= nmain;        // uniform
     const int64_t k0 = (int64_t)(slab ? at - nmain : at) * kTgK;
-    int row, chunk;
     if (q < NA) {
-      const int64_t ld = slab ? p.A2.ld : p.A.ld;
-      uint32_t off = slab ? a2.off[q] : a1.off[q];
       const char* base = slab ? A2 : A1;
+      uint32_t off;
       if constexpr (L::kAK) {
-        tg_place<TM, true, NA>(q, &row, &chunk);
-        const int64_t last = p.krows_a - 1 - k0;
-        if (row > last) row = (int)last;
-        off += (uint32_t)row * (uint32_t)(ld * 2);
-        base += k0 * ld * 2;
+        const uint32_t most = tg_limit(p.krows_a, k0, p.A.ld);
+        off = a1.off[q] + (slab || a1.row[q] < most ? a1.row[q] : most);
+        base += k0 * p.A.ld * 2;
       } else {
+        off = slab ? a2.off[q] : a1.off[q];
         base += k0 * 2;
       }
       tg_copy(base, off, a_buf(st), wave * NA + q);
     } else {
       const int j = q - NA;
-      const int64_t ld = slab ? p.B2.ld : p.B.ld;
-      uint32_t off = slab ? b2.off[j] : b1.off[j];
       const char* base = slab ? B2 : B1;
+      uint32_t off;
       if constexpr (L::kBK) {
-        tg_place<kTgN, true, NB>(j, &row, &chunk);
         int64_t first = k0;
-        if (L::kPaired && !slab) {
-          const int half = (int)(p.kmain / 2 / kTgK);
-          const bool second = at >= half;
-          first = 2 * (k0 - (second ? p.kmain / 2 : 0)) + (second ? 32 : 0);
-          row += row & 32;
-        } else if (!slab) {
-          const int64_t last = p.krows_b - 1 - k0;
-          if (row > last) row = (int)last;
+        if constexpr (L::kPaired) {
+          const bool second = at >= (int)(p.kmain / 2 / kTgK);
+          if (!slab) first = 2 * (k0 - (second ? p.kmain / 2 : 0)) + (second ? 32 : 0);
+          off = b1.off[j] + (slab ? b1.row[j] : pair[j]);
+        } else {
+          const uint32_t most = tg_limit(p.krows_b, k0, p.B.ld);
+          off = b1.off[j] + (slab || b1.row[j] < most ? b1.row[j] : most);
         }
-        off += (uint32_t)row * (uint32_t)(ld * 2);
-        base += first * ld * 2;
+        base += first * p.B.ld * 2;
       } else {
+        off = slab ? b2.off[j] : b1.off[j];
         base += k0 * 2;
       }
       tg_copy(base, off, b_buf(st), wave * NB + j);
@@ -256,7 +268,7 @@ __device__ __forceinline__ void tg_tile(const TgArgs& p, const E& epi, int64_t m
       if constexpr (left > 0) __builtin_amdgcn_sched_group_barrier(0x100, left, 0);
     }
   };
-  auto mma_copies = [&](int set, int cst, int first, int cnt, bool on) {
+  auto mma_copies = [&](int set, int cst, int first, int cnt, bool on, auto of_slab) {
     constexpr int nm = MI * NJ;
 #pragma unroll
     for (int q = 0; q < nm; ++q) {
@@ -264,18 +276,18 @@ __device__ __forceinline__ void tg_tile(const TgArgs& p, const E& epi, int64_t m
           __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][q / NJ], fb[set][q % NJ], acc[q / NJ][q % NJ], 0, 0, 0);
 #pragma unroll
       for (int c = 0; c < cnt; ++c)
-        if (on && (c * nm) / cnt == q) issue_one(cst, first + c);
+        if (on && (c * nm) / cnt == q) issue_one(cst, first + c, of_slab);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   // On entry the fragments of k-step 0 are in set 0 and the copies of stage st + 1 are complete or in flight, as
   // are those of B of stage st + 2; its A tile goes out after this stage's barrier.
-  auto stage = [&](int st, bool refill, bool next) {
+  auto stage = [&](int st, bool refill, bool next, auto of_slab) {
 #pragma unroll
     for (int kk = 0; kk < kTgK / 16 - 1; ++kk) {
       frag(st, kk + 1, (kk + 1) & 1);
       if (kk == 1) {
-        mma_copies(1, st + 2, NA, NB, refill);
+        mma_copies(1, st + 2, NA, NB, refill, of_slab);
       } else {
         mma(kk & 1);
         order();
@@ -287,11 +299,16 @@ __device__ __forceinline__ void tg_tile(const TgArgs& p, const E& epi, int64_t m
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
     if (next) frag(st + 1, 0, 0);
-    mma_copies(1, st + 2, 0, NA, refill);
+    mma_copies(1, st + 2, 0, NA, refill, of_slab);
   };
   auto issue = [&](int st) {
+    if (L::kSlab && s0 + st >= nmain) {
 #pragma unroll
-    for (int q = 0; q < NA + NB; ++q) issue_one(st, q);
+      for (int q = 0; q < NA + NB; ++q) issue_one(st, q, std::true_type{});
+    } else {
+#pragma unroll
+      for (int q = 0; q < NA + NB; ++q) issue_one(st, q, std::false_type{});
+    }
   };
   if (nk > 0) issue(0);
   if (nk > 1) issue(1);
@@ -302,9 +319,13 @@ __device__ __forceinline__ void tg_tile(const TgArgs& p, const E& epi, int64_t m
     frag(0, 0, 0);
   }
   int st = 0;
-  for (; st + 2 < nk; ++st) stage(st, true, true);
-  if (st + 1 < nk) stage(st++, false, true);
-  if (st < nk) stage(st, false, false);
+  const int nm = nmain - s0 < nk ? nmain - s0 : nk;  // main stages of the slice (none: <= 0)
+  for (; st + 2 < nm; ++st) stage(st, true, true, std::false_type{});
+  if constexpr (L::kSlab) {
+    for (; st + 2 < nk; ++st) stage(st, true, true, std::true_type{});
+  }
+  if (st + 1 < nk) stage(st++, false, true, std::false_type{});
+  if (st < nk) stage(st, false, false, std::false_type{});
   __syncthreads();
   epi.template operator()<MI>(acc, m0, n0, wm, wn, z, smem);
 }

@@ -18,6 +18,7 @@
 // against the same matrix read down its rows.
 #include "act.h"
 #include "common.h"
+#include "int8.h"
 #include "launch.h"
 #include "tile_gemm.h"
 
@@ -39,27 +40,6 @@ struct GatedOut {
   float* absmax[2];
   int64_t M, F;
 };
-
-__device__ __forceinline__ uint32_t code4(const float* v, float c) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float x = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(v[i] * c), -127.0f), 127.0f);
-    w |= ((uint32_t)((int32_t)x) & 0xFFu) << (8 * i);
-  }
-  return w;
-}
-
-// 8 of a block's 64 values per lane, 8 neighbouring lanes per block: the codec's codes and absmax.
-__device__ __forceinline__ void store_int8(const float* v, int8_t* codes, float* absmax, int64_t at) {
-  float m = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) m = __builtin_fmaxf(m, __builtin_fabsf(v[e]));
-  m = wave_max(m, 8);
-  const float c = m < 0x1p-120f ? 0.0f : 127.0f / m;
-  *reinterpret_cast<u32x2_t*>(codes + at) = u32x2_t{code4(v, c), code4(v + 4, c)};
-  if ((threadIdx.x & 7) == 0) absmax[at >> 6] = m;
-}
 
 // A = act(G) U, and the 8-bit values of G and U.
 template <int ACT, bool SAVE>
@@ -220,17 +200,12 @@ struct StoreEpi {
 template <class L, class E>
 __global__ __launch_bounds__(kTgThreads, 1) void gated_gemm_kernel(TgArgs p, E epi, TgPlan pl) {
   __shared__ __attribute__((aligned(1024))) uint16_t smem[kTgSmem];
-  int64_t m0, n0;
-  int z;
-  if (!tg_where(pl, p.slices, (int)blockIdx.x, &m0, &n0, &z)) return;
-  if (pl.half) tg_tile<128, L>(p, epi, m0, n0, smem, z);
-  else tg_tile<256, L>(p, epi, m0, n0, smem, z);
+  tg_run<L>(p, epi, pl, smem);
 }
 
 template <class L, class E>
-hipError_t run_tiles(const TgArgs& p, const E& epi, int64_t M, int64_t N, hipStream_t stream) {
-  const TgPlan pl = tg_plan(M, N, p.slices, device_cu_count());
-  hipLaunchKernelGGL((gated_gemm_kernel<L, E>), dim3((unsigned)(pl.tiles_m * pl.tiles_n * p.slices)), dim3(kTgThreads), 0, stream,
+hipError_t run_tiles(const TgArgs& p, const E& epi, const TgPlan& pl, hipStream_t stream) {
+  hipLaunchKernelGGL((gated_gemm_kernel<L, E>), dim3((unsigned)(pl.tiles_m * pl.tiles_n * pl.slices)), dim3(kTgThreads), 0, stream,
                      p, epi, pl);
   return hipGetLastError();
 }
@@ -382,6 +357,14 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(const float* __restri
 
 }  // namespace
 
+namespace {
+
+TgPlan dx_plan(int64_t M, int64_t K, int64_t reduction) {
+  return tg_plan(M, K, (int)(reduction / kTgK), 16 * M, device_cu_count());
+}
+
+}  // namespace
+
 LayerWorkspace gated_workspace_layout(int64_t M, int64_t K, int64_t F, int r, bool bwd) {
   const int64_t Fp = gd_cdiv(F, 64) * 64, rp = gd_cdiv(r, 64) * 64;
   LayerWorkspace L;
@@ -400,7 +383,7 @@ LayerWorkspace gated_workspace_layout(int64_t M, int64_t K, int64_t F, int r, bo
   if (2 * (int64_t)gemv1_partial_bytes(K, r) > part) part = 2 * gemv1_partial_bytes(K, r);
   L.part_off = take(part);
   const int64_t few = M < kMultiSmallRows ? M : kMultiSmallRows;
-  const int64_t S = bwd ? tg_slices(M, K, (2 * Fp + 2 * rp) / kTgK, device_cu_count()) : 1;
+  const int64_t S = bwd ? dx_plan(M, K, 2 * Fp + 2 * rp).slices : 1;
   L.part2_off = take(bwd ? (S > 1 ? S * M * K * 4 : 0) : small_pair_partial_floats(few, K, F) * 4);
   L.total = off > 0 ? off : 256;
   return L;
@@ -420,7 +403,7 @@ LayerWorkspace linear_int8_workspace_layout(int64_t M, int64_t K, int64_t N, int
   L.dy_off = take(Np != N ? M * Np * 2 : 0);
   L.x_off = take(M * K * 2);
   L.part_off = take((int64_t)adapter_partial_bytes(AdapterShape{1, M, K, Np, r, 0.0f}));
-  const int64_t S = tg_slices(M, K, (Np + rp) / kTgK, device_cu_count());
+  const int64_t S = dx_plan(M, K, Np + rp).slices;
   L.part2_off = take(S > 1 ? S * M * K * 4 : 0);
   L.total = off > 0 ? off : 256;
   return L;
@@ -475,9 +458,7 @@ hipError_t gated_product(const LayerBuffers& b, const uint16_t* X, const LayerPr
   p.B2 = {b.l2i, 2 * s.rp, 2 * s.Np};
   p.kmain = s.K;
   p.kslab = 2 * s.rp;
-  p.per_slice = (int)((p.kmain + p.kslab) / kTgK);
-  p.slices = 1;
-  return run_tiles<RowRow>(p, epi, s.M, 2 * s.Np, stream);
+  return run_tiles<RowRow>(p, epi, tg_plan(s.M, 2 * s.Np, (int)((p.kmain + p.kslab) / kTgK), 0, device_cu_count()), stream);
 }
 
 template <typename F1, typename F2>
@@ -510,10 +491,9 @@ hipError_t layer_grads(const LayerPrep& s, const LayerBuffers& b, const uint16_t
     p.kmain = ldy;
     p.kslab = s.n * s.rp;
     p.krows_b = ldy;
-    const int64_t nk = (p.kmain + p.kslab) / kTgK;
-    p.slices = sum.S = tg_slices(s.M, s.K, nk, device_cu_count());
-    p.per_slice = (int)gd_cdiv(nk, p.slices);
-    GD_TRY(run_tiles<L>(p, StoreEpi{dX, p.slices > 1 ? b.part2 : nullptr, s.M, s.K}, s.M, s.K, stream));
+    const TgPlan pl = dx_plan(s.M, s.K, p.kmain + p.kslab);
+    sum.S = pl.slices;
+    GD_TRY(run_tiles<L>(p, StoreEpi{dX, pl.slices > 1 ? b.part2 : nullptr, s.M, s.K}, pl, stream));
   }
   return adapter_grads(sh, o, b.st, have_t ? T : b.t, dL1, dL2, grad_bf16, b.part, dX && sum.S > 1 ? &sum : nullptr, stream);
 }

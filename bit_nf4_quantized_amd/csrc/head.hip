@@ -20,9 +20,9 @@
 //   head_gather_kernel   their rows of H side by side, their label logits; zero rows of dH for the others
 //   head_prob_kernel     the GEMM H W^T in 256 x 256 tiles, P and the tiles' row sums from its accumulators
 //   head_stat_kernel     l, nll, the rows' scales; P_my = -l
-//   head_dh_kernel       the GEMM P W, W read down its rows
 //   head_dw_kernel       the GEMM P^T (scale H), both operands read down their rows
-//   head_loss_kernel     the weighted sum in fp64
+//   head_dh_kernel       the GEMM P W, W read down its rows, in slices of the vocabulary where that fills the device better
+//   head_dh_sum_kernel   the slices' sum; the loss, a weighted sum in fp64
 // Rows are taken in pieces whose P fits a gigabyte. The number of counted rows is
 // known on the device only: the GEMMs plan their tiles there, from a grid for all rows.
 #include "common.h"
@@ -280,13 +280,7 @@ __global__ __launch_bounds__(kTgThreads, 1) void head_prob_kernel(TgArgs p, Prob
                                                                   int64_t N, int cus) {
   __shared__ __attribute__((aligned(1024))) uint16_t smem[kTgSmem];
   epi.rows = piece_rows(count, row0, epi.piece);
-  const TgPlan pl = tg_plan(epi.rows, N, 1, cus);
-  int64_t m0, n0;
-  int z;
-  if (!tg_where(pl, 1, (int)blockIdx.x, &m0, &n0, &z)) return;
-  using L = TgLayout<false, false, false, false>;
-  if (pl.half) tg_tile<128, L>(p, epi, m0, n0, smem, z);
-  else tg_tile<256, L>(p, epi, m0, n0, smem, z);
+  tg_run<TgLayout<false, false, false, false>>(p, epi, tg_plan(epi.rows, N, (int)(p.kmain / kTgK), 0, cus, (int)gridDim.x), smem);
 }
 
 // ---- statistics ----------------------------------------------------------------------------
@@ -305,12 +299,16 @@ struct StatArgs {
   uint16_t* P;             // nullptr: the loss alone
   float* scale;            // of the piece
   float* nll;              // by row
+  TgPlan* plan;            // of P W, made by the first workgroup; nullptr: no dH
+  int64_t K, most;         // its columns, its rows of partials at most
+  int nk, cus, grid;
 };
 
 __global__ __launch_bounds__(1024) void head_stat_kernel(StatArgs a) {
   __shared__ float s_d[16][64], s_l[16][64], s_top[64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t n = piece_rows(a.r.count, a.row0, a.piece), r0 = (int64_t)blockIdx.x * 64;
+  if (a.plan && r0 == 0 && tid == 1023) *a.plan = tg_plan(n, a.K, a.nk, a.most, a.cus, a.grid);
   if (r0 >= n) return;                              // uniform
   const bool in = r0 + lane < n;
   const int64_t row = in ? r0 + lane : n - 1;
@@ -398,19 +396,19 @@ __global__ __launch_bounds__(256) void head_scale_kernel(uint16_t* __restrict__ 
 
 // ---- gradients --------------------------------------------------------------------------------
 
-// dH rows, scaled, at their places; or, in reduction slices, fp32 partials [slices][piece][K].
+// dH rows, scaled, at their places; or, in reduction slices, fp32 partials [slices][n][K].
 struct DhEpi {
   const float* scale;      // of the piece
   const int32_t* rows;
   int64_t n, K, piece;
   uint16_t* dH;
-  float* part;
+  float* part;             // nullptr: one slice
   template <int MI>
   __device__ __forceinline__ void operator()(f32x16_t (&acc)[MI][2], int64_t m0, int64_t n0, int wm, int wn, int z,
                                              uint16_t* smem) const {
     const int lane = threadIdx.x & 63;
     if (part) {
-      tg_store_partial(acc, part + (int64_t)z * piece * K, n, K, m0, n0, wm, wn);
+      tg_store_partial(acc, part + (int64_t)z * n * K, n, K, m0, n0, wm, wn);
       return;
     }
     constexpr int kPitch = 64 + 8;
@@ -438,35 +436,90 @@ struct DhEpi {
   }
 };
 
-__global__ __launch_bounds__(kTgThreads, 1) void head_dh_kernel(TgArgs p, DhEpi epi, const int32_t* count, int64_t row0, int cus) {
+__global__ __launch_bounds__(kTgThreads, 1) void head_dh_kernel(TgArgs p, DhEpi epi, const int32_t* count, int64_t row0,
+                                                                const TgPlan* __restrict__ plan) {
   __shared__ __attribute__((aligned(1024))) uint16_t smem[kTgSmem];
   epi.n = piece_rows(count, row0, epi.piece);
-  const TgPlan pl = tg_plan(epi.n, epi.K, p.slices, cus);
-  int64_t m0, n0;
-  int z;
-  if (!tg_where(pl, p.slices, (int)blockIdx.x, &m0, &n0, &z)) return;
-  using L = TgLayout<false, true, false, false>;
-  if (pl.half) tg_tile<128, L>(p, epi, m0, n0, smem, z);
-  else tg_tile<256, L>(p, epi, m0, n0, smem, z);
+  const TgPlan pl = *plan;
+  if (pl.slices == 1) epi.part = nullptr;
+  tg_run<TgLayout<false, true, false, false>>(p, epi, pl, smem);
 }
 
-// dH from its slices, added in order.
-__global__ __launch_bounds__(256) void head_dh_sum_kernel(const float* __restrict__ part, int S, int64_t piece, int64_t K,
-                                                          const int32_t* count, int64_t row0, const float* __restrict__ scale,
-                                                          const int32_t* __restrict__ rows, uint16_t* __restrict__ dH) {
-  const int64_t n = piece_rows(count, row0, piece), per = K / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = i / per, k = (i - row * per) * 8;
-  if (row >= n) return;
-  f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
-  for (int z = 0; z < S; ++z) {
-    const float* q = part + ((int64_t)z * piece + row) * K + k;
-    a += *reinterpret_cast<const f32x4_t*>(q);
-    b += *reinterpret_cast<const f32x4_t*>(q + 4);
+// The weighted sum of the rows' losses, in fp64 and in a fixed order; the whole workgroup.
+struct LossArgs {
+  const float* nll;
+  const float* weights;
+  const int32_t* rows;
+  const int32_t* count;
+  float divisor;
+  float* loss;
+};
+
+__device__ __forceinline__ void head_loss_body(const LossArgs& a) {
+  __shared__ double red[4];
+  const int n = a.count[0], tid = threadIdx.x;
+  double s = 0.0;
+  for (int i = tid; i < n; i += 1024) {              // 4 rows' loads in flight
+    int32_t m[4];
+    float v[4], w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m[u] = a.rows[i + 256 * u < n ? i + 256 * u : i];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      v[u] = a.nll[m[u]];
+      w[u] = a.weights ? a.weights[m[u]] : 1.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + 256 * u < n) s += (double)v[u] * (double)w[u];
   }
-  const float s = scale[row];
-  *reinterpret_cast<u32x4_t*>(dH + (int64_t)rows[row] * K + k) =
-      u32x4_t{pack_bf16x2(s * a.x, s * a.y), pack_bf16x2(s * a.z, s * a.w), pack_bf16x2(s * b.x, s * b.y), pack_bf16x2(s * b.z, s * b.w)};
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  if ((tid & 63) == 0) red[tid >> 6] = s;
+  __syncthreads();
+  if (tid == 0) {
+    s = (red[0] + red[1]) + (red[2] + red[3]);
+    const double div = a.divisor != 0.0f ? (double)a.divisor : (double)(n > 0 ? n : 1);
+    a.loss[0] = (float)(s / div);
+  }
+}
+
+__global__ __launch_bounds__(256) void head_loss_kernel(LossArgs a) { head_loss_body(a); }
+
+// dH from its slices, added in order, 8 loads in flight; in the last piece, the last workgroup sums the loss.
+__global__ __launch_bounds__(256) void head_dh_sum_kernel(const float* __restrict__ part, const TgPlan* __restrict__ plan, int64_t piece,
+                                                          int64_t K, int64_t row0, const float* __restrict__ scale,
+                                                          const int32_t* __restrict__ rows, uint16_t* __restrict__ dH, LossArgs la) {
+  if (blockIdx.x == gridDim.x - 1) {
+    if (la.loss) head_loss_body(la);
+    return;
+  }
+  const int S = plan->slices;
+  if (S == 1) return;
+  const int64_t n = piece_rows(la.count, row0, piece), per = K / 8, step = n * K;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * per; i += (int64_t)(gridDim.x - 1) * 256) {
+    const int64_t row = i / per, k = (i - row * per) * 8;
+    const float* q = part + i * 8;
+    f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
+    for (int z = 0; z < S; z += 4) {
+      f32x4_t u[4], v[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float* o = q + (z + t < S ? z + t : z) * step;
+        u[t] = *reinterpret_cast<const f32x4_t*>(o);
+        v[t] = *reinterpret_cast<const f32x4_t*>(o + 4);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (z + t >= S) break;                       // uniform
+        a += u[t];
+        b += v[t];
+      }
+    }
+    const float s = scale[row];
+    *reinterpret_cast<u32x4_t*>(dH + (int64_t)rows[row] * K + k) = u32x4_t{
+        pack_bf16x2(s * a.x, s * a.y), pack_bf16x2(s * a.z, s * a.w), pack_bf16x2(s * b.x, s * b.y), pack_bf16x2(s * b.z, s * b.w)};
+  }
 }
 
 // dW tile, with the sum of the pieces before in E (fp32; nullptr: none), to fp32 or bf16.
@@ -523,35 +576,12 @@ __global__ __launch_bounds__(kTgThreads, 1) void head_dw_kernel(TgArgs p, DwEpi 
   p.kmain = (n + kTgK - 1) / kTgK * kTgK;           // P's rows up to there are zeros, H's repeat its last row
   p.krows_a = p.kmain > 0 ? p.kmain : 1;
   p.krows_b = n > 0 ? n : 1;
-  p.per_slice = (int)(p.kmain / kTgK);
-  int64_t m0, n0;
-  int z;
-  if (!tg_where(pl, 1, (int)blockIdx.x, &m0, &n0, &z)) return;
-  using L = TgLayout<true, true, false, false>;
-  if (pl.half) tg_tile<128, L>(p, epi, m0, n0, smem, z);
-  else tg_tile<256, L>(p, epi, m0, n0, smem, z);
+  pl.per_slice = (int)(p.kmain / kTgK);
+  tg_run<TgLayout<true, true, false, false>>(p, epi, pl, smem);
 }
 
-__global__ __launch_bounds__(1024) void head_loss_kernel(const float* __restrict__ nll, const float* __restrict__ weights,
-                                                         const int32_t* __restrict__ rows, const int32_t* __restrict__ count,
-                                                         float divisor, float* __restrict__ loss) {
-  __shared__ double red[16];
-  const int n = count[0], tid = threadIdx.x;
-  double s = 0.0;
-  for (int i = tid; i < n; i += 1024) {
-    const int32_t m = rows[i];
-    s += (double)nll[m] * (weights ? (double)weights[m] : 1.0);
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
-  if ((tid & 63) == 0) red[tid >> 6] = s;
-  __syncthreads();
-  if (tid == 0) {
-    s = 0.0;
-    for (int w = 0; w < 16; ++w) s += red[w];
-    const double div = divisor != 0.0f ? (double)divisor : (double)(n > 0 ? n : 1);
-    loss[0] = (float)(s / div);
-  }
+__global__ __launch_bounds__(256) void head_zero_kernel(uint32_t* __restrict__ p, int64_t words) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256) p[i] = 0u;
 }
 
 // Rows of a piece: P of at most 2^29 values, at least 256 rows.
@@ -560,6 +590,14 @@ int64_t head_piece(int64_t M, int64_t ldp) {
   if (most < 256) most = 256;
   const int64_t all = M > 256 ? hd_cdiv(M, 256) * 256 : 256;
   return all < most ? all : most;
+}
+
+// Rows of partials that dH's slices may take: those of the plan for all rows, and two slices of it at least, which
+// serve fewer counted rows (0: one slice always).
+int64_t head_partial_rows(int64_t rows, int64_t K, int64_t ldp) {
+  if (rows < 1) return 0;
+  const int64_t S = tg_plan(rows, K, (int)(ldp / kTgK), 16 * rows, device_cu_count()).slices;
+  return (S > 2 ? S : 2) * rows;
 }
 
 }  // namespace
@@ -578,8 +616,9 @@ HeadWorkspace head_workspace_layout(int64_t M, int64_t K, int64_t V, bool dH, bo
   L.stat_off = take(8 * hd_cdiv(V, kTgN) * L.piece);
   L.h_off = take(2 * M * K);
   L.p_off = take(2 * L.piece * ldp);
-  const int S = dH ? tg_slices(L.piece < M ? L.piece : M, K, ldp / kTgK, device_cu_count()) : 1;
-  L.part_off = take(S > 1 ? 4 * (int64_t)S * L.piece * K : 0);
+  L.most = dH ? head_partial_rows(L.piece < M ? L.piece : M, K, ldp) : 0;
+  L.part_off = take(4 * L.most * K);
+  L.plan_off = take(sizeof(TgPlan));
   L.dw_off = take(dW && dw_bf16 && M > L.piece ? 4 * V * K : 0);
   L.total = off > 0 ? off : 256;
   return L;
@@ -603,6 +642,7 @@ hipError_t launch_head_loss(const HeadCall& c, hipStream_t stream) {
   uint16_t* P = reinterpret_cast<uint16_t*>(b + L.p_off);
   float* part = reinterpret_cast<float*>(b + L.part_off);
   float* dwsum = reinterpret_cast<float*>(b + L.dw_off);
+  TgPlan* plan = reinterpret_cast<TgPlan*>(b + L.plan_off);
   const int cus = device_cu_count();
   const bool grad = c.dH || c.dW;
 
@@ -617,56 +657,57 @@ hipError_t launch_head_loss(const HeadCall& c, hipStream_t stream) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int S = c.dH ? tg_slices(L.piece < M ? L.piece : M, K, ldp / kTgK, device_cu_count()) : 1;
   const HeadRows hr{rows, count, ref, logit, label};
-  for (int64_t r0 = 0; r0 < M || r0 == 0; r0 += L.piece) {
+  const LossArgs la{c.nll, c.weights, rows, count, c.divisor, c.loss};
+  for (int64_t r0 = 0; r0 < M; r0 += L.piece) {
     const int64_t most = M - r0 < L.piece ? M - r0 : L.piece;     // rows there may be
     const bool last = r0 + L.piece >= M;
-    if (most > 0) {
-      TgArgs p{};
-      p.A = {Hc + r0 * K, K, most};
-      p.B = {c.W, K, V};
-      p.kmain = K;
-      p.per_slice = (int)(K / kTgK);
-      p.slices = 1;
-      const ProbEpi pe{ref + r0, label + r0, 0, V, ldp, L.piece, P, sum, shift};
-      hipLaunchKernelGGL(head_prob_kernel, dim3((unsigned)tg_grid(most, V, 1)), dim3(kTgThreads), 0, stream, p, pe, count, r0, V, cus);
-      const StatArgs sa{sum, shift, (int)tiles, r0, L.piece, ldp, hr, c.weights, c.divisor, c.grad_scale, grad ? P : nullptr,
-                        scale, c.nll};
-      hipLaunchKernelGGL(head_stat_kernel, dim3((unsigned)hd_cdiv(most, 64)), dim3(1024), 0, stream, sa);
-      if (c.dW)
-        hipLaunchKernelGGL(head_scale_kernel, dim3((unsigned)hd_cdiv(most * K / 8, 256)), dim3(256), 0, stream, Hc + r0 * K, scale,
-                           count, r0, L.piece, K);
-    }
-    if (c.dH && most > 0) {
-      TgArgs p{};
-      p.A = {P, ldp, L.piece};
-      p.B = {c.W, K, K};
-      p.kmain = ldp;
-      p.krows_b = V;
-      p.per_slice = (int)hd_cdiv(ldp / kTgK, S);
-      p.slices = S;
-      const DhEpi de{scale, rows + r0, 0, K, L.piece, c.dH, S > 1 ? part : nullptr};
-      hipLaunchKernelGGL(head_dh_kernel, dim3((unsigned)tg_grid(most, K, S)), dim3(kTgThreads), 0, stream, p, de, count, r0, cus);
-      if (S > 1)
-        hipLaunchKernelGGL(head_dh_sum_kernel, dim3((unsigned)hd_cdiv(most * K / 8, 256)), dim3(256), 0, stream, part, S, L.piece, K,
-                           count, r0, scale, rows + r0, c.dH);
-    }
+    TgArgs p{};
+    p.A = {Hc + r0 * K, K, most};
+    p.B = {c.W, K, V};
+    p.kmain = K;
+    const ProbEpi pe{ref + r0, label + r0, 0, V, ldp, L.piece, P, sum, shift};
+    hipLaunchKernelGGL(head_prob_kernel, dim3((unsigned)tg_grid(most, V, (int)(K / kTgK), 0, cus)), dim3(kTgThreads), 0, stream, p, pe,
+                       count, r0, V, cus);
+    const int grid = tg_grid(most, K, (int)(ldp / kTgK), L.most, cus);
+    const StatArgs sa{sum, shift, (int)tiles, r0, L.piece, ldp, hr, c.weights, c.divisor, c.grad_scale, grad ? P : nullptr,
+                      scale, c.nll, c.dH ? plan : nullptr, K, L.most, (int)(ldp / kTgK), cus, grid};
+    hipLaunchKernelGGL(head_stat_kernel, dim3((unsigned)hd_cdiv(most, 64)), dim3(1024), 0, stream, sa);
     if (c.dW) {
-      TgArgs p{};
-      p.A = {P, ldp, ldp};
-      p.B = {Hc + r0 * K, K, K};
-      p.slices = 1;
-      const TgPlan pl = tg_plan(V, K, 1, cus);
+      hipLaunchKernelGGL(head_scale_kernel, dim3((unsigned)hd_cdiv(most * K / 8, 256)), dim3(256), 0, stream, Hc + r0 * K, scale,
+                         count, r0, L.piece, K);
+      TgArgs q{};
+      q.A = {P, ldp, ldp};
+      q.B = {Hc + r0 * K, K, K};
+      const TgPlan pl = tg_plan(V, K, (int)hd_cdiv(most, kTgK), 0, cus);
       float* f32 = c.dw_bf16 ? dwsum : static_cast<float*>(c.dW);
       const DwEpi we{r0 > 0 ? f32 : nullptr, last ? c.dW : f32, last && c.dw_bf16, V, K};
-      hipLaunchKernelGGL(head_dw_kernel, dim3((unsigned)(pl.tiles_m * pl.tiles_n)), dim3(kTgThreads), 0, stream, p, we, pl, count, r0,
+      hipLaunchKernelGGL(head_dw_kernel, dim3((unsigned)(pl.tiles_m * pl.tiles_n)), dim3(kTgThreads), 0, stream, q, we, pl, count, r0,
                          L.piece);
+    }
+    if (c.dH) {
+      TgArgs q{};
+      q.A = {P, ldp, L.piece};
+      q.B = {c.W, K, K};
+      q.kmain = ldp;
+      q.krows_b = V;
+      const DhEpi de{scale, rows + r0, 0, K, L.piece, c.dH, part};
+      hipLaunchKernelGGL(head_dh_kernel, dim3((unsigned)grid), dim3(kTgThreads), 0, stream, q, de, count, r0, plan);
+      LossArgs end = la;
+      if (!last) end.loss = nullptr;
+      int64_t blocks = hd_cdiv(most * K / 8, 256);
+      if (blocks > 8 * cus) blocks = 8 * cus;
+      hipLaunchKernelGGL(head_dh_sum_kernel, dim3((unsigned)blocks + 1), dim3(256), 0, stream, part, plan, L.piece, K, r0, scale,
+                         rows + r0, c.dH, end);
     }
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(head_loss_kernel, dim3(1), dim3(1024), 0, stream, c.nll, c.weights, rows, count, c.divisor, c.loss);
+  if (c.dW && M == 0) {
+    const int64_t words = V * K / (c.dw_bf16 ? 2 : 1);
+    hipLaunchKernelGGL(head_zero_kernel, dim3((unsigned)(4 * cus)), dim3(256), 0, stream, static_cast<uint32_t*>(c.dW), words);
+  }
+  if (!c.dH || M == 0) hipLaunchKernelGGL(head_loss_kernel, dim3(1), dim3(256), 0, stream, la);
   return hipGetLastError();
 }
 

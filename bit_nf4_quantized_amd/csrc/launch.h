@@ -584,7 +584,8 @@ hipError_t launch_norm_bwd(const NormBwd& c, hipStream_t stream);
 // The loss over the vocabulary (head.hip).
 struct HeadWorkspace {
   int64_t piece;            // rows whose probabilities are held at once
-  size_t rows_off, count_off, ref_off, label_off, scale_off, stat_off, h_off, p_off, part_off, dw_off;
+  int64_t most;             // rows of dH's partials
+  size_t rows_off, count_off, ref_off, label_off, scale_off, stat_off, h_off, p_off, part_off, plan_off, dw_off;
   size_t total;
 };
 constexpr int64_t kHeadMaxVocab = (int64_t)1 << 22;

@@ -13,6 +13,7 @@
 // Sums are fp32 in a fixed order; dw is summed per workgroup over its rows, then
 // over the workgroups.
 #include "common.h"
+#include "int8.h"
 #include "launch.h"
 
 #include <type_traits>
@@ -115,21 +116,7 @@ __global__ __launch_bounds__(NormShape<WAVES>::kThreads) void norm_fwd_kernel(No
       for (int e = 0; e < 8; ++e) y[e] = h[i][e] * rstd;
     }
     if (c.y) nm_store(c.y, true, base + k, y);
-    if (c.codes) {                                 // K % 64 == 0: the 8 lanes of a block agree
-      float m = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = __builtin_fmaxf(m, __builtin_fabsf(y[e]));
-      m = wave_max(m, 8);
-      const float q = m < 0x1p-120f ? 0.0f : 127.0f / m;
-      uint32_t b[2] = {0u, 0u};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(y[e] * q), -127.0f), 127.0f);
-        b[e >> 2] |= ((uint32_t)((int32_t)x) & 0xFFu) << (8 * (e & 3));
-      }
-      *reinterpret_cast<u32x2_t*>(c.codes + base + k) = u32x2_t{b[0], b[1]};
-      if ((t & 7) == 0) c.absmax[(base + k) >> 6] = m;
-    }
+    if (c.codes) store_int8(y, c.codes, c.absmax, base + k);   // K % 64 == 0: the 8 lanes of a block agree
   }
 }
 

@@ -45,7 +45,7 @@ struct TgArgs {
   TgOperand A, B, A2, B2;
   int64_t kmain, kslab;        // reductions, multiples of 64 (kslab 0: none)
   int64_t krows_a, krows_b;    // k-major operands: rows that exist (the last one stands for those past it)
-  int per_slice, slices;       // stages per reduction slice
+  int per_slice;               // stages per reduction slice
 };
 
 // The operands' layouts and what a stage means.
@@ -330,43 +330,47 @@ __device__ __forceinline__ void tg_tile(const TgArgs& p, const E& epi, int64_t m
   epi.template operator()<MI>(acc, m0, n0, wm, wn, z, smem);
 }
 
-// How a launch's tiles cover M x N on `cus` compute units, one workgroup each at a time: tiles of 256 or 128 rows,
-// whichever ends sooner. A stage of a half-height tile took 1.0 us beside 1.65 of a full one (P W of 6144 rows, H W^T
-// of 6144 rows); both choices where they matter: P W of 777 rows 264 us in half tiles, ? in full ones. Also used on the
-// device, where M may be known there only.
-constexpr int kTgFullCost = 165, kTgHalfCost = 105;
+// How a launch's tiles cover M x N on `cus` compute units, one workgroup each at a time: tiles of 256 or 128 rows and
+// slices of the reduction of nk stages, whichever end soonest. A stage of a half-height tile took 1.0 us beside 1.65 of
+// a full one (products of 6144 rows). Slices' partials are written and read once (S M N 8 bytes at 4.5 TB/s) and take
+// one launch more; at least 8 stages each, at most 16, and M S at most `most` rows of partials. P W of 777 rows, 4096
+// columns, 501 stages: half tiles in 2 slices 264 us, full ones in 4 214. In fp32 arithmetic, on the host or the device
+// (where M may be known there only: then of the choices that `grid` workgroups hold; whole tiles without slices have to
+// be one).
+constexpr float kTgFullCost = 1.65f, kTgHalfCost = 1.05f;
 
 struct TgPlan {
   int tiles_m, tiles_n, half;     // half: tiles of 128 rows
+  int slices, per_slice;
 };
 
-__host__ __device__ inline int64_t tg_rounds(int64_t M, int64_t N, int rows, int slices, int cus) {
-  return ((M + rows - 1) / rows * ((N + kTgN - 1) / kTgN) * slices + cus - 1) / cus;
-}
-
-__host__ __device__ inline TgPlan tg_plan(int64_t M, int64_t N, int slices, int cus) {
-  const int tn = (int)((N + kTgN - 1) / kTgN), t1 = (int)((M + 255) / 256), t2 = (int)((M + 127) / 128);
-  const bool half = kTgFullCost * tg_rounds(M, N, 256, slices, cus) > kTgHalfCost * tg_rounds(M, N, 128, slices, cus);
-  return TgPlan{half ? t2 : t1, tn, half ? 1 : 0};
-}
-
-// Slices of the reduction (nk stages): what ends soonest by the stages' times above, the partials written and read
-// once (S M N 8 bytes at 4.5 TB/s) and one launch more; of at least 8 stages, at most 16.
-inline int tg_slices(int64_t M, int64_t N, int64_t nk, int cus) {
-  if (M < 1) return 1;
-  int best = 1;
-  double least = 0.0;
-  for (int S = 1; S <= 16 && (S == 1 || nk / S >= 8); ++S) {
-    const int64_t per = (nk + S - 1) / S;
-    if ((nk + per - 1) / per != S) continue;         // a slice would be empty
-    const double full = 0.01 * kTgFullCost * tg_rounds(M, N, 256, S, cus), half = 0.01 * kTgHalfCost * tg_rounds(M, N, 128, S, cus);
-    const double t = per * (full < half ? full : half) + (S > 1 ? 3.0 + 8e-6 / 4.5 * S * M * N : 0.0);
-    if (S == 1 || t < least) {
-      best = S;
+__host__ __device__ inline TgPlan tg_plan(int64_t M, int64_t N, int nk, int64_t most, int cus, int grid = 0x7FFFFFFF) {
+  const int t1 = (int)((M + 255) / 256), t2 = (int)((M + 127) / 128), tn = (int)((N + kTgN - 1) / kTgN);
+  TgPlan best{t1, tn, 0, 1, nk};
+  float least = 3e38f;
+  const float f1 = (float)t1 * tn / cus, f2 = (float)t2 * tn / cus, join = 8e-6f / 4.5f * M * N;
+  for (int S = 1; S <= 16; ++S) {
+    if (S > 1 && (nk < 8 * S || S * M > most)) break;
+    const int per = (nk + S - 1) / S;
+    if (S > 1 && (nk + per - 1) / per != S) continue;    // a slice would be empty
+    const float full = (float)t1 * tn * S <= grid ? kTgFullCost * __builtin_ceilf(f1 * S) : 3e38f;
+    const float half = (float)t2 * tn * S <= grid ? kTgHalfCost * __builtin_ceilf(f2 * S) : 3e38f;
+    const float t = per * (full < half ? full : half) + (S > 1 ? 3.0f + join * S : 0.0f);
+    if (t < least) {
       least = t;
+      best = half < full ? TgPlan{t2, tn, 1, S, per} : TgPlan{t1, tn, 0, S, per};
     }
   }
   return best;
+}
+
+// A grid for plans of any M' <= M that are made on the device: that of M itself, and three rounds where slices or
+// half-height tiles can use them.
+inline int tg_grid(int64_t M, int64_t N, int nk, int64_t most, int cus) {
+  const TgPlan p = tg_plan(M, N, nk, most, cus);
+  const int64_t n = (int64_t)p.tiles_m * p.tiles_n * p.slices;
+  const int64_t all = ((M + 127) / 128) * p.tiles_n * (most > 0 ? 16 : 1), more = all < 3 * cus ? all : 3 * cus;
+  return (int)(n > more ? n : more);
 }
 
 // fp32 partials of a tile, straight from the accumulators (128-byte rows per half wave).
@@ -388,16 +392,11 @@ __device__ __forceinline__ void tg_store_partial(f32x16_t (&acc)[MI][2], float* 
     }
 }
 
-// Workgroups that cover either choice for any M' <= M.
-inline int64_t tg_grid(int64_t M, int64_t N, int slices) {
-  return ((M + 127) / 128) * ((N + kTgN - 1) / kTgN) * slices;
-}
-
 // Tile and slice of workgroup bid: each of the 8 XCDs (bid % 8) takes a contiguous
 // range of the tiles, ordered in groups of 4 tile-rows, so that concurrent tiles
 // share rows of A and columns of B in one L2.
-__device__ __forceinline__ bool tg_where(const TgPlan& pl, int slices, int bid, int64_t* m0, int64_t* n0, int* z) {
-  const int per = pl.tiles_m * pl.tiles_n, n = per * slices;
+__device__ __forceinline__ bool tg_where(const TgPlan& pl, int bid, int64_t* m0, int64_t* n0, int* z) {
+  const int per = pl.tiles_m * pl.tiles_n, n = per * pl.slices;
   if (bid >= n) return false;
   const int xcd = bid % 8, q = n / 8, rem = n % 8;
   const int w = xcd * q + (xcd < rem ? xcd : rem) + bid / 8;
@@ -409,6 +408,17 @@ __device__ __forceinline__ bool tg_where(const TgPlan& pl, int slices, int bid, 
   *m0 = (int64_t)(first + tl % gm) * (pl.half ? 128 : 256);
   *n0 = (int64_t)(tl / gm) * kTgN;
   return true;
+}
+
+// The workgroup's tile of a plan.
+template <class L, class E>
+__device__ __forceinline__ void tg_run(TgArgs& p, const E& epi, const TgPlan& pl, uint16_t* smem) {
+  p.per_slice = pl.per_slice;
+  int64_t m0, n0;
+  int z;
+  if (!tg_where(pl, (int)blockIdx.x, &m0, &n0, &z)) return;
+  if (pl.half) tg_tile<128, L>(p, epi, m0, n0, smem, z);
+  else tg_tile<256, L>(p, epi, m0, n0, smem, z);
 }
 
 }  // namespace qlora

@@ -280,7 +280,7 @@ __global__ __launch_bounds__(kTgThreads, 1) void head_prob_kernel(TgArgs p, Prob
                                                                   int64_t N, int cus) {
   __shared__ __attribute__((aligned(1024))) uint16_t smem[kTgSmem];
   epi.rows = piece_rows(count, row0, epi.piece);
-  tg_run<TgLayout<false, false, false, false>>(p, epi, tg_plan(epi.rows, N, (int)(p.kmain / kTgK), 0, cus, (int)gridDim.x), smem);
+  tg_run<TgLayout<false, false, false, false>>(p, epi, tg_plan1(epi.rows, N, (int)(p.kmain / kTgK), cus, (int)gridDim.x), smem);
 }
 
 // ---- statistics ----------------------------------------------------------------------------

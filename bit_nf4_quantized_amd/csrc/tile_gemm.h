@@ -364,6 +364,14 @@ __host__ __device__ inline TgPlan tg_plan(int64_t M, int64_t N, int nk, int64_t 
   return best;
 }
 
+// The same without slices, in a few integer operations: every workgroup of a product makes it for itself.
+__host__ __device__ inline TgPlan tg_plan1(int64_t M, int64_t N, int nk, int cus, int grid = 0x7FFFFFFF) {
+  const uint32_t t1 = (uint32_t)((M + 255) / 256), t2 = (uint32_t)((M + 127) / 128), tn = (uint32_t)((N + kTgN - 1) / kTgN);
+  const uint32_t full = (t1 * tn + cus - 1) / cus, half = (t2 * tn + cus - 1) / cus;
+  const bool h = 165 * full > 105 * half && t2 * tn <= (uint32_t)grid;
+  return TgPlan{(int)(h ? t2 : t1), (int)tn, h ? 1 : 0, 1, nk};
+}
+
 // A grid for plans of any M' <= M that are made on the device: that of M itself, and three rounds where slices or
 // half-height tiles can use them.
 inline int tg_grid(int64_t M, int64_t N, int nk, int64_t most, int cus) {

@@ -379,6 +379,7 @@ LayerWorkspace gated_workspace_layout(int64_t M, int64_t K, int64_t F, int r, bo
   L.t_off = take(bwd ? 2 * M * r * 2 : 0);
   L.dy_off = take(bwd ? M * 2 * Fp * 2 : 0);
   L.x_off = take(bwd ? M * K * 2 : 0);
+  L.xs_off = take(bwd ? gd_cdiv(M, 64) * K * 4 : 0);
   int64_t part = (int64_t)adapter_partial_bytes(AdapterShape{2, M, K, Fp, r, 0.0f});
   if (2 * (int64_t)gemv1_partial_bytes(K, r) > part) part = 2 * gemv1_partial_bytes(K, r);
   L.part_off = take(part);
@@ -402,6 +403,7 @@ LayerWorkspace linear_int8_workspace_layout(int64_t M, int64_t K, int64_t N, int
   L.t_off = take(M * r * 2);
   L.dy_off = take(Np != N ? M * Np * 2 : 0);
   L.x_off = take(M * K * 2);
+  L.xs_off = take(gd_cdiv(M, 64) * K * 4);
   L.part_off = take((int64_t)adapter_partial_bytes(AdapterShape{1, M, K, Np, r, 0.0f}));
   const int64_t S = dx_plan(M, K, Np + rp).slices;
   L.part2_off = take(S > 1 ? S * M * K * 4 : 0);
@@ -413,7 +415,7 @@ namespace {
 
 struct LayerBuffers {
   uint16_t *wd, *l1t, *l2i, *l2p, *st, *t, *dy, *x;
-  float *part, *part2;
+  float *xs, *part, *part2;
   LayerBuffers(const LayerWorkspace& L, void* ws) {
     char* b = static_cast<char*>(ws);
     auto at = [&](size_t off) { return reinterpret_cast<uint16_t*>(b + off); };
@@ -425,6 +427,7 @@ struct LayerBuffers {
     t = at(L.t_off);
     dy = at(L.dy_off);
     x = at(L.x_off);
+    xs = reinterpret_cast<float*>(b + L.xs_off);
     part = reinterpret_cast<float*>(b + L.part_off);
     part2 = reinterpret_cast<float*>(b + L.part2_off);
   }
@@ -446,6 +449,13 @@ LayerPrep gated_prep(const GatedBase& W, int64_t M, const uint16_t* L1, const ui
   p.L1 = L1;
   p.L2 = L2;
   return p;
+}
+
+// X as int8 values: dL1 reads them as they are (rank <= 64), the other products of X a bf16 copy.
+void lay_int8(LayerPrep& p, const LayerBuffers& b, const Int8Values& x8, bool products) {
+  p.x8 = x8;
+  p.xs = p.r <= 64 ? b.xs : nullptr;
+  p.x = products || p.r > 64 ? b.x : nullptr;
 }
 
 // The product of X with both weights and their adapters, into `epi`.
@@ -474,12 +484,12 @@ hipError_t by_act(int act, F1&& silu, F2&& gelu) { return act == kActSilu ? silu
 // n Np: s U (and T_out, where T is not there yet), dX with the weights read down their rows, the adapters' gradients
 // beside the sums of dX's slices.
 template <class L>
-hipError_t layer_grads(const LayerPrep& s, const LayerBuffers& b, const uint16_t* X, const uint16_t* dY, float scale,
+hipError_t layer_grads(const LayerPrep& s, const LayerBuffers& b, const uint16_t* X, const int8_t* x8, const uint16_t* dY, float scale,
                        const uint16_t* T, bool have_t, uint16_t* dX, void* dL1, void* dL2, bool grad_bf16,
                        hipStream_t stream) {
   const int64_t ldy = s.n * s.Np;
   const AdapterShape sh{s.n, s.M, s.K, s.N, s.r, scale};
-  const AdapterOperands o{X, s.L1, b.l1t, dY, ldy, s.Np, b.l2p, s.Np};
+  const AdapterOperands o{X, x8, b.xs, s.L1, b.l1t, dY, ldy, s.Np, b.l2p, s.Np};
   GD_TRY(adapter_up(sh, o, b.st, have_t ? nullptr : b.t, b.part, stream));
   SplitSum sum{b.part2, dX, s.M * s.K, 1};
   if (dX) {
@@ -537,7 +547,7 @@ hipError_t gated_forward(const GatedBase& W, const uint16_t* X, int64_t M, const
   p.l1t = b.l1t;
   p.l2i = b.l2i;
   GD_TRY(launch_layer_prep(p, stream));
-  GD_TRY(adapter_down(AdapterShape{2, M, K, F, r, s}, AdapterOperands{X, L1, b.l1t, nullptr, 0, 0, nullptr, 0}, b.st, T_out,
+  GD_TRY(adapter_down(AdapterShape{2, M, K, F, r, s}, AdapterOperands{X, nullptr, nullptr, L1, b.l1t, nullptr, 0, 0, nullptr, 0}, b.st, T_out,
                       b.part, stream));
   if (gate8)
     return by_act(
@@ -561,14 +571,13 @@ hipError_t gated_backward(const GatedBase& W, const uint16_t* X, const Int8Value
   p.l2i = gate8 ? nullptr : b.l2i;
   p.l2p = b.l2p;
   if (X8) {
-    p.x8 = *X8;
-    p.x = b.x;
+    lay_int8(p, b, *X8, !gate8 || !T);
     X = b.x;
   }
   GD_TRY(launch_layer_prep(p, stream));
   bool have_t = T != nullptr;
   if (!gate8) {
-    GD_TRY(adapter_down(AdapterShape{2, M, K, F, r, s}, AdapterOperands{X, L1, b.l1t, nullptr, 0, 0, nullptr, 0}, b.st,
+    GD_TRY(adapter_down(AdapterShape{2, M, K, F, r, s}, AdapterOperands{X, nullptr, nullptr, L1, b.l1t, nullptr, 0, 0, nullptr, 0}, b.st,
                         T ? nullptr : b.t, b.part, stream));
     GD_TRY(by_act(
         act, [&] { return gated_product(b, X, p, GatedBwdEpi<kActSilu>{dA, b.dy, M, F, p.Np}, stream); },
@@ -586,7 +595,7 @@ hipError_t gated_backward(const GatedBase& W, const uint16_t* X, const Int8Value
       hipLaunchKernelGGL(gated_dgu_kernel<kActGelu>, dim3((unsigned)blocks), dim3(256), 0, stream, dA, *gate8, *up8, M, F, b.dy);
     GD_TRY(hipGetLastError());
   }
-  return layer_grads<RowPaired>(p, b, X, b.dy, s, T, have_t, dX, dL1, dL2, grad_bf16, stream);
+  return layer_grads<RowPaired>(p, b, X, p.xs ? X8->codes : nullptr, b.dy, s, T, have_t, dX, dL1, dL2, grad_bf16, stream);
 }
 
 hipError_t linear_backward_int8(const NF4View& W, const NF4Table& tab, const Int8Values& X8, const uint16_t* dY, int64_t M,
@@ -610,15 +619,14 @@ hipError_t linear_backward_int8(const NF4View& W, const NF4Table& tab, const Int
   p.L2 = L2;
   p.l1t = b.l1t;
   p.l2p = b.l2p;
-  p.x8 = X8;
-  p.x = b.x;
+  lay_int8(p, b, X8, !T);
   if (p.Np != N) {
     p.dy = dY;
     p.dyp = b.dy;
     dY = b.dy;
   }
   GD_TRY(launch_layer_prep(p, stream));
-  return layer_grads<RowDown>(p, b, b.x, dY, s, T, T != nullptr, dX, dL1, dL2, grad_bf16, stream);
+  return layer_grads<RowDown>(p, b, b.x, p.xs ? X8.codes : nullptr, dY, s, T, T != nullptr, dX, dL1, dL2, grad_bf16, stream);
 }
 
 }  // namespace qlora

@@ -893,8 +893,8 @@ hipError_t adapter_grads(const AdapterShape& a, const AdapterOperands& o, const 
   const int64_t rp = cdiv(a.r, 64) * 64, pitch = a.n * rp, r = a.r;
   if (r <= 64) {
     const SkinnyTn j[2] = {
-        SkinnyTn{o.X, a.K, a.K, sU, pitch, a.M, a.r, 1.0f, false, grad_bf16, dL1, SkinnyBatch{a.n, 0, rp, a.K * r, 0}},
-        SkinnyTn{o.dY, o.ldy, a.N, T, r, a.M, a.r, a.s, true, grad_bf16, dL2, SkinnyBatch{a.n, o.y_step, a.M * r, r * a.N, 0}}};
+        SkinnyTn{o.X, a.K, a.K, sU, pitch, a.M, a.r, 1.0f, false, grad_bf16, dL1, SkinnyBatch{a.n, 0, rp, a.K * r, 0}, o.x8, o.xs},
+        SkinnyTn{o.dY, o.ldy, a.N, T, r, a.M, a.r, a.s, true, grad_bf16, dL2, SkinnyBatch{a.n, o.y_step, a.M * r, r * a.N, 0}, nullptr, nullptr}};
     return skinny_tn_jobs(j, 2, part, split, stream);
   }
   if (split) {

@@ -260,6 +260,8 @@ struct SkinnyTn {          // out [W][r] (transposed: [r][W]) = alpha L^T S
   bool transpose, out_bf16;
   void* out;
   SkinnyBatch batch;
+  const int8_t* L8;        // jobs[0]: L as int8 codes [M][W] of blocks of 64 columns (or NULL), all products' one
+  const float* scales;     // RN32(absmax / 127) [W / 64][M rounded up to 64], finite behind M
 };
 hipError_t skinny_nt_jobs(const SkinnyNt* jobs, int n, float* part, hipStream_t stream);
 // split: another product's slices, added in the same launch as the sums (or NULL)
@@ -455,6 +457,8 @@ struct AdapterShape {
 };
 struct AdapterOperands {
   const uint16_t* X;        // [M][K]
+  const int8_t* x8;         // or for grads, rank <= 64: its int8 codes and scales (SkinnyTn)
+  const float* xs;
   const uint16_t* L1;       // [n][K][r]
   const uint16_t* l1t;      // [n][rp][K]: L1^T, zero rows behind the rank
   const uint16_t* dY;       // of adapter k at k y_step, rows ldy apart, readable up to column ldl
@@ -502,9 +506,10 @@ struct LayerPrep {
   uint16_t *l1t, *l2i, *l2p;
   Int8Values x8;
   uint16_t* x;
+  float* xs;
   const uint16_t* dy;
   uint16_t* dyp;
-  int blocks[5];             // set by the launch
+  int blocks[6];             // set by the launch
 };
 hipError_t launch_layer_prep(LayerPrep p, hipStream_t stream);
 
@@ -516,7 +521,8 @@ struct LayerWorkspace {
   size_t st_off;     // bf16 [M][n rp]: s T, or s U
   size_t t_off;      // bf16 [n][M][r]: T, when the caller has none
   size_t dy_off;     // bf16 [M][n Np]: dG, then dU; or dY of a ragged N
-  size_t x_off;      // bf16 [M][K]: X from its 8-bit values
+  size_t x_off;      // bf16 [M][K]: X from its 8-bit values (where a product needs that)
+  size_t xs_off;     // fp32 [K / 64][M rounded up to 64]: their scales
   size_t part_off;   // fp32 partials of the adapter products
   size_t part2_off;  // fp32 partials of dX's slices; few rows forward: of both base products
   size_t total;

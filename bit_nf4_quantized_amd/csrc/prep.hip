@@ -12,6 +12,7 @@
 //             at rp w, zeros elsewhere
 //             l2p [n][rp][Np] = L2, zeros behind rank and N
 //   x         int8 values -> bf16
+//   xs        their scales RN32(absmax / 127), [K / 64][M rounded up to 64], zeros behind M
 //   dY        [M][N] -> [M][Np], zeros behind N
 #include "common.h"
 #include "launch.h"
@@ -89,6 +90,7 @@ __device__ __forceinline__ void prep_l2(const LayerPrep& p, int id, uint16_t (*t
 __global__ __launch_bounds__(256) void layer_prep_kernel(LayerPrep p) {
   __shared__ float s_q[16];
   __shared__ uint16_t tile[32][33];
+  __shared__ float scale[64][65];
   int id = (int)blockIdx.x;
   if (id < p.blocks[0]) {                            // the longest part first
     const int per = p.blocks[0] / p.n;
@@ -114,8 +116,23 @@ __global__ __launch_bounds__(256) void layer_prep_kernel(LayerPrep p) {
   id -= p.blocks[2];
   if (id < p.blocks[3]) return prep_l2(p, id, tile);
   id -= p.blocks[3];
+  if (id < p.blocks[4]) {                            // read by blocks, written by rows, 64 x 64 through LDS
+    const int64_t nb = p.K / 64, mp = (p.M + 63) / 64 * 64, mt = mp / 64;
+    const int64_t m0 = (id % mt) * 64, b0 = (id / mt) * 64;
+    for (int i = threadIdx.x; i < 4096; i += 256) {
+      const int64_t m = m0 + (i >> 6), b = b0 + (i & 63);
+      scale[i >> 6][i & 63] = m < p.M && b < nb ? p.x8.absmax[m * nb + b] / 127.0f : 0.0f;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 4096; i += 256) {
+      const int64_t b = b0 + (i >> 6);
+      if (b < nb) p.xs[b * mp + m0 + (i & 63)] = scale[i & 63][i >> 6];
+    }
+    return;
+  }
+  id -= p.blocks[4];
   const int64_t per = p.Np / 8, n8 = p.M * per;
-  for (int64_t i = (int64_t)id * 256 + threadIdx.x; i < n8; i += (int64_t)p.blocks[4] * 256) {
+  for (int64_t i = (int64_t)id * 256 + threadIdx.x; i < n8; i += (int64_t)p.blocks[5] * 256) {
     const int64_t m = i / per, c = (i - m * per) * 8;   // N % 8 == 0
     u32x4_t v = {0u, 0u, 0u, 0u};
     if (c < p.N) v = *reinterpret_cast<const u32x4_t*>(p.dy + m * p.N + c);
@@ -135,7 +152,8 @@ hipError_t launch_layer_prep(LayerPrep p, hipStream_t stream) {
   p.blocks[1] = p.x ? blocks(p.M * p.K / 8, 8 * cus) : 0;
   p.blocks[2] = p.l1t ? p.n * (int)(p.K / 32) * (p.rp / 32) : 0;
   p.blocks[3] = p.l2i || p.l2p ? p.n * (int)(p.Np / 32) * (p.rp / 32) : 0;
-  p.blocks[4] = p.dyp ? blocks(p.M * p.Np / 8, 8 * cus) : 0;
+  p.blocks[4] = p.xs ? (int)((p.M + 63) / 64 * ((p.K / 64 + 63) / 64)) : 0;
+  p.blocks[5] = p.dyp ? blocks(p.M * p.Np / 8, 8 * cus) : 0;
   int64_t all = 0;
   for (int b : p.blocks) all += b;
   if (all == 0) return hipSuccess;

@@ -199,6 +199,9 @@ struct TnArgs {
   float c;
   uint64_t seed;
   int64_t l_step, s_step;  // product blockIdx.y of a batch, as in NtArgs (without DROP)
+  const int8_t* L8;        // INT8: L's codes [M][W] (W % 64 == 0) and their scales [W / 64][m_pad], finite up to m_pad
+  const float* scales;     // (M rounded up to 64)
+  int64_t m_pad;
 };
 
 template <bool DROP>
@@ -335,9 +338,20 @@ __device__ __forceinline__ tn_v4i16 tn_read_tr(const char* lds_byte) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) tn_v4i16*)(lds_void_t*)lds_byte);
 }
 
+// INT8: the large operand as int8 values of blocks of 64 columns. Its codes lie in
+// LDS as in memory (rows of 128 bytes); the transpose read of bytes
+// (ds_read_b64_tr_b8: lane j of 16 addresses row j / 2, columns 8 (j % 2) .. +8, and
+// receives column j of the 8 rows) gives a fragment's 8 codes of one column, which
+// are multiplied with their rows' scales and rounded to bf16 in registers: the
+// values of a dequantised copy, bit for bit, at half its bytes.
+typedef int tn_v2i32 __attribute__((ext_vector_type(2)));
+constexpr int kTn8S = SK * SM, kTn8Scale = kTn8S + SK * kTnSRow;   // offsets of S and of the scales in a stage
+static_assert(kTn8Scale + 1024 <= kTnStageBytes, "a stage of int8 values fits");
+__device__ __forceinline__ int tn_8swz(int m) { return ((m >> 1) & 3) << 1; }   // of the 16-byte chunk of row m
+
 // Column tile bx and slice bz of nz of product by.
-__device__ __forceinline__ void skinny_tn_body(TnArgs p, int bx, int by, int bz, int nz) {
-  __shared__ __attribute__((aligned(1024))) char ring[kTnStages * kTnStageBytes];
+template <bool INT8>
+__device__ __forceinline__ void skinny_tn_body(TnArgs p, char* ring, int bx, int by, int bz, int nz) {
   p.L += by * p.l_step;
   p.S += by * p.s_step;
   p.C += (int64_t)by * nz * p.W * SJ;
@@ -352,14 +366,30 @@ __device__ __forceinline__ void skinny_tn_body(TnArgs p, int bx, int by, int bz,
   // -> row 4 (4w + i) + lane / 16, chunk position lane % 16. S: instruction i
   // moves rows 8 (2w + i) .. +7, lane -> row 8 (2w + i) + lane / 8, position
   // lane % 8. The column parts of the source addresses are fixed per lane.
-  int64_t l_col[4], s_col[2];
+  // INT8: L instruction i moves rows 8 (2w + i) .. +7, lane -> row + lane / 8, chunk position lane % 8; every wave copies
+  // the stage's scales too (the same bytes), 64 floats of both 64-column blocks.
+  constexpr int kL = INT8 ? 2 : 4, kCopies = INT8 ? 5 : 6, kSAt = INT8 ? kTn8S : kTnLBytes;
+  int64_t l_col[kL], s_col[2];
   bool s_in[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 4 * (4 * wave + i) + (lane >> 4);
-    int64_t c = c0 + 8 * ((lane & 15) ^ tn_lswz(row));
-    if (c > p.W - 8) c = p.W - 8;  // W % 8 == 0
-    l_col[i] = c;
+  for (int i = 0; i < kL; ++i) {
+    if constexpr (INT8) {
+      const int row = 8 * (2 * wave + i) + (lane >> 3);
+      int64_t c = c0 + 16 * ((lane & 7) ^ tn_8swz(row));
+      if (c > p.W - 16) c = p.W - 16;
+      l_col[i] = c;
+    } else {
+      const int row = 4 * (4 * wave + i) + (lane >> 4);
+      int64_t c = c0 + 8 * ((lane & 15) ^ tn_lswz(row));
+      if (c > p.W - 8) c = p.W - 8;  // W % 8 == 0
+      l_col[i] = c;
+    }
+  }
+  const float* scale_at = nullptr;
+  if constexpr (INT8) {
+    int64_t blk = c0 / 64 + ((lane >> 4) & 1);
+    if (blk > p.W / 64 - 1) blk = p.W / 64 - 1;
+    scale_at = p.scales + blk * p.m_pad + 4 * (lane & 15);
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -372,22 +402,24 @@ __device__ __forceinline__ void skinny_tn_body(TnArgs p, int bx, int by, int bz,
     const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t*)lds);
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(src), "s"(m0) : "memory", "m0");
   };
-  auto issue = [&](int st) {  // the 6 copy instructions of this wave for stage st
+  auto issue = [&](int st) {  // the kCopies copy instructions of this wave for stage st
     const int64_t ms = mz0 + (int64_t)st * SK;
     char* buf = ring + (st % kTnStages) * kTnStageBytes;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 4 * (4 * wave + i) + (lane >> 4);
+    for (int i = 0; i < kL; ++i) {
+      const int row = INT8 ? 8 * (2 * wave + i) + (lane >> 3) : 4 * (4 * wave + i) + (lane >> 4);
       const int64_t m = ms + row;
-      const char* src = m < mz1 ? reinterpret_cast<const char*>(p.L + m * p.ldl + l_col[i]) : zero;
-      copy(src, buf + (4 * wave + i) * 1024);
+      const char* from = INT8 ? reinterpret_cast<const char*>(p.L8 + m * p.W + l_col[i])
+                              : reinterpret_cast<const char*>(p.L + m * p.ldl + l_col[i]);
+      copy(m < mz1 ? from : zero, buf + (kL * wave + i) * 1024);
     }
+    if constexpr (INT8) copy(reinterpret_cast<const char*>(scale_at + ms), buf + kTn8Scale);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int row = 8 * (2 * wave + i) + (lane >> 3);
       const int64_t m = ms + row;
       const char* src = (m < mz1 && s_in[i]) ? reinterpret_cast<const char*>(p.S + m * p.lds + s_col[i]) : zero;
-      copy(src, buf + kTnLBytes + (2 * wave + i) * 1024);
+      copy(src, buf + kSAt + (2 * wave + i) * 1024);
     }
   };
 
@@ -408,7 +440,7 @@ __device__ __forceinline__ void skinny_tn_body(TnArgs p, int bx, int by, int bz,
   auto loff = [&](int row) { return row * kTnLRow + ((((cl >> 3) ^ tn_lswz(row))) << 4) + ((cl & 7) << 1); };
   auto soff = [&](int row, int t) {
     const int c = 32 * t + cs;
-    return kTnLBytes + row * kTnSRow + (((c >> 3) ^ tn_sswz(row)) << 4) + ((c & 7) << 1);
+    return kSAt + row * kTnSRow + (((c >> 3) ^ tn_sswz(row)) << 4) + ((c & 7) << 1);
   };
 
 #pragma unroll
@@ -416,7 +448,7 @@ __device__ __forceinline__ void skinny_tn_body(TnArgs p, int bx, int by, int bz,
     if (st < ns) issue(st);
   for (int st = 0; st < ns; ++st) {
     // this wave's copies of stage st are complete (those of st + 1 may not be)
-    if (st + 1 < ns) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+    if (st + 1 < ns) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(kCopies) : "memory");
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();  // every wave's copies of stage st are visible; stage st-1's reads are done
     if (st + kTnStages - 1 < ns) issue(st + kTnStages - 1);  // into stage st-1's buffer
@@ -424,8 +456,26 @@ __device__ __forceinline__ void skinny_tn_body(TnArgs p, int bx, int by, int bz,
 #pragma unroll
     for (int kk = 0; kk < SK / 16; ++kk) {
       const int r0 = 16 * kk + rbase;
-      const tn_v4i16 a0 = tn_read_tr(buf + loff(r0)), a1 = tn_read_tr(buf + loff(r0 + 4));
-      const bf16x8_t a = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
+      bf16x8_t a;
+      if constexpr (INT8) {
+        const int m = 16 * kk + 8 * (lane >> 5), row = m + (jl >> 1);
+        const int c = 2 * wave + ((lane >> 4) & 1);
+        const char* at = buf + row * SM + ((c ^ tn_8swz(row)) << 4) + 8 * (jl & 1);
+        const tn_v2i32 q = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) tn_v2i32*)(lds_void_t*)at);
+        const f32x4_t* sc = reinterpret_cast<const f32x4_t*>(buf + kTn8Scale + 256 * (wave >> 1) + 4 * m);
+        const f32x4_t s0 = sc[0], s1 = sc[1];
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = (float)(int8_t)(q.x >> (8 * e)) * s0[e];
+          x[4 + e] = (float)(int8_t)(q.y >> (8 * e)) * s1[e];
+        }
+        a = __builtin_bit_cast(bf16x8_t, u32x4_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                                 pack_bf16x2(x[6], x[7])});
+      } else {
+        const tn_v4i16 a0 = tn_read_tr(buf + loff(r0)), a1 = tn_read_tr(buf + loff(r0 + 4));
+        a = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const tn_v4i16 b0 = tn_read_tr(buf + soff(r0, t)), b1 = tn_read_tr(buf + soff(r0 + 4, t));
@@ -447,15 +497,20 @@ __device__ __forceinline__ void skinny_tn_body(TnArgs p, int bx, int by, int bz,
 }
 
 __global__ __launch_bounds__(kSkThreads) void skinny_tn_dma_kernel(TnArgs p) {
-  skinny_tn_body(p, (int)blockIdx.x, 0, (int)blockIdx.z, (int)gridDim.z);
+  __shared__ __attribute__((aligned(1024))) char ring[kTnStages * kTnStageBytes];
+  skinny_tn_body<false>(p, ring, (int)blockIdx.x, 0, (int)blockIdx.z, (int)gridDim.z);
 }
 
+// FIRST8: the first job's large operand is int8 values.
+template <bool FIRST8>
 __global__ __launch_bounds__(kSkThreads) void skinny_tn_jobs_kernel(TnArgs a, TnArgs b, JobGrid ga, JobGrid gb) {
   const bool second = (int)blockIdx.x >= gb.first;
   const TnArgs& p = second ? b : a;
   const JobGrid& g = second ? gb : ga;
   const int id = (int)blockIdx.x - g.first, xy = g.x * g.y;
-  skinny_tn_body(p, id % g.x, id / g.x % g.y, id / xy, g.z);
+  __shared__ __attribute__((aligned(1024))) char ring[kTnStages * kTnStageBytes];
+  if (FIRST8 && !second) skinny_tn_body<true>(a, ring, id % g.x, id / g.x % g.y, id / xy, g.z);
+  else skinny_tn_body<false>(p, ring, id % g.x, id / g.x % g.y, id / xy, g.z);
 }
 
 // sum_z P[z slab .. +4], in order, 8 slices' loads in flight (one at a time, the
@@ -659,6 +714,7 @@ TnArgs tn_args(const SkinnyTn& j, const SkinnySplit& sp, float* part) {
   a.L = j.L; a.S = j.S; a.C = part; a.ldl = j.ldl; a.lds = j.lds; a.M = j.M; a.W = j.W; a.r = j.r; a.m_split = sp.len;
   a.c = 1.0f;
   a.l_step = j.batch.a_step; a.s_step = j.batch.b_step;
+  a.L8 = j.L8; a.scales = j.scales; a.m_pad = sk_cdiv(j.M, SK) * SK;
   return a;
 }
 
@@ -734,7 +790,10 @@ hipError_t skinny_tn_jobs(const SkinnyTn* jobs, int n, float* part, const SplitS
     b = tn_args(jb, sb, more);
     q = sum_job(tn_reduce(jb, sb, more), jb.transpose, jb.batch.n, p.g.end());
   }
-  hipLaunchKernelGGL(skinny_tn_jobs_kernel, dim3((unsigned)gb.end()), dim3(kSkThreads), 0, stream, a, b, ga, gb);
+  if (ja.L8)
+    hipLaunchKernelGGL(skinny_tn_jobs_kernel<true>, dim3((unsigned)gb.end()), dim3(kSkThreads), 0, stream, a, b, ga, gb);
+  else
+    hipLaunchKernelGGL(skinny_tn_jobs_kernel<false>, dim3((unsigned)gb.end()), dim3(kSkThreads), 0, stream, a, b, ga, gb);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   return launch_sums(p, q, split, stream);
@@ -767,7 +826,7 @@ hipError_t skinny_tn(const uint16_t* L, int64_t ldl, int64_t W, const uint16_t* 
                      float* part, float alpha, bool transpose, bool out_bf16, void* out, hipStream_t stream,
                      const DropoutParams* dr) {
   if (dr && (ldl != W || W % 64)) return hipErrorInvalidValue;  // the mask indexes a contiguous [M][W] input
-  const SkinnyTn j{L, ldl, W, S, lds, M, r, alpha, transpose, out_bf16, out, SkinnyBatch{1, 0, 0, 0, 0}};
+  const SkinnyTn j{L, ldl, W, S, lds, M, r, alpha, transpose, out_bf16, out, SkinnyBatch{1, 0, 0, 0, 0}, nullptr, nullptr};
   const SkinnySplit sp = dr ? skinny_split(sk_cdiv(W, SM), M, 0) : tn_split(j);
   TnArgs a = tn_args(j, sp, part);
   if (dr) {

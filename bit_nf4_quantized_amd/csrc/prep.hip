@@ -1,11 +1,11 @@
 // What the products of a layer's pass need beforehand, as one launch of
 // independent parts (each workgroup takes a piece of one part): apart, the parts
 // of a short batch were mostly launch latency (a linear's backward pass of 200
-// rows 101 -> ? us with this and the joined sums).
+// rows 101 -> 56 us with this and the joined sums).
 //
 //   weights   one or two quantised weights [N][K] -> bf16 rows; two of them in
 //             pairs of blocks of 32 rows (row n of weight w at 64 (n / 32) + 32 w
-//             + n % 32), rows N .. Np zeros. 2.5 B per weight: 90 M weights 50 us.
+//             + n % 32), rows N .. Np zeros. 2.5 B per weight: 90 M weights 52 us, 4.3 TB/s.
 //   adapters  32 x 32 tiles, transposed through LDS:
 //             l1t [n][rp][K] = L1^T, rows behind the rank zero
 //             l2i [2 Np][2 rp] = L2^T in the paired rows' order, weight w's columns
@@ -21,10 +21,10 @@ namespace qlora {
 
 namespace {
 
-__device__ __forceinline__ void prep_weights(const LayerPrep& p, int which, int block, int blocks, float* s_q) {
-  const NF4View& W = which ? p.W[1] : p.W[0];
-  if (threadIdx.x < 16) s_q[threadIdx.x] = which ? p.tab[1].q[threadIdx.x] : p.tab[0].q[threadIdx.x];
-  __syncthreads();
+// DQ: double-quantised constants (decided outside the loop: a branch per unit would wait for each unit's loads).
+template <bool DQ>
+__device__ __forceinline__ void prep_weights(const LayerPrep& p, const NF4View& W, int which, int block, int blocks,
+                                             const float* s_q) {
   const float mu = tensor_mean(W);
   const int64_t K8 = W.cols / 8, nunits = W.rows * K8, all = p.Np * K8;
   const uint32_t* codes = reinterpret_cast<const uint32_t*>(W.codes);
@@ -36,7 +36,9 @@ __device__ __forceinline__ void prep_weights(const LayerPrep& p, int which, int 
     for (int u = 0; u < kUnits; ++u) {
       const int64_t un = base + (int64_t)u * 256, uc = un < nunits ? un : nunits - 1;
       c[u] = codes[uc];
-      ap[u] = block_const(W, uc >> 3, mu);
+      const int64_t blk = uc >> 3;
+      if constexpr (DQ) ap[u] = block_scale(W.absmax8[blk], W.scale2[blk / kDqBlock], mu);
+      else ap[u] = W.absmax32[blk];
     }
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
@@ -94,7 +96,12 @@ __global__ __launch_bounds__(256) void layer_prep_kernel(LayerPrep p) {
   int id = (int)blockIdx.x;
   if (id < p.blocks[0]) {                            // the longest part first
     const int per = p.blocks[0] / p.n;
-    prep_weights(p, id / per, id % per, per, s_q);
+    const int which = id >= per ? 1 : 0;
+    const NF4View W = which ? p.W[1] : p.W[0];
+    if (threadIdx.x < 16) s_q[threadIdx.x] = which ? p.tab[1].q[threadIdx.x] : p.tab[0].q[threadIdx.x];
+    __syncthreads();
+    if (W.absmax32) prep_weights<false>(p, W, which, id - which * per, per, s_q);
+    else prep_weights<true>(p, W, which, id - which * per, per, s_q);
     return;
   }
   id -= p.blocks[0];

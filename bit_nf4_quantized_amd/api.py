@@ -1073,16 +1073,21 @@ def qlora_linear_multi_bwd(q: NF4Tensor, X, dY, row_adapter, L1, L2, scale, T=No
 # ---- the rest of a training step ----------------------------------------------------
 
 def _on_device(fn):
-    """Run a wrapper with the device of its first tensor argument as the current one (the kernels, the stream
+    """Run a wrapper with the device of its first argument, a tensor, as the current one (the kernels, the stream
     and the memory allocated here then belong to it); a ``stream`` has to be of that device."""
     import functools
+    import inspect
+
+    names = list(inspect.signature(fn).parameters)
+    at = names.index("stream")
 
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
         import torch
 
-        dev = next((a.get_device() for a in args if isinstance(a, torch.Tensor)), -1)
-        stream = kwargs.get("stream")
+        first = args[0] if args else kwargs.get(names[0])
+        dev = first.get_device() if isinstance(first, torch.Tensor) else -1
+        stream = args[at] if len(args) > at else kwargs.get("stream")
         if stream is not None and dev >= 0 and stream.device.index != dev:
             raise ValueError(f"stream must be of device {dev}, got {stream.device.index}")
         if dev < 0 or dev == torch.cuda.current_device():

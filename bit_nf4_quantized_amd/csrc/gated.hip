@@ -143,7 +143,7 @@ struct GatedBwdEpi {
         const float d = bf16_to_f32(eg[at]);
         float a, da;
         act_both<ACT>(acc[i][0][v], &a, &da);
-        // columns from F on: zeros, also where the weights' padding gave 0 / 0
+        // columns from F on: dA and the weights' padding are zeros
         eg[at] = f32_to_bf16(d * acc[i][1][v] * da);
         eu[at] = f32_to_bf16(d * a);
       }
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(const float* __restri
 namespace {
 
 TgPlan dx_plan(int64_t M, int64_t K, int64_t reduction) {
-  return tg_plan(M, K, (int)(reduction / kTgK), 16 * M, device_cu_count());
+  return tg_plan(M, K, (int)(reduction / kTgK), tg_partial_rows(M), device_cu_count());
 }
 
 }  // namespace
@@ -384,8 +384,7 @@ LayerWorkspace gated_workspace_layout(int64_t M, int64_t K, int64_t F, int r, bo
   if (2 * (int64_t)gemv1_partial_bytes(K, r) > part) part = 2 * gemv1_partial_bytes(K, r);
   L.part_off = take(part);
   const int64_t few = M < kMultiSmallRows ? M : kMultiSmallRows;
-  const int64_t S = bwd ? dx_plan(M, K, 2 * Fp + 2 * rp).slices : 1;
-  L.part2_off = take(bwd ? (S > 1 ? S * M * K * 4 : 0) : small_pair_partial_floats(few, K, F) * 4);
+  L.part2_off = take(bwd ? tg_partial_rows(M) * K * 4 : small_pair_partial_floats(few, K, F) * 4);
   L.total = off > 0 ? off : 256;
   return L;
 }
@@ -405,8 +404,7 @@ LayerWorkspace linear_int8_workspace_layout(int64_t M, int64_t K, int64_t N, int
   L.x_off = take(M * K * 2);
   L.xs_off = take(gd_cdiv(M, 64) * K * 4);
   L.part_off = take((int64_t)adapter_partial_bytes(AdapterShape{1, M, K, Np, r, 0.0f}));
-  const int64_t S = dx_plan(M, K, Np + rp).slices;
-  L.part2_off = take(S > 1 ? S * M * K * 4 : 0);
+  L.part2_off = take(tg_partial_rows(M) * K * 4);
   L.total = off > 0 ? off : 256;
   return L;
 }

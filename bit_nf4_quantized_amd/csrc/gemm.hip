@@ -801,18 +801,18 @@ hipError_t linear_backward(const NF4View& W, const NF4Table& tab, const uint16_t
 
 // ---- adapter products beside another kernel's product --------------------------------------
 
+// Bounds that never shrink as M grows: a workspace for M rows serves fewer.
 size_t adapter_partial_bytes(const AdapterShape& a) {
   const int64_t M = a.M, K = a.K, N = a.N, r = a.r;
-  const Split sT = choose_split(cdiv(M, BM) * cdiv(r, BN), K), sU = choose_split(cdiv(M, BM) * cdiv(r, BN), N);
-  const Split s1 = choose_split(cdiv(K, BM) * cdiv(r, BN), M), s2 = choose_split(cdiv(r, BM) * cdiv(N, BN), M);
-  int64_t part = 0;
+  auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
+  const int64_t rows = least(16 * M, 512 * BM + M);   // slices x rows: at most 512 / (M / BM) + 1 slices
+  const int64_t down = cdiv(M, BK) / 4 > 1 ? cdiv(M, BK) / 4 : 1;   // slices of a reduction over M
+  int64_t part = rows * r * 4;
   auto upd = [&](int64_t b) { part = b > part ? b : part; };
-  upd((int64_t)sT.Z * M * r * 4);
-  upd((int64_t)sU.Z * M * r * 4);
-  upd((int64_t)s1.Z * K * r * 4);
-  upd((int64_t)s2.Z * r * N * 4);
-  if (r <= 64) upd(2 * a.n * (int64_t)skinny_partial_bytes(M, K, N));   // two jobs
-  if (M <= kMidMaxM) upd(a.n * (int64_t)small_t_partial_bytes(M, K, (int)r));
+  upd(least(least(16, cdiv(512, cdiv(K, BM) * cdiv(r, BN))), down) * K * r * 4);
+  upd(least(least(16, cdiv(512, cdiv(r, BM) * cdiv(N, BN))), down) * r * N * 4);
+  if (r <= 64) upd(2 * a.n * (int64_t)skinny_partial_bound(M, K, N));   // two jobs
+  upd(a.n * (int64_t)small_t_partial_bytes(least(M, kMidMaxM), K, (int)r));
   return align_up((size_t)part, 256);
 }
 

@@ -222,6 +222,8 @@ struct SkinnySplit {
 };
 SkinnySplit skinny_split(int64_t tiles, int64_t klen, int64_t fit = 0);
 size_t skinny_partial_bytes(int64_t M, int64_t K, int64_t N);
+// At least that for every M' <= M.
+size_t skinny_partial_bound(int64_t M, int64_t K, int64_t N);
 // dr: A is the adapter input X ([M][K], lda == K), dropped in registers.
 hipError_t skinny_nt(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int64_t M, int64_t K, int r,
                      float* part, float alpha, uint16_t* out, int64_t ldo, float alpha2, uint16_t* out2,

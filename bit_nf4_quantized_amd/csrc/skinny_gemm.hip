@@ -689,6 +689,18 @@ size_t skinny_partial_bytes(int64_t M, int64_t K, int64_t N) {
   return m * SJ * sizeof(float);
 }
 
+size_t skinny_partial_bound(int64_t M, int64_t K, int64_t N) {
+  const int64_t fit = 2 * (int64_t)device_cu_count() > 512 ? 2 * (int64_t)device_cu_count() : 512;
+  auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
+  const int64_t steps = sk_cdiv(K > N ? K : N, SK);
+  int64_t rows = least(least(32, steps) * M, fit * SM + M);   // slices x rows: at most fit / (M / SM) + 1 slices
+  for (const int64_t W : {K, N}) {
+    const int64_t z = least(least(32, sk_cdiv(fit, sk_cdiv(W, SM))), sk_cdiv(M, SK));
+    if (z * W > rows) rows = z * W;
+  }
+  return (size_t)rows * SJ * sizeof(float);
+}
+
 namespace {
 
 NtArgs nt_args(const SkinnyNt& j, const SkinnySplit& sp, float* part) {

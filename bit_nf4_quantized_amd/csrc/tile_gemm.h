@@ -372,6 +372,13 @@ __host__ __device__ inline TgPlan tg_plan1(int64_t M, int64_t N, int nk, int cus
   return TgPlan{(int)(h ? t2 : t1), (int)tn, h ? 1 : 0, 1, nk};
 }
 
+// Rows of partials (slices times M) that a product of M rows may take: 16 slices of few rows, two of many, none of so
+// many that two whole slices would not run sooner. Never fewer for more rows: a workspace for M rows serves fewer.
+inline int64_t tg_partial_rows(int64_t M) {
+  const int64_t m = M < 32768 ? M : 32768, few = 16 * m < 8192 ? 16 * m : 8192;
+  return few > 2 * m ? few : 2 * m;
+}
+
 // A grid for plans of any M' <= M that are made on the device: that of M itself, and three rounds where slices or
 // half-height tiles can use them.
 inline int tg_grid(int64_t M, int64_t N, int nk, int64_t most, int cus) {

@@ -15,7 +15,7 @@
  * Activations in 8 bits ("int8 values") are those of qlora_int8_quantize with
  * blocks of 64: codes [numel] and one fp32 absmax per 64 consecutive values, of a
  * matrix whose rows are a multiple of 64 long. A value is code * RN32(absmax / 127).
- * M (rows) is at most QLORA_LAYER_MAX_ROWS, and may be 0.
+ * M (rows) is at most QLORA_LAYER_MAX_ROWS, and may be 0. A workspace for M rows serves fewer rows too.
  */
 #ifndef QLORA_LAYERS_H
 #define QLORA_LAYERS_H
@@ -78,7 +78,8 @@ int qlora_gated_bwd(const qlora_nf4 *gate, const qlora_nf4 *up, const uint16_t *
 
 /*
  * qlora_linear_bwd with X as int8 values [M][K]: dL1, and T where it is NULL, come from those values rounded to bf16;
- * dX does not depend on X. Arguments otherwise as there; ws: qlora_linear_bwd_int8_workspace(M, K, N, r) bytes.
+ * dX does not depend on X. Arguments otherwise as there, K and N below QLORA_GATED_MAX_COLS; ws:
+ * qlora_linear_bwd_int8_workspace(M, K, N, r) bytes.
  */
 int qlora_linear_bwd_int8_workspace(int64_t M, int64_t K, int64_t N, int r, size_t *bytes);
 int qlora_linear_bwd_int8(const qlora_nf4 *W, const qlora_int8_values *X8, const uint16_t *dY, int64_t M,

@@ -159,6 +159,20 @@ def test_gated_forward(api, M, K, F, r, kind):
         assert (c.fwd().A == o.A).all()            # keeping G and U does not change A
 
 
+@pytest.mark.parametrize("K,F,r", [(256, 11272, 64), (4096, 2056, 24), (1024, 24, 8), (512, 8, 16), (8192, 520, 64)])
+def test_gated_one_token(api, K, F, r):
+    """Few features, uneven shares of them, and more than one round of workgroups holds."""
+    c = Gated(api, 1, K, F, r)
+    o = c.fwd(want_T=True)
+    A, G, Uv, T = layers.gated_fwd(c.X, *c.W, c.L1, c.L2, c.s, c.kind)
+    ET, EG, EU = c.sums(linear.widen(c.X))
+    label = f"gated one token {K}x{F} r{r}"
+    for k in range(2):
+        within(label, f"T{k}", o.T[k], T[k], ET[k])
+    a, _, Ea, _ = act_errors(G, EG, c.kind)
+    within(label, "A", o.A, A, Ea * np.abs(Uv) + np.abs(a) * EU + Ea * EU + 2 * U * np.abs(A))
+
+
 @pytest.mark.parametrize("M,K,F,r", SHAPES)
 @pytest.mark.parametrize("keep", ["nothing", "T", "int8", "all8"])
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
@@ -455,6 +469,16 @@ def test_head_loss(api, M, K, V, dW):
     assert alone.dH is None and alone.dW is None and (alone.nll == o.nll).all() and (alone.loss == o.loss).all()
 
 
+@pytest.mark.parametrize("M,K,V,masked", [(2049, 64, 300, 0.0), (2500, 128, 700, 0.3), (3000, 64, 1000, 0.97), (2100, 128, 9000, 0.5),
+                                          (4200, 64, 9000, 0.9)])
+def test_head_many_rows(api, M, K, V, masked):
+    """Rows counted by one workgroup; fewer counted rows than the grids are for, dH in slices planned from their number."""
+    Hs, W, labels, rng = head_case(M, K, V)
+    labels[rng.random(M) < masked] = -100
+    o = api.qlora_head_loss(dev(Hs), dev(W), dev(labels), need_dW=True)
+    check_head(f"head {M}x{K}x{V} masked {masked}", o, Hs, W, labels)
+
+
 def test_head_no_counted_row(api):
     import torch
 
@@ -546,6 +570,159 @@ def test_head_pieces(api, dW):
         del logp, D, RW
 
 
+# ---- offsets that pass 32 bits ---------------------------------------------------------------------
+
+
+def rows_near(big, small, at, label):
+    """Rows of a large call beside a small call on them: the same products, in sums of another order, so every rounding to
+    bf16 (the adapters' operand, the outputs) may fall the other way: 2-norms within three of them."""
+    d = (big[at:at + small.shape[0]].double() - small.double()).norm()
+    assert d <= 3 * H * small.double().norm(), (label, at, float(d))
+
+
+PLACES = (0, 131000, (1 << 18) - 300)
+
+
+def normal(shape, seed, std=1.0, dtype=None):
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.empty(shape, dtype=dtype or torch.bfloat16, device="cuda").normal_(0, std, generator=g)
+
+
+def test_gated_long(api):
+    import torch
+
+    M, K, F, r, s = 1 << 18, 64, 8256, 8, 0.5
+    rng = np.random.default_rng(0)
+    q = [gpu_quantize(api, (rng.standard_normal((F, K)) / 8).astype(np.float32))[0] for _ in range(2)]
+    X, dA = normal((M, K), 1), normal((M, F), 2)
+    L1, L2 = normal((2, K, r), 3, 0.125), normal((2, r, F), 4, 0.5)
+    o = api.qlora_gated_fwd(*q, X, L1, L2, s, want_T=True, want_int8=True)
+    for at in PLACES:
+        m = slice(at, at + 300)
+        t = api.qlora_gated_fwd(*q, X[m], L1, L2, s, want_T=True, want_int8=True)
+        rows_near(o.A, t.A, at, "A")
+        rows_near(o.T[1], t.T[1], at, "T")
+        rows_near(o.up8[1].view(M, -1), t.up8[1].view(300, -1), at, "up8 absmax")
+        # codes are off by one where G is rounded the other way
+        assert (o.gate8[0].view(M, F)[m].int() - t.gate8[0].view(300, F).int()).abs().max() <= 1
+    full = api.qlora_gated_bwd(*q, X, dA, L1, L2, s)
+    kept = api.qlora_gated_bwd(*q, X, dA, L1, L2, s, T=o.T, gate8=o.gate8, up8=o.up8)
+    sums = [[torch.zeros_like(full[i], dtype=torch.float64) for i in (1, 2)] for _ in range(2)]
+    P = M // 8
+    for m in range(0, M, P):
+        g8, u8 = (tuple(v.view(M, -1)[m:m + P].reshape(-1) for v in w) for w in (o.gate8, o.up8))
+        for k, part in enumerate((api.qlora_gated_bwd(*q, X[m:m + P], dA[m:m + P], L1, L2, s),
+                                  api.qlora_gated_bwd(*q, X[m:m + P], dA[m:m + P], L1, L2, s, gate8=g8, up8=u8,
+                                                      T=o.T[:, m:m + P].contiguous()))):
+            rows_near((full, kept)[k][0], part[0], m, f"dX {k}")
+            for i in range(2):
+                sums[k][i] += part[1 + i].double()
+    for k, got in enumerate((full, kept)):
+        for i in range(2):
+            assert (got[1 + i].double() - sums[k][i]).norm() <= 3 * H * sums[k][i].norm(), (k, i)
+    del o, full, kept
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("K,N", [(64, 8200), (8256, 64)])
+def test_linear_bwd_int8_long(api, K, N):
+    import torch
+
+    M, r, s = 1 << 18, 8, 0.5
+    rng = np.random.default_rng(0)
+    q, _ = gpu_quantize(api, (rng.standard_normal((N, K)) / np.sqrt(K)).astype(np.float32))
+    X8 = api.qlora_int8_quantize(normal((M, K), 1))
+    dY, L1, L2 = normal((M, N), 2), normal((K, r), 3, K ** -0.5), normal((r, N), 4)
+    full = api.qlora_linear_bwd_int8(q, X8, dY, L1, L2, s)
+    sums = [torch.zeros_like(full[i], dtype=torch.float64) for i in (1, 2)]
+    P = M // 8
+    for m in range(0, M, P):
+        x8 = tuple(v.view(M, -1)[m:m + P].reshape(-1) for v in X8)
+        part = api.qlora_linear_bwd_int8(q, x8, dY[m:m + P], L1, L2, s)
+        rows_near(full[0], part[0], m, "dX")
+        for i in range(2):
+            sums[i] += part[1 + i].double()
+    for i in range(2):
+        assert (full[1 + i].double() - sums[i]).norm() <= 3 * H * sums[i].norm(), i
+    del X8, dY, full
+    torch.cuda.empty_cache()
+
+
+def test_norm_long(api):
+    """Rows do not depend on their number: the same bits."""
+    import torch
+
+    M, K = 1 << 18, 8256
+    x, res, w = normal((M, K), 1), normal((M, K), 2, dtype=torch.float32), normal((K,), 3)
+    o = api.qlora_norm_fwd(x, w, residual=res, want_int8=True)
+    g = api.qlora_norm_bwd(x, o.h, o.rstd, w, dres=res, want_dx16=True)
+    dw = torch.zeros(K, dtype=torch.float64, device="cuda")
+    for at in PLACES:
+        m = slice(at, at + 300)
+        t = api.qlora_norm_fwd(x[m], w, residual=res[m], want_int8=True)
+        b = api.qlora_norm_bwd(x[m], t.h, t.rstd, w, dres=res[m], want_dx16=True)
+        for big, small in ((o.y, t.y), (o.h, t.h), (o.rstd, t.rstd), (o.int8[0].view(M, K), t.int8[0].view(300, K)),
+                           (o.int8[1].view(M, -1), t.int8[1].view(300, -1)), (g.dh, b.dh), (g.dx16, b.dx16)):
+            assert (big[m] == small).all()
+    P = M // 8
+    for m in range(0, M, P):
+        dw += api.qlora_norm_bwd(x[m:m + P], o.h[m:m + P], o.rstd[m:m + P], w).dweight.double()
+    # a thread adds M / 1024 products, then the groups' sums are added: (M / 1024 + 1024) u of the magnitudes, whose sum
+    # is M E|dy||xh| < M against a result of about sqrt(M) per column
+    assert (g.dweight.double() - dw).abs().max() <= (M / 1024 + 1024) * U * M
+    del x, res, o, g
+    torch.cuda.empty_cache()
+
+
+def test_head_long_rows(api):
+    import torch
+
+    M, K, V = 1 << 18, 8256, 70
+    Hd, Wd = normal((M, K), 1), normal((V, K), 2, 0.02)
+    Ld = torch.randint(-20, V, (M,), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    o = api.qlora_head_loss(Hd, Wd, Ld, divisor=1.0, need_dW=True)
+    loss, dW = 0.0, torch.zeros(V, K, dtype=torch.float64, device="cuda")
+    P = M // 8
+    for m in range(0, M, P):
+        t = api.qlora_head_loss(Hd[m:m + P], Wd, Ld[m:m + P], divisor=1.0, need_dW=True)
+        rows_near(o.dH, t.dH, m, "dH")
+        # logits in the same order; the statistics' too
+        assert (o.nll[m:m + P] == t.nll).all()
+        loss += t.loss.item()
+        dW += t.dW.double()
+    assert abs(o.loss.item() - loss) <= 8 * U * abs(loss)
+    assert (o.dW.double() - dW).norm() <= 3 * H * dW.norm()
+    del Hd, o
+    torch.cuda.empty_cache()
+
+
+def test_head_long_vocabulary(api):
+    import torch
+
+    M, K, V = 130, 4160, 1 << 19
+    Hd, Wd = normal((M, K), 1), normal((V, K), 2, 0.02)
+    Ld = torch.randint(0, V, (M,), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    Ld[0], Ld[1] = V - 1, 0
+    o = api.qlora_head_loss(Hd, Wd, Ld, need_dW=True)
+    h, C = Hd.double(), 1 << 16
+    S = torch.cat([h @ Wd[v:v + C].double().t().contiguous() for v in range(0, V, C)], 1)
+    nll = torch.logsumexp(S, 1) - S[torch.arange(M), Ld]
+    # logits off by K u |H||W| < 4160 2^-24 4160 0.016, taken loosely; their mean over the vocabulary by far less
+    assert (o.nll.double() - nll).abs().max() < 1e-2
+    D = torch.softmax(S, 1)
+    D[torch.arange(M), Ld] -= 1.0
+    D /= M
+    dH = sum(D[:, v:v + C] @ Wd[v:v + C].double() for v in range(0, V, C))
+    assert (o.dH.double() - dH).norm() <= 3 * H * dH.norm()
+    for v in range(0, V, C):
+        R = D[:, v:v + C].t().contiguous() @ h
+        assert (o.dW[v:v + C].double() - R).norm() <= 3 * H * R.norm(), v
+    del Wd, o, S, D
+    torch.cuda.empty_cache()
+
+
 # ---- as they are used ----------------------------------------------------------------------------
 
 
@@ -572,6 +749,43 @@ def test_same_bits_again(api):
     ref = all_of()
     for got in (all_of(), all_of(fill=255), all_of(fill=0x7F), all_of(stream=torch.cuda.Stream())):
         assert all((a == b).all() for a, b in zip(ref, got))
+
+
+def test_a_workspace_of_more_rows(api):
+    """One of the largest batch's size serves smaller ones, with the same bits."""
+    import torch
+
+    K, F, r, V, most = 128, 192, 16, 900, 700
+
+    def ws(n):
+        return torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+
+    w = [ws(api.qlora_gated_workspace(most, K, F, r)), ws(api.qlora_gated_workspace(most, K, F, r, True)),
+         ws(api.qlora_linear_bwd_int8_workspace(most, K, F, r)), ws(api.qlora_norm_workspace(most, K)),
+         ws(api.qlora_head_workspace(most, K, V, True, True))]
+    for M in (1, 7, 128, 129, 400, 700):
+        c = Gated(api, M, K, F, r)
+        Hs, W, labels, _ = head_case(M, K, V)
+        x8 = api.qlora_int8_quantize(c.Xd)
+        rstd = torch.ones(M, device="cuda")
+        ref, got = ([c.fwd(workspace=v[0]).A, *c.bwd(workspace=v[1]),
+                     *api.qlora_linear_bwd_int8(c.q[0], x8, c.dAd, c.L1d[0].contiguous(), c.L2d[0].contiguous(), 0.5, workspace=v[2]),
+                     api.qlora_norm_bwd(c.Xd, c.Xd, rstd, workspace=v[3]).dweight,
+                     *api.qlora_head_loss(dev(Hs), dev(W), dev(labels), need_dW=True, workspace=v[4])] for v in ([None] * 5, w))
+        assert all((a == b).all() for a, b in zip(ref, got)), M
+
+
+def test_arguments_by_name_and_place(api):
+    import torch
+
+    x = normal((5, 64), 1)
+    w, labels, other = normal((9, 64), 2), torch.tensor([1, 8, -1, 9, 0], device="cuda"), torch.cuda.Stream()
+    a, b = api.qlora_norm_fwd(x), api.qlora_norm_fwd(x=x, weight=None)
+    torch.cuda.synchronize()
+    c = api.qlora_norm_fwd(x, None, 1e-6, None, True, False, None, None, None, other)
+    d, e = api.qlora_head_loss(x, w, labels), api.qlora_head_loss(labels=labels, W=w, H=x, stream=other)
+    torch.cuda.synchronize()
+    assert (a.y == b.y).all() and (a.y == c.y).all() and (d.dH == e.dH).all() and (d.loss == e.loss).all()
 
 
 @pytest.mark.parametrize("M", [1, 40, 200])

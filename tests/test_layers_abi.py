@@ -183,3 +183,18 @@ def test_workspaces_of_no_rows(lib):
         assert size(lib.qlora_gated_workspace, 0, 64, 128, 8, backward) > 0
     assert size(lib.qlora_linear_bwd_int8_workspace, 0, 64, 128, 8) > 0
     assert size(lib.qlora_norm_workspace, 0, 64) > 0
+
+
+def test_workspaces_never_shrink(lib):
+    """One of the largest batch's size serves smaller batches."""
+    rows = [*range(0, 400), *range(400, 17000, 83), 1 << 15, 40000, 1 << 16, 1 << 18, 1 << 21]
+    for K, F, r in ((64, 8, 8), (64, 8, 72), (1024, 64, 64), (4096, 11008, 16), (4096, 11008, 136)):
+        for backward in (0, 1):
+            sizes = [size(lib.qlora_gated_workspace, M, K, F, r, backward) for M in rows]
+            assert sizes == sorted(sizes), (K, F, r, backward)
+        sizes = [size(lib.qlora_linear_bwd_int8_workspace, M, K, F, r) for M in rows]
+        assert sizes == sorted(sizes), (K, F, r)
+        sizes = [size(lib.qlora_head_workspace, M, K, F, 1, 1, 0) for M in rows]
+        assert sizes == sorted(sizes), (K, F)
+        sizes = [size(lib.qlora_norm_workspace, M, K) for M in rows]
+        assert sizes == sorted(sizes), K

@@ -512,6 +512,7 @@ struct LayerPrep {
   const uint16_t* dy;
   uint16_t* dyp;
   int blocks[6];             // set by the launch
+  int weights_first;        // the same
 };
 hipError_t launch_layer_prep(LayerPrep p, hipStream_t stream);
 

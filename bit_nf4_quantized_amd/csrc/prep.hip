@@ -5,7 +5,7 @@
 //
 //   weights   one or two quantised weights [N][K] -> bf16 rows; two of them in
 //             pairs of blocks of 32 rows (row n of weight w at 64 (n / 32) + 32 w
-//             + n % 32), rows N .. Np zeros. 2.5 B per weight: 90 M weights 52 us, 4.3 TB/s.
+//             + n % 32), rows N .. Np zeros. 2.5 B per weight: 90 M weights 50 us, 4.5 TB/s.
 //   adapters  32 x 32 tiles, transposed through LDS:
 //             l1t [n][rp][K] = L1^T, rows behind the rank zero
 //             l2i [2 Np][2 rp] = L2^T in the paired rows' order, weight w's columns
@@ -29,17 +29,31 @@ __device__ __forceinline__ void prep_weights(const LayerPrep& p, const NF4View& 
   const int64_t K8 = W.cols / 8, nunits = W.rows * K8, all = p.Np * K8;
   const uint32_t* codes = reinterpret_cast<const uint32_t*>(W.codes);
   constexpr int kUnits = 4;                          // 8 weights each, 256 units apart, all loads first
-  for (int64_t base = (int64_t)block * 256 * kUnits + threadIdx.x; base < all; base += (int64_t)blocks * 256 * kUnits) {
-    uint32_t c[kUnits];
-    float ap[kUnits];
+  const int64_t stride = (int64_t)blocks * 256 * kUnits;
+  uint32_t c[kUnits];
+  float sc[kUnits];
+  uint8_t c8[kUnits];
+  auto load = [&](int64_t base) {
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
       const int64_t un = base + (int64_t)u * 256, uc = un < nunits ? un : nunits - 1;
       c[u] = codes[uc];
       const int64_t blk = uc >> 3;
-      if constexpr (DQ) ap[u] = block_scale(W.absmax8[blk], W.scale2[blk / kDqBlock], mu);
-      else ap[u] = W.absmax32[blk];
+      if constexpr (DQ) c8[u] = W.absmax8[blk];
+      sc[u] = DQ ? W.scale2[blk / kDqBlock] : W.absmax32[blk];
     }
+  };
+  const int64_t first = (int64_t)block * 256 * kUnits + threadIdx.x;
+  load(first);
+  for (int64_t base = first; base < all; base += stride) {
+    uint32_t cc[kUnits];
+    float ap[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      cc[u] = c[u];
+      ap[u] = DQ ? block_scale(c8[u], sc[u], mu) : sc[u];
+    }
+    load(base + stride);                             // the next turn's, in flight meanwhile
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
       const int64_t un = base + (int64_t)u * 256;
@@ -48,7 +62,7 @@ __device__ __forceinline__ void prep_weights(const LayerPrep& p, const NF4View& 
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t byte = (c[u] >> (8 * i)) & 0xFFu;
+        const uint32_t byte = (cc[u] >> (8 * i)) & 0xFFu;
         o[i] = un < nunits ? pack_bf16x2(s_q[byte & 15u] * ap[u], s_q[byte >> 4] * ap[u]) : 0u;
       }
       const int64_t row = p.n == 2 ? 64 * (n >> 5) + 32 * which + (n & 31) : n;
@@ -94,7 +108,10 @@ __global__ __launch_bounds__(256) void layer_prep_kernel(LayerPrep p) {
   __shared__ uint16_t tile[32][33];
   __shared__ float scale[64][65];
   int id = (int)blockIdx.x;
-  if (id < p.blocks[0]) {                            // the longest part first
+  // The weights first where their workgroups take several turns (90 M weights 53 us, last 69: some start late); last
+  // where they take one, the others' longer ways beside them (16.8 M weights, 200 rows 14.0 us, first 17.5).
+  if (!p.weights_first) id = id + p.blocks[0] < (int)gridDim.x ? id + p.blocks[0] : id + p.blocks[0] - (int)gridDim.x;
+  if (id < p.blocks[0]) {
     const int per = p.blocks[0] / p.n;
     const int which = id >= per ? 1 : 0;
     const NF4View W = which ? p.W[1] : p.W[0];
@@ -156,6 +173,7 @@ hipError_t launch_layer_prep(LayerPrep p, hipStream_t stream) {
     return (int)(b < most ? b : most);
   };
   p.blocks[0] = p.wd ? p.n * blocks(p.Np * p.K / 32, 8 * cus / p.n) : 0;
+  p.weights_first = p.n * p.Np * p.K / 8 > (int64_t)p.blocks[0] * 1024;   // 1024: a workgroup's units per turn
   p.blocks[1] = p.x ? blocks(p.M * p.K / 8, 8 * cus) : 0;
   p.blocks[2] = p.l1t ? p.n * (int)(p.K / 32) * (p.rp / 32) : 0;
   p.blocks[3] = p.l2i || p.l2p ? p.n * (int)(p.Np / 32) * (p.rp / 32) : 0;

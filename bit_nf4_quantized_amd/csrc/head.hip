@@ -308,7 +308,10 @@ __global__ __launch_bounds__(1024) void head_stat_kernel(StatArgs a) {
   __shared__ float s_d[16][64], s_l[16][64], s_top[64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t n = piece_rows(a.r.count, a.row0, a.piece), r0 = (int64_t)blockIdx.x * 64;
-  if (a.plan && r0 == 0 && tid == 1023) *a.plan = tg_plan(n, a.K, a.nk, a.most, a.cus, a.grid);
+  if (a.plan && r0 == 0 && wave == 15) {
+    const TgPlan pl = tg_plan_wave(n, a.K, a.nk, a.most, a.cus, a.grid);
+    if (lane == 0) *a.plan = pl;
+  }
   if (r0 >= n) return;                              // uniform
   const bool in = r0 + lane < n;
   const int64_t row = in ? r0 + lane : n - 1;

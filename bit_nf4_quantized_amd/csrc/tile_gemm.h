@@ -344,24 +344,56 @@ struct TgPlan {
   int slices, per_slice;
 };
 
-__host__ __device__ inline TgPlan tg_plan(int64_t M, int64_t N, int nk, int64_t most, int cus, int grid = 0x7FFFFFFF) {
+// Time of S slices in full or half-height tiles (*half), whichever is less; 3e38 where there may be no S slices.
+__host__ __device__ inline float tg_cost(int64_t M, int64_t N, int nk, int64_t most, int cus, int grid, int S, bool* half) {
   const int t1 = (int)((M + 255) / 256), t2 = (int)((M + 127) / 128), tn = (int)((N + kTgN - 1) / kTgN);
-  TgPlan best{t1, tn, 0, 1, nk};
-  float least = 3e38f;
+  const int per = (nk + S - 1) / S;
+  if (S > 1 && (nk < 8 * S || S * M > most || (nk + per - 1) / per != S)) return 3e38f;   // the last: a slice would be empty
   const float f1 = (float)t1 * tn / cus, f2 = (float)t2 * tn / cus, join = 8e-6f / 4.5f * M * N;
+  const float f = (float)t1 * tn * S <= grid ? kTgFullCost * __builtin_ceilf(f1 * S) : 3e38f;
+  const float h = (float)t2 * tn * S <= grid ? kTgHalfCost * __builtin_ceilf(f2 * S) : 3e38f;
+  *half = h < f;
+  return per * (f < h ? f : h) + (S > 1 ? 3.0f + join * S : 0.0f);
+}
+
+__host__ __device__ inline TgPlan tg_plan_of(int64_t M, int64_t N, int nk, int S, bool half) {
+  const int rows = half ? 128 : 256;
+  return TgPlan{(int)((M + rows - 1) / rows), (int)((N + kTgN - 1) / kTgN), half ? 1 : 0, S, (nk + S - 1) / S};
+}
+
+inline TgPlan tg_plan(int64_t M, int64_t N, int nk, int64_t most, int cus, int grid = 0x7FFFFFFF) {
+  int best = 1;
+  bool half = false;
+  float least = 3e38f;
   for (int S = 1; S <= 16; ++S) {
-    if (S > 1 && (nk < 8 * S || S * M > most)) break;
-    const int per = (nk + S - 1) / S;
-    if (S > 1 && (nk + per - 1) / per != S) continue;    // a slice would be empty
-    const float full = (float)t1 * tn * S <= grid ? kTgFullCost * __builtin_ceilf(f1 * S) : 3e38f;
-    const float half = (float)t2 * tn * S <= grid ? kTgHalfCost * __builtin_ceilf(f2 * S) : 3e38f;
-    const float t = per * (full < half ? full : half) + (S > 1 ? 3.0f + join * S : 0.0f);
+    bool h = false;
+    const float t = tg_cost(M, N, nk, most, cus, grid, S, &h);
     if (t < least) {
       least = t;
-      best = half < full ? TgPlan{t2, tn, 1, S, per} : TgPlan{t1, tn, 0, S, per};
+      best = S;
+      half = h;
     }
   }
-  return best;
+  return tg_plan_of(M, N, nk, best, half);
+}
+
+// The same by a wave, a slice count per lane (one after the other they took 2 us); every lane gets it.
+__device__ inline TgPlan tg_plan_wave(int64_t M, int64_t N, int nk, int64_t most, int cus, int grid) {
+  const int lane = threadIdx.x & 63;
+  bool h = false;
+  float t = lane < 16 ? tg_cost(M, N, nk, most, cus, grid, lane + 1, &h) : 3e38f;
+  int best = 2 * lane + (h ? 1 : 0);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {                  // of equal times the fewest slices
+    const float ot = __shfl_xor(t, o, 64);
+    const int ob = __shfl_xor(best, o, 64);
+    if (ot < t || (ot == t && ob < best)) {
+      t = ot;
+      best = ob;
+    }
+  }
+  best = __builtin_amdgcn_readfirstlane(best);
+  return tg_plan_of(M, N, nk, (best >> 1) + 1, best & 1);
 }
 
 // The same without slices, in a few integer operations: every workgroup of a product makes it for itself.

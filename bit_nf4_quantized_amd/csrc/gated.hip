@@ -530,8 +530,7 @@ hipError_t gated_forward(const GatedBase& W, const uint16_t* X, int64_t M, const
              {gate8 ? gate8->absmax : nullptr, up8 ? up8->absmax : nullptr}, M, F};
   if (!gate8 && gemv1_pair_applies(W, M, r)) return launch_gemv1_pair(W, X, L1, L2, r, s, act, A, T_out, b.part, stream);
   if (M <= kMultiSmallRows) {      // one pass over the 4-bit weights
-    GD_TRY(launch_small_t_partial(X, M, K, L1, r, b.part, stream, 2));
-    GD_TRY(launch_small_pair_base(W, X, M, b.part2, stream));
+    GD_TRY(launch_small_pair(W, X, M, L1, r, b.part, b.part2, stream));
     const int S = small_pair_slices(M, K, F), Z = small_t_slices(K);
     const dim3 grid((unsigned)gd_cdiv(F, 128), (unsigned)gd_cdiv(M, 16));
     if (act == kActSilu)

@@ -550,7 +550,8 @@ hipError_t linear_backward_int8(const NF4View& W, const NF4Table& tab, const Int
 // Up to 128 rows (multi_small.hip): the base products' partials [slices][M][F] of gate, then of up
 int small_pair_slices(int64_t M, int64_t K, int64_t N);
 int64_t small_pair_partial_floats(int64_t M, int64_t K, int64_t N);   // of any batch of up to M rows
-hipError_t launch_small_pair_base(const GatedBase& W, const uint16_t* X, int64_t M, float* part, hipStream_t stream);
+hipError_t launch_small_pair(const GatedBase& W, const uint16_t* X, int64_t M, const uint16_t* L1, int r, float* t_part, float* part,
+                             hipStream_t stream);
 // A single token (gemv1.hip); part: two times gemv1_partial_bytes.
 bool gemv1_pair_applies(const GatedBase& W, int64_t M, int r);
 hipError_t launch_gemv1_pair(const GatedBase& W, const uint16_t* X, const uint16_t* L1, const uint16_t* L2, int r, float s,

@@ -193,26 +193,86 @@ struct BaseLds {
 // check in the loop of one variant for all took 0.4 to 1.5 us of every call (60
 // rows 4096 -> 11008 35.2 -> 36.7); so it costs K = 4160 0.4 to 0.8 us (60 rows
 // -> 11008 37.7 -> 38.2) and nothing where K is a multiple of 128.
-// PAIR: weight blockIdx.z of two (of one shape), whose partials follow the first one's.
+// PAIR: weight blockIdx.z of two (of one shape), the second's partials behind the first's; from blockIdx.z = 2 on T's
+// workgroups (tg of them, 0: none), which the base product does not wait for.
 struct SecondBase {
   NF4View W;
   NF4Table tab;
+  const uint16_t* L1;        // [2][K][r]
+  float* t_part;             // [2][Z][M][r]
+  int r, Z, tg;
 };
+
+// T's partials of 16 rows, 64 ranks and 512 k of one of two adapters, by 8 waves of 2 x 32 k each: those of
+// small_t_partial_kernel but for the order of the waves' sum. After the base product's workgroups on the CUs that those
+// leave idle, where one launch before it took 5 us (96 rows, 4096 -> 2 x 11008).
+__device__ __forceinline__ void pair_t_body(const SecondBase& o, const uint16_t* __restrict__ X, int M, int64_t K, int id, float* red) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int jts = (o.r + 63) / 64, mtiles = (M + 15) / 16;
+  const int z = id % o.Z, jt0 = id / o.Z % jts, mt = id / (o.Z * jts) % mtiles, w = id / (o.Z * jts * mtiles);
+  const uint16_t* L1 = o.L1 + (int64_t)w * K * o.r;
+  float* P = o.t_part + ((int64_t)w * o.Z + z) * M * o.r;
+  const int row = lane & 15, j0 = 64 * jt0, mb = 16 * mt;
+  u32x4_t xa[2];
+  uint32_t h[2][4][8];                                 // all loads first (one round trip)
+#pragma unroll
+  for (int k2 = 0; k2 < 2; ++k2) {
+    const int64_t kw = (int64_t)z * 512 + (2 * wave + k2) * 32 + 8 * (lane >> 4);
+    xa[k2] = u32x4_t{0u, 0u, 0u, 0u};
+    if (mb + row < M && kw < K) xa[k2] = *reinterpret_cast<const u32x4_t*>(X + (int64_t)(mb + row) * K + kw);  // K % 64 == 0
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+      const int j = j0 + 16 * jt + row;
+      const bool in = j < o.r && kw < K;
+      const uint16_t* lp = L1 + (in ? kw * o.r + j : 0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[k2][jt][i] = lp[in ? (int64_t)i * o.r : 0];
+      if (!in) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k2][jt][i] = 0u;
+      }
+    }
+  }
+#pragma unroll
+  for (int jt = 0; jt < 4; ++jt) {
+    f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k2 = 0; k2 < 2; ++k2) {
+      const uint32_t* q = h[k2][jt];
+      const u32x4_t b = {q[0] | (q[1] << 16), q[2] | (q[3] << 16), q[4] | (q[5] << 16), q[6] | (q[7] << 16)};
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xa[k2]), __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[(wave * 16 + 4 * (lane >> 4) + i) * 64 + 16 * jt + row] = acc[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int m = wave; m < 16; m += 8) {                 // thread (m, lane) sums the waves in order
+    float v = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v += red[(q * 16 + m) * 64 + lane];
+    if (mb + m < M && j0 + lane < o.r) P[(int64_t)(mb + m) * o.r + j0 + lane] = v;
+  }
+}
 
 template <int MT, bool RAGGED, bool PAIR>
 __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4Table tab,
                                                                   const uint16_t* __restrict__ X, int M, int slice,
                                                                   float* __restrict__ part, SecondBase other) {
-  if constexpr (PAIR) {
-    if (blockIdx.z) {
-      W = other.W;
-      tab = other.tab;
-      part += (int64_t)gridDim.y * M * W.rows;
-    }
-  }
   using L = BaseLds<MT>;
   __shared__ float s_q[16];                            // a fixed address: table reads need no base
   extern __shared__ __attribute__((aligned(1024))) char smem[];
+  if constexpr (PAIR) {
+    if (blockIdx.z > 1) {                              // uniform
+      const int id = (int)(((blockIdx.z - 2) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x);
+      if (id < other.tg) pair_t_body(other, X, M, W.cols, id, reinterpret_cast<float*>(smem));
+      return;
+    }
+    if (blockIdx.z) {
+      W = other.W;
+      part += (int64_t)gridDim.y * M * W.rows;
+    }
+  }
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave & 1, wk = wave >> 1;
@@ -222,7 +282,7 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
   const int64_t k1 = k0 + slice < K ? k0 + slice : K;
   const int ns = (int)((k1 - k0 + kBaseK - 1) / kBaseK);
   float* s_a = reinterpret_cast<float*>(smem + L::kConst);
-  if (tid < 16) s_q[tid] = tab.q[tid];
+  if (tid < 16) s_q[tid] = PAIR && blockIdx.z ? other.tab.q[tid] : tab.q[tid];
 
   // Copies: waves 0-3 bring X, waves 4-7 the codes, each with a wait count of
   // its own (a wave's copies complete in order: codes, from HBM and several
@@ -492,7 +552,8 @@ hipError_t run_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, in
     (void)hipGetLastError();  // a refusal shows up as a launch error below
     attr_set = true;
   }
-  const dim3 grid((unsigned)((W.rows + kBaseRows - 1) / kBaseRows), (unsigned)sp.S, PAIR ? 2 : 1);
+  const int64_t tiles = (W.rows + kBaseRows - 1) / kBaseRows;
+  const dim3 grid((unsigned)tiles, (unsigned)sp.S, PAIR ? 2 + (unsigned)((other.tg + tiles * sp.S - 1) / (tiles * sp.S)) : 1);
   hipLaunchKernelGGL((small_base_kernel<MT, RAGGED, PAIR>), grid, dim3(kBaseThreads), BaseLds<MT>::kTotal, stream, W, tab, X, M,
                      sp.slice, part, other);
   return hipGetLastError();
@@ -663,9 +724,20 @@ int64_t small_pair_partial_floats(int64_t M, int64_t K, int64_t N) {
   return 2 * (a > b ? a : b) * N;
 }
 
-hipError_t launch_small_pair_base(const GatedBase& W, const uint16_t* X, int64_t M, float* part, hipStream_t stream) {
-  return launch_base<true>(W.gate, W.tab_gate, X, M, base_split(M, W.gate.cols, W.gate.rows, 2), part,
-                           SecondBase{W.up, W.tab_up}, stream);
+hipError_t launch_small_pair(const GatedBase& W, const uint16_t* X, int64_t M, const uint16_t* L1, int r, float* t_part, float* part,
+                             hipStream_t stream) {
+  const BaseSplit sp = base_split(M, W.gate.cols, W.gate.rows, 2);
+  const int64_t tiles = (W.gate.rows + kBaseRows - 1) / kBaseRows;
+  SecondBase o{W.up, W.tab_up, L1, t_part, r, small_t_slices(W.gate.cols), 0};
+  const int64_t idle = (M <= kBaseTwoPerCu ? 2 : 1) * (int64_t)device_cu_count() - 2 * tiles * sp.S;
+  const int64_t tg = 2 * (int64_t)o.Z * ((r + 63) / 64) * ((M + 15) / 16);
+  if (tg <= 4 * idle) {
+    o.tg = (int)tg;
+  } else {
+    const hipError_t e = launch_small_t_partial(X, M, W.gate.cols, L1, r, t_part, stream, 2);
+    if (e != hipSuccess) return e;
+  }
+  return launch_base<true>(W.gate, W.tab_gate, X, M, sp, part, o, stream);
 }
 
 hipError_t launch_multi_small_t(const uint16_t* X, int64_t M, int64_t K, const MultiIds& mi, const uint16_t* L1, int r,

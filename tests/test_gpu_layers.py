@@ -136,7 +136,7 @@ def act_errors(g, e, kind):
 
 
 SHAPES = [(1, 64, 8, 8), (1, 256, 136, 16), (2, 64, 72, 24), (16, 128, 64, 8), (17, 192, 200, 64), (33, 320, 128, 72),
-          (128, 64, 256, 8), (129, 64, 8, 8), (130, 128, 72, 16), (200, 256, 320, 136), (300, 64, 512, 64), (515, 192, 328, 40)]
+          (100, 64, 16384, 8), (128, 64, 256, 8), (129, 64, 8, 8), (130, 128, 72, 16), (200, 256, 320, 136), (300, 64, 512, 64), (515, 192, 328, 40)]
 
 
 @pytest.mark.parametrize("M,K,F,r", SHAPES)

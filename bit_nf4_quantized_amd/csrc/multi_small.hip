@@ -194,7 +194,8 @@ struct BaseLds {
 // rows 4096 -> 11008 35.2 -> 36.7); so it costs K = 4160 0.4 to 0.8 us (60 rows
 // -> 11008 37.7 -> 38.2) and nothing where K is a multiple of 128.
 // PAIR: weight blockIdx.z of two (of one shape), the second's partials behind the first's; from blockIdx.z = 2 on T's
-// workgroups (tg of them, 0: none), which the base product does not wait for.
+// workgroups (tg of them, 0: none), which the base product does not wait for. 96 rows, 4096 -> 2 x 11008: 45.5 us, of
+// tiles on 172 of the 256 CUs.
 struct SecondBase {
   NF4View W;
   NF4Table tab;

@@ -1,0 +1,89 @@
+"""The layer operators' optional inputs, each with and without the others, against
+the float64 oracle, and the bounds of tests/test_gpu_layers.py without the
+allowance for a weight's neighbouring bf16 where no kernel needs it.
+
+Only a single token of rank <= 64 with K a multiple of 256, both weights
+double-quantised in one data type and nothing kept takes the code values from a
+table in fp16 (off by 2^-11 of the value, so that the weight's rounding to bf16 may
+fall to the neighbour: 2 h |X||W|). Everything else multiplies the fp32 code value
+by its block constant and rounds once, which is the oracle's weight bit for bit.
+
+An input in 8 bits is rounded to bf16 as an operand, one rounding of a value that
+the codes give exactly, so the oracle takes the rounded values and no bound grows.
+Given T, gate and up are independent of X here: what a call is given is what it
+has to use.
+"""
+
+import numpy as np
+import pytest
+
+from gpu_util import gpu_quantize, require_gpu
+from oracle import layers, linear
+from test_gpu_layers import H, U, Gated, act_errors, bf16, dev, int8_of, within, within_int8
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def api():
+    return require_gpu()
+
+
+def gate_up_errors(c, X, fp16_table=False):
+    """(E(T), E(G), E(U)) of the bounds' derivation in test_gpu_layers.py."""
+    aX, s = np.abs(X), abs(c.s)
+    ET, E = [], []
+    for k in range(2):
+        L1, L2 = np.abs(linear.widen(c.L1[k])), np.abs(linear.widen(c.L2[k]))
+        et = c.K * U * (aX @ L1)
+        st = s * np.abs(X @ linear.widen(c.L1[k]))
+        est = s * et + H * (st + s * et)
+        base = aX @ np.abs(c.W[k]).T
+        E.append((c.K * U + (2 * H if fp16_table else 0.0)) * base + est @ L2 + c.r * U * ((st + est) @ L2))
+        ET.append(et)
+    return ET, E[0], E[1]
+
+
+@pytest.mark.parametrize("M,K,F,r", [(1, 256, 136, 72), (1, 320, 136, 16), (1, 256, 192, 16), (2, 64, 72, 24), (2, 256, 200, 64), (5, 512, 128, 8),
+                                     (11, 192, 264, 40), (16, 128, 64, 8), (16, 256, 328, 136)])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_gated_forward_few_rows(api, M, K, F, r, kind):
+    c = Gated(api, M, K, F, r, kind=kind, seed=11)
+    save = F % 64 == 0
+    o = c.fwd(want_T=True, want_int8=save)
+    A, G, Uv, T = layers.gated_fwd(c.X, *c.W, c.L1, c.L2, c.s, kind)
+    ET, EG, EU = gate_up_errors(c, linear.widen(c.X))
+    label = f"gated fwd {M}x{K}x{F} r{r} {kind}"
+    for k in range(2):
+        within(label, f"T{k}", o.T[k], T[k], ET[k])
+    a, _, Ea, _ = act_errors(G, EG, kind)
+    within(label, "A", o.A, A, Ea * np.abs(Uv) + np.abs(a) * EU + Ea * EU + 2 * U * np.abs(A))
+    if save:
+        within_int8(label, "gate8", o.gate8, G, EG)
+        within_int8(label, "up8", o.up8, Uv, EU)
+
+
+@pytest.mark.parametrize("M,K,N,r", [(1, 64, 8, 8), (2, 256, 64, 16), (5, 128, 72, 16), (16, 64, 200, 72), (40, 192, 136, 64), (130, 64, 264, 24),
+                                     (150, 128, 328, 136)])
+@pytest.mark.parametrize("given_t", [False, True])
+def test_linear_bwd_int8_few_rows_ragged(api, M, K, N, r, given_t):
+    rng = np.random.default_rng(M + N)
+    q, _ = gpu_quantize(api, (rng.standard_normal((N, K)) / np.sqrt(K)).astype(np.float32))
+    W = linear.widen(api.to_host_bits(api.qlora_dequantize(q)))
+    L1, L2, dY = bf16(rng.standard_normal((K, r)) / np.sqrt(K)), bf16(rng.standard_normal((r, N))), bf16(rng.standard_normal((M, N)))
+    s = 0.75
+    X8, X = int8_of(api, rng.standard_normal((M, K)))
+    X = linear.widen(bf16(X))
+    T = bf16(rng.standard_normal((M, r)))
+    got = api.qlora_linear_bwd_int8(q, X8, dev(dY), dev(L1), dev(L2), s, T=dev(T) if given_t else None)
+    RX, R1, _ = linear.linear_bwd(X, W, L1, L2, s, dY)
+    T = linear.widen(T) if given_t else X @ linear.widen(L1)
+    aX, a1, a2, aY, aW, aT = np.abs(X), *(np.abs(linear.widen(v)) for v in (L1, L2, dY)), np.abs(W), np.abs(T)
+    sU = s * np.abs(linear.widen(dY) @ linear.widen(L2).T)
+    EsU = s * N * U * (aY @ a2.T)
+    EsU = EsU + H * (sU + EsU)
+    label = f"linear int8 {M}x{K}x{N} r{r} T {given_t}"
+    within(label, "dX", got[0], RX, 2 * N * U * (aY @ aW) + EsU @ a1.T + r * U * ((sU + EsU) @ a1.T))
+    within(label, "dL1", got[1], R1, aX.T @ EsU + M * U * (aX.T @ (sU + EsU)))
+    eT = 0.0 * aT if given_t else K * U * (aX @ a1) + H * (aT + K * U * (aX @ a1))
+    within(label, "dL2", got[2], s * (T.T @ linear.widen(dY)), s * (eT.T @ aY + M * U * ((aT + eT).T @ aY)))

@@ -19,7 +19,7 @@ import pytest
 
 from gpu_util import gpu_quantize, require_gpu
 from oracle import layers, linear
-from test_gpu_layers import H, U, Gated, act_errors, bf16, dev, int8_of, within, within_int8
+from test_gpu_layers import H, U, Gated, act_errors, bf16, check_head, dev, head_case, int8_of, within, within_int8
 
 pytestmark = pytest.mark.gpu
 
@@ -63,6 +63,57 @@ def test_gated_forward_few_rows(api, M, K, F, r, kind):
         within_int8(label, "up8", o.up8, Uv, EU)
 
 
+@pytest.mark.parametrize("M,K,F,r", [(1, 64, 8, 8), (5, 64, 72, 16), (20, 128, 192, 16), (33, 128, 200, 136), (140, 64, 328, 64), (150, 192, 256, 72)])
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("kept", [False, True])
+@pytest.mark.parametrize("given_t", [False, True])
+def test_gated_backward_inputs(api, M, K, F, r, x8, kept, given_t):
+    import torch
+
+    if kept:
+        F = (F + 63) // 64 * 64
+    c = Gated(api, M, K, F, r, kind="gelu" if M % 2 else "silu", seed=13)
+    rng = np.random.default_rng(M + F + r)
+    X, kw, x_arg, GU = linear.widen(c.X), {}, None, None
+    if x8:
+        x_arg, X = int8_of(api, X)
+        X = linear.widen(bf16(X))
+    if kept:
+        (kw["gate8"], G), (kw["up8"], Uv) = int8_of(api, 2 * rng.standard_normal((M, F))), int8_of(api, rng.standard_normal((M, F)))
+        GU = (G, Uv)
+    else:
+        G, Uv = layers.gate_up(X, *c.W, c.L1, c.L2, c.s)[:2]
+    if given_t:
+        T = bf16(rng.standard_normal((2, M, r)))
+        kw["T"] = dev(T)
+        T = linear.widen(T)
+    else:
+        T = np.stack([X @ linear.widen(c.L1[k]) for k in range(2)])
+    dX, dL1, dL2 = c.bwd(x_arg, grad_dtype=torch.bfloat16 if r % 16 else torch.float32, **kw)
+    RX, R1, R2, dG, dU = layers.gated_bwd(X, *c.W, c.L1, c.L2, c.s, c.kind, c.dA, GU)
+    aX, s, dA = np.abs(X), abs(c.s), np.abs(linear.widen(c.dA))
+    ET, EG, EU = gate_up_errors(c, X)
+    if kept:
+        EG, EU = 2 * U * np.abs(G), 2 * U * np.abs(Uv)
+    a, d, Ea, Ed = act_errors(G, EG, c.kind)
+    EdG = dA * (EU * np.abs(d) + np.abs(Uv) * Ed + EU * Ed) + 4 * U * np.abs(dG)
+    EdU = dA * Ea + 2 * U * np.abs(dU)
+    label = f"gated bwd {M}x{K}x{F} r{r} {c.kind} X8 {x8} kept {kept} T {given_t}"
+    EX = 0.0
+    for k, (dY, e) in enumerate(((dG, EdG), (dU, EdU))):
+        e = e + H * (np.abs(dY) + e)               # rounded to bf16 as an operand
+        aY, L1, L2, W = np.abs(dY) + e, np.abs(linear.widen(c.L1[k])), np.abs(linear.widen(c.L2[k])), np.abs(c.W[k])
+        sU = s * np.abs(dY @ linear.widen(c.L2[k]).T)
+        EsU = s * (e @ L2.T + F * U * (aY @ L2.T))
+        EsU = EsU + H * (sU + EsU)
+        EX = EX + 2 * F * U * (aY @ W) + e @ W + EsU @ L1.T + r * U * ((sU + EsU) @ L1.T)
+        within(label, f"dL1[{k}]", dL1[k], R1[k], aX.T @ EsU + M * U * (aX.T @ (sU + EsU)))
+        aT = np.abs(T[k])
+        eT = np.zeros_like(aT) if given_t else ET[k] + H * (aT + ET[k])
+        within(label, f"dL2[{k}]", dL2[k], c.s * (T[k].T @ dY), s * (eT.T @ aY + aT.T @ e + M * U * ((aT + eT).T @ aY)))
+    within(label, "dX", dX, RX, EX)
+
+
 @pytest.mark.parametrize("M,K,N,r", [(1, 64, 8, 8), (2, 256, 64, 16), (5, 128, 72, 16), (16, 64, 200, 72), (40, 192, 136, 64), (130, 64, 264, 24),
                                      (150, 128, 328, 136)])
 @pytest.mark.parametrize("given_t", [False, True])
@@ -87,3 +138,40 @@ def test_linear_bwd_int8_few_rows_ragged(api, M, K, N, r, given_t):
     within(label, "dL1", got[1], R1, aX.T @ EsU + M * U * (aX.T @ (sU + EsU)))
     eT = 0.0 * aT if given_t else K * U * (aX @ a1) + H * (aT + K * U * (aX @ a1))
     within(label, "dL2", got[2], s * (T.T @ linear.widen(dY)), s * (eT.T @ aY + M * U * ((aT + eT).T @ aY)))
+
+
+@pytest.mark.parametrize("M,K,V", [(1, 64, 5), (48, 192, 1000), (300, 64, 3001), (2500, 64, 700)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_head_weight_gradient_alone(api, M, K, V, dtype):
+    import torch
+
+    Hs, W, labels, rng = head_case(M, K, V, seed=3)
+    labels[rng.random(M) < 0.3] = -100
+    kw = dict(need_dW=True, grad_dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
+    o = api.qlora_head_loss(dev(Hs), dev(W), dev(labels), need_dH=False, **kw)
+    assert o.dH is None
+    check_head(f"head {M}x{K}x{V} dW alone {dtype}", o, Hs, W, labels)
+    both = api.qlora_head_loss(dev(Hs), dev(W), dev(labels), **kw)
+    assert (both.dW == o.dW).all() and (both.nll == o.nll).all() and (both.loss == o.loss).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_head_pieces_without_a_gradient(api, dtype):
+    """Several pieces of rows, dW without dH and the loss alone: the bits of the call with both gradients."""
+    import torch
+
+    M, K, V = 1100, 64, 1 << 20                       # pieces of 512 rows
+    g = torch.Generator(device="cuda").manual_seed(2)
+    Hd = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_(0, 1, generator=g)
+    Wd = torch.empty(V, K, dtype=torch.bfloat16, device="cuda").normal_(0, 0.25, generator=g)
+    Ld = torch.randint(0, V, (M,), device="cuda", generator=g)
+    kw = dict(grad_dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
+    for some in (Ld, torch.where(torch.arange(M, device="cuda") % 3 == 0, Ld, -100)):
+        both = api.qlora_head_loss(Hd, Wd, some, need_dW=True, **kw)
+        dW = api.qlora_head_loss(Hd, Wd, some, need_dH=False, need_dW=True, **kw)
+        alone = api.qlora_head_loss(Hd, Wd, some, need_dH=False)
+        for o in (dW, alone):
+            assert o.dH is None and (o.nll == both.nll).all() and (o.loss == both.loss).all()
+        assert (dW.dW == both.dW).all()
+        del both, dW, alone
+    torch.cuda.empty_cache()

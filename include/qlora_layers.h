@@ -15,6 +15,8 @@
  * Activations in 8 bits ("int8 values") are those of qlora_int8_quantize with
  * blocks of 64: codes [numel] and one fp32 absmax per 64 consecutive values, of a
  * matrix whose rows are a multiple of 64 long. A value is code * RN32(absmax / 127).
+ * Where these entry points write them, a block that holds an infinity or NaN has that as its absmax and codes 0: its
+ * 64 values are NaN.
  * M (rows) is at most QLORA_LAYER_MAX_ROWS, and may be 0. A workspace for M rows serves fewer rows too.
  */
 #ifndef QLORA_LAYERS_H

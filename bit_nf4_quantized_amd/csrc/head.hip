@@ -26,8 +26,9 @@
 // 6144 counted rows x 4096 x 32000: the two large products 1340-1398 and 1209-1241 us (1.15-1.34 PFLOP/s, the card's
 // power limit), the rest 90. 48 rows: P 57 us and dH 45, each bound by reading W (4.6 and 5.8 TB/s). 700 rows of 32001
 // with dW: P 220 us (750 half-height tiles, 2.9 rounds), dH 195, dW 242 (11 stages a tile, its stores 40 of them).
-// Rows are taken in pieces whose P fits a gigabyte. The number of counted rows is
-// known on the device only: the GEMMs plan their tiles there, from a grid for all rows.
+// Rows are taken in pieces whose P fits a gigabyte, but of 256 rows at least (2 GB of P at 2^22 words). The number of
+// counted rows is known on the device only: the GEMMs plan their tiles there, from a grid for all rows. Without a
+// gradient P is neither stored nor given room: the product's epilogue keeps the tiles' sums.
 #include "common.h"
 #include "launch.h"
 #include "tile_gemm.h"
@@ -169,7 +170,8 @@ __device__ __forceinline__ float max16(float v) {
   return v;
 }
 
-// P and the tile's sums and shifts [tile][piece]. Columns from V on and rows past the counted ones: zeros.
+// P (STORE) and the tile's sums and shifts [tile][piece]. Columns from V on and rows past the counted ones: zeros.
+template <bool STORE>
 struct ProbEpi {
   const float* ref;       // of the piece's first row
   const int32_t* label;
@@ -249,23 +251,27 @@ struct ProbEpi {
         const float a = __expf(acc[i][0][v]), b = __expf(acc[i][1][v]);
         const float s = sum16(a + b);
         mine = (lane & 15) == v ? s : mine;
-        const int at = ((v & 3) + 4 * (lane >> 5) + 8 * (v >> 2)) * 72 + (lane & 31);
-        ep[at] = f32_to_bf16(a);
-        ep[at + 32] = f32_to_bf16(b);
+        if constexpr (STORE) {
+          const int at = ((v & 3) + 4 * (lane >> 5) + 8 * (v >> 2)) * 72 + (lane & 31);
+          ep[at] = f32_to_bf16(a);
+          ep[at + 32] = f32_to_bf16(b);
+        }
       }
       {
         const int v = lane & 15;
         s_part[(2 * wn + ((lane >> 4) & 1)) * 256 + row_of(i, v)] = mine;
       }
-      __builtin_amdgcn_s_waitcnt(0xc07f);           // lgkmcnt(0): the wave's own slice
+      if constexpr (STORE) {
+        __builtin_amdgcn_s_waitcnt(0xc07f);         // lgkmcnt(0): the wave's own slice
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const int r = 8 * it + (lane >> 3), c = 8 * (lane & 7);
-        const u32x4_t val = *reinterpret_cast<const u32x4_t*>(ep + r * 72 + c);
-        const int64_t row = m0 + wm * (32 * MI) + 32 * i + r, col = n0 + 64 * wn + c;
-        if (row < piece && col < ldp) *reinterpret_cast<u32x4_t*>(P + row * ldp + col) = val;
+        for (int it = 0; it < 4; ++it) {
+          const int r = 8 * it + (lane >> 3), c = 8 * (lane & 7);
+          const u32x4_t val = *reinterpret_cast<const u32x4_t*>(ep + r * 72 + c);
+          const int64_t row = m0 + wm * (32 * MI) + 32 * i + r, col = n0 + 64 * wn + c;
+          if (row < piece && col < ldp) *reinterpret_cast<u32x4_t*>(P + row * ldp + col) = val;
+        }
+        __builtin_amdgcn_s_waitcnt(0xc07f);
       }
-      __builtin_amdgcn_s_waitcnt(0xc07f);
     }
     __syncthreads();
     if (tid < TM && m0 + tid < rows) {
@@ -279,7 +285,8 @@ struct ProbEpi {
   }
 };
 
-__global__ __launch_bounds__(kTgThreads, 1) void head_prob_kernel(TgArgs p, ProbEpi epi, const int32_t* count, int64_t row0,
+template <bool STORE>
+__global__ __launch_bounds__(kTgThreads, 1) void head_prob_kernel(TgArgs p, ProbEpi<STORE> epi, const int32_t* count, int64_t row0,
                                                                   int64_t N, int cus) {
   __shared__ __attribute__((aligned(1024))) uint16_t smem[kTgSmem];
   epi.rows = piece_rows(count, row0, epi.piece);
@@ -614,7 +621,7 @@ HeadWorkspace head_workspace_layout(int64_t M, int64_t K, int64_t V, bool dH, bo
   L.scale_off = take(4 * L.piece);
   L.stat_off = take(8 * hd_cdiv(V, kTgN) * L.piece);
   L.h_off = take(2 * M * K);
-  L.p_off = take(2 * L.piece * ldp);
+  L.p_off = take(dH || dW ? 2 * L.piece * ldp : 0);
   L.most = dH ? tg_partial_rows(L.piece < M ? L.piece : M) : 0;
   L.part_off = take(4 * L.most * K);
   L.plan_off = take(sizeof(TgPlan));
@@ -665,9 +672,13 @@ hipError_t launch_head_loss(const HeadCall& c, hipStream_t stream) {
     p.A = {Hc + r0 * K, K, most};
     p.B = {c.W, K, V};
     p.kmain = K;
-    const ProbEpi pe{ref + r0, label + r0, 0, V, ldp, L.piece, P, sum, shift};
-    hipLaunchKernelGGL(head_prob_kernel, dim3((unsigned)tg_grid(most, V, (int)(K / kTgK), 0, cus)), dim3(kTgThreads), 0, stream, p, pe,
-                       count, r0, V, cus);
+    const dim3 tiles_grid((unsigned)tg_grid(most, V, (int)(K / kTgK), 0, cus));
+    if (grad)
+      hipLaunchKernelGGL(head_prob_kernel<true>, tiles_grid, dim3(kTgThreads), 0, stream, p,
+                         ProbEpi<true>{ref + r0, label + r0, 0, V, ldp, L.piece, P, sum, shift}, count, r0, V, cus);
+    else
+      hipLaunchKernelGGL(head_prob_kernel<false>, tiles_grid, dim3(kTgThreads), 0, stream, p,
+                         ProbEpi<false>{ref + r0, label + r0, 0, V, ldp, L.piece, nullptr, sum, shift}, count, r0, V, cus);
     const int grid = tg_grid(most, K, (int)(ldp / kTgK), L.most, cus);
     const StatArgs sa{sum, shift, (int)tiles, r0, L.piece, ldp, hr, c.weights, c.divisor, c.grad_scale, grad ? P : nullptr,
                       scale, c.nll, c.dH ? plan : nullptr, K, L.most, (int)(ldp / kTgK), cus, grid};

@@ -135,7 +135,7 @@ int qlora_norm_bwd(const uint16_t *dy, const void *h, qlora_dtype stream_dtype, 
  * to bf16 once as an operand of the gradients' products (for dW, scaled rows of H too). An infinity or NaN in one row
  * of H reaches no other row of nll or dH.
  * K: a multiple of 64, below 2^23; V in [1, QLORA_HEAD_MAX_VOCAB]. Rows are taken in pieces of at most 2^29 / V (at
- * least 256), so that the workspace holds the probabilities of one piece.
+ * least 256): the workspace holds the probabilities of one piece, 1 GiB or 512 V bytes at most; none without dH and dW.
  */
 int qlora_head_workspace(int64_t M, int64_t K, int64_t V, int dH, int dW, qlora_dtype grad_dtype, size_t *bytes);
 int qlora_head_loss(const uint16_t *H, const uint16_t *W, const int64_t *labels, const float *weights, int64_t M,

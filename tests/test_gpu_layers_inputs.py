@@ -175,3 +175,21 @@ def test_head_pieces_without_a_gradient(api, dtype):
         assert (dW.dW == both.dW).all()
         del both, dW, alone
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M,K,V", [(3, 64, 5), (300, 128, 3001), (2500, 64, 700), (600, 64, 1 << 20)])
+def test_head_alone_stays_in_its_workspace(api, M, K, V):
+    """The loss alone, whose workspace has no room for probabilities: nothing behind it is written."""
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(M)
+    Hd = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_(0, 1, generator=g)
+    Wd = torch.empty(V, K, dtype=torch.bfloat16, device="cuda").normal_(0, 0.25, generator=g)
+    Wd[V // 2] *= 64.0                                # a tile that takes its rows' maxima out
+    Ld = torch.randint(-2, V, (M,), device="cuda", generator=g)
+    full = api.qlora_head_loss(Hd, Wd, Ld)
+    n = api.qlora_head_workspace(M, K, V, False, False)
+    buf = torch.full((n + (1 << 22),), 0xA5, dtype=torch.uint8, device="cuda")
+    o = api.qlora_head_loss(Hd, Wd, Ld, need_dH=False, workspace=buf[:n])
+    assert (buf[n:] == 0xA5).all()
+    assert (o.nll == full.nll).all() and (o.loss == full.loss).all() and torch.isfinite(o.loss).all()

@@ -1017,10 +1017,7 @@ LutPlan lut_plan(const NF4View& W, int64_t M, int r, bool want_fuse) {
 
 __global__ __launch_bounds__(64 * kTsWaves) void small_t_partial_kernel(const uint16_t* __restrict__ X, int M,
                                                                         int64_t K, const uint16_t* __restrict__ L1,
-                                                                        int r, float* __restrict__ P, int mtiles) {
-  // row tile blockIdx.z % mtiles; adapter blockIdx.z / mtiles of several whose partials follow each other
-  L1 += (int64_t)(blockIdx.z / mtiles) * K * r;
-  P += (int64_t)(blockIdx.z / mtiles) * gridDim.x * M * r;
+                                                                        int r, float* __restrict__ P) {
   // wave w: the 32 rows kw .. kw+32 of the slice, 4 MFMA column tiles of 16;
   // A = X rows (lane l: row l%16, k 8 (l/16) .. +8), B = L1 columns (lane l:
   // column l%16 of the tile, the same 8 k)
@@ -1029,7 +1026,7 @@ __global__ __launch_bounds__(64 * kTsWaves) void small_t_partial_kernel(const ui
   const int64_t kw = (int64_t)blockIdx.x * kTsK + wave * kTsRows + 8 * (lane >> 4);
   const int row = lane & 15;
   const int j0 = blockIdx.y * 64;
-  const int mb = (blockIdx.z % mtiles) * 16;   // this workgroup's 16 rows of X
+  const int mb = blockIdx.z * 16;   // this workgroup's 16 rows of X
   u32x4_t xa = {0u, 0u, 0u, 0u};
   if (mb + row < M && kw < K) xa = *reinterpret_cast<const u32x4_t*>(X + (int64_t)(mb + row) * K + kw);  // K % 64 == 0
   uint32_t h[4][8];  // all 32 loads first (one round trip)
@@ -1096,12 +1093,11 @@ size_t small_t_partial_bytes(int64_t M, int64_t K, int r) {
 int small_t_slices(int64_t K) { return (int)((K + kTsK - 1) / kTsK); }
 
 hipError_t launch_small_t_partial(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r, float* part,
-                                  hipStream_t stream, int adapters) {
+                                  hipStream_t stream) {
   if (M < 1 || M > 128) return hipErrorInvalidValue;
-  const int mtiles = (int)((M + 15) / 16);
   hipLaunchKernelGGL(small_t_partial_kernel,
-                     dim3((unsigned)small_t_slices(K), (unsigned)((r + 63) / 64), (unsigned)(mtiles * adapters)),
-                     dim3(64 * kTsWaves), 0, stream, X, (int)M, K, L1, r, part, mtiles);
+                     dim3((unsigned)small_t_slices(K), (unsigned)((r + 63) / 64), (unsigned)((M + 15) / 16)),
+                     dim3(64 * kTsWaves), 0, stream, X, (int)M, K, L1, r, part);
   return hipGetLastError();
 }
 

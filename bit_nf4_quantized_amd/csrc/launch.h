@@ -476,11 +476,11 @@ hipError_t adapter_up(const AdapterShape& a, const AdapterOperands& o, uint16_t*
                       hipStream_t stream);
 hipError_t adapter_grads(const AdapterShape& a, const AdapterOperands& o, const uint16_t* sU, const uint16_t* T, void* dL1,
                          void* dL2, bool grad_bf16, float* part, const SplitSum* split, hipStream_t stream);
-// T partials [slices][M][r] for M <= 128 (gemv.hip), of `adapters` adapters one after another
+// T partials [slices][M][r] for M <= 128 (gemv.hip)
 size_t small_t_partial_bytes(int64_t M, int64_t K, int r);
 int small_t_slices(int64_t K);
 hipError_t launch_small_t_partial(const uint16_t* X, int64_t M, int64_t K, const uint16_t* L1, int r, float* part,
-                                  hipStream_t stream, int adapters = 1);
+                                  hipStream_t stream);
 
 // The gated feed-forward block (gated.hip): two bases [F][K], adapters stacked
 // gate first: L1 [2][K][r], L2 [2][r][F], T [2][M][r].

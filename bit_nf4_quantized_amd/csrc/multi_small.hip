@@ -194,19 +194,21 @@ struct BaseLds {
 // rows 4096 -> 11008 35.2 -> 36.7); so it costs K = 4160 0.4 to 0.8 us (60 rows
 // -> 11008 37.7 -> 38.2) and nothing where K is a multiple of 128.
 // PAIR: weight blockIdx.z of two (of one shape), the second's partials behind the first's; from blockIdx.z = 2 on T's
-// workgroups (tg of them, 0: none), which the base product does not wait for. 96 rows, 4096 -> 2 x 11008: 45.5 us, of
-// tiles on 172 of the 256 CUs.
+// tg workgroups, which the base product does not wait for. 96 rows, 4096 -> 2 x 11008: 45.5 us, of tiles on 172 of the
+// 256 CUs. T by a launch of its own before was slower, whole calls of 17 to 128 rows and ranks 16 to 256: 3 to 10 us
+// where CUs are left idle, by the last round of tiles too (4096 -> 2 x 11008 96 rows rank 16 53.0 -> 49.1, 128 rows rank
+// 256 120.7 -> 112.2; -> 2 x 22016 33 rows rank 16 82.5 -> 78.2). With none idle it is 0.2 to 1.8 us slower too, but for
+// rank 256 of 96 and 128 rows, where it was 0.3 to 1.8 us faster in ten of twelve calls (-> 2 x 16384 161.5, here 162.5).
 struct SecondBase {
   NF4View W;
   NF4Table tab;
   const uint16_t* L1;        // [2][K][r]
   float* t_part;             // [2][Z][M][r]
-  int r, Z, tg;
+  int r, Z, tg;              // tg: 2 Z ranks' tiles of 64 rows' tiles of 16
 };
 
 // T's partials of 16 rows, 64 ranks and 512 k of one of two adapters, by 8 waves of 2 x 32 k each: those of
-// small_t_partial_kernel but for the order of the waves' sum. After the base product's workgroups on the CUs that those
-// leave idle, where one launch before it took 5 us (96 rows, 4096 -> 2 x 11008).
+// small_t_partial_kernel but for the order of the waves' sum.
 __device__ __forceinline__ void pair_t_body(const SecondBase& o, const uint16_t* __restrict__ X, int M, int64_t K, int id, float* red) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int jts = (o.r + 63) / 64, mtiles = (M + 15) / 16;
@@ -264,9 +266,13 @@ __global__ __launch_bounds__(kBaseThreads) void small_base_kernel(NF4View W, NF4
   __shared__ float s_q[16];                            // a fixed address: table reads need no base
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   if constexpr (PAIR) {
+    static_assert(kBaseThreads / 64 * 16 * 64 * 4 <= L::kTotal, "the sums of T's workgroups fit");
     if (blockIdx.z > 1) {                              // uniform
-      const int id = (int)(((blockIdx.z - 2) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x);
-      if (id < other.tg) pair_t_body(other, X, M, W.cols, id, reinterpret_cast<float*>(smem));
+      const int n = (int)((gridDim.z - 2) * gridDim.y * gridDim.x);
+      for (int id = (int)(((blockIdx.z - 2) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x); id < other.tg; id += n) {
+        pair_t_body(other, X, M, W.cols, id, reinterpret_cast<float*>(smem));
+        __syncthreads();                               // the sums' LDS is written again
+      }
       return;
     }
     if (blockIdx.z) {
@@ -554,7 +560,9 @@ hipError_t run_base(const NF4View& W, const NF4Table& tab, const uint16_t* X, in
     attr_set = true;
   }
   const int64_t tiles = (W.rows + kBaseRows - 1) / kBaseRows;
-  const dim3 grid((unsigned)tiles, (unsigned)sp.S, PAIR ? 2 + (unsigned)((other.tg + tiles * sp.S - 1) / (tiles * sp.S)) : 1);
+  int64_t t_layers = (other.tg + tiles * sp.S - 1) / (tiles * sp.S);
+  if (t_layers > 65533) t_layers = 65533;              // the grid's z is at most 65535
+  const dim3 grid((unsigned)tiles, (unsigned)sp.S, PAIR ? 2 + (unsigned)t_layers : 1);
   hipLaunchKernelGGL((small_base_kernel<MT, RAGGED, PAIR>), grid, dim3(kBaseThreads), BaseLds<MT>::kTotal, stream, W, tab, X, M,
                      sp.slice, part, other);
   return hipGetLastError();
@@ -728,16 +736,8 @@ int64_t small_pair_partial_floats(int64_t M, int64_t K, int64_t N) {
 hipError_t launch_small_pair(const GatedBase& W, const uint16_t* X, int64_t M, const uint16_t* L1, int r, float* t_part, float* part,
                              hipStream_t stream) {
   const BaseSplit sp = base_split(M, W.gate.cols, W.gate.rows, 2);
-  const int64_t tiles = (W.gate.rows + kBaseRows - 1) / kBaseRows;
-  SecondBase o{W.up, W.tab_up, L1, t_part, r, small_t_slices(W.gate.cols), 0};
-  const int64_t idle = (M <= kBaseTwoPerCu ? 2 : 1) * (int64_t)device_cu_count() - 2 * tiles * sp.S;
-  const int64_t tg = 2 * (int64_t)o.Z * ((r + 63) / 64) * ((M + 15) / 16);
-  if (tg <= 4 * idle) {
-    o.tg = (int)tg;
-  } else {
-    const hipError_t e = launch_small_t_partial(X, M, W.gate.cols, L1, r, t_part, stream, 2);
-    if (e != hipSuccess) return e;
-  }
+  const int Z = small_t_slices(W.gate.cols);
+  const SecondBase o{W.up, W.tab_up, L1, t_part, r, Z, (int)(2 * (int64_t)Z * ((r + 63) / 64) * ((M + 15) / 16))};
   return launch_base<true>(W.gate, W.tab_gate, X, M, sp, part, o, stream);
 }
 

@@ -63,6 +63,37 @@ def test_gated_forward_few_rows(api, M, K, F, r, kind):
         within_int8(label, "up8", o.up8, Uv, EU)
 
 
+@pytest.mark.parametrize("M,K,F,r", [(17, 576, 16384, 72), (40, 64, 22016, 256), (96, 1088, 1032, 256), (100, 576, 136, 136), (128, 512, 16384, 256),
+                                     (128, 2048, 64, 256)])
+def test_gated_forward_wide_adapters(api, M, K, F, r):
+    """T's workgroups beside the base product's, where those fill the device and where they do not."""
+    test_gated_forward_few_rows(api, M, K, F, r, "silu")
+
+
+def test_gated_forward_longest_rows(api):
+    """More of T's workgroups than a grid has layers for. Signs as X and L1 make T exact."""
+    import torch
+
+    M, K, F, r = 128, (1 << 22) - 64, 8, 256
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def signs(*shape):
+        return torch.randint(0, 2, shape, generator=g, device="cuda", dtype=torch.int8).mul_(2).sub_(1).to(torch.bfloat16)
+
+    w = api.qlora_quantize(torch.empty(F, K, device="cuda").normal_(0, 1, generator=g))
+    X, L1, L2 = signs(M, K), signs(2, K, r), signs(2, r, F)
+    ws = torch.full((api.qlora_gated_workspace(M, K, F, r),), 255, dtype=torch.uint8, device="cuda")
+    o = api.qlora_gated_fwd(w, w, X, L1, L2, 2.0 ** -20, want_T=True, workspace=ws)
+    for k in range(2):
+        T = torch.zeros(M, r, device="cuda")
+        for at in range(0, K, 1 << 18):               # whole numbers below 2^24: exact in every order
+            T += X[:, at:at + (1 << 18)].float() @ L1[k, at:at + (1 << 18)].float()
+        assert (o.T[k] == T.to(torch.bfloat16)).all()
+    assert torch.isfinite(o.A).all()
+    del w, X, L1, ws
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("M,K,F,r", [(1, 64, 8, 8), (5, 64, 72, 16), (20, 128, 192, 16), (33, 128, 200, 136), (140, 64, 328, 64), (150, 192, 256, 72)])
 @pytest.mark.parametrize("x8", [False, True])
 @pytest.mark.parametrize("kept", [False, True])

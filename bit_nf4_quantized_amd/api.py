@@ -1213,7 +1213,8 @@ def qlora_gated_fwd(gate: NF4Tensor, up: NF4Tensor, X, L1, L2, scale: float, act
                     want_int8: bool = False, A=None, T_out=None, workspace=None, stream=None) -> GatedOut:
     """A = act(G) * U, G = X dequant(gate)^T + scale (X L1[0]) L2[0], U likewise from ``up`` and L1[1], L2[1];
     L1 [2, K, r], L2 [2, r, F] bf16, act "silu" or "gelu" (its tanh form). ``want_T``: T = bf16(X L1[i]);
-    ``want_int8``: G and U as int8 values (codes, absmax of 64) for the backward pass."""
+    ``want_int8``: G and U as int8 values (codes, absmax of 64; NaN for a block with a value that is not finite) for the
+    backward pass."""
     return _gated_fwd(X, gate, up, L1, L2, scale, act, want_T, want_int8, A, T_out, workspace, stream=stream)
 
 
@@ -1439,10 +1440,11 @@ def qlora_head_workspace(M: int, K: int, V: int, dH: bool = True, dW: bool = Fal
 @_on_stream
 def qlora_head_loss(H, W, labels, weights=None, divisor: float = 0.0, grad_scale: float = 1.0, need_dH: bool = True,
                     need_dW: bool = False, grad_dtype=None, dH=None, dW=None, workspace=None, stream=None) -> HeadLoss:
-    """Softmax cross entropy of the logits H W^T (bf16 [M, K], [V, K]; the logits are not stored) against int64
-    labels [M]: rows with a label in [0, V) count, with float32 ``weights`` [M] or 1; the sum is divided by
-    ``divisor`` (0: the number of counted rows). Returns the loss, each row's, and grad_scale times the gradients
-    dH (bf16) and, with ``need_dW``, dW (grad_dtype)."""
+    """Softmax cross entropy of the logits H W^T (bf16 [M, K], [V, K]) against int64 labels [M]: rows with a label in
+    [0, V) count, with float32 ``weights`` [M] or 1; the sum is divided by ``divisor`` (0: the number of counted rows).
+    Returns the loss, each row's, and grad_scale times the gradients dH (bf16) and, with ``need_dW``, dW (grad_dtype).
+    The logits are not stored; for a gradient the workspace holds the probabilities of a piece of the rows, 1 GiB or
+    512 V bytes at most."""
     if H.dim() != 2 or W.dim() != 2:
         raise ValueError("H must be [M, K] and W [V, K]")
     (M, K), V = H.shape, W.shape[0]

@@ -17,10 +17,11 @@
 // bits an elementwise kernel makes them. dX is one product over both, [dG dU]
 // against the same matrix read down its rows.
 //
-// Bound by the matrix units at the card's power limit where rows are many: 2048 rows, 4096 -> 2 x 11008, 363-388 us of
-// 412 for the product (1.0 PFLOP/s: 688 tiles are 2.7 rounds of the CUs; 8-bit stores), dX of 8192 rows 1100-1137
-// (1.34 PFLOP/s), dG and dU from 8 bits 134 (5.3 TB/s). 391 rows: 172 tiles on 256 CUs, 112-122 us. The adapters' second
-// products are the last stages of the same tiles (a slab of 2 rp columns, beside K or 2 Fp of the base).
+// Bound by the matrix units where rows are many, in long runs of calls, 4096 -> 2 x 11008: dX of 8192 rows 1096-1107 us
+// (1.35 PFLOP/s; a large library product 1.46), the product computed again for the backward pass 1187-1202 (1.27); the
+// forward product of 2048 rows 290 us, with 8-bit stores 306-311 (1.24: 688 tiles are 2.7 rounds of the CUs); 391 rows
+// 100 (172 tiles on 256 CUs). dG and dU from 8 bits, 8192 rows, 138 us (5.3 TB/s). The adapters' second products are the
+// last stages of the same tiles (a slab of 2 rp columns, beside K or 2 Fp of the base).
 #include "act.h"
 #include "common.h"
 #include "int8.h"

@@ -56,9 +56,10 @@
 // its row r < R / 2 is feature r of gate, r + R / 2 of up, with the block
 // constants, adapter columns and partials of both, and the product act(G) U is
 // made where the waves' row sums are joined, so neither G nor U is written. Its
-// arithmetic is that of MULTI. 4096 -> 2 x 11008, rank 64 (50 MB): 4.8 + 19.2 us, the
-// call 22.2; without the table's reads 12.7, without the scaling 15.4. 16 waves of one
-// chunk each, which would hide both, spilled 127 registers (46 us).
+// arithmetic is that of MULTI. 4096 -> 2 x 11008, rank 64 (50 MB): 4.6 + 18.6 us, the
+// call 22.2; in short runs 19.2, where it took 12.7 without the table's reads and 15.4
+// without the scaling. 16 waves of one chunk each, which would hide both, spilled 127
+// registers (46 us).
 // Every result is deterministic (fixed orders, no atomics).
 #include "common.h"
 #include "act.h"

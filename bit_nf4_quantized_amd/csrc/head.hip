@@ -23,9 +23,10 @@
 //   head_dw_kernel       the GEMM P^T (scale H), both operands read down their rows
 //   head_dh_kernel       the GEMM P W, W read down its rows, in slices of the vocabulary where that fills the device better
 //   head_dh_sum_kernel   the slices' sum; the loss, a weighted sum in fp64
-// 6144 counted rows x 4096 x 32000: the two large products 1340-1398 and 1209-1241 us (1.15-1.34 PFLOP/s, the card's
-// power limit), the rest 90. 48 rows: P 57 us and dH 45, each bound by reading W (4.6 and 5.8 TB/s). 700 rows of 32001
-// with dW: P 220 us (750 half-height tiles, 2.9 rounds), dH 195, dW 242 (11 stages a tile, its stores 40 of them).
+// In long runs of calls, 6144 counted rows x 4096 x 32000: P 1292-1364 us and dH 1187-1281 (1.18-1.36 PFLOP/s; a large
+// library product 1.46), dW 1318-1372, the rest 85. 48 rows: P 64 us, 64 stages of 1.0 us on 125 of the 256 CUs; dH 46,
+// bound by reading W (5.6 TB/s). 700 rows of 32001 with dW: P 194 us (750 half-height tiles, 2.9 rounds), dH 162, dW
+// 194-202 (11 stages a tile, its stores 26 of them).
 // Rows are taken in pieces whose P fits a gigabyte, but of 256 rows at least (2 GB of P at 2^22 words). The number of
 // counted rows is known on the device only: the GEMMs plan their tiles there, from a grid for all rows. Without a
 // gradient P is neither stored nor given room: the product's epilogue keeps the tiles' sums.

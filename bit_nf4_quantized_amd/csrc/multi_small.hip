@@ -194,7 +194,7 @@ struct BaseLds {
 // rows 4096 -> 11008 35.2 -> 36.7); so it costs K = 4160 0.4 to 0.8 us (60 rows
 // -> 11008 37.7 -> 38.2) and nothing where K is a multiple of 128.
 // PAIR: weight blockIdx.z of two (of one shape), the second's partials behind the first's; from blockIdx.z = 2 on T's
-// tg workgroups, which the base product does not wait for. 96 rows, 4096 -> 2 x 11008: 45.5 us, of tiles on 172 of the
+// tg workgroups, which the base product does not wait for. 96 rows, 4096 -> 2 x 11008: 41.3 us, of tiles on 172 of the
 // 256 CUs. T by a launch of its own before was slower, whole calls of 17 to 128 rows and ranks 16 to 256: 3 to 10 us
 // where CUs are left idle, by the last round of tiles too (4096 -> 2 x 11008 96 rows rank 16 53.0 -> 49.1, 128 rows rank
 // 256 120.7 -> 112.2; -> 2 x 22016 33 rows rank 16 82.5 -> 78.2). With none idle it is 0.2 to 1.8 us slower too, but for

@@ -12,8 +12,9 @@
 // from h before its rounding to the residual's type: one rounding each.
 // Sums are fp32 in a fixed order; dw is summed per workgroup over its rows, then
 // over the workgroups. 8192 x 4096, bf16 onto an fp32 stream, with both outputs:
-// 85 us, 5.1 TB/s (a large copy: 5.05). Backward, 1001 x 6656 in bf16: 15.0 us (3.6
-// TB/s, the latency of one or two rows per workgroup) and 4.4 for dw's sum.
+// 86 us, 5.1 TB/s (a large copy: 5.05). Backward, 8192 x 4096 on an fp32 stream: 88 us
+// (5.4 TB/s) and 7.4 for dw's sum; 1001 x 6656 in bf16: 14.7 us (3.6 TB/s, the latency
+// of one or two rows per workgroup) and 4.4.
 #include "common.h"
 #include "int8.h"
 #include "launch.h"

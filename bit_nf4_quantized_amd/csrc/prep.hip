@@ -5,7 +5,7 @@
 //
 //   weights   one or two quantised weights [N][K] -> bf16 rows; two of them in
 //             pairs of blocks of 32 rows (row n of weight w at 64 (n / 32) + 32 w
-//             + n % 32), rows N .. Np zeros. 2.5 B per weight: 90 M weights 50 us, 4.5 TB/s.
+//             + n % 32), rows N .. Np zeros. 2.5 B per weight: 90 M weights 45-50 us, 4.5-5.0 TB/s.
 //   adapters  32 x 32 tiles, transposed through LDS:
 //             l1t [n][rp][K] = L1^T, rows behind the rank zero
 //             l2i [2 Np][2 rp] = L2^T in the paired rows' order, weight w's columns

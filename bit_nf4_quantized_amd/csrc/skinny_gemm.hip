@@ -345,7 +345,7 @@ __device__ __forceinline__ tn_v4i16 tn_read_tr(const char* lds_byte) {
 // are multiplied with their rows' scales and rounded to bf16 in registers: the
 // values of a dequantised copy, bit for bit, at half its bytes and without writing
 // it: the linear's backward of 8192 rows, 4096 -> 11008, 809 -> 765 us; this launch
-// 52 (the 11008 bf16 columns of dL2 in it), 4.1 TB/s.
+// 48-50 (the 11008 bf16 columns of dL2 in it), 4.4 TB/s.
 typedef int tn_v2i32 __attribute__((ext_vector_type(2)));
 constexpr int kTn8S = SK * SM, kTn8Scale = kTn8S + SK * kTnSRow;   // offsets of S and of the scales in a stage
 static_assert(kTn8Scale + 1024 <= kTnStageBytes, "a stage of int8 values fits");

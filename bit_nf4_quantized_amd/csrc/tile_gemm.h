@@ -12,9 +12,9 @@
 // LDS without registers, A double- and B triple-buffered (160 KB); fragments of
 // k-step kk + 1 are read while the MFMAs of kk run; the copies of stage st + 2
 // go out one instruction at a time among the MFMAs of stage st. A wave owns
-// TM / 2 x 64 outputs as 32 x 32 x 16 MFMA accumulators. Large products run at the
-// card's power limit: 8192 x 4096 x 22016 with B k-major 1.34 PFLOP/s, 6144 x 32000 x
-// 4096 with both row-major and P's epilogue 1.15-1.2.
+// TM / 2 x 64 outputs as 32 x 32 x 16 MFMA accumulators. Large products: 8192 x
+// 4096 x 22016 with B k-major 1.35 PFLOP/s, 6144 x 32000 x 4096 with both row-major
+// and P's epilogue 1.18-1.25 (a large library product 1.46).
 //
 // Copies take a uniform 64-bit base per tile and stage and a 32-bit offset per
 // lane (inside the tile; k-major: inside 96 rows, so rows of up to 2^24 elements),
@@ -336,7 +336,7 @@ __device__ __forceinline__ void tg_tile(const TgArgs& p, const E& epi, int64_t m
 // slices of the reduction of nk stages, whichever end soonest. A stage of a half-height tile took 1.0 us beside 1.65 of
 // a full one (products of 6144 rows). Slices' partials are written and read once (S M N 8 bytes at 4.5 TB/s) and take
 // one launch more; at least 8 stages each, at most 16, and M S at most `most` rows of partials. P W of 777 rows, 4096
-// columns, 501 stages: half tiles in 2 slices 264 us, full ones in 4 214. In fp32 arithmetic, on the host or the device
+// columns, 501 stages, both in short runs: half tiles in 2 slices 264 us, full ones in 4 214 (now, in long runs, 162). In fp32 arithmetic, on the host or the device
 // (where M may be known there only: then of the choices that `grid` workgroups hold; whole tiles without slices have to
 // be one).
 constexpr float kTgFullCost = 1.65f, kTgHalfCost = 1.05f;

@@ -15,8 +15,8 @@
  * Activations in 8 bits ("int8 values") are those of qlora_int8_quantize with
  * blocks of 64: codes [numel] and one fp32 absmax per 64 consecutive values, of a
  * matrix whose rows are a multiple of 64 long. A value is code * RN32(absmax / 127).
- * Where these entry points write them, a block that holds an infinity or NaN has that as its absmax and codes 0: its
- * 64 values are NaN.
+ * Where these entry points write them, a block that holds an infinity or NaN
+ * has that as its absmax and codes 0: its 64 values are NaN.
  * M (rows) is at most QLORA_LAYER_MAX_ROWS, and may be 0. A workspace for M rows serves fewer rows too.
  */
 #ifndef QLORA_LAYERS_H
@@ -49,7 +49,10 @@ typedef enum { QLORA_ACT_SILU = 0, QLORA_ACT_GELU_TANH = 1 } qlora_act;
  *   dL1[i], dL2[i]: those of qlora_linear_bwd for the upstream gradient dG (i = 0) or dU (i = 1)
  * act(g) = g sigmoid(g) (SILU) or g sigmoid(z), z = sqrt(8 / pi) (g + 0.044715 g^3) (GELU_TANH). G and U are fp32
  * sums of bf16 products (scale T rounded to bf16 before its second product, as in qlora_linear_fwd) and are not
- * rounded before A; dG and dU are rounded to bf16 once, as the operands of the products that follow.
+ * rounded before A; dG, dU and scale (dG L2^T), scale (dU L2^T) are rounded to bf16 once, as the operands of the products
+ * that follow. A forward call of a single row that keeps no gate8 and up8, of rank up to 64 and K a multiple of 256 with
+ * both weights double-quantised in one data type, may take the code values rounded to fp16, which can move a weight to
+ * the neighbouring bf16: its A then differs in its last bits from that of a call that keeps them.
  *   gate, up     host structs of the quantised weights, both [F][K] (data types may differ).
  *   X            device bf16 [M][K]; backward: or NULL, with X8 its int8 values (dX, dL1, dL2 are then those of the
  *                values rounded to bf16).
@@ -64,7 +67,8 @@ typedef enum { QLORA_ACT_SILU = 0, QLORA_ACT_GELU_TANH = 1 } qlora_act;
  *   dL1, dL2     device, grad_dtype, shaped like L1, L2.
  *   ws           qlora_gated_workspace(M, K, F, r, backward) bytes.
  * Sums run in a fixed order. An infinity or NaN of one row of X, dA, T or the int8 values reaches no other row of A or
- * dX. Shapes: K a multiple of 64, F and r of 8, r in [8, 256], K and F below QLORA_GATED_MAX_COLS. M <= 128 in the
+ * dX; through kept values it reaches all 64 features of its block. Both adapters have one rank; there is no adapter
+ * dropout. Shapes: K a multiple of 64, F and r of 8, r in [8, 256], K and F below QLORA_GATED_MAX_COLS. M <= 128 in the
  * forward pass streams both 4-bit weights once; a larger M and the backward pass dequantise them into ws.
  */
 int qlora_gated_workspace(int64_t M, int64_t K, int64_t F, int r, int backward, size_t *bytes);
@@ -80,8 +84,8 @@ int qlora_gated_bwd(const qlora_nf4 *gate, const qlora_nf4 *up, const uint16_t *
 
 /*
  * qlora_linear_bwd with X as int8 values [M][K]: dL1, and T where it is NULL, come from those values rounded to bf16;
- * dX does not depend on X. Arguments otherwise as there, K and N below QLORA_GATED_MAX_COLS; ws:
- * qlora_linear_bwd_int8_workspace(M, K, N, r) bytes.
+ * dX does not depend on X. There is no adapter dropout (qlora_linear_bwd_dropout has it, from bf16). Arguments otherwise
+ * as there, K and N below QLORA_GATED_MAX_COLS; ws: qlora_linear_bwd_int8_workspace(M, K, N, r) bytes.
  */
 int qlora_linear_bwd_int8_workspace(int64_t M, int64_t K, int64_t N, int r, size_t *bytes);
 int qlora_linear_bwd_int8(const qlora_nf4 *W, const qlora_int8_values *X8, const uint16_t *dY, int64_t M,
@@ -132,8 +136,9 @@ int qlora_norm_bwd(const uint16_t *dy, const void *h, qlora_dtype stream_dtype, 
  *   dH       device bf16 [M][K], or NULL.   dW  device, grad_dtype, [V][K], or NULL.
  *   ws       qlora_head_workspace(M, K, V, dH, dW, grad_dtype) bytes (dH, dW: whether they are computed).
  * Logits and their sums are fp32, the loss is summed in fp64, sums run in a fixed order. The probabilities are rounded
- * to bf16 once as an operand of the gradients' products (for dW, scaled rows of H too). An infinity or NaN in one row
- * of H reaches no other row of nll or dH.
+ * to bf16 once as an operand of the gradients' products (twice in rows where a logit is more than 40 above the label's
+ * and the vocabulary's tiles are brought to one maximum; for dW, scaled rows of H are rounded too). An infinity or NaN
+ * in one row of H reaches no other row of nll or dH.
  * K: a multiple of 64, below 2^23; V in [1, QLORA_HEAD_MAX_VOCAB]. Rows are taken in pieces of at most 2^29 / V (at
  * least 256): the workspace holds the probabilities of one piece, 1 GiB or 512 V bytes at most; none without dH and dW.
  */
